@@ -7,7 +7,8 @@
  *   - the slot_mapping scatter     (pkv_write_slots),
  *   - the block_table gather       (pkv_gather),
  *   - fused paged decode attention that reads K/V through the block table
- *     with a split-K partial pass and a combine pass (pkv_decode_attention).
+ *     with a split-K partial pass and a combine pass (pkv_decode_attention),
+ *   - rotary positions fused with the scatter (pkv_rope_append).
  *
  * Sources restated (cited by page title and section):
  *   [step14_2]  mini-vLLM tutorial "step14_2 - index_select gather"
@@ -161,6 +162,84 @@ PKV_API pkv_status pkv_append_tokens(const pkv_pool* pool, int32_t layer,
                                      const int32_t* token_seq, const int32_t* token_pos,
                                      int64_t num_tokens, const void* k_new, const void* v_new,
                                      int64_t* slot_mapping, cudaStream_t stream);
+
+/* Rotary positions ("vLLM PagedAttention source notes" §2.3: q and k as the
+ * attention sees them; the pages leave positions to the model).
+ *
+ * A descriptor holds the schedule of one model: rotary_dim (the first
+ * rotary_dim dims of a head turn, the others pass), the layout of the pairs,
+ * a factor on the turned dims, and the frequency of pair i as a 64-bit
+ * fraction of a turn per token, step[i] = f_i / (2 pi) * 2^64 mod 2^64, so
+ * that the angle of any 32-bit position is exact modulo one turn.  It is a
+ * plain host struct filled by pkv_rope_init or pkv_rope_init_freqs (no device
+ * memory; copy it freely) and read on the host during each call, so a
+ * captured graph keeps the values it was captured with. */
+#define PKV_ROPE_MAX_PAIRS 128
+
+typedef struct {
+  int32_t rotary_dim;  /* even, <= head_dim */
+  int32_t interleaved; /* 0: pair (i, i + rotary_dim / 2); 1: pair (2 i, 2 i + 1) */
+  float attn_scale;    /* factor on cos and sin */
+  int32_t reserved;
+  uint64_t step[PKV_ROPE_MAX_PAIRS]; /* rotary_dim / 2 entries used */
+} pkv_rope;
+
+/* Schedules of pkv_rope_init, with f_i = base^(-2 i / rotary_dim):
+ *   PLAIN     f_i.
+ *   LINEAR    f_i / factor (positions interpolated).
+ *   BASE      base replaced by base * factor^(rotary_dim / (rotary_dim - 2)).
+ *   BY_PARTS  pairs that make at least turns_fast turns within original_len
+ *             tokens keep f_i, those that make at most turns_slow get
+ *             f_i / factor, linear in the number of turns between; cos and
+ *             sin are multiplied by 0.1 ln(factor) + 1.
+ * factor >= 1 where it is used; original_len > 0 and turns_fast > turns_slow
+ * for BY_PARTS; arguments a schedule does not use are ignored. */
+typedef enum {
+  PKV_ROPE_PLAIN = 0,
+  PKV_ROPE_LINEAR = 1,
+  PKV_ROPE_BASE = 2,
+  PKV_ROPE_BY_PARTS = 3
+} pkv_rope_scaling;
+
+PKV_API pkv_status pkv_rope_init(pkv_rope* rope, int32_t rotary_dim, int32_t interleaved,
+                                 double base, int32_t scaling, double factor,
+                                 double original_len, double turns_fast, double turns_slow);
+/* Any other schedule: inv_freq (host, rotary_dim / 2 values) in radians per
+ * token, and the factor on cos and sin. */
+PKV_API pkv_status pkv_rope_init_freqs(pkv_rope* rope, int32_t rotary_dim, int32_t interleaved,
+                                       const double* inv_freq, double attn_scale);
+
+/* Rotary positions and append in one pass: for every token t that
+ * pkv_append_tokens would store (same block_tables, offsets, token_seq and
+ * token_pos, same slots, same error behaviour), with the angle
+ * P f_i of pair i at the rotary position P = rope_pos[t], or token_pos[t]
+ * where rope_pos is NULL:
+ *     q_out[t] = turned q[t],
+ *     the row of t's slot in k_cache = turned k_new[t], in v_cache = v_new[t].
+ * A pair (a, b) turns to (a c - b s, b c + a s), c = attn_scale cos, s =
+ * attn_scale sin, in fp32, rounded once to the output's type (PKV_I8 pools:
+ * q and q_out are bf16, and the keys are quantised as in pkv_write_slots from
+ * the fp32 result, without a bf16 step between).  Nothing is written for
+ * padding tokens and for tokens out of range, in q_out neither.
+ * q [num_tokens, num_q_heads, head_dim], k_new, v_new [num_tokens, Hkv,
+ * head_dim], q_out as q: consecutive heads within a token, tokens *_stride
+ * elements apart (a multiple of 16 bytes, at least a token's heads), so
+ * slices of one projection's output can be passed as they are.  q_out may be
+ * q itself (same stride); other overlaps are not allowed.  num_q_heads 0
+ * (q and q_out NULL) turns and stores the keys alone.  slot_mapping (int64
+ * [num_tokens], device) receives the slots when not NULL.
+ * Supported: head_dim 32, 64, 128 or 256; rotary_dim a multiple of 16 (half
+ * layout) or 8 (interleaved), for fp32 pools with head_dim <= 128 of 8 or 4;
+ * others PKV_ERR_UNSUPPORTED. */
+PKV_API pkv_status pkv_rope_append(const pkv_pool* pool, int32_t layer, const pkv_rope* rope,
+                                   const int32_t* block_tables, int32_t max_blocks_per_seq,
+                                   const int32_t* offsets, int32_t batch,
+                                   const int32_t* token_seq, const int32_t* token_pos,
+                                   const int32_t* rope_pos, int64_t num_tokens, const void* q,
+                                   int64_t q_stride, int32_t num_q_heads, const void* k_new,
+                                   int64_t k_stride, const void* v_new, int64_t v_stride,
+                                   void* q_out, int64_t q_out_stride, int64_t* slot_mapping,
+                                   cudaStream_t stream);
 
 /* Gather ([step14_2] "Problem" and "Solution"; [vllm-notes] §2.3
  * gather_kv_for_attention; [ch12] §2.2 offset, §2.5 read_layer).

@@ -9,6 +9,7 @@ from ._binding import (  # noqa: F401
     append_tokens,
     Pool,
     PkvError,
+    Rope,
     STATUS_CODES,
     build_slot_mapping,
     copy_blocks,
@@ -26,6 +27,7 @@ from ._binding import (  # noqa: F401
     library_path,
     load,
     prefill_attention,
+    rope_append,
     set_decode_ctas,
     set_debug_skip_fill,
     set_decode_events,

@@ -47,13 +47,28 @@ class _PoolStruct(ctypes.Structure):
     ]
 
 
+class _RopeStruct(ctypes.Structure):
+    _fields_ = [
+        ("rotary_dim", ctypes.c_int32),
+        ("interleaved", ctypes.c_int32),
+        ("attn_scale", ctypes.c_float),
+        ("reserved", ctypes.c_int32),
+        ("step", ctypes.c_uint64 * 128),
+    ]
+
+
 _lib = None
 _P, _I32, _I64, _F32, _SZ = (ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_float,
                              ctypes.c_size_t)
+_F64 = ctypes.c_double
 _SIGS = {
     "pkv_build_slot_mapping": (_I32, [_P, _P, _I32, _P, _I32, _P, _P, _I64, _P, _P]),
     "pkv_write_slots": (_I32, [_P, _I32, _P, _P, _P, _I64, _P]),
     "pkv_append_tokens": (_I32, [_P, _I32, _P, _I32, _P, _I32, _P, _P, _I64, _P, _P, _P, _P]),
+    "pkv_rope_init": (_I32, [_P, _I32, _I32, _F64, _I32, _F64, _F64, _F64, _F64]),
+    "pkv_rope_init_freqs": (_I32, [_P, _I32, _I32, _P, _F64]),
+    "pkv_rope_append": (_I32, [_P, _I32, _P, _P, _I32, _P, _I32, _P, _P, _P, _I64, _P, _I64, _I32,
+                               _P, _I64, _P, _I64, _P, _I64, _P, _P]),
     "pkv_gather": (_I32, [_P, _I32, _P, _I32, _P, _P, _I32, _P, _I64, _P, _P, _P]),
     "pkv_decode_workspace_size": (_SZ, [_I32, _I32, _I32]),
     "pkv_decode_attention": (_I32, [_P, _I32, _P, _I32, _F32, _P, _I32, _P, _P, _I32, _P, _P,
@@ -238,6 +253,113 @@ def append_tokens(pool: Pool, layer: int, block_tables: torch.Tensor,
                                    _ptr(token_pos), token_seq.numel(), _ptr(k_new), _ptr(v_new),
                                    _ptr(slot_mapping), _stream(pool.device))
     _check(st, "pkv_append_tokens")
+
+
+class Rope:
+    """Rotary schedule of a model (``pkv_rope`` in include/pkv.h): the first
+    ``rotary_dim`` dims of a head turn, in pairs (i, i + rotary_dim / 2) or,
+    ``interleaved``, (2 i, 2 i + 1).  ``scaling`` for long contexts is None,
+    ``"linear"``, ``"base"`` or ``"by_parts"`` (with ``factor``, and for the
+    last ``original_len``, ``turns_fast``, ``turns_slow``); or ``inv_freq``
+    gives the frequencies (radians per token) and ``attn_scale`` the factor on
+    cos and sin."""
+
+    _SCALING = {None: 0, "linear": 1, "base": 2, "by_parts": 3}
+
+    def __init__(self, rotary_dim: int, base: float = 10000.0, interleaved: bool = False,
+                 scaling: Optional[str] = None, factor: float = 1.0, original_len: float = 0.0,
+                 turns_fast: float = 32.0, turns_slow: float = 1.0,
+                 inv_freq: Optional[Sequence[float]] = None, attn_scale: float = 1.0):
+        lib = load()
+        self.struct = _RopeStruct()
+        if inv_freq is not None:
+            f = np.ascontiguousarray(np.asarray(inv_freq, dtype=np.float64))
+            if f.shape != (rotary_dim // 2,):
+                raise ValueError("inv_freq must have rotary_dim / 2 entries")
+            _check(lib.pkv_rope_init_freqs(self.ref, rotary_dim, int(bool(interleaved)),
+                                           f.ctypes.data, float(attn_scale)),
+                   "pkv_rope_init_freqs")
+        else:
+            if scaling not in self._SCALING:
+                raise ValueError(f"unknown rotary scaling {scaling!r}")
+            if attn_scale != 1.0:
+                raise ValueError("attn_scale goes with inv_freq")
+            _check(lib.pkv_rope_init(self.ref, rotary_dim, int(bool(interleaved)), float(base),
+                                     self._SCALING[scaling], float(factor), float(original_len),
+                                     float(turns_fast), float(turns_slow)), "pkv_rope_init")
+        self.rotary_dim, self.interleaved = rotary_dim, bool(interleaved)
+        self.attn_scale = float(self.struct.attn_scale)
+
+    @property
+    def ref(self):
+        return ctypes.byref(self.struct)
+
+
+def _index(t: Optional[torch.Tensor], pool: Pool, name: str, ndim: int) -> Optional[int]:
+    """Pointer of a contiguous int32 index tensor on the pool's device."""
+    if t is None:
+        return None
+    if t.dtype != torch.int32 or t.device != pool.device or t.dim() != ndim \
+            or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous int32 tensor of {ndim} dimension(s) on "
+                         f"{pool.device}")
+    return t.data_ptr()
+
+
+def _rows_of(t: torch.Tensor, pool: Pool, name: str, tokens: int, heads: Optional[int]) -> int:
+    """Elements between tokens of a [tokens, heads, head_dim] tensor in the
+    pool's row type, the heads of a token consecutive."""
+    dtype = torch.bfloat16 if pool.dtype == torch.uint8 else pool.dtype
+    if t.dtype != dtype or t.device != pool.device:
+        raise ValueError(f"{name} must be {dtype} on {pool.device}")
+    if t.dim() != 3 or t.shape[0] != tokens or t.shape[2] != pool.head_dim \
+            or (heads is not None and t.shape[1] != heads):
+        raise ValueError(f"{name} must be [{tokens}, {heads or 'heads'}, {pool.head_dim}], "
+                         f"not {tuple(t.shape)}")
+    s = t.stride()
+    row = t.shape[1] * t.shape[2]
+    if s[2] != 1 or (s[1] != t.shape[2] and t.shape[1] > 1):
+        raise ValueError(f"the heads of a token of {name} must be consecutive")
+    return row if tokens <= 1 else s[0]
+
+
+def rope_append(pool: Pool, layer: int, rope: Rope, block_tables: torch.Tensor,
+                offsets: Optional[torch.Tensor], token_seq: torch.Tensor, token_pos: torch.Tensor,
+                q: Optional[torch.Tensor], k_new: torch.Tensor, v_new: torch.Tensor,
+                q_out: Optional[torch.Tensor], rope_pos: Optional[torch.Tensor] = None,
+                slot_mapping: Optional[torch.Tensor] = None) -> None:
+    """Rotary positions and append in one pass: ``q`` ([T, Hq, D]) turned into
+    ``q_out`` (which may be ``q``), ``k_new`` ([T, Hkv, D]) turned and stored
+    with ``v_new`` at the slots of (token_seq, token_pos).  The angle's
+    position is ``rope_pos`` where given, else ``token_pos``.  Tokens of q,
+    k_new, v_new and q_out may lie apart (slices of one projection)."""
+    lib = load()
+    T = token_seq.numel()
+    bt, offs = _index(block_tables, pool, "block_tables", 2), _index(offsets, pool, "offsets", 1)
+    seq, pos = _index(token_seq, pool, "token_seq", 1), _index(token_pos, pool, "token_pos", 1)
+    rpos = _index(rope_pos, pool, "rope_pos", 1)
+    B = block_tables.shape[0]
+    if token_pos.numel() != T or (rope_pos is not None and rope_pos.numel() != T):
+        raise ValueError("token_seq, token_pos and rope_pos must have the same length")
+    if offsets is not None and offsets.numel() != B:
+        raise ValueError("offsets must have one entry per row of block_tables")
+    if slot_mapping is not None and (slot_mapping.dtype != torch.int64 or slot_mapping.numel() != T
+                                     or slot_mapping.device != pool.device
+                                     or not slot_mapping.is_contiguous()):
+        raise ValueError("slot_mapping must be a contiguous int64 tensor with an entry per token")
+    if (q is None) != (q_out is None):
+        raise ValueError("q and q_out go together")
+    hq = 0 if q is None else q.shape[1]
+    qs = 0 if q is None else _rows_of(q, pool, "q", T, None)
+    qos = 0 if q is None else _rows_of(q_out, pool, "q_out", T, hq)
+    ks = _rows_of(k_new, pool, "k_new", T, pool.num_kv_heads)
+    vs = _rows_of(v_new, pool, "v_new", T, pool.num_kv_heads)
+    with _dev(pool):
+        st = lib.pkv_rope_append(pool.ref, layer, rope.ref, bt, block_tables.shape[1], offs, B, seq,
+                                 pos, rpos, T, _ptr(q), qs, hq, k_new.data_ptr(), ks,
+                                 v_new.data_ptr(), vs, _ptr(q_out), qos, _ptr(slot_mapping),
+                                 _stream(pool.device))
+    _check(st, "pkv_rope_append")
 
 
 def gather(pool: Pool, layer: int, block_tables: torch.Tensor, seq_lens: torch.Tensor,

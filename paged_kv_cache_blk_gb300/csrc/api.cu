@@ -176,6 +176,15 @@ int device_facts(int* smem_optin, int** err_word, int* grid, int* validate) {
   return PKV_OK;
 }
 
+int device_sm_count(int* sm_count) {
+  DevInfo* d;
+  const pkv_status st = current_device(&d);
+  if (st == PKV_OK) *sm_count = d->sm_count;
+  return st;
+}
+
+int launch_status(cudaError_t e) { return launched(e); }
+
 unsigned long long wait_limit_ns() { return g_wait_ns.load(); }
 
 int debug_skip_fill() { return g_skip_fill.load(); }

@@ -1,6 +1,6 @@
 // Quantisation of one token row's heads for int8 pools, shared by the
-// quantising scatter (copy_kernels.cu) and the fused decode step
-// (decode.cu), so both store the same bytes.
+// quantising scatter (copy_kernels.cu), the rotary append (rope.cu) and the
+// fused decode step (decode.cu), so all store the same bytes.
 //
 // One warp per (token, kv head), VPL = head_dim / 32 values per lane:
 // absmax of the head (fp32, a warp max over the |x| bit patterns), scale =
@@ -39,6 +39,11 @@ __device__ __forceinline__ void load_bf16(const __nv_bfloat16* src, float (&x)[V
   }
 }
 
+// Code of x in a head whose absmax has the bit pattern `absmax`.
+__device__ __forceinline__ int quantise_value(float x, uint32_t absmax, float scale) {
+  return absmax == 0 ? 0 : min(127, max(-127, __float2int_rn(div_ieee(x, scale))));
+}
+
 // Quantise one head (VPL values per lane); returns the scale, codes in c.
 template <int VPL>
 __device__ __forceinline__ float quantise_head(const float (&x)[VPL], int (&c)[VPL]) {
@@ -48,8 +53,7 @@ __device__ __forceinline__ float quantise_head(const float (&x)[VPL], int (&c)[V
   m = __reduce_max_sync(0xffffffffu, m);
   const float scale = div_ieee(__uint_as_float(m), 127.f);
 #pragma unroll
-  for (int i = 0; i < VPL; ++i)
-    c[i] = m == 0 ? 0 : min(127, max(-127, __float2int_rn(div_ieee(x[i], scale))));
+  for (int i = 0; i < VPL; ++i) c[i] = quantise_value(x[i], m, scale);
   return scale;
 }
 
