@@ -8,7 +8,9 @@
  *   - the block_table gather       (pkv_gather),
  *   - fused paged decode attention that reads K/V through the block table
  *     with a split-K partial pass and a combine pass (pkv_decode_attention),
- *   - rotary positions fused with the scatter (pkv_rope_append).
+ *   - rotary positions fused with the scatter (pkv_rope_append),
+ *   - sparse decode attention over the blocks that a cheap score selects
+ *     (pkv_update_block_bounds, pkv_select_blocks, pkv_decode_attention_sparse).
  *
  * Sources restated (cited by page title and section):
  *   [step14_2]  mini-vLLM tutorial "step14_2 - index_select gather"
@@ -366,6 +368,109 @@ PKV_API pkv_status pkv_decode_attention_shared_prefix(const pkv_pool* pool, int3
                                                       int32_t num_prefix_blocks, void* out,
                                                       void* workspace, size_t workspace_bytes,
                                                       cudaStream_t stream);
+
+/* Sparse decode: attention over the blocks that a cheap score selects for
+ * each query ([ch12] §6 names sparse KV as a next step of paged caches; the
+ * scheme below is this library's reading).  Three calls: the key bounds of
+ * the blocks that received tokens are brought up to date
+ * (pkv_update_block_bounds), every query's blocks are scored from the bounds
+ * and the best selected (pkv_select_blocks), and attention runs over those
+ * (pkv_decode_attention_sparse).  Queries are listed as the tokens of
+ * pkv_append_tokens are: query t belongs to sequence token_seq[t] (negative:
+ * padding) and sees the keys of its positions 0..token_pos[t], so a list may
+ * hold one query per sequence, or several.
+ *
+ * Key bounds.  For a block, layer and kv head: hi_d and lo_d, the largest and
+ * smallest key element d over the block's rows, hence for every key k of the
+ * block q . k <= sum_d (q_d >= 0 ? q_d hi_d : q_d lo_d).  They live in two
+ * caller-owned device arrays,
+ *     bound_codes   bytes [num_blocks, num_layers, Hkv, 2, head_dim], 16-byte
+ *                   aligned: the codes of hi, then those of lo, each stored
+ *                   as the byte code + 128, codes in [-127, 127];
+ *     bound_scales  fp32 [num_blocks, num_layers, Hkv], powers of two;
+ * hi ~ code * scale rounded up, lo rounded down (the bound still holds), with
+ * scale = 2^e, e the smallest exponent in [-40, 40] with absmax <= 127 * 2^e
+ * (larger elements keep the outermost code).  An infinite element or a NaN
+ * gets the outermost code of its side, a NaN of both.
+ *
+ * pkv_update_block_bounds recomputes, for every sequence b, the bounds of the
+ * blocks that hold its positions first_pos[b] .. seq_lens[b] - 1 (first_pos
+ * NULL, or below 0: from 0), each over the block's rows from row 0 to the last
+ * one the sequence holds.  Rows before a first-block offset count: they belong
+ * to a prefix that other sequences share.  After a prompt: first_pos NULL or
+ * the prompt's first position; after a decode step: seq_lens - 1; after a
+ * block copy or swap-in: the positions of the copied blocks.  Sequences that
+ * share a block may be listed together when they hold the same last row of it
+ * (all of a full block).  Supported: head_dim 64 or 128.  Errors as
+ * pkv_decode_attention: a bad sequence or block id is skipped and sets the
+ * device error word. */
+PKV_API pkv_status pkv_update_block_bounds(const pkv_pool* pool, int32_t layer,
+                                           const int32_t* block_tables,
+                                           int32_t max_blocks_per_seq, const int32_t* seq_lens,
+                                           const int32_t* offsets, const int32_t* first_pos,
+                                           int32_t batch, void* bound_codes, float* bound_scales,
+                                           cudaStream_t stream);
+
+/* Score and selection.  The q row of each head is coded like the bounds
+ * (codes rounded to nearest even, scale 2^e; NaN counts as 0), and for query
+ * t, kv head g and table entry j of its n = (offset + token_pos[t]) / bs + 1
+ * entries
+ *     score = max over the query heads h of g of
+ *             2^(e_h) * scale_j * sum_d (q_d >= 0 ? q_d hi_d : q_d lo_d).
+ * The sum is one of whole numbers below 2^24 and the factors are powers of
+ * two, so scores are exact and the selection does not depend on how the work
+ * is split.  If n <= num_selected every entry is selected; otherwise the
+ * first `sink` and the last `recent` entries (sink + recent <= num_selected)
+ * and the best scores among the others, equal scores to the lower entry.  The
+ * last entry, which holds the query itself, is worth a `recent` of 1: bounds
+ * then have to be up to date for full blocks only.
+ * selected: int32 [num_tokens, Hkv, num_selected], the selected entries of the
+ * sequence's table row in ascending order, -1 behind them; selected_count:
+ * int32 [num_tokens, Hkv], their number (0 for padding and for tokens out of
+ * range, which set the device error word; an entry with an invalid block id
+ * sets it too, is not read, and scores lowest).
+ * q: [num_tokens, num_q_heads, head_dim], contiguous, in the type that
+ * pkv_decode_attention takes; the pool's tensors are not read (k_cache and
+ * v_cache may be NULL).  Supported: head_dim 64 or 128; up to 16 query heads
+ * per kv head; max_blocks_per_seq up to 327680; others PKV_ERR_UNSUPPORTED.
+ * One launch, no workspace. */
+PKV_API pkv_status pkv_select_blocks(const pkv_pool* pool, int32_t layer, const void* bound_codes,
+                                     const float* bound_scales, const void* q,
+                                     int32_t num_q_heads, const int32_t* block_tables,
+                                     int32_t max_blocks_per_seq, const int32_t* offsets,
+                                     int32_t batch, const int32_t* token_seq,
+                                     const int32_t* token_pos, int32_t num_tokens,
+                                     int32_t num_selected, int32_t sink, int32_t recent,
+                                     int32_t* selected, int32_t* selected_count,
+                                     cudaStream_t stream);
+
+/* Attention of each query over its selected blocks: for query t and query
+ * head h of kv head g, with i running over the positions i <= token_pos[t] of
+ * sequence token_seq[t] whose table entry is in selected[t][g][0..num_selected),
+ *     out[t][h] = sum_i softmax_i(scale * q[t][h] . K_i[g]) V_i[g].
+ * selected: int32 [num_tokens, Hkv, num_selected] table entries in any order;
+ * negative ones are skipped, an entry listed twice counts twice, entries past
+ * the query's position hold nothing it sees; entries past the table row, and
+ * entries whose block id is outside the pool, are skipped and set the device
+ * error word.  With every entry selected the result is that of
+ * pkv_decode_attention at seq_lens = token_pos + 1.  A query that sees
+ * nothing, or only scores of -inf, gives zeros; a token out of range gives
+ * zeros and sets the error word; the out rows of padding are not written.
+ * Rows that the query does not see are not read.  q, out: [num_tokens,
+ * num_q_heads, head_dim], contiguous, types and pool dtypes as in
+ * pkv_decode_attention (fp32 accumulation; the softmax weights are rounded to
+ * bf16, or to fp16 with the V scales for PKV_I8 pools, for their product with
+ * V).  Supported: head_dim 64 or 128; any num_kv_heads; up to 16 query heads
+ * per kv head; any block_size the pool allows.  One launch, no workspace; may
+ * be captured in a CUDA graph. */
+PKV_API pkv_status pkv_decode_attention_sparse(const pkv_pool* pool, int32_t layer, const void* q,
+                                               int32_t num_q_heads, float scale,
+                                               const int32_t* block_tables,
+                                               int32_t max_blocks_per_seq, const int32_t* offsets,
+                                               int32_t batch, const int32_t* token_seq,
+                                               const int32_t* token_pos, int32_t num_tokens,
+                                               const int32_t* selected, int32_t num_selected,
+                                               void* out, cudaStream_t stream);
 
 /* Paged prefill attention (the prefill batch of
  * "vLLM PagedAttention source notes" §2.4: the prompt tokens' K/V are written

@@ -69,6 +69,11 @@ _SIGS = {
     "pkv_rope_init_freqs": (_I32, [_P, _I32, _I32, _P, _F64]),
     "pkv_rope_append": (_I32, [_P, _I32, _P, _P, _I32, _P, _I32, _P, _P, _P, _I64, _P, _I64, _I32,
                                _P, _I64, _P, _I64, _P, _I64, _P, _P]),
+    "pkv_update_block_bounds": (_I32, [_P, _I32, _P, _I32, _P, _P, _P, _I32, _P, _P, _P]),
+    "pkv_select_blocks": (_I32, [_P, _I32, _P, _P, _P, _I32, _P, _I32, _P, _I32, _P, _P, _I32,
+                                 _I32, _I32, _I32, _P, _P, _P]),
+    "pkv_decode_attention_sparse": (_I32, [_P, _I32, _P, _I32, _F32, _P, _I32, _P, _I32, _P, _P,
+                                           _I32, _P, _I32, _P, _P]),
     "pkv_gather": (_I32, [_P, _I32, _P, _I32, _P, _P, _I32, _P, _I64, _P, _P, _P]),
     "pkv_decode_workspace_size": (_SZ, [_I32, _I32, _I32]),
     "pkv_decode_attention": (_I32, [_P, _I32, _P, _I32, _F32, _P, _I32, _P, _P, _I32, _P, _P,
@@ -454,6 +459,122 @@ def decode_attention_static(pool: Pool, layer: int, q: torch.Tensor, scale: floa
                                              _ptr(seq_lens), _ptr(offsets), seq_lens.numel(),
                                              _ptr(out), _stream(pool.device))
     _check(st, "pkv_decode_attention_static")
+
+
+class BlockBounds:
+    """Key bounds of a pool's blocks (include/pkv.h, "Key bounds"): ``codes``
+    uint8 [num_blocks, num_layers, Hkv, 2, head_dim] and ``scales`` fp32
+    [num_blocks, num_layers, Hkv] on the pool's device."""
+
+    def __init__(self, codes: torch.Tensor, scales: torch.Tensor):
+        if codes.dtype != torch.uint8 or codes.dim() != 5 or codes.shape[3] != 2:
+            raise ValueError("codes must be a uint8 tensor [N, L, Hkv, 2, D]")
+        if scales.dtype != torch.float32 or scales.shape != codes.shape[:3]:
+            raise ValueError("scales must be a float32 tensor [N, L, Hkv]")
+        if codes.device != scales.device or not codes.is_contiguous() or not scales.is_contiguous():
+            raise ValueError("codes and scales must be contiguous tensors on one device")
+        self.codes, self.scales = codes, scales
+
+    @classmethod
+    def for_pool(cls, pool: Pool) -> "BlockBounds":
+        """Bounds for every block of ``pool``, not yet filled."""
+        shape = (pool.num_blocks, pool.num_layers, pool.num_kv_heads)
+        return cls(torch.empty(shape + (2, pool.head_dim), dtype=torch.uint8, device=pool.device),
+                   torch.empty(shape, dtype=torch.float32, device=pool.device))
+
+
+def _bounds_of(bounds: BlockBounds, pool: Pool) -> None:
+    c = bounds.codes
+    if c.device != pool.device or c.shape != (pool.num_blocks, pool.num_layers,
+                                              pool.num_kv_heads, 2, pool.head_dim):
+        raise ValueError("the bounds do not belong to a pool of this shape")
+
+
+def update_block_bounds(pool: Pool, layer: int, bounds: BlockBounds, block_tables: torch.Tensor,
+                        seq_lens: torch.Tensor, offsets: Optional[torch.Tensor],
+                        first_pos: Optional[torch.Tensor] = None) -> None:
+    """Recompute the key bounds of the blocks that hold positions
+    ``first_pos`` (None: 0) .. ``seq_lens`` - 1 of each sequence."""
+    lib = load()
+    bt, lens = _index(block_tables, pool, "block_tables", 2), _index(seq_lens, pool, "seq_lens", 1)
+    offs, first = _index(offsets, pool, "offsets", 1), _index(first_pos, pool, "first_pos", 1)
+    B = block_tables.shape[0]
+    for t in (seq_lens, offsets, first_pos):
+        if t is not None and t.numel() != B:
+            raise ValueError("seq_lens, offsets and first_pos must have one entry per row of "
+                             "block_tables")
+    _bounds_of(bounds, pool)
+    with _dev(pool):
+        st = lib.pkv_update_block_bounds(pool.ref, layer, bt, block_tables.shape[1], lens, offs,
+                                         first, B, bounds.codes.data_ptr(),
+                                         bounds.scales.data_ptr(), _stream(pool.device))
+    _check(st, "pkv_update_block_bounds")
+
+
+def _queries(pool: Pool, q: torch.Tensor, block_tables: torch.Tensor,
+             offsets: Optional[torch.Tensor], token_seq: torch.Tensor, token_pos: torch.Tensor,
+             selected: torch.Tensor):
+    """Checks and pointers shared by select_blocks and decode_attention_sparse."""
+    bt, offs = _index(block_tables, pool, "block_tables", 2), _index(offsets, pool, "offsets", 1)
+    seq, pos = _index(token_seq, pool, "token_seq", 1), _index(token_pos, pool, "token_pos", 1)
+    sel = _index(selected, pool, "selected", 3)
+    T = token_seq.numel()
+    if token_pos.numel() != T:
+        raise ValueError("token_seq and token_pos must have the same length")
+    if offsets is not None and offsets.numel() != block_tables.shape[0]:
+        raise ValueError("offsets must have one entry per row of block_tables")
+    if selected.shape[0] != T or selected.shape[1] != pool.num_kv_heads:
+        raise ValueError(f"selected must be [{T}, {pool.num_kv_heads}, blocks]")
+    _rows_of(q, pool, "q", T, None)
+    if not q.is_contiguous():
+        raise ValueError("q must be contiguous")
+    return bt, offs, seq, pos, sel, T
+
+
+def select_blocks(pool: Pool, layer: int, bounds: BlockBounds, q: torch.Tensor,
+                  block_tables: torch.Tensor, offsets: Optional[torch.Tensor],
+                  token_seq: torch.Tensor, token_pos: torch.Tensor, selected: torch.Tensor,
+                  count: torch.Tensor, sink: int = 0, recent: int = 1) -> None:
+    """Score the blocks of each query's sequence from ``bounds`` and select
+    ``selected.shape[2]`` of them per kv head: table entries into ``selected``
+    (int32 [T, Hkv, K], ascending, -1 behind), their number into ``count``
+    (int32 [T, Hkv]).  The first ``sink`` and last ``recent`` are always in."""
+    lib = load()
+    bt, offs, seq, pos, sel, T = _queries(pool, q, block_tables, offsets, token_seq, token_pos,
+                                          selected)
+    cnt = _index(count, pool, "count", 2)
+    if count.shape != selected.shape[:2]:
+        raise ValueError("count must be [T, Hkv]")
+    _bounds_of(bounds, pool)
+    with _dev(pool):
+        st = lib.pkv_select_blocks(pool.ref, layer, bounds.codes.data_ptr(),
+                                   bounds.scales.data_ptr(), q.data_ptr(), q.shape[1], bt,
+                                   block_tables.shape[1], offs, block_tables.shape[0], seq, pos, T,
+                                   selected.shape[2], sink, recent, sel, cnt,
+                                   _stream(pool.device))
+    _check(st, "pkv_select_blocks")
+
+
+def decode_attention_sparse(pool: Pool, layer: int, q: torch.Tensor, scale: float,
+                            block_tables: torch.Tensor, offsets: Optional[torch.Tensor],
+                            token_seq: torch.Tensor, token_pos: torch.Tensor,
+                            selected: torch.Tensor, out: torch.Tensor) -> None:
+    """Attention of ``q`` ([T, Hq, D]) over the table entries ``selected``
+    (int32 [T, Hkv, K], negative ones skipped) of each query's sequence, at
+    positions up to ``token_pos``, into ``out``."""
+    lib = load()
+    bt, offs, seq, pos, sel, T = _queries(pool, q, block_tables, offsets, token_seq, token_pos,
+                                          selected)
+    if out.shape != q.shape or out.dtype != q.dtype or out.device != q.device \
+            or not out.is_contiguous():
+        raise ValueError("out must be a contiguous tensor like q")
+    with _dev(pool):
+        st = lib.pkv_decode_attention_sparse(pool.ref, layer, q.data_ptr(), q.shape[1],
+                                             float(scale), bt, block_tables.shape[1], offs,
+                                             block_tables.shape[0], seq, pos, T, sel,
+                                             selected.shape[2], out.data_ptr(),
+                                             _stream(pool.device))
+    _check(st, "pkv_decode_attention_sparse")
 
 
 def copy_blocks(pool: Pool, layer: int, src_blocks: torch.Tensor,

@@ -1,0 +1,826 @@
+// Sparse paged decode attention (pkv_decode_attention_sparse): attention of
+// each query over the blocks selected for it, per kv head.
+//
+// What is computed.  For query token t (sequence b, position P) and query
+// head h of kv head g: softmax attention over the tokens i <= P of the blocks
+// that the list of (t, g) names, K and V read in place through the table.
+//
+// What bounds it: the K and V bytes of the selected blocks, one head of each
+// row (256 bytes for bf16, D 128), read once for the G heads of the group.
+//
+// How.  A cluster of CTAs per (t, g); its warps take the 16-row tiles of the
+// listed blocks in turn.  Each warp runs alone: it looks up 32 tiles at a
+// time (one per lane: list entry, table entry, rows covered), keeps a ring of
+// tiles in flight with 16-byte cp.async copies to its own shared memory (rows
+// that the query does not see arrive as zeros, so whatever they hold never
+// enters a product), and holds its own running softmax state:
+//   bf16: S^T = K Q^T with the tile's 16 tokens as M of mma m16n8k16 and the
+//     heads as N; the weights go to the B operand of O^T += V^T P^T with one
+//     movmatrix per 8 x 8, rounded to bf16 (the type of V: an mma takes one
+//     type); the statistics and O stay in fp32.
+//   int8: the same on fp16 mma over the exact codes, q scaled into fp16 by a
+//     power of two, V's scales folded into the weights under a running power
+//     of two (see decode.cu); the rows of a tile are taken in the order that
+//     makes the byte-transposing V load agree with movmatrix.
+//   fp32: fp32 FMAs, two lanes per token for the scores, D / 32 output dims
+//     per lane.
+// At the end the warps' states (m, l, O) are merged by the log-sum-exp rule
+// out of the shared memories of the whole cluster: no workspace, no second
+// kernel.
+#include <cmath>
+#include <type_traits>
+
+#include <cuda_fp16.h>
+
+#include "cluster.cuh"
+#include "common.cuh"
+
+namespace pkv {
+namespace {
+
+constexpr int kSpWarps = 4;
+constexpr int kSpThreads = kSpWarps * 32;
+constexpr int kTile = 16;  // rows of a tile
+constexpr unsigned kAll = 0xffffffffu;
+constexpr float kLog2e = 1.4426950408889634f;
+
+struct SparseParams {
+  const char* k;
+  const char* v;
+  const char* q;
+  char* out;
+  const int32_t* bt;
+  const int32_t* offs;
+  const int32_t* tok_seq;
+  const int32_t* tok_pos;
+  const int32_t* sel;
+  int* err;
+  long long num_blocks;
+  int batch, mb, bs, L, layer, row_bytes, scale_off, hq, hkv, G, K;
+  int parts;      // tiles of a block
+  float qscale;   // scale * log2(e)
+};
+
+// ---- small helpers -----------------------------------------------------------
+
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool live) {
+  const int n = live ? 16 : 0;
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n)
+               : "memory");
+}
+__device__ __forceinline__ void cp_async4(uint32_t dst, const void* src, bool live) {
+  const int n = live ? 4 : 0;
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(n)
+               : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+__device__ __forceinline__ void ldsm_x4(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ void ldsm_x4_t(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+// Lane l receives bytes of column l / 4 (r0) and l / 4 + 8 (r1), rows
+// 4 (l % 4) .. + 3, of the 16 x 16 byte matrix whose rows lanes 0-15 address.
+__device__ __forceinline__ void ldsm_b8_t(uint32_t& r0, uint32_t& r1, uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m16n16.x1.trans.shared.b8 {%0,%1}, [%2];"
+               : "=r"(r0), "=r"(r1)
+               : "r"(addr)
+               : "memory");
+}
+// Transpose of an 8 x 8 matrix of 16-bit elements held one row pair a lane.
+__device__ __forceinline__ uint32_t movmatrix_t(uint32_t x) {
+  uint32_t r;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
+  return r;
+}
+template <bool HALF>
+__device__ __forceinline__ void mma16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                      uint32_t a3, uint32_t b0, uint32_t b1) {
+  if constexpr (HALF)
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+        "{%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+  else
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+        "{%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint4 lds128(uint32_t a) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "r"(a)
+               : "memory");
+  return v;
+}
+__device__ __forceinline__ float lds_f32(uint32_t a) {
+  float v;
+  asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(a) : "memory");
+  return v;
+}
+__device__ __forceinline__ void sts_f32(uint32_t a, float v) {
+  asm volatile("st.shared.f32 [%0], %1;" ::"r"(a), "f"(v) : "memory");
+}
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+// Four codes (bytes c + 128) to fp16 pairs: 1024 + byte, minus 1152.
+__device__ __forceinline__ void codes_to_f16(uint32_t w, uint32_t& lo, uint32_t& hi) {
+  uint32_t a, b;
+  asm("prmt.b32 %0, %1, 0x64646464, 0x4140;" : "=r"(a) : "r"(w));
+  asm("prmt.b32 %0, %1, 0x64646464, 0x4342;" : "=r"(b) : "r"(w));
+  const __half2 bias = __half2half2(__ushort_as_half(0x6480));
+  const __half2 x = __hsub2(*reinterpret_cast<const __half2*>(&a), bias);
+  const __half2 y = __hsub2(*reinterpret_cast<const __half2*>(&b), bias);
+  lo = *reinterpret_cast<const uint32_t*>(&x);
+  hi = *reinterpret_cast<const uint32_t*>(&y);
+}
+
+// ---- staging -------------------------------------------------------------------
+
+// One tile in a warp's ring: K rows, V rows, and for int8 pools their scales.
+template <int MODE, int D>
+struct Tile {
+  static constexpr int kEs = MODE == PKV_F32 ? 4 : MODE == PKV_BF16 ? 2 : 1;
+  static constexpr int kRow = D * kEs;              // bytes of one head of a row
+  static constexpr int kChunks = kRow / 16;         // 16-byte chunks of it
+  static constexpr int kHalf = kTile * kRow;        // K (or V) rows
+  static constexpr int kScales = MODE == PKV_I8 ? 2 * kTile * 4 : 0;
+  static constexpr int kBytes = 2 * kHalf + kScales;
+  static constexpr int kStages = D == 128 ? (MODE == PKV_F32 ? 2 : MODE == PKV_BF16 ? 3 : 5)
+                                          : (MODE == PKV_F32 ? 3 : MODE == PKV_BF16 ? 5 : 8);
+
+  // Byte offset of chunk c of row r: chunks of a row are permuted so that the
+  // 8 rows of an ldmatrix (and the 2 rows x 4 chunks of an LDS.128 phase of
+  // the int8 K reads) fall in 8 different 16-byte columns.
+  static __device__ __forceinline__ int at(int r, int c) {
+    if constexpr (MODE == PKV_I8) {
+      if constexpr (D == 64) return r * kRow + ((c ^ ((r >> 1) & 3)) << 4);
+      return r * kRow + ((c ^ (((r & 1) << 2) | ((r >> 1) & 3))) << 4);
+    }
+    return r * kRow + ((c ^ (r & 7)) << 4);
+  }
+
+  // Start the copies of rows [lo, hi) of the tile whose row 0 is token row
+  // `row`; the other rows are filled with zeros (no byte of them is read).
+  static __device__ __forceinline__ void load(const SparseParams& p, uint32_t dst, long long row,
+                                              int g, int lo, int hi, int lane) {
+    constexpr int RPI = 32 / (kChunks < 32 ? kChunks : 32);  // rows of one instruction
+    const char* kb = p.k + row * p.row_bytes + g * kRow;
+    const char* vb = p.v + row * p.row_bytes + g * kRow;
+    const int c = lane % kChunks, r0 = lane / kChunks;
+#pragma unroll
+    for (int i = 0; i < kTile / RPI; ++i) {
+      const int r = i * RPI + r0;
+      const bool live = r >= lo && r < hi;
+      const long long off = live ? (long long)r * p.row_bytes + c * 16 : 0;
+      cp_async16(dst + at(r, c), kb + off, live);
+      cp_async16(dst + kHalf + at(r, c), vb + off, live);
+    }
+    if constexpr (MODE == PKV_I8) {
+      const int r = lane & 15;
+      const bool live = r >= lo && r < hi;
+      const char* src = (lane < 16 ? p.k : p.v) +
+                        (row + (live ? r : 0)) * p.row_bytes + p.scale_off + 4 * g;
+      cp_async4(dst + 2 * kHalf + lane * 4, src, live);
+    }
+  }
+};
+
+// ---- consumers: the running state of one warp ------------------------------------
+
+// Tensor-core state for bf16 and int8 pools.
+template <int MODE, int D, int NT>
+struct MmaState {
+  static constexpr bool kI8 = MODE == PKV_I8;
+  static constexpr int KS = D / 16;
+  using Tl = Tile<MODE, D>;
+  uint32_t qb[NT][KS][2];
+  float o[NT][KS][4];
+  float m[NT][2], l[NT][2];
+  float qs[NT][2];  // factor of the scores of columns 2 qi, 2 qi + 1
+  int ev;           // int8: biased exponent of the running V-scale normaliser
+  float vf;         // 2^(127 - ev)
+
+  __device__ void init(const SparseParams& p, int t, int g, int lane) {
+    const int gl = lane >> 2, qi = lane & 3;
+    ev = 0;
+    vf = __uint_as_float(254u << 23);
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      m[nt][0] = m[nt][1] = -INFINITY;
+      l[nt][0] = l[nt][1] = 0.f;
+#pragma unroll
+      for (int k = 0; k < KS; ++k)
+#pragma unroll
+        for (int c = 0; c < 4; ++c) o[nt][k][c] = 0.f;
+      const int h = nt * 8 + gl;
+      const bool live = h < p.G;
+      const char* src = p.q + ((long long)t * p.hq + g * p.G + (live ? h : 0)) * (D * 2);
+      if constexpr (!kI8) {
+#pragma unroll
+        for (int k = 0; k < KS; ++k)
+#pragma unroll
+          for (int i = 0; i < 2; ++i)
+            qb[nt][k][i] = live ? *reinterpret_cast<const uint32_t*>(
+                                      src + (k * 16 + i * 8 + qi * 2) * 2)
+                                : 0u;
+        qs[nt][0] = qs[nt][1] = p.qscale;
+      } else {
+        // dims i * 64 + qi * 16 .. + 15: the order of the K codes (scores())
+        uint32_t w[KS / 4][8], mx = 0;
+#pragma unroll
+        for (int i = 0; i < KS / 4; ++i)
+#pragma unroll
+          for (int v = 0; v < 2; ++v) {
+            const uint4 r = live ? *reinterpret_cast<const uint4*>(src + (i * 64 + qi * 16) * 2 +
+                                                                   16 * v)
+                                 : make_uint4(0, 0, 0, 0);
+            w[i][4 * v] = r.x; w[i][4 * v + 1] = r.y; w[i][4 * v + 2] = r.z; w[i][4 * v + 3] = r.w;
+          }
+#pragma unroll
+        for (int i = 0; i < KS / 4; ++i)
+#pragma unroll
+          for (int k = 0; k < 8; ++k)
+            mx = max(mx, max(w[i][k] & 0x7FFFu, (w[i][k] >> 16) & 0x7FFFu));
+        mx = max(mx, __shfl_xor_sync(kAll, mx, 1));
+        mx = max(mx, __shfl_xor_sync(kAll, mx, 2));
+        // 2^e brings the absmax into [2^14, 2^15): fp16 holds every bf16
+        // value down to 2^-28 of it exactly
+        int e = 0;
+        if (mx != 0) e = min(126, max(-126, 141 - (int)((mx >> 7) & 0xFF)));
+        const float up = __uint_as_float((uint32_t)(127 + e) << 23);
+        const float down = __uint_as_float((uint32_t)(127 - e) << 23);
+#pragma unroll
+        for (int i = 0; i < KS / 4; ++i)
+#pragma unroll
+          for (int k = 0; k < 8; ++k)
+            qb[nt][i * 4 + k / 2][k & 1] =
+                pack_f16x2(bf16_lo(w[i][k]) * up, bf16_hi(w[i][k]) * up);
+        qs[nt][0] = p.qscale * __shfl_sync(kAll, down, 8 * qi);
+        qs[nt][1] = p.qscale * __shfl_sync(kAll, down, 8 * qi + 4);
+      }
+    }
+  }
+
+  // One staged tile; rows [lo, hi) are the ones the query sees.
+  __device__ void step(uint32_t st, int lo, int hi, int lane) {
+    const int gl = lane >> 2, qi = lane & 3;
+    // the tokens of this lane's two score rows
+    const int t0 = kI8 ? 4 * (gl >> 1) + (gl & 1) : gl, t1 = kI8 ? t0 + 2 : gl + 8;
+    const bool in0 = t0 >= lo && t0 < hi, in1 = t1 >= lo && t1 < hi;
+    float s[NT][4];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int c = 0; c < 4; ++c) s[nt][c] = 0.f;
+    if constexpr (!kI8) {
+      const int r = (lane & 7) + ((lane >> 3) & 1) * 8, cc = lane >> 4;
+#pragma unroll
+      for (int k = 0; k < KS; ++k) {
+        uint32_t a[4];
+        ldsm_x4(a, st + Tl::at(r, 2 * k + cc));
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+          mma16<false>(s[nt], a[0], a[1], a[2], a[3], qb[nt][k][0], qb[nt][k][1]);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < KS / 4; ++i) {
+        const uint4 x = lds128(st + Tl::at(t0, 4 * i + qi)), y = lds128(st + Tl::at(t1, 4 * i + qi));
+        const uint32_t xw[4] = {x.x, x.y, x.z, x.w}, yw[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          uint32_t a0, a1, a2, a3;
+          codes_to_f16(xw[j], a0, a2);
+          codes_to_f16(yw[j], a1, a3);
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+            mma16<true>(s[nt], a0, a1, a2, a3, qb[nt][i * 4 + j][0], qb[nt][i * 4 + j][1]);
+        }
+      }
+    }
+    float sk0 = 1.f, sk1 = 1.f, w0 = 1.f, w1 = 1.f, rescale = 1.f;
+    if constexpr (kI8) {
+      const uint32_t sc = st + 2 * Tl::kHalf;
+      sk0 = lds_f32(sc + t0 * 4);
+      sk1 = lds_f32(sc + t1 * 4);
+      const float sv0 = lds_f32(sc + (16 + t0) * 4), sv1 = lds_f32(sc + (16 + t1) * 4);
+      int et = max((int)((__float_as_uint(sv0) >> 23) & 0xFF),
+                   (int)((__float_as_uint(sv1) >> 23) & 0xFF));
+      if (__any_sync(kAll, et > ev)) {
+        et = __reduce_max_sync(kAll, et);
+        const int en = min(253, max(ev, et));
+        rescale = ev - en >= -126 ? __uint_as_float((uint32_t)(127 + ev - en) << 23) : 0.f;
+        vf = __uint_as_float((uint32_t)(254 - en) << 23);
+        ev = en;
+      }
+      w0 = sv0 * vf;
+      w1 = sv1 * vf;
+    }
+    uint32_t pb[NT][2];
+    float a[NT][2];
+    bool moved = false;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      s[nt][0] = in0 ? s[nt][0] * qs[nt][0] * sk0 : -INFINITY;
+      s[nt][1] = in0 ? s[nt][1] * qs[nt][1] * sk0 : -INFINITY;
+      s[nt][2] = in1 ? s[nt][2] * qs[nt][0] * sk1 : -INFINITY;
+      s[nt][3] = in1 ? s[nt][3] * qs[nt][1] * sk1 : -INFINITY;
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        float mx = fmaxf(s[nt][c], s[nt][c + 2]);
+        a[nt][c] = 1.f;
+        // the running maximum moves only where some lane passes it
+        if (__any_sync(kAll, mx > m[nt][c])) {
+          mx = fmaxf(mx, __shfl_xor_sync(kAll, mx, 4));
+          mx = fmaxf(mx, __shfl_xor_sync(kAll, mx, 8));
+          mx = fmaxf(mx, __shfl_xor_sync(kAll, mx, 16));
+          const float n = fmaxf(m[nt][c], mx);
+          // nothing but -inf so far: there is nothing to rescale
+          a[nt][c] = m[nt][c] == -INFINITY ? 0.f : exp2f(m[nt][c] - n);
+          m[nt][c] = n;
+        }
+        // scores of -inf carry no weight, even while they are all there is
+        const float base = m[nt][c] == -INFINITY ? 0.f : m[nt][c];
+        s[nt][c] = exp2f(s[nt][c] - base);
+        s[nt][c + 2] = exp2f(s[nt][c + 2] - base);
+        l[nt][c] = l[nt][c] * a[nt][c] + s[nt][c] + s[nt][c + 2];
+        a[nt][c] *= rescale;
+        moved |= a[nt][c] != 1.f;
+      }
+      if constexpr (kI8) {
+        pb[nt][0] = movmatrix_t(pack_f16x2(s[nt][0] * w0, s[nt][1] * w0));
+        pb[nt][1] = movmatrix_t(pack_f16x2(s[nt][2] * w1, s[nt][3] * w1));
+      } else {
+        pb[nt][0] = movmatrix_t(pack_bf16x2(s[nt][0], s[nt][1]));
+        pb[nt][1] = movmatrix_t(pack_bf16x2(s[nt][2], s[nt][3]));
+      }
+    }
+    if (__any_sync(kAll, moved)) {
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int k = 0; k < KS; ++k) {
+          o[nt][k][0] *= a[nt][0];
+          o[nt][k][1] *= a[nt][1];
+          o[nt][k][2] *= a[nt][0];
+          o[nt][k][3] *= a[nt][1];
+        }
+    }
+    const uint32_t sv = st + Tl::kHalf;
+    if constexpr (!kI8) {
+      const int r = (lane & 7) + (lane >> 4) * 8, cc = (lane >> 3) & 1;
+#pragma unroll
+      for (int k = 0; k < KS; ++k) {
+        uint32_t v[4];
+        ldsm_x4_t(v, sv + Tl::at(r, 2 * k + cc));
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+          mma16<false>(o[nt][k], v[0], v[1], v[2], v[3], pb[nt][0], pb[nt][1]);
+      }
+    } else {
+#pragma unroll
+      for (int k = 0; k < KS; ++k) {
+        uint32_t r0, r1, a0, a1, a2, a3;
+        ldsm_b8_t(r0, r1, sv + Tl::at(lane & 15, k));
+        codes_to_f16(r0, a0, a2);
+        codes_to_f16(r1, a1, a3);
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+          mma16<true>(o[nt][k], a0, a1, a2, a3, pb[nt][0], pb[nt][1]);
+      }
+    }
+  }
+
+  // The state to shared memory: O as [head][D], then (m, l) of each head.
+  __device__ void put(const SparseParams& p, uint32_t acc, uint32_t ml, int lane) {
+    const int gl = lane >> 2, qi = lane & 3;
+    // int8: back to the units of V (0 when every V scale was 0 or subnormal)
+    const float back = !kI8 ? 1.f : ev >= 1 ? __uint_as_float((uint32_t)ev << 23) : 0.f;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        float x = l[nt][c];
+        x += __shfl_xor_sync(kAll, x, 4);
+        x += __shfl_xor_sync(kAll, x, 8);
+        x += __shfl_xor_sync(kAll, x, 16);
+        const int h = nt * 8 + 2 * qi + c;
+        if (h < p.G) {
+          if (gl == 0) {
+            sts_f32(ml + h * 8, m[nt][c]);
+            sts_f32(ml + h * 8 + 4, x);
+          }
+#pragma unroll
+          for (int k = 0; k < KS; ++k) {
+            sts_f32(acc + (h * D + k * 16 + gl) * 4, o[nt][k][c] * back);
+            sts_f32(acc + (h * D + k * 16 + gl + 8) * 4, o[nt][k][c + 2] * back);
+          }
+        }
+      }
+  }
+};
+
+// fp32 state: GP heads (G rounded up), q and the weights in shared memory.
+template <int D, int GP>
+struct FmaState {
+  using Tl = Tile<PKV_F32, D>;
+  static constexpr int PD = D / 32;  // output dims of a lane
+  float o[GP][PD], m[GP], l[GP];     // l: this lane's token's share
+  uint32_t sq, sp;
+
+  static constexpr int kExtra = (GP * D + kTile * GP) * 4;  // q, weights
+
+  __device__ void init(const SparseParams& p, int t, int g, int lane, uint32_t extra) {
+    sq = extra;
+    sp = extra + GP * D * 4;
+#pragma unroll
+    for (int h = 0; h < GP; ++h) {
+      m[h] = -INFINITY;
+      l[h] = 0.f;
+#pragma unroll
+      for (int e = 0; e < PD; ++e) o[h][e] = 0.f;
+    }
+    const float* src = reinterpret_cast<const float*>(p.q) + ((long long)t * p.hq + g * p.G) * D;
+    for (int i = lane; i < GP * D; i += 32)
+      sts_f32(sq + i * 4, i < p.G * D ? src[i] * p.qscale : 0.f);
+    __syncwarp();
+  }
+
+  __device__ void step(uint32_t st, int lo, int hi, int lane) {
+    const int tok = lane & 15, side = lane >> 4;  // two lanes a token, half the dims each
+    const bool in = tok >= lo && tok < hi;
+#pragma unroll
+    for (int h0 = 0; h0 < GP; h0 += 4) {
+      float s[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
+      for (int c = 0; c < D / 8; ++c) {
+        const int ch = side * (D / 8) + c;
+        const uint4 kr = lds128(st + Tl::at(tok, ch));
+#pragma unroll
+        for (int h = 0; h < 4; ++h) {
+          const uint4 qr = lds128(sq + ((h0 + h) * D + ch * 4) * 4);
+          s[h] = fmaf(__uint_as_float(qr.x), __uint_as_float(kr.x), s[h]);
+          s[h] = fmaf(__uint_as_float(qr.y), __uint_as_float(kr.y), s[h]);
+          s[h] = fmaf(__uint_as_float(qr.z), __uint_as_float(kr.z), s[h]);
+          s[h] = fmaf(__uint_as_float(qr.w), __uint_as_float(kr.w), s[h]);
+        }
+      }
+#pragma unroll
+      for (int h = 0; h < 4; ++h) {
+        float x = s[h] + __shfl_xor_sync(kAll, s[h], 16);
+        x = in ? x : -INFINITY;
+        float a = 1.f;
+        if (__any_sync(kAll, x > m[h0 + h])) {
+          float mx = x;
+#pragma unroll
+          for (int b = 8; b; b >>= 1) mx = fmaxf(mx, __shfl_xor_sync(kAll, mx, b));
+          const float n = fmaxf(m[h0 + h], mx);
+          a = m[h0 + h] == -INFINITY ? 0.f : exp2f(m[h0 + h] - n);
+          m[h0 + h] = n;
+#pragma unroll
+          for (int e = 0; e < PD; ++e) o[h0 + h][e] *= a;
+        }
+        const float w = exp2f(x - (m[h0 + h] == -INFINITY ? 0.f : m[h0 + h]));
+        l[h0 + h] = l[h0 + h] * a + w;
+        if (side == 0) sts_f32(sp + (tok * GP + h0 + h) * 4, w);
+      }
+    }
+    __syncwarp();
+    const uint32_t sv = st + Tl::kHalf;
+#pragma unroll 4
+    for (int t = 0; t < kTile; ++t) {
+      float v[PD];
+      const int byte = lane * PD * 4;
+      const uint32_t va = sv + Tl::at(t, byte >> 4) + (byte & 15);
+      if constexpr (PD == 4) {
+        const uint4 r = lds128(va);
+        v[0] = __uint_as_float(r.x); v[1] = __uint_as_float(r.y);
+        v[2] = __uint_as_float(r.z); v[3] = __uint_as_float(r.w);
+      } else {
+#pragma unroll
+        for (int e = 0; e < PD; ++e) v[e] = lds_f32(va + 4 * e);
+      }
+#pragma unroll
+      for (int h0 = 0; h0 < GP; h0 += 4) {
+        const uint4 w = lds128(sp + (t * GP + h0) * 4);
+        const float wf[4] = {__uint_as_float(w.x), __uint_as_float(w.y), __uint_as_float(w.z),
+                             __uint_as_float(w.w)};
+#pragma unroll
+        for (int h = 0; h < 4; ++h)
+#pragma unroll
+          for (int e = 0; e < PD; ++e) o[h0 + h][e] = fmaf(wf[h], v[e], o[h0 + h][e]);
+      }
+    }
+    __syncwarp();
+  }
+
+  __device__ void put(const SparseParams& p, uint32_t acc, uint32_t ml, int lane) {
+#pragma unroll
+    for (int h = 0; h < GP; ++h) {
+      float x = l[h];
+#pragma unroll
+      for (int b = 8; b; b >>= 1) x += __shfl_xor_sync(kAll, x, b);
+      if (h < p.G) {
+        if (lane == 0) {
+          sts_f32(ml + h * 8, m[h]);
+          sts_f32(ml + h * 8 + 4, x);
+        }
+#pragma unroll
+        for (int e = 0; e < PD; ++e) sts_f32(acc + (h * D + lane * PD + e) * 4, o[h][e]);
+      }
+    }
+  }
+};
+
+// ---- the kernel -------------------------------------------------------------------
+
+// HEADS: heads the state holds (8 NT for the tensor cores, GP for fp32).
+template <int MODE, int D, int HEADS>
+struct Layout {
+  using Tl = Tile<MODE, D>;
+  static constexpr int kRing = Tl::kStages * Tl::kBytes;
+  static constexpr int kState = HEADS * D * 4 + HEADS * 8;  // of the merge; over the ring
+  static constexpr int kBody = (kRing > kState ? kRing : kState);
+  static constexpr int kExtra = MODE == PKV_F32 ? FmaState<D, HEADS>::kExtra : 0;
+  static constexpr int kWarp = (kBody + kExtra + 127) / 128 * 128;
+  static constexpr int kBytes = kSpWarps * kWarp;
+};
+
+template <int MODE, int D, int HEADS>
+__global__ void __launch_bounds__(kSpThreads) sparse_decode_kernel(const SparseParams p) {
+  using Tl = Tile<MODE, D>;
+  using Lay = Layout<MODE, D, HEADS>;
+  constexpr int NST = Tl::kStages;
+  extern __shared__ __align__(128) unsigned char smem[];
+  griddep_wait();
+  griddep_launch_dependents();
+  uint32_t S;
+  asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(S));
+  const uint32_t rank = cluster_rank();
+  const int row = blockIdx.x / S;
+  const int t = row / p.hkv, g = row - t * p.hkv;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+
+  const int seq = p.tok_seq[t], pos = p.tok_pos[t];
+  if (seq < 0) return;  // padding: the whole cluster leaves, nothing is written
+  int off = 0, end = 0;  // table positions [off, end) are seen
+  if (seq >= p.batch) {
+    if (rank == 0 && tid == 0) set_error(p.err, kErrIndex);
+  } else {
+    off = p.offs ? p.offs[seq] : 0;
+    if (off < 0 || off >= p.bs || pos < 0 || (long long)off + pos >= (long long)p.mb * p.bs) {
+      if (rank == 0 && tid == 0) set_error(p.err, kErrCapacity);
+    } else {
+      end = off + pos + 1;
+    }
+  }
+  const int tiles = end > 0 ? p.K * p.parts : 0;  // a bad token sees nothing: zeros
+
+  const uint32_t base = smem_addr(smem);
+  const uint32_t ring = base + warp * Lay::kWarp;
+  std::conditional_t<MODE == PKV_F32, FmaState<D, HEADS>,
+                     MmaState<MODE == PKV_F32 ? PKV_BF16 : MODE, D, (HEADS + 7) / 8>>
+      state;
+  if constexpr (MODE == PKV_F32)
+    state.init(p, t, g, lane, ring + Lay::kBody);
+  else
+    state.init(p, t, g, lane);
+
+  // ---- lookup: 32 tiles a time, one per lane ----
+  const int32_t* list = p.sel + (long long)row * p.K;
+  const int32_t* table = p.bt + (long long)(end > 0 ? seq : 0) * p.mb;
+  const int stride = (int)S * kSpWarps;
+  const int rows_tile = min(p.bs, kTile);
+  int next = (int)rank * kSpWarps + warp;  // first tile of the batch to come
+  long long my_row = 0;
+  int my_range = 0;
+  unsigned todo = 0;
+  auto lookup = [&]() {
+    // stops at the last batch or at one that has something to do
+    while (todo == 0 && next < tiles) {
+      const long long ts = next + (long long)lane * stride;
+      int lo = 0, hi = 0;
+      if (ts < tiles) {
+        const int j = list[ts / p.parts];
+        if (j >= p.mb) {
+          set_error(p.err, kErrIndex);
+        } else if (j >= 0) {
+          const int r0 = (int)(ts % p.parts) * kTile;
+          const int p0 = j * p.bs + r0;
+          lo = max(0, off - p0);
+          hi = min(rows_tile, end - p0);
+          if (lo < hi) {
+            const int blk = table[j];
+            if (blk < 0 || blk >= p.num_blocks) {
+              set_error(p.err, kErrIndex);
+              hi = 0;
+            } else {
+              my_row = ((long long)blk * p.L + p.layer) * p.bs + r0;
+            }
+          }
+        }
+      }
+      my_range = lo | hi << 8;
+      todo = __ballot_sync(kAll, lo < hi);
+      next = tiles - next <= 32 * stride ? tiles : next + 32 * stride;
+    }
+  };
+  int ranges = 0;  // lane s: the rows of the tile in stage s
+  auto issue = [&](int stage) {
+    lookup();
+    if (todo) {
+      const int src = __ffs(todo) - 1;
+      todo &= todo - 1;
+      const long long r = __shfl_sync(kAll, my_row, src);
+      const int range = __shfl_sync(kAll, my_range, src);
+      if (lane == stage) ranges = range;
+      Tl::load(p, ring + stage * Tl::kBytes, r, g, range & 0xff, range >> 8, lane);
+    } else if (lane == stage) {
+      ranges = 0;
+    }
+    cp_commit();
+  };
+
+#pragma unroll 1
+  for (int s = 0; s < NST - 1; ++s) issue(s);
+  int stage = 0;
+#pragma unroll 1
+  while (true) {
+    cp_wait<NST - 2>();
+    __syncwarp();
+    const int range = __shfl_sync(kAll, ranges, stage);
+    if (range == 0) break;
+    issue(stage == 0 ? NST - 1 : stage - 1);
+    state.step(ring + stage * Tl::kBytes, range & 0xff, range >> 8, lane);
+    if (++stage == NST) stage = 0;
+  }
+  cp_wait<0>();
+  __syncwarp();
+
+  // ---- merge of the cluster's warps ----
+  const uint32_t acc = ring, ml = ring + HEADS * D * 4;
+  state.put(p, acc, ml, lane);
+  if (S > 1)
+    cluster_sync();
+  else
+    __syncthreads();
+  const int pairs = p.G * (D / 2);
+  for (int i = (int)rank * kSpThreads + tid; i < pairs; i += (int)S * kSpThreads) {
+    const int h = i / (D / 2), d = (i % (D / 2)) * 2;
+    float M = -INFINITY;
+    for (uint32_t r = 0; r < S; ++r)
+#pragma unroll
+      for (int w = 0; w < kSpWarps; ++w)
+        M = fmaxf(M, ld_cluster_f32(
+                         cluster_map(base + w * Lay::kWarp + HEADS * D * 4 + h * 8, r)));
+    float x = 0.f, y = 0.f, l = 0.f;
+    for (uint32_t r = 0; r < S; ++r)
+#pragma unroll
+      for (int w = 0; w < kSpWarps; ++w) {
+        const uint32_t a = cluster_map(base + w * Lay::kWarp, r);
+        const float m = ld_cluster_f32(a + HEADS * D * 4 + h * 8);
+        const float lw = ld_cluster_f32(a + HEADS * D * 4 + h * 8 + 4);
+        if (m == -INFINITY && lw == 0.f) continue;  // saw nothing
+        const float f = m == -INFINITY ? 1.f : exp2f(m - M);  // (NaN scores leave m at -inf)
+        l += f * lw;
+        x += f * ld_cluster_f32(a + (h * D + d) * 4);
+        y += f * ld_cluster_f32(a + (h * D + d) * 4 + 4);
+      }
+    const float inv = l > 0.f || l != l ? 1.f / l : 0.f;  // no weight at all: zeros
+    const long long at = ((long long)t * p.hq + g * p.G + h) * D + d;
+    if constexpr (MODE == PKV_F32) {
+      *reinterpret_cast<float2*>(p.out + at * 4) = make_float2(x * inv, y * inv);
+    } else {
+      *reinterpret_cast<uint32_t*>(p.out + at * 2) = pack_bf16x2(x * inv, y * inv);
+    }
+  }
+  if (S > 1) cluster_sync();  // no CTA leaves while another may still read its states
+}
+
+template <int MODE, int D, int HEADS>
+cudaError_t launch_sparse_heads(const SparseParams& p, unsigned rows, unsigned S, cudaStream_t s) {
+  return launch_clusters(sparse_decode_kernel<MODE, D, HEADS>, dim3(rows * S), dim3(kSpThreads),
+                         Layout<MODE, D, HEADS>::kBytes, S, s, p);
+}
+
+template <int MODE, int D>
+cudaError_t launch_sparse_d(const SparseParams& p, unsigned rows, unsigned S, cudaStream_t s) {
+  if constexpr (MODE == PKV_F32) {
+    if (p.G <= 4) return launch_sparse_heads<MODE, D, 4>(p, rows, S, s);
+  }
+  if (p.G <= 8) return launch_sparse_heads<MODE, D, 8>(p, rows, S, s);
+  return launch_sparse_heads<MODE, D, 16>(p, rows, S, s);
+}
+
+bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
+
+constexpr int kSpMaxCluster = 8;
+
+}  // namespace
+}  // namespace pkv
+
+extern "C" pkv_status pkv_decode_attention_sparse(
+    const pkv_pool* pool, int32_t layer, const void* q, int32_t num_q_heads, float scale,
+    const int32_t* block_tables, int32_t max_blocks_per_seq, const int32_t* offsets, int32_t batch,
+    const int32_t* token_seq, const int32_t* token_pos, int32_t num_tokens,
+    const int32_t* selected, int32_t num_selected, void* out, cudaStream_t stream) {
+  pkv::PoolView v;
+  int st = pkv::pool_view(pool, true, &v);
+  if (st != PKV_OK) return (pkv_status)st;
+  if (layer < 0 || layer >= v.num_layers || batch < 0 || num_tokens < 0 || num_q_heads <= 0 ||
+      num_selected < 0 || num_q_heads % v.num_kv_heads != 0 || !std::isfinite(scale))
+    return PKV_ERR_INVALID_ARG;
+  const int G = num_q_heads / v.num_kv_heads;
+  if ((v.head_dim != 64 && v.head_dim != 128) || G > 16) return PKV_ERR_UNSUPPORTED;
+  if (num_tokens == 0) return PKV_OK;
+  if (!q || !out || !token_seq || !token_pos || (num_selected > 0 && !selected) ||
+      (batch > 0 && (!block_tables || max_blocks_per_seq <= 0)))
+    return PKV_ERR_INVALID_ARG;
+  if (!pkv::aligned(q, 16) || !pkv::aligned(out, 16) || !pkv::aligned(block_tables, 4) ||
+      !pkv::aligned(offsets, 4) || !pkv::aligned(token_seq, 4) || !pkv::aligned(token_pos, 4) ||
+      !pkv::aligned(selected, 4))
+    return PKV_ERR_INVALID_ARG;
+  const int mb = batch > 0 ? max_blocks_per_seq : 1;
+  const int parts = v.block_size > pkv::kTile ? v.block_size / pkv::kTile : 1;
+  const int64_t rows = (int64_t)num_tokens * v.num_kv_heads;
+  const int64_t tiles = (int64_t)num_selected * parts;
+  // table positions and tiles are 32-bit in the kernel
+  if ((int64_t)mb * v.block_size > INT32_MAX || tiles > (1 << 30) ||
+      rows > INT32_MAX / pkv::kSpMaxCluster)
+    return PKV_ERR_UNSUPPORTED;
+  int optin, grid, validate, sms;
+  int* err;
+  if ((st = pkv::device_facts(&optin, &err, &grid, &validate)) != PKV_OK) return (pkv_status)st;
+  if ((st = pkv::device_sm_count(&sms)) != PKV_OK) return (pkv_status)st;
+  if (validate) {
+    if ((st = pkv::clear_error_word(err, stream)) != PKV_OK) return (pkv_status)st;
+    if ((st = pkv::launch_status(pkv::launch_validate_tokens(
+             v, block_tables, mb, offsets, batch, token_seq, token_pos, num_tokens, err,
+             stream))) != PKV_OK)
+      return (pkv_status)st;
+    if ((st = pkv::read_and_clear_error_word(err, stream)) != PKV_OK) return (pkv_status)st;
+  }
+  // CTAs of a cluster: until two per SM are there, each warp with a few tiles.
+  unsigned S = 1;
+  while ((int)S < pkv::kSpMaxCluster && rows * S < 2 * sms && tiles > S * pkv::kSpWarps * 2)
+    S *= 2;
+  pkv::SparseParams p;
+  p.k = v.k;
+  p.v = v.v;
+  p.q = static_cast<const char*>(q);
+  p.out = static_cast<char*>(out);
+  p.bt = block_tables;
+  p.offs = offsets;
+  p.tok_seq = token_seq;
+  p.tok_pos = token_pos;
+  p.sel = selected;
+  p.err = err;
+  p.num_blocks = v.num_blocks;
+  p.batch = batch;
+  p.mb = mb;
+  p.bs = v.block_size;
+  p.L = v.num_layers;
+  p.layer = layer;
+  p.row_bytes = v.row_bytes;
+  p.scale_off = v.scale_off;
+  p.hq = num_q_heads;
+  p.hkv = v.num_kv_heads;
+  p.G = G;
+  p.K = num_selected;
+  p.parts = parts;
+  p.qscale = scale * pkv::kLog2e;
+  const unsigned r = (unsigned)rows;
+  const bool d64 = v.head_dim == 64;
+  cudaError_t e;
+  if (v.quant)
+    e = d64 ? pkv::launch_sparse_d<PKV_I8, 64>(p, r, S, stream)
+            : pkv::launch_sparse_d<PKV_I8, 128>(p, r, S, stream);
+  else if (v.io_size == 2)
+    e = d64 ? pkv::launch_sparse_d<PKV_BF16, 64>(p, r, S, stream)
+            : pkv::launch_sparse_d<PKV_BF16, 128>(p, r, S, stream);
+  else
+    e = d64 ? pkv::launch_sparse_d<PKV_F32, 64>(p, r, S, stream)
+            : pkv::launch_sparse_d<PKV_F32, 128>(p, r, S, stream);
+  if ((st = pkv::launch_status(e)) != PKV_OK) return (pkv_status)st;
+  return validate ? (pkv_status)pkv::read_and_clear_error_word(err, stream) : PKV_OK;
+}
