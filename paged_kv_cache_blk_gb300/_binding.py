@@ -153,7 +153,8 @@ def _ptr(t: Optional[torch.Tensor]) -> Optional[int]:
 
 
 def _stream(dev: torch.device) -> int:
-    return torch.cuda.current_stream(dev).cuda_stream
+    # the handle alone: torch.cuda.current_stream builds a Stream object around it
+    return torch._C._cuda_getCurrentRawStream(dev.index)
 
 
 def int8_row_bytes(num_kv_heads: int, head_dim: int) -> int:
@@ -194,10 +195,9 @@ class Pool:
         self.num_blocks, self.num_layers, self.block_size = N, L, bs
         self.num_kv_heads, self.head_dim = H, D
         self.dtype = k_cache.dtype
-
-    @property
-    def ref(self):
-        return ctypes.byref(self.struct)
+        # type of q, out and new rows
+        self.row_dtype = torch.bfloat16 if k_cache.dtype == torch.uint8 else k_cache.dtype
+        self.ref = ctypes.byref(self.struct)
 
 
 class _NoSwitch:
@@ -277,6 +277,7 @@ class Rope:
                  inv_freq: Optional[Sequence[float]] = None, attn_scale: float = 1.0):
         lib = load()
         self.struct = _RopeStruct()
+        self.ref = ctypes.byref(self.struct)
         if inv_freq is not None:
             f = np.ascontiguousarray(np.asarray(inv_freq, dtype=np.float64))
             if f.shape != (rotary_dim // 2,):
@@ -295,37 +296,36 @@ class Rope:
         self.rotary_dim, self.interleaved = rotary_dim, bool(interleaved)
         self.attn_scale = float(self.struct.attn_scale)
 
-    @property
-    def ref(self):
-        return ctypes.byref(self.struct)
+
+_INT32, _BF16, _U8 = torch.int32, torch.bfloat16, torch.uint8
 
 
+# The checks below run on every call and a call's kernels may take a few
+# microseconds, so each reads a tensor's properties once and compares whole
+# tuples.
 def _index(t: Optional[torch.Tensor], pool: Pool, name: str, ndim: int) -> Optional[int]:
     """Pointer of a contiguous int32 index tensor on the pool's device."""
     if t is None:
         return None
-    if t.dtype != torch.int32 or t.device != pool.device or t.dim() != ndim \
+    if t.dtype is not _INT32 or t.device != pool.device or t.dim() != ndim \
             or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous int32 tensor of {ndim} dimension(s) on "
                          f"{pool.device}")
     return t.data_ptr()
 
 
-def _rows_of(t: torch.Tensor, pool: Pool, name: str, tokens: int, heads: Optional[int]) -> int:
+def _rows_of(t: torch.Tensor, pool: Pool, name: str, shape: Tuple[int, int, int]) -> int:
     """Elements between tokens of a [tokens, heads, head_dim] tensor in the
     pool's row type, the heads of a token consecutive."""
-    dtype = torch.bfloat16 if pool.dtype == torch.uint8 else pool.dtype
-    if t.dtype != dtype or t.device != pool.device:
-        raise ValueError(f"{name} must be {dtype} on {pool.device}")
-    if t.dim() != 3 or t.shape[0] != tokens or t.shape[2] != pool.head_dim \
-            or (heads is not None and t.shape[1] != heads):
-        raise ValueError(f"{name} must be [{tokens}, {heads or 'heads'}, {pool.head_dim}], "
-                         f"not {tuple(t.shape)}")
-    s = t.stride()
-    row = t.shape[1] * t.shape[2]
-    if s[2] != 1 or (s[1] != t.shape[2] and t.shape[1] > 1):
+    if t.shape != shape:
+        raise ValueError(f"{name} must be {list(shape)}, not {list(t.shape)}")
+    if t.dtype is not pool.row_dtype or t.device != pool.device:
+        raise ValueError(f"{name} must be {pool.row_dtype} on {pool.device}")
+    tokens, heads, d = shape
+    st, sh, sd = t.stride()
+    if sd != 1 or (sh != d and heads > 1):
         raise ValueError(f"the heads of a token of {name} must be consecutive")
-    return row if tokens <= 1 else s[0]
+    return st if tokens > 1 else heads * d
 
 
 def rope_append(pool: Pool, layer: int, rope: Rope, block_tables: torch.Tensor,
@@ -339,31 +339,33 @@ def rope_append(pool: Pool, layer: int, rope: Rope, block_tables: torch.Tensor,
     position is ``rope_pos`` where given, else ``token_pos``.  Tokens of q,
     k_new, v_new and q_out may lie apart (slices of one projection)."""
     lib = load()
-    T = token_seq.numel()
+    T, = token_seq.shape
+    B, mb = block_tables.shape
     bt, offs = _index(block_tables, pool, "block_tables", 2), _index(offsets, pool, "offsets", 1)
     seq, pos = _index(token_seq, pool, "token_seq", 1), _index(token_pos, pool, "token_pos", 1)
     rpos = _index(rope_pos, pool, "rope_pos", 1)
-    B = block_tables.shape[0]
-    if token_pos.numel() != T or (rope_pos is not None and rope_pos.numel() != T):
+    if token_pos.shape[0] != T or (rope_pos is not None and rope_pos.shape[0] != T):
         raise ValueError("token_seq, token_pos and rope_pos must have the same length")
-    if offsets is not None and offsets.numel() != B:
+    if offsets is not None and offsets.shape[0] != B:
         raise ValueError("offsets must have one entry per row of block_tables")
     if slot_mapping is not None and (slot_mapping.dtype != torch.int64 or slot_mapping.numel() != T
                                      or slot_mapping.device != pool.device
                                      or not slot_mapping.is_contiguous()):
         raise ValueError("slot_mapping must be a contiguous int64 tensor with an entry per token")
-    if (q is None) != (q_out is None):
+    H, D = pool.num_kv_heads, pool.head_dim
+    hq = qs = qos = 0
+    qp = qop = None
+    if q is not None and q_out is not None:
+        hq = q.shape[1]
+        qs, qos = _rows_of(q, pool, "q", (T, hq, D)), _rows_of(q_out, pool, "q_out", (T, hq, D))
+        qp, qop = q.data_ptr(), q_out.data_ptr()
+    elif q is not None or q_out is not None:
         raise ValueError("q and q_out go together")
-    hq = 0 if q is None else q.shape[1]
-    qs = 0 if q is None else _rows_of(q, pool, "q", T, None)
-    qos = 0 if q is None else _rows_of(q_out, pool, "q_out", T, hq)
-    ks = _rows_of(k_new, pool, "k_new", T, pool.num_kv_heads)
-    vs = _rows_of(v_new, pool, "v_new", T, pool.num_kv_heads)
+    ks, vs = _rows_of(k_new, pool, "k_new", (T, H, D)), _rows_of(v_new, pool, "v_new", (T, H, D))
     with _dev(pool):
-        st = lib.pkv_rope_append(pool.ref, layer, rope.ref, bt, block_tables.shape[1], offs, B, seq,
-                                 pos, rpos, T, _ptr(q), qs, hq, k_new.data_ptr(), ks,
-                                 v_new.data_ptr(), vs, _ptr(q_out), qos, _ptr(slot_mapping),
-                                 _stream(pool.device))
+        st = lib.pkv_rope_append(pool.ref, layer, rope.ref, bt, mb, offs, B, seq, pos, rpos, T, qp,
+                                 qs, hq, k_new.data_ptr(), ks, v_new.data_ptr(), vs, qop, qos,
+                                 _ptr(slot_mapping), _stream(pool.device))
     _check(st, "pkv_rope_append")
 
 
@@ -474,6 +476,8 @@ class BlockBounds:
         if codes.device != scales.device or not codes.is_contiguous() or not scales.is_contiguous():
             raise ValueError("codes and scales must be contiguous tensors on one device")
         self.codes, self.scales = codes, scales
+        # [N, L, Hkv, D] and the device, compared with a pool's by every call
+        self.key = (codes.shape[0], codes.shape[1], codes.shape[2], codes.shape[4], codes.device)
 
     @classmethod
     def for_pool(cls, pool: Pool) -> "BlockBounds":
@@ -484,9 +488,8 @@ class BlockBounds:
 
 
 def _bounds_of(bounds: BlockBounds, pool: Pool) -> None:
-    c = bounds.codes
-    if c.device != pool.device or c.shape != (pool.num_blocks, pool.num_layers,
-                                              pool.num_kv_heads, 2, pool.head_dim):
+    if bounds.key != (pool.num_blocks, pool.num_layers, pool.num_kv_heads, pool.head_dim,
+                      pool.device):
         raise ValueError("the bounds do not belong to a pool of this shape")
 
 
@@ -498,15 +501,14 @@ def update_block_bounds(pool: Pool, layer: int, bounds: BlockBounds, block_table
     lib = load()
     bt, lens = _index(block_tables, pool, "block_tables", 2), _index(seq_lens, pool, "seq_lens", 1)
     offs, first = _index(offsets, pool, "offsets", 1), _index(first_pos, pool, "first_pos", 1)
-    B = block_tables.shape[0]
+    B, mb = block_tables.shape
     for t in (seq_lens, offsets, first_pos):
-        if t is not None and t.numel() != B:
+        if t is not None and t.shape[0] != B:
             raise ValueError("seq_lens, offsets and first_pos must have one entry per row of "
                              "block_tables")
     _bounds_of(bounds, pool)
     with _dev(pool):
-        st = lib.pkv_update_block_bounds(pool.ref, layer, bt, block_tables.shape[1], lens, offs,
-                                         first, B, bounds.codes.data_ptr(),
+        st = lib.pkv_update_block_bounds(pool.ref, layer, bt, mb, lens, offs, first, B, bounds.codes.data_ptr(),
                                          bounds.scales.data_ptr(), _stream(pool.device))
     _check(st, "pkv_update_block_bounds")
 
@@ -514,21 +516,24 @@ def update_block_bounds(pool: Pool, layer: int, bounds: BlockBounds, block_table
 def _queries(pool: Pool, q: torch.Tensor, block_tables: torch.Tensor,
              offsets: Optional[torch.Tensor], token_seq: torch.Tensor, token_pos: torch.Tensor,
              selected: torch.Tensor):
-    """Checks and pointers shared by select_blocks and decode_attention_sparse."""
+    """Checks shared by select_blocks and decode_attention_sparse, and their
+    arguments from the tables to the query list."""
+    T, = token_seq.shape
+    B, mb = block_tables.shape
     bt, offs = _index(block_tables, pool, "block_tables", 2), _index(offsets, pool, "offsets", 1)
     seq, pos = _index(token_seq, pool, "token_seq", 1), _index(token_pos, pool, "token_pos", 1)
     sel = _index(selected, pool, "selected", 3)
-    T = token_seq.numel()
-    if token_pos.numel() != T:
+    if token_pos.shape[0] != T:
         raise ValueError("token_seq and token_pos must have the same length")
-    if offsets is not None and offsets.numel() != block_tables.shape[0]:
+    if offsets is not None and offsets.shape[0] != B:
         raise ValueError("offsets must have one entry per row of block_tables")
-    if selected.shape[0] != T or selected.shape[1] != pool.num_kv_heads:
+    t, h, k = selected.shape
+    if t != T or h != pool.num_kv_heads:
         raise ValueError(f"selected must be [{T}, {pool.num_kv_heads}, blocks]")
-    _rows_of(q, pool, "q", T, None)
-    if not q.is_contiguous():
+    hq = q.shape[1]
+    if _rows_of(q, pool, "q", (T, hq, pool.head_dim)) != hq * pool.head_dim:
         raise ValueError("q must be contiguous")
-    return bt, offs, seq, pos, sel, T
+    return (bt, mb, offs, B, seq, pos, T), hq, sel, k
 
 
 def select_blocks(pool: Pool, layer: int, bounds: BlockBounds, q: torch.Tensor,
@@ -540,18 +545,15 @@ def select_blocks(pool: Pool, layer: int, bounds: BlockBounds, q: torch.Tensor,
     (int32 [T, Hkv, K], ascending, -1 behind), their number into ``count``
     (int32 [T, Hkv]).  The first ``sink`` and last ``recent`` are always in."""
     lib = load()
-    bt, offs, seq, pos, sel, T = _queries(pool, q, block_tables, offsets, token_seq, token_pos,
-                                          selected)
+    tokens, hq, sel, k = _queries(pool, q, block_tables, offsets, token_seq, token_pos, selected)
     cnt = _index(count, pool, "count", 2)
-    if count.shape != selected.shape[:2]:
+    if count.shape != (tokens[-1], pool.num_kv_heads):
         raise ValueError("count must be [T, Hkv]")
     _bounds_of(bounds, pool)
     with _dev(pool):
         st = lib.pkv_select_blocks(pool.ref, layer, bounds.codes.data_ptr(),
-                                   bounds.scales.data_ptr(), q.data_ptr(), q.shape[1], bt,
-                                   block_tables.shape[1], offs, block_tables.shape[0], seq, pos, T,
-                                   selected.shape[2], sink, recent, sel, cnt,
-                                   _stream(pool.device))
+                                   bounds.scales.data_ptr(), q.data_ptr(), hq, *tokens, k, sink,
+                                   recent, sel, cnt, _stream(pool.device))
     _check(st, "pkv_select_blocks")
 
 
@@ -563,16 +565,12 @@ def decode_attention_sparse(pool: Pool, layer: int, q: torch.Tensor, scale: floa
     (int32 [T, Hkv, K], negative ones skipped) of each query's sequence, at
     positions up to ``token_pos``, into ``out``."""
     lib = load()
-    bt, offs, seq, pos, sel, T = _queries(pool, q, block_tables, offsets, token_seq, token_pos,
-                                          selected)
-    if out.shape != q.shape or out.dtype != q.dtype or out.device != q.device \
-            or not out.is_contiguous():
-        raise ValueError("out must be a contiguous tensor like q")
+    tokens, hq, sel, k = _queries(pool, q, block_tables, offsets, token_seq, token_pos, selected)
+    if _rows_of(out, pool, "out", (tokens[-1], hq, pool.head_dim)) != hq * pool.head_dim:
+        raise ValueError("out must be contiguous")
     with _dev(pool):
-        st = lib.pkv_decode_attention_sparse(pool.ref, layer, q.data_ptr(), q.shape[1],
-                                             float(scale), bt, block_tables.shape[1], offs,
-                                             block_tables.shape[0], seq, pos, T, sel,
-                                             selected.shape[2], out.data_ptr(),
+        st = lib.pkv_decode_attention_sparse(pool.ref, layer, q.data_ptr(), hq, float(scale),
+                                             *tokens, sel, k, out.data_ptr(),
                                              _stream(pool.device))
     _check(st, "pkv_decode_attention_sparse")
 

@@ -13,13 +13,22 @@
 // How.  One cluster of CTAs per (t, g); each CTA scores a contiguous range of
 // the entries and keeps the scores in its shared memory, so nothing but the
 // result is ever written.  The scores are found on the tensor cores: 16
-// blocks by 8 query heads by 16 code bytes per mma, the codes turned to fp16
-// whole numbers in registers (products and sums below 2^24: exact).  A lane
-// loads 16-byte pieces of its two blocks straight to registers; with the same
-// pieces of the query in its B fragments, the order of k does not matter.
-// The cut is a radix search over the scores as ordered integers, from their
-// cluster-wide range down, 8 bits a step: every CTA counts its own scores and
-// sums the counts of all through distributed shared memory.
+// blocks by 8 query heads by 16 code bytes per mma, the codes turned to biased
+// fp16 whole numbers in registers (sums below 2^24: exact).  A lane
+// loads 16-byte pieces of its blocks straight to registers, and the same
+// pieces of the query, coded once per CTA, from shared memory, so the order of
+// k does not matter.
+//
+// The cut: the scores as ordered integers, counted in 256 bins from the
+// cluster-wide range down.  Every CTA counts its own and sums the counts of
+// all through distributed shared memory.  Once the bin that holds the cut has
+// at most 256 scores (as a rule after the first count), every CTA gathers
+// those and ranks them by (score, entry); a bin that stays larger is counted
+// again 8 bits finer, down to equal scores, of which the lowest entries are
+// taken.
+//
+// What bounds it: with few rows, latency (three cluster barriers, two rounds
+// of loads); with many, the bytes of the bounds.
 #include <cmath>
 
 #include <cuda_fp16.h>
@@ -31,8 +40,7 @@
 namespace pkv {
 namespace {
 
-constexpr int kSelThreads = 256;
-constexpr int kSelWarps = kSelThreads / 32;
+constexpr int kCand = 256;  // scores that are ranked rather than counted
 constexpr unsigned kAll = 0xffffffffu;
 
 struct SelectParams {
@@ -48,30 +56,30 @@ struct SelectParams {
   int* err;
   long long num_blocks;
   int batch, mb, bs, L, layer, hq, hkv, G, K, sink, recent;
+  int q_size;  // bytes of an element of q
   int cap;  // scores a CTA can hold
 };
 
-// Static shared memory: what the CTAs of a cluster read of each other.
+// Static shared memory; the CTAs of a cluster read each other's.
 struct SelectShared {
   uint32_t hist[4][256];
-  uint32_t range[2];  // smallest and largest score of this CTA
-  uint32_t counts[2];
-  uint32_t warp_a[kSelWarps], warp_b[kSelWarps];
-  uint32_t total[256];
+  uint32_t range[2];   // smallest and largest score of this CTA
+  uint32_t counts[2];  // scores of this CTA above the cut, and at it
+  uint32_t cand_key[kCand], cand_at[kCand];  // this CTA's scores in the cut's bin, and their entries
+  uint32_t ncand;
+  // not read by others
+  uint32_t all_key[kCand], all_at[kCand];
   uint32_t pick[3];
+  uint32_t before;
+  uint32_t warp_a[32], warp_b[32];
 };
 
+// Code bytes c + 128 to fp16 numbers 1024 + byte = 1152 + c, two a register.
 __device__ __forceinline__ void codes_to_f16(uint32_t w, uint32_t& lo, uint32_t& hi) {
-  // bytes c + 128 -> fp16 1024 + byte -> minus 1152
-  uint32_t a, b;
-  asm("prmt.b32 %0, %1, 0x64646464, 0x4140;" : "=r"(a) : "r"(w));
-  asm("prmt.b32 %0, %1, 0x64646464, 0x4342;" : "=r"(b) : "r"(w));
-  const __half2 bias = __half2half2(__ushort_as_half(0x6480));  // 1152
-  const __half2 x = __hsub2(*reinterpret_cast<const __half2*>(&a), bias);
-  const __half2 y = __hsub2(*reinterpret_cast<const __half2*>(&b), bias);
-  lo = *reinterpret_cast<const uint32_t*>(&x);
-  hi = *reinterpret_cast<const uint32_t*>(&y);
+  asm("prmt.b32 %0, %1, 0x64646464, 0x4140;" : "=r"(lo) : "r"(w));
+  asm("prmt.b32 %0, %1, 0x64646464, 0x4342;" : "=r"(hi) : "r"(w));
 }
+constexpr float kBias = 1152.f;
 
 __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
                                         uint32_t a3, uint32_t b0, uint32_t b1) {
@@ -82,12 +90,12 @@ __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1,
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// Order-preserving map of a score to an unsigned integer, at least 1.
+// Order-preserving map of a score to an unsigned integer in [1, 2^32 - 2].
 __device__ __forceinline__ uint32_t ordered(float x) {
   uint32_t u = __float_as_uint(x);
   if (u == 0x80000000u) u = 0;  // -0 and +0 are one score
   u = (u & 0x80000000u) ? ~u : u | 0x80000000u;
-  return u ? u : 1u;
+  return min(0xfffffffeu, max(1u, u));
 }
 
 // Inclusive sums of (a, b) over the CTA's threads; every thread calls it.
@@ -104,12 +112,60 @@ __device__ __forceinline__ void block_scan(uint32_t& a, uint32_t& b, SelectShare
   __syncthreads();
 }
 
-// T: type of q; NT: tiles of 8 query heads.
-template <typename T, int D, int NT>
-__global__ void __launch_bounds__(kSelThreads) select_kernel(const SelectParams p) {
-  constexpr int LD = D / 64;  // 16-byte pieces of one bound that a lane holds
+// Sum of a 32-bit word over the first `n` CTAs of the cluster, four loads in
+// flight at a time.
+__device__ __forceinline__ uint32_t cluster_sum(uint32_t addr, uint32_t n) {
+  uint32_t sum = 0;
+  for (uint32_t r = 0; r < n; r += 4) {
+    uint32_t v[4];
+#pragma unroll
+    for (uint32_t u = 0; u < 4; ++u)
+      v[u] = r + u < n ? ld_cluster_u32(cluster_map(addr, r + u)) : 0u;
+    sum += (v[0] + v[1]) + (v[2] + v[3]);
+  }
+  return sum;
+}
+
+__device__ __forceinline__ uint32_t ld_u32(const void* p) {
+  uint32_t v;
+  asm volatile("ld.global.nc.u32 %0, [%1];" : "=r"(v) : "l"(p));
+  return v;
+}
+
+__device__ __forceinline__ uint4 lds128(uint32_t a) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "r"(a)
+               : "memory");
+  return v;
+}
+
+__device__ __forceinline__ void sts_u32(uint32_t a, uint32_t v) {
+  asm volatile("st.shared.u32 [%0], %1;" ::"r"(a), "r"(v) : "memory");
+}
+
+__device__ __forceinline__ void sync_all(uint32_t S) {
+  if (S > 1)
+    cluster_sync();
+  else
+    __syncthreads();
+}
+
+// NT: tiles of 8 query heads.  With one, 80 registers a thread, so that an SM
+// holds 24 warps; with two, 12.
+template <int D, int NT, int THREADS>
+__global__ void __launch_bounds__(THREADS, (NT == 1 ? 768 : 384) / THREADS)
+    select_kernel(const SelectParams p) {
+  constexpr int LD = D / 64;  // 64-element pieces of a bound
+  constexpr int WARPS = THREADS / 32;
+  constexpr int QROW = D * 2 + 16;  // bytes of a coded query row, padded against bank conflicts
+  constexpr int EPL = D / 32;       // elements of a query row a lane codes
   extern __shared__ uint32_t keys[];
   __shared__ SelectShared sh;
+  // the coded query: positive and negative parts, unit, bias of each piece
+  __shared__ __align__(16) unsigned char sq[2][NT * 8 * QROW];
+  __shared__ float s_unit[NT * 8], s_bias[2][LD][NT * 8];
   griddep_wait();
   griddep_launch_dependents();
   uint32_t S;
@@ -119,7 +175,26 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const SelectParams 
   const int t = row / p.hkv, g = row - t * p.hkv;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
 
-  const int seq = p.tok_seq[t], pos = p.tok_pos[t];
+  const int seq = ld_volatile(p.tok_seq + t), pos = ld_volatile(p.tok_pos + t);
+  // this warp's query rows, in flight beside the chain of index loads
+  constexpr int QPW = (NT * 8 + WARPS - 1) / WARPS;
+  uint32_t qraw[QPW][EPL];
+#pragma unroll
+  for (int u = 0; u < QPW; ++u) {
+    const int h = warp + u * WARPS;
+    const char* src = p.q + (((long long)t * p.hq + g * p.G + h) * D + lane * EPL) * p.q_size;
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) qraw[u][i] = 0;
+    if (h < p.G) {
+      if (p.q_size == 4) {
+#pragma unroll
+        for (int i = 0; i < EPL; ++i) qraw[u][i] = ld_u32(src + 4 * i);
+      } else {
+#pragma unroll
+        for (int i = 0; i < EPL / 2; ++i) qraw[u][i] = ld_u32(src + 4 * i);
+      }
+    }
+  }
   int off = 0, n = 0;
   if (seq >= p.batch) {
     if (rank == 0 && tid == 0) set_error(p.err, kErrIndex);
@@ -134,83 +209,85 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const SelectParams 
   int32_t* out = p.sel + (long long)row * p.K;
   if (rank == 0 && tid == 0) p.count[row] = min(n, p.K);
   if (n <= p.K) {  // all of them, or none (the whole cluster leaves)
-    for (int i = rank * kSelThreads + tid; i < p.K; i += S * kSelThreads) out[i] = i < n ? i : -1;
+    for (int i = rank * THREADS + tid; i < p.K; i += S * THREADS) out[i] = i < n ? i : -1;
     return;
   }
   if (rank == 0) {
-    for (int i = tid; i < p.sink; i += kSelThreads) out[i] = i;
-    for (int i = tid; i < p.recent; i += kSelThreads) out[p.K - p.recent + i] = n - p.recent + i;
+    for (int i = tid; i < p.sink; i += THREADS) out[i] = i;
+    for (int i = tid; i < p.recent; i += THREADS) out[p.K - p.recent + i] = n - p.recent + i;
   }
-  int need = p.K - p.sink - p.recent;
+  const int need = p.K - p.sink - p.recent;
   if (need == 0) return;
   const int m = n - p.sink - p.recent;  // scored entries, more than need
   const int per = (m + (int)S - 1) / (int)S;
   const int lo = min(m, (int)rank * per), cnt = min(m, lo + per) - lo;
 
-  // ---- the query: 8-bit codes as fp16 B fragments ------------------------
+  // ---- entries of the first tile -------------------------------------------
   const int gl = lane >> 2, qi = lane & 3;
-  uint32_t bp[NT][LD][4][2], bn[NT][LD][4][2];  // positive and negative parts
-  float f0[NT], f1[NT];                         // 2^e_q of columns 2 qi, 2 qi + 1
+  const int32_t* table = p.bt + (long long)seq * p.mb + p.sink + lo;
+  auto entry = [&](int i) { return i < cnt ? ld_volatile(table + i) : -1; };
+  constexpr int STEP = WARPS * 16;
+  int base = warp * 16;
+  int id0 = entry(base + gl), id1 = entry(base + gl + 8);
+
+  // ---- the query in 8 bits ---------------------------------------------------
 #pragma unroll
-  for (int nt = 0; nt < NT; ++nt) {
-    const int h = nt * 8 + gl;
-    float x[LD][16];
+  for (int u = 0; u < QPW; ++u) {
+    const int h = warp + u * WARPS;
+    if (h >= NT * 8) break;
+    float x[EPL];
+#pragma unroll
+    for (int i = 0; i < EPL; ++i)
+      x[i] = p.q_size == 4 ? __uint_as_float(qraw[u][i])
+             : i & 1       ? bf16_hi(qraw[u][i / 2])
+                           : bf16_lo(qraw[u][i / 2]);
     uint32_t mx = 0;
 #pragma unroll
-    for (int i = 0; i < LD; ++i) {
-      const char* src = p.q + (((long long)t * p.hq + g * p.G + h) * D + i * 64 + qi * 16) *
-                                  (long long)sizeof(T);
-#pragma unroll
-      for (int v = 0; v < (int)sizeof(T); ++v) {
-        const uint4 r = h < p.G ? *reinterpret_cast<const uint4*>(src + 16 * v)
-                                : make_uint4(0, 0, 0, 0);
-        const uint32_t w[4] = {r.x, r.y, r.z, r.w};
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          if constexpr (sizeof(T) == 2) {
-            x[i][8 * v + 2 * k] = bf16_lo(w[k]);
-            x[i][8 * v + 2 * k + 1] = bf16_hi(w[k]);
-          } else {
-            x[i][4 * v + k] = __uint_as_float(w[k]);
-          }
-        }
-      }
-#pragma unroll
-      for (int k = 0; k < 16; ++k) mx = max(mx, __float_as_uint(x[i][k]) & 0x7FFFFFFFu);
-    }
-    mx = max(mx, __shfl_xor_sync(kAll, mx, 1));
-    mx = max(mx, __shfl_xor_sync(kAll, mx, 2));
+    for (int i = 0; i < EPL; ++i) mx = max(mx, __float_as_uint(x[i]) & 0x7FFFFFFFu);
+    mx = __reduce_max_sync(kAll, mx);
     const int e = bound_exponent(mx);
     const float inv = pow2f(-e);
+    int up = 0, down = 0;
+    __half2 hp[EPL / 2], hn[EPL / 2];
 #pragma unroll
-    for (int i = 0; i < LD; ++i)
+    for (int i = 0; i < EPL / 2; ++i) {
+      const int a = min(127, max(-127, __float2int_rn(mul_ieee(x[2 * i], inv))));
+      const int b = min(127, max(-127, __float2int_rn(mul_ieee(x[2 * i + 1], inv))));
+      hp[i] = __floats2half2_rn((float)max(a, 0), (float)max(b, 0));
+      hn[i] = __floats2half2_rn((float)min(a, 0), (float)min(b, 0));
+      up += max(a, 0) + max(b, 0);
+      down += min(a, 0) + min(b, 0);
+    }
+    const uint32_t at = smem_addr(sq[0]) + h * QROW + lane * EPL * 2;
 #pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        const int a = min(127, max(-127, __float2int_rn(mul_ieee(x[i][2 * k], inv))));
-        const int b = min(127, max(-127, __float2int_rn(mul_ieee(x[i][2 * k + 1], inv))));
-        const __half2 hp = __floats2half2_rn((float)max(a, 0), (float)max(b, 0));
-        const __half2 hn = __floats2half2_rn((float)min(a, 0), (float)min(b, 0));
-        bp[nt][i][k >> 1][k & 1] = *reinterpret_cast<const uint32_t*>(&hp);
-        bn[nt][i][k >> 1][k & 1] = *reinterpret_cast<const uint32_t*>(&hn);
-      }
-    const float unit = pow2f(e);
-    f0[nt] = __shfl_sync(kAll, unit, 8 * qi);
-    f1[nt] = __shfl_sync(kAll, unit, 8 * qi + 4);
+    for (int i = 0; i < EPL / 2; ++i) {
+      sts_u32(at + 4 * i, *reinterpret_cast<const uint32_t*>(&hp[i]));
+      sts_u32(at + NT * 8 * QROW + 4 * i, *reinterpret_cast<const uint32_t*>(&hn[i]));
+    }
+    // a piece is held by the lanes of half a warp (D 128) or by all of it
+#pragma unroll
+    for (int o = 1; o < 32 / LD; o <<= 1) {
+      up += __shfl_xor_sync(kAll, up, o);
+      down += __shfl_xor_sync(kAll, down, o);
+    }
+    if (lane % (32 / LD) == 0) {
+      s_bias[0][lane / (32 / LD)][h] = -kBias * (float)up;
+      s_bias[1][lane / (32 / LD)][h] = -kBias * (float)down;
+    }
+    if (lane == 0) s_unit[h] = pow2f(e);
   }
 
-  // ---- scores --------------------------------------------------------------
-  uint32_t kmin = 0xffffffffu, kmax = 0;
-  const int32_t* table = p.bt + (long long)seq * p.mb + p.sink + lo;
-  for (int base = warp * 16; base < cnt; base += kSelWarps * 16) {
-    uint4 w[2][2][LD];
-    float unit[2];
-    bool ok[2];
+  // ---- scores: tiles warp, warp + WARPS, ... of 16 blocks ----------------------
+  // rows lane / 4 and + 8 of a tile
+  uint4 w[2][2][LD];
+  float unit[2];
+  bool ok[2];
+  auto load = [&](int at) {
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
-      const int i = base + gl + 8 * r;
-      const int blk = i < cnt ? table[i] : -1;
+      const int blk = r ? id1 : id0;
       ok[r] = blk >= 0 && blk < p.num_blocks;
-      if (i < cnt && !ok[r] && qi == 0) set_error(p.err, kErrIndex);
+      if (at + gl + 8 * r < cnt && !ok[r] && qi == 0) set_error(p.err, kErrIndex);
       const long long head = ((long long)(ok[r] ? blk : 0) * p.L + p.layer) * p.hkv + g;
       const char* src = p.codes + head * (2 * D) + qi * 16;
 #pragma unroll
@@ -219,41 +296,76 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const SelectParams 
         for (int k = 0; k < LD; ++k) w[r][side][k] = ld_stream(src + side * D + k * 64);
       unit[r] = p.scales[head];
     }
-    float acc[NT][4];
+  };
+  if (base < cnt) load(base);
+  id0 = entry(base + STEP + gl);
+  id1 = entry(base + STEP + gl + 8);
+  __syncthreads();
+  uint32_t kmin = 0xffffffffu, kmax = 0;
+  const uint32_t a_q = smem_addr(sq[0]) + gl * QROW + qi * 32;
+#pragma unroll 1
+  for (; base < cnt; base += STEP) {
+    // One sum per side and 64-element piece, started at minus its bias: codes
+    // enter as 1152 + c, so a piece's partial sums stay below
+    // 1279 * 127 * 64 < 2^24 and are exact.
+    float dot[NT][4];
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
+    for (int nt = 0; nt < NT; ++nt) {
+      float acc[2][LD][4];
 #pragma unroll
-      for (int c = 0; c < 4; ++c) acc[nt][c] = 0.f;
+      for (int side = 0; side < 2; ++side)
 #pragma unroll
-    for (int side = 0; side < 2; ++side)
-#pragma unroll
-      for (int k = 0; k < LD; ++k) {
-        const uint32_t u0[4] = {w[0][side][k].x, w[0][side][k].y, w[0][side][k].z, w[0][side][k].w};
-        const uint32_t u1[4] = {w[1][side][k].x, w[1][side][k].y, w[1][side][k].z, w[1][side][k].w};
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          uint32_t a0, a1, a2, a3;
-          codes_to_f16(u0[c], a0, a2);
-          codes_to_f16(u1[c], a1, a3);
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
-            mma_f16(acc[nt], a0, a1, a2, a3, side ? bn[nt][k][c][0] : bp[nt][k][c][0],
-                    side ? bn[nt][k][c][1] : bp[nt][k][c][1]);
+        for (int k = 0; k < LD; ++k) {
+          const float2 b0 = *reinterpret_cast<const float2*>(&s_bias[side][k][nt * 8 + 2 * qi]);
+          acc[side][k][0] = acc[side][k][2] = b0.x;
+          acc[side][k][1] = acc[side][k][3] = b0.y;
         }
+#pragma unroll
+      for (int half = 0; half < 2; ++half)
+#pragma unroll
+        for (int side = 0; side < 2; ++side)
+#pragma unroll
+          for (int k = 0; k < LD; ++k) {
+            // dims k * 64 + qi * 16 + half * 8 .. + 7 of head gl
+            const uint4 b = lds128(a_q + (side * NT + nt) * 8 * QROW + k * 128 + half * 16);
+            const uint4 &y0 = w[0][side][k], &y1 = w[1][side][k];
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+              const uint32_t u0 = half ? (c ? y0.w : y0.z) : (c ? y0.y : y0.x);
+              const uint32_t u1 = half ? (c ? y1.w : y1.z) : (c ? y1.y : y1.x);
+              uint32_t a0, a1, a2, a3;
+              codes_to_f16(u0, a0, a2);
+              codes_to_f16(u1, a1, a3);
+              mma_f16(acc[side][k], a0, a1, a2, a3, c ? b.z : b.x, c ? b.w : b.y);
+            }
+          }
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        dot[nt][c] = acc[0][0][c] + acc[1][0][c];
+        if constexpr (LD == 2) dot[nt][c] += acc[0][1][c] + acc[1][1][c];
       }
+    }
+    const float u0 = unit[0], u1 = unit[1];
+    const bool ok0 = ok[0], ok1 = ok[1];
+    if (base + STEP < cnt) {
+      load(base + STEP);
+      id0 = entry(base + 2 * STEP + gl);
+      id1 = entry(base + 2 * STEP + gl + 8);
+    }
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
       float best = -INFINITY;
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
-        if (nt * 8 + 2 * qi < p.G) best = fmaxf(best, acc[nt][2 * r] * f0[nt]);
-        if (nt * 8 + 2 * qi + 1 < p.G) best = fmaxf(best, acc[nt][2 * r + 1] * f1[nt]);
+        const float2 f = *reinterpret_cast<const float2*>(&s_unit[nt * 8 + 2 * qi]);
+        if (nt * 8 + 2 * qi < p.G) best = fmaxf(best, dot[nt][2 * r] * f.x);
+        if (nt * 8 + 2 * qi + 1 < p.G) best = fmaxf(best, dot[nt][2 * r + 1] * f.y);
       }
       best = fmaxf(best, __shfl_xor_sync(kAll, best, 1));
       best = fmaxf(best, __shfl_xor_sync(kAll, best, 2));
       const int i = base + gl + 8 * r;
       if (i < cnt) {
-        const uint32_t key = ok[r] ? ordered(best * unit[r]) : 0u;
+        const uint32_t key = (r ? ok1 : ok0) ? ordered(best * (r ? u1 : u0)) : 0u;
         if (qi == 0) keys[i] = key;
         kmin = min(kmin, key);
         kmax = max(kmax, key);
@@ -265,95 +377,172 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const SelectParams 
   kmin = __reduce_min_sync(kAll, kmin);
   kmax = __reduce_max_sync(kAll, kmax);
   if (lane == 0) { sh.warp_a[warp] = kmin; sh.warp_b[warp] = kmax; }
-  for (int i = tid; i < 4 * 256; i += kSelThreads) (&sh.hist[0][0])[i] = 0;
+  for (int i = tid; i < 4 * 256; i += THREADS) (&sh.hist[0][0])[i] = 0;
+  if (tid == 0) sh.ncand = 0;
   __syncthreads();
-  if (tid == 0) {
-    for (int w = 1; w < kSelWarps; ++w) {
-      kmin = min(kmin, sh.warp_a[w]);
-      kmax = max(kmax, sh.warp_b[w]);
-    }
-    sh.range[0] = kmin;
-    sh.range[1] = kmax;
+  if (warp == 0) {
+    kmin = __reduce_min_sync(kAll, lane < WARPS ? sh.warp_a[lane] : 0xffffffffu);
+    kmax = __reduce_max_sync(kAll, lane < WARPS ? sh.warp_b[lane] : 0u);
+    if (lane == 0) { sh.range[0] = kmin; sh.range[1] = kmax; }
   }
-  cluster_sync();
-  const uint32_t a_range = smem_addr(sh.range), a_hist = smem_addr(sh.hist),
-                 a_counts = smem_addr(sh.counts);
-  for (uint32_t r = 0; r < S; ++r) {
-    const uint32_t a = cluster_map(a_range, r);
-    kmin = min(kmin, ld_cluster_u32(a));
-    kmax = max(kmax, ld_cluster_u32(a + 4));
+  sync_all(S);
+  {
+    // one CTA per lane
+    const uint32_t a = cluster_map(smem_addr(sh.range), lane < S ? lane : 0);
+    kmin = __reduce_min_sync(kAll, ld_cluster_u32(a));
+    kmax = __reduce_max_sync(kAll, ld_cluster_u32(a + 4));
   }
 
-  // ---- the cut: 8 bits of (score - smallest) a step ---------------------------
+  // ---- the cut: 8 bits of (score - smallest) a count ---------------------------
+  const uint32_t a_hist = smem_addr(sh.hist), a_counts = smem_addr(sh.counts);
   uint32_t bits = 32 - __clz(kmax - kmin);
   uint32_t prefix = 0;
   uint32_t left = need;  // to be taken among the scores that match the prefix
+  bool ranked = false;   // they are few, and are ranked
 #pragma unroll 1
   for (int step = 0; bits > 0; ++step) {
     const uint32_t width = min(8u, bits), shift = bits - width, mask = (1u << width) - 1;
-    for (int i = tid; i < cnt; i += kSelThreads) {
+    for (int i = tid; i < cnt; i += THREADS) {
       const uint32_t x = keys[i] - kmin;
       if ((bits < 32 ? x >> bits : 0u) == prefix) atomicAdd(&sh.hist[step][(x >> shift) & mask], 1u);
     }
-    cluster_sync();
-    // thread b sums bin 255 - b over the CTAs, so the scan runs from the top
-    const int bin = 255 - tid;
-    uint32_t c = 0;
-    for (uint32_t r = 0; r < S; ++r)
-      c += ld_cluster_u32(cluster_map(a_hist + (step * 256 + bin) * 4, r));
-    uint32_t above = c, dummy = 0;
+    sync_all(S);
+    // a thread sums its bins over the CTAs; the scan runs from the top bin down
+    constexpr int BPT = (256 + THREADS - 1) / THREADS;
+    uint32_t c[BPT], sum = 0, dummy = 0;
+#pragma unroll
+    for (int u = 0; u < BPT; ++u) {
+      const int bin = 255 - (tid * BPT + u);
+      c[u] = bin >= 0 ? cluster_sum(a_hist + (step * 256 + bin) * 4, S) : 0u;
+      sum += c[u];
+    }
+    uint32_t above = sum;
     block_scan(above, dummy, sh);
-    if (above >= left && above - c < left) {
-      sh.pick[0] = bin;
-      sh.pick[1] = left - (above - c);
-      sh.pick[2] = c;
+    above -= sum;
+#pragma unroll
+    for (int u = 0; u < BPT; ++u) {
+      if (above < left && above + c[u] >= left) {
+        sh.pick[0] = 255 - (tid * BPT + u);
+        sh.pick[1] = left - above;
+        sh.pick[2] = c[u];
+      }
+      above += c[u];
     }
     __syncthreads();
     prefix = (prefix << width) | sh.pick[0];
     left = sh.pick[1];
-    const bool whole = left == sh.pick[2];  // every score of the bin is taken
+    const uint32_t found = sh.pick[2];
     bits = shift;
     __syncthreads();
-    if (whole) break;
+    if (left == found) break;  // every score of the bin is taken
+    if (bits > 0 && found <= kCand) {
+      ranked = true;
+      break;
+    }
   }
+  // keys from here on lie above the bin of the cut (no key is 2^32 - 1)
+  const unsigned long long next = kmin + ((prefix + 1ull) << bits);
+  const uint32_t limit = next > 0xffffffffull ? 0xffffffffu : (uint32_t)next;
 
-  // ---- write the taken entries in order ---------------------------------------
-  // a thread's entries are consecutive; `over` are above the cut, `even` match it
-  const int seg = (cnt + kSelThreads - 1) / kSelThreads;
+  // ---- counts above the cut, and at it ------------------------------------------
+  // a thread's entries are consecutive
+  const int seg = (cnt + THREADS - 1) / THREADS;
   const int i0 = min(cnt, tid * seg), i1 = min(cnt, i0 + seg);
   uint32_t over = 0, even = 0;
   for (int i = i0; i < i1; ++i) {
-    const uint32_t x = (keys[i] - kmin) >> bits;
-    over += x > prefix;
-    even += x == prefix;
+    const uint32_t key = keys[i];
+    over += key >= limit;
+    if (key < limit && (key - kmin) >> bits == prefix) {
+      ++even;
+      if (ranked) {
+        const uint32_t slot = atomicAdd(&sh.ncand, 1u);
+        sh.cand_key[slot] = key;
+        sh.cand_at[slot] = lo + i;
+      }
+    }
   }
-  const uint32_t my_over = over, my_even = even;
+  uint32_t my_over = over, my_even = even;
   block_scan(over, even, sh);
-  if (tid == kSelThreads - 1) { sh.counts[0] = over; sh.counts[1] = even; }
-  over -= my_over;
-  even -= my_even;
-  cluster_sync();
-  for (uint32_t r = 0; r < rank; ++r) {
-    const uint32_t a = cluster_map(a_counts, r);
-    over += ld_cluster_u32(a);
-    even += ld_cluster_u32(a + 4);
+  if (tid == THREADS - 1) { sh.counts[0] = over; sh.counts[1] = even; }
+  sync_all(S);
+  // of the CTAs before this one, one per lane
+  const uint32_t a_mine = cluster_map(a_counts, lane < rank ? lane : 0);
+  const uint32_t over0 = __reduce_add_sync(kAll, lane < rank ? ld_cluster_u32(a_mine) : 0u);
+  const uint32_t even0 = __reduce_add_sync(kAll, lane < rank ? ld_cluster_u32(a_mine + 4) : 0u);
+  if (!ranked) {
+    over += over0 - my_over;
+    even += even0 - my_even;
+    for (int i = i0; i < i1; ++i) {
+      const uint32_t key = keys[i];
+      const bool ov = key >= limit, eq = !ov && (key - kmin) >> bits == prefix;
+      if (ov || (eq && even < left)) out[p.sink + over + min(even, left)] = p.sink + lo + i;
+      over += ov;
+      even += eq;
+    }
+  } else {
+    // gather the bin's scores of all CTAs, rank them, and mark the taken ones
+    // among this CTA's with a key above the limit, the others with one below
+    const uint32_t a_key = smem_addr(sh.cand_key), a_at = smem_addr(sh.cand_at);
+    const uint32_t nr =
+        lane < S ? ld_cluster_u32(cluster_map(smem_addr(&sh.ncand), lane)) : 0u;
+    uint32_t start = nr;  // of the entries of CTA `lane`
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const uint32_t y = __shfl_up_sync(kAll, start, o);
+      if (lane >= o) start += y;
+    }
+    const uint32_t at = __shfl_sync(kAll, start, 31);
+    start -= nr;
+    if (tid == 0) sh.before = 0;
+    for (uint32_t r = warp; r < S; r += WARPS) {
+      const uint32_t n0 = __shfl_sync(kAll, nr, r), s0 = __shfl_sync(kAll, start, r);
+      const uint32_t rk = cluster_map(a_key, r), ra = cluster_map(a_at, r);
+      for (uint32_t i = lane; i < n0; i += 32) {
+        sh.all_key[s0 + i] = ld_cluster_u32(rk + 4 * i);
+        sh.all_at[s0 + i] = ld_cluster_u32(ra + 4 * i);
+      }
+    }
+    __syncthreads();
+    for (uint32_t i = tid; i < at; i += THREADS) {
+      const uint32_t key = sh.all_key[i], e = sh.all_at[i];
+      uint32_t better = 0;
+      for (uint32_t j = 0; j < at; ++j) {
+        const uint32_t k2 = sh.all_key[j];
+        better += k2 > key || (k2 == key && sh.all_at[j] < e);
+      }
+      const bool taken = better < left;
+      if ((int)e >= lo && (int)e < lo + cnt) keys[e - lo] = taken ? 0xffffffffu : 0u;
+      if (taken && (int)e < lo) atomicAdd(&sh.before, 1u);
+    }
+    __syncthreads();
+    over = 0;
+    for (int i = i0; i < i1; ++i) over += keys[i] >= limit;
+    my_over = over;
+    uint32_t dummy = 0;
+    block_scan(over, dummy, sh);
+    over += over0 + sh.before - my_over;
+    for (int i = i0; i < i1; ++i)
+      if (keys[i] >= limit) out[p.sink + over++] = p.sink + lo + i;
   }
-  for (int i = i0; i < i1; ++i) {
-    const uint32_t x = (keys[i] - kmin) >> bits;
-    const bool eq = x == prefix;
-    if (x > prefix || (eq && even < left)) out[p.sink + over + min(even, left)] = p.sink + lo + i;
-    over += x > prefix;
-    even += eq;
-  }
-  cluster_sync();  // no CTA leaves while another may still read its counts
+  if (S > 1) cluster_sync();  // no CTA leaves while another may still read its words
 }
 
-template <typename T, int D>
+template <int D, int THREADS>
 cudaError_t launch_select_d(const SelectParams& p, unsigned grid, unsigned S, cudaStream_t s) {
   const size_t smem = (size_t)p.cap * 4;
   if (p.G <= 8)
-    return launch_clusters(select_kernel<T, D, 1>, dim3(grid), dim3(kSelThreads), smem, S, s, p);
-  return launch_clusters(select_kernel<T, D, 2>, dim3(grid), dim3(kSelThreads), smem, S, s, p);
+    return launch_clusters(select_kernel<D, 1, THREADS>, dim3(grid), dim3(THREADS), smem, S, s, p);
+  // (768 threads have no registers for a second set of sums)
+  constexpr int TWO = THREADS < 384 ? THREADS : 384;
+  return launch_clusters(select_kernel<D, 2, TWO>, dim3(grid), dim3(TWO), smem, S, s, p);
+}
+
+template <int D>
+cudaError_t launch_select(const SelectParams& p, int threads, unsigned grid, unsigned S,
+                          cudaStream_t s) {
+  if (threads == 192) return launch_select_d<D, 192>(p, grid, S, s);
+  if (threads == 384) return launch_select_d<D, 384>(p, grid, S, s);
+  return launch_select_d<D, 768>(p, grid, S, s);
 }
 
 bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
@@ -409,12 +598,17 @@ extern "C" pkv_status pkv_select_blocks(const pkv_pool* pool, int32_t layer,
       return (pkv_status)st;
     if ((st = pkv::read_and_clear_error_word(err, stream)) != PKV_OK) return (pkv_status)st;
   }
-  // CTAs of a cluster: until two per SM are there, each with 128 entries or
-  // more, and as many as the scores need room.
-  unsigned S = 1;
-  while ((int)S < pkv::kSelMaxCluster &&
-         ((rows * S < 2 * sms && mb / S > 128) || (mb + S - 1) / S > pkv::kSelMaxCap))
-    S *= 2;
+  // An SM holds 24 warps of this kernel.  Few rows: clusters of CTAs of 24
+  // warps, one an SM; more: CTAs of 12 warps, two an SM; many: one CTA of 6 warps
+  // a row, four an SM.  No more CTAs a row than leave each warp a tile, and
+  // as many as its scores need room.
+  const int tiles = (mb + 15) / 16;
+  const int threads = rows * 8 <= sms ? 768 : rows <= 2 * sms ? 384 : 192;
+  int64_t S = threads == 768 ? 8 : threads == 384 ? 2 * sms / rows : 1;
+  if (S > (tiles * 32 + threads - 1) / threads) S = (tiles * 32 + threads - 1) / threads;
+  if (S > pkv::kSelMaxCluster) S = pkv::kSelMaxCluster;
+  while (S < pkv::kSelMaxCluster && (mb + S - 1) / S > pkv::kSelMaxCap) S *= 2;
+  if (S > pkv::kSelMaxCluster) S = pkv::kSelMaxCluster;
   pkv::SelectParams p;
   p.q = static_cast<const char*>(q);
   p.codes = static_cast<const char*>(bound_codes);
@@ -438,15 +632,12 @@ extern "C" pkv_status pkv_select_blocks(const pkv_pool* pool, int32_t layer,
   p.K = num_selected;
   p.sink = sink;
   p.recent = recent;
-  p.cap = (mb + (int)S - 1) / (int)S;
-  const unsigned ctas = (unsigned)rows * S;
-  cudaError_t e;
-  if (v.io_size == 2)
-    e = v.head_dim == 64 ? pkv::launch_select_d<__nv_bfloat16, 64>(p, ctas, S, stream)
-                         : pkv::launch_select_d<__nv_bfloat16, 128>(p, ctas, S, stream);
-  else
-    e = v.head_dim == 64 ? pkv::launch_select_d<float, 64>(p, ctas, S, stream)
-                         : pkv::launch_select_d<float, 128>(p, ctas, S, stream);
+  p.q_size = v.io_size;
+  p.cap = (int)((mb + S - 1) / S);
+  const unsigned ctas = (unsigned)(rows * S);
+  const cudaError_t e = v.head_dim == 64
+                            ? pkv::launch_select<64>(p, threads, ctas, (unsigned)S, stream)
+                            : pkv::launch_select<128>(p, threads, ctas, (unsigned)S, stream);
   if ((st = pkv::launch_status(e)) != PKV_OK) return (pkv_status)st;
   return validate ? (pkv_status)pkv::read_and_clear_error_word(err, stream) : PKV_OK;
 }
