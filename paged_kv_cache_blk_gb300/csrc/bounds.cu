@@ -131,19 +131,24 @@ __global__ void __launch_bounds__(kBoundThreads) update_bounds_kernel(const Boun
   const int end = off + len;  // table positions held: below 2^31 (mb * bs is checked)
   const int j0 = (off + first) / p.bs;
   const int nj = (end - 1) / p.bs + 1 - j0;
-  const long long items = (long long)nj * p.hkv;
+  const int items = nj * p.hkv;  // (mb * hkv is checked)
   const int col = threadIdx.x % LPH;
+  const int step = p.ctas_seq * GROUPS;
+  const int32_t* table = p.bt + (long long)b * p.mb + j0;
+  int it = x * GROUPS + (int)threadIdx.x / LPH;
+  int blk = it < items ? table[it / p.hkv] : -1;
   // groups of a warp run the same number of steps, so the shuffles stay whole
-  for (long long i0 = (long long)x * GROUPS; i0 < items; i0 += (long long)p.ctas_seq * GROUPS) {
-    const long long it = i0 + threadIdx.x / LPH;
+  for (int i0 = x * GROUPS; i0 < items; i0 += step) {
     const bool live = it < items;
-    const int j = j0 + (int)(live ? it / p.hkv : 0);
-    const int g = (int)(live ? it % p.hkv : 0);
-    const int blk = live ? p.bt[(long long)b * p.mb + j] : -1;
-    const bool ok = live && blk >= 0 && blk < p.num_blocks;
+    const int j = j0 + (live ? it / p.hkv : 0);
+    const int g = live ? it % p.hkv : 0;
+    const int mine = blk;
+    it = it < items - step ? it + step : items;
+    blk = it < items ? table[it / p.hkv] : -1;  // the next step's, ahead of its rows
+    const bool ok = live && mine >= 0 && mine < p.num_blocks;
     if (live && !ok && col == 0) set_error(p.err, kErrIndex);
     const int rows = ok ? min(p.bs, end - j * p.bs) : 0;
-    const char* src = p.k + row_offset(ok ? blk : 0, p.layer, 0, p.L, p.bs, p.row_bytes);
+    const char* src = p.k + row_offset(ok ? mine : 0, p.layer, 0, p.L, p.bs, p.row_bytes);
     const char* elems = src + (long long)(g * LPH + col) * 16;
     const char* unit = src + p.scale_off + 4 * g;
     Extremes<MODE, EPL> ex;
@@ -182,7 +187,7 @@ __global__ void __launch_bounds__(kBoundThreads) update_bounds_kernel(const Boun
       hw[i / 4] |= (uint32_t)(code_up(ex.top(i), inv) + 128) << (8 * (i % 4));
       lw[i / 4] |= (uint32_t)(code_down(ex.bottom(i), inv) + 128) << (8 * (i % 4));
     }
-    const long long head = ((long long)blk * p.L + p.layer) * p.hkv + g;
+    const long long head = ((long long)mine * p.L + p.layer) * p.hkv + g;
     char* dst = p.codes + head * (2 * D) + col * EPL;
     store_bytes(dst, hw);
     store_bytes(dst + D, lw);
@@ -192,12 +197,12 @@ __global__ void __launch_bounds__(kBoundThreads) update_bounds_kernel(const Boun
 
 template <int MODE>
 cudaError_t launch_bounds_mode(BoundParams& p, int d, int batch, int sms, cudaStream_t s) {
-  // Enough CTAs for 16 warps an SM over the batch, none that the longest
-  // possible table would leave idle.
+  // Enough CTAs to fill the SMs over the batch (48 warps each), none that the
+  // longest possible table would leave idle.
   const int lph = d / (MODE == PKV_BF16 ? 8 : MODE == PKV_F32 ? 4 : 16);
   const long long groups = kBoundThreads / lph;
   long long ctas = ((long long)p.mb * p.hkv + groups - 1) / groups;
-  const long long want = (4ll * sms + batch - 1) / batch;
+  const long long want = (12ll * sms + batch - 1) / batch;
   if (ctas > want) ctas = want;
   p.ctas_seq = (int)ctas;
   const dim3 grid((unsigned)(ctas * batch));
@@ -229,8 +234,9 @@ extern "C" pkv_status pkv_update_block_bounds(const pkv_pool* pool, int32_t laye
       !pkv::aligned(first_pos, 4) || !pkv::aligned(bound_codes, 16) ||
       !pkv::aligned(bound_scales, 4))
     return PKV_ERR_INVALID_ARG;
-  // table positions are 32-bit in the kernel
-  if ((int64_t)max_blocks_per_seq * v.block_size > INT32_MAX || batch > (1 << 24))
+  // table positions and (block, head) pairs are 32-bit in the kernel
+  if ((int64_t)max_blocks_per_seq * v.block_size > INT32_MAX || batch > (1 << 24) ||
+      (int64_t)max_blocks_per_seq * v.num_kv_heads > INT32_MAX / 2)
     return PKV_ERR_UNSUPPORTED;
   int optin, grid, validate, sms;
   int* err;

@@ -165,8 +165,13 @@ struct Tile {
   static constexpr int kHalf = kTile * kRow;        // K (or V) rows
   static constexpr int kScales = MODE == PKV_I8 ? 2 * kTile * 4 : 0;
   static constexpr int kBytes = 2 * kHalf + kScales;
+  // Tiles of a warp's ring: what lets two CTAs share an SM.  (64 sequences of
+  // 2048 selected tokens, Hkv 8, D 128: bf16 with 3 tiles 82 us, with 2 and three
+  // CTAs an SM 98, with 5 and one 102; int8 with 5 tiles 72 us, with 3 and
+  // four CTAs 81, with 4 and three 98: the 512 CTAs then no longer fill
+  // whole rounds.)
   static constexpr int kStages = D == 128 ? (MODE == PKV_F32 ? 2 : MODE == PKV_BF16 ? 3 : 5)
-                                          : (MODE == PKV_F32 ? 3 : MODE == PKV_BF16 ? 5 : 8);
+                                          : (MODE == PKV_F32 ? 2 : MODE == PKV_BF16 ? 5 : 8);
 
   // Byte offset of chunk c of row r: chunks of a row are permuted so that the
   // 8 rows of an ldmatrix (and the 2 rows x 4 chunks of an LDS.128 phase of
@@ -460,9 +465,19 @@ struct FmaState {
 #pragma unroll
       for (int e = 0; e < PD; ++e) o[h][e] = 0.f;
     }
-    const float* src = reinterpret_cast<const float*>(p.q) + ((long long)t * p.hq + g * p.G) * D;
-    for (int i = lane; i < GP * D; i += 32)
-      sts_f32(sq + i * 4, i < p.G * D ? src[i] * p.qscale : 0.f);
+    const char* src = p.q + ((long long)t * p.hq + g * p.G) * (D * 4) + lane * 16;
+    uint4 x[GP * D / 128];
+#pragma unroll
+    for (int i = 0; i < GP * D / 128; ++i)
+      x[i] = i * 128 + lane * 4 < p.G * D ? ld_stream(src + i * 512) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+    for (int i = 0; i < GP * D / 128; ++i) {
+      const uint32_t at = sq + i * 512 + lane * 16;
+      sts_f32(at, __uint_as_float(x[i].x) * p.qscale);
+      sts_f32(at + 4, __uint_as_float(x[i].y) * p.qscale);
+      sts_f32(at + 8, __uint_as_float(x[i].z) * p.qscale);
+      sts_f32(at + 12, __uint_as_float(x[i].w) * p.qscale);
+    }
     __syncwarp();
   }
 
@@ -581,7 +596,16 @@ __global__ void __launch_bounds__(kSpThreads) sparse_decode_kernel(const SparseP
   const int t = row / p.hkv, g = row - t * p.hkv;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
 
-  const int seq = p.tok_seq[t], pos = p.tok_pos[t];
+  // The chain of loads before the first row arrives is list, sequence and
+  // position; offset and table entry; row: a batch's list entries are loaded one
+  // batch ahead, the first ones here.
+  const int32_t* list = p.sel + (long long)row * p.K;
+  const int all_tiles = p.K * p.parts;
+  const int stride = (int)S * kSpWarps;
+  int next = (int)rank * kSpWarps + warp;  // first tile of the batch to come
+  auto listed = [&](long long ts) { return ts < all_tiles ? ld_volatile(list + ts / p.parts) : -1; };
+  int ahead = listed(next + (long long)lane * stride);
+  const int seq = ld_volatile(p.tok_seq + t), pos = ld_volatile(p.tok_pos + t);
   if (seq < 0) return;  // padding: the whole cluster leaves, nothing is written
   int off = 0, end = 0;  // table positions [off, end) are seen
   if (seq >= p.batch) {
@@ -594,24 +618,14 @@ __global__ void __launch_bounds__(kSpThreads) sparse_decode_kernel(const SparseP
       end = off + pos + 1;
     }
   }
-  const int tiles = end > 0 ? p.K * p.parts : 0;  // a bad token sees nothing: zeros
+  const int tiles = end > 0 ? all_tiles : 0;  // a bad token sees nothing: zeros
 
   const uint32_t base = smem_addr(smem);
   const uint32_t ring = base + warp * Lay::kWarp;
-  std::conditional_t<MODE == PKV_F32, FmaState<D, HEADS>,
-                     MmaState<MODE == PKV_F32 ? PKV_BF16 : MODE, D, (HEADS + 7) / 8>>
-      state;
-  if constexpr (MODE == PKV_F32)
-    state.init(p, t, g, lane, ring + Lay::kBody);
-  else
-    state.init(p, t, g, lane);
 
   // ---- lookup: 32 tiles a time, one per lane ----
-  const int32_t* list = p.sel + (long long)row * p.K;
   const int32_t* table = p.bt + (long long)(end > 0 ? seq : 0) * p.mb;
-  const int stride = (int)S * kSpWarps;
   const int rows_tile = min(p.bs, kTile);
-  int next = (int)rank * kSpWarps + warp;  // first tile of the batch to come
   long long my_row = 0;
   int my_range = 0;
   unsigned todo = 0;
@@ -619,25 +633,21 @@ __global__ void __launch_bounds__(kSpThreads) sparse_decode_kernel(const SparseP
     // stops at the last batch or at one that has something to do
     while (todo == 0 && next < tiles) {
       const long long ts = next + (long long)lane * stride;
+      const int j = ahead;
+      ahead = listed(ts + 32ll * stride);
       int lo = 0, hi = 0;
-      if (ts < tiles) {
-        const int j = list[ts / p.parts];
-        if (j >= p.mb) {
+      if (j >= p.mb) set_error(p.err, kErrIndex);
+      if (j >= 0 && j < p.mb) {
+        const int blk = ld_volatile(table + j);
+        const int r0 = (int)(ts % p.parts) * kTile;
+        const int p0 = j * p.bs + r0;
+        lo = max(0, off - p0);
+        hi = min(rows_tile, end - p0);
+        if (blk >= 0 && blk < p.num_blocks) {
+          my_row = ((long long)blk * p.L + p.layer) * p.bs + r0;
+        } else if (lo < hi) {
           set_error(p.err, kErrIndex);
-        } else if (j >= 0) {
-          const int r0 = (int)(ts % p.parts) * kTile;
-          const int p0 = j * p.bs + r0;
-          lo = max(0, off - p0);
-          hi = min(rows_tile, end - p0);
-          if (lo < hi) {
-            const int blk = table[j];
-            if (blk < 0 || blk >= p.num_blocks) {
-              set_error(p.err, kErrIndex);
-              hi = 0;
-            } else {
-              my_row = ((long long)blk * p.L + p.layer) * p.bs + r0;
-            }
-          }
+          hi = 0;
         }
       }
       my_range = lo | hi << 8;
@@ -661,8 +671,16 @@ __global__ void __launch_bounds__(kSpThreads) sparse_decode_kernel(const SparseP
     cp_commit();
   };
 
+  // The query: bf16 fragments are plain loads and go ahead of the tiles; the
+  // others compute on it, while the first tiles arrive.
+  std::conditional_t<MODE == PKV_F32, FmaState<D, HEADS>,
+                     MmaState<MODE == PKV_F32 ? PKV_BF16 : MODE, D, (HEADS + 7) / 8>>
+      state;
+  if constexpr (MODE == PKV_BF16) state.init(p, t, g, lane);
 #pragma unroll 1
   for (int s = 0; s < NST - 1; ++s) issue(s);
+  if constexpr (MODE == PKV_F32) state.init(p, t, g, lane, ring + Lay::kBody);
+  if constexpr (MODE == PKV_I8) state.init(p, t, g, lane);
   int stage = 0;
 #pragma unroll 1
   while (true) {
@@ -684,34 +702,43 @@ __global__ void __launch_bounds__(kSpThreads) sparse_decode_kernel(const SparseP
     cluster_sync();
   else
     __syncthreads();
+  // weights of the S * kSpWarps <= 32 states of each head, one state per lane
+  __shared__ float weight[HEADS][32];
+  const int states = (int)S * kSpWarps;
+  const uint32_t st_at = cluster_map(base + (lane % kSpWarps) * Lay::kWarp + HEADS * D * 4,
+                                     lane < states ? lane / kSpWarps : 0);
+  for (int h = warp; h < p.G; h += kSpWarps) {
+    const float m = lane < states ? ld_cluster_f32(st_at + h * 8) : -INFINITY;
+    const float l = lane < states ? ld_cluster_f32(st_at + h * 8 + 4) : 0.f;
+    float M = m;
+#pragma unroll
+    for (int o = 16; o; o >>= 1) M = fmaxf(M, __shfl_xor_sync(kAll, M, o));
+    // a state at -inf saw nothing, or only NaN: its l and O are 0, or NaN
+    const float f = m == -INFINITY ? 1.f : exp2f(m - M);
+    float sum = f * l;
+#pragma unroll
+    for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(kAll, sum, o);
+    weight[h][lane] = sum == 0.f ? 0.f : f / sum;  // no weight at all: zeros
+  }
+  __syncthreads();
   const int pairs = p.G * (D / 2);
   for (int i = (int)rank * kSpThreads + tid; i < pairs; i += (int)S * kSpThreads) {
     const int h = i / (D / 2), d = (i % (D / 2)) * 2;
-    float M = -INFINITY;
-    for (uint32_t r = 0; r < S; ++r)
-#pragma unroll
-      for (int w = 0; w < kSpWarps; ++w)
-        M = fmaxf(M, ld_cluster_f32(
-                         cluster_map(base + w * Lay::kWarp + HEADS * D * 4 + h * 8, r)));
-    float x = 0.f, y = 0.f, l = 0.f;
-    for (uint32_t r = 0; r < S; ++r)
-#pragma unroll
-      for (int w = 0; w < kSpWarps; ++w) {
-        const uint32_t a = cluster_map(base + w * Lay::kWarp, r);
-        const float m = ld_cluster_f32(a + HEADS * D * 4 + h * 8);
-        const float lw = ld_cluster_f32(a + HEADS * D * 4 + h * 8 + 4);
-        if (m == -INFINITY && lw == 0.f) continue;  // saw nothing
-        const float f = m == -INFINITY ? 1.f : exp2f(m - M);  // (NaN scores leave m at -inf)
-        l += f * lw;
-        x += f * ld_cluster_f32(a + (h * D + d) * 4);
-        y += f * ld_cluster_f32(a + (h * D + d) * 4 + 4);
-      }
-    const float inv = l > 0.f || l != l ? 1.f / l : 0.f;  // no weight at all: zeros
+    float x = 0.f, y = 0.f;
+#pragma unroll 4
+    for (int j = 0; j < states; ++j) {
+      const uint32_t a = cluster_map(base + (j % kSpWarps) * Lay::kWarp + (h * D + d) * 4,
+                                     j / kSpWarps);
+      float u, v;
+      asm volatile("ld.shared::cluster.v2.f32 {%0,%1}, [%2];" : "=f"(u), "=f"(v) : "r"(a));
+      x += weight[h][j] * u;
+      y += weight[h][j] * v;
+    }
     const long long at = ((long long)t * p.hq + g * p.G + h) * D + d;
     if constexpr (MODE == PKV_F32) {
-      *reinterpret_cast<float2*>(p.out + at * 4) = make_float2(x * inv, y * inv);
+      *reinterpret_cast<float2*>(p.out + at * 4) = make_float2(x, y);
     } else {
-      *reinterpret_cast<uint32_t*>(p.out + at * 2) = pack_bf16x2(x * inv, y * inv);
+      *reinterpret_cast<uint32_t*>(p.out + at * 2) = pack_bf16x2(x, y);
     }
   }
   if (S > 1) cluster_sync();  // no CTA leaves while another may still read its states
@@ -781,6 +808,9 @@ extern "C" pkv_status pkv_decode_attention_sparse(
     if ((st = pkv::read_and_clear_error_word(err, stream)) != PKV_OK) return (pkv_status)st;
   }
   // CTAs of a cluster: until two per SM are there, each warp with a few tiles.
+  // (More of them cost more than they balance, since every CTA waits for a chain
+  // of index loads first: the 64-sequence case above takes 82 us at S = 1, 91 at 2,
+  // 102 at 4.)
   unsigned S = 1;
   while ((int)S < pkv::kSpMaxCluster && rows * S < 2 * sms && tiles > S * pkv::kSpWarps * 2)
     S *= 2;
