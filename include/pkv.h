@@ -230,9 +230,8 @@ PKV_API pkv_status pkv_rope_init_freqs(pkv_rope* rope, int32_t rotary_dim, int32
  * q itself (same stride); other overlaps are not allowed.  num_q_heads 0
  * (q and q_out NULL) turns and stores the keys alone.  slot_mapping (int64
  * [num_tokens], device) receives the slots when not NULL.
- * Supported: head_dim 32, 64, 128 or 256; rotary_dim a multiple of 16 (half
- * layout) or 8 (interleaved), for fp32 pools with head_dim <= 128 of 8 or 4;
- * others PKV_ERR_UNSUPPORTED. */
+ * Supported: head_dim 32, 64, 128 or 256; rotary_dim a multiple of 8 (of 4 for
+ * fp32 pools with head_dim <= 128); others PKV_ERR_UNSUPPORTED. */
 PKV_API pkv_status pkv_rope_append(const pkv_pool* pool, int32_t layer, const pkv_rope* rope,
                                    const int32_t* block_tables, int32_t max_blocks_per_seq,
                                    const int32_t* offsets, int32_t batch,

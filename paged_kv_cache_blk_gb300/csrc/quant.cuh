@@ -44,6 +44,36 @@ __device__ __forceinline__ int quantise_value(float x, uint32_t absmax, float sc
   return absmax == 0 ? 0 : min(127, max(-127, __float2int_rn(div_ieee(x, scale))));
 }
 
+// The same codes for 4 N values of a head, as stored bytes (code + 128), four a
+// word.  x / scale is first taken as x * (1 / scale): an approximate reciprocal
+// (1 ulp, 2^-23) and two roundings of 2^-24 of a value up to 127, the IEEE
+// quotient one more: together below 2^-14,
+// so both round to the same code unless the value lies that near a half-way
+// point, and only such elements are divided (bf16 rows have exact half-way
+// points, one element in 300).  Scales whose reciprocal is not an
+// ordinary number divide always.
+template <int N>
+__device__ __forceinline__ void quantise_bytes(const float* x, uint32_t absmax, float scale,
+                                               uint32_t (&w)[N]) {
+  float inv;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(scale));
+  const bool exact = !(scale > 7.9e-31f && scale < 1.2e30f);
+  uint32_t b[4 * N];
+#pragma unroll
+  for (int i = 0; i < 4 * N; ++i) {
+    // adding 1.5 * 2^23 + 128 leaves the rounded code + 128 in the low byte
+    const float t = x[i] * inv;
+    const float r = t + 12583040.f;
+    b[i] = __float_as_uint(r);
+    if (exact || fabsf(t - (r - 12583040.f)) > 0.5f - 0x1p-14f)
+      b[i] = (uint32_t)(quantise_value(x[i], absmax, scale) + 128);
+  }
+#pragma unroll
+  for (int i = 0; i < N; ++i)
+    w[i] = __byte_perm(__byte_perm(b[4 * i], b[4 * i + 1], 0x0040),
+                       __byte_perm(b[4 * i + 2], b[4 * i + 3], 0x0040), 0x5410);
+}
+
 // Quantise one head (VPL values per lane); returns the scale, codes in c.
 template <int VPL>
 __device__ __forceinline__ float quantise_head(const float (&x)[VPL], int (&c)[VPL]) {

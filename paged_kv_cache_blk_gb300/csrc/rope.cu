@@ -15,15 +15,20 @@
 // |pos| * 2^-54 turns at most.  The top 32 bits, as a signed fraction of a half turn,
 // go to sincospif, whose argument reduction is then trivial.
 //
-// Layout of the work.  A lane owns 16 bytes (8 elements, 4 of fp32) of a head
-// row, so D / EPL lanes hold one head and a warp 32 * EPL / D of them.  A
-// warp's task is one token and a run of its Hq + 2 Hkv head rows: the lane's
-// columns, and so its cosines and sines, are the same in every row, and are
-// computed once per task.  The other half of a pair lies rotary_dim / 2
-// columns away (half layout: a shuffle of the 4 raw words) or in the same
-// lane (interleaved).
+// Layout of the work.  A lane owns 8 elements (4 of fp32 up to D 128) of a head
+// row, so D / EPL lanes hold one head and a warp 32 * EPL / D of them.  They
+// are EPL / 2 whole pairs: adjacent elements (interleaved), or two runs
+// rotary_dim / 2 apart (half layout), so no pair is split between lanes.  A warp's
+// task is one token and a run of its Hq + 2 Hkv head rows: the lane's columns,
+// and so its cosines and sines, are the same in every row.  The rotary_dim / 2
+// angles of the token are spread over the 32 lanes, once per task, and handed
+// out by shuffles.
+//
+// What bounds it: many tokens, the bytes of q, k and v, read and written
+// once; few, latency (the chain sequence - offset - table entry - store).
 #include <cmath>
 #include <cstring>
+#include <type_traits>
 
 #include "common.cuh"
 #include "quant.cuh"
@@ -66,59 +71,99 @@ __device__ __forceinline__ void rope_sincos(unsigned long long step, int pos, fl
   *c *= scale;
 }
 
-template <typename T, int EPL>
-__device__ __forceinline__ void unpack(const uint4 (&r)[EPL * sizeof(T) / 16], float (&x)[EPL]) {
-  constexpr int NV = EPL * sizeof(T) / 16;
+// The EPL elements of a lane as 32-bit words: two runs of EPL / 2 elements, at
+// byte offsets o0 and o1 of a row (one 16-byte run where ONE).
+template <typename T, int EPL, bool ONE>
+__device__ __forceinline__ void load_runs(const char* row, int o0, int o1,
+                                          uint32_t (&w)[EPL * sizeof(T) / 4]) {
+  constexpr int W = EPL * sizeof(T) / 4;
+  if constexpr (W == 4 && !ONE) {
+    const uint2 a = *reinterpret_cast<const uint2*>(row + o0);
+    const uint2 b = *reinterpret_cast<const uint2*>(row + o1);
+    w[0] = a.x; w[1] = a.y; w[2] = b.x; w[3] = b.y;
+  } else {
 #pragma unroll
-  for (int v = 0; v < NV; ++v) {
-    const uint32_t w[4] = {r[v].x, r[v].y, r[v].z, r[v].w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      if constexpr (sizeof(T) == 2) {
-        x[8 * v + 2 * i] = bf16_lo(w[i]);
-        x[8 * v + 2 * i + 1] = bf16_hi(w[i]);
-      } else {
-        x[4 * v + i] = __uint_as_float(w[i]);
-      }
+    for (int v = 0; v < W / 4; ++v) {
+      const uint4 a = *reinterpret_cast<const uint4*>(row + (v ? o1 : o0));
+      w[4 * v] = a.x; w[4 * v + 1] = a.y; w[4 * v + 2] = a.z; w[4 * v + 3] = a.w;
     }
   }
 }
 
-template <typename T, int EPL>
-__device__ __forceinline__ void store_row(char* dst, const float (&y)[EPL]) {
+template <typename T, int EPL, bool ONE>
+__device__ __forceinline__ void store_runs(char* row, int o0, int o1,
+                                           const uint32_t (&w)[EPL * sizeof(T) / 4]) {
+  constexpr int W = EPL * sizeof(T) / 4;
+  if constexpr (W == 4 && !ONE) {
+    *reinterpret_cast<uint2*>(row + o0) = make_uint2(w[0], w[1]);
+    *reinterpret_cast<uint2*>(row + o1) = make_uint2(w[2], w[3]);
+  } else {
 #pragma unroll
-  for (int v = 0; v < EPL * (int)sizeof(T) / 16; ++v) {
-    uint32_t w[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      if constexpr (sizeof(T) == 2)
-        w[i] = pack_bf16x2(y[8 * v + 2 * i], y[8 * v + 2 * i + 1]);
-      else
-        w[i] = __float_as_uint(y[4 * v + i]);
-    }
-    st_global(dst + 16 * v, make_uint4(w[0], w[1], w[2], w[3]));
+    for (int v = 0; v < W / 4; ++v)
+      st_global(row + (v ? o1 : o0),
+                make_uint4(w[4 * v], w[4 * v + 1], w[4 * v + 2], w[4 * v + 3]));
   }
 }
+
+template <typename T, int EPL>
+__device__ __forceinline__ void unpack(const uint32_t (&w)[EPL * sizeof(T) / 4], float (&x)[EPL]) {
+#pragma unroll
+  for (int i = 0; i < EPL; ++i)
+    x[i] = sizeof(T) == 4 ? __uint_as_float(w[i * sizeof(T) / 4])
+           : i & 1        ? bf16_hi(w[i / 2])
+                          : bf16_lo(w[i / 2]);
+}
+
+template <typename T, int EPL>
+__device__ __forceinline__ void pack(const float (&y)[EPL], uint32_t (&w)[EPL * sizeof(T) / 4]) {
+#pragma unroll
+  for (int i = 0; i < EPL * (int)sizeof(T) / 4; ++i) {
+    if constexpr (sizeof(T) == 2)
+      w[i] = pack_bf16x2(y[2 * i], y[2 * i + 1]);
+    else
+      w[i] = __float_as_uint(y[i]);
+  }
+}
+
+// Cosines and sines of the NF consecutive angles from f0 on.  Lane l computes
+// the angles l * NPL .. l * NPL + NPL - 1 (`step`), the others come from their
+// lanes.
+template <int NF, int NPL>
+__device__ __forceinline__ void hand_out(const unsigned long long (&step)[4], int pos, float scale,
+                                         int f0, float (&s)[NF], float (&c)[NF]) {
+  float ms[NPL], mc[NPL];
+#pragma unroll
+  for (int j = 0; j < NPL; ++j) rope_sincos(step[j], pos, scale, &ms[j], &mc[j]);
+#pragma unroll
+  for (int i = 0; i < NF; ++i) {
+    s[i] = __shfl_sync(kAll, ms[i % NPL], f0 / NPL + i / NPL);
+    c[i] = __shfl_sync(kAll, mc[i % NPL], f0 / NPL + i / NPL);
+  }
+}
+
+enum : int { kRowQ = 0, kRowK = 1, kRowV = 2 };
 
 // T: type of q, k_new, v_new and q_out; EPL: elements per lane; LPH: lanes per
 // head row; INTER: pairs are adjacent elements; QUANT: int8 pool.
 template <typename T, int EPL, int LPH, bool INTER, bool QUANT>
-__global__ void __launch_bounds__(kRopeWarps * 32)
+__global__ void __launch_bounds__(kRopeWarps * 32, 5)
     rope_append_kernel(const __grid_constant__ RopeParams p) {
-  constexpr int NV = EPL * sizeof(T) / 16;
+  constexpr int W = EPL * sizeof(T) / 4;  // words of a lane
   constexpr int RPW = 32 / LPH;
-  constexpr int NF = INTER ? EPL / 2 : EPL;  // frequencies of a lane
+  constexpr int NF = EPL / 2;  // pairs of a lane
+  constexpr int ROW = EPL * LPH * (int)sizeof(T);
   const int lane = threadIdx.x & 31;
   const int sub = lane / LPH, col = lane % LPH;
-  const int d = col * EPL;
-  const bool turns = d < p.rd;
+  const bool turns = col * EPL < p.rd;
   const int half = p.rd / 2;
-  unsigned long long step[NF];
-  const int f0 = INTER ? d / 2 : (d < half ? d : d - half);
+  const int f0 = turns ? col * NF : 0;
+  // first elements of the lane's two runs
+  const int e0 = INTER || !turns ? col * EPL : col * NF;
+  const int e1 = INTER || !turns ? e0 + NF : e0 + half;
+  const int npl = half <= 32 ? 1 : half <= 64 ? 2 : 4;
+  unsigned long long step[4];
 #pragma unroll
-  for (int i = 0; i < NF; ++i) step[i] = turns ? p.step[f0 + i] : 0ull;
-  // the lane that holds the other half of this lane's pairs
-  const int mate = !turns ? col : d < half ? col + half / EPL : col - half / EPL;
+  for (int j = 0; j < 4; ++j) step[j] = j < npl && lane * npl + j < half ? p.step[lane * npl + j] : 0;
   const int rows = p.hq + 2 * p.hkv;
   griddep_wait();
   griddep_launch_dependents();
@@ -126,7 +171,7 @@ __global__ void __launch_bounds__(kRopeWarps * 32)
   const long long warps = (long long)gridDim.x * kRopeWarps;
   for (long long w = blockIdx.x * (long long)kRopeWarps + (threadIdx.x >> 5); w < tasks;
        w += warps) {
-    const long long t = w / p.chunks;
+    const long long t = p.chunks == 1 ? w : w / p.chunks;
     const int chunk = (int)(w - t * p.chunks);
     const int r0 = chunk * p.rows_task;
     const int r1 = min(rows, r0 + p.rows_task);
@@ -141,99 +186,85 @@ __global__ void __launch_bounds__(kRopeWarps * 32)
     if (slot < 0) continue;  // padding or out of range: nothing of this token is written
     const int pos = p.rope_pos ? p.rope_pos[t] : p.ss.tok_pos[t];
     float c[NF], s[NF];
-#pragma unroll
-    for (int i = 0; i < NF; ++i) rope_sincos(step[i], pos, p.attn_scale, &s[i], &c[i]);
-    if constexpr (!INTER) {
-      // y = x c + mate's x * s: the sine of the first half enters negated
-#pragma unroll
-      for (int i = 0; i < NF; ++i) s[i] = d < half ? -s[i] : s[i];
-    }
+    if (npl == 1)
+      hand_out<NF, 1>(step, pos, p.attn_scale, f0, s, c);
+    else if (npl == 2)
+      hand_out<NF, 2>(step, pos, p.attn_scale, f0, s, c);
+    else
+      hand_out<NF, 4>(step, pos, p.attn_scale, f0, s, c);
     const long long dst_row =
-        row_offset(slot / p.bs, p.layer, (int)(slot % p.bs), p.L, p.bs, p.row_bytes);
+        row_offset(slot >> (31 - __clz(p.bs)), p.layer, (int)(slot & (p.bs - 1)), p.L, p.bs,
+                   p.row_bytes);
+
+    // heads [a, b) of one kind: loads of kRopeUnroll steps, then stores
+    auto run = [&](auto kind_tag, const char* src, int a, int b) {
+      constexpr int KIND = decltype(kind_tag)::value;
+      constexpr int ES = sizeof(T);
 #pragma unroll 1
-    for (int rb = r0; rb < r1; rb += RPW * kRopeUnroll) {
-      uint4 raw[kRopeUnroll][NV];
+      for (int rb = a + sub; rb - sub < b; rb += RPW * kRopeUnroll) {
+        uint32_t raw[kRopeUnroll][W] = {};
 #pragma unroll
-      for (int u = 0; u < kRopeUnroll; ++u) {
-        const int r = rb + u * RPW + sub;
-        const char* src = nullptr;
-        if (r < r1) {
-          if (r < p.hq)
-            src = p.q + t * p.q_stride + (long long)r * (EPL * LPH * sizeof(T));
-          else if (r < p.hq + p.hkv)
-            src = p.k_new + t * p.k_stride + (long long)(r - p.hq) * (EPL * LPH * sizeof(T));
-          else
-            src = p.v_new + t * p.v_stride +
-                  (long long)(r - p.hq - p.hkv) * (EPL * LPH * sizeof(T));
-        }
+        for (int u = 0; u < kRopeUnroll; ++u)
+          if (rb + u * RPW < b)
+            load_runs<T, EPL, INTER>(src + (long long)(rb + u * RPW) * ROW, e0 * ES, e1 * ES,
+                                     raw[u]);
 #pragma unroll
-        for (int v = 0; v < NV; ++v)
-          raw[u][v] = src ? *reinterpret_cast<const uint4*>(src + col * (EPL * sizeof(T)) + 16 * v)
-                          : make_uint4(0, 0, 0, 0);
-      }
-#pragma unroll
-      for (int u = 0; u < kRopeUnroll; ++u) {
-        const int r = rb + u * RPW + sub;
-        float y[EPL];
-        unpack<T, EPL>(raw[u], y);
-        if constexpr (INTER) {
-          if (turns && r < p.hq + p.hkv) {
+        for (int u = 0; u < kRopeUnroll; ++u) {
+          const int r = rb + u * RPW;
+          if (r - sub >= b) break;  // (the whole warp)
+          if constexpr (KIND == kRowV && !QUANT) {
+            if (r < b)
+              store_runs<T, EPL, INTER>(p.v_cache + dst_row + (long long)r * ROW, e0 * ES, e1 * ES,
+                                        raw[u]);
+            continue;
+          }
+          float y[EPL];
+          unpack<T, EPL>(raw[u], y);
+          if (KIND != kRowV && turns) {
 #pragma unroll
             for (int i = 0; i < NF; ++i) {
-              const float a = y[2 * i], b = y[2 * i + 1];
-              y[2 * i] = a * c[i] - b * s[i];
-              y[2 * i + 1] = b * c[i] + a * s[i];
+              const int ia = INTER ? 2 * i : i, ib = INTER ? 2 * i + 1 : i + NF;
+              const float x0 = y[ia], x1 = y[ib];
+              y[ia] = x0 * c[i] - x1 * s[i];
+              y[ib] = x1 * c[i] + x0 * s[i];
             }
           }
-        } else {
-          uint4 other[NV];
+          if constexpr (KIND == kRowQ || !QUANT) {
+            char* dst = KIND == kRowQ ? p.q_out + t * p.qo_stride : p.k_cache + dst_row;
+            uint32_t w[W];
+            pack<T, EPL>(y, w);
+            if (r < b)
+              store_runs<T, EPL, INTER>(dst + (long long)r * ROW, e0 * ES, e1 * ES, w);
+          } else {
+            // absmax of the head over its LPH lanes, then scale and codes as
+            // pkv_write_slots
+            char* dst = (KIND == kRowK ? p.k_cache : p.v_cache) + dst_row;
+            uint32_t m = 0;
 #pragma unroll
-          for (int v = 0; v < NV; ++v) {
-            other[v].x = __shfl_sync(kAll, raw[u][v].x, mate, LPH);
-            other[v].y = __shfl_sync(kAll, raw[u][v].y, mate, LPH);
-            other[v].z = __shfl_sync(kAll, raw[u][v].z, mate, LPH);
-            other[v].w = __shfl_sync(kAll, raw[u][v].w, mate, LPH);
+            for (int i = 0; i < EPL; ++i) m = max(m, __float_as_uint(y[i]) & 0x7FFFFFFFu);
+#pragma unroll
+            for (int o = LPH / 2; o; o >>= 1) m = max(m, __shfl_xor_sync(kAll, m, o));
+            if (r < b) {
+              const float scale = div_ieee(__uint_as_float(m), 127.f);
+              uint32_t code[EPL / 4];
+              quantise_bytes<EPL / 4>(y, m, scale, code);
+              char* at = dst + r * (EPL * LPH);
+              *reinterpret_cast<uint32_t*>(at + e0) = code[0];
+              *reinterpret_cast<uint32_t*>(at + e1) = code[EPL / 4 - 1];
+              if (col == 0) *reinterpret_cast<float*>(dst + p.scale_off + 4 * r) = scale;
+            }
           }
-          if (turns && r < p.hq + p.hkv) {
-            float z[EPL];
-            unpack<T, EPL>(other, z);
-#pragma unroll
-            for (int i = 0; i < EPL; ++i) y[i] = y[i] * c[i] + z[i] * s[i];
-          }
-        }
-        if (r < p.hq) {
-          if (r < r1)
-            store_row<T, EPL>(p.q_out + t * p.qo_stride +
-                                  (long long)r * (EPL * LPH * sizeof(T)) + col * (EPL * sizeof(T)),
-                              y);
-          if constexpr (!QUANT) continue;
-        }
-        const bool is_k = r < p.hq + p.hkv;
-        const int g = is_k ? r - p.hq : r - p.hq - p.hkv;
-        char* dst = (is_k ? p.k_cache : p.v_cache) + dst_row;
-        if constexpr (QUANT) {
-          // absmax of the head over its LPH lanes (every lane takes part in
-          // the shuffles), then scale and codes as pkv_write_slots
-          uint32_t m = 0;
-#pragma unroll
-          for (int i = 0; i < EPL; ++i) m = max(m, __float_as_uint(y[i]) & 0x7FFFFFFFu);
-#pragma unroll
-          for (int o = LPH / 2; o; o >>= 1) m = max(m, __shfl_xor_sync(kAll, m, o));
-          if (r >= p.hq && r < r1) {
-            const float scale = div_ieee(__uint_as_float(m), 127.f);
-            int code[EPL];
-#pragma unroll
-            for (int i = 0; i < EPL; ++i) code[i] = quantise_value(y[i], m, scale);
-            store_codes<EPL>(dst + g * (EPL * LPH) + d, code);
-            if (col == 0) *reinterpret_cast<float*>(dst + p.scale_off + 4 * g) = scale;
-          }
-        } else {
-          if (r < r1)
-            store_row<T, EPL>(
-                dst + (long long)g * (EPL * LPH * sizeof(T)) + col * (EPL * sizeof(T)), y);
         }
       }
-    }
+    };
+    const int k0 = p.hq, v0 = p.hq + p.hkv;
+    if (r0 < k0)
+      run(std::integral_constant<int, kRowQ>(), p.q + t * p.q_stride, r0, min(r1, k0));
+    if (r1 > k0 && r0 < v0)
+      run(std::integral_constant<int, kRowK>(), p.k_new + t * p.k_stride, max(r0, k0) - k0,
+          min(r1, v0) - k0);
+    if (r1 > v0)
+      run(std::integral_constant<int, kRowV>(), p.v_new + t * p.v_stride, max(r0, v0) - v0, r1 - v0);
   }
 }
 
@@ -371,9 +402,9 @@ pkv_status pkv_rope_append(const pkv_pool* pool, int32_t layer, const pkv_rope* 
     return PKV_ERR_INVALID_ARG;
   if (v.head_dim != 32 && v.head_dim != 64 && v.head_dim != 128 && v.head_dim != 256)
     return PKV_ERR_UNSUPPORTED;
-  // whole lanes turn: 16-byte pieces of a head, or of each half of its rotary part
+  // a lane's elements turn together
   const int piece = v.io_size == 4 && v.head_dim <= 128 ? 4 : 8;
-  if (rope->rotary_dim % (rope->interleaved ? piece : 2 * piece) != 0) return PKV_ERR_UNSUPPORTED;
+  if (rope->rotary_dim % piece != 0) return PKV_ERR_UNSUPPORTED;
   if (num_q_heads > (1 << 20)) return PKV_ERR_UNSUPPORTED;
   if (num_tokens == 0) return PKV_OK;
   if (!token_seq || !token_pos || !k_new || !v_new) return PKV_ERR_INVALID_ARG;

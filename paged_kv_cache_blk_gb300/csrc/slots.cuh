@@ -44,12 +44,14 @@ __device__ __forceinline__ int64_t token_slot(const SlotSrc& ss, long long t, lo
     if (report) set_error(err, kErrCapacity);
     return -1;
   }
-  const int blk = ss.bt[(long long)b * ss.mb + p / bs];
+  // block sizes are powers of two: a shift instead of a 64-bit division
+  const int shift = 31 - __clz(bs);
+  const int blk = ss.bt[(long long)b * ss.mb + (p >> shift)];
   if (blk < 0 || blk >= num_blocks) {
     if (report) set_error(err, kErrIndex);
     return -1;
   }
-  return (int64_t)blk * bs + p % bs;
+  return ((int64_t)blk << shift) + (p & (bs - 1));
 }
 
 }  // namespace pkv

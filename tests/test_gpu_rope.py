@@ -145,7 +145,8 @@ def _run(dev, dtype, H, G, D, rd, inter, bs=16, lens=None, fused=True, in_place=
     ("bf16", 8, 4, 128, 128), ("bf16", 2, 1, 64, 64), ("bf16", 1, 7, 128, 64),
     ("bf16", 4, 2, 32, 16), ("bf16", 3, 2, 256, 64), ("f32", 4, 3, 64, 64),
     ("f32", 2, 2, 128, 32), ("f32", 1, 5, 256, 256), ("f32", 2, 1, 32, 32),
-    ("i8", 8, 4, 128, 128), ("i8", 2, 3, 64, 32), ("i8", 4, 1, 32, 32), ("i8", 1, 2, 256, 128),
+    ("bf16", 2, 2, 128, 24), ("bf16", 2, 2, 256, 200), ("f32", 2, 2, 64, 20), ("f32", 1, 2, 256, 40),
+    ("i8", 8, 4, 128, 128), ("i8", 2, 3, 64, 32), ("i8", 2, 2, 128, 72), ("i8", 4, 1, 32, 32), ("i8", 1, 2, 256, 128),
 ])
 def test_rope_append(dev, dtype, H, G, D, rd, inter):
     _run(dev, dtype, H, G, D, rd, inter)

@@ -168,7 +168,7 @@ def test_append_refusals(lib):
     assert lib.pkv_rope_append(p, 0, None, 16, 4, None, 2, 16, 16, None, 3, 16, 256, 4, 16, 128, 16,
                                128, 16, 256, None, None) == bad
     assert call(rope=pkv.Rope(128).ref) == bad          # more than the head
-    assert call(rope=pkv.Rope(24).ref) == uns           # half of 24 is not whole lanes
+    assert call(rope=pkv.Rope(20).ref) == uns           # not whole lanes
     assert call(rope=pkv.Rope(12, interleaved=True).ref) == uns
     assert call(pool=ctypes.byref(_pool(head_dim=96)), n=3) == uns
     assert call(pool=ctypes.byref(_pool(dtype=2, head_dim=96)), n=3) == uns
