@@ -13,8 +13,9 @@
 // How.  One cluster of CTAs per (t, g); each CTA scores a contiguous range of
 // the entries and keeps the scores in its shared memory, so nothing but the
 // result is ever written.  The scores are found on the tensor cores: 16
-// blocks by 8 query heads by 16 code bytes per mma, the codes turned to biased
-// fp16 whole numbers in registers (sums below 2^24: exact).  A lane
+// blocks by 8 query heads by 16 code bytes per mma, the code bytes c + 128 taken
+// as fp16 subnormals (sums of whole numbers up to 255 * 127 * 128 < 2^24, in
+// units of 2^-24: exact).  A lane
 // loads 16-byte pieces of its blocks straight to registers, and the same
 // pieces of the query, coded once per CTA, from shared memory, so the order of
 // k does not matter.
@@ -54,7 +55,7 @@ struct SelectParams {
   int32_t* sel;
   int32_t* count;
   int* err;
-  long long num_blocks;
+  uint32_t num_blocks;
   int batch, mb, bs, L, layer, hq, hkv, G, K, sink, recent;
   int q_size;  // bytes of an element of q
   int cap;  // scores a CTA can hold
@@ -74,12 +75,14 @@ struct SelectShared {
   uint32_t warp_a[32], warp_b[32];
 };
 
-// Code bytes c + 128 to fp16 numbers 1024 + byte = 1152 + c, two a register.
+// Code bytes b = c + 128 to the fp16 numbers with those bits, the subnormals
+// b * 2^-24: two a register, one byte permute each.  The tensor cores take
+// subnormals as they are.
 __device__ __forceinline__ void codes_to_f16(uint32_t w, uint32_t& lo, uint32_t& hi) {
-  asm("prmt.b32 %0, %1, 0x64646464, 0x4140;" : "=r"(lo) : "r"(w));
-  asm("prmt.b32 %0, %1, 0x64646464, 0x4342;" : "=r"(hi) : "r"(w));
+  asm("prmt.b32 %0, %1, 0, 0x4140;" : "=r"(lo) : "r"(w));
+  asm("prmt.b32 %0, %1, 0, 0x4342;" : "=r"(hi) : "r"(w));
 }
-constexpr float kBias = 1152.f;
+constexpr float kUnit = 0x1p-24f, kBias = 128.f * kUnit;
 
 __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
                                         uint32_t a3, uint32_t b0, uint32_t b1) {
@@ -108,7 +111,9 @@ __device__ __forceinline__ void block_scan(uint32_t& a, uint32_t& b, SelectShare
   }
   if (lane == 31) { sh.warp_a[warp] = a; sh.warp_b[warp] = b; }
   __syncthreads();
-  for (int w = 0; w < warp; ++w) { a += sh.warp_a[w]; b += sh.warp_b[w]; }
+  // the warps before this one, one per lane
+  a += __reduce_add_sync(kAll, lane < warp ? sh.warp_a[lane] : 0u);
+  b += __reduce_add_sync(kAll, lane < warp ? sh.warp_b[lane] : 0u);
   __syncthreads();
 }
 
@@ -163,9 +168,9 @@ __global__ void __launch_bounds__(THREADS, (NT == 1 ? 768 : 384) / THREADS)
   constexpr int EPL = D / 32;       // elements of a query row a lane codes
   extern __shared__ uint32_t keys[];
   __shared__ SelectShared sh;
-  // the coded query: positive and negative parts, unit, bias of each piece
+  // the coded query: positive and negative parts, unit * 2^24, bias
   __shared__ __align__(16) unsigned char sq[2][NT * 8 * QROW];
-  __shared__ float s_unit[NT * 8], s_bias[2][LD][NT * 8];
+  __shared__ float s_unit[NT * 8], s_bias[NT * 8];
   griddep_wait();
   griddep_launch_dependents();
   uint32_t S;
@@ -203,7 +208,7 @@ __global__ void __launch_bounds__(THREADS, (NT == 1 ? 768 : 384) / THREADS)
     if (off < 0 || off >= p.bs || pos < 0 || (long long)off + pos >= (long long)p.mb * p.bs) {
       if (rank == 0 && tid == 0) set_error(p.err, kErrCapacity);
     } else {
-      n = (off + pos) / p.bs + 1;
+      n = ((off + pos) >> (31 - __clz(p.bs))) + 1;
     }
   }
   int32_t* out = p.sel + (long long)row * p.K;
@@ -228,148 +233,149 @@ __global__ void __launch_bounds__(THREADS, (NT == 1 ? 768 : 384) / THREADS)
   auto entry = [&](int i) { return i < cnt ? ld_volatile(table + i) : -1; };
   constexpr int STEP = WARPS * 16;
   int base = warp * 16;
-  int id0 = entry(base + gl), id1 = entry(base + gl + 8);
+  int id[2] = {entry(base + gl), entry(base + gl + 8)};
 
   // ---- the query in 8 bits ---------------------------------------------------
 #pragma unroll
   for (int u = 0; u < QPW; ++u) {
     const int h = warp + u * WARPS;
     if (h >= NT * 8) break;
-    float x[EPL];
-#pragma unroll
-    for (int i = 0; i < EPL; ++i)
-      x[i] = p.q_size == 4 ? __uint_as_float(qraw[u][i])
-             : i & 1       ? bf16_hi(qraw[u][i / 2])
-                           : bf16_lo(qraw[u][i / 2]);
-    uint32_t mx = 0;
-#pragma unroll
-    for (int i = 0; i < EPL; ++i) mx = max(mx, __float_as_uint(x[i]) & 0x7FFFFFFFu);
-    mx = __reduce_max_sync(kAll, mx);
-    const int e = bound_exponent(mx);
-    const float inv = pow2f(-e);
-    int up = 0, down = 0;
-    __half2 hp[EPL / 2], hn[EPL / 2];
-#pragma unroll
-    for (int i = 0; i < EPL / 2; ++i) {
-      const int a = min(127, max(-127, __float2int_rn(mul_ieee(x[2 * i], inv))));
-      const int b = min(127, max(-127, __float2int_rn(mul_ieee(x[2 * i + 1], inv))));
-      hp[i] = __floats2half2_rn((float)max(a, 0), (float)max(b, 0));
-      hn[i] = __floats2half2_rn((float)min(a, 0), (float)min(b, 0));
-      up += max(a, 0) + max(b, 0);
-      down += min(a, 0) + min(b, 0);
-    }
     const uint32_t at = smem_addr(sq[0]) + h * QROW + lane * EPL * 2;
+    uint32_t hp[EPL / 2] = {}, hn[EPL / 2] = {};
+    int sum = 0;
+    float unit = 0.f;
+    if (h < p.G) {
+      float x[EPL];
+#pragma unroll
+      for (int i = 0; i < EPL; ++i)
+        x[i] = p.q_size == 4 ? __uint_as_float(qraw[u][i])
+               : i & 1       ? bf16_hi(qraw[u][i / 2])
+                             : bf16_lo(qraw[u][i / 2]);
+      uint32_t mx = 0;
+#pragma unroll
+      for (int i = 0; i < EPL; ++i) mx = max(mx, __float_as_uint(x[i]) & 0x7FFFFFFFu);
+      mx = __reduce_max_sync(kAll, mx);
+      const int e = bound_exponent(mx);
+      const float inv = pow2f(-e);
+      unit = pow2f(e) * 0x1p24f;
+#pragma unroll
+      for (int i = 0; i < EPL / 2; ++i) {
+        const int a = min(127, max(-127, __float2int_rn(mul_ieee(x[2 * i], inv))));
+        const int b = min(127, max(-127, __float2int_rn(mul_ieee(x[2 * i + 1], inv))));
+        sum += a + b;
+        const __half2 c = __floats2half2_rn((float)a, (float)b);
+        const __half2 zero = __half2half2(__ushort_as_half(0));
+        const __half2 up = __hmax2(c, zero), down = __hmin2(c, zero);
+        hp[i] = *reinterpret_cast<const uint32_t*>(&up);
+        hn[i] = *reinterpret_cast<const uint32_t*>(&down);
+      }
+      sum = __reduce_add_sync(kAll, sum);
+    }
 #pragma unroll
     for (int i = 0; i < EPL / 2; ++i) {
-      sts_u32(at + 4 * i, *reinterpret_cast<const uint32_t*>(&hp[i]));
-      sts_u32(at + NT * 8 * QROW + 4 * i, *reinterpret_cast<const uint32_t*>(&hn[i]));
+      sts_u32(at + 4 * i, hp[i]);
+      sts_u32(at + NT * 8 * QROW + 4 * i, hn[i]);
     }
-    // a piece is held by the lanes of half a warp (D 128) or by all of it
-#pragma unroll
-    for (int o = 1; o < 32 / LD; o <<= 1) {
-      up += __shfl_xor_sync(kAll, up, o);
-      down += __shfl_xor_sync(kAll, down, o);
+    if (lane == 0) {
+      s_unit[h] = unit;
+      s_bias[h] = -kBias * (float)sum;
     }
-    if (lane % (32 / LD) == 0) {
-      s_bias[0][lane / (32 / LD)][h] = -kBias * (float)up;
-      s_bias[1][lane / (32 / LD)][h] = -kBias * (float)down;
-    }
-    if (lane == 0) s_unit[h] = pow2f(e);
   }
 
   // ---- scores: tiles warp, warp + WARPS, ... of 16 blocks ----------------------
   // rows lane / 4 and + 8 of a tile
+  const char* codes0 = p.codes + ((long long)p.layer * p.hkv + g) * (2 * D) + qi * 16;
+  const float* scales0 = p.scales + (long long)p.layer * p.hkv + g;
+  const uint32_t heads = (uint32_t)p.L * p.hkv;  // of a block
   uint4 w[2][2][LD];
   float unit[2];
   bool ok[2];
   auto load = [&](int at) {
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
-      const int blk = r ? id1 : id0;
-      ok[r] = blk >= 0 && blk < p.num_blocks;
-      if (at + gl + 8 * r < cnt && !ok[r] && qi == 0) set_error(p.err, kErrIndex);
-      const long long head = ((long long)(ok[r] ? blk : 0) * p.L + p.layer) * p.hkv + g;
-      const char* src = p.codes + head * (2 * D) + qi * 16;
+      ok[r] = (uint32_t)id[r] < p.num_blocks;
+      const uint32_t blk = ok[r] ? id[r] : 0u;
+      const char* src = codes0 + (unsigned long long)blk * (heads * (2 * D));
 #pragma unroll
       for (int side = 0; side < 2; ++side)
 #pragma unroll
         for (int k = 0; k < LD; ++k) w[r][side][k] = ld_stream(src + side * D + k * 64);
-      unit[r] = p.scales[head];
+      unit[r] = scales0[(unsigned long long)blk * heads];
+      if (!ok[r] && at + gl + 8 * r < cnt) set_error(p.err, kErrIndex);
+      id[r] = entry(at + STEP + gl + 8 * r);  // of the next tile
     }
   };
   if (base < cnt) load(base);
-  id0 = entry(base + STEP + gl);
-  id1 = entry(base + STEP + gl + 8);
   __syncthreads();
   uint32_t kmin = 0xffffffffu, kmax = 0;
   const uint32_t a_q = smem_addr(sq[0]) + gl * QROW + qi * 32;
+  float bias[NT][2], f[NT][2];  // of columns 2 qi, 2 qi + 1
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+      bias[nt][c] = s_bias[nt * 8 + 2 * qi + c];
+      f[nt][c] = s_unit[nt * 8 + 2 * qi + c];
+    }
+  const bool second = qi & 1;  // this lane ends up with row gl + 8 instead of gl
 #pragma unroll 1
   for (; base < cnt; base += STEP) {
-    // One sum per side and 64-element piece, started at minus its bias: codes
-    // enter as 1152 + c, so a piece's partial sums stay below
-    // 1279 * 127 * 64 < 2^24 and are exact.
-    float dot[NT][4];
+    // Whole numbers (c + 128) q, in units of 2^-24; a dim counts on one side
+    // only, so all of a score stays below 2^24 of them.
+    float best[2];
+    float acc[NT][2][4];
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-      float acc[2][LD][4];
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        acc[nt][0][c] = bias[nt][c & 1];
+        acc[nt][1][c] = 0.f;
+      }
+#pragma unroll
+    for (int half = 0; half < 2; ++half)
 #pragma unroll
       for (int side = 0; side < 2; ++side)
 #pragma unroll
         for (int k = 0; k < LD; ++k) {
-          const float2 b0 = *reinterpret_cast<const float2*>(&s_bias[side][k][nt * 8 + 2 * qi]);
-          acc[side][k][0] = acc[side][k][2] = b0.x;
-          acc[side][k][1] = acc[side][k][3] = b0.y;
-        }
+          const uint4 &y0 = w[0][side][k], &y1 = w[1][side][k];
+          uint32_t a[2][4];
 #pragma unroll
-      for (int half = 0; half < 2; ++half)
-#pragma unroll
-        for (int side = 0; side < 2; ++side)
-#pragma unroll
-          for (int k = 0; k < LD; ++k) {
-            // dims k * 64 + qi * 16 + half * 8 .. + 7 of head gl
-            const uint4 b = lds128(a_q + (side * NT + nt) * 8 * QROW + k * 128 + half * 16);
-            const uint4 &y0 = w[0][side][k], &y1 = w[1][side][k];
-#pragma unroll
-            for (int c = 0; c < 2; ++c) {
-              const uint32_t u0 = half ? (c ? y0.w : y0.z) : (c ? y0.y : y0.x);
-              const uint32_t u1 = half ? (c ? y1.w : y1.z) : (c ? y1.y : y1.x);
-              uint32_t a0, a1, a2, a3;
-              codes_to_f16(u0, a0, a2);
-              codes_to_f16(u1, a1, a3);
-              mma_f16(acc[side][k], a0, a1, a2, a3, c ? b.z : b.x, c ? b.w : b.y);
-            }
+          for (int c = 0; c < 2; ++c) {
+            codes_to_f16(half ? (c ? y0.w : y0.z) : (c ? y0.y : y0.x), a[c][0], a[c][2]);
+            codes_to_f16(half ? (c ? y1.w : y1.z) : (c ? y1.y : y1.x), a[c][1], a[c][3]);
           }
 #pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        dot[nt][c] = acc[0][0][c] + acc[1][0][c];
-        if constexpr (LD == 2) dot[nt][c] += acc[0][1][c] + acc[1][1][c];
-      }
-    }
-    const float u0 = unit[0], u1 = unit[1];
-    const bool ok0 = ok[0], ok1 = ok[1];
-    if (base + STEP < cnt) {
-      load(base + STEP);
-      id0 = entry(base + 2 * STEP + gl);
-      id1 = entry(base + 2 * STEP + gl + 8);
-    }
+          for (int nt = 0; nt < NT; ++nt) {
+            // dims k * 64 + qi * 16 + half * 8 .. + 7 of head gl
+            const uint4 b = lds128(a_q + (side * NT + nt) * 8 * QROW + k * 128 + half * 16);
+            mma_f16(acc[nt][0], a[0][0], a[0][1], a[0][2], a[0][3], b.x, b.y);
+            mma_f16(acc[nt][1], a[1][0], a[1][1], a[1][2], a[1][3], b.z, b.w);
+          }
+        }
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
-      float best = -INFINITY;
+      best[r] = -INFINITY;
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        const float2 f = *reinterpret_cast<const float2*>(&s_unit[nt * 8 + 2 * qi]);
-        if (nt * 8 + 2 * qi < p.G) best = fmaxf(best, dot[nt][2 * r] * f.x);
-        if (nt * 8 + 2 * qi + 1 < p.G) best = fmaxf(best, dot[nt][2 * r + 1] * f.y);
-      }
-      best = fmaxf(best, __shfl_xor_sync(kAll, best, 1));
-      best = fmaxf(best, __shfl_xor_sync(kAll, best, 2));
-      const int i = base + gl + 8 * r;
-      if (i < cnt) {
-        const uint32_t key = (r ? ok1 : ok0) ? ordered(best * (r ? u1 : u0)) : 0u;
-        if (qi == 0) keys[i] = key;
-        kmin = min(kmin, key);
-        kmax = max(kmax, key);
-      }
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          const float x = (acc[nt][0][2 * r + c] + acc[nt][1][2 * r + c]) * f[nt][c];
+          if (nt * 8 + 2 * qi + c < p.G) best[r] = fmaxf(best[r], x);
+        }
+    }
+    const float u = second ? unit[1] : unit[0];
+    const bool valid = second ? ok[1] : ok[0];
+    if (base + STEP < cnt) load(base + STEP);
+    // lanes qi 0 and 2 keep row gl, 1 and 3 row gl + 8
+    float mine = second ? best[1] : best[0];
+    mine = fmaxf(mine, __shfl_xor_sync(kAll, second ? best[0] : best[1], 1));
+    mine = fmaxf(mine, __shfl_xor_sync(kAll, mine, 2));
+    const int i = base + gl + (second ? 8 : 0);
+    if (i < cnt) {
+      const uint32_t key = valid ? ordered(mine * u) : 0u;
+      if (qi < 2) keys[i] = key;
+      kmin = min(kmin, key);
+      kmax = max(kmax, key);
     }
   }
 
@@ -378,7 +384,7 @@ __global__ void __launch_bounds__(THREADS, (NT == 1 ? 768 : 384) / THREADS)
   kmax = __reduce_max_sync(kAll, kmax);
   if (lane == 0) { sh.warp_a[warp] = kmin; sh.warp_b[warp] = kmax; }
   for (int i = tid; i < 4 * 256; i += THREADS) (&sh.hist[0][0])[i] = 0;
-  if (tid == 0) sh.ncand = 0;
+  if (tid == 0) sh.ncand = sh.counts[0] = sh.counts[1] = 0;
   __syncthreads();
   if (warp == 0) {
     kmin = __reduce_min_sync(kAll, lane < WARPS ? sh.warp_a[lane] : 0xffffffffu);
@@ -444,12 +450,9 @@ __global__ void __launch_bounds__(THREADS, (NT == 1 ? 768 : 384) / THREADS)
   const unsigned long long next = kmin + ((prefix + 1ull) << bits);
   const uint32_t limit = next > 0xffffffffull ? 0xffffffffu : (uint32_t)next;
 
-  // ---- counts above the cut, and at it ------------------------------------------
-  // a thread's entries are consecutive
-  const int seg = (cnt + THREADS - 1) / THREADS;
-  const int i0 = min(cnt, tid * seg), i1 = min(cnt, i0 + seg);
+  // ---- counts above the cut, and at it; the few that are ranked -----------------
   uint32_t over = 0, even = 0;
-  for (int i = i0; i < i1; ++i) {
+  for (int i = tid; i < cnt; i += THREADS) {
     const uint32_t key = keys[i];
     over += key >= limit;
     if (key < limit && (key - kmin) >> bits == prefix) {
@@ -461,25 +464,19 @@ __global__ void __launch_bounds__(THREADS, (NT == 1 ? 768 : 384) / THREADS)
       }
     }
   }
-  uint32_t my_over = over, my_even = even;
-  block_scan(over, even, sh);
-  if (tid == THREADS - 1) { sh.counts[0] = over; sh.counts[1] = even; }
+  over = __reduce_add_sync(kAll, over);
+  even = __reduce_add_sync(kAll, even);
+  if (lane == 0) {
+    atomicAdd(&sh.counts[0], over);
+    atomicAdd(&sh.counts[1], even);
+  }
   sync_all(S);
   // of the CTAs before this one, one per lane
   const uint32_t a_mine = cluster_map(a_counts, lane < rank ? lane : 0);
   const uint32_t over0 = __reduce_add_sync(kAll, lane < rank ? ld_cluster_u32(a_mine) : 0u);
   const uint32_t even0 = __reduce_add_sync(kAll, lane < rank ? ld_cluster_u32(a_mine + 4) : 0u);
-  if (!ranked) {
-    over += over0 - my_over;
-    even += even0 - my_even;
-    for (int i = i0; i < i1; ++i) {
-      const uint32_t key = keys[i];
-      const bool ov = key >= limit, eq = !ov && (key - kmin) >> bits == prefix;
-      if (ov || (eq && even < left)) out[p.sink + over + min(even, left)] = p.sink + lo + i;
-      over += ov;
-      even += eq;
-    }
-  } else {
+  uint32_t before = over0;
+  if (ranked) {
     // gather the bin's scores of all CTAs, rank them, and mark the taken ones
     // among this CTA's with a key above the limit, the others with one below
     const uint32_t a_key = smem_addr(sh.cand_key), a_at = smem_addr(sh.cand_at);
@@ -503,26 +500,44 @@ __global__ void __launch_bounds__(THREADS, (NT == 1 ? 768 : 384) / THREADS)
       }
     }
     __syncthreads();
-    for (uint32_t i = tid; i < at; i += THREADS) {
+    for (uint32_t i = warp; i < at; i += WARPS) {
       const uint32_t key = sh.all_key[i], e = sh.all_at[i];
       uint32_t better = 0;
-      for (uint32_t j = 0; j < at; ++j) {
+      for (uint32_t j = lane; j < at; j += 32) {
         const uint32_t k2 = sh.all_key[j];
         better += k2 > key || (k2 == key && sh.all_at[j] < e);
       }
-      const bool taken = better < left;
-      if ((int)e >= lo && (int)e < lo + cnt) keys[e - lo] = taken ? 0xffffffffu : 0u;
-      if (taken && (int)e < lo) atomicAdd(&sh.before, 1u);
+      const bool taken = __reduce_add_sync(kAll, better) < left;
+      if (lane == 0) {
+        if ((int)e >= lo && (int)e < lo + cnt) keys[e - lo] = taken ? 0xffffffffu : 0u;
+        if (taken && (int)e < lo) atomicAdd(&sh.before, 1u);
+      }
     }
     __syncthreads();
-    over = 0;
-    for (int i = i0; i < i1; ++i) over += keys[i] >= limit;
-    my_over = over;
-    uint32_t dummy = 0;
-    block_scan(over, dummy, sh);
-    over += over0 + sh.before - my_over;
-    for (int i = i0; i < i1; ++i)
-      if (keys[i] >= limit) out[p.sink + over++] = p.sink + lo + i;
+    before += sh.before;
+    left = 0;  // none is taken for its place any more
+  }
+
+  // ---- write the taken entries in order: a thread's are consecutive --------------
+  const int seg = (cnt + THREADS - 1) / THREADS;
+  const int i0 = min(cnt, tid * seg), i1 = min(cnt, i0 + seg);
+  over = even = 0;
+  for (int i = i0; i < i1; ++i) {
+    const uint32_t key = keys[i];
+    over += key >= limit;
+    even += left > 0 && key < limit && (key - kmin) >> bits == prefix;
+  }
+  const uint32_t my_over = over, my_even = even;
+  block_scan(over, even, sh);
+  over += before - my_over;
+  even += even0 - my_even;
+  for (int i = i0; i < i1; ++i) {
+    const uint32_t key = keys[i];
+    const bool ov = key >= limit;
+    const bool eq = left > 0 && !ov && (key - kmin) >> bits == prefix;
+    if (ov || (eq && even < left)) out[p.sink + over + min(even, left)] = p.sink + lo + i;
+    over += ov;
+    even += eq;
   }
   if (S > 1) cluster_sync();  // no CTA leaves while another may still read its words
 }
@@ -584,6 +599,8 @@ extern "C" pkv_status pkv_select_blocks(const pkv_pool* pool, int32_t layer,
   // table positions are 32-bit in the kernel, and a cluster holds every score of a row
   if ((int64_t)mb * v.block_size > INT32_MAX || mb > pkv::kSelMaxCluster * pkv::kSelMaxCap)
     return PKV_ERR_UNSUPPORTED;
+  if ((int64_t)v.num_layers * v.num_kv_heads * 2 * v.head_dim > INT32_MAX)
+    return PKV_ERR_UNSUPPORTED;
   const int64_t rows = (int64_t)num_tokens * v.num_kv_heads;
   if (rows > INT32_MAX / pkv::kSelMaxCluster) return PKV_ERR_UNSUPPORTED;
   int optin, grid, validate, sms;
@@ -620,7 +637,7 @@ extern "C" pkv_status pkv_select_blocks(const pkv_pool* pool, int32_t layer,
   p.sel = selected;
   p.count = selected_count;
   p.err = err;
-  p.num_blocks = v.num_blocks;
+  p.num_blocks = (uint32_t)(v.num_blocks < INT32_MAX ? v.num_blocks : INT32_MAX);
   p.batch = batch;
   p.mb = mb;
   p.bs = v.block_size;
