@@ -227,7 +227,8 @@ PKV_API pkv_status pkv_rope_init_freqs(pkv_rope* rope, int32_t rotary_dim, int32
  * head_dim], q_out as q: consecutive heads within a token, tokens *_stride
  * elements apart (a multiple of 16 bytes, at least a token's heads), so
  * slices of one projection's output can be passed as they are.  q_out may be
- * q itself (same stride); other overlaps are not allowed.  num_q_heads 0
+ * q itself (same stride); other overlaps are not allowed, and no two tokens
+ * may name the same slot.  num_q_heads 0
  * (q and q_out NULL) turns and stores the keys alone.  slot_mapping (int64
  * [num_tokens], device) receives the slots when not NULL.
  * Supported: head_dim 32, 64, 128 or 256; rotary_dim a multiple of 8 (of 4 for
@@ -457,9 +458,9 @@ PKV_API pkv_status pkv_select_blocks(const pkv_pool* pool, int32_t layer, const 
  * zeros and sets the error word; the out rows of padding are not written.
  * Rows that the query does not see are not read.  q, out: [num_tokens,
  * num_q_heads, head_dim], contiguous, types and pool dtypes as in
- * pkv_decode_attention (fp32 accumulation; the softmax weights are rounded to
- * bf16, or to fp16 with the V scales for PKV_I8 pools, for their product with
- * V).  Supported: head_dim 64 or 128; any num_kv_heads; up to 16 query heads
+ * pkv_decode_attention (fp32 accumulation; for their product with V the
+ * softmax weights are rounded to 16 bits, in two bf16 parts, and for PKV_I8
+ * pools, with the V scales, to fp16).  Supported: head_dim 64 or 128; any num_kv_heads; up to 16 query heads
  * per kv head; any block_size the pool allows.  One launch, no workspace; may
  * be captured in a CUDA graph. */
 PKV_API pkv_status pkv_decode_attention_sparse(const pkv_pool* pool, int32_t layer, const void* q,

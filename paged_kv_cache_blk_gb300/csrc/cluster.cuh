@@ -18,6 +18,7 @@ __device__ __forceinline__ uint32_t cluster_rank() {
 // shared memory before it are visible to the cluster after it.  It cannot be
 // bounded; callers reach it on every path.
 __device__ __forceinline__ void cluster_sync() {
+  __syncwarp();
   asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
   asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
@@ -44,14 +45,10 @@ __device__ __forceinline__ float ld_cluster_f32(uint32_t addr) {
 template <typename... KArgs, typename... Args>
 cudaError_t launch_clusters(void (*kern)(KArgs...), dim3 grid, dim3 block, size_t smem,
                             unsigned cluster, cudaStream_t s, Args... args) {
-  if (smem > 48 * 1024) {
+  // (48 KB without asking, the kernel's static shared memory included)
+  if (smem > 16 * 1024) {
     const cudaError_t e =
         cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-    if (e != cudaSuccess) return e;
-  }
-  if (cluster > 8) {
-    const cudaError_t e =
-        cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
     if (e != cudaSuccess) return e;
   }
   cudaLaunchConfig_t cfg = {};
