@@ -198,6 +198,7 @@ class Pool:
         # type of q, out and new rows
         self.row_dtype = torch.bfloat16 if k_cache.dtype == torch.uint8 else k_cache.dtype
         self.ref = ctypes.byref(self.struct)
+        self.index = k_cache.get_device()
 
 
 class _NoSwitch:
@@ -307,7 +308,7 @@ def _index(t: Optional[torch.Tensor], pool: Pool, name: str, ndim: int) -> Optio
     """Pointer of a contiguous int32 index tensor on the pool's device."""
     if t is None:
         return None
-    if t.dtype is not _INT32 or t.device != pool.device or t.dim() != ndim \
+    if t.dtype is not _INT32 or t.get_device() != pool.index or t.dim() != ndim \
             or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous int32 tensor of {ndim} dimension(s) on "
                          f"{pool.device}")
@@ -319,7 +320,7 @@ def _rows_of(t: torch.Tensor, pool: Pool, name: str, shape: Tuple[int, int, int]
     pool's row type, the heads of a token consecutive."""
     if t.shape != shape:
         raise ValueError(f"{name} must be {list(shape)}, not {list(t.shape)}")
-    if t.dtype is not pool.row_dtype or t.device != pool.device:
+    if t.dtype is not pool.row_dtype or t.get_device() != pool.index:
         raise ValueError(f"{name} must be {pool.row_dtype} on {pool.device}")
     tokens, heads, d = shape
     st, sh, sd = t.stride()

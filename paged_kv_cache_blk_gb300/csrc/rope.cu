@@ -151,7 +151,7 @@ __global__ void __launch_bounds__(kRopeWarps * 32, 5)
   constexpr int W = EPL * sizeof(T) / 4;  // words of a lane
   constexpr int RPW = 32 / LPH;
   constexpr int NF = EPL / 2;  // pairs of a lane
-  constexpr int ROW = EPL * LPH * (int)sizeof(T);
+  constexpr int ES = sizeof(T), ROW = EPL * LPH * ES;
   const int lane = threadIdx.x & 31;
   const int sub = lane / LPH, col = lane % LPH;
   const bool turns = col * EPL < p.rd;
@@ -175,16 +175,25 @@ __global__ void __launch_bounds__(kRopeWarps * 32, 5)
     const int chunk = (int)(w - t * p.chunks);
     const int r0 = chunk * p.rows_task;
     const int r1 = min(rows, r0 + p.rows_task);
-    const int64_t slot = [&] {
-      int64_t s = 0;
-      if (lane == 0) {
-        s = token_slot(p.ss, t, p.num_blocks, p.bs, p.err, chunk == 0);
-        if (chunk == 0 && p.ss.slots_out) p.ss.slots_out[t] = s;
-      }
-      return __shfl_sync(kAll, s, 0);
-    }();
+    // the first rows are on their way while the chain sequence - offset - table
+    // entry runs
+    const int seq = ld_volatile(p.ss.tok_seq + t);
+    const int pos = ld_volatile((p.rope_pos ? p.rope_pos : p.ss.tok_pos) + t);
+    const int k0 = p.hq, v0 = p.hq + p.hkv;
+    const char* src = r0 < k0   ? p.q + t * p.q_stride
+                      : r0 < v0 ? p.k_new + t * p.k_stride - (long long)k0 * ROW
+                                : p.v_new + t * p.v_stride - (long long)v0 * ROW;
+    uint32_t raw[kRopeUnroll][W];
+    auto fetch = [&](const char* from, int r, int end) {
+#pragma unroll
+      for (int u = 0; u < kRopeUnroll; ++u)
+        if (r + u * RPW < end)
+          load_runs<T, EPL, INTER>(from + (long long)(r + u * RPW) * ROW, e0 * ES, e1 * ES, raw[u]);
+    };
+    if (seq >= 0) fetch(src, r0 + sub, min(r1, r0 < k0 ? k0 : r0 < v0 ? v0 : rows));
+    const int64_t slot = token_slot(p.ss, t, p.num_blocks, p.bs, p.err, chunk == 0 && lane == 0);
+    if (chunk == 0 && lane == 0 && p.ss.slots_out) p.ss.slots_out[t] = slot;
     if (slot < 0) continue;  // padding or out of range: nothing of this token is written
-    const int pos = p.rope_pos ? p.rope_pos[t] : p.ss.tok_pos[t];
     float c[NF], s[NF];
     if (npl == 1)
       hand_out<NF, 1>(step, pos, p.attn_scale, f0, s, c);
@@ -196,18 +205,15 @@ __global__ void __launch_bounds__(kRopeWarps * 32, 5)
         row_offset(slot >> (31 - __clz(p.bs)), p.layer, (int)(slot & (p.bs - 1)), p.L, p.bs,
                    p.row_bytes);
 
-    // heads [a, b) of one kind: loads of kRopeUnroll steps, then stores
-    auto run = [&](auto kind_tag, const char* src, int a, int b) {
+    // heads [a, b) of one kind: loads of kRopeUnroll steps (the task's first are
+    // there), then stores
+    bool there = true;
+    auto run = [&](auto kind_tag, const char* from, int a, int b) {
       constexpr int KIND = decltype(kind_tag)::value;
-      constexpr int ES = sizeof(T);
 #pragma unroll 1
       for (int rb = a + sub; rb - sub < b; rb += RPW * kRopeUnroll) {
-        uint32_t raw[kRopeUnroll][W] = {};
-#pragma unroll
-        for (int u = 0; u < kRopeUnroll; ++u)
-          if (rb + u * RPW < b)
-            load_runs<T, EPL, INTER>(src + (long long)(rb + u * RPW) * ROW, e0 * ES, e1 * ES,
-                                     raw[u]);
+        if (!there) fetch(from, rb, b);
+        there = false;
 #pragma unroll
         for (int u = 0; u < kRopeUnroll; ++u) {
           const int r = rb + u * RPW;
@@ -257,7 +263,6 @@ __global__ void __launch_bounds__(kRopeWarps * 32, 5)
         }
       }
     };
-    const int k0 = p.hq, v0 = p.hq + p.hkv;
     if (r0 < k0)
       run(std::integral_constant<int, kRowQ>(), p.q + t * p.q_stride, r0, min(r1, k0));
     if (r1 > k0 && r0 < v0)
