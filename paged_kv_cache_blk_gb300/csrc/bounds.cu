@@ -1,11 +1,12 @@
 // Key bounds of the blocks that hold new tokens (pkv_update_block_bounds; see
 // bounds.cuh for what they are).
 //
-// The rows of a block are read in place: D / EPL lanes own one (block, kv
-// head), EPL elements (16 bytes) each, and step down the rows, consecutive
-// heads in consecutive lanes, so a warp reads whole 512-byte runs of token
-// rows.  The running extremes stay in the type of the pool (packed bf16
-// maxima; fp32 products code * scale for int8 pools).  Every row from 0 to
+// The rows of a block are read in place.  A warp owns one (block, kv head):
+// D / EPL lanes hold a row, EPL elements (16 bytes) each, and the 32 EPL / D
+// groups of them take every so-manieth row, so that a single block, as after a
+// decode step, is not one long chain of loads.  The running extremes stay in
+// the type of the pool (packed bf16 maxima; fp32 products code * scale for int8
+// pools), and are merged over the groups by shuffles.  Every row from 0 to
 // the last one the sequence holds counts, the rows before a first-block
 // offset too: they belong to a prefix shared with other sequences, and all
 // holders of a full block then store the same bytes.
@@ -52,6 +53,14 @@ struct Extremes<PKV_BF16, EPL> {  // EPL = 8, packed pairs
       asm("min.NaN.bf16x2 %0, %0, %1;" : "+r"(lo[i]) : "r"(w[i]));
     }
   }
+  __device__ void merge(int o) {  // with the lane `o` away
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t a = __shfl_xor_sync(kAll, hi[i], o), b = __shfl_xor_sync(kAll, lo[i], o);
+      asm("max.NaN.bf16x2 %0, %0, %1;" : "+r"(hi[i]) : "r"(a));
+      asm("min.NaN.bf16x2 %0, %0, %1;" : "+r"(lo[i]) : "r"(b));
+    }
+  }
   __device__ float top(int i) const { return i & 1 ? bf16_hi(hi[i / 2]) : bf16_lo(hi[i / 2]); }
   __device__ float bottom(int i) const { return i & 1 ? bf16_hi(lo[i / 2]) : bf16_lo(lo[i / 2]); }
 };
@@ -74,6 +83,13 @@ struct Extremes<PKV_F32, EPL> {  // EPL = 4
       lo[i] = min_nan(lo[i], __uint_as_float(w[i]));
     }
   }
+  __device__ void merge(int o) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      hi[i] = max_nan(hi[i], __shfl_xor_sync(kAll, hi[i], o));
+      lo[i] = min_nan(lo[i], __shfl_xor_sync(kAll, lo[i], o));
+    }
+  }
   __device__ float top(int i) const { return hi[i]; }
   __device__ float bottom(int i) const { return lo[i]; }
 };
@@ -92,10 +108,19 @@ struct Extremes<PKV_I8, EPL> {  // EPL = 16 codes
     const uint32_t w[4] = {r.x, r.y, r.z, r.w};
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
-      const int c = (int)((w[i / 4] >> (8 * (i % 4))) & 0xFFu) - 128;
-      const float x = mul_ieee((float)c, scale);
+      // the byte as the low mantissa bits of 2^23, less 2^23 + 128
+      const float c = __uint_as_float(__byte_perm(w[i / 4], 0x4B000000u, 0x7540 | (i % 4))) -
+                      8388736.f;
+      const float x = mul_ieee(c, scale);
       hi[i] = max_nan(hi[i], x);
       lo[i] = min_nan(lo[i], x);
+    }
+  }
+  __device__ void merge(int o) {
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      hi[i] = max_nan(hi[i], __shfl_xor_sync(kAll, hi[i], o));
+      lo[i] = min_nan(lo[i], __shfl_xor_sync(kAll, lo[i], o));
     }
   }
   __device__ float top(int i) const { return hi[i]; }
@@ -116,8 +141,9 @@ template <int MODE, int D>
 __global__ void __launch_bounds__(kBoundThreads) update_bounds_kernel(const BoundParams p) {
   constexpr int EPL = MODE == PKV_BF16 ? 8 : MODE == PKV_F32 ? 4 : 16;
   constexpr int LPH = D / EPL;
-  constexpr int GROUPS = kBoundThreads / LPH;  // (block, head) pairs of a CTA
-  constexpr int UNROLL = 8;
+  constexpr int RPW = 32 / LPH;                // rows a warp reads at once
+  constexpr int WARPS = kBoundThreads / 32;    // (block, head) pairs of a CTA
+  constexpr int UNROLL = MODE == PKV_I8 ? 4 : 8;
   griddep_wait();
   griddep_launch_dependents();
   const int b = blockIdx.x / p.ctas_seq, x = blockIdx.x % p.ctas_seq;
@@ -131,46 +157,44 @@ __global__ void __launch_bounds__(kBoundThreads) update_bounds_kernel(const Boun
   const int end = off + len;  // table positions held: below 2^31 (mb * bs is checked)
   const int j0 = (off + first) / p.bs;
   const int nj = (end - 1) / p.bs + 1 - j0;
-  const int items = nj * p.hkv;  // (mb * hkv is checked)
-  const int col = threadIdx.x % LPH;
-  const int step = p.ctas_seq * GROUPS;
+  const int lane = threadIdx.x & 31;
+  const int col = lane % LPH, sub = lane / LPH;
+  const int step = p.ctas_seq * WARPS;
+  const int step_j = step / p.hkv, step_g = step - step_j * p.hkv;
   const int32_t* table = p.bt + (long long)b * p.mb + j0;
-  int it = x * GROUPS + (int)threadIdx.x / LPH;
-  int blk = it < items ? table[it / p.hkv] : -1;
-  // groups of a warp run the same number of steps, so the shuffles stay whole
-  for (int i0 = x * GROUPS; i0 < items; i0 += step) {
-    const bool live = it < items;
-    const int j = j0 + (live ? it / p.hkv : 0);
-    const int g = live ? it % p.hkv : 0;
-    const int mine = blk;
-    it = it < items - step ? it + step : items;
-    blk = it < items ? table[it / p.hkv] : -1;  // the next step's, ahead of its rows
-    const bool ok = live && mine >= 0 && mine < p.num_blocks;
-    if (live && !ok && col == 0) set_error(p.err, kErrIndex);
-    const int rows = ok ? min(p.bs, end - j * p.bs) : 0;
-    const char* src = p.k + row_offset(ok ? mine : 0, p.layer, 0, p.L, p.bs, p.row_bytes);
-    const char* elems = src + (long long)(g * LPH + col) * 16;
-    const char* unit = src + p.scale_off + 4 * g;
+  const int first_it = x * WARPS + (int)threadIdx.x / 32;
+  int j = first_it / p.hkv, g = first_it - j * p.hkv;  // blocks from j0 on
+  int blk = j < nj ? table[j] : -1;
+  while (j < nj) {
+    const int mine = blk, head = g, rows = min(p.bs, end - (j0 + j) * p.bs);
+    j += step_j;
+    g += step_g;
+    if (g >= p.hkv) { g -= p.hkv; ++j; }
+    blk = j < nj ? table[j] : -1;  // the next one's, ahead of its rows
+    if (mine < 0 || mine >= p.num_blocks) {
+      if (lane == 0) set_error(p.err, kErrIndex);
+      continue;
+    }
+    const char* src = p.k + row_offset(mine, p.layer, 0, p.L, p.bs, p.row_bytes);
+    const char* elems = src + (long long)(head * LPH + col) * 16;
+    const char* unit = src + p.scale_off + 4 * head;
     Extremes<MODE, EPL> ex;
     ex.init();
-    int r = 0;
-    for (; r + UNROLL <= rows; r += UNROLL) {
+    for (int r = sub; r < rows; r += RPW * UNROLL) {
       uint4 v[UNROLL];
       float s[UNROLL];
 #pragma unroll
       for (int u = 0; u < UNROLL; ++u) {
-        v[u] = ld_stream(elems + (long long)(r + u) * p.row_bytes);
-        s[u] = MODE == PKV_I8
-                   ? *reinterpret_cast<const float*>(unit + (long long)(r + u) * p.row_bytes)
-                   : 0.f;
+        // past the end, the last row again; a block is less than 4 GB
+        const uint32_t at = (uint32_t)min(r + u * RPW, rows - 1) * (uint32_t)p.row_bytes;
+        v[u] = ld_stream(elems + at);
+        s[u] = MODE == PKV_I8 ? *reinterpret_cast<const float*>(unit + at) : 0.f;
       }
 #pragma unroll
       for (int u = 0; u < UNROLL; ++u) ex.add(v[u], s[u]);
     }
-    for (; r < rows; ++r)
-      ex.add(ld_stream(elems + (long long)r * p.row_bytes),
-             MODE == PKV_I8 ? *reinterpret_cast<const float*>(unit + (long long)r * p.row_bytes)
-                            : 0.f);
+#pragma unroll
+    for (int o = LPH; o < 32; o <<= 1) ex.merge(o);
     uint32_t m = 0;
 #pragma unroll
     for (int i = 0; i < EPL; ++i)
@@ -178,20 +202,26 @@ __global__ void __launch_bounds__(kBoundThreads) update_bounds_kernel(const Boun
                      __float_as_uint(ex.bottom(i)) & 0x7FFFFFFFu));
 #pragma unroll
     for (int o = LPH / 2; o; o >>= 1) m = max(m, __shfl_xor_sync(kAll, m, o));
-    if (!ok) continue;
     const int e = bound_exponent(m);
     const float inv = pow2f(-e);
-    uint32_t hw[EPL / 4] = {}, lw[EPL / 4] = {};
+    const long long at = ((long long)mine * p.L + p.layer) * p.hkv + head;
+    char* dst = p.codes + at * (2 * D) + col * EPL;
+    // every group of lanes holds the result: one writes hi, another lo
+    if (sub == 0) {
+      uint32_t w[EPL / 4] = {};
 #pragma unroll
-    for (int i = 0; i < EPL; ++i) {
-      hw[i / 4] |= (uint32_t)(code_up(ex.top(i), inv) + 128) << (8 * (i % 4));
-      lw[i / 4] |= (uint32_t)(code_down(ex.bottom(i), inv) + 128) << (8 * (i % 4));
+      for (int i = 0; i < EPL; ++i)
+        w[i / 4] |= (uint32_t)(code_up(ex.top(i), inv) + 128) << (8 * (i % 4));
+      store_bytes(dst, w);
+      if (col == 0) p.scales[at] = pow2f(e);
     }
-    const long long head = ((long long)mine * p.L + p.layer) * p.hkv + g;
-    char* dst = p.codes + head * (2 * D) + col * EPL;
-    store_bytes(dst, hw);
-    store_bytes(dst + D, lw);
-    if (col == 0) p.scales[head] = pow2f(e);
+    if (sub == (RPW > 1 ? 1 : 0)) {
+      uint32_t w[EPL / 4] = {};
+#pragma unroll
+      for (int i = 0; i < EPL; ++i)
+        w[i / 4] |= (uint32_t)(code_down(ex.bottom(i), inv) + 128) << (8 * (i % 4));
+      store_bytes(dst + D, w);
+    }
   }
 }
 
@@ -199,9 +229,8 @@ template <int MODE>
 cudaError_t launch_bounds_mode(BoundParams& p, int d, int batch, int sms, cudaStream_t s) {
   // Enough CTAs to fill the SMs over the batch (48 warps each), none that the
   // longest possible table would leave idle.
-  const int lph = d / (MODE == PKV_BF16 ? 8 : MODE == PKV_F32 ? 4 : 16);
-  const long long groups = kBoundThreads / lph;
-  long long ctas = ((long long)p.mb * p.hkv + groups - 1) / groups;
+  const long long warps = kBoundThreads / 32;
+  long long ctas = ((long long)p.mb * p.hkv + warps - 1) / warps;
   const long long want = (12ll * sms + batch - 1) / batch;
   if (ctas > want) ctas = want;
   p.ctas_seq = (int)ctas;
@@ -234,9 +263,9 @@ extern "C" pkv_status pkv_update_block_bounds(const pkv_pool* pool, int32_t laye
       !pkv::aligned(first_pos, 4) || !pkv::aligned(bound_codes, 16) ||
       !pkv::aligned(bound_scales, 4))
     return PKV_ERR_INVALID_ARG;
-  // table positions and (block, head) pairs are 32-bit in the kernel
+  // table positions and offsets within a block are 32-bit in the kernel
   if ((int64_t)max_blocks_per_seq * v.block_size > INT32_MAX || batch > (1 << 24) ||
-      (int64_t)max_blocks_per_seq * v.num_kv_heads > INT32_MAX / 2)
+      (int64_t)v.block_size * v.row_bytes > INT32_MAX)
     return PKV_ERR_UNSUPPORTED;
   int optin, grid, validate, sms;
   int* err;

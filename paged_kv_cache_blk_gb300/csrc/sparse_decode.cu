@@ -589,6 +589,7 @@ struct Layout {
   static constexpr int kExtra = MODE == PKV_F32 ? FmaState<D, HEADS>::kExtra : 0;
   static constexpr int kWarp = (kBody + kExtra + 127) / 128 * 128;
   static constexpr int kBytes = kSpWarps * kWarp;
+  static constexpr int kStatic = HEADS * 32 * 4;  // the merge's weights
 };
 
 template <int MODE, int D, int HEADS>
@@ -736,7 +737,7 @@ __global__ void __launch_bounds__(kSpThreads) sparse_decode_kernel(const SparseP
   for (int i = (int)rank * kSpThreads + tid; i < pairs; i += (int)S * kSpThreads) {
     const int h = i / (D / 2), d = (i % (D / 2)) * 2;
     float x = 0.f, y = 0.f;
-#pragma unroll 4
+#pragma unroll 8
     for (int j = 0; j < states; ++j) {
       const uint32_t a = cluster_map(base + (j % kSpWarps) * Lay::kWarp + (h * D + d) * 4,
                                      j / kSpWarps);
@@ -755,24 +756,38 @@ __global__ void __launch_bounds__(kSpThreads) sparse_decode_kernel(const SparseP
   if (S > 1) cluster_sync();  // no CTA leaves while another may still read its states
 }
 
+constexpr int kSpMaxCluster = 8;
+
 template <int MODE, int D, int HEADS>
-cudaError_t launch_sparse_heads(const SparseParams& p, unsigned rows, unsigned S, cudaStream_t s) {
-  return launch_clusters(sparse_decode_kernel<MODE, D, HEADS>, dim3(rows * S), dim3(kSpThreads),
-                         Layout<MODE, D, HEADS>::kBytes, S, s, p);
+cudaError_t launch_sparse_heads(const SparseParams& p, unsigned rows, int sms, cudaStream_t s) {
+  using Lay = Layout<MODE, D, HEADS>;
+  // CTAs of a cluster: as many as the SMs hold at once (by their 228 KB of shared
+  // memory, 1 KB of it the system's for each CTA), each warp with two tiles or
+  // more.  One round of CTAs, not a little more: 45 rows of fp32 blocks, D 128,
+  // take 9.7 us in clusters of 6 and 29 in clusters of 8, which do not all fit.
+  // And where one CTA a row fills the SMs already, more cost more than they
+  // balance, since every CTA waits for a chain of index loads first: 512 rows
+  // of 2048 bf16 tokens take 82 us at S = 1, 91 at 2, 102 at 4.
+  const unsigned fit = 228 * 1024 / (Lay::kBytes + Lay::kStatic + 1024);
+  const long long tiles = (long long)p.K * p.parts;
+  long long S = (long long)fit * sms / rows;
+  if (S > kSpMaxCluster) S = kSpMaxCluster;
+  if (S > tiles / (2 * kSpWarps)) S = tiles / (2 * kSpWarps);
+  if (S < 1) S = 1;
+  return launch_clusters(sparse_decode_kernel<MODE, D, HEADS>, dim3(rows * (unsigned)S),
+                         dim3(kSpThreads), Lay::kBytes, (unsigned)S, s, p);
 }
 
 template <int MODE, int D>
-cudaError_t launch_sparse_d(const SparseParams& p, unsigned rows, unsigned S, cudaStream_t s) {
+cudaError_t launch_sparse_d(const SparseParams& p, unsigned rows, int sms, cudaStream_t s) {
   if constexpr (MODE == PKV_F32) {
-    if (p.G <= 4) return launch_sparse_heads<MODE, D, 4>(p, rows, S, s);
+    if (p.G <= 4) return launch_sparse_heads<MODE, D, 4>(p, rows, sms, s);
   }
-  if (p.G <= 8) return launch_sparse_heads<MODE, D, 8>(p, rows, S, s);
-  return launch_sparse_heads<MODE, D, 16>(p, rows, S, s);
+  if (p.G <= 8) return launch_sparse_heads<MODE, D, 8>(p, rows, sms, s);
+  return launch_sparse_heads<MODE, D, 16>(p, rows, sms, s);
 }
 
 bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
-
-constexpr int kSpMaxCluster = 8;
 
 }  // namespace
 }  // namespace pkv
@@ -818,13 +833,6 @@ extern "C" pkv_status pkv_decode_attention_sparse(
       return (pkv_status)st;
     if ((st = pkv::read_and_clear_error_word(err, stream)) != PKV_OK) return (pkv_status)st;
   }
-  // CTAs of a cluster: until two per SM are there, each warp with a few tiles.
-  // (More of them cost more than they balance, since every CTA waits for a chain
-  // of index loads first: the 64-sequence case above takes 82 us at S = 1, 91 at 2,
-  // 102 at 4.)
-  unsigned S = 1;
-  while ((int)S < pkv::kSpMaxCluster && rows * S < 2 * sms && tiles > S * pkv::kSpWarps * 2)
-    S *= 2;
   pkv::SparseParams p;
   p.k = v.k;
   p.v = v.v;
@@ -854,14 +862,14 @@ extern "C" pkv_status pkv_decode_attention_sparse(
   const bool d64 = v.head_dim == 64;
   cudaError_t e;
   if (v.quant)
-    e = d64 ? pkv::launch_sparse_d<PKV_I8, 64>(p, r, S, stream)
-            : pkv::launch_sparse_d<PKV_I8, 128>(p, r, S, stream);
+    e = d64 ? pkv::launch_sparse_d<PKV_I8, 64>(p, r, sms, stream)
+            : pkv::launch_sparse_d<PKV_I8, 128>(p, r, sms, stream);
   else if (v.io_size == 2)
-    e = d64 ? pkv::launch_sparse_d<PKV_BF16, 64>(p, r, S, stream)
-            : pkv::launch_sparse_d<PKV_BF16, 128>(p, r, S, stream);
+    e = d64 ? pkv::launch_sparse_d<PKV_BF16, 64>(p, r, sms, stream)
+            : pkv::launch_sparse_d<PKV_BF16, 128>(p, r, sms, stream);
   else
-    e = d64 ? pkv::launch_sparse_d<PKV_F32, 64>(p, r, S, stream)
-            : pkv::launch_sparse_d<PKV_F32, 128>(p, r, S, stream);
+    e = d64 ? pkv::launch_sparse_d<PKV_F32, 64>(p, r, sms, stream)
+            : pkv::launch_sparse_d<PKV_F32, 128>(p, r, sms, stream);
   if ((st = pkv::launch_status(e)) != PKV_OK) return (pkv_status)st;
   return validate ? (pkv_status)pkv::read_and_clear_error_word(err, stream) : PKV_OK;
 }
