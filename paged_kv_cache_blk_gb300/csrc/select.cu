@@ -15,21 +15,23 @@
 // result is ever written.  The scores are found on the tensor cores: 16
 // blocks by 8 query heads by 16 code bytes per mma, the code bytes c + 128 taken
 // as fp16 subnormals (sums of whole numbers up to 255 * 127 * 128 < 2^24, in
-// units of 2^-24: exact).  A lane
-// loads 16-byte pieces of its blocks straight to registers, and the same
-// pieces of the query, coded once per CTA, from shared memory, so the order of
-// k does not matter.
+// units of 2^-24: exact).  A lane loads 16-byte pieces of its blocks straight
+// to registers, and the same pieces of the query, coded once per CTA, from
+// shared memory, so the order of k does not matter.
 //
 // The cut: the scores as ordered integers, counted in 256 bins from the
 // cluster-wide range down.  Every CTA counts its own and sums the counts of
 // all through distributed shared memory.  Once the bin that holds the cut has
-// at most 256 scores (as a rule after the first count), every CTA gathers
-// those and ranks them by (score, entry); a bin that stays larger is counted
-// again 8 bits finer, down to equal scores, of which the lowest entries are
-// taken.
+// at most 128 scores (as a rule after the first count), every CTA sends its
+// share of those to the others, and each ranks them by (score, entry); a bin
+// that stays larger is counted again 8 bits finer, down to equal scores, of
+// which the lowest entries are taken.
 //
-// What bounds it: with few rows, latency (three cluster barriers, two rounds
-// of loads); with many, the bytes of the bounds.
+// What bounds it: with few rows, latency (a chain of four loads, three cluster
+// barriers, eight block barriers); with many, the instructions of a tile, about
+// 200 for 4 KB, and of the cut: 14.9 us for 128 of 8192 blocks of one query (Hkv 8,
+// D 128, G 4), 16.8 us for 64 of 64 to 513 blocks of 64 queries, 42 MB of bounds.
+// (Scores to a workspace, and the cut in a second launch, took 18 and 23 us.)
 #include <cmath>
 
 #include <cuda_fp16.h>
@@ -41,7 +43,8 @@
 namespace pkv {
 namespace {
 
-constexpr int kCand = 256;  // scores that are ranked rather than counted
+constexpr int kSelMaxCluster = 8;
+constexpr int kCand = 128;  // scores that are ranked rather than counted
 constexpr unsigned kAll = 0xffffffffu;
 
 struct SelectParams {
@@ -61,17 +64,20 @@ struct SelectParams {
   int cap;  // scores a CTA can hold
 };
 
-// Static shared memory; the CTAs of a cluster read each other's.
+// Static shared memory.  What the CTAs of a cluster tell each other they write
+// into the others' copies (or add to them) ahead of a cluster barrier, so that
+// only the counts of the bins are read across it.
 struct SelectShared {
   uint32_t hist[4][256];
-  uint32_t range[2];   // smallest and largest score of this CTA
-  uint32_t counts[2];  // scores of this CTA above the cut, and at it
-  uint32_t cand_key[kCand], cand_at[kCand];  // this CTA's scores in the cut's bin, and their entries
-  uint32_t ncand;
-  // not read by others
+  uint32_t range[2];                       // smallest and largest score of the cluster
+  uint32_t over0, even0;                   // scores above the cut, and at it, of the CTAs before
+  uint32_t cand_n[kSelMaxCluster];         // scores in the cut's bin of each CTA,
+  uint32_t cand_key[kSelMaxCluster][kCand];  // themselves,
+  uint32_t cand_at[kSelMaxCluster][kCand];   // and their entries
+  // not written by others
   uint32_t all_key[kCand], all_at[kCand];
+  uint32_t counts[2], ncand, before;
   uint32_t pick[3];
-  uint32_t before;
   uint32_t warp_a[32], warp_b[32];
 };
 
@@ -226,6 +232,13 @@ __global__ void __launch_bounds__(THREADS, (NT == 1 ? 768 : 384) / THREADS)
   const int m = n - p.sink - p.recent;  // scored entries, more than need
   const int per = (m + (int)S - 1) / (int)S;
   const int lo = min(m, (int)rank * per), cnt = min(m, lo + per) - lo;
+
+  for (int i = tid; i < 4 * 256; i += THREADS) (&sh.hist[0][0])[i] = 0;
+  if (tid == 0) {
+    sh.range[0] = 0xffffffffu;
+    sh.range[1] = sh.over0 = sh.even0 = sh.counts[0] = sh.counts[1] = sh.ncand = sh.before = 0;
+  }
+  if (S > 1) cluster_arrive();  // waited for before the first write to another CTA
 
   // ---- entries of the first tile -------------------------------------------
   const int gl = lane >> 2, qi = lane & 3;
@@ -383,24 +396,23 @@ __global__ void __launch_bounds__(THREADS, (NT == 1 ? 768 : 384) / THREADS)
   kmin = __reduce_min_sync(kAll, kmin);
   kmax = __reduce_max_sync(kAll, kmax);
   if (lane == 0) { sh.warp_a[warp] = kmin; sh.warp_b[warp] = kmax; }
-  for (int i = tid; i < 4 * 256; i += THREADS) (&sh.hist[0][0])[i] = 0;
-  if (tid == 0) sh.ncand = sh.counts[0] = sh.counts[1] = 0;
+  if (S > 1) cluster_wait();
   __syncthreads();
   if (warp == 0) {
     kmin = __reduce_min_sync(kAll, lane < WARPS ? sh.warp_a[lane] : 0xffffffffu);
     kmax = __reduce_max_sync(kAll, lane < WARPS ? sh.warp_b[lane] : 0u);
-    if (lane == 0) { sh.range[0] = kmin; sh.range[1] = kmax; }
+    if (lane < S) {  // one CTA per lane
+      const uint32_t a = cluster_map(smem_addr(sh.range), lane);
+      red_cluster_min(a, kmin);
+      red_cluster_max(a + 4, kmax);
+    }
   }
   sync_all(S);
-  {
-    // one CTA per lane
-    const uint32_t a = cluster_map(smem_addr(sh.range), lane < S ? lane : 0);
-    kmin = __reduce_min_sync(kAll, ld_cluster_u32(a));
-    kmax = __reduce_max_sync(kAll, ld_cluster_u32(a + 4));
-  }
+  kmin = sh.range[0];
+  kmax = sh.range[1];
 
   // ---- the cut: 8 bits of (score - smallest) a count ---------------------------
-  const uint32_t a_hist = smem_addr(sh.hist), a_counts = smem_addr(sh.counts);
+  const uint32_t a_hist = smem_addr(sh.hist);
   uint32_t bits = 32 - __clz(kmax - kmin);
   uint32_t prefix = 0;
   uint32_t left = need;  // to be taken among the scores that match the prefix
@@ -459,8 +471,10 @@ __global__ void __launch_bounds__(THREADS, (NT == 1 ? 768 : 384) / THREADS)
       ++even;
       if (ranked) {
         const uint32_t slot = atomicAdd(&sh.ncand, 1u);
-        sh.cand_key[slot] = key;
-        sh.cand_at[slot] = lo + i;
+        for (uint32_t r = 0; r < S; ++r) {
+          st_cluster_u32(cluster_map(smem_addr(&sh.cand_key[rank][slot]), r), key);
+          st_cluster_u32(cluster_map(smem_addr(&sh.cand_at[rank][slot]), r), lo + i);
+        }
       }
     }
   }
@@ -470,19 +484,22 @@ __global__ void __launch_bounds__(THREADS, (NT == 1 ? 768 : 384) / THREADS)
     atomicAdd(&sh.counts[0], over);
     atomicAdd(&sh.counts[1], even);
   }
-  sync_all(S);
-  // of the CTAs before this one, one per lane
-  const uint32_t a_mine = cluster_map(a_counts, lane < rank ? lane : 0);
-  const uint32_t over0 = __reduce_add_sync(kAll, lane < rank ? ld_cluster_u32(a_mine) : 0u);
-  const uint32_t even0 = __reduce_add_sync(kAll, lane < rank ? ld_cluster_u32(a_mine + 4) : 0u);
-  uint32_t before = over0;
+  __syncthreads();
+  if (tid < S) {
+    if (tid > rank) {
+      red_cluster_add(cluster_map(smem_addr(&sh.over0), tid), sh.counts[0]);
+      red_cluster_add(cluster_map(smem_addr(&sh.even0), tid), sh.counts[1]);
+    }
+    st_cluster_u32(cluster_map(smem_addr(&sh.cand_n[rank]), tid), sh.ncand);
+  }
+  sync_all(S);  // the last word from another CTA
+  const uint32_t even0 = sh.even0;
+  uint32_t before = sh.over0;
   if (ranked) {
-    // gather the bin's scores of all CTAs, rank them, and mark the taken ones
-    // among this CTA's with a key above the limit, the others with one below
-    const uint32_t a_key = smem_addr(sh.cand_key), a_at = smem_addr(sh.cand_at);
-    const uint32_t nr =
-        lane < S ? ld_cluster_u32(cluster_map(smem_addr(&sh.ncand), lane)) : 0u;
-    uint32_t start = nr;  // of the entries of CTA `lane`
+    // put the bin's scores of all CTAs in one list, rank them, and mark the taken
+    // ones among this CTA's with a key above the limit, the others with one below
+    const uint32_t nr = lane < S ? sh.cand_n[lane] : 0u;
+    uint32_t start = nr;  // of the scores of CTA `lane`
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const uint32_t y = __shfl_up_sync(kAll, start, o);
@@ -490,13 +507,11 @@ __global__ void __launch_bounds__(THREADS, (NT == 1 ? 768 : 384) / THREADS)
     }
     const uint32_t at = __shfl_sync(kAll, start, 31);
     start -= nr;
-    if (tid == 0) sh.before = 0;
     for (uint32_t r = warp; r < S; r += WARPS) {
       const uint32_t n0 = __shfl_sync(kAll, nr, r), s0 = __shfl_sync(kAll, start, r);
-      const uint32_t rk = cluster_map(a_key, r), ra = cluster_map(a_at, r);
       for (uint32_t i = lane; i < n0; i += 32) {
-        sh.all_key[s0 + i] = ld_cluster_u32(rk + 4 * i);
-        sh.all_at[s0 + i] = ld_cluster_u32(ra + 4 * i);
+        sh.all_key[s0 + i] = sh.cand_key[r][i];
+        sh.all_at[s0 + i] = sh.cand_at[r][i];
       }
     }
     __syncthreads();
@@ -539,7 +554,6 @@ __global__ void __launch_bounds__(THREADS, (NT == 1 ? 768 : 384) / THREADS)
     over += ov;
     even += eq;
   }
-  if (S > 1) cluster_sync();  // no CTA leaves while another may still read its words
 }
 
 template <int D, int THREADS>
@@ -562,7 +576,6 @@ cudaError_t launch_select(const SelectParams& p, int threads, unsigned grid, uns
 
 bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 
-constexpr int kSelMaxCluster = 8;
 constexpr int kSelMaxCap = 40 * 1024;  // scores of one CTA: 160 KB
 
 }  // namespace
@@ -615,13 +628,16 @@ extern "C" pkv_status pkv_select_blocks(const pkv_pool* pool, int32_t layer,
       return (pkv_status)st;
     if ((st = pkv::read_and_clear_error_word(err, stream)) != PKV_OK) return (pkv_status)st;
   }
-  // An SM holds 24 warps of this kernel.  Few rows: clusters of CTAs of 24
-  // warps, one an SM; more: CTAs of 12 warps, two an SM; many: one CTA of 6 warps
-  // a row, four an SM.  No more CTAs a row than leave each warp a tile, and
-  // as many as its scores need room.
+  // An SM holds 24 warps of this kernel.  Rows for most of the SMs: one CTA of 24
+  // warps each.  Fewer: clusters of such CTAs, or from 20 rows on of CTAs of 12
+  // warps, as many as fit.  More: CTAs of 12 warps, then of 6, one a row.  (96 rows
+  // of 2048 to 8192 blocks, D 64: one CTA of 24 warps 22.8 us, three of 12 24.0, six
+  // of 6 30.6.)  No more CTAs a row than leave each warp a tile, and as many as its
+  // scores need room.
   const int tiles = (mb + 15) / 16;
-  const int threads = rows * 8 <= sms ? 768 : rows <= 2 * sms ? 384 : 192;
-  int64_t S = threads == 768 ? 8 : threads == 384 ? 2 * sms / rows : 1;
+  const bool most = rows > sms * 5 / 8 && rows <= sms;
+  const int threads = rows * 8 <= sms || most ? 768 : rows <= 2 * sms ? 384 : 192;
+  int64_t S = most ? 1 : threads == 768 ? 8 : threads == 384 ? 2 * sms / rows : 1;
   if (S > (tiles * 32 + threads - 1) / threads) S = (tiles * 32 + threads - 1) / threads;
   if (S > pkv::kSelMaxCluster) S = pkv::kSelMaxCluster;
   while (S < pkv::kSelMaxCluster && (mb + S - 1) / S > pkv::kSelMaxCap) S *= 2;
