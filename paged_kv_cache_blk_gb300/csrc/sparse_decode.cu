@@ -42,8 +42,6 @@
 namespace pkv {
 namespace {
 
-constexpr int kSpWarps = 4;
-constexpr int kSpThreads = kSpWarps * 32;
 constexpr int kTile = 16;  // rows of a tile
 constexpr unsigned kAll = 0xffffffffu;
 constexpr float kLog2e = 1.4426950408889634f;
@@ -70,11 +68,6 @@ struct SparseParams {
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool live) {
   const int n = live ? 16 : 0;
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n)
-               : "memory");
-}
-__device__ __forceinline__ void cp_async4(uint32_t dst, const void* src, bool live) {
-  const int n = live ? 4 : 0;
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(n)
                : "memory");
 }
 __device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
@@ -167,16 +160,8 @@ struct Tile {
   static constexpr int kRow = D * kEs;              // bytes of one head of a row
   static constexpr int kChunks = kRow / 16;         // 16-byte chunks of it
   static constexpr int kHalf = kTile * kRow;        // K (or V) rows
-  static constexpr int kScales = MODE == PKV_I8 ? 2 * kTile * 4 : 0;
+  static constexpr int kScales = MODE == PKV_I8 ? 2 * kTile * 16 : 0;
   static constexpr int kBytes = 2 * kHalf + kScales;
-  // Tiles of a warp's ring: what lets two CTAs share an SM.  (64 sequences of
-  // 2048 selected tokens, Hkv 8, D 128: bf16 with 3 tiles 82 us, with 2 and three
-  // CTAs an SM 98, with 5 and one 102; int8 with 5 tiles 72 us, with 3 and
-  // four CTAs 81, with 4 and three 98: the 512 CTAs then no longer fill
-  // whole rounds.)
-  static constexpr int kStages = D == 128 ? (MODE == PKV_F32 ? 2 : MODE == PKV_BF16 ? 3 : 5)
-                                          : (MODE == PKV_F32 ? 2 : MODE == PKV_BF16 ? 5 : 8);
-
   // Byte offset of chunk c of row r: chunks of a row are permuted so that the
   // 8 rows of an ldmatrix (and the 2 rows x 4 chunks of an LDS.128 phase of
   // the int8 K reads) fall in 8 different 16-byte columns.
@@ -207,9 +192,10 @@ struct Tile {
     if constexpr (MODE == PKV_I8) {
       const int r = lane & 15;
       const bool live = r >= lo && r < hi;
+      // the 16 bytes that hold the head's scale (rows are padded to 16)
       const char* src = (lane < 16 ? p.k : p.v) +
-                        (row + (live ? r : 0)) * p.row_bytes + p.scale_off + 4 * g;
-      cp_async4(dst + 2 * kHalf + lane * 4, src, live);
+                        (row + (live ? r : 0)) * p.row_bytes + p.scale_off + (4 * g & ~15);
+      cp_async16(dst + 2 * kHalf + lane * 16, src, live);
     }
   }
 };
@@ -228,11 +214,13 @@ struct MmaState {
   float qs[NT][2];  // factor of the scores of columns 2 qi, 2 qi + 1
   int ev;           // int8: biased exponent of the running V-scale normaliser
   float vf;         // 2^(127 - ev)
+  int so;           // int8: byte of the head's scale in its 16
 
   __device__ void init(const SparseParams& p, int t, int g, int lane) {
     const int gl = lane >> 2, qi = lane & 3;
     ev = 0;
     vf = __uint_as_float(254u << 23);
+    so = 4 * g & 15;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
       m[nt][0] = m[nt][1] = -INFINITY;
@@ -329,10 +317,10 @@ struct MmaState {
     }
     float sk0 = 1.f, sk1 = 1.f, w0 = 1.f, w1 = 1.f, rescale = 1.f;
     if constexpr (kI8) {
-      const uint32_t sc = st + 2 * Tl::kHalf;
-      sk0 = lds_f32(sc + t0 * 4);
-      sk1 = lds_f32(sc + t1 * 4);
-      const float sv0 = lds_f32(sc + (16 + t0) * 4), sv1 = lds_f32(sc + (16 + t1) * 4);
+      const uint32_t sc = st + 2 * Tl::kHalf + so;
+      sk0 = lds_f32(sc + t0 * 16);
+      sk1 = lds_f32(sc + t1 * 16);
+      const float sv0 = lds_f32(sc + (16 + t0) * 16), sv1 = lds_f32(sc + (16 + t1) * 16);
       int et = max((int)((__float_as_uint(sv0) >> 23) & 0xFF),
                    (int)((__float_as_uint(sv1) >> 23) & 0xFF));
       if (__any_sync(kAll, et > ev)) {
@@ -583,20 +571,33 @@ struct FmaState {
 template <int MODE, int D, int HEADS>
 struct Layout {
   using Tl = Tile<MODE, D>;
-  static constexpr int kRing = Tl::kStages * Tl::kBytes;
+  // Warps of a CTA and tiles of a warp's ring: what lets two CTAs share an SM by
+  // registers and shared memory, of which some 200 KB an SM are better not passed.
+  // 64 sequences of 2048 selected tokens, Hkv 8, D 128: bf16 with 3 tiles 83 us,
+  // with 2 and three CTAs an SM 98, with 5 and one 102 (the 512 CTAs no longer
+  // fill whole rounds).  int8, G 4: 8 warps with 2 tiles 68.6 us, with 3 71.4,
+  // 4 warps with 5 tiles 72.6, with 4 85; G 16: 4 warps 85, 8 (one CTA an SM) 105.
+  static constexpr int kWarps = MODE == PKV_I8 && HEADS <= 8 ? 8 : 4;
+  static constexpr int kStages =
+      MODE == PKV_F32    ? 2
+      : MODE == PKV_BF16 ? (D == 128 ? 3 : 5)
+      : kWarps == 8      ? (D == 128 ? 2 : 3)
+                         : (D == 128 ? 5 : 8);
+  static constexpr int kRing = kStages * Tl::kBytes;
   static constexpr int kState = HEADS * D * 4 + HEADS * 8;  // of the merge; over the ring
   static constexpr int kBody = (kRing > kState ? kRing : kState);
   static constexpr int kExtra = MODE == PKV_F32 ? FmaState<D, HEADS>::kExtra : 0;
   static constexpr int kWarp = (kBody + kExtra + 127) / 128 * 128;
-  static constexpr int kBytes = kSpWarps * kWarp;
+  static constexpr int kBytes = kWarps * kWarp;
   static constexpr int kStatic = HEADS * 32 * 4;  // the merge's weights
 };
 
 template <int MODE, int D, int HEADS>
-__global__ void __launch_bounds__(kSpThreads) sparse_decode_kernel(const SparseParams p) {
+__global__ void __launch_bounds__(Layout<MODE, D, HEADS>::kWarps * 32)
+    sparse_decode_kernel(const SparseParams p) {
   using Tl = Tile<MODE, D>;
   using Lay = Layout<MODE, D, HEADS>;
-  constexpr int NST = Tl::kStages;
+  constexpr int NST = Lay::kStages, kSpWarps = Lay::kWarps, kSpThreads = kSpWarps * 32;
   extern __shared__ __align__(128) unsigned char smem[];
   griddep_wait();
   griddep_launch_dependents();
@@ -756,26 +757,26 @@ __global__ void __launch_bounds__(kSpThreads) sparse_decode_kernel(const SparseP
   if (S > 1) cluster_sync();  // no CTA leaves while another may still read its states
 }
 
-constexpr int kSpMaxCluster = 8;
-
 template <int MODE, int D, int HEADS>
 cudaError_t launch_sparse_heads(const SparseParams& p, unsigned rows, int sms, cudaStream_t s) {
   using Lay = Layout<MODE, D, HEADS>;
   // CTAs of a cluster: as many as the SMs hold at once (by their 228 KB of shared
-  // memory, 1 KB of it the system's for each CTA), each warp with two tiles or
-  // more.  One round of CTAs, not a little more: 45 rows of fp32 blocks, D 128,
+  // memory, 1 KB of it the system's for each CTA, and 64 K registers, 128 a
+  // thread), each warp with two tiles or more.  One round of CTAs, not a little more: 45 rows of fp32 blocks, D 128,
   // take 9.7 us in clusters of 6 and 29 in clusters of 8, which do not all fit.
   // And where one CTA a row fills the SMs already, more cost more than they
   // balance, since every CTA waits for a chain of index loads first: 512 rows
   // of 2048 bf16 tokens take 82 us at S = 1, 91 at 2, 102 at 4.
-  const unsigned fit = 228 * 1024 / (Lay::kBytes + Lay::kStatic + 1024);
+  constexpr int by_memory = 228 * 1024 / (Lay::kBytes + Lay::kStatic + 1024);
+  constexpr int by_registers = 65536 / (128 * Lay::kWarps * 32);
+  constexpr int fit = by_memory < by_registers ? by_memory : by_registers;
   const long long tiles = (long long)p.K * p.parts;
   long long S = (long long)fit * sms / rows;
-  if (S > kSpMaxCluster) S = kSpMaxCluster;
-  if (S > tiles / (2 * kSpWarps)) S = tiles / (2 * kSpWarps);
+  if (S > 32 / Lay::kWarps) S = 32 / Lay::kWarps;  // the merge takes 32 states
+  if (S > tiles / (2 * Lay::kWarps)) S = tiles / (2 * Lay::kWarps);
   if (S < 1) S = 1;
   return launch_clusters(sparse_decode_kernel<MODE, D, HEADS>, dim3(rows * (unsigned)S),
-                         dim3(kSpThreads), Lay::kBytes, (unsigned)S, s, p);
+                         dim3(Lay::kWarps * 32), Lay::kBytes, (unsigned)S, s, p);
 }
 
 template <int MODE, int D>
@@ -819,7 +820,7 @@ extern "C" pkv_status pkv_decode_attention_sparse(
   const int64_t tiles = (int64_t)num_selected * parts;
   // table positions and tiles are 32-bit in the kernel
   if ((int64_t)mb * v.block_size > INT32_MAX || tiles > (1 << 30) ||
-      rows > INT32_MAX / pkv::kSpMaxCluster)
+      rows > INT32_MAX / 8)
     return PKV_ERR_UNSUPPORTED;
   int optin, grid, validate, sms;
   int* err;
