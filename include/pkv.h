@@ -460,9 +460,9 @@ PKV_API pkv_status pkv_select_blocks(const pkv_pool* pool, int32_t layer, const 
  * num_q_heads, head_dim], contiguous, types and pool dtypes as in
  * pkv_decode_attention (fp32 accumulation; for their product with V the
  * softmax weights are rounded to 16 bits, in two bf16 parts, and for PKV_I8
- * pools, with the V scales, to fp16).  Supported: head_dim 64 or 128; any num_kv_heads; up to 16 query heads
- * per kv head; any block_size the pool allows.  One launch, no workspace; may
- * be captured in a CUDA graph. */
+ * pools, with the V scales, to fp16).  Supported: head_dim 64 or 128; any
+ * num_kv_heads; up to 16 query heads per kv head; any block_size the pool
+ * allows.  One launch, no workspace; may be captured in a CUDA graph. */
 PKV_API pkv_status pkv_decode_attention_sparse(const pkv_pool* pool, int32_t layer, const void* q,
                                                int32_t num_q_heads, float scale,
                                                const int32_t* block_tables,

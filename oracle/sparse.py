@@ -7,7 +7,7 @@ from the CUDA library.
 "mini-runtime ch.12 Paged KV Cache" §6 names sparse KV as a next step of paged
 caches and gives no scheme.  The readings taken here:
 
-* A block is judged by the extremes ``hi_d`` and ``lo_d`` of its keys, element
+* A block is described by the extremes ``hi_d`` and ``lo_d`` of its keys, element
   by element: ``q . k <= sum_d max(q_d hi_d, q_d lo_d)`` for each of them.
 * The extremes are stored in 8 bits with one power of two per (block, head),
   rounded outwards, and queries are coded the same way (to nearest), so a

@@ -15,7 +15,7 @@
 // What bounds it: the keys' bytes for bf16 and fp32 pools (73K prompt tokens, Hkv
 // 8, D 128: 29.3 us, 5.6 TB/s; fp32 43.9 us, 6.1 TB/s); for int8 the five
 // instructions a code (38.7 us).  Four heads a warp, without the merge, took 29.4
-// us in bf16 but 28.6 us instead of 7.6 for the last blocks of 20 sequences in
+// us in bf16 but 28.6 us instead of 6.1 for the last blocks of 20 sequences in
 // int8.
 #include "bounds.cuh"
 #include "common.cuh"

@@ -19,8 +19,8 @@
 //     movmatrix per 8 x 8.  An mma takes one type, that of V, and a bf16 weight
 //     alone would be the largest error of the result (0.0022 of its norm
 //     instead of 0.0017, which is the output's own rounding): each weight
-//     enters as a bf16 and the bf16 of what its rounding left, 16 bits
-//     together, in two products (82 us either way on 64 sequences x 2048
+//     enters as the next bf16 below it and the bf16 of what that leaves,
+//     within 2^-16 of it together, in two products (82 us either way on 64 sequences x 2048
 //     tokens).  The statistics and O stay in fp32.
 //   int8: the same on fp16 mma over the exact codes, q scaled into fp16 by a
 //     power of two, V's scales folded into the weights under a running power
@@ -137,6 +137,15 @@ __device__ __forceinline__ void sts_f32(uint32_t a, float v) {
 __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
   uint32_t r;
   asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+// The largest bf16 below each weight (0 for 0): what is left is positive, so
+// both parts of a weight give an infinite V its own sign, and neither a NaN.
+__device__ __forceinline__ uint32_t below_bf16x2(float lo, float hi) {
+  uint32_t r;
+  asm("prmt.b32 %0, %1, %2, 0x7632;"
+      : "=r"(r)
+      : "r"(max(__float_as_uint(lo), 1u) - 1u), "r"(max(__float_as_uint(hi), 1u) - 1u));
   return r;
 }
 // Four codes (bytes c + 128) to fp16 pairs: 1024 + byte, minus 1152.
@@ -334,7 +343,7 @@ struct MmaState {
       w1 = sv1 * vf;
     }
     uint32_t pb[NT][2];
-    [[maybe_unused]] uint32_t rest[NT][2];  // bf16: what the rounding of the weights left
+    [[maybe_unused]] uint32_t rest[NT][2];  // bf16: what is left of the weights
     float a[NT][2];
     bool moved = false;
 #pragma unroll
@@ -369,7 +378,7 @@ struct MmaState {
         pb[nt][0] = movmatrix_t(pack_f16x2(s[nt][0] * w0, s[nt][1] * w0));
         pb[nt][1] = movmatrix_t(pack_f16x2(s[nt][2] * w1, s[nt][3] * w1));
       } else {
-        const uint32_t h0 = pack_bf16x2(s[nt][0], s[nt][1]), h1 = pack_bf16x2(s[nt][2], s[nt][3]);
+        const uint32_t h0 = below_bf16x2(s[nt][0], s[nt][1]), h1 = below_bf16x2(s[nt][2], s[nt][3]);
         pb[nt][0] = movmatrix_t(h0);
         pb[nt][1] = movmatrix_t(h1);
         rest[nt][0] = movmatrix_t(pack_bf16x2(s[nt][0] - bf16_lo(h0), s[nt][1] - bf16_hi(h0)));
@@ -762,8 +771,9 @@ cudaError_t launch_sparse_heads(const SparseParams& p, unsigned rows, int sms, c
   using Lay = Layout<MODE, D, HEADS>;
   // CTAs of a cluster: as many as the SMs hold at once (by their 228 KB of shared
   // memory, 1 KB of it the system's for each CTA, and 64 K registers, 128 a
-  // thread), each warp with two tiles or more.  One round of CTAs, not a little more: 45 rows of fp32 blocks, D 128,
-  // take 9.7 us in clusters of 6 and 29 in clusters of 8, which do not all fit.
+  // thread), each warp with two tiles or more.  One round of CTAs, not a little
+  // more: 45 rows of fp32 blocks, D 128, take 9.7 us in clusters of 6 and 29 in
+  // clusters of 8, which do not all fit.
   // And where one CTA a row fills the SMs already, more cost more than they
   // balance, since every CTA waits for a chain of index loads first: 512 rows
   // of 2048 bf16 tokens take 82 us at S = 1, 91 at 2, 102 at 4.

@@ -509,8 +509,39 @@ def test_sparse_special_lists(dev):
     assert bool(run([2, 5])[0].isnan().all())
 
 
-@pytest.mark.parametrize("dtype", ["bf16", "i8"])
-def test_sparse_nan_keys_and_infinite_scores(dev, dtype):
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("top", [False, True])
+def test_sparse_infinite_values(dev, dtype, top):
+    """An infinite value that is seen is what the sum over its element becomes, whether its
+    weight is a power of two (the row of the largest score) or not; other elements stay."""
+    w, spec, pool = _case(dev, dtype, 2, 128, 16, [100], 61, offsets=False)
+    bt, _, offs, _ = dev_batch(w.batch, dev)
+    q = rand_rows((1, 8, 128), dtype, 62, dev)
+    one = lambda a: torch.tensor([a], dtype=torch.int32, device=dev)
+    sel = torch.tensor([[[0, 2, 3]] * 2], dtype=torch.int32, device=dev)
+    out = torch.empty_like(q)
+
+    def run():
+        pkv.decode_attention_sparse(pool, w.layer, q, 128 ** -0.5, bt, offs, one(0), one(99), sel, out)
+        return out.clone()
+
+    clean = run()
+    blk = int(w.batch.block_tables[0, 2])
+    if top:
+        # every head's largest score: 2 |q|^2 / sqrt(D) of one head, the others' below it
+        q[:] = q[:, :1]
+        pool.k_cache[blk, w.layer, 5] = 2 * q[0, 0]
+        clean = run()
+    pool.v_cache[blk, w.layer, 5, 0, 7] = float("inf")
+    pool.v_cache[blk, w.layer, 5, 0, 70] = -float("inf")
+    pool.v_cache[blk, w.layer, 5, 1, 126] = float("inf")
+    got = run()
+    want = clean.clone()
+    want[0, :4, 7], want[0, :4, 70], want[0, 4:, 126] = float("inf"), -float("inf"), float("inf")
+    assert torch.equal(got, want)
+
+
+def test_sparse_nan_keys_and_infinite_scores(dev):
     w, spec, pool = _case(dev, "bf16", 1, 128, 16, [64], 59, offsets=False)
     bt, _, offs, _ = dev_batch(w.batch, dev)
     q = rand_rows((1, 4, 128), "bf16", 60, dev).abs()
