@@ -8,9 +8,11 @@
 // What bounds it: the K and V bytes of the selected blocks, one head of each
 // row (256 bytes for bf16, D 128), read once for the G heads of the group.
 //
-// How.  A cluster of CTAs per (t, g); its warps take the 16-row tiles of the
-// listed blocks in turn.  Each warp runs alone: it looks up 32 tiles at a
-// time (one per lane: list entry, table entry, rows covered), keeps a ring of
+// How.  A cluster of CTAs per (t, g); its warps take the pieces of the listed
+// blocks, 16 rows or a smaller block each, in turn.  Each warp runs alone: it
+// looks up 32 pieces at a time (one per lane: list entry, table entry, rows
+// covered), makes 16-row tiles of them (with a tile a block, 33 sequences of 101
+// blocks of 8 rows, fp32, Hkv 8, D 64, took 47 us instead of 30), keeps a ring of
 // tiles in flight with 16-byte cp.async copies to its own shared memory (rows
 // that the query does not see arrive as zeros, so whatever they hold never
 // enters a product), and holds its own running softmax state:
@@ -20,8 +22,8 @@
 //     alone would be the largest error of the result (0.0022 of its norm
 //     instead of 0.0017, which is the output's own rounding): each weight
 //     enters as the next bf16 below it and the bf16 of what that leaves,
-//     within 2^-16 of it together, in two products (82 us either way on 64 sequences x 2048
-//     tokens).  The statistics and O stay in fp32.
+//     within 2^-16 of it together, in two products (83 us either way on 64
+//     sequences x 2048 tokens).  The statistics and O stay in fp32.
 //   int8: the same on fp16 mma over the exact codes, q scaled into fp16 by a
 //     power of two, V's scales folded into the weights under a running power
 //     of two (see decode.cu); the rows of a tile are taken in the order that
@@ -59,7 +61,8 @@ struct SparseParams {
   int* err;
   long long num_blocks;
   int batch, mb, bs, L, layer, row_bytes, scale_off, hq, hkv, G, K;
-  int parts;      // tiles of a block (a power of two)
+  int parts;      // pieces of a block (a power of two)
+  int piece_bits; // log2 of the rows of a piece
   float qscale;   // scale * log2(e)
 };
 
@@ -182,29 +185,37 @@ struct Tile {
     return r * kRow + ((c ^ (r & 7)) << 4);
   }
 
-  // Start the copies of rows [lo, hi) of the tile whose row 0 is token row
-  // `row`; the other rows are filled with zeros (no byte of them is read).
+  // Start the copies of the tile's rows in `mask`; the others are filled with
+  // zeros (no byte of them is read).  `row` of lane u: the token row of the first
+  // row of piece u; a tile of one piece passes ONE.
+  template <bool ONE>
   static __device__ __forceinline__ void load(const SparseParams& p, uint32_t dst, long long row,
-                                              int g, int lo, int hi, int lane) {
+                                              int g, uint32_t mask, int lane) {
     constexpr int RPI = 32 / (kChunks < 32 ? kChunks : 32);  // rows of one instruction
-    const char* kb = p.k + row * p.row_bytes + g * kRow;
-    const char* vb = p.v + row * p.row_bytes + g * kRow;
-    const int c = lane % kChunks, r0 = lane / kChunks;
+    const long long row0 = ONE ? row : __shfl_sync(kAll, row, 0);
+    // bytes from row0 to row r (0 for a row that is not copied)
+    auto bytes_to = [&](int r) -> long long {
+      const bool live = mask >> r & 1;
+      if constexpr (ONE) return live ? (long long)r * p.row_bytes : 0;
+      const long long at_row =
+          __shfl_sync(kAll, row, r >> p.piece_bits) + (r & ((1 << p.piece_bits) - 1));
+      return live ? (at_row - row0) * p.row_bytes : 0;
+    };
+    const char* kb = p.k + row0 * p.row_bytes;
+    const char* vb = p.v + row0 * p.row_bytes;
+    const int c = lane % kChunks, r0 = lane / kChunks, col = g * kRow + c * 16;
 #pragma unroll
     for (int i = 0; i < kTile / RPI; ++i) {
       const int r = i * RPI + r0;
-      const bool live = r >= lo && r < hi;
-      const long long off = live ? (long long)r * p.row_bytes + c * 16 : 0;
-      cp_async16(dst + at(r, c), kb + off, live);
-      cp_async16(dst + kHalf + at(r, c), vb + off, live);
+      const long long off = bytes_to(r) + col;
+      cp_async16(dst + at(r, c), kb + off, mask >> r & 1);
+      cp_async16(dst + kHalf + at(r, c), vb + off, mask >> r & 1);
     }
     if constexpr (MODE == PKV_I8) {
       const int r = lane & 15;
-      const bool live = r >= lo && r < hi;
       // the 16 bytes that hold the head's scale (rows are padded to 16)
-      const char* src = (lane < 16 ? p.k : p.v) +
-                        (row + (live ? r : 0)) * p.row_bytes + p.scale_off + (4 * g & ~15);
-      cp_async16(dst + 2 * kHalf + lane * 16, src, live);
+      const char* src = (lane < 16 ? kb : vb) + bytes_to(r) + p.scale_off + (4 * g & ~15);
+      cp_async16(dst + 2 * kHalf + lane * 16, src, mask >> r & 1);
     }
   }
 };
@@ -287,12 +298,12 @@ struct MmaState {
     }
   }
 
-  // One staged tile; rows [lo, hi) are the ones the query sees.
-  __device__ void step(uint32_t st, int lo, int hi, int lane) {
+  // One staged tile; the rows in `mask` are the ones the query sees.
+  __device__ void step(uint32_t st, uint32_t mask, int lane) {
     const int gl = lane >> 2, qi = lane & 3;
     // the tokens of this lane's two score rows
     const int t0 = kI8 ? 4 * (gl >> 1) + (gl & 1) : gl, t1 = kI8 ? t0 + 2 : gl + 8;
-    const bool in0 = t0 >= lo && t0 < hi, in1 = t1 >= lo && t1 < hi;
+    const bool in0 = mask >> t0 & 1, in1 = mask >> t1 & 1;
     float s[NT][4];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
@@ -488,9 +499,9 @@ struct FmaState {
     __syncwarp();
   }
 
-  __device__ void step(uint32_t st, int lo, int hi, int lane) {
+  __device__ void step(uint32_t st, uint32_t mask, int lane) {
     const int tok = lane & 15, side = lane >> 4;  // two lanes a token, half the dims each
-    const bool in = tok >= lo && tok < hi;
+    const bool in = mask >> tok & 1;
 #pragma unroll
     for (int h0 = 0; h0 < GP; h0 += 4) {
       float s[4] = {0.f, 0.f, 0.f, 0.f};
@@ -621,11 +632,11 @@ __global__ void __launch_bounds__(Layout<MODE, D, HEADS>::kWarps * 32)
   // position; offset and table entry; row: a batch's list entries are loaded one
   // batch ahead, the first ones here.
   const int32_t* list = p.sel + (long long)row * p.K;
-  const int all_tiles = p.K * p.parts;
+  const int all_pieces = p.K * p.parts;
   const int part_bits = 31 - __clz(p.parts);
   const int stride = (int)S * kSpWarps;
-  int next = (int)rank * kSpWarps + warp;  // first tile of the batch to come
-  auto listed = [&](long long ts) { return ts < all_tiles ? ld_volatile(list + (ts >> part_bits)) : -1; };
+  int next = (int)rank * kSpWarps + warp;  // first piece of the batch to come
+  auto listed = [&](long long ts) { return ts < all_pieces ? ld_volatile(list + (ts >> part_bits)) : -1; };
   int ahead = listed(next + (long long)lane * stride);
   const int seq = ld_volatile(p.tok_seq + t), pos = ld_volatile(p.tok_pos + t);
   if (seq < 0) return;  // padding: the whole cluster leaves, nothing is written
@@ -640,20 +651,20 @@ __global__ void __launch_bounds__(Layout<MODE, D, HEADS>::kWarps * 32)
       end = off + pos + 1;
     }
   }
-  const int tiles = end > 0 ? all_tiles : 0;  // a bad token sees nothing: zeros
+  const int pieces = end > 0 ? all_pieces : 0;  // a bad token sees nothing: zeros
 
   const uint32_t base = smem_addr(smem);
   const uint32_t ring = base + warp * Lay::kWarp;
 
-  // ---- lookup: 32 tiles a time, one per lane ----
+  // ---- lookup: 32 pieces a time, one per lane ----
   const int32_t* table = p.bt + (long long)(end > 0 ? seq : 0) * p.mb;
-  const int rows_tile = min(p.bs, kTile);
+  const int rows_piece = 1 << p.piece_bits;
   long long my_row = 0;
-  int my_range = 0;
+  uint32_t my_mask = 0;
   unsigned todo = 0;
   auto lookup = [&]() {
     // stops at the last batch or at one that has something to do
-    while (todo == 0 && next < tiles) {
+    while (todo == 0 && next < pieces) {
       const long long ts = next + (long long)lane * stride;
       const int j = ahead;
       ahead = listed(ts + 32ll * stride);
@@ -664,7 +675,7 @@ __global__ void __launch_bounds__(Layout<MODE, D, HEADS>::kWarps * 32)
         const int r0 = (int)(ts & (p.parts - 1)) * kTile;
         const int p0 = j * p.bs + r0;
         lo = max(0, off - p0);
-        hi = min(rows_tile, end - p0);
+        hi = min(rows_piece, end - p0);
         if (blk >= 0 && blk < p.num_blocks) {
           my_row = ((long long)blk * p.L + p.layer) * p.bs + r0;
         } else if (lo < hi) {
@@ -672,24 +683,37 @@ __global__ void __launch_bounds__(Layout<MODE, D, HEADS>::kWarps * 32)
           hi = 0;
         }
       }
-      my_range = lo | hi << 8;
+      my_mask = lo < hi ? (1u << hi) - (1u << lo) : 0u;
       todo = __ballot_sync(kAll, lo < hi);
-      next = tiles - next <= 32 * stride ? tiles : next + 32 * stride;
+      next = pieces - next <= 32 * stride ? pieces : next + 32 * stride;
     }
   };
-  int ranges = 0;  // lane s: the rows of the tile in stage s
+  uint32_t masks = 0;  // lane s: the rows of the tile in stage s
   auto issue = [&](int stage) {
     lookup();
+    uint32_t mask = 0;
     if (todo) {
-      const int src = __ffs(todo) - 1;
+      const uint32_t dst = ring + stage * Tl::kBytes;
+      int src = __ffs(todo) - 1;
       todo &= todo - 1;
-      const long long r = __shfl_sync(kAll, my_row, src);
-      const int range = __shfl_sync(kAll, my_range, src);
-      if (lane == stage) ranges = range;
-      Tl::load(p, ring + stage * Tl::kBytes, r, g, range & 0xff, range >> 8, lane);
-    } else if (lane == stage) {
-      ranges = 0;
+      long long r = __shfl_sync(kAll, my_row, src);
+      mask = __shfl_sync(kAll, my_mask, src);
+      if (rows_piece == kTile) {
+        Tl::template load<true>(p, dst, r, g, mask, lane);
+      } else {
+        for (int u = 1; u < kTile >> p.piece_bits; ++u) {
+          lookup();
+          if (todo == 0) break;
+          src = __ffs(todo) - 1;
+          todo &= todo - 1;
+          const long long x = __shfl_sync(kAll, my_row, src);
+          mask |= __shfl_sync(kAll, my_mask, src) << (u << p.piece_bits);
+          if (lane >= u) r = x;
+        }
+        Tl::template load<false>(p, dst, r, g, mask, lane);
+      }
     }
+    if (lane == stage) masks = mask;
     cp_commit();
   };
 
@@ -708,10 +732,10 @@ __global__ void __launch_bounds__(Layout<MODE, D, HEADS>::kWarps * 32)
   while (true) {
     cp_wait<NST - 2>();
     __syncwarp();
-    const int range = __shfl_sync(kAll, ranges, stage);
-    if (range == 0) break;
+    const uint32_t mask = __shfl_sync(kAll, masks, stage);
+    if (mask == 0) break;
     issue(stage == 0 ? NST - 1 : stage - 1);
-    state.step(ring + stage * Tl::kBytes, range & 0xff, range >> 8, lane);
+    state.step(ring + stage * Tl::kBytes, mask, lane);
     if (++stage == NST) stage = 0;
   }
   cp_wait<0>();
@@ -780,7 +804,7 @@ cudaError_t launch_sparse_heads(const SparseParams& p, unsigned rows, int sms, c
   constexpr int by_memory = 228 * 1024 / (Lay::kBytes + Lay::kStatic + 1024);
   constexpr int by_registers = 65536 / (128 * Lay::kWarps * 32);
   constexpr int fit = by_memory < by_registers ? by_memory : by_registers;
-  const long long tiles = (long long)p.K * p.parts;
+  const long long tiles = ((long long)p.K * p.parts << p.piece_bits) / kTile;
   long long S = (long long)fit * sms / rows;
   if (S > 32 / Lay::kWarps) S = 32 / Lay::kWarps;  // the merge takes 32 states
   if (S > tiles / (2 * Lay::kWarps)) S = tiles / (2 * Lay::kWarps);
@@ -827,9 +851,9 @@ extern "C" pkv_status pkv_decode_attention_sparse(
   const int mb = batch > 0 ? max_blocks_per_seq : 1;
   const int parts = v.block_size > pkv::kTile ? v.block_size / pkv::kTile : 1;
   const int64_t rows = (int64_t)num_tokens * v.num_kv_heads;
-  const int64_t tiles = (int64_t)num_selected * parts;
-  // table positions and tiles are 32-bit in the kernel
-  if ((int64_t)mb * v.block_size > INT32_MAX || tiles > (1 << 30) ||
+  const int64_t pieces = (int64_t)num_selected * parts;
+  // table positions and pieces are 32-bit in the kernel
+  if ((int64_t)mb * v.block_size > INT32_MAX || pieces > (1 << 30) ||
       rows > INT32_MAX / 8)
     return PKV_ERR_UNSUPPORTED;
   int optin, grid, validate, sms;
@@ -868,6 +892,8 @@ extern "C" pkv_status pkv_decode_attention_sparse(
   p.G = G;
   p.K = num_selected;
   p.parts = parts;
+  p.piece_bits = 0;
+  while (p.piece_bits < 4 && 1 << p.piece_bits < v.block_size) ++p.piece_bits;
   p.qscale = scale * pkv::kLog2e;
   const unsigned r = (unsigned)rows;
   const bool d64 = v.head_dim == 64;
