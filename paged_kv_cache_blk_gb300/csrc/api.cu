@@ -176,10 +176,12 @@ int device_facts(int* smem_optin, int** err_word, int* grid, int* validate) {
   return PKV_OK;
 }
 
-int device_sm_count(int* sm_count) {
+int device_sm_count(int* sm_count, int* ordinal) {
   DevInfo* d;
   const pkv_status st = current_device(&d);
-  if (st == PKV_OK) *sm_count = d->sm_count;
+  if (st != PKV_OK) return st;
+  *sm_count = d->sm_count;
+  if (ordinal) *ordinal = (int)(d - g_dev);
   return st;
 }
 

@@ -68,30 +68,45 @@ __device__ __forceinline__ float ld_cluster_f32(uint32_t addr) {
 
 // Launch `kern` on `s` as clusters of `cluster` CTAs along x (grid.x a
 // multiple of it) and as a programmatic dependent of the work before it.
+// Dynamic shared memory that passes 48 KB with the kernel's own has to be
+// allowed before (allow_shared).
+struct ClusterLaunch {
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[2];
+  ClusterLaunch(dim3 grid, dim3 block, size_t smem, unsigned cluster, cudaStream_t s) {
+    cfg.gridDim = grid;
+    cfg.blockDim = block;
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = cluster;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+  }
+};
+
 template <typename... KArgs, typename... Args>
 cudaError_t launch_clusters(void (*kern)(KArgs...), dim3 grid, dim3 block, size_t smem,
                             unsigned cluster, cudaStream_t s, Args... args) {
-  // (48 KB without asking, the kernel's static shared memory included)
-  if (smem > 16 * 1024) {
-    const cudaError_t e =
-        cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-    if (e != cudaSuccess) return e;
-  }
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = grid;
-  cfg.blockDim = block;
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = s;
-  cudaLaunchAttribute attr[2];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = cluster;
-  attr[1].val.clusterDim.y = 1;
-  attr[1].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, kern, static_cast<KArgs>(args)...);
+  ClusterLaunch l(grid, block, smem, cluster, s);
+  return cudaLaunchKernelEx(&l.cfg, kern, static_cast<KArgs>(args)...);
+}
+
+template <typename... KArgs>
+cudaError_t allow_shared(void (*kern)(KArgs...), size_t smem) {
+  return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+}
+
+// Clusters of `cluster` CTAs that the device holds at once.
+template <typename... KArgs>
+cudaError_t max_clusters(void (*kern)(KArgs...), int threads, size_t smem, unsigned cluster,
+                         int* n) {
+  ClusterLaunch l(dim3(cluster), dim3(threads), smem, cluster, nullptr);
+  return cudaOccupancyMaxActiveClusters(n, kern, &l.cfg);
 }
 
 }  // namespace pkv

@@ -558,12 +558,15 @@ __global__ void __launch_bounds__(THREADS, (NT == 1 ? 768 : 384) / THREADS)
 
 template <int D, int THREADS>
 cudaError_t launch_select_d(const SelectParams& p, unsigned grid, unsigned S, cudaStream_t s) {
-  const size_t smem = (size_t)p.cap * 4;
-  if (p.G <= 8)
-    return launch_clusters(select_kernel<D, 1, THREADS>, dim3(grid), dim3(THREADS), smem, S, s, p);
   // (768 threads have no registers for a second set of sums)
   constexpr int TWO = THREADS < 384 ? THREADS : 384;
-  return launch_clusters(select_kernel<D, 2, TWO>, dim3(grid), dim3(TWO), smem, S, s, p);
+  const size_t smem = (size_t)p.cap * 4;
+  const auto kern = p.G <= 8 ? select_kernel<D, 1, THREADS> : select_kernel<D, 2, TWO>;
+  if (smem > 16 * 1024) {  // (48 KB without asking, the kernel's static shared memory included)
+    const cudaError_t e = allow_shared(kern, smem);
+    if (e != cudaSuccess) return e;
+  }
+  return launch_clusters(kern, dim3(grid), dim3(p.G <= 8 ? THREADS : TWO), smem, S, s, p);
 }
 
 template <int D>

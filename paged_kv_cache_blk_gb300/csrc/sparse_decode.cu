@@ -33,7 +33,10 @@
 // At the end the warps' states (m, l, O) are merged by the log-sum-exp rule
 // out of the shared memories of the whole cluster: no workspace, no second
 // kernel.
+#include <atomic>
+#include <climits>
 #include <cmath>
+#include <mutex>
 #include <type_traits>
 
 #include <cuda_fp16.h>
@@ -44,7 +47,11 @@
 namespace pkv {
 namespace {
 
-constexpr int kTile = 16;  // rows of a tile
+constexpr int kTile = 16;       // rows of a tile
+constexpr int kMaxWarps = 8;    // of a CTA
+constexpr int kMaxCluster = 8;  // CTAs
+constexpr int kMaxStates = 48;  // warps of a cluster (with 64, 16 us where 48 take 13)
+constexpr int kStates = 64;     // room for them, two a lane in their merge
 constexpr unsigned kAll = 0xffffffffu;
 constexpr float kLog2e = 1.4426950408889634f;
 
@@ -591,25 +598,22 @@ struct FmaState {
 template <int MODE, int D, int HEADS>
 struct Layout {
   using Tl = Tile<MODE, D>;
-  // Warps of a CTA and tiles of a warp's ring: what lets two CTAs share an SM by
-  // registers and shared memory, of which some 200 KB an SM are better not passed.
-  // 64 sequences of 2048 selected tokens, Hkv 8, D 128: bf16 with 3 tiles 83 us,
-  // with 2 and three CTAs an SM 98, with 5 and one 102 (the 512 CTAs no longer
-  // fill whole rounds).  int8, G 4: 8 warps with 2 tiles 68.6 us, with 3 71.4,
-  // 4 warps with 5 tiles 72.6, with 4 85; G 16: 4 warps 85, 8 (one CTA an SM) 105.
-  static constexpr int kWarps = MODE == PKV_I8 && HEADS <= 8 ? 8 : 4;
-  static constexpr int kStages =
-      MODE == PKV_F32    ? 2
-      : MODE == PKV_BF16 ? (D == 128 ? 3 : 5)
-      : kWarps == 8      ? (D == 128 ? 2 : 3)
-                         : (D == 128 ? 5 : 8);
+  // Tiles of a warp's ring; the warps of a CTA are chosen at the launch.  64
+  // sequences of 2048 selected tokens, Hkv 8, D 128, 4 warps a CTA: bf16 with 3 tiles
+  // 83 us, with 2 98, with 5 102; int8, 8 warps, with 2 68.6, with 3 71.4.
+  static constexpr int kStages = MODE == PKV_F32    ? 2
+                                 : MODE == PKV_BF16 ? (D == 128 ? 3 : 5)
+                                 : HEADS <= 8       ? (D == 128 ? 2 : 3)
+                                                    : (D == 128 ? 5 : 8);
   static constexpr int kRing = kStages * Tl::kBytes;
   static constexpr int kState = HEADS * D * 4 + HEADS * 8;  // of the merge; over the ring
   static constexpr int kBody = (kRing > kState ? kRing : kState);
   static constexpr int kExtra = MODE == PKV_F32 ? FmaState<D, HEADS>::kExtra : 0;
   static constexpr int kWarp = (kBody + kExtra + 127) / 128 * 128;
-  static constexpr int kBytes = kWarps * kWarp;
-  static constexpr int kStatic = HEADS * 32 * 4;  // the merge's weights
+  static constexpr int kStatic = (HEADS + 1) * kStates * 4;  // the merge's weights, addresses
+  static constexpr int kFit = (227 * 1024 - kStatic) / kWarp;
+  static constexpr int kLimit = MODE == PKV_F32 && HEADS > 8 ? 4 : kMaxWarps;  // (4 fill the FMAs)
+  static constexpr int kWarps = kFit < kLimit ? kFit : kLimit;  // of a CTA at most
 };
 
 template <int MODE, int D, int HEADS>
@@ -617,7 +621,8 @@ __global__ void __launch_bounds__(Layout<MODE, D, HEADS>::kWarps * 32)
     sparse_decode_kernel(const SparseParams p) {
   using Tl = Tile<MODE, D>;
   using Lay = Layout<MODE, D, HEADS>;
-  constexpr int NST = Lay::kStages, kSpWarps = Lay::kWarps, kSpThreads = kSpWarps * 32;
+  constexpr int NST = Lay::kStages;
+  const int W = blockDim.x >> 5;  // warps of a CTA
   extern __shared__ __align__(128) unsigned char smem[];
   griddep_wait();
   griddep_launch_dependents();
@@ -634,8 +639,8 @@ __global__ void __launch_bounds__(Layout<MODE, D, HEADS>::kWarps * 32)
   const int32_t* list = p.sel + (long long)row * p.K;
   const int all_pieces = p.K * p.parts;
   const int part_bits = 31 - __clz(p.parts);
-  const int stride = (int)S * kSpWarps;
-  int next = (int)rank * kSpWarps + warp;  // first piece of the batch to come
+  const int stride = (int)S * W;
+  int next = (int)rank * W + warp;  // first piece of the batch to come
   auto listed = [&](long long ts) { return ts < all_pieces ? ld_volatile(list + (ts >> part_bits)) : -1; };
   int ahead = listed(next + (long long)lane * stride);
   const int seq = ld_volatile(p.tok_seq + t), pos = ld_volatile(p.tok_pos + t);
@@ -748,78 +753,150 @@ __global__ void __launch_bounds__(Layout<MODE, D, HEADS>::kWarps * 32)
     cluster_sync();
   else
     __syncthreads();
-  // weights of the S * kSpWarps <= 32 states of each head, one state per lane
-  __shared__ float weight[HEADS][32];
-  const int states = (int)S * kSpWarps;
-  const uint32_t st_at = cluster_map(base + (lane % kSpWarps) * Lay::kWarp + HEADS * D * 4,
-                                     lane < states ? lane / kSpWarps : 0);
-  for (int h = warp; h < p.G; h += kSpWarps) {
-    const float m = lane < states ? ld_cluster_f32(st_at + h * 8) : -INFINITY;
-    const float l = lane < states ? ld_cluster_f32(st_at + h * 8 + 4) : 0.f;
-    float M = m;
+  // weights of the S * W states of each head
+  __shared__ float weight[HEADS][kStates];
+  __shared__ uint32_t state_at[kStates];
+  const int states = (int)S * W;
+  uint32_t at[2];
+#pragma unroll
+  for (int u = 0; u < 2; ++u) {
+    const int j = min(lane + 32 * u, states - 1);
+    at[u] = cluster_map(base + (j % W) * Lay::kWarp, j / W);
+    if (warp == 0) state_at[lane + 32 * u] = at[u];
+  }
+  for (int h = warp; h < p.G; h += W) {
+    float m[2] = {-INFINITY, -INFINITY}, f[2], M = -INFINITY, sum = 0.f;
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      const int j = lane + 32 * u;
+      f[u] = 0.f;
+      if (j < states) {
+        m[u] = ld_cluster_f32(at[u] + HEADS * D * 4 + h * 8);
+        f[u] = ld_cluster_f32(at[u] + HEADS * D * 4 + h * 8 + 4);
+      }
+      M = fmaxf(M, m[u]);
+    }
 #pragma unroll
     for (int o = 16; o; o >>= 1) M = fmaxf(M, __shfl_xor_sync(kAll, M, o));
-    // a state at -inf saw nothing, or only NaN: its l and O are 0, or NaN
-    const float f = m == -INFINITY ? 1.f : exp2f(m - M);
-    float sum = f * l;
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      // a state at -inf saw nothing, or only NaN: its l and O are 0, or NaN
+      const float l = f[u];
+      f[u] = m[u] == -INFINITY ? 1.f : exp2f(m[u] - M);
+      sum += f[u] * l;
+    }
 #pragma unroll
     for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(kAll, sum, o);
-    weight[h][lane] = sum == 0.f ? 0.f : f / sum;  // no weight at all: zeros
+#pragma unroll
+    for (int u = 0; u < 2; ++u)  // no weight at all: zeros
+      weight[h][lane + 32 * u] = sum == 0.f ? 0.f : f[u] / sum;
   }
   __syncthreads();
   const int pairs = p.G * (D / 2);
-  for (int i = (int)rank * kSpThreads + tid; i < pairs; i += (int)S * kSpThreads) {
+  for (int i = (int)(rank * blockDim.x) + tid; i < pairs; i += (int)(S * blockDim.x)) {
     const int h = i / (D / 2), d = (i % (D / 2)) * 2;
     float x = 0.f, y = 0.f;
 #pragma unroll 8
     for (int j = 0; j < states; ++j) {
-      const uint32_t a = cluster_map(base + (j % kSpWarps) * Lay::kWarp + (h * D + d) * 4,
-                                     j / kSpWarps);
       float u, v;
-      asm volatile("ld.shared::cluster.v2.f32 {%0,%1}, [%2];" : "=f"(u), "=f"(v) : "r"(a));
+      asm volatile("ld.shared::cluster.v2.f32 {%0,%1}, [%2];"
+                   : "=f"(u), "=f"(v)
+                   : "r"(state_at[j] + (h * D + d) * 4));
       x += weight[h][j] * u;
       y += weight[h][j] * v;
     }
-    const long long at = ((long long)t * p.hq + g * p.G + h) * D + d;
+    const long long dst = ((long long)t * p.hq + g * p.G + h) * D + d;
     if constexpr (MODE == PKV_F32) {
-      *reinterpret_cast<float2*>(p.out + at * 4) = make_float2(x, y);
+      *reinterpret_cast<float2*>(p.out + dst * 4) = make_float2(x, y);
     } else {
-      *reinterpret_cast<uint32_t*>(p.out + at * 2) = pack_bf16x2(x, y);
+      *reinterpret_cast<uint32_t*>(p.out + dst * 2) = pack_bf16x2(x, y);
     }
   }
   if (S > 1) cluster_sync();  // no CTA leaves while another may still read its states
 }
 
+// How many clusters of S CTAs of W warps the device holds at once, asked of it
+// once for each kernel.
+struct Residency {
+  std::atomic<bool> ready{false};
+  int clusters[kMaxWarps + 1][kMaxCluster + 1] = {};
+};
+std::mutex residency_mu;
+
 template <int MODE, int D, int HEADS>
-cudaError_t launch_sparse_heads(const SparseParams& p, unsigned rows, int sms, cudaStream_t s) {
+cudaError_t residency(int dev, const Residency** out) {
   using Lay = Layout<MODE, D, HEADS>;
-  // CTAs of a cluster: as many as the SMs hold at once (by their 228 KB of shared
-  // memory, 1 KB of it the system's for each CTA, and 64 K registers, 128 a
-  // thread), each warp with two tiles or more.  One round of CTAs, not a little
-  // more: 45 rows of fp32 blocks, D 128, take 9.7 us in clusters of 6 and 29 in
-  // clusters of 8, which do not all fit.
-  // And where one CTA a row fills the SMs already, more cost more than they
-  // balance, since every CTA waits for a chain of index loads first: 512 rows
-  // of 2048 bf16 tokens take 82 us at S = 1, 91 at 2, 102 at 4.
-  constexpr int by_memory = 228 * 1024 / (Lay::kBytes + Lay::kStatic + 1024);
-  constexpr int by_registers = 65536 / (128 * Lay::kWarps * 32);
-  constexpr int fit = by_memory < by_registers ? by_memory : by_registers;
+  static Residency of_device[64];
+  Residency& r = of_device[dev];
+  *out = &r;
+  if (r.ready.load(std::memory_order_acquire)) return cudaSuccess;
+  std::lock_guard<std::mutex> lock(residency_mu);
+  if (r.ready.load(std::memory_order_relaxed)) return cudaSuccess;
+  const auto kern = sparse_decode_kernel<MODE, D, HEADS>;
+  cudaError_t e = allow_shared(kern, (size_t)Lay::kWarps * Lay::kWarp);
+  for (int W = 1; W <= Lay::kWarps; ++W)
+    for (int S = 1; S <= kMaxCluster && e == cudaSuccess; ++S)
+      e = max_clusters(kern, W * 32, (size_t)W * Lay::kWarp, S, &r.clusters[W][S]);
+  if (e == cudaSuccess) r.ready.store(true, std::memory_order_release);
+  return e;
+}
+
+// Warps W of a CTA and CTAs S of a cluster.  All that the device holds at once
+// should have work, and the rows should fill whole rounds of it.  A warp's time
+// for a tile grows with the L warps on its SM, about as 12 + L; a round costs it
+// half a tile more, and a cluster 2 (1 beside the longer fp32 tiles) and a quarter
+// for each of its CTAs.  The pair with the least
+//     rounds * (tiles of a warp + 1/2 + 2 + S / 4) * (12 + L)
+// is taken, clusters where one round is enough and with two tiles or more a warp.
+// Of 50 cases of all types timed with every pair, it is within 13 % of the best
+// in all and within 5 % in 47.  R rows of K blocks of 16, D 128, G 4, by W x S:
+// fp32, R 264, K 60 3 x 1 45.6 us, 4 x 1 52.1, 2 x 1 57.7; R 160, K 100 1 x 5 48.1,
+// 3 x 1 64.1, 4 x 1 76.9; bf16, R 512, K 128 2 x 1 83.0, 4 x 1 84.5, 8 x 1 92.2,
+// 3 x 1 107; R 40, K 100 8 x 3 10.6, 4 x 3 11.4, 3 x 7 12.5; R 16, K 300 8 x 6 14.4,
+// 4 x 8 14.8.
+template <int MODE, int D, int HEADS>
+cudaError_t launch_sparse_heads(const SparseParams& p, unsigned rows, int dev, int sms,
+                                cudaStream_t s) {
+  using Lay = Layout<MODE, D, HEADS>;
+  const Residency* r;
+  cudaError_t e = residency<MODE, D, HEADS>(dev, &r);
+  if (e != cudaSuccess) return e;
   const long long tiles = ((long long)p.K * p.parts << p.piece_bits) / kTile;
-  long long S = (long long)fit * sms / rows;
-  if (S > 32 / Lay::kWarps) S = 32 / Lay::kWarps;  // the merge takes 32 states
-  if (S > tiles / (2 * Lay::kWarps)) S = tiles / (2 * Lay::kWarps);
-  if (S < 1) S = 1;
-  return launch_clusters(sparse_decode_kernel<MODE, D, HEADS>, dim3(rows * (unsigned)S),
-                         dim3(Lay::kWarps * 32), Lay::kBytes, (unsigned)S, s, p);
+  int warps = 1, ctas = 1;
+  long long least = LLONG_MAX;
+  constexpr bool kF32 = MODE == PKV_F32;
+  for (const int W : {8, 6, 4, 3, 2, 1}) {
+    // (beside the tensor cores' short tiles 6 warps and 1, and clusters of 3, gain nothing)
+    if (W > Lay::kWarps || (!kF32 && (W == 6 || W == 1))) continue;
+    for (int S = 1; S <= kMaxCluster && W * S <= kMaxStates; ++S) {
+      const int fit = r->clusters[W][S];
+      if (fit < 1) break;
+      if (S > 1 && (rows > (unsigned)fit || tiles < 2 * W * S || (!kF32 && W == 3))) break;
+      const long long rounds = (rows + (long long)fit - 1) / fit;
+      const long long held = rounds > 1 ? fit : (long long)rows * S;
+      const long long L = W * ((held + sms - 1) / sms);
+      const long long each = (tiles + W * S - 1) / (W * S);  // tiles of a warp
+      const long long more = S > 1 ? (kF32 ? 4 : 8) + S : 0;
+      const long long cost = rounds * (4 * each + 2 + more) * (12 + L);
+      if (cost < least) {
+        least = cost;
+        warps = W;
+        ctas = S;
+      }
+    }
+  }
+  return launch_clusters(sparse_decode_kernel<MODE, D, HEADS>, dim3(rows * (unsigned)ctas),
+                         dim3(warps * 32), (size_t)warps * Lay::kWarp, (unsigned)ctas, s, p);
 }
 
 template <int MODE, int D>
-cudaError_t launch_sparse_d(const SparseParams& p, unsigned rows, int sms, cudaStream_t s) {
+cudaError_t launch_sparse_d(const SparseParams& p, unsigned rows, int dev, int sms,
+                            cudaStream_t s) {
   if constexpr (MODE == PKV_F32) {
-    if (p.G <= 4) return launch_sparse_heads<MODE, D, 4>(p, rows, sms, s);
+    if (p.G <= 4) return launch_sparse_heads<MODE, D, 4>(p, rows, dev, sms, s);
   }
-  if (p.G <= 8) return launch_sparse_heads<MODE, D, 8>(p, rows, sms, s);
-  return launch_sparse_heads<MODE, D, 16>(p, rows, sms, s);
+  if (p.G <= 8) return launch_sparse_heads<MODE, D, 8>(p, rows, dev, sms, s);
+  return launch_sparse_heads<MODE, D, 16>(p, rows, dev, sms, s);
 }
 
 bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
@@ -856,10 +933,10 @@ extern "C" pkv_status pkv_decode_attention_sparse(
   if ((int64_t)mb * v.block_size > INT32_MAX || pieces > (1 << 30) ||
       rows > INT32_MAX / 8)
     return PKV_ERR_UNSUPPORTED;
-  int optin, grid, validate, sms;
+  int optin, grid, validate, sms, dev;
   int* err;
   if ((st = pkv::device_facts(&optin, &err, &grid, &validate)) != PKV_OK) return (pkv_status)st;
-  if ((st = pkv::device_sm_count(&sms)) != PKV_OK) return (pkv_status)st;
+  if ((st = pkv::device_sm_count(&sms, &dev)) != PKV_OK) return (pkv_status)st;
   if (validate) {
     if ((st = pkv::clear_error_word(err, stream)) != PKV_OK) return (pkv_status)st;
     if ((st = pkv::launch_status(pkv::launch_validate_tokens(
@@ -899,14 +976,14 @@ extern "C" pkv_status pkv_decode_attention_sparse(
   const bool d64 = v.head_dim == 64;
   cudaError_t e;
   if (v.quant)
-    e = d64 ? pkv::launch_sparse_d<PKV_I8, 64>(p, r, sms, stream)
-            : pkv::launch_sparse_d<PKV_I8, 128>(p, r, sms, stream);
+    e = d64 ? pkv::launch_sparse_d<PKV_I8, 64>(p, r, dev, sms, stream)
+            : pkv::launch_sparse_d<PKV_I8, 128>(p, r, dev, sms, stream);
   else if (v.io_size == 2)
-    e = d64 ? pkv::launch_sparse_d<PKV_BF16, 64>(p, r, sms, stream)
-            : pkv::launch_sparse_d<PKV_BF16, 128>(p, r, sms, stream);
+    e = d64 ? pkv::launch_sparse_d<PKV_BF16, 64>(p, r, dev, sms, stream)
+            : pkv::launch_sparse_d<PKV_BF16, 128>(p, r, dev, sms, stream);
   else
-    e = d64 ? pkv::launch_sparse_d<PKV_F32, 64>(p, r, sms, stream)
-            : pkv::launch_sparse_d<PKV_F32, 128>(p, r, sms, stream);
+    e = d64 ? pkv::launch_sparse_d<PKV_F32, 64>(p, r, dev, sms, stream)
+            : pkv::launch_sparse_d<PKV_F32, 128>(p, r, dev, sms, stream);
   if ((st = pkv::launch_status(e)) != PKV_OK) return (pkv_status)st;
   return validate ? (pkv_status)pkv::read_and_clear_error_word(err, stream) : PKV_OK;
 }

@@ -406,6 +406,17 @@ def test_sparse_attention_long_lists(dev, dtype, D):
     _run_sparse(dev, dtype, 2, 4, D, 16, [3000, 1500], 150, q_per=20, seed=29)
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32", "i8"])
+@pytest.mark.parametrize("H,G,D,bs,lens,K,q_per", [
+    (8, 2, 64, 16, [300, 90, 20], 5, 15), (8, 1, 128, 8, [260, 200], 30, 23),
+    (8, 4, 128, 16, [700], 40, 5), (4, 9, 64, 32, [500, 40], 12, 11),
+    (1, 3, 128, 4, [900], 200, 2), (4, 5, 128, 2, [100, 60, 7], 40, 9),
+])
+def test_sparse_attention_many_rows(dev, dtype, H, G, D, bs, lens, K, q_per):
+    """Rows for part of the SMs, for one CTA each and for several rounds; tiles of small blocks."""
+    _run_sparse(dev, dtype, H, G, D, bs, lens, K, q_per=q_per, seed=71)
+
+
 def test_sparse_equals_dense_on_every_entry(dev):
     """With all entries listed, pkv_decode_attention's result within both calls' bounds."""
     w, spec, pool = _case(dev, "bf16", 8, 128, 16, [900, 37, 512], 39)
