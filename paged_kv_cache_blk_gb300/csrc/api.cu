@@ -25,8 +25,6 @@ std::atomic<unsigned long long> g_wait_ns{0};
 std::atomic<int> g_skip_fill{0};
 std::atomic<unsigned> g_epoch{0};
 
-constexpr int kMaxDevices = 64;
-
 struct DevInfo {
   std::atomic<bool> ready{false};
   int sm_count = 0;
@@ -34,7 +32,7 @@ struct DevInfo {
   int* err = nullptr;
 };
 
-DevInfo g_dev[kMaxDevices];
+DevInfo g_dev[pkv::kDevices];
 std::mutex g_dev_mu;
 
 pkv_status current_device(DevInfo** out) {
@@ -43,7 +41,7 @@ pkv_status current_device(DevInfo** out) {
     cudaGetLastError();
     return PKV_ERR_CUDA;
   }
-  if (dev < 0 || dev >= kMaxDevices) return PKV_ERR_UNSUPPORTED;
+  if (dev < 0 || dev >= pkv::kDevices) return PKV_ERR_UNSUPPORTED;
   DevInfo& d = g_dev[dev];
   if (!d.ready.load(std::memory_order_acquire)) {
     std::lock_guard<std::mutex> lock(g_dev_mu);

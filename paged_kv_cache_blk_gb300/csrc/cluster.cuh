@@ -2,6 +2,7 @@
 // shared memory (select.cu, sparse_decode.cu).
 #pragma once
 
+#include <atomic>
 #include <cstdint>
 
 #include "common.cuh"
@@ -96,17 +97,36 @@ cudaError_t launch_clusters(void (*kern)(KArgs...), dim3 grid, dim3 block, size_
   return cudaLaunchKernelEx(&l.cfg, kern, static_cast<KArgs>(args)...);
 }
 
+// Facts of the current device, asked of it once and kept by the caller, in a
+// word for each device (of kDevices) that starts as 0.
+
+// Allow the kernel's launches up to `smem` bytes of dynamic shared memory:
+// always the same number, so that calls of several threads agree.
 template <typename... KArgs>
-cudaError_t allow_shared(void (*kern)(KArgs...), size_t smem) {
-  return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+cudaError_t allow_shared(void (*kern)(KArgs...), size_t smem, std::atomic<int>& done) {
+  if (done.load(std::memory_order_acquire)) return cudaSuccess;
+  const cudaError_t e =
+      cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  if (e == cudaSuccess) done.store(1, std::memory_order_release);
+  return e;
 }
 
-// Clusters of `cluster` CTAs that the device holds at once.
+// The clusters of `cluster` CTAs that the device holds at once.  (Its parts
+// differ in SMs, and a cluster lies in one: 15 clusters of 8 CTAs fit on 152 SMs.)
 template <typename... KArgs>
-cudaError_t max_clusters(void (*kern)(KArgs...), int threads, size_t smem, unsigned cluster,
-                         int* n) {
-  ClusterLaunch l(dim3(cluster), dim3(threads), smem, cluster, nullptr);
-  return cudaOccupancyMaxActiveClusters(n, kern, &l.cfg);
+cudaError_t clusters_held(void (*kern)(KArgs...), int threads, size_t smem, unsigned cluster,
+                          std::atomic<int>& known, int* n) {
+  int k = known.load(std::memory_order_relaxed);
+  if (k == 0) {
+    ClusterLaunch l(dim3(cluster), dim3(threads), smem, cluster, nullptr);
+    int held = 0;
+    const cudaError_t e = cudaOccupancyMaxActiveClusters(&held, kern, &l.cfg);
+    if (e != cudaSuccess) return e;
+    k = held + 1;
+    known.store(k, std::memory_order_relaxed);
+  }
+  *n = k - 1;
+  return cudaSuccess;
 }
 
 }  // namespace pkv

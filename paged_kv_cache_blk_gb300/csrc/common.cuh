@@ -428,7 +428,8 @@ cudaError_t launch_prefix_pass(const PoolView& pv, int layer, const void* q, int
 // shared memory limit, the sticky error word, the decode grid size and the
 // validate flag.  Returns a pkv_status value.
 int device_facts(int* smem_optin, int** err_word, int* decode_grid, int* validate);
-int device_sm_count(int* sm_count, int* ordinal = nullptr);  // (ordinal: below 64)
+constexpr int kDevices = 64;  // ordinals are below it
+int device_sm_count(int* sm_count, int* ordinal = nullptr);
 // A launch's result as a pkv_status value (and the CUDA error cleared).
 int launch_status(cudaError_t e);
 // Validate-mode helpers of api.cu (pkv_status values).

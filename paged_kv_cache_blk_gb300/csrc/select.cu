@@ -32,6 +32,7 @@
 // 200 for 4 KB, and of the cut: 14.9 us for 128 of 8192 blocks of one query (Hkv 8,
 // D 128, G 4), 16.8 us for 64 of 64 to 513 blocks of 64 queries, 42 MB of bounds.
 // (Scores to a workspace, and the cut in a second launch, took 18 and 23 us.)
+#include <climits>
 #include <cmath>
 
 #include <cuda_fp16.h>
@@ -556,30 +557,66 @@ __global__ void __launch_bounds__(THREADS, (NT == 1 ? 768 : 384) / THREADS)
   }
 }
 
-template <int D, int THREADS>
-cudaError_t launch_select_d(const SelectParams& p, unsigned grid, unsigned S, cudaStream_t s) {
-  // (768 threads have no registers for a second set of sums)
-  constexpr int TWO = THREADS < 384 ? THREADS : 384;
-  const size_t smem = (size_t)p.cap * 4;
-  const auto kern = p.G <= 8 ? select_kernel<D, 1, THREADS> : select_kernel<D, 2, TWO>;
-  if (smem > 16 * 1024) {  // (48 KB without asking, the kernel's static shared memory included)
-    const cudaError_t e = allow_shared(kern, smem);
-    if (e != cudaSuccess) return e;
-  }
-  return launch_clusters(kern, dim3(grid), dim3(p.G <= 8 ? THREADS : TWO), smem, S, s, p);
-}
+constexpr int kSelMaxCap = 40 * 1024;  // scores of one CTA: 160 KB
 
-template <int D>
-cudaError_t launch_select(const SelectParams& p, int threads, unsigned grid, unsigned S,
-                          cudaStream_t s) {
-  if (threads == 192) return launch_select_d<D, 192>(p, grid, S, s);
-  if (threads == 384) return launch_select_d<D, 384>(p, grid, S, s);
-  return launch_select_d<D, 768>(p, grid, S, s);
+// Threads T of a CTA and CTAs S of a cluster.  A warp's time for a tile of 16
+// blocks grows slowly with the L warps on its SM, about as 64 + L, and the cut
+// costs it that of 4 tiles, in a cluster of one and a quarter for each CTA more.
+// The pair with the least
+//     rounds * (tiles of a warp + 4 + 1 + S / 4) * (64 + L)
+// is taken; clusters only where one round of them is enough, unless the scores
+// need their room.  Of 284 cases timed with every pair (1 to 1000 rows of 90 to
+// 8000 blocks, D 64 and 128, G 4 and 16) it is within 14 % of the best one in all
+// and within 10 % in 280.  T x S for D 128, G 4: 43 rows of 2000 blocks 384 x 3 12.5
+// us, 384 x 7 19.7, 768 x 1 15.8; 170 rows of 2000 192 x 3 24.1, 384 x 1 26.3, 192 x 1
+// 32.6; 8 of 8000 768 x 8 13.8, 384 x 8 15.2.
+template <int D, int NT>
+cudaError_t launch_select(SelectParams& p, unsigned rows, int dev, int sms, cudaStream_t s) {
+  // (768 threads have no registers for a second set of sums)
+  constexpr int kThreads[2][3] = {{768, 384, 192}, {384, 192, 0}}, kChoices = 4 - NT;
+  constexpr int kPart = kSelMaxCap * 4 / 8;  // bytes: shared memory is asked for in eighths
+  static std::atomic<int> allowed[kDevices][3], known[kDevices][3][9][kSelMaxCluster + 1];
+  void (*const kern[3])(SelectParams) = {
+      NT == 1 ? select_kernel<D, 1, 768> : select_kernel<D, 2, 384>,
+      NT == 1 ? select_kernel<D, 1, 384> : select_kernel<D, 2, 192>,
+      NT == 1 ? select_kernel<D, 1, 192> : nullptr};
+  const int tiles = (p.mb + 15) / 16;
+  int choice = -1, ctas = 1;
+  long long least = LLONG_MAX;
+  for (int c = 0; c < kChoices; ++c) {
+    const int T = kThreads[NT - 1][c], W = T / 32;
+    cudaError_t e = allow_shared(kern[c], kSelMaxCap * 4, allowed[dev][c]);
+    if (e != cudaSuccess) return e;
+    for (int S = 1; S <= kSelMaxCluster && (S - 1) * W < tiles; ++S) {
+      const int cap = (p.mb + S - 1) / S, part = (cap * 4 + kPart - 1) / kPart;
+      if (cap > kSelMaxCap) continue;
+      int fit = 0;
+      e = clusters_held(kern[c], T, (size_t)part * kPart, (unsigned)S, known[dev][c][part][S], &fit);
+      if (e != cudaSuccess) return e;
+      if (fit < 1) break;
+      const long long rounds = (rows + (long long)fit - 1) / fit;
+      // (a sixteenth stays free: 96 rows of 1600 blocks take 18.5 us as 384 x 3, of which
+      // 97 fit, 14.7 as 768 x 1)
+      const bool one_round = rows + rows / 16 <= (unsigned)fit;
+      if (S > 1 && !one_round && (p.mb + S - 2) / (S - 1) <= kSelMaxCap) break;
+      const long long held = rounds > 1 ? (long long)fit * S : (long long)rows * S;
+      const long long L = W * ((held + sms - 1) / sms);
+      const long long each = (tiles + W * S - 1) / (W * S);  // tiles of a warp
+      const long long cost = rounds * (4 * each + 16 + (S > 1 ? 4 + S : 0)) * (64 + L);
+      if (cost < least) {
+        least = cost;
+        choice = c;
+        ctas = S;
+      }
+    }
+  }
+  if (choice < 0) return cudaErrorInvalidConfiguration;
+  p.cap = (p.mb + ctas - 1) / ctas;
+  return launch_clusters(kern[choice], dim3(rows * (unsigned)ctas), dim3(kThreads[NT - 1][choice]),
+                         (size_t)p.cap * 4, (unsigned)ctas, s, p);
 }
 
 bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
-
-constexpr int kSelMaxCap = 40 * 1024;  // scores of one CTA: 160 KB
 
 }  // namespace
 }  // namespace pkv
@@ -619,10 +656,10 @@ extern "C" pkv_status pkv_select_blocks(const pkv_pool* pool, int32_t layer,
     return PKV_ERR_UNSUPPORTED;
   const int64_t rows = (int64_t)num_tokens * v.num_kv_heads;
   if (rows > INT32_MAX / pkv::kSelMaxCluster) return PKV_ERR_UNSUPPORTED;
-  int optin, grid, validate, sms;
+  int optin, grid, validate, sms, dev;
   int* err;
   if ((st = pkv::device_facts(&optin, &err, &grid, &validate)) != PKV_OK) return (pkv_status)st;
-  if ((st = pkv::device_sm_count(&sms)) != PKV_OK) return (pkv_status)st;
+  if ((st = pkv::device_sm_count(&sms, &dev)) != PKV_OK) return (pkv_status)st;
   if (validate) {
     if ((st = pkv::clear_error_word(err, stream)) != PKV_OK) return (pkv_status)st;
     if ((st = pkv::launch_status(pkv::launch_validate_tokens(
@@ -631,20 +668,6 @@ extern "C" pkv_status pkv_select_blocks(const pkv_pool* pool, int32_t layer,
       return (pkv_status)st;
     if ((st = pkv::read_and_clear_error_word(err, stream)) != PKV_OK) return (pkv_status)st;
   }
-  // An SM holds 24 warps of this kernel.  Rows for most of the SMs: one CTA of 24
-  // warps each.  Fewer: clusters of such CTAs, or from 20 rows on of CTAs of 12
-  // warps, as many as fit.  More: CTAs of 12 warps, then of 6, one a row.  (96 rows
-  // of 2048 to 8192 blocks, D 64: one CTA of 24 warps 22.8 us, three of 12 24.0, six
-  // of 6 30.6.)  No more CTAs a row than leave each warp a tile, and as many as its
-  // scores need room.
-  const int tiles = (mb + 15) / 16;
-  const bool most = rows > sms * 5 / 8 && rows <= sms;
-  const int threads = rows * 8 <= sms || most ? 768 : rows <= 2 * sms ? 384 : 192;
-  int64_t S = most ? 1 : threads == 768 ? 8 : threads == 384 ? 2 * sms / rows : 1;
-  if (S > (tiles * 32 + threads - 1) / threads) S = (tiles * 32 + threads - 1) / threads;
-  if (S > pkv::kSelMaxCluster) S = pkv::kSelMaxCluster;
-  while (S < pkv::kSelMaxCluster && (mb + S - 1) / S > pkv::kSelMaxCap) S *= 2;
-  if (S > pkv::kSelMaxCluster) S = pkv::kSelMaxCluster;
   pkv::SelectParams p;
   p.q = static_cast<const char*>(q);
   p.codes = static_cast<const char*>(bound_codes);
@@ -669,11 +692,14 @@ extern "C" pkv_status pkv_select_blocks(const pkv_pool* pool, int32_t layer,
   p.sink = sink;
   p.recent = recent;
   p.q_size = v.io_size;
-  p.cap = (int)((mb + S - 1) / S);
-  const unsigned ctas = (unsigned)(rows * S);
-  const cudaError_t e = v.head_dim == 64
-                            ? pkv::launch_select<64>(p, threads, ctas, (unsigned)S, stream)
-                            : pkv::launch_select<128>(p, threads, ctas, (unsigned)S, stream);
+  const unsigned r = (unsigned)rows;
+  cudaError_t e;
+  if (v.head_dim == 64)
+    e = G <= 8 ? pkv::launch_select<64, 1>(p, r, dev, sms, stream)
+               : pkv::launch_select<64, 2>(p, r, dev, sms, stream);
+  else
+    e = G <= 8 ? pkv::launch_select<128, 1>(p, r, dev, sms, stream)
+               : pkv::launch_select<128, 2>(p, r, dev, sms, stream);
   if ((st = pkv::launch_status(e)) != PKV_OK) return (pkv_status)st;
   return validate ? (pkv_status)pkv::read_and_clear_error_word(err, stream) : PKV_OK;
 }

@@ -33,10 +33,8 @@
 // At the end the warps' states (m, l, O) are merged by the log-sum-exp rule
 // out of the shared memories of the whole cluster: no workspace, no second
 // kernel.
-#include <atomic>
 #include <climits>
 #include <cmath>
-#include <mutex>
 #include <type_traits>
 
 #include <cuda_fp16.h>
@@ -815,32 +813,6 @@ __global__ void __launch_bounds__(Layout<MODE, D, HEADS>::kWarps * 32)
   if (S > 1) cluster_sync();  // no CTA leaves while another may still read its states
 }
 
-// How many clusters of S CTAs of W warps the device holds at once, asked of it
-// once for each kernel.
-struct Residency {
-  std::atomic<bool> ready{false};
-  int clusters[kMaxWarps + 1][kMaxCluster + 1] = {};
-};
-std::mutex residency_mu;
-
-template <int MODE, int D, int HEADS>
-cudaError_t residency(int dev, const Residency** out) {
-  using Lay = Layout<MODE, D, HEADS>;
-  static Residency of_device[64];
-  Residency& r = of_device[dev];
-  *out = &r;
-  if (r.ready.load(std::memory_order_acquire)) return cudaSuccess;
-  std::lock_guard<std::mutex> lock(residency_mu);
-  if (r.ready.load(std::memory_order_relaxed)) return cudaSuccess;
-  const auto kern = sparse_decode_kernel<MODE, D, HEADS>;
-  cudaError_t e = allow_shared(kern, (size_t)Lay::kWarps * Lay::kWarp);
-  for (int W = 1; W <= Lay::kWarps; ++W)
-    for (int S = 1; S <= kMaxCluster && e == cudaSuccess; ++S)
-      e = max_clusters(kern, W * 32, (size_t)W * Lay::kWarp, S, &r.clusters[W][S]);
-  if (e == cudaSuccess) r.ready.store(true, std::memory_order_release);
-  return e;
-}
-
 // Warps W of a CTA and CTAs S of a cluster.  All that the device holds at once
 // should have work, and the rows should fill whole rounds of it.  A warp's time
 // for a tile grows with the L warps on its SM, about as 12 + L; a round costs it
@@ -858,8 +830,9 @@ template <int MODE, int D, int HEADS>
 cudaError_t launch_sparse_heads(const SparseParams& p, unsigned rows, int dev, int sms,
                                 cudaStream_t s) {
   using Lay = Layout<MODE, D, HEADS>;
-  const Residency* r;
-  cudaError_t e = residency<MODE, D, HEADS>(dev, &r);
+  static std::atomic<int> allowed[kDevices], known[kDevices][kMaxWarps + 1][kMaxCluster + 1];
+  const auto kern = sparse_decode_kernel<MODE, D, HEADS>;
+  cudaError_t e = allow_shared(kern, (size_t)Lay::kWarps * Lay::kWarp, allowed[dev]);
   if (e != cudaSuccess) return e;
   const long long tiles = ((long long)p.K * p.parts << p.piece_bits) / kTile;
   int warps = 1, ctas = 1;
@@ -869,9 +842,11 @@ cudaError_t launch_sparse_heads(const SparseParams& p, unsigned rows, int dev, i
     // (beside the tensor cores' short tiles 6 warps and 1, and clusters of 3, gain nothing)
     if (W > Lay::kWarps || (!kF32 && (W == 6 || W == 1))) continue;
     for (int S = 1; S <= kMaxCluster && W * S <= kMaxStates; ++S) {
-      const int fit = r->clusters[W][S];
-      if (fit < 1) break;
-      if (S > 1 && (rows > (unsigned)fit || tiles < 2 * W * S || (!kF32 && W == 3))) break;
+      if (S > 1 && (tiles < 2 * W * S || (!kF32 && W == 3))) break;
+      int fit = 0;
+      e = clusters_held(kern, W * 32, (size_t)W * Lay::kWarp, (unsigned)S, known[dev][W][S], &fit);
+      if (e != cudaSuccess) return e;
+      if (fit < 1 || (S > 1 && rows > (unsigned)fit)) break;
       const long long rounds = (rows + (long long)fit - 1) / fit;
       const long long held = rounds > 1 ? fit : (long long)rows * S;
       const long long L = W * ((held + sms - 1) / sms);
@@ -885,8 +860,8 @@ cudaError_t launch_sparse_heads(const SparseParams& p, unsigned rows, int dev, i
       }
     }
   }
-  return launch_clusters(sparse_decode_kernel<MODE, D, HEADS>, dim3(rows * (unsigned)ctas),
-                         dim3(warps * 32), (size_t)warps * Lay::kWarp, (unsigned)ctas, s, p);
+  return launch_clusters(kern, dim3(rows * (unsigned)ctas), dim3(warps * 32),
+                         (size_t)warps * Lay::kWarp, (unsigned)ctas, s, p);
 }
 
 template <int MODE, int D>

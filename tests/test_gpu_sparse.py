@@ -278,6 +278,13 @@ def test_select_many_queries(dev):
     _run_select(dev, "bf16", 8, 2, 64, 16, [300, 900, 77], 9, 1, 1, q_per=30, seed=27)
 
 
+@pytest.mark.parametrize("G,D", [(2, 64), (12, 128)])
+@pytest.mark.parametrize("q_per", [2, 4, 9, 13, 24])
+def test_select_many_rows(dev, G, D, q_per):
+    """Rows for a part of the SMs up to several for each; clusters of every size."""
+    _run_select(dev, "bf16", 8, G, D, 4, [6300, 900], 12, 1, 1, q_per=q_per, seed=77)
+
+
 @pytest.mark.parametrize("scale_q", [0.0, 1e-30, 1e30])
 def test_select_query_range(dev, scale_q):
     _run_select(dev, "f32", 2, 2, 64, 16, [800], 5, 0, 1, scale_q=scale_q, seed=37)
