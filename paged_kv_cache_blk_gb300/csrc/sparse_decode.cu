@@ -839,10 +839,10 @@ cudaError_t launch_sparse_heads(const SparseParams& p, unsigned rows, int dev, i
   long long least = LLONG_MAX;
   constexpr bool kF32 = MODE == PKV_F32;
   for (const int W : {8, 6, 4, 3, 2, 1}) {
-    // (beside the tensor cores' short tiles 6 warps and 1, and clusters of 3, gain nothing)
+    // (beside the tensor cores' short tiles 6 warps and 1, and clusters below 4, gain nothing)
     if (W > Lay::kWarps || (!kF32 && (W == 6 || W == 1))) continue;
     for (int S = 1; S <= kMaxCluster && W * S <= kMaxStates; ++S) {
-      if (S > 1 && (tiles < 2 * W * S || (!kF32 && W == 3))) break;
+      if (S > 1 && (tiles < 2 * W * S || (!kF32 && W < 4))) break;
       int fit = 0;
       e = clusters_held(kern, W * 32, (size_t)W * Lay::kWarp, (unsigned)S, known[dev][W][S], &fit);
       if (e != cudaSuccess) return e;
