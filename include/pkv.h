@@ -279,7 +279,10 @@ PKV_API size_t pkv_decode_workspace_size(int32_t batch, int32_t num_q_heads, int
  * rows (code * scale).  Both products run on fp16 tensor cores over the
  * exact codes: q is scaled by a power of two into fp16, and the V scales
  * are folded into the softmax weights (normalised by a running power of
- * two), which are rounded to fp16 for the P.V product.
+ * two, that of the largest V scale read so far), which are rounded to fp16 for
+ * the P.V product: of a weight times its scale what is below 2^-14 of the
+ * largest scale loses digits and what is below 2^-25 of it counts as nothing,
+ * however small the weight of the row with that scale.
  * The work is split along the sequence across the GPU; partial softmax
  * states go to `workspace` (>= pkv_decode_workspace_size bytes, contents
  * need no initialisation and are overwritten) and a second kernel combines
@@ -458,9 +461,10 @@ PKV_API pkv_status pkv_select_blocks(const pkv_pool* pool, int32_t layer, const 
  * zeros and sets the error word; the out rows of padding are not written.
  * Rows that the query does not see are not read.  q, out: [num_tokens,
  * num_q_heads, head_dim], contiguous, types and pool dtypes as in
- * pkv_decode_attention (fp32 accumulation; for their product with V the
- * softmax weights are rounded to 16 bits, in two bf16 parts, and for PKV_I8
- * pools, with the V scales, to fp16).  Supported: head_dim 64 or 128; any
+ * pkv_decode_attention (fp32 accumulation; the softmax weights enter their
+ * product with V as two bf16 parts, within 2^-16 of each together; for PKV_I8 pools
+ * the weights times the V scales, as two fp16 parts, within 2^-22 of each or 2^-27
+ * of the largest of the head, whatever the scales).  Supported: head_dim 64 or 128; any
  * num_kv_heads; up to 16 query heads per kv head; any block_size the pool
  * allows.  One launch, no workspace; may be captured in a CUDA graph. */
 PKV_API pkv_status pkv_decode_attention_sparse(const pkv_pool* pool, int32_t layer, const void* q,

@@ -25,9 +25,18 @@
 //     within 2^-16 of it together, in two products (83 us either way on 64
 //     sequences x 2048 tokens).  The statistics and O stay in fp32.
 //   int8: the same on fp16 mma over the exact codes, q scaled into fp16 by a
-//     power of two, V's scales folded into the weights under a running power
-//     of two (see decode.cu); the rows of a tile are taken in the order that
-//     makes the byte-transposing V load agree with movmatrix.
+//     power of two.  V's scales are folded into the weights; the products of a
+//     head are taken in units of a power of two in which the largest of them, as
+//     weights stand now, is 2^2 to 2^15, and each enters as an fp16 and the fp16 of
+//     what that leaves: within 2^-22 of it, or 2^-27 of the largest.  (One fp16
+//     alone, in units of the largest V scale, lost all of a result to a row of next
+//     to no weight whose scale was 2^30 that of the others.  64 sequences x 2048
+//     tokens, 8 kv heads, D 128, with G 4 and 16: that one part 67.9 and 80.9 us,
+//     two parts 68.7 and 89.3; two bf16 parts, which need no units, 71.4 and 97.3:
+//     a code takes twice the instructions to bf16.)  With up to 4 heads a group the
+//     second parts take the columns that the first leave empty: one mma, not two.
+//     The rows of a tile are taken in the order that makes the byte-transposing V
+//     load agree with movmatrix.
 //   fp32: fp32 FMAs, two lanes per token for the scores, D / 32 output dims
 //     per lane.
 // At the end the warps' states (m, l, O) are merged by the log-sum-exp rule
@@ -52,6 +61,13 @@ constexpr int kMaxStates = 48;  // warps of a cluster (with 64, 16 us where 48 t
 constexpr int kStates = 64;     // room for them, two a lane in their merge
 constexpr unsigned kAll = 0xffffffffu;
 constexpr float kLog2e = 1.4426950408889634f;
+
+// int8: products of weights and V scales in units of O.  Units are chosen so that
+// the largest is 2^6 to 2^7 of them, for exponents of it from kLeastTop to kMostTop, and
+// again once it has moved by more than 2^kDrift or a scale passes kMostProduct:
+// scales up to 2^8 times the largest product need no look at the products.
+constexpr float kMostProduct = 32768.f;
+constexpr int kDrift = 4, kLeastTop = -120, kMostTop = 127;
 
 struct SparseParams {
   const char* k;
@@ -156,6 +172,15 @@ __device__ __forceinline__ uint32_t below_bf16x2(float lo, float hi) {
       : "r"(max(__float_as_uint(lo), 1u) - 1u), "r"(max(__float_as_uint(hi), 1u) - 1u));
   return r;
 }
+// The nearest finite fp16 of each: what an infinite product leaves is infinite.
+__device__ __forceinline__ uint32_t pack_f16x2_finite(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.satfinite.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+__device__ __forceinline__ float2 unpack_f16x2(uint32_t w) {
+  return __half22float2(*reinterpret_cast<const __half2*>(&w));
+}
 // Four codes (bytes c + 128) to fp16 pairs: 1024 + byte, minus 1152.
 __device__ __forceinline__ void codes_to_f16(uint32_t w, uint32_t& lo, uint32_t& hi) {
   uint32_t a, b;
@@ -227,34 +252,72 @@ struct Tile {
 
 // ---- consumers: the running state of one warp ------------------------------------
 
-// Tensor-core state for bf16 and int8 pools.
-template <int MODE, int D, int NT>
+// Tensor-core state for bf16 and int8 pools.  HEADS 4 (int8): the heads stand twice
+// among the 8 columns, and in the product with V the weights' first parts take
+// columns 0-3 and what is left of them 4-7.
+template <int MODE, int D, int HEADS>
 struct MmaState {
-  static constexpr bool kI8 = MODE == PKV_I8;
+  static constexpr bool kI8 = MODE == PKV_I8, kTwice = HEADS == 4;
+  static constexpr int NT = (HEADS + 7) / 8;
   static constexpr int KS = D / 16;
   using Tl = Tile<MODE, D>;
   uint32_t qb[NT][KS][2];
   float o[NT][KS][4];
   float m[NT][2], l[NT][2];
   float qs[NT][2];  // factor of the scores of columns 2 qi, 2 qi + 1
-  int ev;           // int8: biased exponent of the running V-scale normaliser
-  float vf;         // 2^(127 - ev)
   int so;           // int8: byte of the head's scale in its 16
+  // int8: O of a column is held in units of 1 / unit.  drift: the logarithm of the
+  // largest product, as weights stand now, over the power of two that the unit was
+  // chosen for; widest: the largest unit of the lane's columns.
+  float unit[NT][2], drift[NT][2], widest;
+  static __device__ __forceinline__ float unit_of(int top) {
+    return __uint_as_float((uint32_t)(133 - top) << 23);
+  }
+
+  // Off the usual path: units for the products `x` (weights times V scales) of a
+  // tile, where the ones so far have drifted or may not hold them; a: factor of O.
+  __device__ void choose_units(const float (&x)[NT][4], float (&a)[NT][2]) {
+    widest = 0.f;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        float mx = fmaxf(fabsf(x[nt][c]), fabsf(x[nt][c + 2]));
+        mx = fmaxf(mx, __shfl_xor_sync(kAll, mx, 4));
+        mx = fmaxf(mx, __shfl_xor_sync(kAll, mx, 8));
+        mx = fmaxf(mx, __shfl_xor_sync(kAll, mx, 16));
+        const int old = 133 - (int)(__float_as_uint(unit[nt][c]) >> 23);
+        // the largest of the tile's products and of those before
+        const float most = fmaxf((float)((int)(__float_as_uint(mx) >> 23) - 127),
+                                 (float)old + drift[nt][c]);
+        const int top = min(kMostTop, max(kLeastTop, (int)floorf(most)));
+        if (abs(top - old) > kDrift) {
+          const int k = old - top;  // in two steps: 2^k may pass the range of fp32
+          a[nt][c] *= __uint_as_float((uint32_t)(127 + k / 2) << 23);
+          a[nt][c] *= __uint_as_float((uint32_t)(127 + (k - k / 2)) << 23);
+          unit[nt][c] = unit_of(top);
+          drift[nt][c] = fmaxf(most - (float)top, 0.f);
+        } else {
+          drift[nt][c] = most - (float)old;
+        }
+        widest = fmaxf(widest, unit[nt][c]);
+      }
+  }
 
   __device__ void init(const SparseParams& p, int t, int g, int lane) {
     const int gl = lane >> 2, qi = lane & 3;
-    ev = 0;
-    vf = __uint_as_float(254u << 23);
     so = 4 * g & 15;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
       m[nt][0] = m[nt][1] = -INFINITY;
       l[nt][0] = l[nt][1] = 0.f;
+      unit[nt][0] = unit[nt][1] = widest = unit_of(kLeastTop);
+      drift[nt][0] = drift[nt][1] = 0.f;
 #pragma unroll
       for (int k = 0; k < KS; ++k)
 #pragma unroll
         for (int c = 0; c < 4; ++c) o[nt][k][c] = 0.f;
-      const int h = nt * 8 + gl;
+      const int h = kTwice ? gl & 3 : nt * 8 + gl;
       const bool live = h < p.G;
       const char* src = p.q + ((long long)t * p.hq + g * p.G + (live ? h : 0)) * (D * 2);
       if constexpr (!kI8) {
@@ -340,28 +403,17 @@ struct MmaState {
         }
       }
     }
-    float sk0 = 1.f, sk1 = 1.f, w0 = 1.f, w1 = 1.f, rescale = 1.f;
+    float sk0 = 1.f, sk1 = 1.f, sv0 = 1.f, sv1 = 1.f;
     if constexpr (kI8) {
       const uint32_t sc = st + 2 * Tl::kHalf + so;
       sk0 = lds_f32(sc + t0 * 16);
       sk1 = lds_f32(sc + t1 * 16);
-      const float sv0 = lds_f32(sc + (16 + t0) * 16), sv1 = lds_f32(sc + (16 + t1) * 16);
-      int et = max((int)((__float_as_uint(sv0) >> 23) & 0xFF),
-                   (int)((__float_as_uint(sv1) >> 23) & 0xFF));
-      if (__any_sync(kAll, et > ev)) {
-        et = __reduce_max_sync(kAll, et);
-        const int en = min(253, max(ev, et));
-        rescale = ev - en >= -126 ? __uint_as_float((uint32_t)(127 + ev - en) << 23) : 0.f;
-        vf = __uint_as_float((uint32_t)(254 - en) << 23);
-        ev = en;
-      }
-      w0 = sv0 * vf;
-      w1 = sv1 * vf;
+      sv0 = lds_f32(sc + (16 + t0) * 16);
+      sv1 = lds_f32(sc + (16 + t1) * 16);
     }
-    uint32_t pb[NT][2];
-    [[maybe_unused]] uint32_t rest[NT][2];  // bf16: what is left of the weights
-    float a[NT][2];
+    float a[NT][2];  // factor of O
     bool moved = false;
+    [[maybe_unused]] bool choose = false;  // int8: units of O
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
       s[nt][0] = in0 ? s[nt][0] * qs[nt][0] * sk0 : -INFINITY;
@@ -371,6 +423,7 @@ struct MmaState {
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
         float mx = fmaxf(s[nt][c], s[nt][c + 2]);
+        float shrink = 1.f;
         a[nt][c] = 1.f;
         // the running maximum moves only where some lane passes it
         if (__any_sync(kAll, mx > m[nt][c])) {
@@ -379,29 +432,35 @@ struct MmaState {
           mx = fmaxf(mx, __shfl_xor_sync(kAll, mx, 16));
           const float n = fmaxf(m[nt][c], mx);
           // nothing but -inf so far: there is nothing to rescale
-          a[nt][c] = m[nt][c] == -INFINITY ? 0.f : exp2f(m[nt][c] - n);
+          shrink = m[nt][c] == -INFINITY ? 0.f : exp2f(m[nt][c] - n);
+          a[nt][c] = shrink;
+          if constexpr (kI8) {
+            if (m[nt][c] != -INFINITY && n > m[nt][c]) drift[nt][c] += m[nt][c] - n;
+            choose |= drift[nt][c] < -kDrift;
+          }
           m[nt][c] = n;
         }
         // scores of -inf carry no weight, even while they are all there is
         const float base = m[nt][c] == -INFINITY ? 0.f : m[nt][c];
         s[nt][c] = exp2f(s[nt][c] - base);
         s[nt][c + 2] = exp2f(s[nt][c + 2] - base);
-        l[nt][c] = l[nt][c] * a[nt][c] + s[nt][c] + s[nt][c + 2];
-        a[nt][c] *= rescale;
+        l[nt][c] = l[nt][c] * shrink + s[nt][c] + s[nt][c + 2];
         moved |= a[nt][c] != 1.f;
       }
-      if constexpr (kI8) {
-        pb[nt][0] = movmatrix_t(pack_f16x2(s[nt][0] * w0, s[nt][1] * w0));
-        pb[nt][1] = movmatrix_t(pack_f16x2(s[nt][2] * w1, s[nt][3] * w1));
-      } else {
-        const uint32_t h0 = below_bf16x2(s[nt][0], s[nt][1]), h1 = below_bf16x2(s[nt][2], s[nt][3]);
-        pb[nt][0] = movmatrix_t(h0);
-        pb[nt][1] = movmatrix_t(h1);
-        rest[nt][0] = movmatrix_t(pack_bf16x2(s[nt][0] - bf16_lo(h0), s[nt][1] - bf16_hi(h0)));
-        rest[nt][1] = movmatrix_t(pack_bf16x2(s[nt][2] - bf16_lo(h1), s[nt][3] - bf16_hi(h1)));
-      }
+    }
+    if constexpr (kI8) {
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int c = 0; c < 4; ++c) s[nt][c] *= c < 2 ? sv0 : sv1;
+      // (no weight is above 1)
+      choose |= fmaxf(fabsf(sv0), fabsf(sv1)) * widest > kMostProduct;
+      moved |= choose;
     }
     if (__any_sync(kAll, moved)) {
+      if constexpr (kI8) {
+        if (__any_sync(kAll, choose)) choose_units(s, a);
+      }
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -411,6 +470,28 @@ struct MmaState {
           o[nt][k][2] *= a[nt][0];
           o[nt][k][3] *= a[nt][1];
         }
+    }
+    uint32_t pb[NT][2];  // the first parts of the weights (times V scales),
+    [[maybe_unused]] uint32_t rest[NT][2];  // and what is left of them
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      uint32_t h[2], r[2];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        float x = s[nt][2 * i], y = s[nt][2 * i + 1];
+        if constexpr (kI8) {
+          x *= unit[nt][0];
+          y *= unit[nt][1];
+          h[i] = pack_f16x2_finite(x, y);
+          const float2 f = unpack_f16x2(h[i]);
+          r[i] = pack_f16x2(x - f.x, y - f.y);
+        } else {
+          h[i] = below_bf16x2(x, y);
+          r[i] = pack_bf16x2(x - bf16_lo(h[i]), y - bf16_hi(h[i]));
+        }
+        pb[nt][i] = movmatrix_t(kTwice && qi >= 2 ? r[i] : h[i]);
+        if constexpr (!kTwice) rest[nt][i] = movmatrix_t(r[i]);
+      }
     }
     const uint32_t sv = st + Tl::kHalf;
     if constexpr (!kI8) {
@@ -427,14 +508,26 @@ struct MmaState {
       }
     } else {
 #pragma unroll
-      for (int k = 0; k < KS; ++k) {
-        uint32_t r0, r1, a0, a1, a2, a3;
-        ldsm_b8_t(r0, r1, sv + Tl::at(lane & 15, k));
-        codes_to_f16(r0, a0, a2);
-        codes_to_f16(r1, a1, a3);
+      for (int k = 0; k < KS; k += 2) {  // (two at a time: products into one sum lie apart)
+        uint32_t v[2][4];
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-          mma16<true>(o[nt][k], a0, a1, a2, a3, pb[nt][0], pb[nt][1]);
+        for (int u = 0; u < 2; ++u) {
+          uint32_t r0, r1;
+          ldsm_b8_t(r0, r1, sv + Tl::at(lane & 15, k + u));
+          codes_to_f16(r0, v[u][0], v[u][2]);
+          codes_to_f16(r1, v[u][1], v[u][3]);
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+            mma16<true>(o[nt][k + u], v[u][0], v[u][1], v[u][2], v[u][3], pb[nt][0], pb[nt][1]);
+        }
+        if constexpr (!kTwice) {
+#pragma unroll
+          for (int u = 0; u < 2; ++u)
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+              mma16<true>(o[nt][k + u], v[u][0], v[u][1], v[u][2], v[u][3], rest[nt][0],
+                          rest[nt][1]);
+        }
       }
     }
   }
@@ -442,8 +535,12 @@ struct MmaState {
   // The state to shared memory: O as [head][D], then (m, l) of each head.
   __device__ void put(const SparseParams& p, uint32_t acc, uint32_t ml, int lane) {
     const int gl = lane >> 2, qi = lane & 3;
-    // int8: back to the units of V (0 when every V scale was 0 or subnormal)
-    const float back = !kI8 ? 1.f : ev >= 1 ? __uint_as_float((uint32_t)ev << 23) : 0.f;
+    if constexpr (kTwice) {
+#pragma unroll
+      for (int k = 0; k < KS; ++k)
+#pragma unroll
+        for (int c = 0; c < 4; ++c) o[0][k][c] += __shfl_xor_sync(kAll, o[0][k][c], 2);
+    }
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -453,6 +550,8 @@ struct MmaState {
         x += __shfl_xor_sync(kAll, x, 8);
         x += __shfl_xor_sync(kAll, x, 16);
         const int h = nt * 8 + 2 * qi + c;
+        // int8: back to the units of V
+        const float back = kI8 ? __uint_as_float((254u << 23) - __float_as_uint(unit[nt][c])) : 1.f;
         if (h < p.G) {
           if (gl == 0) {
             sts_f32(ml + h * 8, m[nt][c]);
@@ -592,7 +691,7 @@ struct FmaState {
 
 // ---- the kernel -------------------------------------------------------------------
 
-// HEADS: heads the state holds (8 NT for the tensor cores, GP for fp32).
+// HEADS: heads the state holds, G rounded up (bf16: 8 or 16, the others 4 too).
 template <int MODE, int D, int HEADS>
 struct Layout {
   using Tl = Tile<MODE, D>;
@@ -723,7 +822,7 @@ __global__ void __launch_bounds__(Layout<MODE, D, HEADS>::kWarps * 32)
   // The query: bf16 fragments are plain loads and go ahead of the tiles; the
   // others compute on it, while the first tiles arrive.
   std::conditional_t<MODE == PKV_F32, FmaState<D, HEADS>,
-                     MmaState<MODE == PKV_F32 ? PKV_BF16 : MODE, D, (HEADS + 7) / 8>>
+                     MmaState<MODE == PKV_F32 ? PKV_BF16 : MODE, D, HEADS>>
       state;
   if constexpr (MODE == PKV_BF16) state.init(p, t, g, lane);
 #pragma unroll 1
@@ -867,7 +966,7 @@ cudaError_t launch_sparse_heads(const SparseParams& p, unsigned rows, int dev, i
 template <int MODE, int D>
 cudaError_t launch_sparse_d(const SparseParams& p, unsigned rows, int dev, int sms,
                             cudaStream_t s) {
-  if constexpr (MODE == PKV_F32) {
+  if constexpr (MODE != PKV_BF16) {
     if (p.G <= 4) return launch_sparse_heads<MODE, D, 4>(p, rows, dev, sms, s);
   }
   if (p.G <= 8) return launch_sparse_heads<MODE, D, 8>(p, rows, dev, sms, s);
