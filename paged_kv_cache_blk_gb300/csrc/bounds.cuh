@@ -49,16 +49,21 @@ __device__ __forceinline__ float min_nan(float a, float b) {
   return r;
 }
 
-// Codes of hi (rounded up) and lo (rounded down) in units 1 / inv.  A NaN
-// takes the outermost code.
+// Codes of hi (rounded up) and lo (rounded down) in units 1 / inv, a power of
+// two.  The product is exact but where it lies below the range of fp32: rounded the
+// code's way there too, it does not become 0.  A NaN takes the outermost code.
 __device__ __forceinline__ int code_up(float x, float inv) {
+  float y;
   int c;
-  asm("cvt.rpi.s32.f32 %0, %1;" : "=r"(c) : "f"(mul_ieee(x, inv)));
+  asm("mul.rp.f32 %0, %1, %2;" : "=f"(y) : "f"(x), "f"(inv));
+  asm("cvt.rpi.s32.f32 %0, %1;" : "=r"(c) : "f"(y));
   return x != x ? 127 : min(127, max(-127, c));
 }
 __device__ __forceinline__ int code_down(float x, float inv) {
+  float y;
   int c;
-  asm("cvt.rmi.s32.f32 %0, %1;" : "=r"(c) : "f"(mul_ieee(x, inv)));
+  asm("mul.rm.f32 %0, %1, %2;" : "=f"(y) : "f"(x), "f"(inv));
+  asm("cvt.rmi.s32.f32 %0, %1;" : "=r"(c) : "f"(y));
   return x != x ? -127 : min(127, max(-127, c));
 }
 
