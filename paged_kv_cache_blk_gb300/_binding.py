@@ -266,9 +266,10 @@ class Rope:
     ``rotary_dim`` dims of a head turn, in pairs (i, i + rotary_dim / 2) or,
     ``interleaved``, (2 i, 2 i + 1).  ``scaling`` for long contexts is None,
     ``"linear"``, ``"base"`` or ``"by_parts"`` (with ``factor``, and for the
-    last ``original_len``, ``turns_fast``, ``turns_slow``); or ``inv_freq``
-    gives the frequencies (radians per token) and ``attn_scale`` the factor on
-    cos and sin."""
+    last ``original_len``, ``turns_fast``, ``turns_slow``).  Any other
+    schedule, such as the ramp of ``by_parts`` with another factor on cos and
+    sin, is given as ``inv_freq`` (radians per token) and ``attn_scale`` (that
+    factor), without ``scaling`` and ``factor``."""
 
     _SCALING = {None: 0, "linear": 1, "base": 2, "by_parts": 3}
 
@@ -280,6 +281,9 @@ class Rope:
         self.struct = _RopeStruct()
         self.ref = ctypes.byref(self.struct)
         if inv_freq is not None:
+            if scaling is not None or factor != 1.0:
+                raise ValueError("inv_freq takes the place of a schedule: scaling and factor do "
+                                 "not go with it")
             f = np.ascontiguousarray(np.asarray(inv_freq, dtype=np.float64))
             if f.shape != (rotary_dim // 2,):
                 raise ValueError("inv_freq must have rotary_dim / 2 entries")
