@@ -319,6 +319,12 @@ def _index(t: Optional[torch.Tensor], pool: Pool, name: str, ndim: int) -> Optio
     return t.data_ptr()
 
 
+def _heads_of(q: torch.Tensor) -> int:
+    if q.dim() != 3:
+        raise ValueError(f"q must be [tokens, heads, head_dim], not {list(q.shape)}")
+    return q.shape[1]
+
+
 def _rows_of(t: torch.Tensor, pool: Pool, name: str, shape: Tuple[int, int, int]) -> int:
     """Elements between tokens of a [tokens, heads, head_dim] tensor in the
     pool's row type, the heads of a token consecutive."""
@@ -361,7 +367,7 @@ def rope_append(pool: Pool, layer: int, rope: Rope, block_tables: torch.Tensor,
     hq = qs = qos = 0
     qp = qop = None
     if q is not None and q_out is not None:
-        hq = q.shape[1]
+        hq = _heads_of(q)
         qs, qos = _rows_of(q, pool, "q", (T, hq, D)), _rows_of(q_out, pool, "q_out", (T, hq, D))
         qp, qop = q.data_ptr(), q_out.data_ptr()
     elif q is not None or q_out is not None:
@@ -535,7 +541,7 @@ def _queries(pool: Pool, q: torch.Tensor, block_tables: torch.Tensor,
     t, h, k = selected.shape
     if t != T or h != pool.num_kv_heads:
         raise ValueError(f"selected must be [{T}, {pool.num_kv_heads}, blocks]")
-    hq = q.shape[1]
+    hq = _heads_of(q)
     if _rows_of(q, pool, "q", (T, hq, pool.head_dim)) != hq * pool.head_dim:
         raise ValueError("q must be contiguous")
     return (bt, mb, offs, B, seq, pos, T), hq, sel, k
