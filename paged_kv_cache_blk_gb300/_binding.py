@@ -152,9 +152,17 @@ def _ptr(t: Optional[torch.Tensor]) -> Optional[int]:
     return None if t is None else t.data_ptr()
 
 
+# The handle alone, where torch offers it: torch.cuda.current_stream
+# builds a Stream object around it.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream(dev: torch.device) -> int:
-    # the handle alone: torch.cuda.current_stream builds a Stream object around it
-    return torch._C._cuda_getCurrentRawStream(dev.index)
+    if dev.index is None:
+        raise ValueError(f"the pool is on {dev}, not on a CUDA device")
+    if _raw_stream is None:
+        return torch.cuda.current_stream(dev).cuda_stream
+    return _raw_stream(dev.index)
 
 
 def int8_row_bytes(num_kv_heads: int, head_dim: int) -> int:

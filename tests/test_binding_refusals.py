@@ -60,3 +60,36 @@ def test_index_tensors_of_another_rank(bad):
         pkv.rope_append(pool, 0, pkv.Rope(64), bt, None, seq, i(3), q, k, k, torch.zeros(3, 4, 64))
     with pytest.raises(ValueError):
         pkv.update_block_bounds(pool, 0, bounds, bt, i(2, 1) if bad == "token_seq" else i(2), None)
+
+
+# ---- the current stream ---------------------------------------------------------------
+
+def test_a_pool_in_host_memory_has_no_stream():
+    pool, bounds, i = _host_args()
+    with pytest.raises(ValueError):
+        pkv.update_block_bounds(pool, 0, bounds, i(2, 4), i(2), None)
+
+
+def test_the_stream_without_torchs_short_cut(monkeypatch):
+    """A torch that has no call for the handle alone: the documented one is used."""
+    from paged_kv_cache_blk_gb300 import _binding as B
+
+    class Stream:
+        cuda_stream = 1234
+
+    seen = []
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda d: seen.append(d) or Stream())
+    monkeypatch.setattr(B, "_raw_stream", None)
+    dev = torch.device("cuda", 0)
+    assert B._stream(dev) == 1234 and seen == [dev]
+
+
+def test_import_without_torchs_short_cut():
+    import subprocess
+    import sys
+    code = ("import torch\n"
+            "if hasattr(torch._C, '_cuda_getCurrentRawStream'):\n"
+            "    del torch._C._cuda_getCurrentRawStream\n"
+            "from paged_kv_cache_blk_gb300 import _binding as B\n"
+            "assert B._raw_stream is None\n")
+    assert subprocess.run([sys.executable, "-c", code]).returncode == 0
