@@ -695,13 +695,15 @@ struct FmaState {
 template <int MODE, int D, int HEADS>
 struct Layout {
   using Tl = Tile<MODE, D>;
-  // Tiles of a warp's ring; the warps of a CTA are chosen at the launch.  64
-  // sequences of 2048 selected tokens, Hkv 8, D 128, 4 warps a CTA: bf16 with 3 tiles
-  // 83 us, with 2 98, with 5 102; int8, 8 warps, with 2 68.6, with 3 71.4.
-  static constexpr int kStages = MODE == PKV_F32    ? 2
-                                 : MODE == PKV_BF16 ? (D == 128 ? 3 : 5)
-                                 : HEADS <= 8       ? (D == 128 ? 2 : 3)
-                                                    : (D == 128 ? 5 : 8);
+  // Tiles of a warp's ring: three; two where a tile is large (fp32) or its work long
+  // beside its bytes (int8, D 128).  Times over those of the best count from 2 to 8 of
+  // each of 11 batches (1 to 128 sequences, 40 to 300 blocks of 16; geometric means):
+  // bf16, D 64, G 2 to 16: with 3 1.02-1.06, with 2 1.07-1.10, 4 1.03-1.09, 5 1.05-1.14;
+  // int8, D 64, G 4 to 16: 3 1.02-1.04, 2 1.03-1.04, 4 1.04-1.06, 8 1.14-1.19; int8,
+  // D 128, G 12 and 16: 2 1.01, 3 1.01-1.02, 5 1.04.  64 sequences x 2048 tokens, G 4,
+  // D 128: bf16 with 3 81.8 us, 2 82.5, 4 88.3; int8 2 64.4, 3 70.0, 5 67.5; fp32, 32
+  // sequences, 2 84.9, 3 90.6.
+  static constexpr int kStages = MODE == PKV_F32 || (MODE == PKV_I8 && D == 128) ? 2 : 3;
   static constexpr int kRing = kStages * Tl::kBytes;
   static constexpr int kState = HEADS * D * 4 + HEADS * 8;  // of the merge; over the ring
   static constexpr int kBody = (kRing > kState ? kRing : kState);
@@ -919,8 +921,9 @@ __global__ void __launch_bounds__(Layout<MODE, D, HEADS>::kWarps * 32)
 // for each of its CTAs.  The pair with the least
 //     rounds * (tiles of a warp + 1/2 + 2 + S / 4) * (12 + L)
 // is taken, clusters where one round is enough and with two tiles or more a warp.
-// Of 50 cases of all types timed with every pair, it is within 13 % of the best
-// in all and within 5 % in 47.  R rows of K blocks of 16, D 128, G 4, by W x S:
+// Of 50 cases of all types timed with every pair, it is within 5 % of the best in
+// 45 and within 14 % in 48; 80 rows of 100 blocks, D 64, G 16, take 18 % (int8) and 27 %
+// (bf16) more than with 6 x 3.  R rows of K blocks of 16, D 128, G 4, by W x S:
 // fp32, R 264, K 60 3 x 1 45.6 us, 4 x 1 52.1, 2 x 1 57.7; R 160, K 100 1 x 5 48.1,
 // 3 x 1 64.1, 4 x 1 76.9; bf16, R 512, K 128 2 x 1 83.0, 4 x 1 84.5, 8 x 1 92.2,
 // 3 x 1 107; R 40, K 100 8 x 3 10.6, 4 x 3 11.4, 3 x 7 12.5; R 16, K 300 8 x 6 14.4,

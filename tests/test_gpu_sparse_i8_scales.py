@@ -98,7 +98,7 @@ def test_a_large_value_scale_of_a_low_scoring_row(dev, D, H, G, bs, where, bits)
     pool.k_cache[blk, w.layer, row, :H * D] = 1           # codes -127 against positive queries:
     _scales(pool.k_cache, spec)[blk, w.layer, row] = 0.25  # its logits are the lowest by far
     _scales(pool.v_cache, spec)[blk, w.layer, row] *= 2.0 ** bits
-    sel = np.broadcast_to(np.arange(nb, dtype=np.int32), (1, H, nb))
+    sel = np.tile(np.arange(nb, dtype=np.int32), (1, H, 1))
     out = torch.empty_like(q)
     bt, _, offs, _ = dev_batch(w.batch, dev)
     scale = D ** -0.5
