@@ -206,8 +206,9 @@ typedef enum {
 PKV_API pkv_status pkv_rope_init(pkv_rope* rope, int32_t rotary_dim, int32_t interleaved,
                                  double base, int32_t scaling, double factor,
                                  double original_len, double turns_fast, double turns_slow);
-/* Any other schedule: inv_freq (host, rotary_dim / 2 values) in radians per
- * token, and the factor on cos and sin. */
+/* Any other schedule, such as the ramp of BY_PARTS with another factor on cos
+ * and sin: inv_freq (host, rotary_dim / 2 values) in radians per token, and that
+ * factor. */
 PKV_API pkv_status pkv_rope_init_freqs(pkv_rope* rope, int32_t rotary_dim, int32_t interleaved,
                                        const double* inv_freq, double attn_scale);
 
@@ -394,7 +395,8 @@ PKV_API pkv_status pkv_decode_attention_shared_prefix(const pkv_pool* pool, int3
  * hi ~ code * scale rounded up, lo rounded down (the bound still holds), with
  * scale = 2^e, e the smallest exponent in [-40, 40] with absmax <= 127 * 2^e
  * (larger elements keep the outermost code).  An infinite element or a NaN
- * gets the outermost code of its side, a NaN of both.
+ * gets the outermost code of its side, a NaN of both.  The elements of PKV_I8 pools
+ * are their codes times scales as fp32 rounds the products.
  *
  * pkv_update_block_bounds recomputes, for every sequence b, the bounds of the
  * blocks that hold its positions first_pos[b] .. seq_lens[b] - 1 (first_pos
@@ -430,8 +432,10 @@ PKV_API pkv_status pkv_update_block_bounds(const pkv_pool* pool, int32_t layer,
  * selected: int32 [num_tokens, Hkv, num_selected], the selected entries of the
  * sequence's table row in ascending order, -1 behind them; selected_count:
  * int32 [num_tokens, Hkv], their number (0 for padding and for tokens out of
- * range, which set the device error word; an entry with an invalid block id
- * sets it too, is not read, and scores lowest).
+ * range, which set the device error word; a scored entry with an invalid block
+ * id sets it too, is not read, and scores lowest.  Entries that are taken without
+ * a score, the forced ones and all of a query's num_selected or fewer, are not
+ * looked up).
  * q: [num_tokens, num_q_heads, head_dim], contiguous, in the type that
  * pkv_decode_attention takes; the pool's tensors are not read (k_cache and
  * v_cache may be NULL).  Supported: head_dim 64 or 128; up to 16 query heads

@@ -13,10 +13,11 @@
 // store the same bytes.
 //
 // What bounds it: the keys' bytes for bf16 and fp32 pools (73K prompt tokens, Hkv
-// 8, D 128: 29.3 us, 5.6 TB/s; fp32 43.9 us, 6.1 TB/s); for int8 the five
-// instructions a code (38.7 us).  Four heads a warp, without the merge, took 29.4
-// us in bf16 but 28.6 us instead of 6.1 for the last blocks of 20 sequences in
-// int8.
+// 8, D 128: 29.2 us, 5.7 TB/s; fp32 43.5 us, 6.1 TB/s).  int8 (38.9 us, 1.9 TB/s): 25 M
+// instructions, 20 us at full issue, most of them (permutes, maxima, minima) on the
+// ALU pipe, 66 % of its cycles busy, at 14 warps an SM (104 registers allow 16).  Four
+// heads a warp, without the merge, took 29.4 us in bf16 but 28.6 us instead of 6.1
+// for the last blocks of 20 sequences in int8.
 #include "bounds.cuh"
 #include "common.cuh"
 #include "slots.cuh"
@@ -207,8 +208,12 @@ __global__ void __launch_bounds__(kBoundThreads) update_bounds_kernel(const Boun
 
 template <int MODE>
 cudaError_t launch_bounds_mode(BoundParams& p, int d, int batch, int sms, cudaStream_t s) {
-  // Enough CTAs to fill the SMs over the batch (48 warps each), none that the
-  // longest possible table would leave idle.
+  // 12 CTAs an SM over the batch, two to three times what it holds at once (4 of 104
+  // registers for int8, 5 of 96 for bf16, D 128), so that the CTAs of long sequences
+  // find room behind those of short ones; none that the longest possible table
+  // would leave idle.  Prompts of 512 to 4096 tokens, 32 sequences: with 5 34.5 us, with
+  // 10 30.1, 12 29.2, 20 28.6 (int8 47.8, 39.9, 38.9, 37.2); their last blocks alone, bs 16
+  // (int8): 3.6, 4.4, 4.7, 5.9.
   const long long warps = kBoundThreads / 32;
   long long ctas = ((long long)p.mb * p.hkv + warps - 1) / warps;
   const long long want = (12ll * sms + batch - 1) / batch;

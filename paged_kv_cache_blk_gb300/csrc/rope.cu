@@ -24,8 +24,11 @@
 // angles of the token are spread over the 32 lanes, once per task, and handed
 // out by shuffles.
 //
-// What bounds it: many tokens, the bytes of q, k and v, read and written
-// once; few, latency (the chain sequence - offset - table entry - store).
+// What bounds it: many tokens, the bytes of q, k and v, read and written once
+// (8192 entries, Hq 32, Hkv 8, D 128, bf16: 30.8 us, 0.87 of the copy rate); into
+// int8 pools, instructions and the latency of absmax chains at 20 warps an SM (6000
+// tokens: 35.9 us, 18.4 M instructions, 14.6 us at full issue; 49 % of the slots used); few
+// tokens, latency (the chain sequence - offset - table entry - store: 2.6 us).
 #include <cmath>
 #include <cstring>
 #include <type_traits>

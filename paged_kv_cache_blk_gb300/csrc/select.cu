@@ -27,11 +27,12 @@
 // that stays larger is counted again 8 bits finer, down to equal scores, of
 // which the lowest entries are taken.
 //
-// What bounds it: with few rows, latency (a chain of four loads, three cluster
-// barriers, eight block barriers); with many, the instructions of a tile, about
-// 200 for 4 KB, and of the cut: 14.9 us for 128 of 8192 blocks of one query (Hkv 8,
-// D 128, G 4), 16.8 us for 64 of 64 to 513 blocks of 64 queries, 42 MB of bounds.
-// (Scores to a workspace, and the cut in a second launch, took 18 and 23 us.)
+// What bounds it: latency.  One query: a chain of four loads, then with one count
+// four cluster barriers and nine block barriers, eleven where scores are ranked:
+// 14.9 us for 128 of 8192 blocks (Hkv 8, D 128, G 4), of which the instructions, 2.4 M
+// on 64 SMs, are 4.5.  64 queries, 64 of 64 to 513 blocks each, 42 MB of bounds: 16.8 us,
+// 4.5 of them instructions at full issue (5.6 M, 34 % of the slots used, 4.4 warps an
+// SMSP).  (Scores to a workspace, and the cut in a second launch, took 18 and 23 us.)
 #include <climits>
 #include <cmath>
 
