@@ -225,8 +225,6 @@ cudaError_t launch_bounds_mode(BoundParams& p, int d, int batch, int sms, cudaSt
   return launch_kernel(update_bounds_kernel<MODE, 128>, grid, dim3(kBoundThreads), 0, s, true, p);
 }
 
-bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
-
 }  // namespace
 }  // namespace pkv
 

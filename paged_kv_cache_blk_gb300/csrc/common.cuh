@@ -281,6 +281,10 @@ __device__ __forceinline__ void st_global(void* p, const uint4& v) {
 // ---- internal launch interface (host side, C++ linkage) ---------------------
 namespace pkv {
 
+inline bool aligned(const void* p, uintptr_t a) {
+  return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0;
+}
+
 // Launch `kern` on `s`; with `pdl` as a programmatic dependent of the work
 // before it (the kernel must call griddep_wait() before reading inputs).
 template <typename... KArgs, typename... Args>

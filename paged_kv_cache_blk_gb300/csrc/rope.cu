@@ -334,8 +334,6 @@ uint64_t turn_step(double f) {
   return x >= 18446744073709551616.0 ? 0ull : (uint64_t)x;
 }
 
-bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
-
 }  // namespace
 }  // namespace pkv
 

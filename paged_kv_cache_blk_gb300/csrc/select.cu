@@ -41,6 +41,7 @@
 #include "bounds.cuh"
 #include "cluster.cuh"
 #include "common.cuh"
+#include "mma.cuh"
 
 namespace pkv {
 namespace {
@@ -86,20 +87,11 @@ struct SelectShared {
 // Code bytes b = c + 128 to the fp16 numbers with those bits, the subnormals
 // b * 2^-24: two a register, one byte permute each.  The tensor cores take
 // subnormals as they are.
-__device__ __forceinline__ void codes_to_f16(uint32_t w, uint32_t& lo, uint32_t& hi) {
+__device__ __forceinline__ void codes_as_f16(uint32_t w, uint32_t& lo, uint32_t& hi) {
   asm("prmt.b32 %0, %1, 0, 0x4140;" : "=r"(lo) : "r"(w));
   asm("prmt.b32 %0, %1, 0, 0x4342;" : "=r"(hi) : "r"(w));
 }
 constexpr float kUnit = 0x1p-24f, kBias = 128.f * kUnit;
-
-__device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
-                                        uint32_t a3, uint32_t b0, uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
-      "{%8,%9}, {%0,%1,%2,%3};"
-      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
 
 // Order-preserving map of a score to an unsigned integer in [1, 2^32 - 2].
 __device__ __forceinline__ uint32_t ordered(float x) {
@@ -142,15 +134,6 @@ __device__ __forceinline__ uint32_t cluster_sum(uint32_t addr, uint32_t n) {
 __device__ __forceinline__ uint32_t ld_u32(const void* p) {
   uint32_t v;
   asm volatile("ld.global.nc.u32 %0, [%1];" : "=r"(v) : "l"(p));
-  return v;
-}
-
-__device__ __forceinline__ uint4 lds128(uint32_t a) {
-  uint4 v;
-  asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
-               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-               : "r"(a)
-               : "memory");
   return v;
 }
 
@@ -356,15 +339,15 @@ __global__ void __launch_bounds__(THREADS, (NT == 1 ? 768 : 384) / THREADS)
           uint32_t a[2][4];
 #pragma unroll
           for (int c = 0; c < 2; ++c) {
-            codes_to_f16(half ? (c ? y0.w : y0.z) : (c ? y0.y : y0.x), a[c][0], a[c][2]);
-            codes_to_f16(half ? (c ? y1.w : y1.z) : (c ? y1.y : y1.x), a[c][1], a[c][3]);
+            codes_as_f16(half ? (c ? y0.w : y0.z) : (c ? y0.y : y0.x), a[c][0], a[c][2]);
+            codes_as_f16(half ? (c ? y1.w : y1.z) : (c ? y1.y : y1.x), a[c][1], a[c][3]);
           }
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) {
             // dims k * 64 + qi * 16 + half * 8 .. + 7 of head gl
             const uint4 b = lds128(a_q + (side * NT + nt) * 8 * QROW + k * 128 + half * 16);
-            mma_f16(acc[nt][0], a[0][0], a[0][1], a[0][2], a[0][3], b.x, b.y);
-            mma_f16(acc[nt][1], a[1][0], a[1][1], a[1][2], a[1][3], b.z, b.w);
+            mma16<true>(acc[nt][0], a[0][0], a[0][1], a[0][2], a[0][3], b.x, b.y);
+            mma16<true>(acc[nt][1], a[1][0], a[1][1], a[1][2], a[1][3], b.z, b.w);
           }
         }
 #pragma unroll
@@ -616,8 +599,6 @@ cudaError_t launch_select(SelectParams& p, unsigned rows, int dev, int sms, cuda
   return launch_clusters(kern[choice], dim3(rows * (unsigned)ctas), dim3(kThreads[NT - 1][choice]),
                          (size_t)p.cap * 4, (unsigned)ctas, s, p);
 }
-
-bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 
 }  // namespace
 }  // namespace pkv
