@@ -10,7 +10,11 @@
  *     with a split-K partial pass and a combine pass (pkv_decode_attention),
  *   - rotary positions fused with the scatter (pkv_rope_append),
  *   - sparse decode attention over the blocks that a cheap score selects
- *     (pkv_update_block_bounds, pkv_select_blocks, pkv_decode_attention_sparse).
+ *     (pkv_update_block_bounds, pkv_select_blocks, pkv_decode_attention_sparse),
+ *   - attention with a sliding window and first tokens that stay visible
+ *     (pkv_decode_attention_window, pkv_prefill_attention_window),
+ *   - verification of drafted trees of tokens (pkv_decode_attention_tree,
+ *     pkv_accept_tokens).
  *
  * Sources restated (cited by page title and section):
  *   [step14_2]  mini-vLLM tutorial "step14_2 - index_select gather"
@@ -508,6 +512,106 @@ PKV_API pkv_status pkv_prefill_attention(const pkv_pool* pool, int32_t layer, co
                                          const int32_t* seq_lens, const int32_t* offsets,
                                          const int64_t* cu_q, int32_t batch, int64_t total_q,
                                          int32_t max_q_len, void* out, cudaStream_t stream);
+
+/* Sliding windows ("vLLM PagedAttention source notes" §2.3: attention over
+ * what the block table names; a window layer sees part of it).  A query at
+ * logical position P of a sequence sees the keys i <= P with
+ *     i > P - window  or  i < sink:
+ * the window's `window` tokens, its own among them, and the first `sink`
+ * tokens of the sequence, which stay visible.  window >= 1, sink >= 0
+ * (PKV_ERR_INVALID_ARG).  Table entries whose block holds no key that a query of
+ * the call sees are not read: their blocks may have been freed and the
+ * entries may hold anything.  Rows that no query of the sequence sees are not
+ * read, and whatever they hold does not reach a result.
+ * Supported by both calls: any pool dtype; head_dim 64 or 128; any num_kv_heads;
+ * up to 16 query heads per kv head; any block_size the pool allows;
+ * max_blocks_per_seq * block_size up to 2^30; others PKV_ERR_UNSUPPORTED.
+ * Types and pool dtypes of q and out as in pkv_decode_attention.
+ *
+ * pkv_decode_attention_window: one query per sequence, its last token
+ * (P = seq_lens[b] - 1); arguments, empty sequences and errors as
+ * pkv_decode_attention, without a workspace: one launch.  Arithmetic as
+ * pkv_decode_attention_sparse. */
+PKV_API pkv_status pkv_decode_attention_window(const pkv_pool* pool, int32_t layer, const void* q,
+                                               int32_t num_q_heads, float scale,
+                                               const int32_t* block_tables,
+                                               int32_t max_blocks_per_seq,
+                                               const int32_t* seq_lens, const int32_t* offsets,
+                                               int32_t batch, int32_t window, int32_t sink,
+                                               void* out, cudaStream_t stream);
+
+/* The same for the last n_b = cu_q[b+1] - cu_q[b] tokens of each sequence (prompts,
+ * chunks after a cached context): arguments, their rules and errors as
+ * pkv_prefill_attention, with every pool dtype and block size.  out rows
+ * behind cu_q[batch], and those of skipped sequences, are not written.  No
+ * workspace. */
+PKV_API pkv_status pkv_prefill_attention_window(const pkv_pool* pool, int32_t layer, const void* q,
+                                                int32_t num_q_heads, float scale,
+                                                const int32_t* block_tables,
+                                                int32_t max_blocks_per_seq,
+                                                const int32_t* seq_lens, const int32_t* offsets,
+                                                const int64_t* cu_q, int32_t batch,
+                                                int64_t total_q, int32_t max_q_len, int32_t window,
+                                                int32_t sink, void* out, cudaStream_t stream);
+
+/* Verification of drafted tokens: the last n_b = cu_q[b+1] - cu_q[b] tokens of
+ * sequence b are drafted (their K and V already stored, e.g. by
+ * pkv_rope_append with rope_pos the positions along the tree), and all are
+ * attended for in one pass over the context of ctx = seq_lens[b] - n_b tokens.
+ * Query i of the sequence sees
+ *   - the context, or with window > 0 its keys k with
+ *     k > P - window or k < sink, P = q_pos[cu_q[b] + i] (at least ctx; NULL:
+ *     ctx + i), the query's position along its branch;
+ *   - drafted token j where bit j % 64 of
+ *     tree_mask[(cu_q[b] + i) * mask_words + j / 64] is set, j < n_b: for a
+ *     tree, the token itself and what it hangs on.  The bits alone decide
+ *     among drafted tokens; bits from n_b on are ignored.
+ * tree_mask NULL (mask_words 0, q_pos NULL): a chain; query i sees the keys up
+ * to ctx + i, under the window if there is one, as in
+ * pkv_prefill_attention_window.  window 0: no window (sink is then ignored).
+ * A query that sees nothing, or only scores of -inf, gives zeros.
+ * tree_mask: uint64 [total_q, mask_words] (device); max_q_len, which bounds
+ * every n_b, is at most 64 * mask_words (PKV_ERR_INVALID_ARG); q_pos: int32
+ * [total_q].  Other arguments, rules, errors and supported shapes as
+ * pkv_prefill_attention_window.
+ * The tiles of all sequences are split evenly over the GPU whatever their lengths;
+ * states of split parts go to `workspace`
+ * (>= pkv_decode_tree_workspace_size bytes, 16-byte aligned, contents need no
+ * initialisation; two calls that may run at once need one each) and a second
+ * kernel merges them.  0 from the size call: bad shape or no device. */
+PKV_API size_t pkv_decode_tree_workspace_size(const pkv_pool* pool, int32_t batch,
+                                              int32_t num_q_heads, int32_t max_q_len);
+PKV_API pkv_status pkv_decode_attention_tree(const pkv_pool* pool, int32_t layer, const void* q,
+                                             int32_t num_q_heads, float scale,
+                                             const int32_t* block_tables,
+                                             int32_t max_blocks_per_seq, const int32_t* seq_lens,
+                                             const int32_t* offsets, const int64_t* cu_q,
+                                             int32_t batch, int64_t total_q, int32_t max_q_len,
+                                             const uint64_t* tree_mask, int32_t mask_words,
+                                             const int32_t* q_pos, int32_t window, int32_t sink,
+                                             void* out, void* workspace, size_t workspace_bytes,
+                                             cudaStream_t stream);
+
+/* After verification: the K and V rows of the accepted drafted tokens move
+ * right behind the context, where a chain would have stored them.  With a_k =
+ * accepted[b * max_accepted + k], k < accepted_count[b], the indices of the
+ * accepted tokens among the n_b drafted ones (strictly ascending, as a path
+ * from the root of a tree whose tokens come after what they hang on), the rows
+ * of position ctx + a_k go to position ctx + k, in one layer or in every one
+ * (layer -1).  Other rows keep what they hold.  seq_lens, offsets, cu_q as
+ * the verification had them.  A sequence with n_b == 0 or accepted_count 0 is
+ * left alone; one whose numbers are out of range (PKV_ERR_CAPACITY in validate
+ * mode) or whose path does not ascend below n_b or meets an invalid block id
+ * (PKV_ERR_INDEX) moves nothing and sets the device error word.  The blocks of
+ * drafted tokens must not be shared (copy-on-write guarantees it).
+ * accepted: int32 [batch, max_accepted], accepted_count: int32 [batch],
+ * device.  Any pool.  One launch, no workspace. */
+PKV_API pkv_status pkv_accept_tokens(const pkv_pool* pool, int32_t layer,
+                                     const int32_t* block_tables, int32_t max_blocks_per_seq,
+                                     const int32_t* seq_lens, const int32_t* offsets,
+                                     const int64_t* cu_q, int32_t batch, const int32_t* accepted,
+                                     int32_t max_accepted, const int32_t* accepted_count,
+                                     cudaStream_t stream);
 
 /* Allocation-free paged decode attention.  The paper has no counterpart:
  * this is a library convenience.  Same computation, arguments, results and

@@ -74,6 +74,14 @@ _SIGS = {
                                  _I32, _I32, _I32, _P, _P, _P]),
     "pkv_decode_attention_sparse": (_I32, [_P, _I32, _P, _I32, _F32, _P, _I32, _P, _I32, _P, _P,
                                            _I32, _P, _I32, _P, _P]),
+    "pkv_decode_attention_window": (_I32, [_P, _I32, _P, _I32, _F32, _P, _I32, _P, _P, _I32, _I32,
+                                           _I32, _P, _P]),
+    "pkv_prefill_attention_window": (_I32, [_P, _I32, _P, _I32, _F32, _P, _I32, _P, _P, _P, _I32,
+                                            _I64, _I32, _I32, _I32, _P, _P]),
+    "pkv_decode_tree_workspace_size": (_SZ, [_P, _I32, _I32, _I32]),
+    "pkv_decode_attention_tree": (_I32, [_P, _I32, _P, _I32, _F32, _P, _I32, _P, _P, _P, _I32,
+                                         _I64, _I32, _P, _I32, _P, _I32, _I32, _P, _P, _SZ, _P]),
+    "pkv_accept_tokens": (_I32, [_P, _I32, _P, _I32, _P, _P, _P, _I32, _P, _I32, _P, _P]),
     "pkv_gather": (_I32, [_P, _I32, _P, _I32, _P, _P, _I32, _P, _I64, _P, _P, _P]),
     "pkv_decode_workspace_size": (_SZ, [_I32, _I32, _I32]),
     "pkv_decode_attention": (_I32, [_P, _I32, _P, _I32, _F32, _P, _I32, _P, _P, _I32, _P, _P,
@@ -592,6 +600,133 @@ def decode_attention_sparse(pool: Pool, layer: int, q: torch.Tensor, scale: floa
                                              *tokens, sel, k, out.data_ptr(),
                                              _stream(pool.device))
     _check(st, "pkv_decode_attention_sparse")
+
+
+def _sequences(pool: Pool, block_tables: torch.Tensor, seq_lens: torch.Tensor,
+               offsets: Optional[torch.Tensor], cu_q: Optional[torch.Tensor]):
+    """Checks of the tables, lengths and offsets of a batch (and of where its
+    queries lie), and their pointers and numbers."""
+    bt, lens = _index(block_tables, pool, "block_tables", 2), _index(seq_lens, pool, "seq_lens", 1)
+    offs = _index(offsets, pool, "offsets", 1)
+    B, mb = block_tables.shape
+    if seq_lens.shape[0] != B or (offsets is not None and offsets.shape[0] != B):
+        raise ValueError("seq_lens and offsets must have one entry per row of block_tables")
+    if cu_q is not None and (cu_q.dtype is not torch.int64 or cu_q.get_device() != pool.index
+                             or cu_q.shape != (B + 1,) or not cu_q.is_contiguous()):
+        raise ValueError(f"cu_q must be a contiguous int64 tensor of {B + 1} entries on "
+                         f"{pool.device}")
+    return bt, mb, lens, offs, B
+
+
+def _attended(pool: Pool, q: torch.Tensor, out: torch.Tensor, rows: Optional[int] = None) -> int:
+    """Checks of q and out ([rows, Hq, D], contiguous); the number of heads."""
+    hq = _heads_of(q)
+    shape = (q.shape[0] if rows is None else rows, hq, pool.head_dim)
+    for t, name in ((q, "q"), (out, "out")):
+        if _rows_of(t, pool, name, shape) != hq * pool.head_dim:
+            raise ValueError(f"{name} must be contiguous")
+    return hq
+
+
+def decode_attention_window(pool: Pool, layer: int, q: torch.Tensor, scale: float,
+                            block_tables: torch.Tensor, seq_lens: torch.Tensor,
+                            offsets: Optional[torch.Tensor], window: int, out: torch.Tensor,
+                            sink: int = 0) -> None:
+    """Decode attention of ``q`` ([B, Hq, D]) into ``out`` over the last
+    ``window`` tokens of each sequence and its first ``sink``."""
+    lib = load()
+    bt, mb, lens, offs, B = _sequences(pool, block_tables, seq_lens, offsets, None)
+    hq = _attended(pool, q, out, B)
+    with _dev(pool):
+        st = lib.pkv_decode_attention_window(pool.ref, layer, q.data_ptr(), hq, float(scale), bt,
+                                             mb, lens, offs, B, window, sink, out.data_ptr(),
+                                             _stream(pool.device))
+    _check(st, "pkv_decode_attention_window")
+
+
+def prefill_attention_window(pool: Pool, layer: int, q: torch.Tensor, scale: float,
+                             block_tables: torch.Tensor, seq_lens: torch.Tensor,
+                             offsets: Optional[torch.Tensor], cu_q: torch.Tensor, max_q_len: int,
+                             window: int, out: torch.Tensor, sink: int = 0) -> None:
+    """Prefill attention of ``q`` ([T, Hq, D], the last cu_q[b+1]-cu_q[b] tokens
+    of each sequence) into ``out``, each token over the last ``window`` tokens
+    up to its own and the first ``sink``."""
+    lib = load()
+    bt, mb, lens, offs, B = _sequences(pool, block_tables, seq_lens, offsets, cu_q)
+    hq = _attended(pool, q, out)
+    with _dev(pool):
+        st = lib.pkv_prefill_attention_window(pool.ref, layer, q.data_ptr(), hq, float(scale), bt,
+                                              mb, lens, offs, cu_q.data_ptr(), B, q.shape[0],
+                                              max_q_len, window, sink, out.data_ptr(),
+                                              _stream(pool.device))
+    _check(st, "pkv_prefill_attention_window")
+
+
+def decode_tree_workspace_size(pool: Pool, batch: int, num_q_heads: int, max_q_len: int) -> int:
+    with _dev(pool):
+        n = int(load().pkv_decode_tree_workspace_size(pool.ref, batch, num_q_heads, max_q_len))
+    if n == 0:
+        raise PkvError(1, "pkv_decode_tree_workspace_size", "bad shape or no CUDA device")
+    return n
+
+
+def decode_attention_tree(pool: Pool, layer: int, q: torch.Tensor, scale: float,
+                          block_tables: torch.Tensor, seq_lens: torch.Tensor,
+                          offsets: Optional[torch.Tensor], cu_q: torch.Tensor, max_q_len: int,
+                          tree_mask: Optional[torch.Tensor], out: torch.Tensor,
+                          workspace: torch.Tensor, q_pos: Optional[torch.Tensor] = None,
+                          window: int = 0, sink: int = 0) -> None:
+    """Attention of the drafted tokens ``q`` ([T, Hq, D], the last
+    cu_q[b+1]-cu_q[b] tokens of each sequence, at most ``max_q_len``) into
+    ``out``: over their context and, by the bits of ``tree_mask`` (int64 [T,
+    words], bit j of a row: sees drafted token j; None: a chain), over one
+    another.  ``window`` (0: none) and ``sink`` limit the context around
+    ``q_pos`` (int32 [T], positions along the tree)."""
+    lib = load()
+    bt, mb, lens, offs, B = _sequences(pool, block_tables, seq_lens, offsets, cu_q)
+    hq = _attended(pool, q, out)
+    T, words, mask = q.shape[0], 0, None
+    if tree_mask is not None:
+        if tree_mask.dtype is not torch.int64 or tree_mask.get_device() != pool.index \
+                or tree_mask.dim() != 2 or tree_mask.shape[0] != T \
+                or not tree_mask.is_contiguous():
+            raise ValueError(f"tree_mask must be a contiguous int64 tensor [{T}, words] on "
+                             f"{pool.device}")
+        words, mask = tree_mask.shape[1], tree_mask.data_ptr()
+        if words == 0:
+            raise ValueError("tree_mask must have a word per 64 drafted tokens")
+    qp = _index(q_pos, pool, "q_pos", 1)
+    if q_pos is not None and (tree_mask is None or q_pos.shape[0] != T):
+        raise ValueError("q_pos goes with tree_mask and has one entry per token")
+    if T == 0:  # (tensors of no elements have no address)
+        words, mask, qp = 0, None, None
+    if workspace.get_device() != pool.index or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be a contiguous tensor on {pool.device}")
+    with _dev(pool):
+        st = lib.pkv_decode_attention_tree(pool.ref, layer, q.data_ptr(), hq, float(scale), bt, mb,
+                                           lens, offs, cu_q.data_ptr(), B, T, max_q_len, mask,
+                                           words, qp, window, sink, out.data_ptr(),
+                                           workspace.data_ptr(),
+                                           workspace.numel() * workspace.element_size(),
+                                           _stream(pool.device))
+    _check(st, "pkv_decode_attention_tree")
+
+
+def accept_tokens(pool: Pool, layer: int, block_tables: torch.Tensor, seq_lens: torch.Tensor,
+                  offsets: Optional[torch.Tensor], cu_q: torch.Tensor, accepted: torch.Tensor,
+                  count: torch.Tensor) -> None:
+    """Move the K and V rows of the accepted drafted tokens right behind the
+    context: ``accepted`` (int32 [B, most]) holds the ``count`` (int32 [B])
+    ascending indices of each sequence; one layer or every one (-1)."""
+    lib = load()
+    bt, mb, lens, offs, B = _sequences(pool, block_tables, seq_lens, offsets, cu_q)
+    path, cnt = _index(accepted, pool, "accepted", 2), _index(count, pool, "count", 1)
+    if accepted.shape[0] != B or count.shape[0] != B:
+        raise ValueError("accepted and count must have one entry per row of block_tables")
+    with _dev(pool):
+        st = lib.pkv_accept_tokens(pool.ref, layer, bt, mb, lens, offs, cu_q.data_ptr(), B, path,
+                                   accepted.shape[1], cnt, _stream(pool.device))
+    _check(st, "pkv_accept_tokens")
 
 
 def copy_blocks(pool: Pool, layer: int, src_blocks: torch.Tensor,

@@ -1,5 +1,5 @@
-// The warp-level product and the shared-memory read of its operands that the block
-// selection and the sparse decode share (select.cu, sparse_decode.cu).
+// Warp-level products, the copies into shared memory and the reads of operands from it that
+// kernels share (select.cu, sparse_decode.cu, rows.cuh).
 #pragma once
 
 #include <cstdint>
@@ -33,6 +33,56 @@ __device__ __forceinline__ uint4 lds128(uint32_t a) {
                : "r"(a)
                : "memory");
   return v;
+}
+
+// 16 bytes to shared memory, zeros where not live (nothing is read then).
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool live) {
+  const int n = live ? 16 : 0;
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n)
+               : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+__device__ __forceinline__ void ldsm_x4(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ void ldsm_x4_t(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+// Lane l receives bytes of column l / 4 (r0) and l / 4 + 8 (r1), rows
+// 4 (l % 4) .. + 3, of the 16 x 16 byte matrix whose rows lanes 0-15 address.
+__device__ __forceinline__ void ldsm_b8_t(uint32_t& r0, uint32_t& r1, uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m16n16.x1.trans.shared.b8 {%0,%1}, [%2];"
+               : "=r"(r0), "=r"(r1)
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ float lds_f32(uint32_t a) {
+  float v;
+  asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(a) : "memory");
+  return v;
+}
+__device__ __forceinline__ void sts_f32(uint32_t a, float v) {
+  asm volatile("st.shared.f32 [%0], %1;" ::"r"(a), "f"(v) : "memory");
+}
+// The largest bf16 below each weight (0 for 0): what is left is positive, so
+// both parts of a weight give an infinite V its own sign, and neither a NaN.
+__device__ __forceinline__ uint32_t below_bf16x2(float lo, float hi) {
+  uint32_t r;
+  asm("prmt.b32 %0, %1, %2, 0x7632;"
+      : "=r"(r)
+      : "r"(max(__float_as_uint(lo), 1u) - 1u), "r"(max(__float_as_uint(hi), 1u) - 1u));
+  return r;
 }
 
 }  // namespace pkv

@@ -1,0 +1,696 @@
+// Attention of several query rows a kv head over one stream of its keys, on mma.sync:
+// the general form of pkv_decode_attention_tree and pkv_prefill_attention_window, for
+// every pool type, head_dim 64 and 128, any group of heads and block size (prefill.cu
+// holds the tcgen05 form for bf16 pools of head_dim 128).
+//
+// What is computed.  The rows of a unit are (new token, query head of kv head g) pairs
+// of one sequence, M = 16 WR of them (WR 1, 2 or 4).  Softmax attention over the keys
+// that each row sees (span.cuh: a window, first tokens, a mask among the new tokens), K
+// and V read in place through the block table.
+//
+// How.  A CTA of 4 warps streams the unit's tiles of KT keys through a ring of cp.async
+// stages; rows that no query of the unit sees arrive as zeros, and are not read.  WR
+// warps share out the rows and WK = 4 / WR the keys of each tile, so few rows cost few
+// products (16 rows: every warp takes a quarter of the keys).  Each warp holds Q in
+// registers and a running softmax (maximum, sum, O) of its 16 rows over its keys; the WK
+// states of a row are merged in shared memory at the end.
+//   bf16: S = Q K^T and O += P V on mma m16n8k16.  A weight enters P V as two bf16 parts,
+//     within 2^-16 of it together (one part alone would be the largest error of the result).
+//   int8: the same: codes are whole numbers up to 127, exact in bf16, K's scales are
+//     factors of the scores and V's of the weights.  The tile's keys are taken in the
+//     order that makes the byte-transposing V load agree with the scores' registers.
+//   fp32: mma m16n8k8 on tf32 in three products: x = hi + lo, each the nearest tf32, and
+//     x y ~ hi hi + hi lo + lo hi, within 2^-21 of it.  The tensor cores add with
+//     truncation, so the small products come first, and O is not their accumulator: each
+//     tile's P V is summed from zero and added to O with rounding.
+#pragma once
+
+#include <climits>
+#include <cmath>
+
+#include "cluster.cuh"
+#include "common.cuh"
+#include "mma.cuh"
+#include "span.cuh"
+
+namespace pkv {
+
+struct RowsParams {
+  PlanParams plan;
+  const char* k;
+  const char* v;
+  const char* q;
+  char* out;
+  const int32_t* bt;
+  const int32_t* q_pos;          // tree: positions of the queries, or NULL
+  const unsigned long long* mask;  // tree: [total_q, words], or NULL (each token sees those before it)
+  int words;
+  int* err;
+  float* part;  // states of split units
+  long long num_blocks;
+  int L, layer, row_bytes, scale_off, hq, bs_bits;
+  int units_max;  // prefill: units of one kv head of the longest sequence
+  float qscale;   // scale * log2(e)
+};
+
+constexpr int kRowsWarps = 4;
+constexpr int kRowsThreads = kRowsWarps * 32;
+
+namespace {
+
+constexpr unsigned kAllLanes = 0xffffffffu;
+
+__device__ __forceinline__ uint32_t tf32_of(float x) {
+  uint32_t r;
+  asm("cvt.rna.tf32.f32 %0, %1;" : "=r"(r) : "f"(x));
+  return r;
+}
+__device__ __forceinline__ void split_tf32(float x, uint32_t& hi, uint32_t& lo) {
+  hi = tf32_of(x);
+  lo = tf32_of(x - __uint_as_float(hi));
+}
+// d += a b: 16 x 8 x 8
+__device__ __forceinline__ void mma8_tf32(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
+                                          uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+      "{%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+// Four codes (bytes c + 128) to bf16 pairs.  The low 7 bits of a byte behind 0x43 are
+// 128 + them; the byte's top bit says whether 128 or 256 is to be taken off.
+__device__ __forceinline__ uint32_t codes_pair_bf16(uint32_t spread) {
+  const uint32_t x = spread & 0xFF7FFF7Fu, y = (~spread & 0x00800080u) | 0x43004300u;
+  const __nv_bfloat162 d = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&x),
+                                   *reinterpret_cast<const __nv_bfloat162*>(&y));
+  return *reinterpret_cast<const uint32_t*>(&d);
+}
+__device__ __forceinline__ void codes_to_bf16(uint32_t w, uint32_t& lo, uint32_t& hi) {
+  uint32_t a, b;
+  asm("prmt.b32 %0, %1, 0x43434343, 0x4140;" : "=r"(a) : "r"(w));
+  asm("prmt.b32 %0, %1, 0x43434343, 0x4342;" : "=r"(b) : "r"(w));
+  lo = codes_pair_bf16(a);
+  hi = codes_pair_bf16(b);
+}
+
+template <int MODE, int D>
+struct RowsTile {
+  static constexpr int kEs = MODE == PKV_F32 ? 4 : MODE == PKV_BF16 ? 2 : 1;
+  static constexpr int kKeys = MODE == PKV_F32 ? 32 : 64;
+  static constexpr int kRow = D * kEs;
+  static constexpr int kChunks = kRow / 16;
+  static constexpr int kHalf = kKeys * kRow;
+  static constexpr int kBytes = 2 * kHalf + (MODE == PKV_I8 ? 2 * kKeys * 16 : 0);
+  static constexpr int kStages = kBytes > 16384 ? 3 : 4;
+  // Byte offset of chunk c of row r, permuted so that each 8-lane phase of the reads
+  // falls in 8 different 16-byte columns.
+  static __device__ __forceinline__ int at(int r, int c) {
+    if constexpr (MODE == PKV_I8) {
+      if constexpr (D == 64) return r * kRow + ((c ^ ((r >> 1) & 3)) << 4);
+      return r * kRow + ((c ^ (((r & 1) << 2) | ((r >> 1) & 3))) << 4);
+    } else if constexpr (MODE == PKV_F32) {
+      return r * kRow + ((c ^ (((r & 6)) ^ ((r & 1) << 2))) << 4);
+    }
+    return r * kRow + ((c ^ (r & 7)) << 4);
+  }
+};
+
+template <int MODE, int D, int WR>
+struct RowsLayout {
+  using Tl = RowsTile<MODE, D>;
+  static constexpr int kRing = Tl::kStages * Tl::kBytes;
+  static constexpr int kAccRow = D + 4;  // floats between rows of a merged state
+  static constexpr int kMerge = kRowsWarps * 16 * (kAccRow + 2) * 4;
+  static constexpr int kSmem = kRing > kMerge ? kRing : kMerge;
+};
+
+// One unit's work: rows first_row .. of sequence b, kv head g, tiles t0 .. t1 of its list.
+struct RowsPiece {
+  SeqSpan s;
+  TileList t;
+  int b, g, first_row, t0, t1;
+  int lo, hi;    // keys that some row of the unit may see: lo .. hi, and the first ones
+  float* part;   // where the state goes, or NULL: finished here
+};
+
+template <int MODE, int D, int WR, bool TREE>
+__device__ __forceinline__ void rows_piece(const RowsParams& p, const RowsPiece& w,
+                                           unsigned char* smem) {
+  using Tl = RowsTile<MODE, D>;
+  using Lay = RowsLayout<MODE, D, WR>;
+  constexpr bool kI8 = MODE == PKV_I8, kF32 = MODE == PKV_F32;
+  constexpr int WK = kRowsWarps / WR, KT = Tl::kKeys, KW = KT / WK, NT = KW / 8;
+  constexpr int NST = Tl::kStages, M = 16 * WR, NO = D / 8;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int wr = warp % WR, wk = warp / WR;
+  const int gl = lane >> 2, qi = lane & 3;
+  const int G = p.plan.G, n = w.s.n, rows = n * G, off = w.s.off;
+  const uint32_t base = smem_addr(smem);
+
+  // ---- copies: each warp a quarter of a tile's rows ----
+  constexpr int RW = KT / kRowsWarps;
+  const int sink_end = off + p.plan.span.sink;
+  const int my_r = warp * RW + lane % RW;  // the row of a tile that this lane looks up
+  const int32_t* table = p.bt + (long long)w.b * p.plan.span.mb;
+  auto seen_by_some = [&](int pos) {
+    return pos >= off && pos <= off + w.hi && (pos >= off + w.lo || pos < sink_end);
+  };
+  auto lookup = [&](int i) -> int {  // block of the lane's row in tile i, INT_MIN: a row of zeros
+    if (i >= w.t1) return INT_MIN;
+    const int pos = w.t.tile(i) * KT + my_r;
+    return seen_by_some(pos) ? table[pos >> p.bs_bits] : INT_MIN;
+  };
+  int ahead = lookup(w.t0);
+  auto issue = [&](int i, int stage) {
+    if (i < w.t1) {
+      const int pos = w.t.tile(i) * KT + my_r;
+      int blk = ahead;
+      if (blk != INT_MIN && (blk < 0 || blk >= p.num_blocks)) {
+        set_error(p.err, kErrIndex);
+        blk = INT_MIN;
+      }
+      const unsigned live = __ballot_sync(kAllLanes, blk != INT_MIN);
+      const long long at =
+          blk == INT_MIN ? 0
+                         : ((((long long)blk * p.L + p.layer) << p.bs_bits) +
+                            (pos & ((1 << p.bs_bits) - 1))) * p.row_bytes;
+      ahead = lookup(i + 1);
+      const uint32_t dst = base + stage * Tl::kBytes;
+      constexpr int C = Tl::kChunks;
+#pragma unroll
+      for (int u = 0; u < RW * C / 32; ++u) {
+        const int e = u * 32 + lane, r = e / C, c = e % C;
+        const long long src = __shfl_sync(kAllLanes, at, r) + w.g * Tl::kRow + c * 16;
+        const bool on = live >> r & 1;
+        const uint32_t d = dst + Tl::at(warp * RW + r, c);
+        cp_async16(d, p.k + (on ? src : 0), on);
+        cp_async16(d + Tl::kHalf, p.v + (on ? src : 0), on);
+      }
+      if constexpr (kI8) {
+        // the 16 bytes that hold the head's scale: lanes 0-15 of K, the others of V
+        const bool on = live >> lane & 1;
+        const long long src = on ? at + p.scale_off + (4 * w.g & ~15) : 0;
+        cp_async16(dst + 2 * Tl::kHalf + (lane / RW * KT + my_r) * 16,
+                   (lane < RW ? p.k : p.v) + src, on);
+      }
+    }
+    cp_commit();
+  };
+
+  // ---- the warp's rows: row 0 is gl, row 1 is gl + 8 of its 16 ----
+  // a row sees table positions off .. top that are lo or later or first tokens, and, in a
+  // masked tree, of the positions behind top those with their bit
+  int lo[2], top[2];
+  const unsigned long long* bits[2];
+  bool live_row[2];
+  long long qrow[2];
+  const bool masked_tree = TREE && p.mask != nullptr;
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int r = w.first_row + wr * 16 + gl + 8 * i;
+    live_row[i] = r < rows;
+    const int tok = live_row[i] ? r / G : 0, h = live_row[i] ? r - tok * G : 0;
+    qrow[i] = (w.s.q0 + tok) * p.hq + w.g * G + h;
+    int pos = w.s.ctx + tok;
+    top[i] = off + (masked_tree ? w.s.ctx - 1 : pos);
+    bits[i] = masked_tree ? p.mask + (w.s.q0 + tok) * p.words : nullptr;
+    lo[i] = 0;
+    if (p.plan.span.window > 0) {
+      if (TREE && p.q_pos) pos = max(w.s.ctx, p.q_pos[w.s.q0 + tok]);
+      const long long first = (long long)pos - p.plan.span.window + 1;
+      lo[i] = off + (int)max(0ll, min(first, (long long)kMaxPositions - 2048));
+    }
+  }
+  auto sees = [&](int i, int pos) -> bool {
+    if (pos <= top[i]) return pos >= off && (pos >= lo[i] || pos < sink_end);
+    if (!TREE || bits[i] == nullptr) return false;
+    const int d = pos - top[i] - 1;
+    return d < n && (bits[i][d >> 6] >> (d & 63) & 1);
+  };
+  // keys from full_lo to full_hi are seen by every row of the warp
+  int full_lo = max(live_row[0] ? lo[0] : 0, live_row[1] ? lo[1] : 0);
+  int full_hi = min(live_row[0] ? top[0] : INT_MAX, live_row[1] ? top[1] : INT_MAX);
+  full_lo = max(off, __reduce_max_sync(kAllLanes, full_lo));
+  full_hi = __reduce_min_sync(kAllLanes, full_hi);
+
+  // Q in the registers of the A operand
+  constexpr int KS = kF32 ? D / 8 : D / 16;
+  uint32_t qa[KS][4];
+  {
+    const char* src[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) src[i] = p.q + qrow[i] * (D * (kF32 ? 4 : 2));
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      if constexpr (MODE == PKV_BF16) {
+#pragma unroll
+        for (int k = 0; k < KS; ++k) {
+          const char* x = src[i] + (k * 16 + 2 * qi) * 2;
+          qa[k][i] = live_row[i] ? *reinterpret_cast<const uint32_t*>(x) : 0u;
+          qa[k][2 + i] = live_row[i] ? *reinterpret_cast<const uint32_t*>(x + 16) : 0u;
+        }
+      } else if constexpr (kI8) {
+        // step 4 i + j: dims 64 i + 16 qi + 4 j .. + 3, the order of the K codes
+#pragma unroll
+        for (int k = 0; k < KS; ++k) {
+          const char* x = src[i] + ((k >> 2) * 64 + 16 * qi + 4 * (k & 3)) * 2;
+          const uint2 y = live_row[i] ? *reinterpret_cast<const uint2*>(x) : make_uint2(0u, 0u);
+          qa[k][i] = y.x;
+          qa[k][2 + i] = y.y;
+        }
+      } else {
+        // steps 2 i, 2 i + 1: dims 16 i + 4 qi .. + 3
+#pragma unroll
+        for (int k = 0; k < KS; k += 2) {
+          const char* x = src[i] + (k * 8 + 4 * qi) * 4;
+          const uint4 y = live_row[i] ? *reinterpret_cast<const uint4*>(x)
+                                      : make_uint4(0u, 0u, 0u, 0u);
+          qa[k][i] = y.x;
+          qa[k][2 + i] = y.y;
+          qa[k + 1][i] = y.z;
+          qa[k + 1][2 + i] = y.w;
+        }
+      }
+    }
+  }
+
+  float o[NO][4], m[2], l[2];
+#pragma unroll
+  for (int k = 0; k < NO; ++k)
+#pragma unroll
+    for (int c = 0; c < 4; ++c) o[k][c] = 0.f;
+  m[0] = m[1] = -INFINITY;
+  l[0] = l[1] = 0.f;
+
+#pragma unroll 1
+  for (int s = 0; s < NST - 1; ++s) issue(w.t0 + s, s);
+  int stage = 0;
+#pragma unroll 1
+  for (int i = w.t0; i < w.t1; ++i) {
+    cp_wait<NST - 2>();
+    __syncthreads();
+    issue(i + NST - 1, stage == 0 ? NST - 1 : stage - 1);
+    const uint32_t st = base + stage * Tl::kBytes, sv = st + Tl::kHalf;
+    if (++stage == NST) stage = 0;
+    const int k0 = wk * KW;  // the warp's keys of the tile
+
+    // ---- scores ----
+    float s[NT][4];
+#pragma unroll
+    for (int j = 0; j < NT; ++j)
+#pragma unroll
+      for (int c = 0; c < 4; ++c) s[j][c] = 0.f;
+    if constexpr (MODE == PKV_BF16) {
+      const int r = k0 + (lane & 7) + ((lane >> 4) & 1) * 8, cc = (lane >> 3) & 1;
+#pragma unroll
+      for (int k = 0; k < KS; ++k)
+#pragma unroll
+        for (int j = 0; j < NT; j += 2) {
+          uint32_t b[4];
+          ldsm_x4(b, st + Tl::at(r + j * 8, 2 * k + cc));
+          mma16<false>(s[j], qa[k][0], qa[k][1], qa[k][2], qa[k][3], b[0], b[1]);
+          mma16<false>(s[j + 1], qa[k][0], qa[k][1], qa[k][2], qa[k][3], b[2], b[3]);
+        }
+    } else if constexpr (kI8) {
+      const int r = k0 + 4 * (gl >> 1) + (gl & 1);
+#pragma unroll
+      for (int j = 0; j < NT; j += 2)
+#pragma unroll
+        for (int u = 0; u < KS / 4; ++u) {
+          const uint4 x = lds128(st + Tl::at(r + j * 8, 4 * u + qi));
+          const uint4 y = lds128(st + Tl::at(r + j * 8 + 2, 4 * u + qi));
+          const uint32_t xw[4] = {x.x, x.y, x.z, x.w}, yw[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+          for (int v = 0; v < 4; ++v) {
+            uint32_t b0, b1;
+            const int k = 4 * u + v;
+            codes_to_bf16(xw[v], b0, b1);
+            mma16<false>(s[j], qa[k][0], qa[k][1], qa[k][2], qa[k][3], b0, b1);
+            codes_to_bf16(yw[v], b0, b1);
+            mma16<false>(s[j + 1], qa[k][0], qa[k][1], qa[k][2], qa[k][3], b0, b1);
+          }
+        }
+    } else {
+      float big[NT][4];
+#pragma unroll
+      for (int j = 0; j < NT; ++j)
+#pragma unroll
+        for (int c = 0; c < 4; ++c) big[j][c] = 0.f;
+#pragma unroll
+      for (int k = 0; k < KS; k += 2) {
+        uint32_t ah[2][4], al[2][4];
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+#pragma unroll
+          for (int c = 0; c < 4; ++c) split_tf32(__uint_as_float(qa[k + u][c]), ah[u][c], al[u][c]);
+#pragma unroll
+        for (int j = 0; j < NT; ++j) {
+          const uint4 x = lds128(st + Tl::at(k0 + j * 8 + gl, 2 * k + qi));
+          const uint32_t xw[4] = {x.x, x.y, x.z, x.w};
+          uint32_t bh[4], bl[4];
+#pragma unroll
+          for (int c = 0; c < 4; ++c) split_tf32(__uint_as_float(xw[c]), bh[c], bl[c]);
+#pragma unroll
+          for (int u = 0; u < 2; ++u) {
+            mma8_tf32(s[j], al[u], bh[2 * u], bh[2 * u + 1]);
+            mma8_tf32(s[j], ah[u], bl[2 * u], bl[2 * u + 1]);
+            mma8_tf32(big[j], ah[u], bh[2 * u], bh[2 * u + 1]);
+          }
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < NT; ++j)
+#pragma unroll
+        for (int c = 0; c < 4; ++c) s[j][c] += big[j][c];
+    }
+
+    // ---- softmax ----
+    // key of column c (0, 1) of score tile j, within the warp's keys
+    auto key = [&](int j, int c) {
+      if constexpr (kI8) return (j >> 1) * 16 + 4 * qi + (j & 1) * 2 + c;
+      return j * 8 + 2 * qi + c;
+    };
+    const int p0 = w.t.tile(i) * KT + k0;
+    const bool full = p0 >= full_lo && p0 + KW - 1 <= full_hi;
+    float mx[2] = {-INFINITY, -INFINITY};
+    [[maybe_unused]] float scale_v[NT][2];
+#pragma unroll
+    for (int j = 0; j < NT; ++j)
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        float f = p.qscale;
+        if constexpr (kI8) {
+          const uint32_t sc = st + 2 * Tl::kHalf + (k0 + key(j, c)) * 16 + (4 * w.g & 15);
+          f *= lds_f32(sc);
+          scale_v[j][c] = lds_f32(sc + KT * 16);
+        }
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+          float x = s[j][2 * r + c] * f;
+          if (!full) x = sees(r, p0 + key(j, c)) ? x : -INFINITY;
+          s[j][2 * r + c] = x;
+          mx[r] = fmaxf(mx[r], x);
+        }
+      }
+    float a[2];
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      a[r] = 1.f;
+      // the running maximum moves only where some lane passes it
+      if (__any_sync(kAllLanes, mx[r] > m[r])) {
+        float x = fmaxf(mx[r], __shfl_xor_sync(kAllLanes, mx[r], 1));
+        x = fmaxf(x, __shfl_xor_sync(kAllLanes, x, 2));
+        const float top_m = fmaxf(m[r], x);
+        a[r] = m[r] == -INFINITY ? 0.f : exp2f(m[r] - top_m);
+        m[r] = top_m;
+      }
+      // scores of -inf carry no weight, even while they are all there is
+      const float base_m = m[r] == -INFINITY ? 0.f : m[r];
+      float sum = 0.f;
+#pragma unroll
+      for (int j = 0; j < NT; ++j)
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          const float e = exp2f(s[j][2 * r + c] - base_m);
+          sum += e;
+          s[j][2 * r + c] = e;
+          if constexpr (kI8) s[j][2 * r + c] = e * scale_v[j][c];
+        }
+      l[r] = l[r] * a[r] + sum;
+    }
+    if constexpr (!kF32) {
+      if (__any_sync(kAllLanes, a[0] != 1.f || a[1] != 1.f)) {
+#pragma unroll
+        for (int k = 0; k < NO; ++k) {
+          o[k][0] *= a[0];
+          o[k][1] *= a[0];
+          o[k][2] *= a[1];
+          o[k][3] *= a[1];
+        }
+      }
+    }
+
+    // ---- O += P V ----
+    if constexpr (!kF32) {
+      uint32_t ph[NT / 2][4], pl[NT / 2][4];
+#pragma unroll
+      for (int j = 0; j < NT / 2; ++j)
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          const float x = s[2 * j + (c >> 1)][2 * (c & 1)], y = s[2 * j + (c >> 1)][2 * (c & 1) + 1];
+          if constexpr (kI8) {  // (infinite products: what the finite part leaves is infinite)
+            constexpr float kMost = 3.38953139e38f;
+            ph[j][c] = pack_bf16x2(fminf(fmaxf(x, -kMost), kMost), fminf(fmaxf(y, -kMost), kMost));
+          } else {
+            ph[j][c] = below_bf16x2(x, y);
+          }
+          pl[j][c] = pack_bf16x2(x - bf16_lo(ph[j][c]), y - bf16_hi(ph[j][c]));
+        }
+      if constexpr (kI8) {
+#pragma unroll
+        for (int k = 0; k < NO; k += 2)
+#pragma unroll
+          for (int j = 0; j < NT / 2; ++j) {
+            uint32_t r0, r1, b0, b1;
+            ldsm_b8_t(r0, r1, sv + Tl::at(k0 + j * 16 + (lane & 15), k / 2));
+            codes_to_bf16(r0, b0, b1);
+            mma16<false>(o[k], ph[j][0], ph[j][1], ph[j][2], ph[j][3], b0, b1);
+            mma16<false>(o[k], pl[j][0], pl[j][1], pl[j][2], pl[j][3], b0, b1);
+            codes_to_bf16(r1, b0, b1);
+            mma16<false>(o[k + 1], ph[j][0], ph[j][1], ph[j][2], ph[j][3], b0, b1);
+            mma16<false>(o[k + 1], pl[j][0], pl[j][1], pl[j][2], pl[j][3], b0, b1);
+          }
+      } else {
+        const int r = k0 + (lane & 7) + ((lane >> 3) & 1) * 8, cc = lane >> 4;
+#pragma unroll
+        for (int j = 0; j < NT / 2; ++j)
+#pragma unroll
+          for (int k = 0; k < NO; k += 2) {
+            uint32_t b[4];
+            ldsm_x4_t(b, sv + Tl::at(r + j * 16, k + cc));
+            mma16<false>(o[k], ph[j][0], ph[j][1], ph[j][2], ph[j][3], b[0], b[1]);
+            mma16<false>(o[k + 1], ph[j][0], ph[j][1], ph[j][2], ph[j][3], b[2], b[3]);
+            mma16<false>(o[k], pl[j][0], pl[j][1], pl[j][2], pl[j][3], b[0], b[1]);
+            mma16<false>(o[k + 1], pl[j][0], pl[j][1], pl[j][2], pl[j][3], b[2], b[3]);
+          }
+      }
+    } else {
+      uint32_t ph[NT][4], pl[NT][4];  // columns qi, qi + 4 of a step: keys 2 qi, 2 qi + 1
+#pragma unroll
+      for (int j = 0; j < NT; ++j) {
+        split_tf32(s[j][0], ph[j][0], pl[j][0]);
+        split_tf32(s[j][2], ph[j][1], pl[j][1]);
+        split_tf32(s[j][1], ph[j][2], pl[j][2]);
+        split_tf32(s[j][3], ph[j][3], pl[j][3]);
+      }
+      // dims 32 q + 4 column + u of the four output tiles 4 q + u
+#pragma unroll
+      for (int q = 0; q < D / 32; ++q) {
+        float acc[4][4], big[4][4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+#pragma unroll
+          for (int c = 0; c < 4; ++c) acc[u][c] = big[u][c] = 0.f;
+#pragma unroll
+        for (int j = 0; j < NT; ++j) {
+          const uint4 x = lds128(sv + Tl::at(k0 + j * 8 + 2 * qi, 8 * q + gl));
+          const uint4 y = lds128(sv + Tl::at(k0 + j * 8 + 2 * qi + 1, 8 * q + gl));
+          const uint32_t xw[4] = {x.x, x.y, x.z, x.w}, yw[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+          for (int u = 0; u < 4; ++u) {
+            uint32_t h0, l0, h1, l1;
+            split_tf32(__uint_as_float(xw[u]), h0, l0);
+            split_tf32(__uint_as_float(yw[u]), h1, l1);
+            mma8_tf32(acc[u], pl[j], h0, h1);
+            mma8_tf32(acc[u], ph[j], l0, l1);
+            mma8_tf32(big[u], ph[j], h0, h1);
+          }
+        }
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+#pragma unroll
+          for (int c = 0; c < 4; ++c)
+            o[4 * q + u][c] = fmaf(o[4 * q + u][c], a[c >> 1], acc[u][c] + big[u][c]);
+      }
+    }
+  }
+  cp_wait<0>();
+  __syncthreads();
+
+  // ---- the states to shared memory, and their merge ----
+  float* acc = reinterpret_cast<float*>(smem);
+  float* ml = acc + kRowsWarps * 16 * Lay::kAccRow;
+#pragma unroll
+  for (int r = 0; r < 2; ++r) {
+    l[r] += __shfl_xor_sync(kAllLanes, l[r], 1);
+    l[r] += __shfl_xor_sync(kAllLanes, l[r], 2);
+    const int row = wk * M + wr * 16 + gl + 8 * r;
+    if (qi == 0) {
+      ml[2 * row] = m[r];
+      ml[2 * row + 1] = l[r];
+    }
+#pragma unroll
+    for (int k = 0; k < NO; ++k) {
+      if constexpr (kF32) {
+        acc[row * Lay::kAccRow + (k >> 2) * 32 + 8 * qi + (k & 3)] = o[k][2 * r];
+        acc[row * Lay::kAccRow + (k >> 2) * 32 + 8 * qi + 4 + (k & 3)] = o[k][2 * r + 1];
+      } else {
+        *reinterpret_cast<float2*>(acc + row * Lay::kAccRow + k * 8 + 2 * qi) =
+            make_float2(o[k][2 * r], o[k][2 * r + 1]);
+      }
+    }
+  }
+  __syncthreads();
+  // four dims a thread
+  for (int e = tid; e < M * (D / 4); e += kRowsThreads) {
+    const int row = e / (D / 4), d = e % (D / 4) * 4, r = w.first_row + row;
+    if (r >= rows) break;
+    float top_m = -INFINITY;
+#pragma unroll
+    for (int u = 0; u < WK; ++u) top_m = fmaxf(top_m, ml[2 * (u * M + row)]);
+    float sum = 0.f, x[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int u = 0; u < WK; ++u) {
+      const float mu = ml[2 * (u * M + row)];
+      // a state at -inf saw nothing, or only NaN: its sum and O are 0, or NaN
+      const float f = mu == -INFINITY ? 1.f : exp2f(mu - top_m);
+      sum += f * ml[2 * (u * M + row) + 1];
+      const float4 y = *reinterpret_cast<const float4*>(acc + (u * M + row) * Lay::kAccRow + d);
+      x[0] += f * y.x;
+      x[1] += f * y.y;
+      x[2] += f * y.z;
+      x[3] += f * y.w;
+    }
+    if (w.part) {
+      float* dst = w.part + (long long)row * (D + 4);
+      *reinterpret_cast<float4*>(dst + 4 + d) = make_float4(x[0], x[1], x[2], x[3]);
+      if (d == 0) *reinterpret_cast<float2*>(dst) = make_float2(top_m, sum);
+      continue;
+    }
+    const float inv = sum == 0.f ? 0.f : 1.f / sum;  // no weight at all: zeros
+    const int tok = r / G;
+    const long long at = ((w.s.q0 + tok) * p.hq + w.g * G + (r - tok * G)) * D + d;
+    if constexpr (kF32) {
+      *reinterpret_cast<float4*>(p.out + at * 4) =
+          make_float4(x[0] * inv, x[1] * inv, x[2] * inv, x[3] * inv);
+    } else {
+      *reinterpret_cast<uint2*>(p.out + at * 2) =
+          make_uint2(pack_bf16x2(x[0] * inv, x[1] * inv), pack_bf16x2(x[2] * inv, x[3] * inv));
+    }
+  }
+  __syncthreads();  // before the ring is filled again
+}
+
+// Tree: the batch's tiles split evenly over the grid (span.cuh).
+template <int MODE, int D, int WR>
+__global__ void __launch_bounds__(kRowsThreads) rows_tree_kernel(const RowsParams p) {
+  constexpr int KT = RowsTile<MODE, D>::kKeys, M = 16 * WR;
+  extern __shared__ __align__(128) unsigned char smem[];
+  __shared__ long long scratch[32];
+  griddep_wait();
+  griddep_launch_dependents();
+  const long long total = plan_tiles<KT>(p.plan, p.plan.span.batch, scratch);
+  const long long chunk = plan_chunk(p.plan, total, gridDim.x);
+  long long at = blockIdx.x * chunk;
+  const long long end = min(total, at + chunk);
+  if (blockIdx.x == 0) {
+    for (int b = threadIdx.x; b < p.plan.span.batch; b += blockDim.x)
+      if (seq_span(p.plan.span, b).bad) set_error(p.err, kErrCapacity);
+  }
+  if (at >= end) return;
+  long long first;
+  int b = plan_find<KT>(p.plan, at, scratch, &first);
+  while (at < end) {
+    const SeqPlan q = seq_plan<KT>(p.plan, b);
+    if (at >= first + q.tiles) {  // the next sequence
+      first += q.tiles;
+      ++b;
+      continue;
+    }
+    const long long unit = (at - first) / q.t.nt;
+    RowsPiece w;
+    w.s = q.s;
+    w.t = q.t;
+    w.b = b;
+    w.g = (int)(unit / q.nru);
+    w.first_row = (int)(unit - (long long)w.g * q.nru) * M;
+    w.t0 = (int)(at - first - unit * q.t.nt);
+    w.t1 = (int)min((long long)q.t.nt, w.t0 + (end - at));
+    w.lo = window_start(q.s.ctx, p.plan.span.window);
+    w.hi = q.s.ctx + q.s.n - 1;
+    w.part = nullptr;
+    if (w.t0 > 0 || w.t1 < q.t.nt)
+      w.part = p.part + (2ll * blockIdx.x + (w.t0 == 0 ? 1 : 0)) * (M * (D + 4));
+    rows_piece<MODE, D, WR, true>(p, w, smem);
+    at += w.t1 - w.t0;
+  }
+}
+
+// Prefill: a unit a CTA, whole, the longest first.
+template <int MODE, int D>
+__global__ void __launch_bounds__(kRowsThreads) rows_prefill_kernel(const RowsParams p) {
+  constexpr int KT = RowsTile<MODE, D>::kKeys, M = 64;
+  extern __shared__ __align__(128) unsigned char smem[];
+  griddep_wait();
+  griddep_launch_dependents();
+  const int per = p.plan.span.batch * p.plan.hkv;
+  const int u = p.units_max - 1 - (int)(blockIdx.x / per), rest = (int)(blockIdx.x % per);
+  RowsPiece w;
+  w.b = rest / p.plan.hkv;
+  w.g = rest - w.b * p.plan.hkv;
+  w.s = seq_span(p.plan.span, w.b);
+  if (w.s.bad && u == 0 && w.g == 0 && threadIdx.x == 0) set_error(p.err, kErrCapacity);
+  w.first_row = u * M;
+  if (w.first_row >= w.s.n * p.plan.G) return;
+  const int tok0 = w.first_row / p.plan.G;
+  const int tok1 = min(w.s.n - 1, (w.first_row + M - 1) / p.plan.G);
+  w.lo = window_start(w.s.ctx + tok0, p.plan.span.window);
+  w.hi = w.s.ctx + tok1;
+  w.t = tile_list<KT>(w.s.off, w.lo, w.hi, p.plan.span.sink);
+  w.t0 = 0;
+  w.t1 = w.t.nt;
+  w.part = nullptr;
+  rows_piece<MODE, D, 4, false>(p, w, smem);
+}
+
+template <int MODE, int D, int WR>
+cudaError_t launch_rows_tree_wr(const RowsParams& p, int grid, int dev, cudaStream_t s) {
+  static std::atomic<int> allowed[kDevices];
+  const auto kern = rows_tree_kernel<MODE, D, WR>;
+  constexpr size_t smem = RowsLayout<MODE, D, WR>::kSmem;
+  const cudaError_t e = allow_shared(kern, smem, allowed[dev]);
+  if (e != cudaSuccess) return e;
+  return launch_kernel(kern, dim3((unsigned)grid), dim3(kRowsThreads), smem, s, true, p);
+}
+
+template <int MODE, int D>
+cudaError_t launch_rows_d(const RowsParams& p, bool tree, long long grid, int dev, cudaStream_t s) {
+  if (tree) {
+    if (p.plan.unit_rows == 16) return launch_rows_tree_wr<MODE, D, 1>(p, (int)grid, dev, s);
+    if (p.plan.unit_rows == 32) return launch_rows_tree_wr<MODE, D, 2>(p, (int)grid, dev, s);
+    return launch_rows_tree_wr<MODE, D, 4>(p, (int)grid, dev, s);
+  }
+  static std::atomic<int> allowed[kDevices];
+  const auto kern = rows_prefill_kernel<MODE, D>;
+  constexpr size_t smem = RowsLayout<MODE, D, 4>::kSmem;
+  const cudaError_t e = allow_shared(kern, smem, allowed[dev]);
+  if (e != cudaSuccess) return e;
+  return launch_kernel(kern, dim3((unsigned)grid), dim3(kRowsThreads), smem, s, true, p);
+}
+
+}  // namespace
+
+// CTAs of 4 warps that an SM holds at once (rows_*.cu): the grid of the tree kernel.
+template <int MODE, int D>
+constexpr int rows_ctas() {
+  constexpr int n = 227 * 1024 / (RowsLayout<MODE, D, 4>::kSmem + 2048);
+  return n < 3 ? n : 3;
+}
+
+// One translation unit a pool type.
+cudaError_t launch_rows_bf16(const RowsParams& p, int D, bool tree, long long grid, int dev, cudaStream_t s);
+cudaError_t launch_rows_i8(const RowsParams& p, int D, bool tree, long long grid, int dev, cudaStream_t s);
+cudaError_t launch_rows_f32(const RowsParams& p, int D, bool tree, long long grid, int dev, cudaStream_t s);
+
+}  // namespace pkv

@@ -1,0 +1,12 @@
+// The kernels of rows.cuh for i8 pools.
+#include "rows.cuh"
+
+namespace pkv {
+
+cudaError_t launch_rows_i8(const RowsParams& p, int D, bool tree, long long grid, int dev,
+                        cudaStream_t s) {
+  return D == 64 ? launch_rows_d<PKV_I8, 64>(p, tree, grid, dev, s)
+                 : launch_rows_d<PKV_I8, 128>(p, tree, grid, dev, s);
+}
+
+}  // namespace pkv

@@ -1,0 +1,189 @@
+// Which keys the new tokens of a sequence see under a window, first tokens that
+// stay visible and a mask among the new tokens (rows.cuh, prefill.cu), the key
+// tiles that hold them, and how the tiles of a batch are split over a grid.
+#pragma once
+
+#include <cstdint>
+
+#include "common.cuh"
+
+namespace pkv {
+
+// Host limit on max_blocks_per_seq * block_size: table positions, and sums of two
+// of them, are 32-bit in the kernels.
+constexpr long long kMaxPositions = 1ll << 30;
+
+struct SpanParams {
+  const int32_t* lens;
+  const int32_t* offs;
+  const long long* cu_q;  // NULL: one new token a sequence
+  long long total_q;
+  int batch, mb, bs, max_q_len;
+  int window;  // 0: none
+  int sink;    // at most kMaxPositions
+};
+
+// The new tokens of sequence b: query rows q0 .. q0 + n - 1, its last n positions.
+struct SeqSpan {
+  long long q0;
+  int n, ctx, off;
+  bool ok;  // false: nothing is computed (bad: an error, and not just no tokens)
+  bool bad;
+};
+
+__device__ __forceinline__ SeqSpan seq_span(const SpanParams& p, int b) {
+  SeqSpan s;
+  long long q1;
+  if (p.cu_q) {
+    s.q0 = p.cu_q[b];
+    q1 = p.cu_q[b + 1];
+  } else {
+    s.q0 = b;
+    q1 = b + 1;
+  }
+  const int len = p.lens[b];
+  s.off = p.offs ? p.offs[b] : 0;
+  const long long n = p.cu_q || len != 0 ? q1 - s.q0 : 0;
+  s.bad = n < 0 || (n > 0 && (n > p.max_q_len || s.q0 < 0 || q1 > p.total_q || len < n || s.off < 0 ||
+                    s.off >= p.bs || (long long)s.off + len > (long long)p.mb * p.bs));
+  s.ok = n > 0 && !s.bad;
+  s.n = s.ok ? (int)n : 0;
+  s.ctx = len - s.n;
+  return s;
+}
+
+// Key tiles of KT table positions that hold a key which some of the queries see: the
+// queries' windows begin at key lo or later and they see keys up to hi; ns tiles of
+// first tokens from tile s0 on, then the tiles from w0 on, nt in all.
+struct TileList {
+  int s0, ns, w0, nt;
+  __device__ __forceinline__ int tile(int i) const { return i < ns ? s0 + i : w0 + (i - ns); }
+};
+
+template <int KT>
+__device__ __forceinline__ TileList tile_list(int off, int lo, int hi, int sink) {
+  TileList t;
+  t.w0 = (off + lo) / KT;
+  t.s0 = off / KT;
+  const int s = sink < lo ? sink : lo;  // first tokens before the windows
+  t.ns = s > 0 ? min((off + s - 1) / KT + 1, t.w0) - t.s0 : 0;
+  t.ns = max(t.ns, 0);
+  t.nt = t.ns + (off + hi) / KT - t.w0 + 1;
+  return t;
+}
+
+// First key of the window of a query at position pos.
+__device__ __forceinline__ int window_start(int pos, int window) {
+  return window > 0 ? max(0, pos - window + 1) : 0;
+}
+
+// ---- one list of tiles for a batch, split evenly over a grid --------------------------
+//
+// A unit is UR query rows (tokens x heads of a group) of one sequence and kv head over
+// all of the sequence's tiles.  The units of all sequences in order, tile by tile, are
+// one line of T tiles; CTA c takes the tiles [c * chunk, (c + 1) * chunk) of it, so
+// every CTA has the same work whatever the lengths.  A unit that lies in one CTA's share
+// is finished there; of the others each CTA leaves the state of its part in slot
+// 2 c (a unit that began before the share) or 2 c + 1 (one that goes on behind it), and a
+// second kernel merges them.
+
+struct PlanParams {
+  SpanParams span;
+  int unit_rows;  // UR
+  int G, hkv;
+  int least;  // tiles of a share at least
+};
+
+struct SeqPlan {
+  SeqSpan s;
+  TileList t;
+  int nru;  // units of one kv head
+  long long tiles;
+};
+
+template <int KT>
+__device__ __forceinline__ SeqPlan seq_plan(const PlanParams& p, int b) {
+  SeqPlan q;
+  q.s = seq_span(p.span, b);
+  q.t = TileList{0, 0, 0, 0};
+  q.nru = 0;
+  if (q.s.ok) {
+    q.t = tile_list<KT>(q.s.off, window_start(q.s.ctx, p.span.window), q.s.ctx + q.s.n - 1,
+                        p.span.sink);
+    q.nru = (q.s.n * p.G + p.unit_rows - 1) / p.unit_rows;
+  }
+  q.tiles = (long long)q.t.nt * q.nru * p.hkv;
+  return q;
+}
+
+// Sum of x over the block; s: 32 words of shared memory.  Every thread gets it.
+__device__ __forceinline__ long long block_sum(long long x, long long* s) {
+#pragma unroll
+  for (int o = 16; o; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+  const int warp = threadIdx.x >> 5;
+  __syncthreads();
+  if ((threadIdx.x & 31) == 0) s[warp] = x;
+  __syncthreads();
+  x = 0;
+  for (int w = 0; w < (int)(blockDim.x >> 5); ++w) x += s[w];
+  return x;
+}
+
+// Tiles of the sequences before sequence `end`, over the whole block.
+template <int KT>
+__device__ __forceinline__ long long plan_tiles(const PlanParams& p, int end, long long* s) {
+  long long x = 0;
+  for (int b = threadIdx.x; b < end; b += blockDim.x) x += seq_plan<KT>(p, b).tiles;
+  return block_sum(x, s);
+}
+
+__device__ __forceinline__ long long plan_chunk(const PlanParams& p, long long total, int grid) {
+  const long long c = (total + grid - 1) / grid;
+  return c > p.least ? c : p.least;
+}
+
+// The sequence that holds tile `at` of the line, and its first tile: over the whole block.
+template <int KT>
+__device__ __forceinline__ int plan_find(const PlanParams& p, long long at, long long* s,
+                                         long long* first) {
+  __shared__ int found;
+  __shared__ long long found_first;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  long long base = 0;
+  if (tid == 0) found = p.span.batch;
+  for (int b0 = 0; b0 < p.span.batch; b0 += blockDim.x) {
+    const int b = b0 + tid;
+    const long long mine = b < p.span.batch ? seq_plan<KT>(p, b).tiles : 0;
+    long long incl = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long y = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += y;
+    }
+    __syncthreads();
+    if (lane == 31) s[warp] = incl;
+    __syncthreads();
+    long long before = base, all = 0;
+    for (int w = 0; w < (int)(blockDim.x >> 5); ++w) {
+      if (w < warp) before += s[w];
+      all += s[w];
+    }
+    const long long end = before + incl, begin = end - mine;
+    if (at >= begin && at < end) {
+      found = b;
+      found_first = begin;
+    }
+    base += all;
+    if (at < base) break;
+  }
+  __syncthreads();
+  *first = found_first;
+  return found;
+}
+
+// Host side (tree.cu): checks the sequences and the table entries that hold a key which is
+// seen, for validate mode.
+cudaError_t launch_validate_spans(const SpanParams& p, const int32_t* bt, long long num_blocks,
+                                  int* err, cudaStream_t s);
+
+}  // namespace pkv

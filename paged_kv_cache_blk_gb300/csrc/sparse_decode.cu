@@ -51,6 +51,7 @@
 #include "cluster.cuh"
 #include "common.cuh"
 #include "mma.cuh"
+#include "span.cuh"
 
 namespace pkv {
 namespace {
@@ -86,67 +87,22 @@ struct SparseParams {
   int parts;      // pieces of a block (a power of two)
   int piece_bits; // log2 of the rows of a piece
   float qscale;   // scale * log2(e)
+  // the window form: K is then the number of blocks that a query sees at most
+  const int32_t* lens;
+  int window, sink;
 };
 
 // ---- small helpers -----------------------------------------------------------
 
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool live) {
-  const int n = live ? 16 : 0;
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n)
-               : "memory");
-}
-__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void cp_wait() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
-
-__device__ __forceinline__ void ldsm_x4(uint32_t (&r)[4], uint32_t addr) {
-  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-               : "r"(addr)
-               : "memory");
-}
-__device__ __forceinline__ void ldsm_x4_t(uint32_t (&r)[4], uint32_t addr) {
-  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-               : "r"(addr)
-               : "memory");
-}
-// Lane l receives bytes of column l / 4 (r0) and l / 4 + 8 (r1), rows
-// 4 (l % 4) .. + 3, of the 16 x 16 byte matrix whose rows lanes 0-15 address.
-__device__ __forceinline__ void ldsm_b8_t(uint32_t& r0, uint32_t& r1, uint32_t addr) {
-  asm volatile("ldmatrix.sync.aligned.m16n16.x1.trans.shared.b8 {%0,%1}, [%2];"
-               : "=r"(r0), "=r"(r1)
-               : "r"(addr)
-               : "memory");
-}
 // Transpose of an 8 x 8 matrix of 16-bit elements held one row pair a lane.
 __device__ __forceinline__ uint32_t movmatrix_t(uint32_t x) {
   uint32_t r;
   asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
   return r;
 }
-__device__ __forceinline__ float lds_f32(uint32_t a) {
-  float v;
-  asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(a) : "memory");
-  return v;
-}
-__device__ __forceinline__ void sts_f32(uint32_t a, float v) {
-  asm volatile("st.shared.f32 [%0], %1;" ::"r"(a), "f"(v) : "memory");
-}
 __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
   uint32_t r;
   asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-  return r;
-}
-// The largest bf16 below each weight (0 for 0): what is left is positive, so
-// both parts of a weight give an infinite V its own sign, and neither a NaN.
-__device__ __forceinline__ uint32_t below_bf16x2(float lo, float hi) {
-  uint32_t r;
-  asm("prmt.b32 %0, %1, %2, 0x7632;"
-      : "=r"(r)
-      : "r"(max(__float_as_uint(lo), 1u) - 1u), "r"(max(__float_as_uint(hi), 1u) - 1u));
   return r;
 }
 // The nearest finite fp16 of each: what an infinite product leaves is infinite.
@@ -692,7 +648,9 @@ struct Layout {
   static constexpr int kWarps = kFit < kLimit ? kFit : kLimit;  // of a CTA at most
 };
 
-template <int MODE, int D, int HEADS>
+// WINDOW: the query of row t is the last token of sequence t, and its blocks are no list
+// but those with one of the first `sink` or the last `window` tokens.
+template <int MODE, int D, int HEADS, bool WINDOW>
 __global__ void __launch_bounds__(Layout<MODE, D, HEADS>::kWarps * 32)
     sparse_decode_kernel(const SparseParams p) {
   using Tl = Tile<MODE, D>;
@@ -712,24 +670,46 @@ __global__ void __launch_bounds__(Layout<MODE, D, HEADS>::kWarps * 32)
   // The chain of loads before the first row arrives is list, sequence and
   // position; offset and table entry; row: a batch's list entries are loaded one
   // batch ahead, the first ones here.
-  const int32_t* list = p.sel + (long long)row * p.K;
-  const int all_pieces = p.K * p.parts;
+  const int32_t* list = WINDOW ? nullptr : p.sel + (long long)row * p.K;
+  int all_pieces = p.K * p.parts;
+  // window form: the first `heads` listed blocks are the table's first, the others follow
+  // from block `tail` on; table positions [hide_lo, hide_hi) are not seen
+  [[maybe_unused]] int heads = 0, tail = 0, hide_lo = 0, hide_hi = 0;
   const int part_bits = 31 - __clz(p.parts);
   const int stride = (int)S * W;
   int next = (int)rank * W + warp;  // first piece of the batch to come
-  auto listed = [&](long long ts) { return ts < all_pieces ? ld_volatile(list + (ts >> part_bits)) : -1; };
-  int ahead = listed(next + (long long)lane * stride);
-  const int seq = ld_volatile(p.tok_seq + t), pos = ld_volatile(p.tok_pos + t);
+  auto listed = [&](long long ts) {
+    if (ts >= all_pieces) return -1;
+    const int u = (int)(ts >> part_bits);
+    if constexpr (WINDOW) return u < heads ? u : tail + (u - heads);
+    return ld_volatile(list + u);
+  };
+  int ahead = WINDOW ? -1 : listed(next + (long long)lane * stride);
+  const int seq = WINDOW ? t : ld_volatile(p.tok_seq + t);
+  const int pos = WINDOW ? ld_volatile(p.lens + t) - 1 : ld_volatile(p.tok_pos + t);
   if (seq < 0) return;  // padding: the whole cluster leaves, nothing is written
   int off = 0, end = 0;  // table positions [off, end) are seen
   if (seq >= p.batch) {
     if (rank == 0 && tid == 0) set_error(p.err, kErrIndex);
   } else {
     off = p.offs ? p.offs[seq] : 0;
-    if (off < 0 || off >= p.bs || pos < 0 || (long long)off + pos >= (long long)p.mb * p.bs) {
+    if (off < 0 || off >= p.bs || pos < (WINDOW ? -1 : 0) ||
+        (long long)off + pos >= (long long)p.mb * p.bs) {
       if (rank == 0 && tid == 0) set_error(p.err, kErrCapacity);
-    } else {
+    } else if (!WINDOW || pos >= 0) {
       end = off + pos + 1;
+    }
+  }
+  if constexpr (WINDOW) {
+    if (end > 0) {
+      const int bs_bits = 31 - __clz(p.bs);
+      hide_lo = min(off + p.sink, end);
+      hide_hi = max(off, end - p.window);
+      tail = hide_hi >> bs_bits;
+      const int last_head = min(hide_lo, hide_hi) - 1;
+      heads = last_head >= off ? min((last_head >> bs_bits) + 1, tail) : 0;
+      all_pieces = (heads + ((end - 1) >> bs_bits) - tail + 1) * p.parts;
+      ahead = listed(next + (long long)lane * stride);
     }
   }
   const int pieces = end > 0 ? all_pieces : 0;  // a bad token sees nothing: zeros
@@ -751,12 +731,19 @@ __global__ void __launch_bounds__(Layout<MODE, D, HEADS>::kWarps * 32)
       ahead = listed(ts + 32ll * stride);
       int lo = 0, hi = 0;
       if (j >= p.mb) set_error(p.err, kErrIndex);
+      uint32_t hidden = 0;
       if (j >= 0 && j < p.mb) {
-        const int blk = ld_volatile(table + j);
         const int r0 = (int)(ts & (p.parts - 1)) * kTile;
         const int p0 = j * p.bs + r0;
         lo = max(0, off - p0);
         hi = min(rows_piece, end - p0);
+        if constexpr (WINDOW) {
+          const int a = max(0, hide_lo - p0), b = min(rows_piece, hide_hi - p0);
+          if (a < b) hidden = (1u << b) - (1u << a);
+          // a block without a token that is seen is not looked up
+          if (lo >= hi || (((1u << hi) - (1u << lo)) & ~hidden) == 0) lo = hi = 0;
+        }
+        const int blk = WINDOW && lo >= hi ? 0 : ld_volatile(table + j);
         if (blk >= 0 && blk < p.num_blocks) {
           my_row = ((long long)blk * p.L + p.layer) * p.bs + r0;
         } else if (lo < hi) {
@@ -764,7 +751,7 @@ __global__ void __launch_bounds__(Layout<MODE, D, HEADS>::kWarps * 32)
           hi = 0;
         }
       }
-      my_mask = lo < hi ? (1u << hi) - (1u << lo) : 0u;
+      my_mask = lo < hi ? ((1u << hi) - (1u << lo)) & ~hidden : 0u;
       todo = __ballot_sync(kAll, lo < hi);
       next = pieces - next <= 32 * stride ? pieces : next + 32 * stride;
     }
@@ -905,12 +892,12 @@ __global__ void __launch_bounds__(Layout<MODE, D, HEADS>::kWarps * 32)
 // 3 x 1 64.1, 4 x 1 76.9; bf16, R 512, K 128 2 x 1 83.0, 4 x 1 84.5, 8 x 1 92.2,
 // 3 x 1 107; R 40, K 100 8 x 3 10.6, 4 x 3 11.4, 3 x 7 12.5; R 16, K 300 8 x 6 14.4,
 // 4 x 8 14.8.
-template <int MODE, int D, int HEADS>
+template <int MODE, int D, int HEADS, bool WINDOW>
 cudaError_t launch_sparse_heads(const SparseParams& p, unsigned rows, int dev, int sms,
                                 cudaStream_t s) {
   using Lay = Layout<MODE, D, HEADS>;
   static std::atomic<int> allowed[kDevices], known[kDevices][kMaxWarps + 1][kMaxCluster + 1];
-  const auto kern = sparse_decode_kernel<MODE, D, HEADS>;
+  const auto kern = sparse_decode_kernel<MODE, D, HEADS, WINDOW>;
   cudaError_t e = allow_shared(kern, (size_t)Lay::kWarps * Lay::kWarp, allowed[dev]);
   if (e != cudaSuccess) return e;
   const long long tiles = ((long long)p.K * p.parts << p.piece_bits) / kTile;
@@ -943,14 +930,57 @@ cudaError_t launch_sparse_heads(const SparseParams& p, unsigned rows, int dev, i
                          (size_t)warps * Lay::kWarp, (unsigned)ctas, s, p);
 }
 
-template <int MODE, int D>
+template <int MODE, int D, bool WINDOW>
 cudaError_t launch_sparse_d(const SparseParams& p, unsigned rows, int dev, int sms,
                             cudaStream_t s) {
   if constexpr (MODE != PKV_BF16) {
-    if (p.G <= 4) return launch_sparse_heads<MODE, D, 4>(p, rows, dev, sms, s);
+    if (p.G <= 4) return launch_sparse_heads<MODE, D, 4, WINDOW>(p, rows, dev, sms, s);
   }
-  if (p.G <= 8) return launch_sparse_heads<MODE, D, 8>(p, rows, dev, sms, s);
-  return launch_sparse_heads<MODE, D, 16>(p, rows, dev, sms, s);
+  if (p.G <= 8) return launch_sparse_heads<MODE, D, 8, WINDOW>(p, rows, dev, sms, s);
+  return launch_sparse_heads<MODE, D, 16, WINDOW>(p, rows, dev, sms, s);
+}
+
+template <bool WINDOW>
+cudaError_t launch_sparse(const PoolView& v, const SparseParams& p, unsigned rows, int dev, int sms,
+                          cudaStream_t s) {
+  const bool d64 = v.head_dim == 64;
+  if (v.quant)
+    return d64 ? launch_sparse_d<PKV_I8, 64, WINDOW>(p, rows, dev, sms, s)
+               : launch_sparse_d<PKV_I8, 128, WINDOW>(p, rows, dev, sms, s);
+  if (v.io_size == 2)
+    return d64 ? launch_sparse_d<PKV_BF16, 64, WINDOW>(p, rows, dev, sms, s)
+               : launch_sparse_d<PKV_BF16, 128, WINDOW>(p, rows, dev, sms, s);
+  return d64 ? launch_sparse_d<PKV_F32, 64, WINDOW>(p, rows, dev, sms, s)
+             : launch_sparse_d<PKV_F32, 128, WINDOW>(p, rows, dev, sms, s);
+}
+
+// The parameters that the two calls share.
+SparseParams sparse_params(const PoolView& v, int layer, const void* q, int num_q_heads,
+                           float scale, const int32_t* bt, int mb, const int32_t* offs, int batch,
+                           void* out, int* err) {
+  SparseParams p = {};
+  p.k = v.k;
+  p.v = v.v;
+  p.q = static_cast<const char*>(q);
+  p.out = static_cast<char*>(out);
+  p.bt = bt;
+  p.offs = offs;
+  p.err = err;
+  p.num_blocks = v.num_blocks;
+  p.batch = batch;
+  p.mb = mb;
+  p.bs = v.block_size;
+  p.L = v.num_layers;
+  p.layer = layer;
+  p.row_bytes = v.row_bytes;
+  p.scale_off = v.scale_off;
+  p.hq = num_q_heads;
+  p.hkv = v.num_kv_heads;
+  p.G = num_q_heads / v.num_kv_heads;
+  p.parts = v.block_size > kTile ? v.block_size / kTile : 1;
+  while (p.piece_bits < 4 && 1 << p.piece_bits < v.block_size) ++p.piece_bits;
+  p.qscale = scale * kLog2e;
+  return p;
 }
 
 }  // namespace
@@ -997,45 +1027,71 @@ extern "C" pkv_status pkv_decode_attention_sparse(
       return (pkv_status)st;
     if ((st = pkv::read_and_clear_error_word(err, stream)) != PKV_OK) return (pkv_status)st;
   }
-  pkv::SparseParams p;
-  p.k = v.k;
-  p.v = v.v;
-  p.q = static_cast<const char*>(q);
-  p.out = static_cast<char*>(out);
-  p.bt = block_tables;
-  p.offs = offsets;
+  pkv::SparseParams p = pkv::sparse_params(v, layer, q, num_q_heads, scale, block_tables, mb, offsets,
+                                           batch, out, err);
   p.tok_seq = token_seq;
   p.tok_pos = token_pos;
   p.sel = selected;
-  p.err = err;
-  p.num_blocks = v.num_blocks;
-  p.batch = batch;
-  p.mb = mb;
-  p.bs = v.block_size;
-  p.L = v.num_layers;
-  p.layer = layer;
-  p.row_bytes = v.row_bytes;
-  p.scale_off = v.scale_off;
-  p.hq = num_q_heads;
-  p.hkv = v.num_kv_heads;
-  p.G = G;
   p.K = num_selected;
-  p.parts = parts;
-  p.piece_bits = 0;
-  while (p.piece_bits < 4 && 1 << p.piece_bits < v.block_size) ++p.piece_bits;
-  p.qscale = scale * pkv::kLog2e;
-  const unsigned r = (unsigned)rows;
-  const bool d64 = v.head_dim == 64;
-  cudaError_t e;
-  if (v.quant)
-    e = d64 ? pkv::launch_sparse_d<PKV_I8, 64>(p, r, dev, sms, stream)
-            : pkv::launch_sparse_d<PKV_I8, 128>(p, r, dev, sms, stream);
-  else if (v.io_size == 2)
-    e = d64 ? pkv::launch_sparse_d<PKV_BF16, 64>(p, r, dev, sms, stream)
-            : pkv::launch_sparse_d<PKV_BF16, 128>(p, r, dev, sms, stream);
-  else
-    e = d64 ? pkv::launch_sparse_d<PKV_F32, 64>(p, r, dev, sms, stream)
-            : pkv::launch_sparse_d<PKV_F32, 128>(p, r, dev, sms, stream);
+  const cudaError_t e = pkv::launch_sparse<false>(v, p, (unsigned)rows, dev, sms, stream);
+  if ((st = pkv::launch_status(e)) != PKV_OK) return (pkv_status)st;
+  return validate ? (pkv_status)pkv::read_and_clear_error_word(err, stream) : PKV_OK;
+}
+
+extern "C" pkv_status pkv_decode_attention_window(
+    const pkv_pool* pool, int32_t layer, const void* q, int32_t num_q_heads, float scale,
+    const int32_t* block_tables, int32_t max_blocks_per_seq, const int32_t* seq_lens,
+    const int32_t* offsets, int32_t batch, int32_t window, int32_t sink, void* out,
+    cudaStream_t stream) {
+  pkv::PoolView v;
+  int st = pkv::pool_view(pool, true, &v);
+  if (st != PKV_OK) return (pkv_status)st;
+  if (layer < 0 || layer >= v.num_layers || batch < 0 || num_q_heads <= 0 || window < 1 ||
+      sink < 0 || num_q_heads % v.num_kv_heads != 0 || !std::isfinite(scale))
+    return PKV_ERR_INVALID_ARG;
+  if ((v.head_dim != 64 && v.head_dim != 128) || num_q_heads / v.num_kv_heads > 16)
+    return PKV_ERR_UNSUPPORTED;
+  if (batch == 0) return PKV_OK;
+  if (!q || !out || !block_tables || !seq_lens || max_blocks_per_seq <= 0)
+    return PKV_ERR_INVALID_ARG;
+  if (!pkv::aligned(q, 16) || !pkv::aligned(out, 16) || !pkv::aligned(block_tables, 4) ||
+      !pkv::aligned(seq_lens, 4) || !pkv::aligned(offsets, 4))
+    return PKV_ERR_INVALID_ARG;
+  const int64_t rows = (int64_t)batch * v.num_kv_heads;
+  if ((int64_t)max_blocks_per_seq * v.block_size > pkv::kMaxPositions || rows > INT32_MAX / 8)
+    return PKV_ERR_UNSUPPORTED;
+  int optin, grid, validate, sms, dev;
+  int* err;
+  if ((st = pkv::device_facts(&optin, &err, &grid, &validate)) != PKV_OK) return (pkv_status)st;
+  if ((st = pkv::device_sm_count(&sms, &dev)) != PKV_OK) return (pkv_status)st;
+  pkv::SparseParams p = pkv::sparse_params(v, layer, q, num_q_heads, scale, block_tables,
+                                           max_blocks_per_seq, offsets, batch, out, err);
+  p.lens = seq_lens;
+  p.window = window;
+  p.sink = (int)(sink < pkv::kMaxPositions ? sink : pkv::kMaxPositions);
+  if (validate) {
+    pkv::SpanParams sp = {};
+    sp.lens = seq_lens;
+    sp.offs = offsets;
+    sp.total_q = batch;
+    sp.batch = batch;
+    sp.mb = max_blocks_per_seq;
+    sp.bs = v.block_size;
+    sp.max_q_len = 1;
+    sp.window = window;
+    sp.sink = p.sink;
+    if ((st = pkv::clear_error_word(err, stream)) != PKV_OK) return (pkv_status)st;
+    if ((st = pkv::launch_status(pkv::launch_validate_spans(sp, block_tables, v.num_blocks, err,
+                                                            stream))) != PKV_OK)
+      return (pkv_status)st;
+    if ((st = pkv::read_and_clear_error_word(err, stream)) != PKV_OK) return (pkv_status)st;
+  }
+  // the blocks that a query sees at most: those of the first tokens, from any row of a block
+  // on, and those of the window
+  const int64_t bs = v.block_size;
+  const int64_t most = (sink > 0 ? (bs - 1 + p.sink + bs - 1) / bs : 0) + (window + bs - 2) / bs + 1;
+  p.K = (int)(most < max_blocks_per_seq ? most : max_blocks_per_seq);
+  const cudaError_t e = pkv::launch_sparse<true>(v, p, (unsigned)rows, dev, sms, stream);
   if ((st = pkv::launch_status(e)) != PKV_OK) return (pkv_status)st;
   return validate ? (pkv_status)pkv::read_and_clear_error_word(err, stream) : PKV_OK;
 }

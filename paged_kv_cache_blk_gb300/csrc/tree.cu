@@ -1,0 +1,331 @@
+// Entry points of the tree decode and the windowed prefill (pkv_decode_attention_tree,
+// pkv_prefill_attention_window): checks, choice of the kernel, and the merge of the states
+// that the tree kernels leave where a unit of work was split.
+#include <algorithm>
+
+#include "rows.cuh"
+
+namespace pkv {
+namespace {
+
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr int kCombineWarps = 8;
+
+struct CombineParams {
+  PlanParams plan;
+  const float* part;
+  char* out;
+  int hq, D, f32, grid;  // grid: CTAs of the kernel that left the states
+  int blocks_seq;        // CTAs of a sequence
+};
+
+// A warp a (token, query head): the states of its unit in the CTAs that shared it, by the
+// log-sum-exp rule.  Rows that one CTA finished are left alone.
+template <int KT>
+__global__ void __launch_bounds__(kCombineWarps * 32) tree_combine_kernel(const CombineParams p) {
+  __shared__ long long scratch[32];
+  griddep_wait();
+  griddep_launch_dependents();
+  const int b = blockIdx.x / p.blocks_seq;
+  const int first_row = (blockIdx.x - b * p.blocks_seq) * kCombineWarps;
+  const SeqPlan q = seq_plan<KT>(p.plan, b);
+  if (first_row >= q.s.n * p.hq) return;
+  // tiles of the batch, and of the sequences before this one
+  long long all = 0, before = 0;
+  for (int i = threadIdx.x; i < p.plan.span.batch; i += blockDim.x) {
+    const long long x = seq_plan<KT>(p.plan, i).tiles;
+    all += x;
+    before += i < b ? x : 0;
+  }
+  const long long chunk = plan_chunk(p.plan, block_sum(all, scratch), p.grid);
+  before = block_sum(before, scratch);
+  const int lane = threadIdx.x & 31, row = first_row + (threadIdx.x >> 5);
+  if (row >= q.s.n * p.hq) return;
+  const int tok = row / p.hq, h = row - tok * p.hq, g = h / p.plan.G;
+  const int r = tok * p.plan.G + h - g * p.plan.G, ur = p.plan.unit_rows, unit = r / ur;
+  const long long start = before + ((long long)g * q.nru + unit) * q.t.nt;
+  const long long c0 = start / chunk, c1 = (start + q.t.nt - 1) / chunk;
+  if (c0 == c1) return;
+  const long long row_floats = p.D + 4, slot = ur * row_floats;
+  const float* at = p.part + (r - unit * ur) * row_floats;
+  // the first CTA began the unit (slot 2 c + 1) unless it starts exactly before its share
+  auto state = [&](long long c) { return at + (2 * c + (c == c0 ? 1 : 0)) * slot; };
+  const int pieces = (int)(c1 - c0) + 1;
+  float top = -INFINITY;
+  for (int i = lane; i < pieces; i += 32) top = fmaxf(top, state(c0 + i)[0]);
+#pragma unroll
+  for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(kAllLanes, top, o));
+  const int d = lane * 4;
+  float sum = 0.f, x[4] = {0.f, 0.f, 0.f, 0.f};
+  for (int i0 = 0; i0 < pieces; i0 += 32) {
+    float f = 0.f;
+    if (i0 + lane < pieces) {
+      const float2 ml = *reinterpret_cast<const float2*>(state(c0 + i0 + lane));
+      // a state at -inf saw nothing, or only NaN: its sum and O are 0, or NaN
+      f = ml.x == -INFINITY ? 1.f : exp2f(ml.x - top);
+      sum += f * ml.y;
+    }
+    const int m = min(32, pieces - i0);
+#pragma unroll 4
+    for (int j = 0; j < m; ++j) {
+      const float fj = __shfl_sync(kAllLanes, f, j);
+      if (d < p.D) {
+        const float4 y = *reinterpret_cast<const float4*>(state(c0 + i0 + j) + 4 + d);
+        x[0] += fj * y.x;
+        x[1] += fj * y.y;
+        x[2] += fj * y.z;
+        x[3] += fj * y.w;
+      }
+    }
+  }
+#pragma unroll
+  for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(kAllLanes, sum, o);
+  if (d >= p.D) return;
+  const float inv = sum == 0.f ? 0.f : 1.f / sum;  // no weight at all: zeros
+  const long long dst = ((q.s.q0 + tok) * p.hq + h) * p.D + d;
+  if (p.f32)
+    *reinterpret_cast<float4*>(p.out + dst * 4) =
+        make_float4(x[0] * inv, x[1] * inv, x[2] * inv, x[3] * inv);
+  else
+    *reinterpret_cast<uint2*>(p.out + dst * 2) =
+        make_uint2(pack_bf16x2(x[0] * inv, x[1] * inv), pack_bf16x2(x[2] * inv, x[3] * inv));
+}
+
+// One CTA a sequence: its numbers, and the entries of the blocks that hold a seen key.
+__global__ void validate_spans_kernel(const SpanParams p, const int32_t* bt, long long num_blocks,
+                                      int* err) {
+  const int b = blockIdx.x;
+  const SeqSpan s = seq_span(p, b);
+  if (s.bad && threadIdx.x == 0) set_error(err, kErrCapacity);
+  if (!s.ok) return;
+  const int last = s.off + s.ctx + s.n - 1, lo = s.off + window_start(s.ctx, p.window);
+  const int sink_end = min(s.off + p.sink, last + 1);
+  for (int e = threadIdx.x; e <= last / p.bs; e += blockDim.x) {
+    const int first = max(s.off, e * p.bs), end = min(last + 1, (e + 1) * p.bs);
+    if (end <= lo && first >= sink_end) continue;
+    const int blk = bt[(long long)b * p.mb + e];
+    if (blk < 0 || blk >= num_blocks) set_error(err, kErrIndex);
+  }
+}
+
+// How a tree call runs: units of unit_rows rows, split over `grid` CTAs.
+struct TreePath {
+  int unit_rows, grid;
+  size_t bytes;  // of workspace
+};
+
+TreePath tree_path(const PoolView& v, int G, int max_q_len, int sms) {
+  TreePath t;
+  const long long rows = (long long)max_q_len * G;
+  t.unit_rows = rows <= 16 ? 16 : rows <= 32 ? 32 : 64;
+  int ctas;
+  if (v.quant)
+    ctas = v.head_dim == 64 ? rows_ctas<PKV_I8, 64>() : rows_ctas<PKV_I8, 128>();
+  else if (v.io_size == 2)
+    ctas = v.head_dim == 64 ? rows_ctas<PKV_BF16, 64>() : rows_ctas<PKV_BF16, 128>();
+  else
+    ctas = v.head_dim == 64 ? rows_ctas<PKV_F32, 64>() : rows_ctas<PKV_F32, 128>();
+  t.grid = sms * ctas;
+  t.bytes = (size_t)2 * t.grid * t.unit_rows * (v.head_dim + 4) * 4;
+  return t;
+}
+
+cudaError_t launch_rows(const PoolView& v, const RowsParams& p, bool tree, long long grid, int dev,
+                        cudaStream_t s) {
+  if (v.quant) return launch_rows_i8(p, v.head_dim, tree, grid, dev, s);
+  if (v.io_size == 2) return launch_rows_bf16(p, v.head_dim, tree, grid, dev, s);
+  return launch_rows_f32(p, v.head_dim, tree, grid, dev, s);
+}
+
+// The arguments that the two calls share.
+struct Call {
+  const pkv_pool* pool;
+  int32_t layer;
+  const void* q;
+  int32_t num_q_heads;
+  float scale;
+  const int32_t* block_tables;
+  int32_t max_blocks_per_seq;
+  const int32_t *seq_lens, *offsets;
+  const int64_t* cu_q;
+  int32_t batch;
+  int64_t total_q;
+  int32_t max_q_len, window, sink;
+  void* out;
+};
+
+// Their checks, in the order of the other calls.  *empty: there is nothing to compute.
+int check_call(const Call& c, PoolView* v, bool* empty) {
+  const int st = pool_view(c.pool, true, v);
+  if (st != PKV_OK) return st;
+  if (c.layer < 0 || c.layer >= v->num_layers || c.batch < 0 || c.num_q_heads <= 0 ||
+      c.total_q < 0 || c.max_q_len < 0 || c.window < 0 || c.sink < 0 ||
+      c.num_q_heads % v->num_kv_heads != 0 || !std::isfinite(c.scale))
+    return PKV_ERR_INVALID_ARG;
+  if ((v->head_dim != 64 && v->head_dim != 128) || c.num_q_heads / v->num_kv_heads > 16)
+    return PKV_ERR_UNSUPPORTED;
+  *empty = c.batch == 0 || c.total_q == 0 || c.max_q_len == 0;
+  if (*empty) return PKV_OK;
+  if (!c.q || !c.out || !c.block_tables || !c.seq_lens || !c.cu_q || c.max_blocks_per_seq <= 0)
+    return PKV_ERR_INVALID_ARG;
+  if (!aligned(c.q, 16) || !aligned(c.out, 16) || !aligned(c.block_tables, 4) ||
+      !aligned(c.seq_lens, 4) || !aligned(c.offsets, 4) || !aligned(c.cu_q, 8))
+    return PKV_ERR_INVALID_ARG;
+  // rows, positions and grids are 32-bit in the kernels
+  const int64_t units = ((int64_t)c.max_q_len * c.num_q_heads + 7) / 8;
+  if ((int64_t)c.max_blocks_per_seq * v->block_size > kMaxPositions || c.total_q > INT32_MAX ||
+      c.batch > 65535 || units * c.batch > INT32_MAX || units > (1 << 26))
+    return PKV_ERR_UNSUPPORTED;
+  return PKV_OK;
+}
+
+RowsParams rows_params(const Call& c, const PoolView& v, int* err) {
+  RowsParams p = {};
+  SpanParams& s = p.plan.span;
+  s.lens = c.seq_lens;
+  s.offs = c.offsets;
+  s.cu_q = reinterpret_cast<const long long*>(c.cu_q);
+  s.total_q = c.total_q;
+  s.batch = c.batch;
+  s.mb = c.max_blocks_per_seq;
+  s.bs = v.block_size;
+  s.max_q_len = c.max_q_len;
+  s.window = c.window;
+  s.sink = c.sink < kMaxPositions ? c.sink : (int)kMaxPositions;
+  p.plan.G = c.num_q_heads / v.num_kv_heads;
+  p.plan.hkv = v.num_kv_heads;
+  p.plan.least = 1;
+  p.k = v.k;
+  p.v = v.v;
+  p.q = static_cast<const char*>(c.q);
+  p.out = static_cast<char*>(c.out);
+  p.bt = c.block_tables;
+  p.err = err;
+  p.num_blocks = v.num_blocks;
+  p.L = v.num_layers;
+  p.layer = c.layer;
+  p.row_bytes = v.row_bytes;
+  p.scale_off = v.scale_off;
+  p.hq = c.num_q_heads;
+  while (1 << p.bs_bits < v.block_size) ++p.bs_bits;
+  p.qscale = c.scale * kLog2e;
+  return p;
+}
+
+int validate_call(const RowsParams& p, cudaStream_t stream) {
+  int st;
+  if ((st = clear_error_word(p.err, stream)) != PKV_OK) return st;
+  if ((st = launch_status(launch_validate_spans(p.plan.span, p.bt, p.num_blocks, p.err,
+                                                stream))) != PKV_OK)
+    return st;
+  return read_and_clear_error_word(p.err, stream);
+}
+
+}  // namespace
+
+cudaError_t launch_validate_spans(const SpanParams& p, const int32_t* bt, long long num_blocks,
+                                  int* err, cudaStream_t s) {
+  validate_spans_kernel<<<(unsigned)p.batch, 128, 0, s>>>(p, bt, num_blocks, err);
+  return cudaGetLastError();
+}
+
+}  // namespace pkv
+
+extern "C" {
+
+size_t pkv_decode_tree_workspace_size(const pkv_pool* pool, int32_t batch, int32_t num_q_heads,
+                                      int32_t max_q_len) {
+  pkv::PoolView v;
+  if (pkv::pool_view(pool, false, &v) != PKV_OK) return 0;
+  if (batch < 0 || num_q_heads <= 0 || num_q_heads % v.num_kv_heads != 0 || max_q_len < 0) return 0;
+  if (v.head_dim != 64 && v.head_dim != 128) return 0;
+  int sms;
+  if (pkv::device_sm_count(&sms) != PKV_OK) return 0;
+  return pkv::tree_path(v, num_q_heads / v.num_kv_heads, max_q_len, sms).bytes;
+}
+
+pkv_status pkv_decode_attention_tree(const pkv_pool* pool, int32_t layer, const void* q,
+                                     int32_t num_q_heads, float scale, const int32_t* block_tables,
+                                     int32_t max_blocks_per_seq, const int32_t* seq_lens,
+                                     const int32_t* offsets, const int64_t* cu_q, int32_t batch,
+                                     int64_t total_q, int32_t max_q_len, const uint64_t* tree_mask,
+                                     int32_t mask_words, const int32_t* q_pos, int32_t window,
+                                     int32_t sink, void* out, void* workspace,
+                                     size_t workspace_bytes, cudaStream_t stream) {
+  const pkv::Call c = {pool, layer, q, num_q_heads, scale, block_tables, max_blocks_per_seq,
+                       seq_lens, offsets, cu_q, batch, total_q, max_q_len, window, sink, out};
+  pkv::PoolView v;
+  bool empty;
+  int st = pkv::check_call(c, &v, &empty);
+  if (st != PKV_OK) return (pkv_status)st;
+  // the mask has a bit for each drafted token; positions go with a mask
+  if (tree_mask ? mask_words < 1 || max_q_len > (int64_t)64 * mask_words
+                : mask_words != 0 || q_pos != nullptr)
+    return PKV_ERR_INVALID_ARG;
+  if (empty) return PKV_OK;
+  if (!pkv::aligned(tree_mask, 8) || !pkv::aligned(q_pos, 4)) return PKV_ERR_INVALID_ARG;
+  if (!workspace || !pkv::aligned(workspace, 16)) return PKV_ERR_WORKSPACE;
+  int optin, decode_grid, validate, sms, dev;
+  int* err;
+  if ((st = pkv::device_facts(&optin, &err, &decode_grid, &validate)) != PKV_OK)
+    return (pkv_status)st;
+  if ((st = pkv::device_sm_count(&sms, &dev)) != PKV_OK) return (pkv_status)st;
+  pkv::RowsParams p = pkv::rows_params(c, v, err);
+  const pkv::TreePath path = pkv::tree_path(v, p.plan.G, max_q_len, sms);
+  if (workspace_bytes < path.bytes) return PKV_ERR_WORKSPACE;
+  p.plan.unit_rows = path.unit_rows;
+  p.part = static_cast<float*>(workspace);
+  p.mask = reinterpret_cast<const unsigned long long*>(tree_mask);
+  p.words = mask_words;
+  p.q_pos = q_pos;
+  if (validate && (st = pkv::validate_call(p, stream)) != PKV_OK) return (pkv_status)st;
+  if ((st = pkv::launch_status(pkv::launch_rows(v, p, true, path.grid, dev, stream))) != PKV_OK)
+    return (pkv_status)st;
+  pkv::CombineParams m = {};
+  m.plan = p.plan;
+  m.part = p.part;
+  m.out = p.out;
+  m.hq = num_q_heads;
+  m.D = v.head_dim;
+  m.f32 = v.io_size == 4;
+  m.grid = path.grid;
+  m.blocks_seq = (int)(((int64_t)max_q_len * num_q_heads + pkv::kCombineWarps - 1) /
+                       pkv::kCombineWarps);
+  const auto kern = m.f32 ? pkv::tree_combine_kernel<32> : pkv::tree_combine_kernel<64>;
+  st = pkv::launch_status(pkv::launch_kernel(kern, dim3((unsigned)(m.blocks_seq * batch)),
+                                             dim3(pkv::kCombineWarps * 32), 0, stream, true, m));
+  if (st != PKV_OK) return (pkv_status)st;
+  return validate ? (pkv_status)pkv::read_and_clear_error_word(err, stream) : PKV_OK;
+}
+
+pkv_status pkv_prefill_attention_window(const pkv_pool* pool, int32_t layer, const void* q,
+                                        int32_t num_q_heads, float scale,
+                                        const int32_t* block_tables, int32_t max_blocks_per_seq,
+                                        const int32_t* seq_lens, const int32_t* offsets,
+                                        const int64_t* cu_q, int32_t batch, int64_t total_q,
+                                        int32_t max_q_len, int32_t window, int32_t sink, void* out,
+                                        cudaStream_t stream) {
+  const pkv::Call c = {pool, layer, q, num_q_heads, scale, block_tables, max_blocks_per_seq,
+                       seq_lens, offsets, cu_q, batch, total_q, max_q_len, window, sink, out};
+  pkv::PoolView v;
+  bool empty;
+  int st = pkv::check_call(c, &v, &empty);
+  if (st != PKV_OK) return (pkv_status)st;
+  if (window < 1) return PKV_ERR_INVALID_ARG;
+  if (empty) return PKV_OK;
+  int optin, decode_grid, validate, sms, dev;
+  int* err;
+  if ((st = pkv::device_facts(&optin, &err, &decode_grid, &validate)) != PKV_OK)
+    return (pkv_status)st;
+  if ((st = pkv::device_sm_count(&sms, &dev)) != PKV_OK) return (pkv_status)st;
+  pkv::RowsParams p = pkv::rows_params(c, v, err);
+  p.plan.unit_rows = 64;
+  if (validate && (st = pkv::validate_call(p, stream)) != PKV_OK) return (pkv_status)st;
+  p.units_max = (int)(((int64_t)max_q_len * p.plan.G + 63) / 64);
+  const long long grid = (long long)p.units_max * batch * v.num_kv_heads;
+  if ((st = pkv::launch_status(pkv::launch_rows(v, p, false, grid, dev, stream))) != PKV_OK)
+    return (pkv_status)st;
+  return validate ? (pkv_status)pkv::read_and_clear_error_word(err, stream) : PKV_OK;
+}
+
+}  // extern "C"
