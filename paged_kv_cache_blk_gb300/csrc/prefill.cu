@@ -50,6 +50,7 @@
 
 #include "common.cuh"
 #include "pkv.h"
+#include "span.cuh"
 #include "tma.cuh"
 
 namespace pkv {
@@ -59,10 +60,18 @@ constexpr int kPfWarps = 10;  // 0-3 softmax A, 4-7 softmax B, 8 TMA, 9 MMA
 constexpr int kWarpTma = 8;
 constexpr int kWarpMma = 9;
 constexpr int kWarpFwd = 10;  // CTA pairs: forwards this CTA's halves to the other CTA
-// threads of a CTA: one more warp in a CTA pair
-template <bool SHARE>
+
+// What an item computes, and which keys its rows see.
+enum PfMode : int {
+  kCausal,  // prefill
+  kPrefix,  // prefix pass of shared-prefix decode
+  kWindow,  // prefill under a sliding window and first tokens (span.cuh)
+  kTree,    // drafted tokens over their context: parts of units (span.cuh), any mask
+};
+// threads of a CTA: one more warp in a CTA pair, and for trees
+template <int MODE, bool SHARE>
 constexpr int pf_threads() {
-  return (kPfWarps + (SHARE ? 1 : 0)) * 32;
+  return (kPfWarps + (SHARE || MODE == kTree ? 1 : 0)) * 32;
 }
 constexpr int kRows = 128;   // MMA M: query rows per tile
 constexpr int kKeys = 128;   // keys per KV tile (MMA N of Q K^T, K of P V)
@@ -102,6 +111,13 @@ struct PfParams {
   int prefix_blocks, key_tiles, nsplit, per_split;
   float* pre_ml;
   float* pre_acc;
+  // windows and trees
+  int window, sink;
+  PlanParams plan;                 // trees
+  const int32_t* q_pos;            // as in RowsParams
+  const unsigned long long* mask;
+  int words;
+  float* part;
   unsigned long long wait_ns;  // bound of one wait (0 = the default)
   int epoch;  // this launch's number (see WaitCtl)
   int skip_fill;  // test hook: 1 = CTA 0, 2 = every CTA stalls its MMA warp
@@ -274,20 +290,73 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   return r;
 }
 
+// Which columns of a tile a row sees: an interval, or any set as a word for each 32-column
+// chunk.
+struct IntervalMask {
+  int c_lo, c_hi;
+  struct Chunk {
+    int lo, hi;  // within the chunk
+    __device__ __forceinline__ bool none() const { return hi < 0 || lo > 31; }
+    __device__ __forceinline__ bool all() const { return lo <= 0 && hi >= 31; }
+    __device__ __forceinline__ bool sees(int j) const { return j >= lo && j <= hi; }
+  };
+  __device__ __forceinline__ Chunk chunk(int c0) const { return Chunk{c_lo - c0, c_hi - c0}; }
+};
+
+// Columns a .. b of those from c0 on, as bits.
+__device__ __forceinline__ uint32_t column_bits(int a, int b, int c0) {
+  const int lo = max(a - c0, 0), hi = min(b - c0, 31);
+  return lo > hi ? 0u : (0xffffffffu << lo) & (0xffffffffu >> (31 - hi));
+}
+
+// Windows and trees: of the columns first .. top those before sink_end or from win on, and
+// the drafted columns behind top whose bit is set.
+struct SpanMask {
+  int first, top, sink_end, win;
+  int draft, drafted;  // column of drafted token 0, and their number (0: top says it all)
+  unsigned long long w0, w1;  // the first 128 bits
+  const unsigned long long* bits;
+  struct Chunk {
+    uint32_t w;
+    __device__ __forceinline__ bool none() const { return w == 0; }
+    __device__ __forceinline__ bool all() const { return w == 0xffffffffu; }
+    __device__ __forceinline__ bool sees(int j) const { return w >> j & 1; }
+  };
+  __device__ __forceinline__ unsigned long long word(int i) const {
+    return i == 0 ? w0 : i == 1 ? w1 : bits[i];
+  }
+  __device__ __forceinline__ Chunk chunk(int c0) const {
+    uint32_t w = column_bits(first, min(top, sink_end - 1), c0) | column_bits(max(first, win), top, c0);
+    const int d = c0 - draft;  // drafted token of the chunk's first column
+    if (drafted > 0 && d > -32 && d < drafted) {
+      unsigned long long x;
+      if (d < 0) {
+        x = w0 << -d;
+      } else {
+        x = word(d >> 6) >> (d & 63);
+        // (a second word where the chunk goes on in it and it holds drafted tokens)
+        if ((d & 63) > 32 && ((d >> 6) + 1) * 64 < drafted) x |= word((d >> 6) + 1) << (64 - (d & 63));
+      }
+      w |= (uint32_t)x & column_bits(0, drafted - 1, d);
+    }
+    return Chunk{w};
+  }
+};
+
 // Softmax of one S tile for one row: reads the row from TMEM, masks it,
 // updates the running state, rescales the O row when the maximum moved, and
 // writes the row's P as bf16 pairs back into TMEM, where the P V product reads
 // it as its A operand.
+template <class Mask>
 __device__ __forceinline__ void softmax_tile(uint32_t tS, uint32_t tO, uint32_t lane_base, int t,
-                                             int c_lo, int c_hi, bool full_tile, float qs,
+                                             const Mask& mask, bool full_tile, float qs,
                                              RowState& st) {
   // With a positive scale the maximum is taken on the raw scores and the scale
   // goes into the exponent's FMA; otherwise each score is scaled first.
   const bool pre = qs <= 0.f;
   const float qe = pre ? 1.f : qs;
-  // one 32-column chunk of the S row, scaled when needed and masked (the key
-  // in column c is valid for c_lo <= c <= c_hi)
-  auto load_chunk = [&](int c0, float (&x)[32]) {
+  // one 32-column chunk of the S row, scaled when needed and masked
+  auto load_chunk = [&](int c0, const typename Mask::Chunk& seen, float (&x)[32]) {
     uint32_t v[32];
     tmem_ld32(tS + lane_base + c0, v);
     tmem_wait_ld();
@@ -295,7 +364,7 @@ __device__ __forceinline__ void softmax_tile(uint32_t tS, uint32_t tO, uint32_t 
     for (int j = 0; j < 32; ++j) {
       float f = __uint_as_float(v[j]);
       if (pre) f *= qs;
-      if (!full_tile) f = (c0 + j >= c_lo && c0 + j <= c_hi) ? f : -INFINITY;
+      if (!full_tile) f = seen.sees(j) ? f : -INFINITY;
       x[j] = f;
     }
   };
@@ -352,14 +421,16 @@ __device__ __forceinline__ void softmax_tile(uint32_t tS, uint32_t tO, uint32_t 
       // row's keys of the warp (its P is zero: no exponentials) or inside all
       // of them (no mask code); the votes keep the TMEM accesses warp-uniform
       bool plain = full_tile;
+      typename Mask::Chunk seen{};
       if (!full_tile) {
-        if (__all_sync(0xffffffffu, c0 > c_hi || c0 + 31 < c_lo)) {
+        seen = mask.chunk(c0);
+        if (__all_sync(0xffffffffu, seen.none())) {
           const uint32_t z[16] = {0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u,
                                   0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u};
           tmem_st16(tS + lane_base + (c0 >> 1), z);
           continue;
         }
-        plain = __all_sync(0xffffffffu, c0 >= c_lo && c0 + 31 <= c_hi);
+        plain = __all_sync(0xffffffffu, seen.all());
       }
       if (plain && !pre) {
         // the common case, kept free of masking and scaling code
@@ -369,7 +440,7 @@ __device__ __forceinline__ void softmax_tile(uint32_t tS, uint32_t tO, uint32_t 
 #pragma unroll
         for (int j = 0; j < 32; ++j) x[j] = __uint_as_float(v[j]);
       } else {
-        load_chunk(c0, x);
+        load_chunk(c0, seen, x);
       }
       const float cm = chunk_max(x) * qe;
       uint32_t w[16];
@@ -427,8 +498,14 @@ struct Item {
   long long q0, nq, qtA, qtB, first_pos, spanned;
   int off;
   int t0, c;  // shared-prefix prefix pass: first key tile and split index
+  // windows and trees: tile i is the sequence's tile list.tile(t0 + i); `lo` the first key of
+  // the windows; trees: where a part's state goes (-1: a whole unit), and after the last item
+  TileList list;
+  int lo, slot;
+  bool end;
 };
 
+template <int MODE>
 __device__ __forceinline__ Item make_item(const PfParams& p, long long i, int tid) {
   Item it{};
   const long long per = (long long)p.batch * p.hkv;
@@ -439,13 +516,15 @@ __device__ __forceinline__ Item make_item(const PfParams& p, long long i, int ti
   it.q0 = p.cu_q[it.b];
   const long long q1 = p.cu_q[it.b + 1];
   it.nq = q1 - it.q0;
+  if (MODE == kWindow && it.nq < 0 && px == 0 && it.g == 0 && tid == 0)
+    set_error(p.err, kErrCapacity);
   if (it.nq <= 0) return it;
   const int TQ = p.TQ;
   const long long ntq = (it.nq + TQ - 1) / TQ;
   if (px >= (ntq + 1) / 2) return it;
   const long long len = p.lens[it.b];
   it.off = p.offs ? p.offs[it.b] : 0;
-  if (it.nq > p.max_q_len || len < it.nq || it.off < 0 || it.off >= p.bs || q1 > p.total_q ||
+  if ((MODE == kWindow && it.q0 < 0) || it.nq > p.max_q_len || len < it.nq || it.off < 0 || it.off >= p.bs || q1 > p.total_q ||
       (long long)it.off + len > (long long)p.mb * p.bs) {
     // reported once, by the item of the sequence's first pair and head
     if (px == 0 && it.g == 0 && tid == 0) set_error(p.err, kErrCapacity);
@@ -461,6 +540,16 @@ __device__ __forceinline__ Item make_item(const PfParams& p, long long i, int ti
   };
   it.nA = tiles_for(it.qtA);
   it.nB = tiles_for(it.qtB);
+  if constexpr (MODE == kWindow) {
+    // the list of all four query tiles of a CTA pair (items px & ~1 and px | 1), from the
+    // window of their first token on
+    const long long qt0 = ntq - 2 - 2 * (px | 1);
+    it.lo = window_start((int)(it.first_pos + max(0ll, qt0) * TQ), p.window);
+    it.list = tile_list<kKeys>(it.off, it.lo, (int)len - 1, p.sink);
+    const int skipped = it.list.w0 - it.list.ns;
+    if (it.nA > 0) it.nA -= skipped;
+    it.nB -= skipped;
+  }
   it.spanned = ((long long)it.off + len + p.bs - 1) / p.bs;
   it.valid = true;
   return it;
@@ -496,6 +585,78 @@ __device__ __forceinline__ Item make_item_prefix(const PfParams& p, long long i)
   return it;
 }
 
+// Trees: the parts of units that make up this CTA's share, one after the other.  Tile B
+// holds a unit's first 128 rows, tile A the next where there are more.
+struct TreeCursor {
+  long long at, end, first;  // tiles of the line; first: that of sequence b
+  int b;
+  __device__ __forceinline__ bool next(const PfParams& p, Item& it) {
+    while (at < end) {
+      const SeqPlan q = seq_plan<kKeys>(p.plan, b);
+      if (at >= first + q.tiles) {
+        first += q.tiles;
+        ++b;
+        continue;
+      }
+      const long long unit = (at - first) / q.t.nt;
+      it = Item{};
+      it.valid = true;
+      it.b = b;
+      it.g = (int)(unit / q.nru);
+      it.qtB = 2 * (unit - (long long)it.g * q.nru);
+      it.qtA = it.qtB + 1;
+      it.q0 = q.s.q0;
+      it.nq = q.s.n;
+      it.off = q.s.off;
+      it.first_pos = q.s.ctx;
+      it.spanned = ((long long)q.s.off + q.s.ctx + q.s.n + p.bs - 1) / p.bs;
+      it.list = q.t;
+      it.lo = window_start(q.s.ctx, p.window);
+      it.t0 = (int)(at - first - unit * q.t.nt);
+      it.nB = (int)min((long long)(q.t.nt - it.t0), end - at);
+      it.nA = it.qtA * p.TQ < it.nq ? it.nB : 0;
+      it.slot = it.nB == q.t.nt ? -1 : 2 * (int)blockIdx.x + (it.t0 == 0 ? 1 : 0);
+      at += it.nB;
+      return true;
+    }
+    return false;
+  }
+};
+
+// Windows and trees: a block is needed if it holds a first token or a key from `lo` on
+// (the others' table entries are not looked up), and the V rows of a tile that hold neither,
+// or lie outside the sequence, are cleared: their P is 0, but 0 times what they hold need not be.
+__device__ __forceinline__ bool block_needed(const PfParams& p, const Item& it, long long lb) {
+  const long long first = lb * p.bs;
+  return first + p.bs > it.off + it.lo || (p.sink > 0 && first < (long long)it.off + p.sink);
+}
+// Rows hide_lo .. hide_hi - 1 of the sequence's table positions, and those outside
+// off .. end - 1, are not seen by any query of the item's CTA pair.
+struct SeenRows {
+  int off, end, hide_lo, hide_hi;
+  __device__ __forceinline__ bool whole(int p0) const {
+    return p0 >= off && p0 + kKeys <= end && (p0 >= hide_hi || p0 + kKeys <= hide_lo);
+  }
+  __device__ __forceinline__ bool has(int pos) const {
+    return pos >= off && pos < end && (pos < hide_lo || pos >= hide_hi);
+  }
+};
+__device__ __forceinline__ SeenRows seen_rows(const PfParams& p, const Item& it) {
+  return SeenRows{it.off, it.off + p.lens[it.b], it.off + p.sink, it.off + it.lo};
+}
+// A warp clears the rows of 128 bytes of a loaded half tile that are not seen.
+__device__ __forceinline__ void clear_rows(uint32_t half, const SeenRows& s, int p0, int lane) {
+  for (int r = lane >> 3; r < kKeys; r += 4) {
+    if (!s.has(p0 + r))
+      asm volatile("st.shared.v4.u32 [%0], {%1,%1,%1,%1};" ::"r"(half + r * 128 + (lane & 7) * 16),
+                   "r"(0)
+                   : "memory");
+  }
+  // before the tensor cores and the copy to the other CTA read them
+  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+  __syncwarp();
+}
+
 // CTA pairs: cluster item c gives the pair the query-tile pairs 2 c' and
 // 2 c' + 1 of one (sequence, kv head) (c' = c / (batch x Hkv)); the even CTA
 // holds the later pair, whose key tiles cover the other's.
@@ -526,11 +687,12 @@ __device__ __forceinline__ long long item_of(const PfParams& p, long long c, uin
 // Each CTA waits for every release of its slots before it leaves (so no
 // copy or arrive of the other CTA still targets it), and the two leave
 // together (a cluster barrier).
-template <bool PREFIX, bool SHARE>
-__global__ void __launch_bounds__(pf_threads<SHARE>(), 1)
+template <int MODE, bool SHARE>
+__global__ void __launch_bounds__((pf_threads<MODE, SHARE>()), 1)
     prefill_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk,
                    const __grid_constant__ CUtensorMap tv, const PfParams p) {
-  static_assert(!(PREFIX && SHARE), "the prefix pass runs on single CTAs");
+  constexpr bool PREFIX = MODE == kPrefix, TREE = MODE == kTree, SPAN = MODE == kWindow || TREE;
+  static_assert(!((PREFIX || TREE) && SHARE), "the prefix pass and trees run on single CTAs");
   extern __shared__ __align__(1024) unsigned char smem_raw[];
   // Prefix pass of shared-prefix decode: it reads nothing the grid before it
   // (the suffix pass) writes, and that grid's own inputs were complete when
@@ -621,10 +783,40 @@ __global__ void __launch_bounds__(pf_threads<SHARE>(), 1)
   // this CTA's item of (cluster) item c, and the item whose key tiles the
   // pair streams (the even CTA's)
   auto own_item = [&](long long c) {
-    return PREFIX ? make_item_prefix(p, c) : make_item(p, SHARE ? item_of(p, c, rank) : c, tid);
+    return PREFIX ? make_item_prefix(p, c)
+                  : make_item<MODE>(p, SHARE ? item_of(p, c, rank) : c, tid);
   };
   auto lead_item = [&](long long c, const Item& own) {
-    return !SHARE || rank == 0 ? own : make_item(p, item_of(p, c, 0), tid);
+    return !SHARE || rank == 0 ? own : make_item<MODE>(p, item_of(p, c, 0), tid);
+  };
+  // trees: this CTA's share of the line of tiles; every role walks it with its own copy
+  [[maybe_unused]] TreeCursor cur;
+  if constexpr (TREE) {
+    long long* scratch = reinterpret_cast<long long*>(s_items);  // (before the first item)
+    const long long total = plan_tiles<kKeys>(p.plan, p.batch, scratch);
+    const long long chunk = plan_chunk(p.plan, total, gridDim.x);
+    cur.at = min(total, blockIdx.x * chunk);
+    cur.end = min(total, cur.at + chunk);
+    if (blockIdx.x == 0) {
+      for (int b = tid; b < p.batch; b += blockDim.x)
+        if (seq_span(p.plan.span, b).bad) set_error(p.err, kErrCapacity);
+    }
+    cur.b = cur.at < cur.end ? plan_find<kKeys>(p.plan, cur.at, scratch, &cur.first) : 0;
+    __syncthreads();
+  }
+  // the next item and the one whose tiles are streamed: c counts the CTA's items
+  auto next_item = [&](long long& c, Item& own, Item& lead) -> bool {
+    if constexpr (TREE) {
+      if (!cur.next(p, own)) return false;
+      lead = own;
+      return true;
+    } else {
+      if (c >= n_items) return false;
+      own = own_item(c);
+      lead = lead_item(c, own);
+      c += i_step;
+      return true;
+    }
   };
   const WaitCtl w = make_wait_ctl(p.err, p.wait_ns, p.epoch);
   bool ok = true;
@@ -635,9 +827,14 @@ __global__ void __launch_bounds__(pf_threads<SHARE>(), 1)
     long long ld = 0;  // K / V loads issued so far (ring position)
     int jq = 0;        // items whose Q was loaded
     long long ni = 0;  // items published
-    for (long long i = i_first; i < n_items && ok; i += i_step, ++ni) {
-      const Item it = own_item(i);
-      const Item lead = lead_item(i, it);
+    Item it, lead;
+    for (long long i = i_first; ok; ++ni) {
+      const bool more = next_item(i, it, lead);
+      if (!more) {
+        if constexpr (!TREE) break;
+        it = lead = Item{};  // the MMA warp does not know the number of parts: an end mark
+        it.end = true;
+      }
       {
         const int r = (int)(ni % kItemRing);
         const long long use = ni / kItemRing;
@@ -651,6 +848,7 @@ __global__ void __launch_bounds__(pf_threads<SHARE>(), 1)
           mbar_arrive(b_ifull0 + 8u * r);
         }
       }
+      if (!more) break;
       if (!lead.valid) continue;
       if (it.valid) {
         // Q of this item once the previous item's S products have read the old one
@@ -676,15 +874,17 @@ __global__ void __launch_bounds__(pf_threads<SHARE>(), 1)
         const int t = li >> 1, is_v = li & 1;
         // one CTA: both 64-column halves; a pair: this CTA's half, counted on
         // its own "half loaded" barrier (the other half comes from the peer)
-        const uint32_t bar = SHARE ? slot_half(slot) : slot_full(slot);
+        // (trees: V tiles are looked over by warp 10 before they are multiplied)
+        const uint32_t bar = SHARE || (TREE && is_v) ? slot_half(slot) : slot_full(slot);
         if (lane == 0) mbar_arrive_expect_tx(bar, SHARE ? kHalf : kTileBytes);
         __syncwarp();
         for (int k2 = lane; k2 < (SHARE ? 1 : 2) * blocks_per_tile; k2 += 32) {
           const int h = SHARE ? (int)rank : k2 / blocks_per_tile;
           const int k = SHARE ? k2 : k2 % blocks_per_tile;
-          const long long lb = (long long)(PREFIX ? lead.t0 + t : t) * blocks_per_tile + k;
+          const int tile = SPAN ? lead.list.tile(lead.t0 + t) : PREFIX ? lead.t0 + t : t;
+          const long long lb = (long long)tile * blocks_per_tile + k;
           long long coord = p.blk_coord_limit;                       // out of range: zeros
-          if (lb < lead.spanned) {
+          if (lb < lead.spanned && (!SPAN || block_needed(p, lead, lb))) {
             const int blk = p.bt[(long long)lead.b * p.mb + lb];
             if (blk >= 0 && blk < p.num_blocks) {
               coord = (long long)blk * p.L + p.layer;
@@ -711,6 +911,9 @@ __global__ void __launch_bounds__(pf_threads<SHARE>(), 1)
         // (after which the other CTA sends nothing more into it)
         mbar_wait_drain(slot_half(slot), ph, p.err);
         mbar_wait_sleep(slot_empty(slot), ph, w);
+      } else if (TREE && (slot & 1)) {  // (a ring of an even number of slots: V in the odd ones)
+        static_assert(kSlots % 2 == 0, "K and V keep their slots");
+        mbar_wait_drain(slot_half(slot), ph, p.err);
       } else {
         mbar_wait_drain(slot_full(slot), ph, p.err);
       }
@@ -720,22 +923,55 @@ __global__ void __launch_bounds__(pf_threads<SHARE>(), 1)
     // ================= CTA pair: this CTA's half of each slot to the other CTA =================
     // once its copy landed; this CTA's "slot full" then waits only for the
     // other CTA's half
-    if (lane == 0) {
+    // (windows: the whole warp, which clears V rows that no query sees before they go)
+    if (lane == 0 || SPAN) {
       const uint32_t half_off = rank * kHalf;
       long long ld = 0;
       for (long long i = i_first; i < n_items && ok; i += i_step) {
         const Item lead = lead_item(i, own_item(i));
         if (!lead.valid) continue;
+        [[maybe_unused]] SeenRows seen;
+        if constexpr (SPAN) seen = seen_rows(p, lead);
         for (int li = 0; li < 2 * lead.nB; ++li, ++ld) {
           const int slot = (int)(ld % kSlots);
-          if (!mbar_wait_sleep(slot_half(slot), (uint32_t)((ld / kSlots) & 1), w)) {
+          bool landed = mbar_wait_sleep(slot_half(slot), (uint32_t)((ld / kSlots) & 1), w);
+          if constexpr (SPAN) landed = __all_sync(0xffffffffu, landed);
+          if (!landed) {
             ok = false;
             break;
+          }
+          if constexpr (SPAN) {
+            const int p0 = lead.list.tile(li >> 1) * kKeys;
+            if ((li & 1) && !seen.whole(p0))
+              clear_rows(smem_addr(slot_ptr(slot)) + half_off, seen, p0, lane);
+            if (lane != 0) continue;
           }
           mbar_arrive_expect_tx(slot_full(slot), kHalf);
           const uint32_t src = smem_addr(slot_ptr(slot)) + half_off;
           bulk_s2s(peer_addr(src, peer), src, kHalf, peer_addr(slot_full(slot), peer));
         }
+      }
+    }
+  } else if (TREE && warp == kWarpFwd) {
+    // ================= trees: V rows that no query sees cleared, then the tile handed on ========
+    long long ld = 0, i = i_first;
+    Item it, lead;
+    while (ok && next_item(i, it, lead)) {
+      const SeenRows seen = seen_rows(p, it);
+      for (int t = 0; t < it.nB; ++t, ld += 2) {
+        const long long idx = ld + 1;
+        const int slot = (int)(idx % kSlots);
+        const bool landed = mbar_wait_sleep(slot_half(slot), (uint32_t)((idx / kSlots) & 1), w);
+        if (!__all_sync(0xffffffffu, landed)) {
+          ok = false;
+          break;
+        }
+        const int p0 = it.list.tile(it.t0 + t) * kKeys;
+        if (!seen.whole(p0)) {
+          clear_rows(smem_addr(slot_ptr(slot)), seen, p0, lane);
+          clear_rows(smem_addr(slot_ptr(slot)) + kHalf, seen, p0, lane);
+        }
+        if (lane == 0) mbar_arrive(slot_full(slot));
       }
     }
   } else if (warp == kWarpMma) {
@@ -802,7 +1038,7 @@ __global__ void __launch_bounds__(pf_threads<SHARE>(), 1)
         umma_commit(b_pvdone0 + 8u * x);
       };
       long long ni = 0;  // items read from the loads warp
-      for (long long i = i_first; i < n_items && ok; i += i_step, ++ni) {
+      for (long long i = i_first; (TREE || i < n_items) && ok; i += i_step, ++ni) {
         const int r = (int)(ni % kItemRing);
         if (!mbar_wait_sleep(b_ifull0 + 8u * r, (uint32_t)((ni / kItemRing) & 1), w)) {
           ok = false;
@@ -811,6 +1047,7 @@ __global__ void __launch_bounds__(pf_threads<SHARE>(), 1)
         const Item it = s_items[2 * r];
         const Item lead = s_items[2 * r + 1];
         mbar_arrive(b_iempty0 + 8u * r);
+        if (TREE && it.end) break;
         if (!lead.valid) continue;
         const int nA = it.valid ? it.nA : 0, nB = it.valid ? it.nB : 0;
         const long long base = ld;  // load index of K(0) of this item
@@ -880,8 +1117,15 @@ __global__ void __launch_bounds__(pf_threads<SHARE>(), 1)
     const uint32_t b_sfull = b_sfull0 + 8u * x, b_pfull = b_pfull0 + 8u * x;
     const uint32_t b_pvdone = b_pvdone0 + 8u * x, b_ofree = b_ofree0 + 8u * x;
     long long nt = 0;  // tiles of this warpgroup across items (barrier phases)
-    for (long long i = i_first; i < n_items && ok; i += i_step) {
-      const Item it = own_item(i);
+    for (long long i = i_first; ok;) {
+      Item it;
+      if constexpr (TREE) {
+        if (!cur.next(p, it)) break;
+      } else {
+        if (i >= n_items) break;
+        it = own_item(i);
+        i += i_step;
+      }
       if (!it.valid) continue;
       const int nX = x == 0 ? it.nA : it.nB;
       if (nX == 0) continue;
@@ -906,11 +1150,48 @@ __global__ void __launch_bounds__(pf_threads<SHARE>(), 1)
           key_hi = min((long long)p.prefix_blocks * p.bs, ob + lb);
         }
       }
+      // windows and trees, in table positions: the row sees first .. top, of these the first
+      // tokens and those from win on, and drafted tokens behind top by their bits
+      [[maybe_unused]] SpanMask span;
+      [[maybe_unused]] int span_top = 0, span_win = 0;
+      if constexpr (SPAN) {
+        const long long qrow = it.q0 + (row_ok ? qi : 0);
+        const bool masked = TREE && p.mask != nullptr;
+        span_top = row_ok ? it.off + (int)(masked ? it.first_pos - 1 : pos) : -1;
+        long long at = pos;
+        if (TREE && p.q_pos) at = max(it.first_pos, (long long)p.q_pos[qrow]);
+        if (p.window > 0)
+          span_win = it.off + (int)max(0ll, min(at - p.window + 1, kMaxPositions - 2048));
+        span.drafted = masked && row_ok ? (int)it.nq : 0;
+        span.w0 = span.w1 = 0;
+        span.bits = masked ? p.mask + qrow * p.words : nullptr;
+        if (masked) {
+          span.w0 = span.bits[0];
+          if (p.words > 1) span.w1 = span.bits[1];
+        }
+      }
       RowState st{-INFINITY, 0.f};
       for (int t = 0; t < nX && ok; ++t, ++nt) {
         const bool waited = mbar_wait_sleep(b_sfull, (uint32_t)(nt & 1), w);
         if (!__all_sync(0xffffffffu, waited)) { ok = false; break; }
         tc_fence_after();
+        if constexpr (SPAN) {
+          const int tp0 = it.list.tile(it.t0 + t) * kKeys;
+          span.first = it.off - tp0;
+          span.top = span_top - tp0;
+          span.sink_end = it.off + p.sink - tp0;
+          span.win = span_win - tp0;
+          span.draft = it.off + (int)it.first_pos - tp0;
+          // (a padding row may be taken for one that sees everything: it is not stored)
+          const bool full = !row_ok || (span.first <= 0 && span.top >= kKeys - 1 &&
+                                        (span.win <= 0 || span.sink_end >= kKeys));
+          softmax_tile(tS(x), tO(x), lane_base, t, span, __all_sync(0xffffffffu, full), p.qscale,
+                       st);
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(b_pfull);
+          continue;
+        }
         int c_lo, c_hi;
         bool full_tile;
         if constexpr (PREFIX) {
@@ -925,7 +1206,7 @@ __global__ void __launch_bounds__(pf_threads<SHARE>(), 1)
           c_hi = row_ok ? (int)min((long long)kKeys - 1, pos + it.off - tp0) : -1;
           full_tile = (t > 0 || it.off == 0) && t < t_mask_lo && rows_full;
         }
-        softmax_tile(tS(x), tO(x), lane_base, t, c_lo, c_hi, full_tile, p.qscale, st);
+        softmax_tile(tS(x), tO(x), lane_base, t, IntervalMask{c_lo, c_hi}, full_tile, p.qscale, st);
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(b_pfull);
@@ -960,7 +1241,32 @@ __global__ void __launch_bounds__(pf_threads<SHARE>(), 1)
         if (lane == 0) mbar_arrive(b_ofree);
         continue;
       }
-      const float inv = st.l > 0.f ? 1.f / st.l : 0.f;
+      if constexpr (TREE) {
+        if (it.slot >= 0) {
+          // a part of a unit: the row's state, merged by the kernel that follows
+          float* srow = p.part + ((long long)it.slot * (2 * kRows) + (x == 0 ? kRows : 0) + r) *
+                                     (kD + 4);
+          if (row_ok) *reinterpret_cast<float2*>(srow) = make_float2(st.m_used, st.l);
+#pragma unroll 1
+          for (int c0 = 0; c0 < kD; c0 += 32) {
+            uint32_t v[32];
+            tmem_ld32(tO(x) + lane_base + c0, v);
+            tmem_wait_ld();
+            if (row_ok) {
+#pragma unroll
+              for (int j = 0; j < 32; j += 4)
+                *reinterpret_cast<uint4*>(srow + 4 + c0 + j) = make_uint4(v[j], v[j + 1], v[j + 2],
+                                                                          v[j + 3]);
+            }
+          }
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(b_ofree);
+          continue;
+        }
+      }
+      // (windows and trees: a NaN of the sum is one of the result)
+      const float inv = (SPAN ? st.l != 0.f : st.l > 0.f) ? 1.f / st.l : 0.f;
       __nv_bfloat16* orow = static_cast<__nv_bfloat16*>(p.out) +
                             ((it.q0 + qi) * p.hq + (long long)it.g * G + hh) * kD;
 #pragma unroll 1
@@ -1088,7 +1394,7 @@ cudaError_t prefill_setup(const PoolView& pv, int layer, const void* q, int num_
   return cudaSuccess;
 }
 
-template <bool PREFIX>
+template <int MODE>
 cudaError_t prefill_launch(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
                            const PfParams& p, int sm_count, cudaStream_t s) {
   static int configured[64] = {0};
@@ -1096,24 +1402,25 @@ cudaError_t prefill_launch(const CUtensorMap& tq, const CUtensorMap& tk, const C
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (dev >= 0 && dev < 64 && configured[dev] == 0) {
-    e = cudaFuncSetAttribute(prefill_kernel<PREFIX, false>,
+    e = cudaFuncSetAttribute(prefill_kernel<MODE, false>,
                              cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
     if (e != cudaSuccess) return e;
     configured[dev] = 1;
   }
   const long long grid = p.n_items < sm_count ? p.n_items : sm_count;
-  return launch_kernel(prefill_kernel<PREFIX, false>, dim3((unsigned)grid),
-                       dim3(pf_threads<false>()), (size_t)kSmemBytes, s, true, tq, tk, tv, p);
+  return launch_kernel(prefill_kernel<MODE, false>, dim3((unsigned)grid),
+                       dim3(pf_threads<MODE, false>()), (size_t)kSmemBytes, s, true, tq, tk, tv, p);
 }
 
 // CTA pairs: clusters of two CTAs, as many as can be resident at once (at
 // most one per two SMs), as a programmatic dependent of the work before.
+template <int MODE>
 cudaError_t prefill_launch_pairs(const CUtensorMap& tq, const CUtensorMap& tk,
                                  const CUtensorMap& tv, const PfParams& p, int sm_count,
                                  cudaStream_t s) {
-  auto kern = prefill_kernel<false, true>;
+  auto kern = prefill_kernel<MODE, true>;
   cudaLaunchConfig_t cfg = {};
-  cfg.blockDim = dim3(pf_threads<true>());
+  cfg.blockDim = dim3(pf_threads<MODE, true>());
   cfg.dynamicSmemBytes = (size_t)kSmemBytes;
   cfg.stream = s;
   cudaLaunchAttribute attr[2];
@@ -1153,7 +1460,8 @@ cudaError_t prefill_launch_pairs(const CUtensorMap& tq, const CUtensorMap& tk,
 cudaError_t launch_prefill(const PoolView& pv, int layer, const void* q, int num_q_heads,
                            float scale, const int32_t* bt, int mb, const int32_t* lens,
                            const int32_t* offs, const int64_t* cu_q, int batch, long long total_q,
-                           int max_q_len, void* out, int* err, int sm_count, cudaStream_t s) {
+                           int max_q_len, int window, int sink, void* out, int* err, int sm_count,
+                           cudaStream_t s) {
   if (batch == 0 || total_q == 0 || max_q_len == 0) return cudaSuccess;
   CUtensorMap tq, tk, tv;
   PfParams p;
@@ -1166,7 +1474,32 @@ cudaError_t launch_prefill(const PoolView& pv, int layer, const void* q, int num
   const long long ntq = (max_q_len + p.TQ - 1) / p.TQ;
   // CTA pairs: pairs of query-tile pairs per (sequence, kv head)
   p.n_items = ((ntq + 1) / 2 + 1) / 2 * (long long)batch * pv.num_kv_heads;
-  return prefill_launch_pairs(tq, tk, tv, p, sm_count, s);
+  p.window = window;
+  p.sink = sink;
+  return window > 0 ? prefill_launch_pairs<kWindow>(tq, tk, tv, p, sm_count, s)
+                    : prefill_launch_pairs<kCausal>(tq, tk, tv, p, sm_count, s);
+}
+
+cudaError_t launch_prefill_tree(const PoolView& pv, int layer, const void* q, int num_q_heads,
+                                float scale, const int32_t* bt, const PlanParams& plan,
+                                const int32_t* q_pos, const unsigned long long* mask, int words,
+                                float* part, void* out, int* err, int sm_count, cudaStream_t s) {
+  CUtensorMap tq, tk, tv;
+  PfParams p;
+  const SpanParams& sp = plan.span;
+  const cudaError_t e = prefill_setup(pv, layer, q, num_q_heads, scale, bt, sp.mb, sp.lens, sp.offs,
+                                      sp.batch, sp.total_q, err, &tq, &tk, &tv, &p);
+  if (e != cudaSuccess) return e;
+  p.out = out;
+  p.window = sp.window;
+  p.sink = sp.sink;
+  p.plan = plan;
+  p.q_pos = q_pos;
+  p.mask = mask;
+  p.words = words;
+  p.part = part;
+  p.n_items = sm_count;  // the grid: the line of tiles is split over it
+  return prefill_launch<kTree>(tq, tk, tv, p, sm_count, s);
 }
 
 void prefix_plan(const PoolView& pv, int num_q_heads, int batch, int prefix_blocks, int sm_count,
@@ -1204,7 +1537,7 @@ cudaError_t launch_prefix_pass(const PoolView& pv, int layer, const void* q, int
   p.pre_acc = pre_acc;
   const long long ntq = (batch + p.TQ - 1) / p.TQ;
   p.n_items = (ntq + 1) / 2 * (long long)nsplit * pv.num_kv_heads;
-  return prefill_launch<true>(tq, tk, tv, p, sm_count, s);
+  return prefill_launch<kPrefix>(tq, tk, tv, p, sm_count, s);
 }
 
 }  // namespace pkv

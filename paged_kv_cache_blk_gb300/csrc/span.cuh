@@ -186,4 +186,11 @@ __device__ __forceinline__ int plan_find(const PlanParams& p, long long at, long
 cudaError_t launch_validate_spans(const SpanParams& p, const int32_t* bt, long long num_blocks,
                                   int* err, cudaStream_t s);
 
+// Host side (prefill.cu, where prefill_supported): the tree decode on tcgen05, units of 256
+// rows, key tiles of 128, split over a grid of sm_count CTAs (one where fewer SMs are free).
+cudaError_t launch_prefill_tree(const PoolView& pv, int layer, const void* q, int num_q_heads,
+                                float scale, const int32_t* bt, const PlanParams& plan,
+                                const int32_t* q_pos, const unsigned long long* mask, int words,
+                                float* part, void* out, int* err, int sm_count, cudaStream_t s);
+
 }  // namespace pkv

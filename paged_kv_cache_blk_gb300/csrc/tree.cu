@@ -110,6 +110,7 @@ __global__ void validate_spans_kernel(const SpanParams p, const int32_t* bt, lon
 
 // How a tree call runs: units of unit_rows rows, split over `grid` CTAs.
 struct TreePath {
+  bool tcgen05;
   int unit_rows, grid;
   size_t bytes;  // of workspace
 };
@@ -117,6 +118,13 @@ struct TreePath {
 TreePath tree_path(const PoolView& v, int G, int max_q_len, int sms) {
   TreePath t;
   const long long rows = (long long)max_q_len * G;
+  t.tcgen05 = rows > 32 && prefill_supported(v, G * v.num_kv_heads) == 0;
+  if (t.tcgen05) {
+    t.unit_rows = 256;
+    t.grid = sms;
+    t.bytes = (size_t)2 * t.grid * t.unit_rows * (v.head_dim + 4) * 4;
+    return t;
+  }
   t.unit_rows = rows <= 16 ? 16 : rows <= 32 ? 32 : 64;
   int ctas;
   if (v.quant)
@@ -279,8 +287,12 @@ pkv_status pkv_decode_attention_tree(const pkv_pool* pool, int32_t layer, const 
   p.words = mask_words;
   p.q_pos = q_pos;
   if (validate && (st = pkv::validate_call(p, stream)) != PKV_OK) return (pkv_status)st;
-  if ((st = pkv::launch_status(pkv::launch_rows(v, p, true, path.grid, dev, stream))) != PKV_OK)
-    return (pkv_status)st;
+  const cudaError_t e =
+      path.tcgen05
+          ? pkv::launch_prefill_tree(v, layer, q, num_q_heads, scale, block_tables, p.plan, q_pos,
+                                     p.mask, mask_words, p.part, out, err, sms, stream)
+          : pkv::launch_rows(v, p, true, path.grid, dev, stream);
+  if ((st = pkv::launch_status(e)) != PKV_OK) return (pkv_status)st;
   pkv::CombineParams m = {};
   m.plan = p.plan;
   m.part = p.part;
@@ -291,7 +303,9 @@ pkv_status pkv_decode_attention_tree(const pkv_pool* pool, int32_t layer, const 
   m.grid = path.grid;
   m.blocks_seq = (int)(((int64_t)max_q_len * num_q_heads + pkv::kCombineWarps - 1) /
                        pkv::kCombineWarps);
-  const auto kern = m.f32 ? pkv::tree_combine_kernel<32> : pkv::tree_combine_kernel<64>;
+  const auto kern = path.tcgen05 ? pkv::tree_combine_kernel<128>
+                    : m.f32      ? pkv::tree_combine_kernel<32>
+                                 : pkv::tree_combine_kernel<64>;
   st = pkv::launch_status(pkv::launch_kernel(kern, dim3((unsigned)(m.blocks_seq * batch)),
                                              dim3(pkv::kCombineWarps * 32), 0, stream, true, m));
   if (st != PKV_OK) return (pkv_status)st;
@@ -323,8 +337,13 @@ pkv_status pkv_prefill_attention_window(const pkv_pool* pool, int32_t layer, con
   if (validate && (st = pkv::validate_call(p, stream)) != PKV_OK) return (pkv_status)st;
   p.units_max = (int)(((int64_t)max_q_len * p.plan.G + 63) / 64);
   const long long grid = (long long)p.units_max * batch * v.num_kv_heads;
-  if ((st = pkv::launch_status(pkv::launch_rows(v, p, false, grid, dev, stream))) != PKV_OK)
-    return (pkv_status)st;
+  const cudaError_t e =
+      pkv::prefill_supported(v, num_q_heads) == 0
+          ? pkv::launch_prefill(v, layer, q, num_q_heads, scale, block_tables, max_blocks_per_seq,
+                                seq_lens, offsets, cu_q, batch, total_q, max_q_len, window,
+                                p.plan.span.sink, out, err, sms, stream)
+          : pkv::launch_rows(v, p, false, grid, dev, stream);
+  if ((st = pkv::launch_status(e)) != PKV_OK) return (pkv_status)st;
   return validate ? (pkv_status)pkv::read_and_clear_error_word(err, stream) : PKV_OK;
 }
 
