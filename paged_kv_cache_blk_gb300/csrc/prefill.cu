@@ -598,7 +598,7 @@ struct TreeCursor {
         ++b;
         continue;
       }
-      const long long unit = (at - first) / q.t.nt;
+      const long long unit = div_pos(at - first, q.t.nt);
       it = Item{};
       it.valid = true;
       it.b = b;
@@ -793,15 +793,15 @@ __global__ void __launch_bounds__((pf_threads<MODE, SHARE>()), 1)
   [[maybe_unused]] TreeCursor cur;
   if constexpr (TREE) {
     long long* scratch = reinterpret_cast<long long*>(s_items);  // (before the first item)
-    const long long total = plan_tiles<kKeys>(p.plan, p.batch, scratch);
-    const long long chunk = plan_chunk(p.plan, total, gridDim.x);
-    cur.at = min(total, blockIdx.x * chunk);
-    cur.end = min(total, cur.at + chunk);
+    const PlanShare share = plan_share<kKeys>(p.plan, blockIdx.x, gridDim.x, scratch);
+    cur.at = share.at;
+    cur.end = share.end;
+    cur.first = share.first;
+    cur.b = share.b;
     if (blockIdx.x == 0) {
       for (int b = tid; b < p.batch; b += blockDim.x)
         if (seq_span(p.plan.span, b).bad) set_error(p.err, kErrCapacity);
     }
-    cur.b = cur.at < cur.end ? plan_find<kKeys>(p.plan, cur.at, scratch, &cur.first) : 0;
     __syncthreads();
   }
   // the next item and the one whose tiles are streamed: c counts the CTA's items

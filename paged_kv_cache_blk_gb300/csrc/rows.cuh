@@ -125,6 +125,15 @@ struct RowsLayout {
   static constexpr int kSmem = kRing > kMerge ? kRing : kMerge;
 };
 
+// CTAs that an SM holds at once, of the tree kernel its grid: what shared memory allows, up to
+// three (two with head_dim 128 but for int8), which then share the registers.
+template <int MODE, int D>
+constexpr int rows_ctas() {
+  constexpr int fit = 227 * 1024 / (RowsLayout<MODE, D, 4>::kSmem + 2048);
+  constexpr int most = D == 64 || MODE == PKV_I8 ? 3 : 2;
+  return fit < most ? fit : most;
+}
+
 // One unit's work: rows first_row .. of sequence b, kv head g, tiles t0 .. t1 of its list.
 struct RowsPiece {
   SeqSpan s;
@@ -584,23 +593,20 @@ __device__ __forceinline__ void rows_piece(const RowsParams& p, const RowsPiece&
 
 // Tree: the batch's tiles split evenly over the grid (span.cuh).
 template <int MODE, int D, int WR>
-__global__ void __launch_bounds__(kRowsThreads) rows_tree_kernel(const RowsParams p) {
+__global__ void __launch_bounds__(kRowsThreads, (rows_ctas<MODE, D>())) rows_tree_kernel(const RowsParams p) {
   constexpr int KT = RowsTile<MODE, D>::kKeys, M = 16 * WR;
   extern __shared__ __align__(128) unsigned char smem[];
   __shared__ long long scratch[32];
   griddep_wait();
   griddep_launch_dependents();
-  const long long total = plan_tiles<KT>(p.plan, p.plan.span.batch, scratch);
-  const long long chunk = plan_chunk(p.plan, total, gridDim.x);
-  long long at = blockIdx.x * chunk;
-  const long long end = min(total, at + chunk);
+  const PlanShare share = plan_share<KT>(p.plan, blockIdx.x, gridDim.x, scratch);
+  long long at = share.at, first = share.first;
+  const long long end = share.end;
+  int b = share.b;
   if (blockIdx.x == 0) {
-    for (int b = threadIdx.x; b < p.plan.span.batch; b += blockDim.x)
-      if (seq_span(p.plan.span, b).bad) set_error(p.err, kErrCapacity);
+    for (int i = threadIdx.x; i < p.plan.span.batch; i += blockDim.x)
+      if (seq_span(p.plan.span, i).bad) set_error(p.err, kErrCapacity);
   }
-  if (at >= end) return;
-  long long first;
-  int b = plan_find<KT>(p.plan, at, scratch, &first);
   while (at < end) {
     const SeqPlan q = seq_plan<KT>(p.plan, b);
     if (at >= first + q.tiles) {  // the next sequence
@@ -608,7 +614,7 @@ __global__ void __launch_bounds__(kRowsThreads) rows_tree_kernel(const RowsParam
       ++b;
       continue;
     }
-    const long long unit = (at - first) / q.t.nt;
+    const long long unit = div_pos(at - first, q.t.nt);
     RowsPiece w;
     w.s = q.s;
     w.t = q.t;
@@ -629,7 +635,7 @@ __global__ void __launch_bounds__(kRowsThreads) rows_tree_kernel(const RowsParam
 
 // Prefill: a unit a CTA, whole, the longest first.
 template <int MODE, int D>
-__global__ void __launch_bounds__(kRowsThreads) rows_prefill_kernel(const RowsParams p) {
+__global__ void __launch_bounds__(kRowsThreads, (rows_ctas<MODE, D>())) rows_prefill_kernel(const RowsParams p) {
   constexpr int KT = RowsTile<MODE, D>::kKeys, M = 64;
   extern __shared__ __align__(128) unsigned char smem[];
   griddep_wait();
@@ -680,13 +686,6 @@ cudaError_t launch_rows_d(const RowsParams& p, bool tree, long long grid, int de
 }
 
 }  // namespace
-
-// CTAs of 4 warps that an SM holds at once (rows_*.cu): the grid of the tree kernel.
-template <int MODE, int D>
-constexpr int rows_ctas() {
-  constexpr int n = 227 * 1024 / (RowsLayout<MODE, D, 4>::kSmem + 2048);
-  return n < 3 ? n : 3;
-}
 
 // One translation unit a pool type.
 cudaError_t launch_rows_bf16(const RowsParams& p, int D, bool tree, long long grid, int dev, cudaStream_t s);

@@ -116,68 +116,95 @@ __device__ __forceinline__ SeqPlan seq_plan(const PlanParams& p, int b) {
   return q;
 }
 
-// Sum of x over the block; s: 32 words of shared memory.  Every thread gets it.
-__device__ __forceinline__ long long block_sum(long long x, long long* s) {
-#pragma unroll
-  for (int o = 16; o; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
-  const int warp = threadIdx.x >> 5;
-  __syncthreads();
-  if ((threadIdx.x & 31) == 0) s[warp] = x;
-  __syncthreads();
-  x = 0;
-  for (int w = 0; w < (int)(blockDim.x >> 5); ++w) x += s[w];
-  return x;
-}
-
-// Tiles of the sequences before sequence `end`, over the whole block.
-template <int KT>
-__device__ __forceinline__ long long plan_tiles(const PlanParams& p, int end, long long* s) {
-  long long x = 0;
-  for (int b = threadIdx.x; b < end; b += blockDim.x) x += seq_plan<KT>(p, b).tiles;
-  return block_sum(x, s);
+// a / b for positive numbers, by the short division where they fit.
+__device__ __forceinline__ long long div_pos(long long a, long long b) {
+  if (((a | b) >> 32) == 0) return (uint32_t)a / (uint32_t)b;
+  return a / b;
 }
 
 __device__ __forceinline__ long long plan_chunk(const PlanParams& p, long long total, int grid) {
-  const long long c = (total + grid - 1) / grid;
+  const long long c = div_pos(total + grid - 1, grid);
   return c > p.least ? c : p.least;
 }
 
-// The sequence that holds tile `at` of the line, and its first tile: over the whole block.
-template <int KT>
-__device__ __forceinline__ int plan_find(const PlanParams& p, long long at, long long* s,
-                                         long long* first) {
-  __shared__ int found;
-  __shared__ long long found_first;
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  long long base = 0;
-  if (tid == 0) found = p.span.batch;
-  for (int b0 = 0; b0 < p.span.batch; b0 += blockDim.x) {
-    const int b = b0 + tid;
-    const long long mine = b < p.span.batch ? seq_plan<KT>(p, b).tiles : 0;
-    long long incl = mine;
+// What the merge needs of the line: its length, and the tiles before one sequence.
+struct PlanSums {
+  long long total, before;
+};
+
+// A CTA's share: tiles at .. end - 1, the first of them in sequence b, whose own tiles begin
+// at `first`.
+struct PlanShare {
+  long long at, end, first;
+  int b;
+};
+
+// Inclusive sum of x over the threads of the block, and the sum over all (s: 32 words of shared
+// memory).
+__device__ __forceinline__ long long block_scan(long long x, long long* s, long long* all) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const long long y = __shfl_up_sync(0xffffffffu, incl, o);
-      if (lane >= o) incl += y;
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long y = __shfl_up_sync(0xffffffffu, x, o);
+    if (lane >= o) x += y;
+  }
+  __syncthreads();
+  if (lane == 31) s[warp] = x;
+  __syncthreads();
+  long long sum = 0;
+  for (int w = 0; w < (int)(blockDim.x >> 5); ++w) {
+    if (w < warp) x += s[w];
+    sum += s[w];
+  }
+  *all = sum;
+  return x;
+}
+
+// Over the whole block, which looks at each sequence once.
+template <int KT>
+__device__ __forceinline__ PlanSums plan_sums(const PlanParams& p, int seq, long long* s) {
+  long long all = 0, before = 0;
+  for (int b = threadIdx.x; b < p.span.batch; b += blockDim.x) {
+    const long long tiles = seq_plan<KT>(p, b).tiles;
+    all += tiles;
+    before += b < seq ? tiles : 0;
+  }
+  PlanSums r;
+  block_scan(all, s, &r.total);
+  block_scan(before, s, &r.before);
+  return r;
+}
+
+// Over the whole block.  Batches of up to blockDim.x sequences take one look at each.
+template <int KT>
+__device__ __forceinline__ PlanShare plan_share(const PlanParams& p, int cta, int grid,
+                                                long long* s) {
+  __shared__ PlanShare found;
+  const int n = (int)blockDim.x, tid = threadIdx.x;
+  const bool once = p.span.batch <= n;
+  long long mine = tid < p.span.batch ? seq_plan<KT>(p, tid).tiles : 0;
+  long long total, incl = block_scan(mine, s, &total);
+  for (int b0 = n; b0 < p.span.batch; b0 += n) {
+    long long all;
+    block_scan(b0 + tid < p.span.batch ? seq_plan<KT>(p, b0 + tid).tiles : 0, s, &all);
+    total += all;
+  }
+  const long long chunk = plan_chunk(p, total, grid);
+  const long long at = min(total, cta * chunk), end = min(total, at + chunk);
+  if (at >= end) return PlanShare{at, end, 0, 0};
+  long long base = 0;
+  for (int b0 = 0;; b0 += n) {
+    long long all = total;
+    if (!once) {
+      mine = b0 + tid < p.span.batch ? seq_plan<KT>(p, b0 + tid).tiles : 0;
+      incl = block_scan(mine, s, &all);
     }
-    __syncthreads();
-    if (lane == 31) s[warp] = incl;
-    __syncthreads();
-    long long before = base, all = 0;
-    for (int w = 0; w < (int)(blockDim.x >> 5); ++w) {
-      if (w < warp) before += s[w];
-      all += s[w];
-    }
-    const long long end = before + incl, begin = end - mine;
-    if (at >= begin && at < end) {
-      found = b;
-      found_first = begin;
-    }
+    const long long stop = base + incl;
+    if (at >= stop - mine && at < stop) found = PlanShare{at, end, stop - mine, b0 + tid};
     base += all;
     if (at < base) break;
   }
   __syncthreads();
-  *first = found_first;
   return found;
 }
 

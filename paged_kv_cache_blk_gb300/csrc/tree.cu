@@ -10,6 +10,7 @@ namespace {
 
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr int kCombineWarps = 8;
+constexpr int kInFlight = 8;  // states that a warp of the merge loads at once
 
 struct CombineParams {
   PlanParams plan;
@@ -17,69 +18,58 @@ struct CombineParams {
   char* out;
   int hq, D, f32, grid;  // grid: CTAs of the kernel that left the states
   int blocks_seq;        // CTAs of a sequence
+  int rows_warp;         // rows a warp takes, one after the other
 };
 
-// A warp a (token, query head): the states of its unit in the CTAs that shared it, by the
-// log-sum-exp rule.  Rows that one CTA finished are left alone.
-template <int KT>
-__global__ void __launch_bounds__(kCombineWarps * 32) tree_combine_kernel(const CombineParams p) {
-  __shared__ long long scratch[32];
-  griddep_wait();
-  griddep_launch_dependents();
-  const int b = blockIdx.x / p.blocks_seq;
-  const int first_row = (blockIdx.x - b * p.blocks_seq) * kCombineWarps;
-  const SeqPlan q = seq_plan<KT>(p.plan, b);
-  if (first_row >= q.s.n * p.hq) return;
-  // tiles of the batch, and of the sequences before this one
-  long long all = 0, before = 0;
-  for (int i = threadIdx.x; i < p.plan.span.batch; i += blockDim.x) {
-    const long long x = seq_plan<KT>(p.plan, i).tiles;
-    all += x;
-    before += i < b ? x : 0;
-  }
-  const long long chunk = plan_chunk(p.plan, block_sum(all, scratch), p.grid);
-  before = block_sum(before, scratch);
-  const int lane = threadIdx.x & 31, row = first_row + (threadIdx.x >> 5);
-  if (row >= q.s.n * p.hq) return;
+// One (token, query head) row, by one warp: the states of its unit in the CTAs that shared it,
+// by the log-sum-exp rule.  Rows that one CTA finished are left alone.
+__device__ __forceinline__ void combine_row(const CombineParams& p, const SeqPlan& q,
+                                            long long chunk, long long before, int row) {
+  const int lane = threadIdx.x & 31;
   const int tok = row / p.hq, h = row - tok * p.hq, g = h / p.plan.G;
   const int r = tok * p.plan.G + h - g * p.plan.G, ur = p.plan.unit_rows, unit = r / ur;
   const long long start = before + ((long long)g * q.nru + unit) * q.t.nt;
-  const long long c0 = start / chunk, c1 = (start + q.t.nt - 1) / chunk;
+  const long long c0 = div_pos(start, chunk), c1 = div_pos(start + q.t.nt - 1, chunk);
   if (c0 == c1) return;
   const long long row_floats = p.D + 4, slot = ur * row_floats;
   const float* at = p.part + (r - unit * ur) * row_floats;
-  // the first CTA began the unit (slot 2 c + 1) unless it starts exactly before its share
+  // (the CTA with the unit's first tile left its part in slot 2 c + 1)
   auto state = [&](long long c) { return at + (2 * c + (c == c0 ? 1 : 0)) * slot; };
-  const int pieces = (int)(c1 - c0) + 1;
-  float top = -INFINITY;
-  for (int i = lane; i < pieces; i += 32) top = fmaxf(top, state(c0 + i)[0]);
+  const int pieces = (int)(c1 - c0) + 1, d = lane * 4;
+  float top = -INFINITY, sum = 0.f, x[4] = {0.f, 0.f, 0.f, 0.f};
+  // a state's numbers and values are loaded together: one round trip for kInFlight of them
+  for (int i0 = 0; i0 < pieces; i0 += kInFlight) {
+    float2 ml[kInFlight];
+    float4 y[kInFlight];
 #pragma unroll
-  for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(kAllLanes, top, o));
-  const int d = lane * 4;
-  float sum = 0.f, x[4] = {0.f, 0.f, 0.f, 0.f};
-  for (int i0 = 0; i0 < pieces; i0 += 32) {
-    float f = 0.f;
-    if (i0 + lane < pieces) {
-      const float2 ml = *reinterpret_cast<const float2*>(state(c0 + i0 + lane));
-      // a state at -inf saw nothing, or only NaN: its sum and O are 0, or NaN
-      f = ml.x == -INFINITY ? 1.f : exp2f(ml.x - top);
-      sum += f * ml.y;
-    }
-    const int m = min(32, pieces - i0);
-#pragma unroll 4
-    for (int j = 0; j < m; ++j) {
-      const float fj = __shfl_sync(kAllLanes, f, j);
-      if (d < p.D) {
-        const float4 y = *reinterpret_cast<const float4*>(state(c0 + i0 + j) + 4 + d);
-        x[0] += fj * y.x;
-        x[1] += fj * y.y;
-        x[2] += fj * y.z;
-        x[3] += fj * y.w;
+    for (int u = 0; u < kInFlight; ++u) {
+      ml[u] = make_float2(-INFINITY, 0.f);
+      y[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (i0 + u < pieces) {
+        const float* s = state(c0 + i0 + u);
+        ml[u] = *reinterpret_cast<const float2*>(s);
+        if (d < p.D) y[u] = *reinterpret_cast<const float4*>(s + 4 + d);
       }
     }
-  }
+    float most = top;
 #pragma unroll
-  for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(kAllLanes, sum, o);
+    for (int u = 0; u < kInFlight; ++u) most = fmaxf(most, ml[u].x);
+    const float shrink = most == top ? 1.f : exp2f(top - most);
+    top = most;
+    sum *= shrink;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) x[e] *= shrink;
+#pragma unroll
+    for (int u = 0; u < kInFlight; ++u) {
+      // a state at -inf saw nothing, or only NaN: its sum and O are 0, or NaN
+      const float f = ml[u].x == -INFINITY ? 1.f : exp2f(ml[u].x - top);
+      sum += f * ml[u].y;
+      x[0] += f * y[u].x;
+      x[1] += f * y[u].y;
+      x[2] += f * y[u].z;
+      x[3] += f * y[u].w;
+    }
+  }
   if (d >= p.D) return;
   const float inv = sum == 0.f ? 0.f : 1.f / sum;  // no weight at all: zeros
   const long long dst = ((q.s.q0 + tok) * p.hq + h) * p.D + d;
@@ -89,6 +79,31 @@ __global__ void __launch_bounds__(kCombineWarps * 32) tree_combine_kernel(const 
   else
     *reinterpret_cast<uint2*>(p.out + dst * 2) =
         make_uint2(pack_bf16x2(x[0] * inv, x[1] * inv), pack_bf16x2(x[2] * inv, x[3] * inv));
+}
+
+// A CTA takes kCombineWarps * rows_warp rows of one sequence.
+template <int KT>
+__global__ void __launch_bounds__(kCombineWarps * 32) tree_combine_kernel(const CombineParams p) {
+  __shared__ long long scratch[32];
+  // What stands before the wait reads inputs alone, which were complete when the grid that
+  // leaves the states let this one launch: it runs beside that grid's end.
+  const int b = blockIdx.x / p.blocks_seq;
+  const int first_row = (blockIdx.x - b * p.blocks_seq) * (kCombineWarps * p.rows_warp);
+  const SeqPlan q = seq_plan<KT>(p.plan, b);
+  if (first_row >= q.s.n * p.hq) {
+    griddep_wait();
+    griddep_launch_dependents();
+    return;
+  }
+  const PlanSums sums = plan_sums<KT>(p.plan, b, scratch);
+  const long long chunk = plan_chunk(p.plan, sums.total, p.grid), before = sums.before;
+  griddep_wait();
+  griddep_launch_dependents();
+  for (int i = 0; i < p.rows_warp; ++i) {
+    const int row = first_row + i * kCombineWarps + (int)(threadIdx.x >> 5);
+    if (row >= q.s.n * p.hq) break;
+    combine_row(p, q, chunk, before, row);
+  }
 }
 
 // One CTA a sequence: its numbers, and the entries of the blocks that hold a seen key.
@@ -301,8 +316,12 @@ pkv_status pkv_decode_attention_tree(const pkv_pool* pool, int32_t layer, const 
   m.D = v.head_dim;
   m.f32 = v.io_size == 4;
   m.grid = path.grid;
-  m.blocks_seq = (int)(((int64_t)max_q_len * num_q_heads + pkv::kCombineWarps - 1) /
-                       pkv::kCombineWarps);
+  // as many CTAs as the device holds about at once: each goes over the batch first
+  const int64_t rows = (int64_t)max_q_len * num_q_heads;
+  const int64_t all = rows * batch / pkv::kCombineWarps;
+  m.rows_warp = (int)std::max<int64_t>(1, std::min<int64_t>(64, all / (6 * sms)));
+  const int64_t cta_rows = (int64_t)pkv::kCombineWarps * m.rows_warp;
+  m.blocks_seq = (int)((rows + cta_rows - 1) / cta_rows);
   const auto kern = path.tcgen05 ? pkv::tree_combine_kernel<128>
                     : m.f32      ? pkv::tree_combine_kernel<32>
                                  : pkv::tree_combine_kernel<64>;
