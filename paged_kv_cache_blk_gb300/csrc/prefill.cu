@@ -112,8 +112,7 @@ struct PfParams {
   float* pre_ml;
   float* pre_acc;
   // windows and trees
-  int window, sink;
-  PlanParams plan;                 // trees
+  PlanParams plan;                 // (windows: its span alone)
   const int32_t* q_pos;            // as in RowsParams
   const unsigned long long* mask;
   int words;
@@ -309,39 +308,33 @@ __device__ __forceinline__ uint32_t column_bits(int a, int b, int c0) {
   return lo > hi ? 0u : (0xffffffffu << lo) & (0xffffffffu >> (31 - hi));
 }
 
-// Windows and trees: of the columns first .. top those before sink_end or from win on, and
-// the drafted columns behind top whose bit is set.
-struct SpanMask {
-  int first, top, sink_end, win;
-  int draft, drafted;  // column of drafted token 0, and their number (0: top says it all)
-  unsigned long long w0, w1;  // the first 128 bits
-  const unsigned long long* bits;
+// Windows and trees: which of a tile's columns a row sees, a bit each.
+struct WordMask {
+  uint32_t w[kKeys / 32];
   struct Chunk {
     uint32_t w;
     __device__ __forceinline__ bool none() const { return w == 0; }
     __device__ __forceinline__ bool all() const { return w == 0xffffffffu; }
     __device__ __forceinline__ bool sees(int j) const { return w >> j & 1; }
   };
-  __device__ __forceinline__ unsigned long long word(int i) const {
-    return i == 0 ? w0 : i == 1 ? w1 : bits[i];
-  }
   __device__ __forceinline__ Chunk chunk(int c0) const {
-    uint32_t w = column_bits(first, min(top, sink_end - 1), c0) | column_bits(max(first, win), top, c0);
-    const int d = c0 - draft;  // drafted token of the chunk's first column
-    if (drafted > 0 && d > -32 && d < drafted) {
-      unsigned long long x;
-      if (d < 0) {
-        x = w0 << -d;
-      } else {
-        x = word(d >> 6) >> (d & 63);
-        // (a second word where the chunk goes on in it and it holds drafted tokens)
-        if ((d & 63) > 32 && ((d >> 6) + 1) * 64 < drafted) x |= word((d >> 6) + 1) << (64 - (d & 63));
-      }
-      w |= (uint32_t)x & column_bits(0, drafted - 1, d);
-    }
-    return Chunk{w};
+    return Chunk{c0 < 64 ? (c0 == 0 ? w[0] : w[1]) : (c0 == 64 ? w[2] : w[3])};
   }
 };
+
+// 32 drafted tokens from number d on (which may lie before the first) of a row's mask.
+__device__ __forceinline__ uint32_t draft_bits(const unsigned long long* bits, int d, int n) {
+  if (d <= -32 || d >= n) return 0;
+  unsigned long long x;
+  if (d < 0) {
+    x = bits[0] << -d;
+  } else {
+    x = bits[d >> 6] >> (d & 63);
+    // (the next word where the 32 go on in it and it holds drafted tokens)
+    if ((d & 63) > 32 && ((d >> 6) + 1) * 64 < n) x |= bits[(d >> 6) + 1] << (64 - (d & 63));
+  }
+  return (uint32_t)x & column_bits(0, n - 1, d);
+}
 
 // Softmax of one S tile for one row: reads the row from TMEM, masks it,
 // updates the running state, rescales the O row when the maximum moved, and
@@ -498,9 +491,9 @@ struct Item {
   long long q0, nq, qtA, qtB, first_pos, spanned;
   int off;
   int t0, c;  // shared-prefix prefix pass: first key tile and split index
-  // windows and trees: tile i is the sequence's tile list.tile(t0 + i); `lo` the first key of
-  // the windows; trees: where a part's state goes (-1: a whole unit), and after the last item
-  TileList list;
+  // windows and trees: tile i is tile t0 + i of the list; `lo` the first key of the windows;
+  // trees: where a part's state goes (-1: a whole unit), and after the last item
+  KeyList list;
   int lo, slot;
   bool end;
 };
@@ -538,17 +531,21 @@ __device__ __forceinline__ Item make_item(const PfParams& p, long long i, int ti
     const long long last = min(it.nq, (qt + 1) * TQ) - 1;
     return (int)((it.off + it.first_pos + last) / kKeys) + 1;
   };
-  it.nA = tiles_for(it.qtA);
-  it.nB = tiles_for(it.qtB);
-  if constexpr (MODE == kWindow) {
+  if constexpr (MODE != kWindow) {
+    it.nA = tiles_for(it.qtA);
+    it.nB = tiles_for(it.qtB);
+  } else {
     // the list of all four query tiles of a CTA pair (items px & ~1 and px | 1), from the
     // window of their first token on
     const long long qt0 = ntq - 2 - 2 * (px | 1);
-    it.lo = window_start((int)(it.first_pos + max(0ll, qt0) * TQ), p.window);
-    it.list = tile_list<kKeys>(it.off, it.lo, (int)len - 1, p.sink);
-    const int skipped = it.list.w0 - it.list.ns;
-    if (it.nA > 0) it.nA -= skipped;
-    it.nB -= skipped;
+    it.lo = window_start((int)(it.first_pos + max(0ll, qt0) * TQ), p.plan.span.window);
+    it.list = key_list<kKeys>(p.plan.span, it.off, it.lo, (int)len - 1);
+    auto listed = [&](long long qt) {
+      const int last = (int)(min(it.nq, (qt + 1) * TQ) - 1 + it.first_pos) + it.off;
+      return qt < 0 ? 0 : it.list.behind(last) / kKeys + 1;
+    };
+    it.nA = listed(it.qtA);
+    it.nB = listed(it.qtB);
   }
   it.spanned = ((long long)it.off + len + p.bs - 1) / p.bs;
   it.valid = true;
@@ -611,7 +608,7 @@ struct TreeCursor {
       it.first_pos = q.s.ctx;
       it.spanned = ((long long)q.s.off + q.s.ctx + q.s.n + p.bs - 1) / p.bs;
       it.list = q.t;
-      it.lo = window_start(q.s.ctx, p.window);
+      it.lo = window_start(q.s.ctx, p.plan.span.window);
       it.t0 = (int)(at - first - unit * q.t.nt);
       it.nB = (int)min((long long)(q.t.nt - it.t0), end - at);
       it.nA = it.qtA * p.TQ < it.nq ? it.nB : 0;
@@ -623,31 +620,26 @@ struct TreeCursor {
   }
 };
 
-// Windows and trees: a block is needed if it holds a first token or a key from `lo` on
-// (the others' table entries are not looked up), and the V rows of a tile that hold neither,
-// or lie outside the sequence, are cleared: their P is 0, but 0 times what they hold need not be.
-__device__ __forceinline__ bool block_needed(const PfParams& p, const Item& it, long long lb) {
-  const long long first = lb * p.bs;
-  return first + p.bs > it.off + it.lo || (p.sink > 0 && first < (long long)it.off + p.sink);
-}
-// Rows hide_lo .. hide_hi - 1 of the sequence's table positions, and those outside
-// off .. end - 1, are not seen by any query of the item's CTA pair.
+// Windows and trees: the V rows of a tile that no query sees (of the item's CTA pair, or of the
+// tree) are cleared: their P is 0, but 0 times what they hold need not be.  Of the list's
+// places these are the ones outside first .. end - 1 and from hide_lo to hide_hi - 1.
 struct SeenRows {
-  int off, end, hide_lo, hide_hi;
-  __device__ __forceinline__ bool whole(int p0) const {
-    return p0 >= off && p0 + kKeys <= end && (p0 >= hide_hi || p0 + kKeys <= hide_lo);
+  int first, end, hide_lo, hide_hi;
+  __device__ __forceinline__ bool whole(int x0) const {
+    return x0 >= first && x0 + kKeys <= end && (x0 >= hide_hi || x0 + kKeys <= hide_lo);
   }
-  __device__ __forceinline__ bool has(int pos) const {
-    return pos >= off && pos < end && (pos < hide_lo || pos >= hide_hi);
+  __device__ __forceinline__ bool has(int x) const {
+    return x >= first && x < end && (x < hide_lo || x >= hide_hi);
   }
 };
 __device__ __forceinline__ SeenRows seen_rows(const PfParams& p, const Item& it) {
-  return SeenRows{it.off, it.off + p.lens[it.b], it.off + p.sink, it.off + it.lo};
+  return SeenRows{it.list.first(it.off), it.list.behind(it.off + p.lens[it.b]),
+                  it.list.first(it.off + p.plan.span.sink), it.list.behind(it.off + it.lo)};
 }
 // A warp clears the rows of 128 bytes of a loaded half tile that are not seen.
-__device__ __forceinline__ void clear_rows(uint32_t half, const SeenRows& s, int p0, int lane) {
+__device__ __forceinline__ void clear_rows(uint32_t half, const SeenRows& s, int x0, int lane) {
   for (int r = lane >> 3; r < kKeys; r += 4) {
-    if (!s.has(p0 + r))
+    if (!s.has(x0 + r))
       asm volatile("st.shared.v4.u32 [%0], {%1,%1,%1,%1};" ::"r"(half + r * 128 + (lane & 7) * 16),
                    "r"(0)
                    : "memory");
@@ -881,10 +873,10 @@ __global__ void __launch_bounds__((pf_threads<MODE, SHARE>()), 1)
         for (int k2 = lane; k2 < (SHARE ? 1 : 2) * blocks_per_tile; k2 += 32) {
           const int h = SHARE ? (int)rank : k2 / blocks_per_tile;
           const int k = SHARE ? k2 : k2 % blocks_per_tile;
-          const int tile = SPAN ? lead.list.tile(lead.t0 + t) : PREFIX ? lead.t0 + t : t;
-          const long long lb = (long long)tile * blocks_per_tile + k;
+          long long lb = (long long)(PREFIX || SPAN ? lead.t0 + t : t) * blocks_per_tile + k;
+          if constexpr (SPAN) lb = lead.list.position((int)lb * p.bs) / p.bs;
           long long coord = p.blk_coord_limit;                       // out of range: zeros
-          if (lb < lead.spanned && (!SPAN || block_needed(p, lead, lb))) {
+          if (lb < lead.spanned) {
             const int blk = p.bt[(long long)lead.b * p.mb + lb];
             if (blk >= 0 && blk < p.num_blocks) {
               coord = (long long)blk * p.L + p.layer;
@@ -941,9 +933,9 @@ __global__ void __launch_bounds__((pf_threads<MODE, SHARE>()), 1)
             break;
           }
           if constexpr (SPAN) {
-            const int p0 = lead.list.tile(li >> 1) * kKeys;
-            if ((li & 1) && !seen.whole(p0))
-              clear_rows(smem_addr(slot_ptr(slot)) + half_off, seen, p0, lane);
+            const int x0 = (li >> 1) * kKeys;
+            if ((li & 1) && !seen.whole(x0))
+              clear_rows(smem_addr(slot_ptr(slot)) + half_off, seen, x0, lane);
             if (lane != 0) continue;
           }
           mbar_arrive_expect_tx(slot_full(slot), kHalf);
@@ -966,10 +958,10 @@ __global__ void __launch_bounds__((pf_threads<MODE, SHARE>()), 1)
           ok = false;
           break;
         }
-        const int p0 = it.list.tile(it.t0 + t) * kKeys;
-        if (!seen.whole(p0)) {
-          clear_rows(smem_addr(slot_ptr(slot)), seen, p0, lane);
-          clear_rows(smem_addr(slot_ptr(slot)) + kHalf, seen, p0, lane);
+        const int x0 = (it.t0 + t) * kKeys;
+        if (!seen.whole(x0)) {
+          clear_rows(smem_addr(slot_ptr(slot)), seen, x0, lane);
+          clear_rows(smem_addr(slot_ptr(slot)) + kHalf, seen, x0, lane);
         }
         if (lane == 0) mbar_arrive(slot_full(slot));
       }
@@ -1150,24 +1142,22 @@ __global__ void __launch_bounds__((pf_threads<MODE, SHARE>()), 1)
           key_hi = min((long long)p.prefix_blocks * p.bs, ob + lb);
         }
       }
-      // windows and trees, in table positions: the row sees first .. top, of these the first
-      // tokens and those from win on, and drafted tokens behind top by their bits
-      [[maybe_unused]] SpanMask span;
-      [[maybe_unused]] int span_top = 0, span_win = 0;
+      // windows and trees: of the list's places the row sees those up to s_top that are first
+      // tokens or s_win or later, and drafted tokens by their bits
+      [[maybe_unused]] int s_top = -1, s_win = 0;
+      [[maybe_unused]] const unsigned long long* s_bits = nullptr;
       if constexpr (SPAN) {
-        const long long qrow = it.q0 + (row_ok ? qi : 0);
-        const bool masked = TREE && p.mask != nullptr;
-        span_top = row_ok ? it.off + (int)(masked ? it.first_pos - 1 : pos) : -1;
-        long long at = pos;
-        if (TREE && p.q_pos) at = max(it.first_pos, (long long)p.q_pos[qrow]);
-        if (p.window > 0)
-          span_win = it.off + (int)max(0ll, min(at - p.window + 1, kMaxPositions - 2048));
-        span.drafted = masked && row_ok ? (int)it.nq : 0;
-        span.w0 = span.w1 = 0;
-        span.bits = masked ? p.mask + qrow * p.words : nullptr;
-        if (masked) {
-          span.w0 = span.bits[0];
-          if (p.words > 1) span.w1 = span.bits[1];
+        if (row_ok) {
+          long long at = pos;
+          s_top = it.list.last(it.off + (int)pos);
+          if (TREE && p.mask) {
+            s_bits = p.mask + (it.q0 + qi) * p.words;
+            s_top = it.list.last(it.off + (int)it.first_pos - 1);
+            if (p.q_pos) at = max(it.first_pos, (long long)p.q_pos[it.q0 + qi]);
+          }
+          const int window = p.plan.span.window;
+          const long long first = window > 0 ? max(0ll, min(at - window + 1, kMaxPositions)) : 0;
+          s_win = it.list.behind(it.off + (int)first);
         }
       }
       RowState st{-INFINITY, 0.f};
@@ -1176,17 +1166,26 @@ __global__ void __launch_bounds__((pf_threads<MODE, SHARE>()), 1)
         if (!__all_sync(0xffffffffu, waited)) { ok = false; break; }
         tc_fence_after();
         if constexpr (SPAN) {
-          const int tp0 = it.list.tile(it.t0 + t) * kKeys;
-          span.first = it.off - tp0;
-          span.top = span_top - tp0;
-          span.sink_end = it.off + p.sink - tp0;
-          span.win = span_win - tp0;
-          span.draft = it.off + (int)it.first_pos - tp0;
+          const int x0 = (it.t0 + t) * kKeys, first = it.list.first(it.off) - x0;
+          const int sink_end = it.list.first(it.off + p.plan.span.sink) - x0;
+          const int top = s_top - x0, win = s_win - x0;
           // (a padding row may be taken for one that sees everything: it is not stored)
-          const bool full = !row_ok || (span.first <= 0 && span.top >= kKeys - 1 &&
-                                        (span.win <= 0 || span.sink_end >= kKeys));
-          softmax_tile(tS(x), tO(x), lane_base, t, span, __all_sync(0xffffffffu, full), p.qscale,
-                       st);
+          const bool full = __all_sync(
+              0xffffffffu,
+              !row_ok || (first <= 0 && top >= kKeys - 1 && (win <= 0 || sink_end >= kKeys)));
+          WordMask seen;
+#pragma unroll
+          for (int c = 0; c < kKeys / 32; ++c) {
+            seen.w[c] = 0;
+            if (!full) {
+              seen.w[c] = column_bits(first, min(top, sink_end - 1), 32 * c) |
+                          column_bits(max(first, win), top, 32 * c);
+              if (TREE && s_bits)
+                seen.w[c] |= draft_bits(
+                    s_bits, 32 * c + x0 - it.list.behind(it.off + (int)it.first_pos), (int)it.nq);
+            }
+          }
+          softmax_tile(tS(x), tO(x), lane_base, t, seen, full, p.qscale, st);
           tc_fence_before();
           __syncwarp();
           if (lane == 0) mbar_arrive(b_pfull);
@@ -1474,8 +1473,9 @@ cudaError_t launch_prefill(const PoolView& pv, int layer, const void* q, int num
   const long long ntq = (max_q_len + p.TQ - 1) / p.TQ;
   // CTA pairs: pairs of query-tile pairs per (sequence, kv head)
   p.n_items = ((ntq + 1) / 2 + 1) / 2 * (long long)batch * pv.num_kv_heads;
-  p.window = window;
-  p.sink = sink;
+  p.plan.span.window = window;
+  p.plan.span.sink = sink;
+  p.plan.span.gran = pv.block_size;
   return window > 0 ? prefill_launch_pairs<kWindow>(tq, tk, tv, p, sm_count, s)
                     : prefill_launch_pairs<kCausal>(tq, tk, tv, p, sm_count, s);
 }
@@ -1491,8 +1491,6 @@ cudaError_t launch_prefill_tree(const PoolView& pv, int layer, const void* q, in
                                       sp.batch, sp.total_q, err, &tq, &tk, &tv, &p);
   if (e != cudaSuccess) return e;
   p.out = out;
-  p.window = sp.window;
-  p.sink = sp.sink;
   p.plan = plan;
   p.q_pos = q_pos;
   p.mask = mask;

@@ -137,7 +137,7 @@ constexpr int rows_ctas() {
 // One unit's work: rows first_row .. of sequence b, kv head g, tiles t0 .. t1 of its list.
 struct RowsPiece {
   SeqSpan s;
-  TileList t;
+  KeyList t;
   int b, g, first_row, t0, t1;
   int lo, hi;    // keys that some row of the unit may see: lo .. hi, and the first ones
   float* part;   // where the state goes, or NULL: finished here
@@ -159,7 +159,7 @@ __device__ __forceinline__ void rows_piece(const RowsParams& p, const RowsPiece&
 
   // ---- copies: each warp a quarter of a tile's rows ----
   constexpr int RW = KT / kRowsWarps;
-  const int sink_end = off + p.plan.span.sink;
+  const int sink_end = off + p.plan.span.sink;  // table position
   const int my_r = warp * RW + lane % RW;  // the row of a tile that this lane looks up
   const int32_t* table = p.bt + (long long)w.b * p.plan.span.mb;
   auto seen_by_some = [&](int pos) {
@@ -167,13 +167,13 @@ __device__ __forceinline__ void rows_piece(const RowsParams& p, const RowsPiece&
   };
   auto lookup = [&](int i) -> int {  // block of the lane's row in tile i, INT_MIN: a row of zeros
     if (i >= w.t1) return INT_MIN;
-    const int pos = w.t.tile(i) * KT + my_r;
+    const int pos = w.t.position(i * KT + my_r);
     return seen_by_some(pos) ? table[pos >> p.bs_bits] : INT_MIN;
   };
   int ahead = lookup(w.t0);
   auto issue = [&](int i, int stage) {
     if (i < w.t1) {
-      const int pos = w.t.tile(i) * KT + my_r;
+      const int pos = w.t.position(i * KT + my_r);
       int blk = ahead;
       if (blk != INT_MIN && (blk < 0 || blk >= p.num_blocks)) {
         set_error(p.err, kErrIndex);
@@ -208,8 +208,8 @@ __device__ __forceinline__ void rows_piece(const RowsParams& p, const RowsPiece&
   };
 
   // ---- the warp's rows: row 0 is gl, row 1 is gl + 8 of its 16 ----
-  // a row sees table positions off .. top that are lo or later or first tokens, and, in a
-  // masked tree, of the positions behind top those with their bit
+  // a row sees the places first .. top of the list that are first tokens or lo or later, and,
+  // in a masked tree, of the places from draft on those with their bit
   int lo[2], top[2];
   const unsigned long long* bits[2];
   bool live_row[2];
@@ -222,25 +222,27 @@ __device__ __forceinline__ void rows_piece(const RowsParams& p, const RowsPiece&
     const int tok = live_row[i] ? r / G : 0, h = live_row[i] ? r - tok * G : 0;
     qrow[i] = (w.s.q0 + tok) * p.hq + w.g * G + h;
     int pos = w.s.ctx + tok;
-    top[i] = off + (masked_tree ? w.s.ctx - 1 : pos);
+    top[i] = w.t.last(off + (masked_tree ? w.s.ctx - 1 : pos));
     bits[i] = masked_tree ? p.mask + (w.s.q0 + tok) * p.words : nullptr;
-    lo[i] = 0;
+    lo[i] = w.t.behind(off);
     if (p.plan.span.window > 0) {
       if (TREE && p.q_pos) pos = max(w.s.ctx, p.q_pos[w.s.q0 + tok]);
       const long long first = (long long)pos - p.plan.span.window + 1;
-      lo[i] = off + (int)max(0ll, min(first, (long long)kMaxPositions - 2048));
+      lo[i] = w.t.behind(off + (int)max(0ll, min(first, kMaxPositions)));
     }
   }
-  auto sees = [&](int i, int pos) -> bool {
-    if (pos <= top[i]) return pos >= off && (pos >= lo[i] || pos < sink_end);
+  const int first_place = w.t.first(off), sink_place = w.t.first(sink_end);
+  const int draft = w.t.behind(off + w.s.ctx);
+  auto sees = [&](int i, int x) -> bool {
+    if (x <= top[i]) return x >= first_place && (x >= lo[i] || x < sink_place);
     if (!TREE || bits[i] == nullptr) return false;
-    const int d = pos - top[i] - 1;
-    return d < n && (bits[i][d >> 6] >> (d & 63) & 1);
+    const int d = x - draft;
+    return d >= 0 && d < n && (bits[i][d >> 6] >> (d & 63) & 1);
   };
   // keys from full_lo to full_hi are seen by every row of the warp
-  int full_lo = max(live_row[0] ? lo[0] : 0, live_row[1] ? lo[1] : 0);
+  int full_lo = max(live_row[0] ? lo[0] : INT_MIN, live_row[1] ? lo[1] : INT_MIN);
   int full_hi = min(live_row[0] ? top[0] : INT_MAX, live_row[1] ? top[1] : INT_MAX);
-  full_lo = max(off, __reduce_max_sync(kAllLanes, full_lo));
+  full_lo = max(first_place, __reduce_max_sync(kAllLanes, full_lo));
   full_hi = __reduce_min_sync(kAllLanes, full_hi);
 
   // Q in the registers of the A operand
@@ -380,7 +382,7 @@ __device__ __forceinline__ void rows_piece(const RowsParams& p, const RowsPiece&
       if constexpr (kI8) return (j >> 1) * 16 + 4 * qi + (j & 1) * 2 + c;
       return j * 8 + 2 * qi + c;
     };
-    const int p0 = w.t.tile(i) * KT + k0;
+    const int p0 = i * KT + k0;
     const bool full = p0 >= full_lo && p0 + KW - 1 <= full_hi;
     float mx[2] = {-INFINITY, -INFINITY};
     [[maybe_unused]] float scale_v[NT][2];
@@ -653,7 +655,7 @@ __global__ void __launch_bounds__(kRowsThreads, (rows_ctas<MODE, D>())) rows_pre
   const int tok1 = min(w.s.n - 1, (w.first_row + M - 1) / p.plan.G);
   w.lo = window_start(w.s.ctx + tok0, p.plan.span.window);
   w.hi = w.s.ctx + tok1;
-  w.t = tile_list<KT>(w.s.off, w.lo, w.hi, p.plan.span.sink);
+  w.t = key_list<KT>(p.plan.span, w.s.off, w.lo, w.hi);
   w.t0 = 0;
   w.t1 = w.t.nt;
   w.part = nullptr;

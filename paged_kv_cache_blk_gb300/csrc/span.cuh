@@ -21,6 +21,7 @@ struct SpanParams {
   int batch, mb, bs, max_q_len;
   int window;  // 0: none
   int sink;    // at most kMaxPositions
+  int gran;    // lists of keys begin at multiples of it (a power of two, up to a key tile)
 };
 
 // The new tokens of sequence b: query rows q0 .. q0 + n - 1, its last n positions.
@@ -52,23 +53,32 @@ __device__ __forceinline__ SeqSpan seq_span(const SpanParams& p, int b) {
   return s;
 }
 
-// Key tiles of KT table positions that hold a key which some of the queries see: the
-// queries' windows begin at key lo or later and they see keys up to hi; ns tiles of
-// first tokens from tile s0 on, then the tiles from w0 on, nt in all.
-struct TileList {
-  int s0, ns, w0, nt;
-  __device__ __forceinline__ int tile(int i) const { return i < ns ? s0 + i : w0 + (i - ns); }
+// The keys that some of the queries see, in a row: the first tokens, then those from the
+// earliest window on, each from and up to a multiple of `gran` table positions.  Place x of
+// the list holds table position x + s0 where x < head, x + shift behind; tile i is places
+// i KT .. i KT + KT - 1, nt tiles in all.  (Where the two parts meet, s0 = shift.)
+struct KeyList {
+  int s0, head, shift, nt;
+  __device__ __forceinline__ int position(int x) const { return x + (x < head ? s0 : shift); }
+  // places of table positions: of one among the first tokens, of one from the windows on, and
+  // of the last one that a row sees (which may lie before every window)
+  __device__ __forceinline__ int first(int pos) const { return pos - (head > 0 ? s0 : shift); }
+  __device__ __forceinline__ int behind(int pos) const { return pos - shift; }
+  __device__ __forceinline__ int last(int pos) const {
+    return pos - shift >= head ? pos - shift : min(pos - s0, head - 1);
+  }
 };
 
+// lo: the key that the earliest window begins with; hi: the last key.
 template <int KT>
-__device__ __forceinline__ TileList tile_list(int off, int lo, int hi, int sink) {
-  TileList t;
-  t.w0 = (off + lo) / KT;
-  t.s0 = off / KT;
-  const int s = sink < lo ? sink : lo;  // first tokens before the windows
-  t.ns = s > 0 ? min((off + s - 1) / KT + 1, t.w0) - t.s0 : 0;
-  t.ns = max(t.ns, 0);
-  t.nt = t.ns + (off + hi) / KT - t.w0 + 1;
+__device__ __forceinline__ KeyList key_list(const SpanParams& p, int off, int lo, int hi) {
+  KeyList t;
+  const int down = -p.gran, w0 = (off + lo) & down;
+  const int s = min(p.sink, lo);  // first tokens before the windows
+  t.s0 = off & down;
+  t.head = s > 0 ? max(0, min((off + s + p.gran - 1) & down, w0) - t.s0) : 0;
+  t.shift = w0 - t.head;
+  t.nt = (off + hi - t.shift + KT) / KT;
   return t;
 }
 
@@ -96,7 +106,7 @@ struct PlanParams {
 
 struct SeqPlan {
   SeqSpan s;
-  TileList t;
+  KeyList t;
   int nru;  // units of one kv head
   long long tiles;
 };
@@ -105,11 +115,11 @@ template <int KT>
 __device__ __forceinline__ SeqPlan seq_plan(const PlanParams& p, int b) {
   SeqPlan q;
   q.s = seq_span(p.span, b);
-  q.t = TileList{0, 0, 0, 0};
+  q.t = KeyList{0, 0, 0, 0};
   q.nru = 0;
   if (q.s.ok) {
-    q.t = tile_list<KT>(q.s.off, window_start(q.s.ctx, p.span.window), q.s.ctx + q.s.n - 1,
-                        p.span.sink);
+    q.t = key_list<KT>(p.span, q.s.off, window_start(q.s.ctx, p.span.window),
+                       q.s.ctx + q.s.n - 1);
     q.nru = (q.s.n * p.G + p.unit_rows - 1) / p.unit_rows;
   }
   q.tiles = (long long)q.t.nt * q.nru * p.hkv;

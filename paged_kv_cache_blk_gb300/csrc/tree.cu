@@ -215,6 +215,7 @@ RowsParams rows_params(const Call& c, const PoolView& v, int* err) {
   s.max_q_len = c.max_q_len;
   s.window = c.window;
   s.sink = c.sink < kMaxPositions ? c.sink : (int)kMaxPositions;
+  s.gran = 1;
   p.plan.G = c.num_q_heads / v.num_kv_heads;
   p.plan.hkv = v.num_kv_heads;
   p.plan.least = 1;
@@ -297,6 +298,7 @@ pkv_status pkv_decode_attention_tree(const pkv_pool* pool, int32_t layer, const 
   const pkv::TreePath path = pkv::tree_path(v, p.plan.G, max_q_len, sms);
   if (workspace_bytes < path.bytes) return PKV_ERR_WORKSPACE;
   p.plan.unit_rows = path.unit_rows;
+  if (path.tcgen05) p.plan.span.gran = v.block_size;  // (tensor copies of whole blocks)
   p.part = static_cast<float*>(workspace);
   p.mask = reinterpret_cast<const unsigned long long*>(tree_mask);
   p.words = mask_words;
