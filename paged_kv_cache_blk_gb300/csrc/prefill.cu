@@ -67,11 +67,13 @@ enum PfMode : int {
   kPrefix,  // prefix pass of shared-prefix decode
   kWindow,  // prefill under a sliding window and first tokens (span.cuh)
   kTree,    // drafted tokens over their context: parts of units (span.cuh), any mask
+  kNarrow,  // the same for up to 128 rows: both tiles are those rows, over half of the keys each
 };
+__host__ __device__ constexpr bool is_tree(int mode) { return mode == kTree || mode == kNarrow; }
 // threads of a CTA: one more warp in a CTA pair, and for trees
 template <int MODE, bool SHARE>
 constexpr int pf_threads() {
-  return (kPfWarps + (SHARE || MODE == kTree ? 1 : 0)) * 32;
+  return (kPfWarps + (SHARE || is_tree(MODE) ? 1 : 0)) * 32;
 }
 constexpr int kRows = 128;   // MMA M: query rows per tile
 constexpr int kKeys = 128;   // keys per KV tile (MMA N of Q K^T, K of P V)
@@ -138,6 +140,8 @@ __device__ __forceinline__ uint64_t desc_sw128(uint32_t saddr, uint32_t lbo, uin
 constexpr uint32_t kIdescKK =
     (1u << 4) | (1u << 7) | (1u << 10) | ((128u >> 3) << 17) | ((128u >> 4) << 24);
 constexpr uint32_t kIdescKMN = kIdescKK | (1u << 16);  // B MN-major
+// the same with N 64
+constexpr uint32_t kIdescHalf = kIdescKK ^ ((128u >> 3) << 17) ^ ((64u >> 3) << 17);
 
 __device__ __forceinline__ void umma(uint32_t d_tmem, uint64_t a, uint64_t b, uint32_t idesc,
                                      uint32_t accumulate) {
@@ -309,8 +313,9 @@ __device__ __forceinline__ uint32_t column_bits(int a, int b, int c0) {
 }
 
 // Windows and trees: which of a tile's columns a row sees, a bit each.
+template <int COLS>
 struct WordMask {
-  uint32_t w[kKeys / 32];
+  uint32_t w[COLS / 32];
   struct Chunk {
     uint32_t w;
     __device__ __forceinline__ bool none() const { return w == 0; }
@@ -318,7 +323,8 @@ struct WordMask {
     __device__ __forceinline__ bool sees(int j) const { return w >> j & 1; }
   };
   __device__ __forceinline__ Chunk chunk(int c0) const {
-    return Chunk{c0 < 64 ? (c0 == 0 ? w[0] : w[1]) : (c0 == 64 ? w[2] : w[3])};
+    if constexpr (COLS == 64) return Chunk{c0 == 0 ? w[0] : w[1]};
+    return Chunk{c0 < 64 ? (c0 == 0 ? w[0] : w[1]) : (c0 == 64 ? w[COLS / 32 - 2] : w[COLS / 32 - 1])};
   }
 };
 
@@ -340,7 +346,7 @@ __device__ __forceinline__ uint32_t draft_bits(const unsigned long long* bits, i
 // updates the running state, rescales the O row when the maximum moved, and
 // writes the row's P as bf16 pairs back into TMEM, where the P V product reads
 // it as its A operand.
-template <class Mask>
+template <int COLS, class Mask>
 __device__ __forceinline__ void softmax_tile(uint32_t tS, uint32_t tO, uint32_t lane_base, int t,
                                              const Mask& mask, bool full_tile, float qs,
                                              RowState& st) {
@@ -408,7 +414,7 @@ __device__ __forceinline__ void softmax_tile(uint32_t tS, uint32_t tO, uint32_t 
     // zeros); a padding row, all keys masked, keeps P = 0 throughout.
     float mu = st.m_used;
 #pragma unroll 1
-    for (int c0 = 0; c0 < kKeys; c0 += 32) {
+    for (int c0 = 0; c0 < COLS; c0 += 32) {
       float x[32];
       // in a masked tile (the causal diagonal) a chunk is often outside every
       // row's keys of the warp (its P is zero: no exponentials) or inside all
@@ -583,7 +589,8 @@ __device__ __forceinline__ Item make_item_prefix(const PfParams& p, long long i)
 }
 
 // Trees: the parts of units that make up this CTA's share, one after the other.  Tile B
-// holds a unit's first 128 rows, tile A the next where there are more.
+// holds a unit's first 128 rows, tile A the next where there are more (NARROW: the same rows).
+template <bool NARROW>
 struct TreeCursor {
   long long at, end, first;  // tiles of the line; first: that of sequence b
   int b;
@@ -600,8 +607,8 @@ struct TreeCursor {
       it.valid = true;
       it.b = b;
       it.g = (int)(unit / q.nru);
-      it.qtB = 2 * (unit - (long long)it.g * q.nru);
-      it.qtA = it.qtB + 1;
+      it.qtB = (NARROW ? 1 : 2) * (unit - (long long)it.g * q.nru);
+      it.qtA = it.qtB + (NARROW ? 0 : 1);
       it.q0 = q.s.q0;
       it.nq = q.s.n;
       it.off = q.s.off;
@@ -683,7 +690,9 @@ template <int MODE, bool SHARE>
 __global__ void __launch_bounds__((pf_threads<MODE, SHARE>()), 1)
     prefill_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk,
                    const __grid_constant__ CUtensorMap tv, const PfParams p) {
-  constexpr bool PREFIX = MODE == kPrefix, TREE = MODE == kTree, SPAN = MODE == kWindow || TREE;
+  constexpr bool PREFIX = MODE == kPrefix, TREE = is_tree(MODE), NARROW = MODE == kNarrow,
+                 SPAN = MODE == kWindow || TREE;
+  constexpr int COLS = NARROW ? kKeys / 2 : kKeys;  // keys of one S product
   static_assert(!((PREFIX || TREE) && SHARE), "the prefix pass and trees run on single CTAs");
   extern __shared__ __align__(1024) unsigned char smem_raw[];
   // Prefix pass of shared-prefix decode: it reads nothing the grid before it
@@ -706,7 +715,7 @@ __global__ void __launch_bounds__((pf_threads<MODE, SHARE>()), 1)
   // barriers: Q full, ring full[kSlots], ring empty[kSlots], then per tile
   // A / B: S ready, P written, O += P V done, O read by the epilogue, then
   // (CTA pairs) this CTA's own half of a slot loaded[kSlots]
-  static_assert((3 * kSlots + 12 + 2 * kItemRing) * 8 <= kOffTslot - kOffBar,
+  static_assert((3 * kSlots + 13 + 2 * kItemRing) * 8 <= kOffTslot - kOffBar,
                 "barriers overlap the TMEM address slot");
   static_assert(kItemRing * 2 * sizeof(Item) <= 1024, "item ring overflows its carve");
   const uint32_t b_qfull = smem_addr(&bars[0]);
@@ -724,6 +733,9 @@ __global__ void __launch_bounds__((pf_threads<MODE, SHARE>()), 1)
   // by the MMA warp, whose thread must keep issuing products
   const uint32_t b_ifull0 = smem_addr(&bars[12 + 3 * kSlots]);
   const uint32_t b_iempty0 = smem_addr(&bars[12 + 3 * kSlots + kItemRing]);
+  // narrow trees: maximum and sum of every row in both tiles (where the second Q tile would be)
+  const uint32_t b_mlfull = smem_addr(&bars[12 + 3 * kSlots + 2 * kItemRing]);
+  float2* s_ml = reinterpret_cast<float2*>(sQ + kTileBytes);
   Item* s_items = reinterpret_cast<Item*>(smem + kOffItems);
   auto slot_full = [&](int i) { return b_full0 + 8u * i; };
   auto slot_empty = [&](int i) { return b_empty0 + 8u * i; };
@@ -743,8 +755,9 @@ __global__ void __launch_bounds__((pf_threads<MODE, SHARE>()), 1)
       mbar_init(b_sfull0 + 8u * x, 1);
       mbar_init(b_pfull0 + 8u * x, 4);
       mbar_init(b_pvdone0 + 8u * x, 1);
-      mbar_init(b_ofree0 + 8u * x, 4);
+      mbar_init(b_ofree0 + 8u * x, NARROW ? 8 : 4);
     }
+    mbar_init(b_mlfull, 8);
     mbar_init(b_drain, 1);
     mbar_init(b_stall, 1);
     for (int r = 0; r < kItemRing; ++r) {
@@ -782,7 +795,7 @@ __global__ void __launch_bounds__((pf_threads<MODE, SHARE>()), 1)
     return !SHARE || rank == 0 ? own : make_item<MODE>(p, item_of(p, c, 0), tid);
   };
   // trees: this CTA's share of the line of tiles; every role walks it with its own copy
-  [[maybe_unused]] TreeCursor cur;
+  [[maybe_unused]] TreeCursor<NARROW> cur;
   if constexpr (TREE) {
     long long* scratch = reinterpret_cast<long long*>(s_items);  // (before the first item)
     const PlanShare share = plan_share<kKeys>(p.plan, blockIdx.x, gridDim.x, scratch);
@@ -846,8 +859,10 @@ __global__ void __launch_bounds__((pf_threads<MODE, SHARE>()), 1)
         // Q of this item once the previous item's S products have read the old one
         if (jq > 0 && !mbar_wait_sleep(b_qempty, (jq - 1) & 1, w)) { ok = false; break; }
         if (lane == 0) {
-          mbar_arrive_expect_tx(b_qfull, (it.nA > 0 ? 2 : 1) * kTileBytes);
-          for (int x = (it.nA > 0 ? 0 : 1); x < 2; ++x) {
+          // (narrow trees: one tile, in the place of A)
+          const int x_end = NARROW ? 1 : 2, x_begin = NARROW || it.nA > 0 ? 0 : 1;
+          mbar_arrive_expect_tx(b_qfull, (x_end - x_begin) * kTileBytes);
+          for (int x = x_begin; x < x_end; ++x) {
             const int z = (int)(it.q0 + (x == 0 ? it.qtA : it.qtB) * TQ);
             for (int h = 0; h < 2; ++h)
               tma_3d(smem_addr(sQ + x * kTileBytes + h * kHalf), &tq, h * 64, it.g * G, z,
@@ -1007,22 +1022,25 @@ __global__ void __launch_bounds__((pf_threads<MODE, SHARE>()), 1)
       // (the start address is the descriptor's low field, in 16-byte units;
       // shared addresses stay below 256 KB, so the addition never carries).
       auto issue_s = [&](int x, long long k_idx) {
-        const uint64_t a0 = desc_sw128(q_addr + x * kTileBytes, 16, 1024);
-        const uint64_t b0 = desc_sw128(smem_addr(slot_ptr(slot_of(k_idx))), 16, 1024);
+        // (narrow trees: the same rows, and the half of the keys that the tile takes)
+        const uint64_t a0 = desc_sw128(q_addr + (NARROW ? 0 : x * kTileBytes), 16, 1024);
+        const uint64_t b0 = desc_sw128(smem_addr(slot_ptr(slot_of(k_idx))) + (NARROW ? x * COLS * 128 : 0),
+                                       16, 1024);
         tc_fence_after();
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
           const uint64_t step = (uint64_t)(((k >> 2) * kHalf + (k & 3) * 32) >> 4);
-          umma(tS(x), a0 + step, b0 + step, kIdescKK, k > 0);
+          umma(tS(x), a0 + step, b0 + step, NARROW ? kIdescHalf : kIdescKK, k > 0);
         }
         umma_commit(b_sfull0 + 8u * x);
       };
       auto issue_pv = [&](int x, long long v_idx, bool first) {
-        const uint64_t b0 = desc_sw128(smem_addr(slot_ptr(slot_of(v_idx))), kHalf, 1024);
+        const uint64_t b0 = desc_sw128(smem_addr(slot_ptr(slot_of(v_idx))) + (NARROW ? x * COLS * 128 : 0),
+                                       kHalf, 1024);
         const uint32_t p0 = tS(x), o0 = tO(x);
         tc_fence_after();
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
+        for (int k = 0; k < COLS / 16; ++k) {
           // A = P from TMEM (S columns of tile x), B = V MN-major
           umma_ts(o0, p0 + 8u * k, b0 + (uint64_t)((k * 2048) >> 4), kIdescKMN,
                   (!first || k > 0) ? 1u : 0u);
@@ -1109,6 +1127,7 @@ __global__ void __launch_bounds__((pf_threads<MODE, SHARE>()), 1)
     const uint32_t b_sfull = b_sfull0 + 8u * x, b_pfull = b_pfull0 + 8u * x;
     const uint32_t b_pvdone = b_pvdone0 + 8u * x, b_ofree = b_ofree0 + 8u * x;
     long long nt = 0;  // tiles of this warpgroup across items (barrier phases)
+    [[maybe_unused]] int ni = 0;  // items (narrow trees: phases of b_mlfull)
     for (long long i = i_first; ok;) {
       Item it;
       if constexpr (TREE) {
@@ -1166,16 +1185,17 @@ __global__ void __launch_bounds__((pf_threads<MODE, SHARE>()), 1)
         if (!__all_sync(0xffffffffu, waited)) { ok = false; break; }
         tc_fence_after();
         if constexpr (SPAN) {
-          const int x0 = (it.t0 + t) * kKeys, first = it.list.first(it.off) - x0;
+          const int x0 = (it.t0 + t) * kKeys + (NARROW ? x * COLS : 0);
+          const int first = it.list.first(it.off) - x0;
           const int sink_end = it.list.first(it.off + p.plan.span.sink) - x0;
           const int top = s_top - x0, win = s_win - x0;
           // (a padding row may be taken for one that sees everything: it is not stored)
           const bool full = __all_sync(
               0xffffffffu,
-              !row_ok || (first <= 0 && top >= kKeys - 1 && (win <= 0 || sink_end >= kKeys)));
-          WordMask seen;
+              !row_ok || (first <= 0 && top >= COLS - 1 && (win <= 0 || sink_end >= COLS)));
+          WordMask<COLS> seen;
 #pragma unroll
-          for (int c = 0; c < kKeys / 32; ++c) {
+          for (int c = 0; c < COLS / 32; ++c) {
             seen.w[c] = 0;
             if (!full) {
               seen.w[c] = column_bits(first, min(top, sink_end - 1), 32 * c) |
@@ -1185,7 +1205,7 @@ __global__ void __launch_bounds__((pf_threads<MODE, SHARE>()), 1)
                     s_bits, 32 * c + x0 - it.list.behind(it.off + (int)it.first_pos), (int)it.nq);
             }
           }
-          softmax_tile(tS(x), tO(x), lane_base, t, seen, full, p.qscale, st);
+          softmax_tile<COLS>(tS(x), tO(x), lane_base, t, seen, full, p.qscale, st);
           tc_fence_before();
           __syncwarp();
           if (lane == 0) mbar_arrive(b_pfull);
@@ -1205,7 +1225,8 @@ __global__ void __launch_bounds__((pf_threads<MODE, SHARE>()), 1)
           c_hi = row_ok ? (int)min((long long)kKeys - 1, pos + it.off - tp0) : -1;
           full_tile = (t > 0 || it.off == 0) && t < t_mask_lo && rows_full;
         }
-        softmax_tile(tS(x), tO(x), lane_base, t, IntervalMask{c_lo, c_hi}, full_tile, p.qscale, st);
+        softmax_tile<kKeys>(tS(x), tO(x), lane_base, t, IntervalMask{c_lo, c_hi}, full_tile,
+                            p.qscale, st);
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(b_pfull);
@@ -1215,6 +1236,62 @@ __global__ void __launch_bounds__((pf_threads<MODE, SHARE>()), 1)
       const bool waited = mbar_wait_sleep(b_pvdone, (uint32_t)((nt - 1) & 1), w);
       if (!__all_sync(0xffffffffu, waited)) { ok = false; break; }
       tc_fence_after();
+      if constexpr (NARROW) {
+        // The row's two states, one a tile, merged: both threads of a row read both O (their
+        // lanes of TMEM are the same) and take half of the columns each.
+        s_ml[x * kRows + r] = make_float2(st.m_used, st.l);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(b_mlfull);
+        bool both = mbar_wait_sleep(b_pvdone0 + 8u * (1 - x), (uint32_t)((nt - 1) & 1), w);
+        both = both && mbar_wait_sleep(b_mlfull, (uint32_t)(ni & 1), w);
+        ++ni;
+        if (!__all_sync(0xffffffffu, both)) { ok = false; break; }
+        tc_fence_after();
+        const float2 a = s_ml[r], b = s_ml[kRows + r];
+        const float top = fmaxf(a.x, b.x);
+        // a state at -inf saw nothing, or only NaN: its sum and O are 0, or NaN
+        const float fa = a.x == -INFINITY ? 1.f : exp2f(a.x - top);
+        const float fb = b.x == -INFINITY ? 1.f : exp2f(b.x - top);
+        const float sum = fa * a.y + fb * b.y;
+        const bool part = it.slot >= 0;
+        const float inv = part ? 1.f : sum == 0.f ? 0.f : 1.f / sum;
+        float* srow = p.part + ((long long)it.slot * kRows + r) * (kD + 4);
+        __nv_bfloat16* orow = static_cast<__nv_bfloat16*>(p.out) +
+                              ((it.q0 + qi) * p.hq + (long long)it.g * G + hh) * kD;
+        if (part && row_ok && x == 0) *reinterpret_cast<float2*>(srow) = make_float2(top, sum);
+#pragma unroll 1
+        for (int c0 = x * (kD / 2); c0 < (x + 1) * (kD / 2); c0 += 16) {
+          uint32_t u[16], v[16];
+          tmem_ld16(tO(0) + lane_base + c0, u);
+          tmem_ld16(tO(1) + lane_base + c0, v);
+          tmem_wait_ld();
+          float o[16];
+#pragma unroll
+          for (int j = 0; j < 16; ++j)
+            o[j] = (__uint_as_float(u[j]) * fa + __uint_as_float(v[j]) * fb) * inv;
+          if (row_ok) {
+            if (part) {
+#pragma unroll
+              for (int j = 0; j < 16; j += 4)
+                *reinterpret_cast<float4*>(srow + 4 + c0 + j) =
+                    make_float4(o[j], o[j + 1], o[j + 2], o[j + 3]);
+            } else {
+#pragma unroll
+              for (int j = 0; j < 16; j += 8)
+                *reinterpret_cast<uint4*>(orow + c0 + j) =
+                    make_uint4(pack_bf16x2(o[j], o[j + 1]), pack_bf16x2(o[j + 2], o[j + 3]),
+                               pack_bf16x2(o[j + 4], o[j + 5]), pack_bf16x2(o[j + 6], o[j + 7]));
+            }
+          }
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(b_ofree0);
+          mbar_arrive(b_ofree0 + 8u);
+        }
+        continue;
+      }
       if constexpr (PREFIX) {
         // the row's state (m, l, unnormalised O) for the decode combine
         const long long row = ((long long)it.c * p.batch + qi) * p.hq + (long long)it.g * G + hh;
@@ -1487,6 +1564,7 @@ cudaError_t launch_prefill_tree(const PoolView& pv, int layer, const void* q, in
   CUtensorMap tq, tk, tv;
   PfParams p;
   const SpanParams& sp = plan.span;
+  const bool narrow = plan.unit_rows == kRows;
   const cudaError_t e = prefill_setup(pv, layer, q, num_q_heads, scale, bt, sp.mb, sp.lens, sp.offs,
                                       sp.batch, sp.total_q, err, &tq, &tk, &tv, &p);
   if (e != cudaSuccess) return e;
@@ -1497,7 +1575,8 @@ cudaError_t launch_prefill_tree(const PoolView& pv, int layer, const void* q, in
   p.words = words;
   p.part = part;
   p.n_items = sm_count;  // the grid: the line of tiles is split over it
-  return prefill_launch<kTree>(tq, tk, tv, p, sm_count, s);
+  return narrow ? prefill_launch<kNarrow>(tq, tk, tv, p, sm_count, s)
+                : prefill_launch<kTree>(tq, tk, tv, p, sm_count, s);
 }
 
 void prefix_plan(const PoolView& pv, int num_q_heads, int batch, int prefix_blocks, int sm_count,

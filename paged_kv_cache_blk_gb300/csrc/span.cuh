@@ -224,7 +224,7 @@ cudaError_t launch_validate_spans(const SpanParams& p, const int32_t* bt, long l
                                   int* err, cudaStream_t s);
 
 // Host side (prefill.cu, where prefill_supported): the tree decode on tcgen05, units of 256
-// rows, key tiles of 128, split over a grid of sm_count CTAs (one where fewer SMs are free).
+// rows, or of 128 where none has more, key tiles of 128, split over a grid of sm_count CTAs.
 cudaError_t launch_prefill_tree(const PoolView& pv, int layer, const void* q, int num_q_heads,
                                 float scale, const int32_t* bt, const PlanParams& plan,
                                 const int32_t* q_pos, const unsigned long long* mask, int words,

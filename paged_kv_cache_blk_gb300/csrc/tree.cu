@@ -135,7 +135,7 @@ TreePath tree_path(const PoolView& v, int G, int max_q_len, int sms) {
   const long long rows = (long long)max_q_len * G;
   t.tcgen05 = rows > 32 && prefill_supported(v, G * v.num_kv_heads) == 0;
   if (t.tcgen05) {
-    t.unit_rows = 256;
+    t.unit_rows = rows <= 128 ? 128 : 256;
     t.grid = sms;
     t.bytes = (size_t)2 * t.grid * t.unit_rows * (v.head_dim + 4) * 4;
     return t;
