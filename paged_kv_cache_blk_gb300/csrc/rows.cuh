@@ -116,23 +116,27 @@ struct RowsTile {
   }
 };
 
-template <int MODE, int D, int WR>
+// MT: 16-row tiles of a warp; RG: groups of warps that share out a unit's rows.
+template <int MODE, int D, int MT, int RG>
 struct RowsLayout {
   using Tl = RowsTile<MODE, D>;
+  static constexpr int kRows = 16 * MT * RG;
   static constexpr int kRing = Tl::kStages * Tl::kBytes;
+  // Q: with two row tiles in shared memory (fp32 as two tf32 parts), with one in registers
+  static constexpr bool kQShared = MT > 1;
+  static constexpr int kQRow = D * (MODE == PKV_F32 ? 4 : 2);
+  static constexpr int kQ = kQShared ? kRows * kQRow * (MODE == PKV_F32 ? 2 : 1) : 0;
   static constexpr int kAccRow = D + 4;  // floats between rows of a merged state
-  static constexpr int kMerge = kRowsWarps * 16 * (kAccRow + 2) * 4;
-  static constexpr int kSmem = kRing > kMerge ? kRing : kMerge;
+  static constexpr int kMerge = kRowsWarps * 16 * MT * (kAccRow + 2) * 4;
+  static constexpr int kQAt = kRing > kMerge ? kRing : kMerge;
+  static constexpr int kSeenAt = kQAt + kQ;  // what each of a warp's rows sees
+  static constexpr int kSmem = kSeenAt + kRowsWarps * 16 * MT * 16;
+  // CTAs that an SM holds at once, of the tree kernel its grid: what shared memory and O's
+  // registers allow
+  static constexpr int kFit = 227 * 1024 / (kSmem + 2048);
+  static constexpr int kMost = D == 64 || (MODE == PKV_I8 && MT == 1) ? 3 : 2;
+  static constexpr int kCtas = kFit < kMost ? kFit : kMost;
 };
-
-// CTAs that an SM holds at once, of the tree kernel its grid: what shared memory allows, up to
-// three (two with head_dim 128 but for int8), which then share the registers.
-template <int MODE, int D>
-constexpr int rows_ctas() {
-  constexpr int fit = 227 * 1024 / (RowsLayout<MODE, D, 4>::kSmem + 2048);
-  constexpr int most = D == 64 || MODE == PKV_I8 ? 3 : 2;
-  return fit < most ? fit : most;
-}
 
 // One unit's work: rows first_row .. of sequence b, kv head g, tiles t0 .. t1 of its list.
 struct RowsPiece {
@@ -143,19 +147,20 @@ struct RowsPiece {
   float* part;   // where the state goes, or NULL: finished here
 };
 
-template <int MODE, int D, int WR, bool TREE>
+template <int MODE, int D, int MT, int RG, bool TREE>
 __device__ __forceinline__ void rows_piece(const RowsParams& p, const RowsPiece& w,
                                            unsigned char* smem) {
   using Tl = RowsTile<MODE, D>;
-  using Lay = RowsLayout<MODE, D, WR>;
+  using Lay = RowsLayout<MODE, D, MT, RG>;
   constexpr bool kI8 = MODE == PKV_I8, kF32 = MODE == PKV_F32;
-  constexpr int WK = kRowsWarps / WR, KT = Tl::kKeys, KW = KT / WK, NT = KW / 8;
-  constexpr int NST = Tl::kStages, M = 16 * WR, NO = D / 8;
+  constexpr int WK = kRowsWarps / RG, KT = Tl::kKeys, KW = KT / WK, NT = KW / 8;
+  constexpr int NST = Tl::kStages, M = Lay::kRows, NO = D / 8;
+  constexpr bool kTwoParts = MT == 1;  // of a weight in P V
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int wr = warp % WR, wk = warp / WR;
+  const int wr = warp % RG, wk = warp / RG;
   const int gl = lane >> 2, qi = lane & 3;
   const int G = p.plan.G, n = w.s.n, rows = n * G, off = w.s.off;
-  const uint32_t base = smem_addr(smem);
+  const uint32_t base = smem_addr(smem), sq = base + Lay::kQAt;
 
   // ---- copies: each warp a quarter of a tile's rows ----
   constexpr int RW = KT / kRowsWarps;
@@ -206,67 +211,78 @@ __device__ __forceinline__ void rows_piece(const RowsParams& p, const RowsPiece&
     }
     cp_commit();
   };
+#pragma unroll 1
+  for (int s = 0; s < NST - 1; ++s) issue(w.t0 + s, s);
 
-  // ---- the warp's rows: row 0 is gl, row 1 is gl + 8 of its 16 ----
-  // a row sees the places first .. top of the list that are first tokens or lo or later, and,
-  // in a masked tree, of the places from draft on those with their bit
-  int lo[2], top[2];
-  const unsigned long long* bits[2];
-  bool live_row[2];
-  long long qrow[2];
+  // ---- what the warp's rows see, a row a lane ----
+  // the places first .. top of the list that are first tokens or lo or later, and, in a masked
+  // tree, of the places from draft on those with their bit
   const bool masked_tree = TREE && p.mask != nullptr;
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const int r = w.first_row + wr * 16 + gl + 8 * i;
-    live_row[i] = r < rows;
-    const int tok = live_row[i] ? r / G : 0, h = live_row[i] ? r - tok * G : 0;
-    qrow[i] = (w.s.q0 + tok) * p.hq + w.g * G + h;
-    int pos = w.s.ctx + tok;
-    top[i] = w.t.last(off + (masked_tree ? w.s.ctx - 1 : pos));
-    bits[i] = masked_tree ? p.mask + (w.s.q0 + tok) * p.words : nullptr;
-    lo[i] = w.t.behind(off);
+  const int first_place = w.t.first(off), sink_place = w.t.first(sink_end);
+  const int draft = w.t.behind(off + w.s.ctx);
+  const int warp_row = w.first_row + wr * 16 * MT;
+  const uint32_t seen_at = base + Lay::kSeenAt + warp * (16 * MT * 16);
+  int full_lo, full_hi;  // places that every row of the warp sees
+  {
+    const int r = warp_row + lane % (16 * MT);
+    const bool live = r < rows;
+    const int tok = live ? r / G : 0;
+    int pos = w.s.ctx + tok, lo = w.t.behind(off);
+    const int top = w.t.last(off + (masked_tree ? w.s.ctx - 1 : pos));
     if (p.plan.span.window > 0) {
       if (TREE && p.q_pos) pos = max(w.s.ctx, p.q_pos[w.s.q0 + tok]);
       const long long first = (long long)pos - p.plan.span.window + 1;
-      lo[i] = w.t.behind(off + (int)max(0ll, min(first, kMaxPositions)));
+      lo = w.t.behind(off + (int)max(0ll, min(first, kMaxPositions)));
     }
+    if (lane < 16 * MT)
+      sts128(seen_at + lane * 16, make_uint4((uint32_t)lo, (uint32_t)top, (uint32_t)tok, 0u));
+    full_lo = max(first_place, __reduce_max_sync(kAllLanes, live ? lo : INT_MIN));
+    full_hi = __reduce_min_sync(kAllLanes, live ? top : INT_MAX);
+    __syncwarp();
   }
-  const int first_place = w.t.first(off), sink_place = w.t.first(sink_end);
-  const int draft = w.t.behind(off + w.s.ctx);
-  auto sees = [&](int i, int x) -> bool {
-    if (x <= top[i]) return x >= first_place && (x >= lo[i] || x < sink_place);
-    if (!TREE || bits[i] == nullptr) return false;
-    const int d = x - draft;
-    return d >= 0 && d < n && (bits[i][d >> 6] >> (d & 63) & 1);
+  // row i (of gl, gl + 8) of row tile mt: is place x seen?
+  struct RowSees {
+    int lo, top;
+    const unsigned long long* bits;
   };
-  // keys from full_lo to full_hi are seen by every row of the warp
-  int full_lo = max(live_row[0] ? lo[0] : INT_MIN, live_row[1] ? lo[1] : INT_MIN);
-  int full_hi = min(live_row[0] ? top[0] : INT_MAX, live_row[1] ? top[1] : INT_MAX);
-  full_lo = max(first_place, __reduce_max_sync(kAllLanes, full_lo));
-  full_hi = __reduce_min_sync(kAllLanes, full_hi);
+  auto row_sees = [&](int mt, int i) {
+    const uint4 v = lds128(seen_at + (mt * 16 + gl + 8 * i) * 16);
+    return RowSees{(int)v.x, (int)v.y,
+                   masked_tree ? p.mask + (w.s.q0 + (int)v.z) * p.words : nullptr};
+  };
+  auto sees = [&](const RowSees& r, int x) -> bool {
+    if (x <= r.top) return x >= first_place && (x >= r.lo || x < sink_place);
+    if (!TREE || r.bits == nullptr) return false;
+    const int d = x - draft;
+    return d >= 0 && d < n && (r.bits[d >> 6] >> (d & 63) & 1);
+  };
 
-  // Q in the registers of the A operand
+  // ---- Q, rows behind the last one as zeros ----
+  auto q_row = [&](int r) {
+    const int tok = r / G;
+    return p.q + ((w.s.q0 + tok) * p.hq + w.g * G + (r - tok * G)) * (long long)Lay::kQRow;
+  };
   constexpr int KS = kF32 ? D / 8 : D / 16;
-  uint32_t qa[KS][4];
-  {
-    const char* src[2];
-#pragma unroll
-    for (int i = 0; i < 2; ++i) src[i] = p.q + qrow[i] * (D * (kF32 ? 4 : 2));
+  [[maybe_unused]] uint32_t qa[Lay::kQShared ? 1 : KS][4];
+  if constexpr (!Lay::kQShared) {
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
+      const int r = warp_row + gl + 8 * i;
+      const bool live = r < rows;
+      const char* src = q_row(live ? r : 0);
       if constexpr (MODE == PKV_BF16) {
 #pragma unroll
         for (int k = 0; k < KS; ++k) {
-          const char* x = src[i] + (k * 16 + 2 * qi) * 2;
-          qa[k][i] = live_row[i] ? *reinterpret_cast<const uint32_t*>(x) : 0u;
-          qa[k][2 + i] = live_row[i] ? *reinterpret_cast<const uint32_t*>(x + 16) : 0u;
+          const char* x = src + (k * 16 + 2 * qi) * 2;
+          qa[k][i] = live ? *reinterpret_cast<const uint32_t*>(x) : 0u;
+          qa[k][2 + i] = live ? *reinterpret_cast<const uint32_t*>(x + 16) : 0u;
         }
       } else if constexpr (kI8) {
         // step 4 i + j: dims 64 i + 16 qi + 4 j .. + 3, the order of the K codes
 #pragma unroll
         for (int k = 0; k < KS; ++k) {
-          const char* x = src[i] + ((k >> 2) * 64 + 16 * qi + 4 * (k & 3)) * 2;
-          const uint2 y = live_row[i] ? *reinterpret_cast<const uint2*>(x) : make_uint2(0u, 0u);
+          const char* x = src + ((k >> 2) * 64 + 16 * qi + 4 * (k & 3)) * 2;
+          const uint2 y = live ? *reinterpret_cast<const uint2*>(x) : make_uint2(0u, 0u);
           qa[k][i] = y.x;
           qa[k][2 + i] = y.y;
         }
@@ -274,9 +290,8 @@ __device__ __forceinline__ void rows_piece(const RowsParams& p, const RowsPiece&
         // steps 2 i, 2 i + 1: dims 16 i + 4 qi .. + 3
 #pragma unroll
         for (int k = 0; k < KS; k += 2) {
-          const char* x = src[i] + (k * 8 + 4 * qi) * 4;
-          const uint4 y = live_row[i] ? *reinterpret_cast<const uint4*>(x)
-                                      : make_uint4(0u, 0u, 0u, 0u);
+          const char* x = src + (k * 8 + 4 * qi) * 4;
+          const uint4 y = live ? *reinterpret_cast<const uint4*>(x) : make_uint4(0u, 0u, 0u, 0u);
           qa[k][i] = y.x;
           qa[k][2 + i] = y.y;
           qa[k + 1][i] = y.z;
@@ -284,18 +299,76 @@ __device__ __forceinline__ void rows_piece(const RowsParams& p, const RowsPiece&
         }
       }
     }
+  } else {
+    // 16-byte chunks; int8: a chunk's two groups of 4 dims (64 i + 16 c + 4 j ..) go where step
+    // 4 i + j takes them, columns 2 c, 2 c + 1 and 8 + 2 c, 9 + 2 c of it
+    constexpr int C = Lay::kQRow / 16;
+#pragma unroll 4
+    for (int e = tid; e < M * C; e += kRowsThreads) {
+      const int r = e / C, c = e % C;
+      uint4 x = make_uint4(0u, 0u, 0u, 0u);
+      if (w.first_row + r < rows) x = ld_stream(q_row(w.first_row + r) + c * 16);
+      const uint32_t at = sq + r * Lay::kQRow;
+      if constexpr (MODE == PKV_BF16) {
+        sts128(at + ((c ^ (r & 7)) << 4), x);
+      } else if constexpr (kI8) {
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          const int d = 8 * c + 4 * u, step = (d >> 6) * 4 + ((d >> 2) & 3), col = (d >> 4) & 3;
+          sts32(at + (((2 * step) ^ (r & 7)) << 4) + col * 4, u ? x.z : x.x);
+          sts32(at + (((2 * step + 1) ^ (r & 7)) << 4) + col * 4, u ? x.w : x.y);
+        }
+      } else {
+        uint4 h, l;
+        split_tf32(__uint_as_float(x.x), h.x, l.x);
+        split_tf32(__uint_as_float(x.y), h.y, l.y);
+        split_tf32(__uint_as_float(x.z), h.z, l.z);
+        split_tf32(__uint_as_float(x.w), h.w, l.w);
+        sts128(sq + Tl::at(r, c), h);
+        sts128(sq + M * Lay::kQRow + Tl::at(r, c), l);
+      }
+    }
+  }
+  // the A operand of step k of row tile mt (bf16, int8)
+  auto q_frag = [&](int mt, int k, uint32_t (&a)[4]) {
+    if constexpr (Lay::kQShared) {
+      const int r = wr * 16 * MT + mt * 16 + (lane & 15);
+      ldsm_x4(a, sq + r * Lay::kQRow + (((2 * k + (lane >> 4)) ^ (r & 7)) << 4));
+    } else {
+#pragma unroll
+      for (int c = 0; c < 4; ++c) a[c] = qa[k][c];
+    }
+  };
+  // fp32: both parts of steps k, k + 1
+  auto q_frag_tf32 = [&](int mt, int k, uint32_t (&h)[2][4], uint32_t (&l)[2][4]) {
+    if constexpr (Lay::kQShared) {
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int r = wr * 16 * MT + mt * 16 + gl + 8 * i;
+        const uint4 x = lds128(sq + Tl::at(r, 2 * k + qi));
+        const uint4 y = lds128(sq + M * Lay::kQRow + Tl::at(r, 2 * k + qi));
+        h[0][i] = x.x; h[0][2 + i] = x.y; h[1][i] = x.z; h[1][2 + i] = x.w;
+        l[0][i] = y.x; l[0][2 + i] = y.y; l[1][i] = y.z; l[1][2 + i] = y.w;
+      }
+    } else {
+#pragma unroll
+      for (int u = 0; u < 2; ++u)
+#pragma unroll
+        for (int c = 0; c < 4; ++c) split_tf32(__uint_as_float(qa[k + u][c]), h[u][c], l[u][c]);
+    }
+  };
+
+  float o[MT][NO][4], m[MT][2], l[MT][2];
+#pragma unroll
+  for (int mt = 0; mt < MT; ++mt) {
+#pragma unroll
+    for (int k = 0; k < NO; ++k)
+#pragma unroll
+      for (int c = 0; c < 4; ++c) o[mt][k][c] = 0.f;
+    m[mt][0] = m[mt][1] = -INFINITY;
+    l[mt][0] = l[mt][1] = 0.f;
   }
 
-  float o[NO][4], m[2], l[2];
-#pragma unroll
-  for (int k = 0; k < NO; ++k)
-#pragma unroll
-    for (int c = 0; c < 4; ++c) o[k][c] = 0.f;
-  m[0] = m[1] = -INFINITY;
-  l[0] = l[1] = 0.f;
-
-#pragma unroll 1
-  for (int s = 0; s < NST - 1; ++s) issue(w.t0 + s, s);
   int stage = 0;
 #pragma unroll 1
   for (int i = w.t0; i < w.t1; ++i) {
@@ -307,73 +380,93 @@ __device__ __forceinline__ void rows_piece(const RowsParams& p, const RowsPiece&
     const int k0 = wk * KW;  // the warp's keys of the tile
 
     // ---- scores ----
-    float s[NT][4];
+    float s[MT][NT][4];
 #pragma unroll
-    for (int j = 0; j < NT; ++j)
+    for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-      for (int c = 0; c < 4; ++c) s[j][c] = 0.f;
+      for (int j = 0; j < NT; ++j)
+#pragma unroll
+        for (int c = 0; c < 4; ++c) s[mt][j][c] = 0.f;
     if constexpr (MODE == PKV_BF16) {
       const int r = k0 + (lane & 7) + ((lane >> 4) & 1) * 8, cc = (lane >> 3) & 1;
 #pragma unroll
-      for (int k = 0; k < KS; ++k)
+      for (int k = 0; k < KS; ++k) {
+        uint32_t a[MT][4];
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt) q_frag(mt, k, a[mt]);
 #pragma unroll
         for (int j = 0; j < NT; j += 2) {
           uint32_t b[4];
           ldsm_x4(b, st + Tl::at(r + j * 8, 2 * k + cc));
-          mma16<false>(s[j], qa[k][0], qa[k][1], qa[k][2], qa[k][3], b[0], b[1]);
-          mma16<false>(s[j + 1], qa[k][0], qa[k][1], qa[k][2], qa[k][3], b[2], b[3]);
-        }
-    } else if constexpr (kI8) {
-      const int r = k0 + 4 * (gl >> 1) + (gl & 1);
 #pragma unroll
-      for (int j = 0; j < NT; j += 2)
-#pragma unroll
-        for (int u = 0; u < KS / 4; ++u) {
-          const uint4 x = lds128(st + Tl::at(r + j * 8, 4 * u + qi));
-          const uint4 y = lds128(st + Tl::at(r + j * 8 + 2, 4 * u + qi));
-          const uint32_t xw[4] = {x.x, x.y, x.z, x.w}, yw[4] = {y.x, y.y, y.z, y.w};
-#pragma unroll
-          for (int v = 0; v < 4; ++v) {
-            uint32_t b0, b1;
-            const int k = 4 * u + v;
-            codes_to_bf16(xw[v], b0, b1);
-            mma16<false>(s[j], qa[k][0], qa[k][1], qa[k][2], qa[k][3], b0, b1);
-            codes_to_bf16(yw[v], b0, b1);
-            mma16<false>(s[j + 1], qa[k][0], qa[k][1], qa[k][2], qa[k][3], b0, b1);
-          }
-        }
-    } else {
-      float big[NT][4];
-#pragma unroll
-      for (int j = 0; j < NT; ++j)
-#pragma unroll
-        for (int c = 0; c < 4; ++c) big[j][c] = 0.f;
-#pragma unroll
-      for (int k = 0; k < KS; k += 2) {
-        uint32_t ah[2][4], al[2][4];
-#pragma unroll
-        for (int u = 0; u < 2; ++u)
-#pragma unroll
-          for (int c = 0; c < 4; ++c) split_tf32(__uint_as_float(qa[k + u][c]), ah[u][c], al[u][c]);
-#pragma unroll
-        for (int j = 0; j < NT; ++j) {
-          const uint4 x = lds128(st + Tl::at(k0 + j * 8 + gl, 2 * k + qi));
-          const uint32_t xw[4] = {x.x, x.y, x.z, x.w};
-          uint32_t bh[4], bl[4];
-#pragma unroll
-          for (int c = 0; c < 4; ++c) split_tf32(__uint_as_float(xw[c]), bh[c], bl[c]);
-#pragma unroll
-          for (int u = 0; u < 2; ++u) {
-            mma8_tf32(s[j], al[u], bh[2 * u], bh[2 * u + 1]);
-            mma8_tf32(s[j], ah[u], bl[2 * u], bl[2 * u + 1]);
-            mma8_tf32(big[j], ah[u], bh[2 * u], bh[2 * u + 1]);
+          for (int mt = 0; mt < MT; ++mt) {
+            mma16<false>(s[mt][j], a[mt][0], a[mt][1], a[mt][2], a[mt][3], b[0], b[1]);
+            mma16<false>(s[mt][j + 1], a[mt][0], a[mt][1], a[mt][2], a[mt][3], b[2], b[3]);
           }
         }
       }
+    } else if constexpr (kI8) {
+      const int r = k0 + 4 * (gl >> 1) + (gl & 1);
 #pragma unroll
-      for (int j = 0; j < NT; ++j)
+      for (int u = 0; u < KS / 4; ++u) {
+        uint4 x[NT];
 #pragma unroll
-        for (int c = 0; c < 4; ++c) s[j][c] += big[j][c];
+        for (int j = 0; j < NT; ++j)
+          x[j] = lds128(st + Tl::at(r + (j >> 1) * 16 + (j & 1) * 2, 4 * u + qi));
+#pragma unroll
+        for (int v = 0; v < 4; ++v) {
+          uint32_t a[MT][4];
+#pragma unroll
+          for (int mt = 0; mt < MT; ++mt) q_frag(mt, 4 * u + v, a[mt]);
+#pragma unroll
+          for (int j = 0; j < NT; ++j) {
+            uint32_t b0, b1;
+            codes_to_bf16(v == 0 ? x[j].x : v == 1 ? x[j].y : v == 2 ? x[j].z : x[j].w, b0, b1);
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt)
+              mma16<false>(s[mt][j], a[mt][0], a[mt][1], a[mt][2], a[mt][3], b0, b1);
+          }
+        }
+      }
+    } else {
+      float big[MT][NT][4];
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+        for (int j = 0; j < NT; ++j)
+#pragma unroll
+          for (int c = 0; c < 4; ++c) big[mt][j][c] = 0.f;
+#pragma unroll
+      for (int k = 0; k < KS; k += 2) {
+        uint32_t bh[NT][4], bl[NT][4];
+#pragma unroll
+        for (int j = 0; j < NT; ++j) {
+          const uint4 x = lds128(st + Tl::at(k0 + j * 8 + gl, 2 * k + qi));
+          split_tf32(__uint_as_float(x.x), bh[j][0], bl[j][0]);
+          split_tf32(__uint_as_float(x.y), bh[j][1], bl[j][1]);
+          split_tf32(__uint_as_float(x.z), bh[j][2], bl[j][2]);
+          split_tf32(__uint_as_float(x.w), bh[j][3], bl[j][3]);
+        }
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt) {
+          uint32_t ah[2][4], al[2][4];
+          q_frag_tf32(mt, k, ah, al);
+#pragma unroll
+          for (int u = 0; u < 2; ++u)
+#pragma unroll
+            for (int j = 0; j < NT; ++j) {
+              mma8_tf32(s[mt][j], al[u], bh[j][2 * u], bh[j][2 * u + 1]);
+              mma8_tf32(s[mt][j], ah[u], bl[j][2 * u], bl[j][2 * u + 1]);
+              mma8_tf32(big[mt][j], ah[u], bh[j][2 * u], bh[j][2 * u + 1]);
+            }
+        }
+      }
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+        for (int j = 0; j < NT; ++j)
+#pragma unroll
+          for (int c = 0; c < 4; ++c) s[mt][j][c] += big[mt][j][c];
     }
 
     // ---- softmax ----
@@ -384,93 +477,121 @@ __device__ __forceinline__ void rows_piece(const RowsParams& p, const RowsPiece&
     };
     const int p0 = i * KT + k0;
     const bool full = p0 >= full_lo && p0 + KW - 1 <= full_hi;
-    float mx[2] = {-INFINITY, -INFINITY};
-    [[maybe_unused]] float scale_v[NT][2];
-#pragma unroll
-    for (int j = 0; j < NT; ++j)
-#pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        float f = p.qscale;
-        if constexpr (kI8) {
-          const uint32_t sc = st + 2 * Tl::kHalf + (k0 + key(j, c)) * 16 + (4 * w.g & 15);
-          f *= lds_f32(sc);
-          scale_v[j][c] = lds_f32(sc + KT * 16);
-        }
-#pragma unroll
-        for (int r = 0; r < 2; ++r) {
-          float x = s[j][2 * r + c] * f;
-          if (!full) x = sees(r, p0 + key(j, c)) ? x : -INFINITY;
-          s[j][2 * r + c] = x;
-          mx[r] = fmaxf(mx[r], x);
-        }
-      }
-    float a[2];
-#pragma unroll
-    for (int r = 0; r < 2; ++r) {
-      a[r] = 1.f;
-      // the running maximum moves only where some lane passes it
-      if (__any_sync(kAllLanes, mx[r] > m[r])) {
-        float x = fmaxf(mx[r], __shfl_xor_sync(kAllLanes, mx[r], 1));
-        x = fmaxf(x, __shfl_xor_sync(kAllLanes, x, 2));
-        const float top_m = fmaxf(m[r], x);
-        a[r] = m[r] == -INFINITY ? 0.f : exp2f(m[r] - top_m);
-        m[r] = top_m;
-      }
-      // scores of -inf carry no weight, even while they are all there is
-      const float base_m = m[r] == -INFINITY ? 0.f : m[r];
-      float sum = 0.f;
+    [[maybe_unused]] float factor[NT][2], scale_v[NT][2];
+    if constexpr (kI8) {
 #pragma unroll
       for (int j = 0; j < NT; ++j)
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
-          const float e = exp2f(s[j][2 * r + c] - base_m);
-          sum += e;
-          s[j][2 * r + c] = e;
-          if constexpr (kI8) s[j][2 * r + c] = e * scale_v[j][c];
+          const uint32_t sc = st + 2 * Tl::kHalf + (k0 + key(j, c)) * 16 + (4 * w.g & 15);
+          factor[j][c] = p.qscale * lds_f32(sc);
+          scale_v[j][c] = lds_f32(sc + KT * 16);
         }
-      l[r] = l[r] * a[r] + sum;
     }
-    if constexpr (!kF32) {
-      if (__any_sync(kAllLanes, a[0] != 1.f || a[1] != 1.f)) {
+    float a[MT][2];
 #pragma unroll
-        for (int k = 0; k < NO; ++k) {
-          o[k][0] *= a[0];
-          o[k][1] *= a[0];
-          o[k][2] *= a[1];
-          o[k][3] *= a[1];
+    for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        float mx = -INFINITY;
+#pragma unroll
+        for (int j = 0; j < NT; ++j)
+#pragma unroll
+          for (int c = 0; c < 2; ++c) s[mt][j][2 * r + c] *= kI8 ? factor[j][c] : p.qscale;
+        if (!full) {
+          const RowSees row = row_sees(mt, r);
+#pragma unroll
+          for (int j = 0; j < NT; ++j)
+#pragma unroll
+            for (int c = 0; c < 2; ++c)
+              if (!sees(row, p0 + key(j, c))) s[mt][j][2 * r + c] = -INFINITY;
         }
+#pragma unroll
+        for (int j = 0; j < NT; ++j)
+#pragma unroll
+          for (int c = 0; c < 2; ++c) mx = fmaxf(mx, s[mt][j][2 * r + c]);
+        a[mt][r] = 1.f;
+        // the running maximum moves only where some lane passes it
+        if (__any_sync(kAllLanes, mx > m[mt][r])) {
+          mx = fmaxf(mx, __shfl_xor_sync(kAllLanes, mx, 1));
+          mx = fmaxf(mx, __shfl_xor_sync(kAllLanes, mx, 2));
+          const float top_m = fmaxf(m[mt][r], mx);
+          a[mt][r] = m[mt][r] == -INFINITY ? 0.f : exp2f(m[mt][r] - top_m);
+          m[mt][r] = top_m;
+        }
+        // scores of -inf carry no weight, even while they are all there is
+        const float base_m = m[mt][r] == -INFINITY ? 0.f : m[mt][r];
+        float sum = 0.f;
+#pragma unroll
+        for (int j = 0; j < NT; ++j)
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            const float e = exp2f(s[mt][j][2 * r + c] - base_m);
+            sum += e;
+            s[mt][j][2 * r + c] = e;
+            if constexpr (kI8) s[mt][j][2 * r + c] = e * scale_v[j][c];
+          }
+        l[mt][r] = l[mt][r] * a[mt][r] + sum;
       }
+    if constexpr (!kF32) {
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt)
+        if (__any_sync(kAllLanes, a[mt][0] != 1.f || a[mt][1] != 1.f)) {
+#pragma unroll
+          for (int k = 0; k < NO; ++k) {
+            o[mt][k][0] *= a[mt][0];
+            o[mt][k][1] *= a[mt][0];
+            o[mt][k][2] *= a[mt][1];
+            o[mt][k][3] *= a[mt][1];
+          }
+        }
     }
 
     // ---- O += P V ----
     if constexpr (!kF32) {
-      uint32_t ph[NT / 2][4], pl[NT / 2][4];
+      uint32_t ph[MT][NT / 2][4];
+      [[maybe_unused]] uint32_t pl[MT][NT / 2][4];
 #pragma unroll
-      for (int j = 0; j < NT / 2; ++j)
+      for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          const float x = s[2 * j + (c >> 1)][2 * (c & 1)], y = s[2 * j + (c >> 1)][2 * (c & 1) + 1];
-          if constexpr (kI8) {  // (infinite products: what the finite part leaves is infinite)
-            constexpr float kMost = 3.38953139e38f;
-            ph[j][c] = pack_bf16x2(fminf(fmaxf(x, -kMost), kMost), fminf(fmaxf(y, -kMost), kMost));
-          } else {
-            ph[j][c] = below_bf16x2(x, y);
+        for (int j = 0; j < NT / 2; ++j)
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            const float x = s[mt][2 * j + (c >> 1)][2 * (c & 1)];
+            const float y = s[mt][2 * j + (c >> 1)][2 * (c & 1) + 1];
+            if constexpr (!kTwoParts) {
+              ph[mt][j][c] = pack_bf16x2(x, y);
+            } else {
+              if constexpr (kI8) {  // (infinite products: what the finite part leaves is infinite)
+                constexpr float kMost = 3.38953139e38f;
+                ph[mt][j][c] =
+                    pack_bf16x2(fminf(fmaxf(x, -kMost), kMost), fminf(fmaxf(y, -kMost), kMost));
+              } else {
+                ph[mt][j][c] = below_bf16x2(x, y);
+              }
+              pl[mt][j][c] = pack_bf16x2(x - bf16_lo(ph[mt][j][c]), y - bf16_hi(ph[mt][j][c]));
+            }
           }
-          pl[j][c] = pack_bf16x2(x - bf16_lo(ph[j][c]), y - bf16_hi(ph[j][c]));
+      // two output tiles' worth of one V operand
+      auto add = [&](int j, int k, uint32_t b0, uint32_t b1) {
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt) {
+          mma16<false>(o[mt][k], ph[mt][j][0], ph[mt][j][1], ph[mt][j][2], ph[mt][j][3], b0, b1);
+          if constexpr (kTwoParts)
+            mma16<false>(o[mt][k], pl[mt][j][0], pl[mt][j][1], pl[mt][j][2], pl[mt][j][3], b0, b1);
         }
+      };
       if constexpr (kI8) {
 #pragma unroll
         for (int k = 0; k < NO; k += 2)
 #pragma unroll
           for (int j = 0; j < NT / 2; ++j) {
-            uint32_t r0, r1, b0, b1;
+            uint32_t r0, r1, b0, b1, b2, b3;
             ldsm_b8_t(r0, r1, sv + Tl::at(k0 + j * 16 + (lane & 15), k / 2));
             codes_to_bf16(r0, b0, b1);
-            mma16<false>(o[k], ph[j][0], ph[j][1], ph[j][2], ph[j][3], b0, b1);
-            mma16<false>(o[k], pl[j][0], pl[j][1], pl[j][2], pl[j][3], b0, b1);
-            codes_to_bf16(r1, b0, b1);
-            mma16<false>(o[k + 1], ph[j][0], ph[j][1], ph[j][2], ph[j][3], b0, b1);
-            mma16<false>(o[k + 1], pl[j][0], pl[j][1], pl[j][2], pl[j][3], b0, b1);
+            codes_to_bf16(r1, b2, b3);
+            add(j, k, b0, b1);
+            add(j, k + 1, b2, b3);
           }
       } else {
         const int r = k0 + (lane & 7) + ((lane >> 3) & 1) * 8, cc = lane >> 4;
@@ -480,49 +601,58 @@ __device__ __forceinline__ void rows_piece(const RowsParams& p, const RowsPiece&
           for (int k = 0; k < NO; k += 2) {
             uint32_t b[4];
             ldsm_x4_t(b, sv + Tl::at(r + j * 16, k + cc));
-            mma16<false>(o[k], ph[j][0], ph[j][1], ph[j][2], ph[j][3], b[0], b[1]);
-            mma16<false>(o[k + 1], ph[j][0], ph[j][1], ph[j][2], ph[j][3], b[2], b[3]);
-            mma16<false>(o[k], pl[j][0], pl[j][1], pl[j][2], pl[j][3], b[0], b[1]);
-            mma16<false>(o[k + 1], pl[j][0], pl[j][1], pl[j][2], pl[j][3], b[2], b[3]);
+            add(j, k, b[0], b[1]);
+            add(j, k + 1, b[2], b[3]);
           }
       }
     } else {
-      uint32_t ph[NT][4], pl[NT][4];  // columns qi, qi + 4 of a step: keys 2 qi, 2 qi + 1
+      uint32_t ph[MT][NT][4], pl[MT][NT][4];  // columns qi, qi + 4 of a step: keys 2 qi, 2 qi + 1
 #pragma unroll
-      for (int j = 0; j < NT; ++j) {
-        split_tf32(s[j][0], ph[j][0], pl[j][0]);
-        split_tf32(s[j][2], ph[j][1], pl[j][1]);
-        split_tf32(s[j][1], ph[j][2], pl[j][2]);
-        split_tf32(s[j][3], ph[j][3], pl[j][3]);
-      }
+      for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+        for (int j = 0; j < NT; ++j) {
+          split_tf32(s[mt][j][0], ph[mt][j][0], pl[mt][j][0]);
+          split_tf32(s[mt][j][2], ph[mt][j][1], pl[mt][j][1]);
+          split_tf32(s[mt][j][1], ph[mt][j][2], pl[mt][j][2]);
+          split_tf32(s[mt][j][3], ph[mt][j][3], pl[mt][j][3]);
+        }
       // dims 32 q + 4 column + u of the four output tiles 4 q + u
 #pragma unroll
       for (int q = 0; q < D / 32; ++q) {
-        float acc[4][4], big[4][4];
-#pragma unroll
-        for (int u = 0; u < 4; ++u)
-#pragma unroll
-          for (int c = 0; c < 4; ++c) acc[u][c] = big[u][c] = 0.f;
+        uint4 x[NT], y[NT];
 #pragma unroll
         for (int j = 0; j < NT; ++j) {
-          const uint4 x = lds128(sv + Tl::at(k0 + j * 8 + 2 * qi, 8 * q + gl));
-          const uint4 y = lds128(sv + Tl::at(k0 + j * 8 + 2 * qi + 1, 8 * q + gl));
-          const uint32_t xw[4] = {x.x, x.y, x.z, x.w}, yw[4] = {y.x, y.y, y.z, y.w};
-#pragma unroll
-          for (int u = 0; u < 4; ++u) {
-            uint32_t h0, l0, h1, l1;
-            split_tf32(__uint_as_float(xw[u]), h0, l0);
-            split_tf32(__uint_as_float(yw[u]), h1, l1);
-            mma8_tf32(acc[u], pl[j], h0, h1);
-            mma8_tf32(acc[u], ph[j], l0, l1);
-            mma8_tf32(big[u], ph[j], h0, h1);
-          }
+          x[j] = lds128(sv + Tl::at(k0 + j * 8 + 2 * qi, 8 * q + gl));
+          y[j] = lds128(sv + Tl::at(k0 + j * 8 + 2 * qi + 1, 8 * q + gl));
         }
 #pragma unroll
-        for (int u = 0; u < 4; ++u)
+        for (int u = 0; u < 4; ++u) {
+          float acc[MT][4], big[MT][4];
 #pragma unroll
-          for (int c = 0; c < 4; ++c)
-            o[4 * q + u][c] = fmaf(o[4 * q + u][c], a[c >> 1], acc[u][c] + big[u][c]);
+          for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+            for (int c = 0; c < 4; ++c) acc[mt][c] = big[mt][c] = 0.f;
+#pragma unroll
+          for (int j = 0; j < NT; ++j) {
+            uint32_t h0, l0, h1, l1;
+            split_tf32(__uint_as_float(u == 0 ? x[j].x : u == 1 ? x[j].y : u == 2 ? x[j].z : x[j].w),
+                       h0, l0);
+            split_tf32(__uint_as_float(u == 0 ? y[j].x : u == 1 ? y[j].y : u == 2 ? y[j].z : y[j].w),
+                       h1, l1);
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt) {
+              mma8_tf32(acc[mt], pl[mt][j], h0, h1);
+              mma8_tf32(acc[mt], ph[mt][j], l0, l1);
+              mma8_tf32(big[mt], ph[mt][j], h0, h1);
+            }
+          }
+#pragma unroll
+          for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+            for (int c = 0; c < 4; ++c)
+              o[mt][4 * q + u][c] =
+                  fmaf(o[mt][4 * q + u][c], a[mt][c >> 1], acc[mt][c] + big[mt][c]);
+        }
       }
     }
   }
@@ -531,27 +661,30 @@ __device__ __forceinline__ void rows_piece(const RowsParams& p, const RowsPiece&
 
   // ---- the states to shared memory, and their merge ----
   float* acc = reinterpret_cast<float*>(smem);
-  float* ml = acc + kRowsWarps * 16 * Lay::kAccRow;
+  float* ml = acc + kRowsWarps * 16 * MT * Lay::kAccRow;
 #pragma unroll
-  for (int r = 0; r < 2; ++r) {
-    l[r] += __shfl_xor_sync(kAllLanes, l[r], 1);
-    l[r] += __shfl_xor_sync(kAllLanes, l[r], 2);
-    const int row = wk * M + wr * 16 + gl + 8 * r;
-    if (qi == 0) {
-      ml[2 * row] = m[r];
-      ml[2 * row + 1] = l[r];
-    }
+  for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-    for (int k = 0; k < NO; ++k) {
-      if constexpr (kF32) {
-        acc[row * Lay::kAccRow + (k >> 2) * 32 + 8 * qi + (k & 3)] = o[k][2 * r];
-        acc[row * Lay::kAccRow + (k >> 2) * 32 + 8 * qi + 4 + (k & 3)] = o[k][2 * r + 1];
-      } else {
-        *reinterpret_cast<float2*>(acc + row * Lay::kAccRow + k * 8 + 2 * qi) =
-            make_float2(o[k][2 * r], o[k][2 * r + 1]);
+    for (int r = 0; r < 2; ++r) {
+      float sum = l[mt][r];
+      sum += __shfl_xor_sync(kAllLanes, sum, 1);
+      sum += __shfl_xor_sync(kAllLanes, sum, 2);
+      const int row = wk * M + wr * 16 * MT + mt * 16 + gl + 8 * r;
+      if (qi == 0) {
+        ml[2 * row] = m[mt][r];
+        ml[2 * row + 1] = sum;
+      }
+#pragma unroll
+      for (int k = 0; k < NO; ++k) {
+        if constexpr (kF32) {
+          acc[row * Lay::kAccRow + (k >> 2) * 32 + 8 * qi + (k & 3)] = o[mt][k][2 * r];
+          acc[row * Lay::kAccRow + (k >> 2) * 32 + 8 * qi + 4 + (k & 3)] = o[mt][k][2 * r + 1];
+        } else {
+          *reinterpret_cast<float2*>(acc + row * Lay::kAccRow + k * 8 + 2 * qi) =
+              make_float2(o[mt][k][2 * r], o[mt][k][2 * r + 1]);
+        }
       }
     }
-  }
   __syncthreads();
   // four dims a thread
   for (int e = tid; e < M * (D / 4); e += kRowsThreads) {
@@ -594,9 +727,10 @@ __device__ __forceinline__ void rows_piece(const RowsParams& p, const RowsPiece&
 }
 
 // Tree: the batch's tiles split evenly over the grid (span.cuh).
-template <int MODE, int D, int WR>
-__global__ void __launch_bounds__(kRowsThreads, (rows_ctas<MODE, D>())) rows_tree_kernel(const RowsParams p) {
-  constexpr int KT = RowsTile<MODE, D>::kKeys, M = 16 * WR;
+template <int MODE, int D, int MT, int RG>
+__global__ void __launch_bounds__(kRowsThreads, (RowsLayout<MODE, D, MT, RG>::kCtas))
+    rows_tree_kernel(const RowsParams p) {
+  constexpr int KT = RowsTile<MODE, D>::kKeys, M = RowsLayout<MODE, D, MT, RG>::kRows;
   extern __shared__ __align__(128) unsigned char smem[];
   __shared__ long long scratch[32];
   griddep_wait();
@@ -630,15 +764,16 @@ __global__ void __launch_bounds__(kRowsThreads, (rows_ctas<MODE, D>())) rows_tre
     w.part = nullptr;
     if (w.t0 > 0 || w.t1 < q.t.nt)
       w.part = p.part + (2ll * blockIdx.x + (w.t0 == 0 ? 1 : 0)) * (M * (D + 4));
-    rows_piece<MODE, D, WR, true>(p, w, smem);
+    rows_piece<MODE, D, MT, RG, true>(p, w, smem);
     at += w.t1 - w.t0;
   }
 }
 
 // Prefill: a unit a CTA, whole, the longest first.
-template <int MODE, int D>
-__global__ void __launch_bounds__(kRowsThreads, (rows_ctas<MODE, D>())) rows_prefill_kernel(const RowsParams p) {
-  constexpr int KT = RowsTile<MODE, D>::kKeys, M = 64;
+template <int MODE, int D, int MT, int RG>
+__global__ void __launch_bounds__(kRowsThreads, (RowsLayout<MODE, D, MT, RG>::kCtas))
+    rows_prefill_kernel(const RowsParams p) {
+  constexpr int KT = RowsTile<MODE, D>::kKeys, M = RowsLayout<MODE, D, MT, RG>::kRows;
   extern __shared__ __align__(128) unsigned char smem[];
   griddep_wait();
   griddep_launch_dependents();
@@ -659,39 +794,58 @@ __global__ void __launch_bounds__(kRowsThreads, (rows_ctas<MODE, D>())) rows_pre
   w.t0 = 0;
   w.t1 = w.t.nt;
   w.part = nullptr;
-  rows_piece<MODE, D, 4, false>(p, w, smem);
+  rows_piece<MODE, D, MT, RG, false>(p, w, smem);
 }
 
-template <int MODE, int D, int WR>
-cudaError_t launch_rows_tree_wr(const RowsParams& p, int grid, int dev, cudaStream_t s) {
+template <int MODE, int D, int MT, int RG, bool TREE>
+cudaError_t launch_rows_as(const RowsParams& p, long long grid, int dev, cudaStream_t s) {
   static std::atomic<int> allowed[kDevices];
-  const auto kern = rows_tree_kernel<MODE, D, WR>;
-  constexpr size_t smem = RowsLayout<MODE, D, WR>::kSmem;
+  const auto kern = [] {
+    if constexpr (TREE) return rows_tree_kernel<MODE, D, MT, RG>;
+    else return rows_prefill_kernel<MODE, D, MT, RG>;
+  }();
+  constexpr size_t smem = RowsLayout<MODE, D, MT, RG>::kSmem;
   const cudaError_t e = allow_shared(kern, smem, allowed[dev]);
   if (e != cudaSuccess) return e;
   return launch_kernel(kern, dim3((unsigned)grid), dim3(kRowsThreads), smem, s, true, p);
 }
+
+// Units of 16, 32 or 64 rows.  A warp holds two row tiles where its registers allow: what it
+// reads and converts of K and V then serves both.
+template <int MODE, int D>
+struct RowsShapes {
+  static constexpr int kMT = MODE == PKV_F32 && D == 128 ? 1 : 2;
+  using R16 = RowsLayout<MODE, D, 1, 1>;
+  using R32 = RowsLayout<MODE, D, kMT, 2 / kMT>;
+  using R64 = RowsLayout<MODE, D, kMT, 4 / kMT>;
+};
 
 template <int MODE, int D>
 cudaError_t launch_rows_d(const RowsParams& p, bool tree, long long grid, int dev, cudaStream_t s) {
-  if (tree) {
-    if (p.plan.unit_rows == 16) return launch_rows_tree_wr<MODE, D, 1>(p, (int)grid, dev, s);
-    if (p.plan.unit_rows == 32) return launch_rows_tree_wr<MODE, D, 2>(p, (int)grid, dev, s);
-    return launch_rows_tree_wr<MODE, D, 4>(p, (int)grid, dev, s);
-  }
-  static std::atomic<int> allowed[kDevices];
-  const auto kern = rows_prefill_kernel<MODE, D>;
-  constexpr size_t smem = RowsLayout<MODE, D, 4>::kSmem;
-  const cudaError_t e = allow_shared(kern, smem, allowed[dev]);
-  if (e != cudaSuccess) return e;
-  return launch_kernel(kern, dim3((unsigned)grid), dim3(kRowsThreads), smem, s, true, p);
+  constexpr int MT = RowsShapes<MODE, D>::kMT;
+  if (!tree) return launch_rows_as<MODE, D, MT, 4 / MT, false>(p, grid, dev, s);
+  if (p.plan.unit_rows == 16) return launch_rows_as<MODE, D, 1, 1, true>(p, grid, dev, s);
+  if (p.plan.unit_rows == 32) return launch_rows_as<MODE, D, MT, 2 / MT, true>(p, grid, dev, s);
+  return launch_rows_as<MODE, D, MT, 4 / MT, true>(p, grid, dev, s);
+}
+
+template <int MODE, int D>
+constexpr int rows_ctas_d(int unit_rows) {
+  using S = RowsShapes<MODE, D>;
+  return unit_rows == 16 ? S::R16::kCtas : unit_rows == 32 ? S::R32::kCtas : S::R64::kCtas;
 }
 
 }  // namespace
 
 // One translation unit a pool type.
-cudaError_t launch_rows_bf16(const RowsParams& p, int D, bool tree, long long grid, int dev, cudaStream_t s);
-cudaError_t launch_rows_i8(const RowsParams& p, int D, bool tree, long long grid, int dev, cudaStream_t s);
-cudaError_t launch_rows_f32(const RowsParams& p, int D, bool tree, long long grid, int dev, cudaStream_t s);
+cudaError_t launch_rows_bf16(const RowsParams& p, int D, bool tree, long long grid, int dev,
+                             cudaStream_t s);
+int rows_ctas_bf16(int D, int unit_rows);  // CTAs of the tree kernel that an SM holds
+cudaError_t launch_rows_i8(const RowsParams& p, int D, bool tree, long long grid, int dev,
+                           cudaStream_t s);
+int rows_ctas_i8(int D, int unit_rows);  // CTAs of the tree kernel that an SM holds
+cudaError_t launch_rows_f32(const RowsParams& p, int D, bool tree, long long grid, int dev,
+                            cudaStream_t s);
+int rows_ctas_f32(int D, int unit_rows);  // CTAs of the tree kernel that an SM holds
 
 }  // namespace pkv

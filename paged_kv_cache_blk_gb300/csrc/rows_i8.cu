@@ -1,12 +1,16 @@
-// The kernels of rows.cuh for i8 pools.
+// The kernels of rows.cuh for int8 pools.
 #include "rows.cuh"
 
 namespace pkv {
 
 cudaError_t launch_rows_i8(const RowsParams& p, int D, bool tree, long long grid, int dev,
-                        cudaStream_t s) {
+                           cudaStream_t s) {
   return D == 64 ? launch_rows_d<PKV_I8, 64>(p, tree, grid, dev, s)
                  : launch_rows_d<PKV_I8, 128>(p, tree, grid, dev, s);
+}
+
+int rows_ctas_i8(int D, int unit_rows) {
+  return D == 64 ? rows_ctas_d<PKV_I8, 64>(unit_rows) : rows_ctas_d<PKV_I8, 128>(unit_rows);
 }
 
 }  // namespace pkv

@@ -141,13 +141,9 @@ TreePath tree_path(const PoolView& v, int G, int max_q_len, int sms) {
     return t;
   }
   t.unit_rows = rows <= 16 ? 16 : rows <= 32 ? 32 : 64;
-  int ctas;
-  if (v.quant)
-    ctas = v.head_dim == 64 ? rows_ctas<PKV_I8, 64>() : rows_ctas<PKV_I8, 128>();
-  else if (v.io_size == 2)
-    ctas = v.head_dim == 64 ? rows_ctas<PKV_BF16, 64>() : rows_ctas<PKV_BF16, 128>();
-  else
-    ctas = v.head_dim == 64 ? rows_ctas<PKV_F32, 64>() : rows_ctas<PKV_F32, 128>();
+  const int ctas = v.quant          ? rows_ctas_i8(v.head_dim, t.unit_rows)
+                   : v.io_size == 2 ? rows_ctas_bf16(v.head_dim, t.unit_rows)
+                                    : rows_ctas_f32(v.head_dim, t.unit_rows);
   t.grid = sms * ctas;
   t.bytes = (size_t)2 * t.grid * t.unit_rows * (v.head_dim + 4) * 4;
   return t;
