@@ -67,6 +67,20 @@ __device__ __forceinline__ float ld_cluster_f32(uint32_t addr) {
   return __uint_as_float(ld_cluster_u32(addr));
 }
 
+__device__ __forceinline__ float2 ld_cluster_f32x2(uint32_t addr) {
+  float2 v;
+  asm volatile("ld.shared::cluster.v2.f32 {%0,%1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(addr) : "memory");
+  return v;
+}
+__device__ __forceinline__ float4 ld_cluster_f32x4(uint32_t addr) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0,%1,%2,%3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(addr)
+               : "memory");
+  return v;
+}
+
 // Launch `kern` on `s` as clusters of `cluster` CTAs along x (grid.x a
 // multiple of it) and as a programmatic dependent of the work before it.
 // Dynamic shared memory that passes 48 KB with the kernel's own has to be

@@ -306,12 +306,6 @@ struct IntervalMask {
   __device__ __forceinline__ Chunk chunk(int c0) const { return Chunk{c_lo - c0, c_hi - c0}; }
 };
 
-// Columns a .. b of those from c0 on, as bits.
-__device__ __forceinline__ uint32_t column_bits(int a, int b, int c0) {
-  const int lo = max(a - c0, 0), hi = min(b - c0, 31);
-  return lo > hi ? 0u : (0xffffffffu << lo) & (0xffffffffu >> (31 - hi));
-}
-
 // Windows and trees: which of a tile's columns a row sees, a bit each.
 template <int COLS>
 struct WordMask {
@@ -327,20 +321,6 @@ struct WordMask {
     return Chunk{c0 < 64 ? (c0 == 0 ? w[0] : w[1]) : (c0 == 64 ? w[COLS / 32 - 2] : w[COLS / 32 - 1])};
   }
 };
-
-// 32 drafted tokens from number d on (which may lie before the first) of a row's mask.
-__device__ __forceinline__ uint32_t draft_bits(const unsigned long long* bits, int d, int n) {
-  if (d <= -32 || d >= n) return 0;
-  unsigned long long x;
-  if (d < 0) {
-    x = bits[0] << -d;
-  } else {
-    x = bits[d >> 6] >> (d & 63);
-    // (the next word where the 32 go on in it and it holds drafted tokens)
-    if ((d & 63) > 32 && ((d >> 6) + 1) * 64 < n) x |= bits[(d >> 6) + 1] << (64 - (d & 63));
-  }
-  return (uint32_t)x & column_bits(0, n - 1, d);
-}
 
 // Softmax of one S tile for one row: reads the row from TMEM, masks it,
 // updates the running state, rescales the O row when the maximum moved, and
@@ -592,22 +572,24 @@ __device__ __forceinline__ Item make_item_prefix(const PfParams& p, long long i)
 // holds a unit's first 128 rows, tile A the next where there are more (NARROW: the same rows).
 template <bool NARROW>
 struct TreeCursor {
-  long long at, end, first;  // tiles of the line; first: that of sequence b
+  long long at, end, first;  // steps of the line; first: that of sequence b
   int b;
   __device__ __forceinline__ bool next(const PfParams& p, Item& it) {
     while (at < end) {
       const SeqPlan q = seq_plan<kKeys>(p.plan, b);
-      if (at >= first + q.tiles) {
-        first += q.tiles;
+      if (at >= first + q.all_steps) {
+        first += q.all_steps;
         ++b;
         continue;
       }
-      const long long unit = div_pos(at - first, q.t.nt);
+      const PlanPart part = plan_part(p.plan, q, at - first, end - at);
+      at += part.steps;
+      if (part.t0 == part.t1) continue;
       it = Item{};
       it.valid = true;
       it.b = b;
-      it.g = (int)(unit / q.nru);
-      it.qtB = (NARROW ? 1 : 2) * (unit - (long long)it.g * q.nru);
+      it.g = part.unit / q.nru;
+      it.qtB = (NARROW ? 1 : 2) * (part.unit - it.g * q.nru);
       it.qtA = it.qtB + (NARROW ? 0 : 1);
       it.q0 = q.s.q0;
       it.nq = q.s.n;
@@ -616,11 +598,10 @@ struct TreeCursor {
       it.spanned = ((long long)q.s.off + q.s.ctx + q.s.n + p.bs - 1) / p.bs;
       it.list = q.t;
       it.lo = window_start(q.s.ctx, p.plan.span.window);
-      it.t0 = (int)(at - first - unit * q.t.nt);
-      it.nB = (int)min((long long)(q.t.nt - it.t0), end - at);
+      it.t0 = part.t0;
+      it.nB = part.t1 - part.t0;
       it.nA = it.qtA * p.TQ < it.nq ? it.nB : 0;
       it.slot = it.nB == q.t.nt ? -1 : 2 * (int)blockIdx.x + (it.t0 == 0 ? 1 : 0);
-      at += it.nB;
       return true;
     }
     return false;
@@ -1161,23 +1142,12 @@ __global__ void __launch_bounds__((pf_threads<MODE, SHARE>()), 1)
           key_hi = min((long long)p.prefix_blocks * p.bs, ob + lb);
         }
       }
-      // windows and trees: of the list's places the row sees those up to s_top that are first
-      // tokens or s_win or later, and drafted tokens by their bits
-      [[maybe_unused]] int s_top = -1, s_win = 0;
-      [[maybe_unused]] const unsigned long long* s_bits = nullptr;
+      [[maybe_unused]] RowSees s_row;  // windows and trees
       if constexpr (SPAN) {
-        if (row_ok) {
-          long long at = pos;
-          s_top = it.list.last(it.off + (int)pos);
-          if (TREE && p.mask) {
-            s_bits = p.mask + (it.q0 + qi) * p.words;
-            s_top = it.list.last(it.off + (int)it.first_pos - 1);
-            if (p.q_pos) at = max(it.first_pos, (long long)p.q_pos[it.q0 + qi]);
-          }
-          const int window = p.plan.span.window;
-          const long long first = window > 0 ? max(0ll, min(at - window + 1, kMaxPositions)) : 0;
-          s_win = it.list.behind(it.off + (int)first);
-        }
+        s_row = row_sees(p.plan.span, it.list, it.off, (int)it.first_pos, (int)it.nq,
+                         (int)(row_ok ? qi : 0), it.q0 + (row_ok ? qi : 0), TREE ? p.q_pos : nullptr,
+                         TREE ? p.mask : nullptr, p.words);
+        if (!row_ok) s_row.top = -1, s_row.bits = nullptr;
       }
       RowState st{-INFINITY, 0.f};
       for (int t = 0; t < nX && ok; ++t, ++nt) {
@@ -1186,25 +1156,11 @@ __global__ void __launch_bounds__((pf_threads<MODE, SHARE>()), 1)
         tc_fence_after();
         if constexpr (SPAN) {
           const int x0 = (it.t0 + t) * kKeys + (NARROW ? x * COLS : 0);
-          const int first = it.list.first(it.off) - x0;
-          const int sink_end = it.list.first(it.off + p.plan.span.sink) - x0;
-          const int top = s_top - x0, win = s_win - x0;
           // (a padding row may be taken for one that sees everything: it is not stored)
-          const bool full = __all_sync(
-              0xffffffffu,
-              !row_ok || (first <= 0 && top >= COLS - 1 && (win <= 0 || sink_end >= COLS)));
+          const bool full = __all_sync(0xffffffffu, !row_ok || s_row.all(x0, COLS));
           WordMask<COLS> seen;
 #pragma unroll
-          for (int c = 0; c < COLS / 32; ++c) {
-            seen.w[c] = 0;
-            if (!full) {
-              seen.w[c] = column_bits(first, min(top, sink_end - 1), 32 * c) |
-                          column_bits(max(first, win), top, 32 * c);
-              if (TREE && s_bits)
-                seen.w[c] |= draft_bits(
-                    s_bits, 32 * c + x0 - it.list.behind(it.off + (int)it.first_pos), (int)it.nq);
-            }
-          }
+          for (int c = 0; c < COLS / 32; ++c) seen.w[c] = full ? 0u : s_row.bits_from(x0 + 32 * c);
           softmax_tile<COLS>(tS(x), tO(x), lane_base, t, seen, full, p.qscale, st);
           tc_fence_before();
           __syncwarp();

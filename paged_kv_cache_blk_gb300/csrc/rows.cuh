@@ -50,10 +50,12 @@ struct RowsParams {
   long long num_blocks;
   int L, layer, row_bytes, scale_off, hq, bs_bits;
   int units_max;  // prefill: units of one kv head of the longest sequence
+  long long keys_most;  // prefill: keys that a unit's rows see at most
   float qscale;   // scale * log2(e)
 };
 
 constexpr int kRowsWarps = 4;
+constexpr int kRowsMaxCluster = 8;
 constexpr int kRowsThreads = kRowsWarps * 32;
 
 namespace {
@@ -130,7 +132,7 @@ struct RowsLayout {
   static constexpr int kMerge = kRowsWarps * 16 * MT * (kAccRow + 2) * 4;
   static constexpr int kQAt = kRing > kMerge ? kRing : kMerge;
   static constexpr int kSeenAt = kQAt + kQ;  // what each of a warp's rows sees
-  static constexpr int kSmem = kSeenAt + kRowsWarps * 16 * MT * 16;
+  static constexpr int kSmem = kSeenAt + kRowsWarps * 16 * MT * (int)sizeof(RowSees);
   // CTAs that an SM holds at once, of the tree kernel its grid: what shared memory and O's
   // registers allow
   static constexpr int kFit = 227 * 1024 / (kSmem + 2048);
@@ -148,7 +150,7 @@ struct RowsPiece {
 };
 
 template <int MODE, int D, int MT, int RG, bool TREE>
-__device__ __forceinline__ void rows_piece(const RowsParams& p, const RowsPiece& w,
+__device__ __forceinline__ void rows_piece(const RowsParams& p, const RowsPiece& w, int ctas,
                                            unsigned char* smem) {
   using Tl = RowsTile<MODE, D>;
   using Lay = RowsLayout<MODE, D, MT, RG>;
@@ -214,48 +216,21 @@ __device__ __forceinline__ void rows_piece(const RowsParams& p, const RowsPiece&
 #pragma unroll 1
   for (int s = 0; s < NST - 1; ++s) issue(w.t0 + s, s);
 
-  // ---- what the warp's rows see, a row a lane ----
-  // the places first .. top of the list that are first tokens or lo or later, and, in a masked
-  // tree, of the places from draft on those with their bit
-  const bool masked_tree = TREE && p.mask != nullptr;
-  const int first_place = w.t.first(off), sink_place = w.t.first(sink_end);
-  const int draft = w.t.behind(off + w.s.ctx);
+  // ---- what the warp's rows see, a row a lane: kept in shared memory ----
   const int warp_row = w.first_row + wr * 16 * MT;
-  const uint32_t seen_at = base + Lay::kSeenAt + warp * (16 * MT * 16);
+  RowSees* seen_rows = reinterpret_cast<RowSees*>(smem + Lay::kSeenAt) + warp * (16 * MT);
   int full_lo, full_hi;  // places that every row of the warp sees
   {
     const int r = warp_row + lane % (16 * MT);
     const bool live = r < rows;
     const int tok = live ? r / G : 0;
-    int pos = w.s.ctx + tok, lo = w.t.behind(off);
-    const int top = w.t.last(off + (masked_tree ? w.s.ctx - 1 : pos));
-    if (p.plan.span.window > 0) {
-      if (TREE && p.q_pos) pos = max(w.s.ctx, p.q_pos[w.s.q0 + tok]);
-      const long long first = (long long)pos - p.plan.span.window + 1;
-      lo = w.t.behind(off + (int)max(0ll, min(first, kMaxPositions)));
-    }
-    if (lane < 16 * MT)
-      sts128(seen_at + lane * 16, make_uint4((uint32_t)lo, (uint32_t)top, (uint32_t)tok, 0u));
-    full_lo = max(first_place, __reduce_max_sync(kAllLanes, live ? lo : INT_MIN));
-    full_hi = __reduce_min_sync(kAllLanes, live ? top : INT_MAX);
+    const RowSees row = row_sees(p.plan.span, w.t, off, w.s.ctx, n, tok, w.s.q0 + tok,
+                                 TREE ? p.q_pos : nullptr, TREE ? p.mask : nullptr, p.words);
+    if (lane < 16 * MT) seen_rows[lane] = row;
+    full_lo = max(row.first, __reduce_max_sync(kAllLanes, live ? row.lo : INT_MIN));
+    full_hi = __reduce_min_sync(kAllLanes, live ? row.top : INT_MAX);
     __syncwarp();
   }
-  // row i (of gl, gl + 8) of row tile mt: is place x seen?
-  struct RowSees {
-    int lo, top;
-    const unsigned long long* bits;
-  };
-  auto row_sees = [&](int mt, int i) {
-    const uint4 v = lds128(seen_at + (mt * 16 + gl + 8 * i) * 16);
-    return RowSees{(int)v.x, (int)v.y,
-                   masked_tree ? p.mask + (w.s.q0 + (int)v.z) * p.words : nullptr};
-  };
-  auto sees = [&](const RowSees& r, int x) -> bool {
-    if (x <= r.top) return x >= first_place && (x >= r.lo || x < sink_place);
-    if (!TREE || r.bits == nullptr) return false;
-    const int d = x - draft;
-    return d >= 0 && d < n && (r.bits[d >> 6] >> (d & 63) & 1);
-  };
 
   // ---- Q, rows behind the last one as zeros ----
   auto q_row = [&](int r) {
@@ -499,12 +474,12 @@ __device__ __forceinline__ void rows_piece(const RowsParams& p, const RowsPiece&
 #pragma unroll
           for (int c = 0; c < 2; ++c) s[mt][j][2 * r + c] *= kI8 ? factor[j][c] : p.qscale;
         if (!full) {
-          const RowSees row = row_sees(mt, r);
+          const uint32_t bits = seen_rows[mt * 16 + gl + 8 * r].bits_from(p0) >> key(0, 0);
 #pragma unroll
           for (int j = 0; j < NT; ++j)
 #pragma unroll
             for (int c = 0; c < 2; ++c)
-              if (!sees(row, p0 + key(j, c))) s[mt][j][2 * r + c] = -INFINITY;
+              if (!(bits >> (key(j, c) - key(0, 0)) & 1)) s[mt][j][2 * r + c] = -INFINITY;
         }
 #pragma unroll
         for (int j = 0; j < NT; ++j)
@@ -659,6 +634,20 @@ __device__ __forceinline__ void rows_piece(const RowsParams& p, const RowsPiece&
   cp_wait<0>();
   __syncthreads();
 
+  // four dims of a row's result
+  auto finish = [&](int r, int d, float sum, const float (&x)[4]) {
+    const float inv = sum == 0.f ? 0.f : 1.f / sum;  // no weight at all: zeros
+    const int tok = r / G;
+    const long long at = ((w.s.q0 + tok) * p.hq + w.g * G + (r - tok * G)) * D + d;
+    if constexpr (kF32) {
+      *reinterpret_cast<float4*>(p.out + at * 4) =
+          make_float4(x[0] * inv, x[1] * inv, x[2] * inv, x[3] * inv);
+    } else {
+      *reinterpret_cast<uint2*>(p.out + at * 2) =
+          make_uint2(pack_bf16x2(x[0] * inv, x[1] * inv), pack_bf16x2(x[2] * inv, x[3] * inv));
+    }
+  };
+
   // ---- the states to shared memory, and their merge ----
   float* acc = reinterpret_cast<float*>(smem);
   float* ml = acc + kRowsWarps * 16 * MT * Lay::kAccRow;
@@ -686,6 +675,49 @@ __device__ __forceinline__ void rows_piece(const RowsParams& p, const RowsPiece&
       }
     }
   __syncthreads();
+  if constexpr (!TREE) {
+    // prefill: a cluster's CTAs share the unit's tiles, and its rows in their merge
+    if (ctas > 1) {
+      cluster_sync();
+      const uint32_t rank = cluster_rank();
+      for (int e = (int)rank * kRowsThreads + tid; e < M * (D / 4); e += ctas * kRowsThreads) {
+        const int row = e / (D / 4), d = e % (D / 4) * 4, r = w.first_row + row;
+        if (r >= rows) break;
+        float top_m = -INFINITY, sum = 0.f, x[4] = {0.f, 0.f, 0.f, 0.f};
+        for (int c = 0; c < ctas; ++c) {
+          const uint32_t ml_c = cluster_map(smem_addr(ml), c), acc_c = cluster_map(base, c);
+          float2 s[WK];
+          float4 y[WK];
+#pragma unroll
+          for (int u = 0; u < WK; ++u) {
+            s[u] = ld_cluster_f32x2(ml_c + (u * M + row) * 8);
+            y[u] = ld_cluster_f32x4(acc_c + ((u * M + row) * Lay::kAccRow + d) * 4);
+          }
+          float most = top_m;
+#pragma unroll
+          for (int u = 0; u < WK; ++u) most = fmaxf(most, s[u].x);
+          const float shrink = most == top_m ? 1.f : exp2f(top_m - most);
+          top_m = most;
+          sum *= shrink;
+#pragma unroll
+          for (int k = 0; k < 4; ++k) x[k] *= shrink;
+#pragma unroll
+          for (int u = 0; u < WK; ++u) {
+            // a state at -inf saw nothing, or only NaN: its sum and O are 0, or NaN
+            const float f = s[u].x == -INFINITY ? 1.f : exp2f(s[u].x - top_m);
+            sum += f * s[u].y;
+            x[0] += f * y[u].x;
+            x[1] += f * y[u].y;
+            x[2] += f * y[u].z;
+            x[3] += f * y[u].w;
+          }
+        }
+        finish(r, d, sum, x);
+      }
+      cluster_sync();  // no CTA leaves while another may still read its states
+      return;
+    }
+  }
   // four dims a thread
   for (int e = tid; e < M * (D / 4); e += kRowsThreads) {
     const int row = e / (D / 4), d = e % (D / 4) * 4, r = w.first_row + row;
@@ -712,16 +744,7 @@ __device__ __forceinline__ void rows_piece(const RowsParams& p, const RowsPiece&
       if (d == 0) *reinterpret_cast<float2*>(dst) = make_float2(top_m, sum);
       continue;
     }
-    const float inv = sum == 0.f ? 0.f : 1.f / sum;  // no weight at all: zeros
-    const int tok = r / G;
-    const long long at = ((w.s.q0 + tok) * p.hq + w.g * G + (r - tok * G)) * D + d;
-    if constexpr (kF32) {
-      *reinterpret_cast<float4*>(p.out + at * 4) =
-          make_float4(x[0] * inv, x[1] * inv, x[2] * inv, x[3] * inv);
-    } else {
-      *reinterpret_cast<uint2*>(p.out + at * 2) =
-          make_uint2(pack_bf16x2(x[0] * inv, x[1] * inv), pack_bf16x2(x[2] * inv, x[3] * inv));
-    }
+    finish(r, d, sum, x);
   }
   __syncthreads();  // before the ring is filled again
 }
@@ -745,31 +768,33 @@ __global__ void __launch_bounds__(kRowsThreads, (RowsLayout<MODE, D, MT, RG>::kC
   }
   while (at < end) {
     const SeqPlan q = seq_plan<KT>(p.plan, b);
-    if (at >= first + q.tiles) {  // the next sequence
-      first += q.tiles;
+    if (at >= first + q.all_steps) {  // the next sequence
+      first += q.all_steps;
       ++b;
       continue;
     }
-    const long long unit = div_pos(at - first, q.t.nt);
+    const PlanPart part = plan_part(p.plan, q, at - first, end - at);
+    at += part.steps;
+    if (part.t0 == part.t1) continue;
     RowsPiece w;
     w.s = q.s;
     w.t = q.t;
     w.b = b;
-    w.g = (int)(unit / q.nru);
-    w.first_row = (int)(unit - (long long)w.g * q.nru) * M;
-    w.t0 = (int)(at - first - unit * q.t.nt);
-    w.t1 = (int)min((long long)q.t.nt, w.t0 + (end - at));
+    w.g = part.unit / q.nru;
+    w.first_row = (part.unit - w.g * q.nru) * M;
+    w.t0 = part.t0;
+    w.t1 = part.t1;
     w.lo = window_start(q.s.ctx, p.plan.span.window);
     w.hi = q.s.ctx + q.s.n - 1;
     w.part = nullptr;
     if (w.t0 > 0 || w.t1 < q.t.nt)
       w.part = p.part + (2ll * blockIdx.x + (w.t0 == 0 ? 1 : 0)) * (M * (D + 4));
-    rows_piece<MODE, D, MT, RG, true>(p, w, smem);
-    at += w.t1 - w.t0;
+    rows_piece<MODE, D, MT, RG, true>(p, w, 1, smem);
   }
 }
 
-// Prefill: a unit a CTA, whole, the longest first.
+// Prefill: a unit a cluster of CTAs, which take its tiles in turns of equal length; the last
+// rows' units first.
 template <int MODE, int D, int MT, int RG>
 __global__ void __launch_bounds__(kRowsThreads, (RowsLayout<MODE, D, MT, RG>::kCtas))
     rows_prefill_kernel(const RowsParams p) {
@@ -777,37 +802,65 @@ __global__ void __launch_bounds__(kRowsThreads, (RowsLayout<MODE, D, MT, RG>::kC
   extern __shared__ __align__(128) unsigned char smem[];
   griddep_wait();
   griddep_launch_dependents();
+  uint32_t ctas;
+  asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(ctas));
+  const int rank = (int)cluster_rank(), item = (int)(blockIdx.x / ctas);
   const int per = p.plan.span.batch * p.plan.hkv;
-  const int u = p.units_max - 1 - (int)(blockIdx.x / per), rest = (int)(blockIdx.x % per);
+  const int u = p.units_max - 1 - item / per, rest = item % per;
   RowsPiece w;
   w.b = rest / p.plan.hkv;
   w.g = rest - w.b * p.plan.hkv;
   w.s = seq_span(p.plan.span, w.b);
-  if (w.s.bad && u == 0 && w.g == 0 && threadIdx.x == 0) set_error(p.err, kErrCapacity);
+  if (w.s.bad && u == 0 && w.g == 0 && rank == 0 && threadIdx.x == 0) set_error(p.err, kErrCapacity);
   w.first_row = u * M;
-  if (w.first_row >= w.s.n * p.plan.G) return;
+  if (w.first_row >= w.s.n * p.plan.G) return;  // the whole cluster
   const int tok0 = w.first_row / p.plan.G;
   const int tok1 = min(w.s.n - 1, (w.first_row + M - 1) / p.plan.G);
   w.lo = window_start(w.s.ctx + tok0, p.plan.span.window);
   w.hi = w.s.ctx + tok1;
   w.t = key_list<KT>(p.plan.span, w.s.off, w.lo, w.hi);
-  w.t0 = 0;
-  w.t1 = w.t.nt;
+  w.t0 = (int)((long long)w.t.nt * rank / ctas);
+  w.t1 = (int)((long long)w.t.nt * (rank + 1) / ctas);
   w.part = nullptr;
-  rows_piece<MODE, D, MT, RG, false>(p, w, smem);
+  rows_piece<MODE, D, MT, RG, false>(p, w, (int)ctas, smem);
 }
 
-template <int MODE, int D, int MT, int RG, bool TREE>
-cudaError_t launch_rows_as(const RowsParams& p, long long grid, int dev, cudaStream_t s) {
+template <int MODE, int D, int MT, int RG>
+cudaError_t launch_tree_as(const RowsParams& p, long long grid, int dev, cudaStream_t s) {
   static std::atomic<int> allowed[kDevices];
-  const auto kern = [] {
-    if constexpr (TREE) return rows_tree_kernel<MODE, D, MT, RG>;
-    else return rows_prefill_kernel<MODE, D, MT, RG>;
-  }();
+  const auto kern = rows_tree_kernel<MODE, D, MT, RG>;
   constexpr size_t smem = RowsLayout<MODE, D, MT, RG>::kSmem;
   const cudaError_t e = allow_shared(kern, smem, allowed[dev]);
   if (e != cudaSuccess) return e;
   return launch_kernel(kern, dim3((unsigned)grid), dim3(kRowsThreads), smem, s, true, p);
+}
+
+// Clusters of as many CTAs as the device holds at once beside one another, with two tiles each
+// or more.
+template <int MODE, int D, int MT, int RG>
+cudaError_t launch_prefill_as(const RowsParams& p, int dev, cudaStream_t s) {
+  static std::atomic<int> allowed[kDevices], known[kDevices][kRowsMaxCluster + 1];
+  using Lay = RowsLayout<MODE, D, MT, RG>;
+  const auto kern = rows_prefill_kernel<MODE, D, MT, RG>;
+  cudaError_t e = allow_shared(kern, Lay::kSmem, allowed[dev]);
+  if (e != cudaSuccess) return e;
+  const long long units = (long long)p.units_max * p.plan.span.batch * p.plan.hkv;
+  const long long tiles = (p.keys_most + RowsTile<MODE, D>::kKeys - 1) / RowsTile<MODE, D>::kKeys + 1;
+  int ctas = 1;
+  for (int c = kRowsMaxCluster; c > 1; c >>= 1) {
+    int held = 0;
+    e = clusters_held(kern, kRowsThreads, Lay::kSmem, (unsigned)c, known[dev][c], &held);
+    if (e != cudaSuccess) return e;
+    if (units <= held && tiles >= 2 * c) {
+      ctas = c;
+      break;
+    }
+  }
+  if (ctas == 1)
+    return launch_kernel(kern, dim3((unsigned)units), dim3(kRowsThreads), (size_t)Lay::kSmem, s, true,
+                         p);
+  return launch_clusters(kern, dim3((unsigned)(units * ctas)), dim3(kRowsThreads), Lay::kSmem,
+                         (unsigned)ctas, s, p);
 }
 
 // Units of 16, 32 or 64 rows.  A warp holds two row tiles where its registers allow: what it
@@ -823,10 +876,14 @@ struct RowsShapes {
 template <int MODE, int D>
 cudaError_t launch_rows_d(const RowsParams& p, bool tree, long long grid, int dev, cudaStream_t s) {
   constexpr int MT = RowsShapes<MODE, D>::kMT;
-  if (!tree) return launch_rows_as<MODE, D, MT, 4 / MT, false>(p, grid, dev, s);
-  if (p.plan.unit_rows == 16) return launch_rows_as<MODE, D, 1, 1, true>(p, grid, dev, s);
-  if (p.plan.unit_rows == 32) return launch_rows_as<MODE, D, MT, 2 / MT, true>(p, grid, dev, s);
-  return launch_rows_as<MODE, D, MT, 4 / MT, true>(p, grid, dev, s);
+  const int rows = p.plan.unit_rows;
+  if (tree)
+    return rows == 16   ? launch_tree_as<MODE, D, 1, 1>(p, grid, dev, s)
+           : rows == 32 ? launch_tree_as<MODE, D, MT, 2 / MT>(p, grid, dev, s)
+                        : launch_tree_as<MODE, D, MT, 4 / MT>(p, grid, dev, s);
+  return rows == 16   ? launch_prefill_as<MODE, D, 1, 1>(p, dev, s)
+         : rows == 32 ? launch_prefill_as<MODE, D, MT, 2 / MT>(p, dev, s)
+                      : launch_prefill_as<MODE, D, MT, 4 / MT>(p, dev, s);
 }
 
 template <int MODE, int D>

@@ -87,29 +87,92 @@ __device__ __forceinline__ int window_start(int pos, int window) {
   return window > 0 ? max(0, pos - window + 1) : 0;
 }
 
+// Places a .. b of the 32 from c0 on, as bits.
+__device__ __forceinline__ uint32_t column_bits(int a, int b, int c0) {
+  const int lo = max(a - c0, 0), hi = min(b - c0, 31);
+  return lo > hi ? 0u : (0xffffffffu << lo) & (0xffffffffu >> (31 - hi));
+}
+
+// 32 drafted tokens from number d on (which may lie before the first) of a row's mask of n.
+__device__ __forceinline__ uint32_t draft_bits(const unsigned long long* bits, int d, int n) {
+  if (d <= -32 || d >= n) return 0;
+  unsigned long long x;
+  if (d < 0) {
+    x = bits[0] << -d;
+  } else {
+    x = bits[d >> 6] >> (d & 63);
+    // (the next word where the 32 go on in it and it holds drafted tokens)
+    if ((d & 63) > 32 && ((d >> 6) + 1) * 64 < n) x |= bits[(d >> 6) + 1] << (64 - (d & 63));
+  }
+  return (uint32_t)x & column_bits(0, n - 1, d);
+}
+
+// What a query sees of a list: the places first .. top that are first tokens (before sink) or
+// in its window (lo or later), and the drafted tokens, from place draft on, by their bits.
+struct RowSees {
+  int first, sink, lo, top, draft, n;
+  const unsigned long long* bits;
+  __device__ __forceinline__ bool all(int x, int keys) const {  // of places x .. x + keys - 1
+    return x >= first && x + keys - 1 <= top && (x >= lo || x + keys <= sink);
+  }
+  __device__ __forceinline__ uint32_t bits_from(int x) const {  // of the 32 places from x on
+    uint32_t w = column_bits(first, min(top, sink - 1), x) | column_bits(max(first, lo), top, x);
+    if (bits) w |= draft_bits(bits, x - draft, n);
+    return w;
+  }
+};
+
+// Token tok of n new ones, query row `query` of the batch; q_pos and mask may be NULL (see
+// pkv_decode_attention_tree).
+__device__ __forceinline__ RowSees row_sees(const SpanParams& p, const KeyList& t, int off, int ctx,
+                                            int n, int tok, long long query, const int32_t* q_pos,
+                                            const unsigned long long* mask, int words) {
+  RowSees r;
+  r.first = t.first(off);
+  r.sink = t.first(off + p.sink);
+  r.top = t.last(off + (mask ? ctx - 1 : ctx + tok));
+  r.draft = t.behind(off + ctx);
+  r.n = n;
+  r.bits = mask ? mask + query * words : nullptr;
+  long long start = 0;
+  if (p.window > 0) {
+    const int pos = q_pos ? max(ctx, q_pos[query]) : ctx + tok;
+    start = max(0ll, min((long long)pos - p.window + 1, kMaxPositions));
+  }
+  r.lo = t.behind(off + (int)start);
+  return r;
+}
+
 // ---- one list of tiles for a batch, split evenly over a grid --------------------------
 //
 // A unit is UR query rows (tokens x heads of a group) of one sequence and kv head over
-// all of the sequence's tiles.  The units of all sequences in order, tile by tile, are
-// one line of T tiles; CTA c takes the tiles [c * chunk, (c + 1) * chunk) of it, so
-// every CTA has the same work whatever the lengths.  A unit that lies in one CTA's share
-// is finished there; of the others each CTA leaves the state of its part in slot
-// 2 c (a unit that began before the share) or 2 c + 1 (one that goes on behind it), and a
-// second kernel merges them.
+// all of the sequence's tiles, with `lead` steps of no work before them that stand for what a
+// unit costs besides its tiles.  The units of all sequences in order, step by step, are one
+// line of T steps; CTA c takes the steps [c * chunk, (c + 1) * chunk) of it, so every CTA has
+// the same work whatever the lengths.  A unit whose tiles lie in one CTA's share is finished
+// there; of the others each CTA leaves the state of its part in slot 2 c (a part that does not
+// begin with the unit's first tile) or 2 c + 1, and a second kernel merges them.
 
 struct PlanParams {
   SpanParams span;
   int unit_rows;  // UR
   int G, hkv;
-  int least;  // tiles of a share at least
+  int lead;  // steps before a unit's tiles
 };
 
 struct SeqPlan {
   SeqSpan s;
   KeyList t;
   int nru;  // units of one kv head
-  long long tiles;
+  int steps;  // of a unit
+  long long all_steps;
 };
+
+// A part of a unit: steps x .. of it, at most `most` of them.
+struct PlanPart {
+  int unit, t0, t1, steps;  // unit of the sequence (kv head major); tiles t0 .. t1 - 1
+};
+
 
 template <int KT>
 __device__ __forceinline__ SeqPlan seq_plan(const PlanParams& p, int b) {
@@ -122,7 +185,8 @@ __device__ __forceinline__ SeqPlan seq_plan(const PlanParams& p, int b) {
                        q.s.ctx + q.s.n - 1);
     q.nru = (q.s.n * p.G + p.unit_rows - 1) / p.unit_rows;
   }
-  q.tiles = (long long)q.t.nt * q.nru * p.hkv;
+  q.steps = q.t.nt + p.lead;
+  q.all_steps = (long long)q.steps * q.nru * p.hkv;
   return q;
 }
 
@@ -132,17 +196,29 @@ __device__ __forceinline__ long long div_pos(long long a, long long b) {
   return a / b;
 }
 
-__device__ __forceinline__ long long plan_chunk(const PlanParams& p, long long total, int grid) {
-  const long long c = div_pos(total + grid - 1, grid);
-  return c > p.least ? c : p.least;
+// Steps of a share.
+__device__ __forceinline__ long long plan_chunk(long long total, int grid) {
+  return max(1ll, div_pos(total + grid - 1, grid));
 }
 
-// What the merge needs of the line: its length, and the tiles before one sequence.
+// The part that begins `at` steps into the sequence's, up to `most` steps.
+__device__ __forceinline__ PlanPart plan_part(const PlanParams& p, const SeqPlan& q, long long at,
+                                              long long most) {
+  PlanPart r;
+  r.unit = (int)div_pos(at, q.steps);
+  const int x = (int)(at - (long long)r.unit * q.steps);
+  r.steps = (int)min((long long)(q.steps - x), most);
+  r.t0 = max(0, x - p.lead);
+  r.t1 = max(0, x + r.steps - p.lead);
+  return r;
+}
+
+// What the merge needs of the line: its length, and the steps before one sequence.
 struct PlanSums {
   long long total, before;
 };
 
-// A CTA's share: tiles at .. end - 1, the first of them in sequence b, whose own tiles begin
+// A CTA's share: steps at .. end - 1, the first of them in sequence b, whose own steps begin
 // at `first`.
 struct PlanShare {
   long long at, end, first;
@@ -175,9 +251,9 @@ template <int KT>
 __device__ __forceinline__ PlanSums plan_sums(const PlanParams& p, int seq, long long* s) {
   long long all = 0, before = 0;
   for (int b = threadIdx.x; b < p.span.batch; b += blockDim.x) {
-    const long long tiles = seq_plan<KT>(p, b).tiles;
-    all += tiles;
-    before += b < seq ? tiles : 0;
+    const long long steps = seq_plan<KT>(p, b).all_steps;
+    all += steps;
+    before += b < seq ? steps : 0;
   }
   PlanSums r;
   block_scan(all, s, &r.total);
@@ -192,21 +268,21 @@ __device__ __forceinline__ PlanShare plan_share(const PlanParams& p, int cta, in
   __shared__ PlanShare found;
   const int n = (int)blockDim.x, tid = threadIdx.x;
   const bool once = p.span.batch <= n;
-  long long mine = tid < p.span.batch ? seq_plan<KT>(p, tid).tiles : 0;
+  long long mine = tid < p.span.batch ? seq_plan<KT>(p, tid).all_steps : 0;
   long long total, incl = block_scan(mine, s, &total);
   for (int b0 = n; b0 < p.span.batch; b0 += n) {
     long long all;
-    block_scan(b0 + tid < p.span.batch ? seq_plan<KT>(p, b0 + tid).tiles : 0, s, &all);
+    block_scan(b0 + tid < p.span.batch ? seq_plan<KT>(p, b0 + tid).all_steps : 0, s, &all);
     total += all;
   }
-  const long long chunk = plan_chunk(p, total, grid);
+  const long long chunk = plan_chunk(total, grid);
   const long long at = min(total, cta * chunk), end = min(total, at + chunk);
   if (at >= end) return PlanShare{at, end, 0, 0};
   long long base = 0;
   for (int b0 = 0;; b0 += n) {
     long long all = total;
     if (!once) {
-      mine = b0 + tid < p.span.batch ? seq_plan<KT>(p, b0 + tid).tiles : 0;
+      mine = b0 + tid < p.span.batch ? seq_plan<KT>(p, b0 + tid).all_steps : 0;
       incl = block_scan(mine, s, &all);
     }
     const long long stop = base + incl;

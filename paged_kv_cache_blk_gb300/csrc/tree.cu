@@ -28,7 +28,7 @@ __device__ __forceinline__ void combine_row(const CombineParams& p, const SeqPla
   const int lane = threadIdx.x & 31;
   const int tok = row / p.hq, h = row - tok * p.hq, g = h / p.plan.G;
   const int r = tok * p.plan.G + h - g * p.plan.G, ur = p.plan.unit_rows, unit = r / ur;
-  const long long start = before + ((long long)g * q.nru + unit) * q.t.nt;
+  const long long start = before + ((long long)g * q.nru + unit) * q.steps + p.plan.lead;
   const long long c0 = div_pos(start, chunk), c1 = div_pos(start + q.t.nt - 1, chunk);
   if (c0 == c1) return;
   const long long row_floats = p.D + 4, slot = ur * row_floats;
@@ -96,7 +96,7 @@ __global__ void __launch_bounds__(kCombineWarps * 32) tree_combine_kernel(const 
     return;
   }
   const PlanSums sums = plan_sums<KT>(p.plan, b, scratch);
-  const long long chunk = plan_chunk(p.plan, sums.total, p.grid), before = sums.before;
+  const long long chunk = plan_chunk(sums.total, p.grid), before = sums.before;
   griddep_wait();
   griddep_launch_dependents();
   for (int i = 0; i < p.rows_warp; ++i) {
@@ -154,6 +154,11 @@ cudaError_t launch_rows(const PoolView& v, const RowsParams& p, bool tree, long 
   if (v.quant) return launch_rows_i8(p, v.head_dim, tree, grid, dev, s);
   if (v.io_size == 2) return launch_rows_bf16(p, v.head_dim, tree, grid, dev, s);
   return launch_rows_f32(p, v.head_dim, tree, grid, dev, s);
+}
+
+// Which kernel a windowed prefill takes, where both could.
+bool prefill_on_tcgen05(const PoolView& v, const RowsParams& p, int sms) {
+  return prefill_supported(v, p.hq) == 0 && p.plan.unit_rows > 32;
 }
 
 // The arguments that the two calls share.
@@ -214,7 +219,6 @@ RowsParams rows_params(const Call& c, const PoolView& v, int* err) {
   s.gran = 1;
   p.plan.G = c.num_q_heads / v.num_kv_heads;
   p.plan.hkv = v.num_kv_heads;
-  p.plan.least = 1;
   p.k = v.k;
   p.v = v.v;
   p.q = static_cast<const char*>(c.q);
@@ -294,6 +298,7 @@ pkv_status pkv_decode_attention_tree(const pkv_pool* pool, int32_t layer, const 
   const pkv::TreePath path = pkv::tree_path(v, p.plan.G, max_q_len, sms);
   if (workspace_bytes < path.bytes) return PKV_ERR_WORKSPACE;
   p.plan.unit_rows = path.unit_rows;
+  p.plan.lead = path.tcgen05 ? 2 : 4;
   if (path.tcgen05) p.plan.span.gran = v.block_size;  // (tensor copies of whole blocks)
   p.part = static_cast<float*>(workspace);
   p.mask = reinterpret_cast<const unsigned long long*>(tree_mask);
@@ -350,16 +355,18 @@ pkv_status pkv_prefill_attention_window(const pkv_pool* pool, int32_t layer, con
     return (pkv_status)st;
   if ((st = pkv::device_sm_count(&sms, &dev)) != PKV_OK) return (pkv_status)st;
   pkv::RowsParams p = pkv::rows_params(c, v, err);
-  p.plan.unit_rows = 64;
+  const int64_t rows = (int64_t)max_q_len * p.plan.G;
+  p.plan.unit_rows = rows <= 16 ? 16 : rows <= 32 ? 32 : 64;
   if (validate && (st = pkv::validate_call(p, stream)) != PKV_OK) return (pkv_status)st;
-  p.units_max = (int)(((int64_t)max_q_len * p.plan.G + 63) / 64);
-  const long long grid = (long long)p.units_max * batch * v.num_kv_heads;
+  p.units_max = (int)((rows + p.plan.unit_rows - 1) / p.plan.unit_rows);
+  const int64_t held = (int64_t)max_blocks_per_seq * v.block_size;
+  p.keys_most = std::min(held, (int64_t)window + p.plan.span.sink + p.plan.unit_rows / p.plan.G);
   const cudaError_t e =
-      pkv::prefill_supported(v, num_q_heads) == 0
+      pkv::prefill_on_tcgen05(v, p, sms)
           ? pkv::launch_prefill(v, layer, q, num_q_heads, scale, block_tables, max_blocks_per_seq,
                                 seq_lens, offsets, cu_q, batch, total_q, max_q_len, window,
                                 p.plan.span.sink, out, err, sms, stream)
-          : pkv::launch_rows(v, p, false, grid, dev, stream);
+          : pkv::launch_rows(v, p, false, 0, dev, stream);
   if ((st = pkv::launch_status(e)) != PKV_OK) return (pkv_status)st;
   return validate ? (pkv_status)pkv::read_and_clear_error_word(err, stream) : PKV_OK;
 }
