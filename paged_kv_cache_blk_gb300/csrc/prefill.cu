@@ -60,6 +60,7 @@ constexpr int kPfWarps = 10;  // 0-3 softmax A, 4-7 softmax B, 8 TMA, 9 MMA
 constexpr int kWarpTma = 8;
 constexpr int kWarpMma = 9;
 constexpr int kWarpFwd = 10;  // CTA pairs: forwards this CTA's halves to the other CTA
+constexpr int kWarpV = 11;    // trees: loads V, beside the K of warp 8
 
 // What an item computes, and which keys its rows see.
 enum PfMode : int {
@@ -70,28 +71,34 @@ enum PfMode : int {
   kNarrow,  // the same for up to 128 rows: both tiles are those rows, over half of the keys each
 };
 __host__ __device__ constexpr bool is_tree(int mode) { return mode == kTree || mode == kNarrow; }
-// threads of a CTA: one more warp in a CTA pair, and for trees
+// threads of a CTA: one more warp in a CTA pair, two for trees
 template <int MODE, bool SHARE>
 constexpr int pf_threads() {
-  return (kPfWarps + (SHARE || is_tree(MODE) ? 1 : 0)) * 32;
+  return (kPfWarps + (is_tree(MODE) ? 2 : SHARE ? 1 : 0)) * 32;
 }
 constexpr int kRows = 128;   // MMA M: query rows per tile
 constexpr int kKeys = 128;   // keys per KV tile (MMA N of Q K^T, K of P V)
 constexpr int kD = 128;      // head_dim
 constexpr int kHalf = 128 * 64 * 2;  // one 128-row x 64-column bf16 half tile (16 KB)
 constexpr int kTileBytes = 2 * kHalf;  // 32 KB
-constexpr int kSlots = 4;              // K / V ring: K(t) V(t) K(t+1) V(t+1)
 constexpr uint32_t kTmemCols = 512;    // S_A, S_B, O_A, O_B
 constexpr float kLog2e = 1.4426950408889634f;
 
-// shared-memory carve, from a 1024-aligned base
-constexpr int kOffQ = 0;                              // Q_A, Q_B
-constexpr int kOffKV = 2 * kTileBytes;                // ring of kSlots tiles
-constexpr int kOffBar = kOffKV + kSlots * kTileBytes;
-constexpr int kOffTslot = kOffBar + 320;              // TMEM address, after the barriers
-constexpr int kItemRing = 4;                          // items the loads warp publishes ahead
-constexpr int kOffItems = kOffBar + 512;              // [kItemRing][own item, lead item]
-constexpr int kSmemBytes = kOffItems + 1024 + 1024;   // + alignment slack
+// Shared-memory carve, from a 1024-aligned base.  Narrow trees, one Q tile a CTA, are bound by
+// the bytes in flight: the ring takes the place of the second.
+constexpr int kItemRing = 4;  // items the loads warp publishes ahead
+template <int MODE>
+struct PfCarve {
+  static constexpr int kSlots = MODE == kNarrow ? 6 : 4;  // K / V ring: K(t) V(t) K(t+1) V(t+1) ...
+  static constexpr int kOffQ = 0;                          // Q_A, Q_B
+  static constexpr int kOffKV = (MODE == kNarrow ? 1 : 2) * kTileBytes;  // the ring
+  static constexpr int kOffBar = kOffKV + kSlots * kTileBytes;
+  static constexpr int kOffTslot = kOffBar + 320;  // TMEM address, after the barriers
+  static constexpr int kOffItems = kOffBar + 512;  // [kItemRing][own item, lead item]
+  // (the carve of narrow trees leaves no room to align an unaligned base: checked)
+  static constexpr int kSlack = MODE == kNarrow ? 0 : 1024;
+  static constexpr int kSmemBytes = kOffItems + 1024 + kSlack;
+};
 
 struct PfParams {
   const int32_t* bt;
@@ -269,6 +276,14 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&v)[16
       "r"(v[8]), "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]),
       "r"(v[15])
       : "memory");
+}
+
+__device__ __forceinline__ void tmem_ld2(uint32_t taddr, uint32_t& a, uint32_t& b) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x2.b32 {%0,%1}, [%2];" : "=r"(a), "=r"(b) : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_st2(uint32_t taddr, uint32_t a, uint32_t b) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x2.b32 [%0], {%1,%2};" ::"r"(taddr), "r"(a), "r"(b)
+               : "memory");
 }
 
 __device__ __forceinline__ void tmem_wait_ld() {
@@ -683,6 +698,12 @@ __global__ void __launch_bounds__((pf_threads<MODE, SHARE>()), 1)
   // the combine after this grid still sees both.
   if constexpr (!PREFIX) griddep_wait();
   griddep_launch_dependents();
+  using Carve = PfCarve<MODE>;
+  constexpr int kSlots = Carve::kSlots;
+  if (Carve::kSlack == 0 && (reinterpret_cast<uintptr_t>(smem_raw) & 1023)) {
+    set_error(p.err, kErrTimeout);  // (nothing is computed)
+    return;
+  }
   unsigned char* smem = reinterpret_cast<unsigned char*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -690,13 +711,13 @@ __global__ void __launch_bounds__((pf_threads<MODE, SHARE>()), 1)
   const int blocks_per_tile = kKeys / p.bs;
 
   // ---- shared memory, barriers, TMEM --------------------------------------------------
-  unsigned char* sQ = smem + kOffQ;  // [A | B]
-  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + kOffBar);
-  uint32_t* tslot = reinterpret_cast<uint32_t*>(smem + kOffTslot);
+  unsigned char* sQ = smem + Carve::kOffQ;  // [A | B]
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + Carve::kOffBar);
+  uint32_t* tslot = reinterpret_cast<uint32_t*>(smem + Carve::kOffTslot);
   // barriers: Q full, ring full[kSlots], ring empty[kSlots], then per tile
   // A / B: S ready, P written, O += P V done, O read by the epilogue, then
   // (CTA pairs) this CTA's own half of a slot loaded[kSlots]
-  static_assert((3 * kSlots + 13 + 2 * kItemRing) * 8 <= kOffTslot - kOffBar,
+  static_assert((3 * kSlots + 13 + 2 * kItemRing) * 8 <= Carve::kOffTslot - Carve::kOffBar,
                 "barriers overlap the TMEM address slot");
   static_assert(kItemRing * 2 * sizeof(Item) <= 1024, "item ring overflows its carve");
   const uint32_t b_qfull = smem_addr(&bars[0]);
@@ -714,15 +735,14 @@ __global__ void __launch_bounds__((pf_threads<MODE, SHARE>()), 1)
   // by the MMA warp, whose thread must keep issuing products
   const uint32_t b_ifull0 = smem_addr(&bars[12 + 3 * kSlots]);
   const uint32_t b_iempty0 = smem_addr(&bars[12 + 3 * kSlots + kItemRing]);
-  // narrow trees: maximum and sum of every row in both tiles (where the second Q tile would be)
+  // narrow trees: the maximum and sum of every row in both tiles are in TMEM
   const uint32_t b_mlfull = smem_addr(&bars[12 + 3 * kSlots + 2 * kItemRing]);
-  float2* s_ml = reinterpret_cast<float2*>(sQ + kTileBytes);
-  Item* s_items = reinterpret_cast<Item*>(smem + kOffItems);
+  Item* s_items = reinterpret_cast<Item*>(smem + Carve::kOffItems);
   auto slot_full = [&](int i) { return b_full0 + 8u * i; };
   auto slot_empty = [&](int i) { return b_empty0 + 8u * i; };
   auto slot_half = [&](int i) { return b_half0 + 8u * i; };
   const uint32_t rank = SHARE ? cluster_rank() : 0u, peer = rank ^ 1u;
-  auto slot_ptr = [&](int i) { return smem + kOffKV + i * kTileBytes; };
+  auto slot_ptr = [&](int i) { return smem + Carve::kOffKV + i * kTileBytes; };
 
   if (tid == 0) {
     mbar_init(b_qfull, 1);
@@ -807,10 +827,16 @@ __global__ void __launch_bounds__((pf_threads<MODE, SHARE>()), 1)
   const WaitCtl w = make_wait_ctl(p.err, p.wait_ns, p.epoch);
   bool ok = true;
 
-  if (warp == kWarpTma) {
+  if (warp == kWarpTma || (TREE && warp == kWarpV)) {
     // ================= TMA producer: per item Q, then K(0) V(0) K(1) V(1) ... =================
+    // Trees: K by one warp and V by another.  A tile of 16-row blocks is 16 tensor copies, which
+    // a warp issues one by one: with one warp for both, and the blocks looked up for each, the
+    // products waited for it (16 trees of 96 rows on 8192 tokens 163 us, now 127; of 256 rows 188
+    // and 164).
+    const bool k_warp = warp == kWarpTma;
+    const int li0 = k_warp ? 0 : 1, li_step = TREE ? 2 : 1;
     const int box_bytes = p.bs * 128;
-    long long ld = 0;  // K / V loads issued so far (ring position)
+    long long ld = li0;  // this warp's next K / V load (ring position)
     int jq = 0;        // items whose Q was loaded
     long long ni = 0;  // items published
     Item it, lead;
@@ -821,7 +847,7 @@ __global__ void __launch_bounds__((pf_threads<MODE, SHARE>()), 1)
         it = lead = Item{};  // the MMA warp does not know the number of parts: an end mark
         it.end = true;
       }
-      {
+      if (k_warp) {
         const int r = (int)(ni % kItemRing);
         const long long use = ni / kItemRing;
         if (use > 0 && !mbar_wait_sleep(b_iempty0 + 8u * r, (uint32_t)((use - 1) & 1), w)) {
@@ -836,7 +862,21 @@ __global__ void __launch_bounds__((pf_threads<MODE, SHARE>()), 1)
       }
       if (!more) break;
       if (!lead.valid) continue;
-      if (it.valid) {
+      // windows and trees: the block that this lane copies of a tile (-1: zeros); looked up a
+      // tile ahead
+      [[maybe_unused]] auto block_of = [&](int t) -> int {
+        if (lane >= (SHARE ? 1 : 2) * blocks_per_tile || t >= lead.nB) return -1;
+        const int k = SHARE ? lane : lane % blocks_per_tile;
+        const int lb = lead.list.position(((lead.t0 + t) * blocks_per_tile + k) * p.bs) / p.bs;
+        if (lb >= lead.spanned) return -1;
+        const int blk = p.bt[(long long)lead.b * p.mb + lb];
+        if (blk >= 0 && blk < p.num_blocks) return blk;
+        set_error(p.err, kErrIndex);
+        return -1;
+      };
+      [[maybe_unused]] int ahead = -1, now = -1;
+      if constexpr (SPAN) ahead = block_of(0);
+      if (it.valid && k_warp) {
         // Q of this item once the previous item's S products have read the old one
         if (jq > 0 && !mbar_wait_sleep(b_qempty, (jq - 1) & 1, w)) { ok = false; break; }
         if (lane == 0) {
@@ -852,7 +892,7 @@ __global__ void __launch_bounds__((pf_threads<MODE, SHARE>()), 1)
         }
         ++jq;
       }
-      for (int li = 0; li < 2 * lead.nB && ok; ++li, ++ld) {
+      for (int li = li0; li < 2 * lead.nB && ok; li += li_step, ld += li_step) {
         const int slot = (int)(ld % kSlots);
         const long long use = ld / kSlots;
         if (use > 0 && !mbar_wait_sleep(slot_empty(slot), (uint32_t)((use - 1) & 1), w)) {
@@ -866,11 +906,21 @@ __global__ void __launch_bounds__((pf_threads<MODE, SHARE>()), 1)
         const uint32_t bar = SHARE || (TREE && is_v) ? slot_half(slot) : slot_full(slot);
         if (lane == 0) mbar_arrive_expect_tx(bar, SHARE ? kHalf : kTileBytes);
         __syncwarp();
+        if constexpr (SPAN) {
+          if (TREE || !is_v) now = ahead;
+          if (lane < (SHARE ? 1 : 2) * blocks_per_tile) {
+            const int h = SHARE ? (int)rank : lane / blocks_per_tile;
+            const int k = SHARE ? lane : lane % blocks_per_tile;
+            const long long coord = now < 0 ? p.blk_coord_limit : (long long)now * p.L + p.layer;
+            tma_4d(smem_addr(slot_ptr(slot) + h * kHalf + k * box_bytes), is_v ? &tv : &tk, h * 64,
+                   lead.g, 0, (int)coord, bar);
+          }
+          if (TREE || !is_v) ahead = block_of(t + 1);
+        } else {
         for (int k2 = lane; k2 < (SHARE ? 1 : 2) * blocks_per_tile; k2 += 32) {
           const int h = SHARE ? (int)rank : k2 / blocks_per_tile;
           const int k = SHARE ? k2 : k2 % blocks_per_tile;
-          long long lb = (long long)(PREFIX || SPAN ? lead.t0 + t : t) * blocks_per_tile + k;
-          if constexpr (SPAN) lb = lead.list.position((int)lb * p.bs) / p.bs;
+          const long long lb = (long long)(PREFIX ? lead.t0 + t : t) * blocks_per_tile + k;
           long long coord = p.blk_coord_limit;                       // out of range: zeros
           if (lb < lead.spanned) {
             const int blk = p.bt[(long long)lead.b * p.mb + lb];
@@ -883,6 +933,7 @@ __global__ void __launch_bounds__((pf_threads<MODE, SHARE>()), 1)
           tma_4d(smem_addr(slot_ptr(slot) + h * kHalf + k * box_bytes), is_v ? &tv : &tk, h * 64,
                  lead.g, 0, (int)coord, bar);
         }
+        }
         __syncwarp();
       }
     }
@@ -890,7 +941,7 @@ __global__ void __launch_bounds__((pf_threads<MODE, SHARE>()), 1)
     // warps gave up, nothing else waited for the last ones.  A slot holds at
     // most one load in flight (it is refilled only after its release), so the
     // last load of each slot and the last Q load are the ones to wait for.
-    for (long long idx = ld - kSlots; idx < ld; ++idx) {
+    for (long long idx = ld - kSlots; idx < ld; idx += li_step) {
       if (idx < 0) continue;
       const int slot = (int)(idx % kSlots);
       const uint32_t ph = (uint32_t)((idx / kSlots) & 1);
@@ -1195,7 +1246,9 @@ __global__ void __launch_bounds__((pf_threads<MODE, SHARE>()), 1)
       if constexpr (NARROW) {
         // The row's two states, one a tile, merged: both threads of a row read both O (their
         // lanes of TMEM are the same) and take half of the columns each.
-        s_ml[x * kRows + r] = make_float2(st.m_used, st.l);
+        tmem_st2(tS(x) + lane_base + COLS, __float_as_uint(st.m_used), __float_as_uint(st.l));
+        tmem_wait_st();
+        tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(b_mlfull);
         bool both = mbar_wait_sleep(b_pvdone0 + 8u * (1 - x), (uint32_t)((nt - 1) & 1), w);
@@ -1203,7 +1256,12 @@ __global__ void __launch_bounds__((pf_threads<MODE, SHARE>()), 1)
         ++ni;
         if (!__all_sync(0xffffffffu, both)) { ok = false; break; }
         tc_fence_after();
-        const float2 a = s_ml[r], b = s_ml[kRows + r];
+        uint32_t ab[4];
+        tmem_ld2(tS(0) + lane_base + COLS, ab[0], ab[1]);
+        tmem_ld2(tS(1) + lane_base + COLS, ab[2], ab[3]);
+        tmem_wait_ld();
+        const float2 a = make_float2(__uint_as_float(ab[0]), __uint_as_float(ab[1]));
+        const float2 b = make_float2(__uint_as_float(ab[2]), __uint_as_float(ab[3]));
         const float top = fmaxf(a.x, b.x);
         // a state at -inf saw nothing, or only NaN: its sum and O are 0, or NaN
         const float fa = a.x == -INFINITY ? 1.f : exp2f(a.x - top);
@@ -1435,13 +1493,15 @@ cudaError_t prefill_launch(const CUtensorMap& tq, const CUtensorMap& tk, const C
   if (e != cudaSuccess) return e;
   if (dev >= 0 && dev < 64 && configured[dev] == 0) {
     e = cudaFuncSetAttribute(prefill_kernel<MODE, false>,
-                             cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
+                             cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             PfCarve<MODE>::kSmemBytes);
     if (e != cudaSuccess) return e;
     configured[dev] = 1;
   }
   const long long grid = p.n_items < sm_count ? p.n_items : sm_count;
   return launch_kernel(prefill_kernel<MODE, false>, dim3((unsigned)grid),
-                       dim3(pf_threads<MODE, false>()), (size_t)kSmemBytes, s, true, tq, tk, tv, p);
+                       dim3(pf_threads<MODE, false>()), (size_t)PfCarve<MODE>::kSmemBytes, s, true,
+                       tq, tk, tv, p);
 }
 
 // CTA pairs: clusters of two CTAs, as many as can be resident at once (at
@@ -1453,7 +1513,7 @@ cudaError_t prefill_launch_pairs(const CUtensorMap& tq, const CUtensorMap& tk,
   auto kern = prefill_kernel<MODE, true>;
   cudaLaunchConfig_t cfg = {};
   cfg.blockDim = dim3(pf_threads<MODE, true>());
-  cfg.dynamicSmemBytes = (size_t)kSmemBytes;
+  cfg.dynamicSmemBytes = (size_t)PfCarve<MODE>::kSmemBytes;
   cfg.stream = s;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -1469,7 +1529,8 @@ cudaError_t prefill_launch_pairs(const CUtensorMap& tq, const CUtensorMap& tk,
   if (e != cudaSuccess) return e;
   if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
   if (max_pairs[dev] == 0) {
-    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             PfCarve<MODE>::kSmemBytes);
     if (e != cudaSuccess) return e;
     // resident clusters: a persistent grid larger than this would queue
     cfg.gridDim = dim3(2 * (unsigned)(sm_count / 2 > 0 ? sm_count / 2 : 1));
