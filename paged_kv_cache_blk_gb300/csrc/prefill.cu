@@ -84,21 +84,16 @@ constexpr int kTileBytes = 2 * kHalf;  // 32 KB
 constexpr uint32_t kTmemCols = 512;    // S_A, S_B, O_A, O_B
 constexpr float kLog2e = 1.4426950408889634f;
 
-// Shared-memory carve, from a 1024-aligned base.  Narrow trees, one Q tile a CTA, are bound by
-// the bytes in flight: the ring takes the place of the second.
-constexpr int kItemRing = 4;  // items the loads warp publishes ahead
-template <int MODE>
-struct PfCarve {
-  static constexpr int kSlots = MODE == kNarrow ? 6 : 4;  // K / V ring: K(t) V(t) K(t+1) V(t+1) ...
-  static constexpr int kOffQ = 0;                          // Q_A, Q_B
-  static constexpr int kOffKV = (MODE == kNarrow ? 1 : 2) * kTileBytes;  // the ring
-  static constexpr int kOffBar = kOffKV + kSlots * kTileBytes;
-  static constexpr int kOffTslot = kOffBar + 320;  // TMEM address, after the barriers
-  static constexpr int kOffItems = kOffBar + 512;  // [kItemRing][own item, lead item]
-  // (the carve of narrow trees leaves no room to align an unaligned base: checked)
-  static constexpr int kSlack = MODE == kNarrow ? 0 : 1024;
-  static constexpr int kSmemBytes = kOffItems + 1024 + kSlack;
-};
+constexpr int kSlots = 4;              // K / V ring: K(t) V(t) K(t+1) V(t+1)
+
+// shared-memory carve, from a 1024-aligned base
+constexpr int kOffQ = 0;                              // Q_A, Q_B
+constexpr int kOffKV = 2 * kTileBytes;                // ring of kSlots tiles
+constexpr int kOffBar = kOffKV + kSlots * kTileBytes;
+constexpr int kOffTslot = kOffBar + 384;              // TMEM address, after the barriers
+constexpr int kItemRing = 4;                          // items the loads warp publishes ahead
+constexpr int kOffItems = kOffBar + 512;              // [kItemRing][own item, lead item]
+constexpr int kSmemBytes = kOffItems + 1024 + 1024;   // + alignment slack
 
 struct PfParams {
   const int32_t* bt;
@@ -147,8 +142,6 @@ __device__ __forceinline__ uint64_t desc_sw128(uint32_t saddr, uint32_t lbo, uin
 constexpr uint32_t kIdescKK =
     (1u << 4) | (1u << 7) | (1u << 10) | ((128u >> 3) << 17) | ((128u >> 4) << 24);
 constexpr uint32_t kIdescKMN = kIdescKK | (1u << 16);  // B MN-major
-// the same with N 64
-constexpr uint32_t kIdescHalf = kIdescKK ^ ((128u >> 3) << 17) ^ ((64u >> 3) << 17);
 
 __device__ __forceinline__ void umma(uint32_t d_tmem, uint64_t a, uint64_t b, uint32_t idesc,
                                      uint32_t accumulate) {
@@ -341,10 +334,11 @@ struct WordMask {
 // updates the running state, rescales the O row when the maximum moved, and
 // writes the row's P as bf16 pairs back into TMEM, where the P V product reads
 // it as its A operand.
-template <int COLS, class Mask>
-__device__ __forceinline__ void softmax_tile(uint32_t tS, uint32_t tO, uint32_t lane_base, int t,
+// settled() is true once the products into O so far are done: asked only before O is rescaled.
+template <int COLS, class Mask, class Settled>
+__device__ __forceinline__ bool softmax_tile(uint32_t tS, uint32_t tO, uint32_t lane_base, int t,
                                              const Mask& mask, bool full_tile, float qs,
-                                             RowState& st) {
+                                             RowState& st, const Settled& settled) {
   // With a positive scale the maximum is taken on the raw scores and the scale
   // goes into the exponent's FMA; otherwise each score is scaled first.
   const bool pre = qs <= 0.f;
@@ -393,9 +387,9 @@ __device__ __forceinline__ void softmax_tile(uint32_t tS, uint32_t tO, uint32_t 
   //
   // Every tcgen05.ld / st below is a warp-wide instruction, so all control
   // flow around them is warp-uniform: per-row decisions only select data.
-  // The O rescale needs P(t-1) V(t-1) to have completed; it has, because
-  // S(t) was issued after it and its commit (the "S ready" barrier) covers
-  // every earlier product.
+  // The O rescale needs P(t-1) V(t-1) to have completed; it has where S(t) was
+  // issued after it, as its commit (the "S ready" barrier) covers every earlier
+  // product (narrow trees, which issue S(t) before it, wait: settled).
   float psum = 0.f, alpha = 1.f;
   {
     // One pass against the maximum in use.  Each chunk's maximum is checked
@@ -469,6 +463,7 @@ __device__ __forceinline__ void softmax_tile(uint32_t tS, uint32_t tO, uint32_t 
     st.m_used = mu;
   }
   if (t > 0 && __any_sync(0xffffffffu, alpha != 1.f)) {
+    if (!settled()) return false;
 #pragma unroll 1
     for (int c0 = 0; c0 < kD; c0 += 32) {
       uint32_t v[32];
@@ -481,6 +476,7 @@ __device__ __forceinline__ void softmax_tile(uint32_t tS, uint32_t tO, uint32_t 
   }
   tmem_wait_st();
   st.l = st.l * alpha + psum;
+  return true;
 }
 
 // One work item: a pair of query tiles of one (sequence, kv head).  All roles
@@ -698,12 +694,6 @@ __global__ void __launch_bounds__((pf_threads<MODE, SHARE>()), 1)
   // the combine after this grid still sees both.
   if constexpr (!PREFIX) griddep_wait();
   griddep_launch_dependents();
-  using Carve = PfCarve<MODE>;
-  constexpr int kSlots = Carve::kSlots;
-  if (Carve::kSlack == 0 && (reinterpret_cast<uintptr_t>(smem_raw) & 1023)) {
-    set_error(p.err, kErrTimeout);  // (nothing is computed)
-    return;
-  }
   unsigned char* smem = reinterpret_cast<unsigned char*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -711,13 +701,13 @@ __global__ void __launch_bounds__((pf_threads<MODE, SHARE>()), 1)
   const int blocks_per_tile = kKeys / p.bs;
 
   // ---- shared memory, barriers, TMEM --------------------------------------------------
-  unsigned char* sQ = smem + Carve::kOffQ;  // [A | B]
-  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + Carve::kOffBar);
-  uint32_t* tslot = reinterpret_cast<uint32_t*>(smem + Carve::kOffTslot);
+  unsigned char* sQ = smem + kOffQ;  // [A | B]
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + kOffBar);
+  uint32_t* tslot = reinterpret_cast<uint32_t*>(smem + kOffTslot);
   // barriers: Q full, ring full[kSlots], ring empty[kSlots], then per tile
   // A / B: S ready, P written, O += P V done, O read by the epilogue, then
   // (CTA pairs) this CTA's own half of a slot loaded[kSlots]
-  static_assert((3 * kSlots + 13 + 2 * kItemRing) * 8 <= Carve::kOffTslot - Carve::kOffBar,
+  static_assert((3 * kSlots + 17 + 2 * kItemRing) * 8 <= kOffTslot - kOffBar,
                 "barriers overlap the TMEM address slot");
   static_assert(kItemRing * 2 * sizeof(Item) <= 1024, "item ring overflows its carve");
   const uint32_t b_qfull = smem_addr(&bars[0]);
@@ -737,12 +727,21 @@ __global__ void __launch_bounds__((pf_threads<MODE, SHARE>()), 1)
   const uint32_t b_iempty0 = smem_addr(&bars[12 + 3 * kSlots + kItemRing]);
   // narrow trees: the maximum and sum of every row in both tiles are in TMEM
   const uint32_t b_mlfull = smem_addr(&bars[12 + 3 * kSlots + 2 * kItemRing]);
-  Item* s_items = reinterpret_cast<Item*>(smem + Carve::kOffItems);
+  // narrow trees, whose softmax may be a tile ahead of P V: "P written" and "O += P V done" of
+  // A / B, for tiles of even and of odd number
+  const uint32_t b_odd0 = smem_addr(&bars[13 + 3 * kSlots + 2 * kItemRing]);
+  [[maybe_unused]] auto p_full = [&](int x, long long tile) {
+    return (tile & 1 ? b_odd0 : b_pfull0) + 8u * x;
+  };
+  [[maybe_unused]] auto pv_done = [&](int x, long long tile) {
+    return (tile & 1 ? b_odd0 + 16u : b_pvdone0) + 8u * x;
+  };
+  Item* s_items = reinterpret_cast<Item*>(smem + kOffItems);
   auto slot_full = [&](int i) { return b_full0 + 8u * i; };
   auto slot_empty = [&](int i) { return b_empty0 + 8u * i; };
   auto slot_half = [&](int i) { return b_half0 + 8u * i; };
   const uint32_t rank = SHARE ? cluster_rank() : 0u, peer = rank ^ 1u;
-  auto slot_ptr = [&](int i) { return smem + Carve::kOffKV + i * kTileBytes; };
+  auto slot_ptr = [&](int i) { return smem + kOffKV + i * kTileBytes; };
 
   if (tid == 0) {
     mbar_init(b_qfull, 1);
@@ -759,6 +758,10 @@ __global__ void __launch_bounds__((pf_threads<MODE, SHARE>()), 1)
       mbar_init(b_ofree0 + 8u * x, NARROW ? 8 : 4);
     }
     mbar_init(b_mlfull, 8);
+    for (int x = 0; x < 2; ++x) {
+      mbar_init(b_odd0 + 8u * x, 4);
+      mbar_init(b_odd0 + 16u + 8u * x, 1);
+    }
     mbar_init(b_drain, 1);
     mbar_init(b_stall, 1);
     for (int r = 0; r < kItemRing; ++r) {
@@ -783,6 +786,8 @@ __global__ void __launch_bounds__((pf_threads<MODE, SHARE>()), 1)
   // TMEM columns: S_A [0,128), S_B [128,256), O_A [256,384), O_B [384,512)
   auto tS = [&](int x) { return tmem + 128u * x; };
   auto tO = [&](int x) { return tmem + 256u + 128u * x; };
+  // narrow trees: S of all keys in the columns of A and B by turns, a half of them a tile
+  [[maybe_unused]] auto tH = [&](int buf, int x) { return tmem + 128u * buf + 64u * x; };
   const long long n_items = p.n_items;
   const long long i_first = SHARE ? blockIdx.x >> 1 : blockIdx.x;
   const long long i_step = SHARE ? gridDim.x >> 1 : gridDim.x;
@@ -1054,22 +1059,22 @@ __global__ void __launch_bounds__((pf_threads<MODE, SHARE>()), 1)
       // (the start address is the descriptor's low field, in 16-byte units;
       // shared addresses stay below 256 KB, so the addition never carries).
       auto issue_s = [&](int x, long long k_idx) {
-        // (narrow trees: the same rows, and the half of the keys that the tile takes)
+        // (narrow trees: one Q, and x the turn of the columns)
         const uint64_t a0 = desc_sw128(q_addr + (NARROW ? 0 : x * kTileBytes), 16, 1024);
-        const uint64_t b0 = desc_sw128(smem_addr(slot_ptr(slot_of(k_idx))) + (NARROW ? x * COLS * 128 : 0),
-                                       16, 1024);
+        const uint64_t b0 = desc_sw128(smem_addr(slot_ptr(slot_of(k_idx))), 16, 1024);
         tc_fence_after();
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
           const uint64_t step = (uint64_t)(((k >> 2) * kHalf + (k & 3) * 32) >> 4);
-          umma(tS(x), a0 + step, b0 + step, NARROW ? kIdescHalf : kIdescKK, k > 0);
+          umma(tS(x), a0 + step, b0 + step, kIdescKK, k > 0);
         }
         umma_commit(b_sfull0 + 8u * x);
       };
-      auto issue_pv = [&](int x, long long v_idx, bool first) {
+      // (narrow trees: P and V of the half of the keys that tile x takes, of tile number `tile`)
+      auto issue_pv = [&](int x, long long v_idx, bool first, long long tile = 0) {
         const uint64_t b0 = desc_sw128(smem_addr(slot_ptr(slot_of(v_idx))) + (NARROW ? x * COLS * 128 : 0),
                                        kHalf, 1024);
-        const uint32_t p0 = tS(x), o0 = tO(x);
+        const uint32_t p0 = NARROW ? tH((int)(tile & 1), x) : tS(x), o0 = tO(x);
         tc_fence_after();
 #pragma unroll
         for (int k = 0; k < COLS / 16; ++k) {
@@ -1077,7 +1082,7 @@ __global__ void __launch_bounds__((pf_threads<MODE, SHARE>()), 1)
           umma_ts(o0, p0 + 8u * k, b0 + (uint64_t)((k * 2048) >> 4), kIdescKMN,
                   (!first || k > 0) ? 1u : 0u);
         }
-        umma_commit(b_pvdone0 + 8u * x);
+        umma_commit(NARROW ? pv_done(x, tile) : b_pvdone0 + 8u * x);
       };
       long long ni = 0;  // items read from the loads warp
       for (long long i = i_first; (TREE || i < n_items) && ok; i += i_step, ++ni) {
@@ -1097,6 +1102,39 @@ __global__ void __launch_bounds__((pf_threads<MODE, SHARE>()), 1)
         if (it.valid) {
           if (!mbar_wait_sleep(b_qfull, jq & 1, w) || !ready(base)) { ok = false; break; }
           ++jq;
+          if constexpr (NARROW) {
+            // S(0) | S(t+1) PV_A(t) PV_B(t) | ...: S of the next keys is there when the softmax
+            // of the last is done, and one product serves both tiles
+            issue_s((int)(nt[0] & 1), base);
+            if (nB == 1) umma_commit(b_qempty);
+            for (int t = 0; t < nB && ok; ++t) {
+              const long long ki = base + 2 * t, vi = ki + 1;
+              const int turn = (int)(nt[0] & 1);
+              release(ki);
+              // the first PV overwrites both O, and S(1) the columns through which the last
+              // item's tiles exchange their rows' states: its epilogue must be over
+              if (t == 0 && ne[0] > 0) {
+                ok = mbar_wait_sleep(b_ofree0, (ne[0] - 1) & 1, w) &&
+                     mbar_wait_sleep(b_ofree0 + 8u, (ne[0] - 1) & 1, w);
+                if (!ok) break;
+              }
+              if (t + 1 < nB) {
+                if (!ready(ki + 2)) { ok = false; break; }
+                issue_s(turn ^ 1, ki + 2);
+                if (t + 2 == nB) umma_commit(b_qempty);
+              }
+              if (!ready(vi)) { ok = false; break; }
+              for (int x = 0; x < 2 && ok; ++x) {
+                ok = mbar_wait_sleep(p_full(x, nt[0]), (uint32_t)((nt[0] >> 1) & 1), w);
+                if (ok) issue_pv(x, vi, t == 0, nt[0]);
+              }
+              if (!ok) break;
+              release(vi);
+              ++nt[0];
+            }
+            ++ne[0];
+            continue;
+          }
           if (nA > 0) issue_s(0, base);
           issue_s(1, base);
           // Q may be replaced once the last S product of the item completes: the
@@ -1202,7 +1240,9 @@ __global__ void __launch_bounds__((pf_threads<MODE, SHARE>()), 1)
       }
       RowState st{-INFINITY, 0.f};
       for (int t = 0; t < nX && ok; ++t, ++nt) {
-        const bool waited = mbar_wait_sleep(b_sfull, (uint32_t)(nt & 1), w);
+        const bool waited =
+            NARROW ? mbar_wait_sleep(b_sfull0 + 8u * (uint32_t)(nt & 1), (uint32_t)((nt >> 1) & 1), w)
+                   : mbar_wait_sleep(b_sfull, (uint32_t)(nt & 1), w);
         if (!__all_sync(0xffffffffu, waited)) { ok = false; break; }
         tc_fence_after();
         if constexpr (SPAN) {
@@ -1212,10 +1252,18 @@ __global__ void __launch_bounds__((pf_threads<MODE, SHARE>()), 1)
           WordMask<COLS> seen;
 #pragma unroll
           for (int c = 0; c < COLS / 32; ++c) seen.w[c] = full ? 0u : s_row.bits_from(x0 + 32 * c);
-          softmax_tile<COLS>(tS(x), tO(x), lane_base, t, seen, full, p.qscale, st);
+          const bool done = softmax_tile<COLS>(
+              NARROW ? tH((int)(nt & 1), x) : tS(x), tO(x), lane_base, t, seen, full, p.qscale, st, [&] {
+                if constexpr (!NARROW) return true;
+                const bool waited =
+                    mbar_wait_sleep(pv_done(x, nt - 1), (uint32_t)(((nt - 1) >> 1) & 1), w);
+                tc_fence_after();
+                return (bool)__all_sync(0xffffffffu, waited);
+              });
+          if (!done) { ok = false; break; }
           tc_fence_before();
           __syncwarp();
-          if (lane == 0) mbar_arrive(b_pfull);
+          if (lane == 0) mbar_arrive(NARROW ? p_full(x, nt) : b_pfull);
           continue;
         }
         int c_lo, c_hi;
@@ -1233,32 +1281,36 @@ __global__ void __launch_bounds__((pf_threads<MODE, SHARE>()), 1)
           full_tile = (t > 0 || it.off == 0) && t < t_mask_lo && rows_full;
         }
         softmax_tile<kKeys>(tS(x), tO(x), lane_base, t, IntervalMask{c_lo, c_hi}, full_tile,
-                            p.qscale, st);
+                            p.qscale, st, [] { return true; });
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(b_pfull);
       }
       if (!ok) break;
       // epilogue: O row / l -> bf16 -> out, then hand O back to the MMA warp
-      const bool waited = mbar_wait_sleep(b_pvdone, (uint32_t)((nt - 1) & 1), w);
+      const bool waited =
+          NARROW ? mbar_wait_sleep(pv_done(x, nt - 1), (uint32_t)(((nt - 1) >> 1) & 1), w)
+                 : mbar_wait_sleep(b_pvdone, (uint32_t)((nt - 1) & 1), w);
       if (!__all_sync(0xffffffffu, waited)) { ok = false; break; }
       tc_fence_after();
       if constexpr (NARROW) {
         // The row's two states, one a tile, merged: both threads of a row read both O (their
         // lanes of TMEM are the same) and take half of the columns each.
-        tmem_st2(tS(x) + lane_base + COLS, __float_as_uint(st.m_used), __float_as_uint(st.l));
+        // (in the columns of the last tile's P, which are free until the next item's S(1))
+        const int last = (int)((nt - 1) & 1);
+        tmem_st2(tH(last, x) + lane_base, __float_as_uint(st.m_used), __float_as_uint(st.l));
         tmem_wait_st();
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(b_mlfull);
-        bool both = mbar_wait_sleep(b_pvdone0 + 8u * (1 - x), (uint32_t)((nt - 1) & 1), w);
+        bool both = mbar_wait_sleep(pv_done(1 - x, nt - 1), (uint32_t)(((nt - 1) >> 1) & 1), w);
         both = both && mbar_wait_sleep(b_mlfull, (uint32_t)(ni & 1), w);
         ++ni;
         if (!__all_sync(0xffffffffu, both)) { ok = false; break; }
         tc_fence_after();
         uint32_t ab[4];
-        tmem_ld2(tS(0) + lane_base + COLS, ab[0], ab[1]);
-        tmem_ld2(tS(1) + lane_base + COLS, ab[2], ab[3]);
+        tmem_ld2(tH(last, 0) + lane_base, ab[0], ab[1]);
+        tmem_ld2(tH(last, 1) + lane_base, ab[2], ab[3]);
         tmem_wait_ld();
         const float2 a = make_float2(__uint_as_float(ab[0]), __uint_as_float(ab[1]));
         const float2 b = make_float2(__uint_as_float(ab[2]), __uint_as_float(ab[3]));
@@ -1494,13 +1546,13 @@ cudaError_t prefill_launch(const CUtensorMap& tq, const CUtensorMap& tk, const C
   if (dev >= 0 && dev < 64 && configured[dev] == 0) {
     e = cudaFuncSetAttribute(prefill_kernel<MODE, false>,
                              cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             PfCarve<MODE>::kSmemBytes);
+                             kSmemBytes);
     if (e != cudaSuccess) return e;
     configured[dev] = 1;
   }
   const long long grid = p.n_items < sm_count ? p.n_items : sm_count;
   return launch_kernel(prefill_kernel<MODE, false>, dim3((unsigned)grid),
-                       dim3(pf_threads<MODE, false>()), (size_t)PfCarve<MODE>::kSmemBytes, s, true,
+                       dim3(pf_threads<MODE, false>()), (size_t)kSmemBytes, s, true,
                        tq, tk, tv, p);
 }
 
@@ -1513,7 +1565,7 @@ cudaError_t prefill_launch_pairs(const CUtensorMap& tq, const CUtensorMap& tk,
   auto kern = prefill_kernel<MODE, true>;
   cudaLaunchConfig_t cfg = {};
   cfg.blockDim = dim3(pf_threads<MODE, true>());
-  cfg.dynamicSmemBytes = (size_t)PfCarve<MODE>::kSmemBytes;
+  cfg.dynamicSmemBytes = (size_t)kSmemBytes;
   cfg.stream = s;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -1530,7 +1582,7 @@ cudaError_t prefill_launch_pairs(const CUtensorMap& tq, const CUtensorMap& tk,
   if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
   if (max_pairs[dev] == 0) {
     e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             PfCarve<MODE>::kSmemBytes);
+                             kSmemBytes);
     if (e != cudaSuccess) return e;
     // resident clusters: a persistent grid larger than this would queue
     cfg.gridDim = dim3(2 * (unsigned)(sm_count / 2 > 0 ? sm_count / 2 : 1));
