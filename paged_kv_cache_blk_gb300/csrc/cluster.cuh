@@ -125,6 +125,15 @@ cudaError_t allow_shared(void (*kern)(KArgs...), size_t smem, std::atomic<int>& 
   return e;
 }
 
+// Allow its clusters more than 8 CTAs.
+template <typename... KArgs>
+cudaError_t allow_wide_clusters(void (*kern)(KArgs...), std::atomic<int>& done) {
+  if (done.load(std::memory_order_acquire)) return cudaSuccess;
+  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+  if (e == cudaSuccess) done.store(1, std::memory_order_release);
+  return e;
+}
+
 // The clusters of `cluster` CTAs that the device holds at once.  (Its parts
 // differ in SMs, and a cluster lies in one: 15 clusters of 8 CTAs fit on 152 SMs.)
 template <typename... KArgs>

@@ -61,6 +61,10 @@ constexpr int kMaxWarps = 8;    // of a CTA
 constexpr int kMaxCluster = 8;  // CTAs
 constexpr int kMaxStates = 48;  // warps of a cluster (with 64, 16 us where 48 take 13)
 constexpr int kStates = 64;     // room for them, two a lane in their merge
+// One sequence under a window of 4096, 8 kv heads, D 128, G 4, bf16, by warps x CTAs: 8 x 6 11.5
+// us, 4 x 12 10.0, 4 x 16 11.4; of 16384 24.7, 20.1, 21.1; of 65536 78.8, 62.2, 61.2.
+constexpr int kWideCluster = 16;
+constexpr int kLongWindow = 512;  // tiles
 constexpr unsigned kAll = 0xffffffffu;
 constexpr float kLog2e = 1.4426950408889634f;
 
@@ -896,10 +900,16 @@ template <int MODE, int D, int HEADS, bool WINDOW>
 cudaError_t launch_sparse_heads(const SparseParams& p, unsigned rows, int dev, int sms,
                                 cudaStream_t s) {
   using Lay = Layout<MODE, D, HEADS>;
-  static std::atomic<int> allowed[kDevices], known[kDevices][kMaxWarps + 1][kMaxCluster + 1];
+  // windows: clusters of up to 16 CTAs, and up to 64 states where these are long
+  constexpr int kMost = WINDOW ? kWideCluster : kMaxCluster;
+  static std::atomic<int> allowed[kDevices], known[kDevices][kMaxWarps + 1][kMost + 1];
   const auto kern = sparse_decode_kernel<MODE, D, HEADS, WINDOW>;
   cudaError_t e = allow_shared(kern, (size_t)Lay::kWarps * Lay::kWarp, allowed[dev]);
   if (e != cudaSuccess) return e;
+  if constexpr (WINDOW) {
+    static std::atomic<int> wide[kDevices];
+    if ((e = allow_wide_clusters(kern, wide[dev])) != cudaSuccess) return e;
+  }
   const long long tiles = ((long long)p.K * p.parts << p.piece_bits) / kTile;
   int warps = 1, ctas = 1;
   long long least = LLONG_MAX;
@@ -907,7 +917,8 @@ cudaError_t launch_sparse_heads(const SparseParams& p, unsigned rows, int dev, i
   for (const int W : {8, 6, 4, 3, 2, 1}) {
     // (beside the tensor cores' short tiles 6 warps and 1, and clusters below 4, gain nothing)
     if (W > Lay::kWarps || (!kF32 && (W == 6 || W == 1))) continue;
-    for (int S = 1; S <= kMaxCluster && W * S <= kMaxStates; ++S) {
+    const int most_states = WINDOW && tiles >= kLongWindow ? kStates : kMaxStates;
+    for (int S = 1; S <= kMost && W * S <= most_states; ++S) {
       if (S > 1 && (tiles < 2 * W * S || (!kF32 && W < 4))) break;
       int fit = 0;
       e = clusters_held(kern, W * 32, (size_t)W * Lay::kWarp, (unsigned)S, known[dev][W][S], &fit);
