@@ -142,6 +142,7 @@ __device__ __forceinline__ uint64_t desc_sw128(uint32_t saddr, uint32_t lbo, uin
 constexpr uint32_t kIdescKK =
     (1u << 4) | (1u << 7) | (1u << 10) | ((128u >> 3) << 17) | ((128u >> 4) << 24);
 constexpr uint32_t kIdescKMN = kIdescKK | (1u << 16);  // B MN-major
+constexpr uint32_t kIdescKMN64 = kIdescKMN ^ ((128u >> 3) << 17) ^ ((64u >> 3) << 17);  // with N 64
 
 __device__ __forceinline__ void umma(uint32_t d_tmem, uint64_t a, uint64_t b, uint32_t idesc,
                                      uint32_t accumulate) {
@@ -335,7 +336,7 @@ struct WordMask {
 // writes the row's P as bf16 pairs back into TMEM, where the P V product reads
 // it as its A operand.
 // settled() is true once the products into O so far are done: asked only before O is rescaled.
-template <int COLS, class Mask, class Settled>
+template <int COLS, int HD, class Mask, class Settled>
 __device__ __forceinline__ bool softmax_tile(uint32_t tS, uint32_t tO, uint32_t lane_base, int t,
                                              const Mask& mask, bool full_tile, float qs,
                                              RowState& st, const Settled& settled) {
@@ -465,7 +466,7 @@ __device__ __forceinline__ bool softmax_tile(uint32_t tS, uint32_t tO, uint32_t 
   if (t > 0 && __any_sync(0xffffffffu, alpha != 1.f)) {
     if (!settled()) return false;
 #pragma unroll 1
-    for (int c0 = 0; c0 < kD; c0 += 32) {
+    for (int c0 = 0; c0 < HD; c0 += 32) {
       uint32_t v[32];
       tmem_ld32(tO + lane_base + c0, v);
       tmem_wait_ld();
@@ -635,9 +636,9 @@ __device__ __forceinline__ SeenRows seen_rows(const PfParams& p, const Item& it)
   return SeenRows{it.list.first(it.off), it.list.behind(it.off + p.lens[it.b]),
                   it.list.first(it.off + p.plan.span.sink), it.list.behind(it.off + it.lo)};
 }
-// A warp clears the rows of 128 bytes of a loaded half tile that are not seen.
-__device__ __forceinline__ void clear_rows(uint32_t half, const SeenRows& s, int x0, int lane) {
-  for (int r = lane >> 3; r < kKeys; r += 4) {
+// A warp clears the rows of 128 bytes, n from place x0 on, that are not seen.
+__device__ __forceinline__ void clear_rows(uint32_t half, const SeenRows& s, int x0, int n, int lane) {
+  for (int r = lane >> 3; r < n; r += 4) {
     if (!s.has(x0 + r))
       asm volatile("st.shared.v4.u32 [%0], {%1,%1,%1,%1};" ::"r"(half + r * 128 + (lane & 7) * 16),
                    "r"(0)
@@ -678,13 +679,17 @@ __device__ __forceinline__ long long item_of(const PfParams& p, long long c, uin
 // Each CTA waits for every release of its slots before it leaves (so no
 // copy or arrive of the other CTA still targets it), and the two leave
 // together (a cluster barrier).
-template <int MODE, bool SHARE>
+template <int MODE, bool SHARE, int HD>
 __global__ void __launch_bounds__((pf_threads<MODE, SHARE>()), 1)
     prefill_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk,
                    const __grid_constant__ CUtensorMap tv, const PfParams p) {
   constexpr bool PREFIX = MODE == kPrefix, TREE = is_tree(MODE), NARROW = MODE == kNarrow,
                  SPAN = MODE == kWindow || TREE;
-  constexpr int COLS = NARROW ? kKeys / 2 : kKeys;  // keys of one S product
+  constexpr int COLS = NARROW ? kKeys / 2 : kKeys;  // keys of one softmax tile
+  // head_dim 64 (windows and trees): one 64-column half a tile; a pair's CTAs load 64 of its rows
+  // each instead of a half
+  constexpr int kD = HD, kHalves = kD / 64, kLoaded = kHalves * kHalf, kOwn = kLoaded / 2;
+  static_assert(HD == 128 || SPAN, "head_dim 64 is for windows and trees");
   static_assert(!((PREFIX || TREE) && SHARE), "the prefix pass and trees run on single CTAs");
   extern __shared__ __align__(1024) unsigned char smem_raw[];
   // Prefix pass of shared-prefix decode: it reads nothing the grid before it
@@ -699,6 +704,8 @@ __global__ void __launch_bounds__((pf_threads<MODE, SHARE>()), 1)
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int TQ = p.TQ, G = p.G;
   const int blocks_per_tile = kKeys / p.bs;
+  // the tensor copies of one load, a lane each, and the first of this CTA's blocks of a tile
+  const int own_copies = SHARE ? blocks_per_tile / (kD == 64 ? 2 : 1) : kHalves * blocks_per_tile;
 
   // ---- shared memory, barriers, TMEM --------------------------------------------------
   unsigned char* sQ = smem + kOffQ;  // [A | B]
@@ -776,6 +783,14 @@ __global__ void __launch_bounds__((pf_threads<MODE, SHARE>()), 1)
                  "r"(kTmemCols)
                  : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  if constexpr (SPAN) {
+    // rows of the Q tiles that no copy fills (groups that do not divide 128)
+    for (int e = tid; e < 4 * (kRows - TQ * G) * 8; e += blockDim.x) {
+      const int h = e & 3, r = TQ * G + (e >> 5), c = (e >> 2) & 7;
+      *reinterpret_cast<uint4*>(sQ + h * kHalf + r * 128 + c * 16) = make_uint4(0u, 0u, 0u, 0u);
+    }
+    if (TQ * G < kRows) asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
   }
   tc_fence_before();
   __syncthreads();
@@ -867,11 +882,14 @@ __global__ void __launch_bounds__((pf_threads<MODE, SHARE>()), 1)
       }
       if (!more) break;
       if (!lead.valid) continue;
-      // windows and trees: the block that this lane copies of a tile (-1: zeros); looked up a
-      // tile ahead
+      // windows and trees: the block that this lane copies of a tile, and its number (-1: zeros)
+      // looked up a tile ahead
+      [[maybe_unused]] auto own_block = [&] {
+        return SHARE ? lane + (kD == 64 ? (int)rank * own_copies : 0) : lane % blocks_per_tile;
+      };
       [[maybe_unused]] auto block_of = [&](int t) -> int {
-        if (lane >= (SHARE ? 1 : 2) * blocks_per_tile || t >= lead.nB) return -1;
-        const int k = SHARE ? lane : lane % blocks_per_tile;
+        if (lane >= own_copies || t >= lead.nB) return -1;
+        const int k = own_block();
         const int lb = lead.list.position(((lead.t0 + t) * blocks_per_tile + k) * p.bs) / p.bs;
         if (lb >= lead.spanned) return -1;
         const int blk = p.bt[(long long)lead.b * p.mb + lb];
@@ -887,10 +905,10 @@ __global__ void __launch_bounds__((pf_threads<MODE, SHARE>()), 1)
         if (lane == 0) {
           // (narrow trees: one tile, in the place of A)
           const int x_end = NARROW ? 1 : 2, x_begin = NARROW || it.nA > 0 ? 0 : 1;
-          mbar_arrive_expect_tx(b_qfull, (x_end - x_begin) * kTileBytes);
+          mbar_arrive_expect_tx(b_qfull, (x_end - x_begin) * (SPAN ? kHalves * TQ * G * 128 : kTileBytes));
           for (int x = x_begin; x < x_end; ++x) {
             const int z = (int)(it.q0 + (x == 0 ? it.qtA : it.qtB) * TQ);
-            for (int h = 0; h < 2; ++h)
+            for (int h = 0; h < kHalves; ++h)
               tma_3d(smem_addr(sQ + x * kTileBytes + h * kHalf), &tq, h * 64, it.g * G, z,
                      b_qfull);
           }
@@ -909,13 +927,13 @@ __global__ void __launch_bounds__((pf_threads<MODE, SHARE>()), 1)
         // its own "half loaded" barrier (the other half comes from the peer)
         // (trees: V tiles are looked over by warp 10 before they are multiplied)
         const uint32_t bar = SHARE || (TREE && is_v) ? slot_half(slot) : slot_full(slot);
-        if (lane == 0) mbar_arrive_expect_tx(bar, SHARE ? kHalf : kTileBytes);
+        if (lane == 0) mbar_arrive_expect_tx(bar, SHARE ? kOwn : kLoaded);
         __syncwarp();
         if constexpr (SPAN) {
           if (TREE || !is_v) now = ahead;
-          if (lane < (SHARE ? 1 : 2) * blocks_per_tile) {
-            const int h = SHARE ? (int)rank : lane / blocks_per_tile;
-            const int k = SHARE ? lane : lane % blocks_per_tile;
+          if (lane < own_copies) {
+            const int h = kHalves == 1 ? 0 : SHARE ? (int)rank : lane / blocks_per_tile;
+            const int k = own_block();
             const long long coord = now < 0 ? p.blk_coord_limit : (long long)now * p.L + p.layer;
             tma_4d(smem_addr(slot_ptr(slot) + h * kHalf + k * box_bytes), is_v ? &tv : &tk, h * 64,
                    lead.g, 0, (int)coord, bar);
@@ -969,7 +987,7 @@ __global__ void __launch_bounds__((pf_threads<MODE, SHARE>()), 1)
     // other CTA's half
     // (windows: the whole warp, which clears V rows that no query sees before they go)
     if (lane == 0 || SPAN) {
-      const uint32_t half_off = rank * kHalf;
+      const uint32_t half_off = rank * kOwn;
       long long ld = 0;
       for (long long i = i_first; i < n_items && ok; i += i_step) {
         const Item lead = lead_item(i, own_item(i));
@@ -987,12 +1005,13 @@ __global__ void __launch_bounds__((pf_threads<MODE, SHARE>()), 1)
           if constexpr (SPAN) {
             const int x0 = (li >> 1) * kKeys;
             if ((li & 1) && !seen.whole(x0))
-              clear_rows(smem_addr(slot_ptr(slot)) + half_off, seen, x0, lane);
+              clear_rows(smem_addr(slot_ptr(slot)) + half_off, seen,
+                         x0 + (kD == 64 ? (int)rank * 64 : 0), kOwn / 128, lane);
             if (lane != 0) continue;
           }
-          mbar_arrive_expect_tx(slot_full(slot), kHalf);
+          mbar_arrive_expect_tx(slot_full(slot), kOwn);
           const uint32_t src = smem_addr(slot_ptr(slot)) + half_off;
-          bulk_s2s(peer_addr(src, peer), src, kHalf, peer_addr(slot_full(slot), peer));
+          bulk_s2s(peer_addr(src, peer), src, kOwn, peer_addr(slot_full(slot), peer));
         }
       }
     }
@@ -1012,8 +1031,8 @@ __global__ void __launch_bounds__((pf_threads<MODE, SHARE>()), 1)
         }
         const int x0 = (it.t0 + t) * kKeys;
         if (!seen.whole(x0)) {
-          clear_rows(smem_addr(slot_ptr(slot)), seen, x0, lane);
-          clear_rows(smem_addr(slot_ptr(slot)) + kHalf, seen, x0, lane);
+          for (int h = 0; h < kHalves; ++h)
+            clear_rows(smem_addr(slot_ptr(slot)) + h * kHalf, seen, x0, kKeys, lane);
         }
         if (lane == 0) mbar_arrive(slot_full(slot));
       }
@@ -1064,7 +1083,7 @@ __global__ void __launch_bounds__((pf_threads<MODE, SHARE>()), 1)
         const uint64_t b0 = desc_sw128(smem_addr(slot_ptr(slot_of(k_idx))), 16, 1024);
         tc_fence_after();
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
+        for (int k = 0; k < kD / 16; ++k) {
           const uint64_t step = (uint64_t)(((k >> 2) * kHalf + (k & 3) * 32) >> 4);
           umma(tS(x), a0 + step, b0 + step, kIdescKK, k > 0);
         }
@@ -1079,7 +1098,7 @@ __global__ void __launch_bounds__((pf_threads<MODE, SHARE>()), 1)
 #pragma unroll
         for (int k = 0; k < COLS / 16; ++k) {
           // A = P from TMEM (S columns of tile x), B = V MN-major
-          umma_ts(o0, p0 + 8u * k, b0 + (uint64_t)((k * 2048) >> 4), kIdescKMN,
+          umma_ts(o0, p0 + 8u * k, b0 + (uint64_t)((k * 2048) >> 4), kD == 64 ? kIdescKMN64 : kIdescKMN,
                   (!first || k > 0) ? 1u : 0u);
         }
         umma_commit(NARROW ? pv_done(x, tile) : b_pvdone0 + 8u * x);
@@ -1192,7 +1211,8 @@ __global__ void __launch_bounds__((pf_threads<MODE, SHARE>()), 1)
     // ================= softmax: warpgroup x = 0 (tile A) or 1 (tile B), one row per thread ======
     const int x = warp >> 2;
     const int r = tid & 127;                 // MMA row = TMEM lane
-    const int qtok = r / G, hh = r - qtok * G;
+    // (a row behind the tile's tokens, where G does not divide 128, is of no token)
+    const int qtok = SPAN && r >= TQ * G ? 1 << 29 : r / G, hh = r % G;
     const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t b_sfull = b_sfull0 + 8u * x, b_pfull = b_pfull0 + 8u * x;
     const uint32_t b_pvdone = b_pvdone0 + 8u * x, b_ofree = b_ofree0 + 8u * x;
@@ -1252,7 +1272,7 @@ __global__ void __launch_bounds__((pf_threads<MODE, SHARE>()), 1)
           WordMask<COLS> seen;
 #pragma unroll
           for (int c = 0; c < COLS / 32; ++c) seen.w[c] = full ? 0u : s_row.bits_from(x0 + 32 * c);
-          const bool done = softmax_tile<COLS>(
+          const bool done = softmax_tile<COLS, kD>(
               NARROW ? tH((int)(nt & 1), x) : tS(x), tO(x), lane_base, t, seen, full, p.qscale, st, [&] {
                 if constexpr (!NARROW) return true;
                 const bool waited =
@@ -1280,7 +1300,7 @@ __global__ void __launch_bounds__((pf_threads<MODE, SHARE>()), 1)
           c_hi = row_ok ? (int)min((long long)kKeys - 1, pos + it.off - tp0) : -1;
           full_tile = (t > 0 || it.off == 0) && t < t_mask_lo && rows_full;
         }
-        softmax_tile<kKeys>(tS(x), tO(x), lane_base, t, IntervalMask{c_lo, c_hi}, full_tile,
+        softmax_tile<kKeys, kD>(tS(x), tO(x), lane_base, t, IntervalMask{c_lo, c_hi}, full_tile,
                             p.qscale, st, [] { return true; });
         tc_fence_before();
         __syncwarp();
@@ -1321,7 +1341,7 @@ __global__ void __launch_bounds__((pf_threads<MODE, SHARE>()), 1)
         const float sum = fa * a.y + fb * b.y;
         const bool part = it.slot >= 0;
         const float inv = part ? 1.f : sum == 0.f ? 0.f : 1.f / sum;
-        float* srow = p.part + ((long long)it.slot * kRows + r) * (kD + 4);
+        float* srow = p.part + ((long long)it.slot * p.plan.unit_rows + r) * (kD + 4);
         __nv_bfloat16* orow = static_cast<__nv_bfloat16*>(p.out) +
                               ((it.q0 + qi) * p.hq + (long long)it.g * G + hh) * kD;
         if (part && row_ok && x == 0) *reinterpret_cast<float2*>(srow) = make_float2(top, sum);
@@ -1386,7 +1406,7 @@ __global__ void __launch_bounds__((pf_threads<MODE, SHARE>()), 1)
       if constexpr (TREE) {
         if (it.slot >= 0) {
           // a part of a unit: the row's state, merged by the kernel that follows
-          float* srow = p.part + ((long long)it.slot * (2 * kRows) + (x == 0 ? kRows : 0) + r) *
+          float* srow = p.part + ((long long)it.slot * p.plan.unit_rows + (x == 0 ? TQ * G : 0) + r) *
                                      (kD + 4);
           if (row_ok) *reinterpret_cast<float2*>(srow) = make_float2(st.m_used, st.l);
 #pragma unroll 1
@@ -1470,6 +1490,14 @@ __global__ void __launch_bounds__((pf_threads<MODE, SHARE>()), 1)
 
 }  // namespace
 
+// Windows and trees: bf16, head_dim 64 or 128, blocks of 8 to 128 rows (a pair's CTAs with
+// head_dim 64: to 64), up to 16 heads a group.
+bool span_supported(const PoolView& pv, int num_q_heads, bool pairs) {
+  return pv.elem_size == 2 && (pv.head_dim == 64 || pv.head_dim == 128) && pv.block_size >= 8 &&
+         pv.block_size <= (pairs && pv.head_dim == 64 ? kKeys / 2 : kKeys) &&
+         num_q_heads / pv.num_kv_heads <= 16;
+}
+
 int prefill_supported(const PoolView& pv, int num_q_heads) {
   if (pv.elem_size != 2 || pv.head_dim != kD) return 1;
   if (pv.block_size < 8 || pv.block_size > kKeys || kKeys % pv.block_size) return 1;
@@ -1489,10 +1517,10 @@ cudaError_t prefill_setup(const PoolView& pv, int layer, const void* q, int num_
                           const int32_t* offs, int batch, long long total_q, int* err,
                           CUtensorMap* tq, CUtensorMap* tk, CUtensorMap* tv, PfParams* pp) {
   const int G = num_q_heads / pv.num_kv_heads;
-  const int TQ = kRows / G;
+  const int TQ = kRows / G, D = pv.head_dim;
   {
-    cuuint64_t dims[3] = {(cuuint64_t)kD, (cuuint64_t)num_q_heads, (cuuint64_t)total_q};
-    cuuint64_t strides[2] = {(cuuint64_t)kD * 2, (cuuint64_t)num_q_heads * kD * 2};
+    cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)num_q_heads, (cuuint64_t)total_q};
+    cuuint64_t strides[2] = {(cuuint64_t)D * 2, (cuuint64_t)num_q_heads * D * 2};
     cuuint32_t box[3] = {64, (cuuint32_t)G, (cuuint32_t)TQ};
     if (!encode_tiled(tq, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, q, dims, strides, box,
                       CU_TENSOR_MAP_SWIZZLE_128B))
@@ -1500,9 +1528,9 @@ cudaError_t prefill_setup(const PoolView& pv, int layer, const void* q, int num_
   }
   const long long nl = pv.num_blocks * pv.num_layers;
   {
-    cuuint64_t dims[4] = {(cuuint64_t)kD, (cuuint64_t)pv.num_kv_heads, (cuuint64_t)pv.block_size,
+    cuuint64_t dims[4] = {(cuuint64_t)D, (cuuint64_t)pv.num_kv_heads, (cuuint64_t)pv.block_size,
                           (cuuint64_t)nl};
-    cuuint64_t strides[3] = {(cuuint64_t)kD * 2, (cuuint64_t)pv.row_bytes,
+    cuuint64_t strides[3] = {(cuuint64_t)D * 2, (cuuint64_t)pv.row_bytes,
                              (cuuint64_t)pv.row_bytes * pv.block_size};
     cuuint32_t box[4] = {64, 1, (cuuint32_t)pv.block_size, 1};
     if (!encode_tiled(tk, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, pv.k, dims, strides, box,
@@ -1536,7 +1564,7 @@ cudaError_t prefill_setup(const PoolView& pv, int layer, const void* q, int num_
   return cudaSuccess;
 }
 
-template <int MODE>
+template <int MODE, int HD = kD>
 cudaError_t prefill_launch(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
                            const PfParams& p, int sm_count, cudaStream_t s) {
   static int configured[64] = {0};
@@ -1544,25 +1572,25 @@ cudaError_t prefill_launch(const CUtensorMap& tq, const CUtensorMap& tk, const C
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (dev >= 0 && dev < 64 && configured[dev] == 0) {
-    e = cudaFuncSetAttribute(prefill_kernel<MODE, false>,
+    e = cudaFuncSetAttribute(prefill_kernel<MODE, false, HD>,
                              cudaFuncAttributeMaxDynamicSharedMemorySize,
                              kSmemBytes);
     if (e != cudaSuccess) return e;
     configured[dev] = 1;
   }
   const long long grid = p.n_items < sm_count ? p.n_items : sm_count;
-  return launch_kernel(prefill_kernel<MODE, false>, dim3((unsigned)grid),
+  return launch_kernel(prefill_kernel<MODE, false, HD>, dim3((unsigned)grid),
                        dim3(pf_threads<MODE, false>()), (size_t)kSmemBytes, s, true,
                        tq, tk, tv, p);
 }
 
 // CTA pairs: clusters of two CTAs, as many as can be resident at once (at
 // most one per two SMs), as a programmatic dependent of the work before.
-template <int MODE>
+template <int MODE, int HD = kD>
 cudaError_t prefill_launch_pairs(const CUtensorMap& tq, const CUtensorMap& tk,
                                  const CUtensorMap& tv, const PfParams& p, int sm_count,
                                  cudaStream_t s) {
-  auto kern = prefill_kernel<MODE, true>;
+  auto kern = prefill_kernel<MODE, true, HD>;
   cudaLaunchConfig_t cfg = {};
   cfg.blockDim = dim3(pf_threads<MODE, true>());
   cfg.dynamicSmemBytes = (size_t)kSmemBytes;
@@ -1622,8 +1650,9 @@ cudaError_t launch_prefill(const PoolView& pv, int layer, const void* q, int num
   p.plan.span.window = window;
   p.plan.span.sink = sink;
   p.plan.span.gran = pv.block_size;
-  return window > 0 ? prefill_launch_pairs<kWindow>(tq, tk, tv, p, sm_count, s)
-                    : prefill_launch_pairs<kCausal>(tq, tk, tv, p, sm_count, s);
+  if (window == 0) return prefill_launch_pairs<kCausal>(tq, tk, tv, p, sm_count, s);
+  return pv.head_dim == 64 ? prefill_launch_pairs<kWindow, 64>(tq, tk, tv, p, sm_count, s)
+                           : prefill_launch_pairs<kWindow>(tq, tk, tv, p, sm_count, s);
 }
 
 cudaError_t launch_prefill_tree(const PoolView& pv, int layer, const void* q, int num_q_heads,
@@ -1633,7 +1662,7 @@ cudaError_t launch_prefill_tree(const PoolView& pv, int layer, const void* q, in
   CUtensorMap tq, tk, tv;
   PfParams p;
   const SpanParams& sp = plan.span;
-  const bool narrow = plan.unit_rows == kRows;
+  const bool narrow = plan.unit_rows <= kRows;
   const cudaError_t e = prefill_setup(pv, layer, q, num_q_heads, scale, bt, sp.mb, sp.lens, sp.offs,
                                       sp.batch, sp.total_q, err, &tq, &tk, &tv, &p);
   if (e != cudaSuccess) return e;
@@ -1644,6 +1673,9 @@ cudaError_t launch_prefill_tree(const PoolView& pv, int layer, const void* q, in
   p.words = words;
   p.part = part;
   p.n_items = sm_count;  // the grid: the line of tiles is split over it
+  if (pv.head_dim == 64)
+    return narrow ? prefill_launch<kNarrow, 64>(tq, tk, tv, p, sm_count, s)
+                  : prefill_launch<kTree, 64>(tq, tk, tv, p, sm_count, s);
   return narrow ? prefill_launch<kNarrow>(tq, tk, tv, p, sm_count, s)
                 : prefill_launch<kTree>(tq, tk, tv, p, sm_count, s);
 }

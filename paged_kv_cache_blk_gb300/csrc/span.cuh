@@ -299,8 +299,10 @@ __device__ __forceinline__ PlanShare plan_share(const PlanParams& p, int cta, in
 cudaError_t launch_validate_spans(const SpanParams& p, const int32_t* bt, long long num_blocks,
                                   int* err, cudaStream_t s);
 
-// Host side (prefill.cu, where prefill_supported): the tree decode on tcgen05, units of 256
-// rows, or of 128 where none has more, key tiles of 128, split over a grid of sm_count CTAs.
+// Host side (prefill.cu): whether the tcgen05 kernels take a windowed prefill (pairs) or a tree.
+bool span_supported(const PoolView& pv, int num_q_heads, bool pairs);
+// The tree decode on them: units of two tiles of 128 / G tokens, or of one where no sequence has
+// more; key tiles of 128; split over a grid of sm_count CTAs.
 cudaError_t launch_prefill_tree(const PoolView& pv, int layer, const void* q, int num_q_heads,
                                 float scale, const int32_t* bt, const PlanParams& plan,
                                 const int32_t* q_pos, const unsigned long long* mask, int words,

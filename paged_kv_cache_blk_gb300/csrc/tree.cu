@@ -133,9 +133,10 @@ struct TreePath {
 TreePath tree_path(const PoolView& v, int G, int max_q_len, int sms) {
   TreePath t;
   const long long rows = (long long)max_q_len * G;
-  t.tcgen05 = rows > 32 && prefill_supported(v, G * v.num_kv_heads) == 0;
+  t.tcgen05 = rows > 32 && span_supported(v, G * v.num_kv_heads, false);
   if (t.tcgen05) {
-    t.unit_rows = rows <= 128 ? 128 : 256;
+    const int tile = 128 / G * G;  // rows of whole tokens
+    t.unit_rows = rows <= tile ? tile : 2 * tile;
     t.grid = sms;
     t.bytes = (size_t)2 * t.grid * t.unit_rows * (v.head_dim + 4) * 4;
     return t;
@@ -156,9 +157,25 @@ cudaError_t launch_rows(const PoolView& v, const RowsParams& p, bool tree, long 
   return launch_rows_f32(p, v.head_dim, tree, grid, dev, s);
 }
 
-// Which kernel a windowed prefill takes, where both could.
+// Whether a windowed prefill takes the tcgen05 kernel, where both could.  It works on whole
+// windows of 4 tiles of 128 rows a CTA pair; the mma.sync kernel shares a unit's keys out over a
+// cluster where units are few.  Estimated from a tile's time in us (128 keys x 2 tiles a CTA; 64
+// keys x 64 rows a CTA, beside the others of its SM) and what an item costs besides: 30 tokens on
+// 4096 under a window of 4096, 32 / 8 heads, D 128: tcgen05 66 us, mma.sync 35; 100 tokens 78
+// and 58; 512 tokens 79 and 200; under a window of 500, 100 tokens 20 and 18.
 bool prefill_on_tcgen05(const PoolView& v, const RowsParams& p, int sms) {
-  return prefill_supported(v, p.hq) == 0 && p.plan.unit_rows > 32;
+  if (!span_supported(v, p.hq, true) || p.plan.unit_rows <= 32) return false;
+  const bool d64 = v.head_dim == 64;
+  const double heads = (double)p.plan.span.batch * v.num_kv_heads;
+  const int tokens = 128 / p.plan.G, tiles_q = (p.plan.span.max_q_len + tokens - 1) / tokens;
+  const double items = (tiles_q + 3) / 4 * heads;
+  const double pairs_us = std::ceil(items / (sms / 2)) * (p.keys_most / 128. * (d64 ? 2.1 : 2.5) + 8);
+  const double units = p.units_max * heads, held = sms * rows_ctas_bf16(v.head_dim, 64);
+  int ctas = kRowsMaxCluster;
+  while (ctas > 1 && units * ctas > held) ctas >>= 1;
+  const double rows_us =
+      std::ceil(units * ctas / held) * (p.keys_most / 64. / ctas * (d64 ? 2.0 : 3.3) + 7);
+  return pairs_us <= rows_us;
 }
 
 // The arguments that the two calls share.

@@ -244,6 +244,11 @@ PREFILLS = [
     ("bf16", 2, 2, 128, 32, [333, 64], [100, 64], 1, 0), ("bf16", 1, 8, 128, 16, [400, 17], [33, 17], 200, 150),
     ("bf16", 1, 16, 128, 8, [150, 90], [150, 8], 17, 3), ("bf16", 1, 4, 128, 128, [900, 1], [300, 1], 300, 2),
     ("bf16", 2, 4, 128, 64, [1000, 520, 33, 95], [1000, 520, 33, 95], 257, 40),
+    ("bf16", 2, 4, 64, 16, [700, 260, 33], [700, 40, 33], 129, 5), ("bf16", 1, 8, 64, 64, [900, 70], [300, 70], 300, 2),
+    ("bf16", 1, 1, 64, 8, [500], [400], 90, 17), ("bf16", 1, 16, 64, 32, [300], [150], 1, 0),
+    ("bf16", 1, 2, 64, 128, [400], [200], 130, 4), ("bf16", 2, 3, 128, 16, [700, 129], [600, 129], 200, 9),
+    ("bf16", 1, 5, 128, 64, [500], [300], 64, 1), ("bf16", 1, 7, 64, 16, [400, 90], [400, 33], 150, 2),
+    ("bf16", 1, 11, 128, 8, [250], [100], 33, 1), ("bf16", 1, 13, 64, 32, [200], [200], 70, 0),
     ("bf16", 1, 4, 128, 16, [1500], [700], 5000, 9),
     ("bf16", 2, 3, 128, 16, [150, 20], [150, 3], 50, 4), ("bf16", 1, 5, 64, 16, [200, 70], [130, 70], 64, 1),
     ("bf16", 2, 1, 64, 4, [90], [90], 20, 2), ("bf16", 1, 2, 128, 256, [600], [300], 280, 10),
@@ -353,6 +358,11 @@ TREES = [
     ("bf16", 1, 1, 128, 8, [1500, 140], [130, 129], 0, 0), ("bf16", 1, 8, 128, 64, [700, 65], [33, 20], 0, 0),
     ("bf16", 1, 16, 128, 128, [600], [40], 0, 0), ("bf16", 2, 2, 128, 32, [2000, 1000], [100, 64], 130, 5),
     ("bf16", 2, 4, 128, 16, [900, 300], [64, 20], 300, 4), ("bf16", 1, 16, 128, 16, [400, 30], [16, 16], 40, 0),
+    ("bf16", 2, 4, 64, 16, [900, 64, 400], [64, 64, 11], 0, 0), ("bf16", 1, 1, 64, 8, [1500, 140], [130, 129], 200, 3),
+    ("bf16", 1, 16, 64, 128, [600, 90], [40, 7], 0, 0), ("bf16", 2, 8, 64, 32, [500], [16], 100, 4),
+    ("bf16", 1, 3, 128, 16, [900, 300], [84, 85], 0, 0), ("bf16", 2, 5, 128, 64, [400, 50], [26, 50], 77, 1),
+    ("bf16", 1, 7, 64, 16, [700], [100], 0, 0), ("bf16", 1, 13, 128, 8, [300], [20], 0, 0),
+    ("bf16", 1, 9, 64, 16, [300, 20], [14, 15], 0, 0),
     ("bf16", 2, 3, 128, 16, [200, 50], [7, 30], 0, 0), ("bf16", 3, 1, 64, 8, [120], [5], 30, 3),
     ("bf16", 1, 16, 64, 1, [90], [70], 0, 0), ("bf16", 2, 5, 64, 512, [1100, 600], [13, 4], 600, 20),
     ("f32", 2, 5, 64, 16, [300, 3], [17, 3], 0, 0), ("f32", 1, 4, 128, 16, [150, 100], [4, 1], 64, 4),
@@ -396,11 +406,13 @@ def test_tree_odd_masks(dev, dtype, D, n):
                   trees=[wide, np.zeros((0, 192), bool), np.ones((1, 192), bool)], seed=9)
 
 
-@pytest.mark.parametrize("dtype,D,n", [("bf16", 128, 8), ("bf16", 128, 40), ("bf16", 64, 8), ("f32", 64, 3),
+@pytest.mark.parametrize("dtype,D,n", [("bf16", 128, 8), ("bf16", 128, 40), ("bf16", 64, 8), ("bf16", 64, 40), ("f32", 64, 3),
                                        ("i8", 128, 16)])
 def test_tree_split(dev, dtype, D, n):
     """Units split over many CTAs, units finished by one, and sequences of no tokens between."""
     _run_tree(dev, dtype, 1, 4, D, 16, [20000], [n], 0, 0, seed=10)
+    if dtype == "bf16":
+        _run_tree(dev, dtype, 1, 3, D, 32, [9000, 700, 50], [n, n, n], 0, 0, seed=12)
     lens = [int(x) for x in np.random.default_rng(3).integers(40, 900, 30)]
     new = [n if i % 3 else 0 for i in range(30)]
     _run_tree(dev, dtype, 2, 2, D, 16, lens, new, 0, 0, seed=11)
