@@ -521,8 +521,8 @@ PKV_API pkv_status pkv_prefill_attention(const pkv_pool* pool, int32_t layer, co
  * tokens of the sequence, which stay visible.  window >= 1, sink >= 0
  * (PKV_ERR_INVALID_ARG).  Table entries whose block holds no key that a query of
  * the call sees are not read: their blocks may have been freed and the
- * entries may hold anything.  Rows that no query of the sequence sees are not
- * read, and whatever they hold does not reach a result.
+ * entries may hold anything.  What a key or value row holds that a query does
+ * not see, NaN and infinities included, does not reach that query's result.
  * Supported by both calls: any pool dtype; head_dim 64 or 128; any num_kv_heads;
  * up to 16 query heads per kv head; any block_size the pool allows;
  * max_blocks_per_seq * block_size up to 2^30; others PKV_ERR_UNSUPPORTED.

@@ -402,12 +402,13 @@ cudaError_t launch_decode_combine_prefix(const DecodeLaunch& a, const float* pre
 
 // 0 = the prefill kernel handles this pool and head count; 1 = unsupported
 int prefill_supported(const PoolView& pv, int num_q_heads);
-// window 0: causal; else under that window, with the first `sink` tokens
+// window 0: causal; else under that window, with the first `sink` tokens (and `repair`)
+struct Repair;
 cudaError_t launch_prefill(const PoolView& pv, int layer, const void* q, int num_q_heads,
                            float scale, const int32_t* bt, int mb, const int32_t* lens,
                            const int32_t* offs, const int64_t* cu_q, int batch, long long total_q,
                            int max_q_len, int window, int sink, void* out, int* err, int sm_count,
-                           cudaStream_t s);
+                           cudaStream_t s, const Repair* repair = nullptr);
 
 // Process-wide settings of the bounded waits (pkv_set_wait_limit_ns; 0 = the
 // default bound) and the test hook that makes the first CTA of the decode

@@ -50,6 +50,7 @@
 
 #include "common.cuh"
 #include "pkv.h"
+#include "repair.cuh"
 #include "span.cuh"
 #include "tma.cuh"
 
@@ -117,6 +118,7 @@ struct PfParams {
   float* pre_acc;
   // windows and trees
   PlanParams plan;                 // (windows: its span alone)
+  Repair repair;
   const int32_t* q_pos;            // as in RowsParams
   const unsigned long long* mask;
   int words;
@@ -682,7 +684,7 @@ __device__ __forceinline__ long long item_of(const PfParams& p, long long c, uin
 template <int MODE, bool SHARE, int HD>
 __global__ void __launch_bounds__((pf_threads<MODE, SHARE>()), 1)
     prefill_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk,
-                   const __grid_constant__ CUtensorMap tv, const PfParams p) {
+                   const __grid_constant__ CUtensorMap tv, const __grid_constant__ PfParams p) {
   constexpr bool PREFIX = MODE == kPrefix, TREE = is_tree(MODE), NARROW = MODE == kNarrow,
                  SPAN = MODE == kWindow || TREE;
   constexpr int COLS = NARROW ? kKeys / 2 : kKeys;  // keys of one softmax tile
@@ -1345,6 +1347,7 @@ __global__ void __launch_bounds__((pf_threads<MODE, SHARE>()), 1)
         __nv_bfloat16* orow = static_cast<__nv_bfloat16*>(p.out) +
                               ((it.q0 + qi) * p.hq + (long long)it.g * G + hh) * kD;
         if (part && row_ok && x == 0) *reinterpret_cast<float2*>(srow) = make_float2(top, sum);
+        float finite = 0.f;  // 0 unless a value is not finite
 #pragma unroll 1
         for (int c0 = x * (kD / 2); c0 < (x + 1) * (kD / 2); c0 += 16) {
           uint32_t u[16], v[16];
@@ -1355,6 +1358,8 @@ __global__ void __launch_bounds__((pf_threads<MODE, SHARE>()), 1)
 #pragma unroll
           for (int j = 0; j < 16; ++j)
             o[j] = (__uint_as_float(u[j]) * fa + __uint_as_float(v[j]) * fb) * inv;
+#pragma unroll
+          for (int j = 0; j < 16; ++j) finite = fmaf(o[j], 0.f, finite);
           if (row_ok) {
             if (part) {
 #pragma unroll
@@ -1376,6 +1381,8 @@ __global__ void __launch_bounds__((pf_threads<MODE, SHARE>()), 1)
           mbar_arrive(b_ofree0);
           mbar_arrive(b_ofree0 + 8u);
         }
+        if (row_ok && !part && nonfinite(finite) && !nonfinite(sum))
+          repair_query<16>(p.repair, it.b, (int)qi, it.g * G + hh, x * (kD / 2), kD / 2);
         continue;
       }
       if constexpr (PREFIX) {
@@ -1427,6 +1434,7 @@ __global__ void __launch_bounds__((pf_threads<MODE, SHARE>()), 1)
           continue;
         }
       }
+      [[maybe_unused]] float finite = 0.f;  // 0 unless a value is not finite
       // (windows and trees: a NaN of the sum is one of the result)
       const float inv = (SPAN ? st.l != 0.f : st.l > 0.f) ? 1.f / st.l : 0.f;
       __nv_bfloat16* orow = static_cast<__nv_bfloat16*>(p.out) +
@@ -1436,6 +1444,10 @@ __global__ void __launch_bounds__((pf_threads<MODE, SHARE>()), 1)
         uint32_t v[32];
         tmem_ld32(tO(x) + lane_base + c0, v);
         tmem_wait_ld();
+        if constexpr (SPAN) {
+#pragma unroll
+          for (int j = 0; j < 32; ++j) finite = fmaf(__uint_as_float(v[j]), 0.f, finite);
+        }
         if (row_ok) {
           if ((reinterpret_cast<uintptr_t>(p.out) & 31) == 0) {
             // 32-byte stores (full sectors) when the output allows them
@@ -1467,6 +1479,10 @@ __global__ void __launch_bounds__((pf_threads<MODE, SHARE>()), 1)
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(b_ofree);
+      if constexpr (SPAN) {
+        if (row_ok && nonfinite(finite) && !nonfinite(st.l))
+          repair_query<16>(p.repair, it.b, (int)qi, it.g * G + hh, 0, kD);
+      }
     }
   }
 
@@ -1634,7 +1650,7 @@ cudaError_t launch_prefill(const PoolView& pv, int layer, const void* q, int num
                            float scale, const int32_t* bt, int mb, const int32_t* lens,
                            const int32_t* offs, const int64_t* cu_q, int batch, long long total_q,
                            int max_q_len, int window, int sink, void* out, int* err, int sm_count,
-                           cudaStream_t s) {
+                           cudaStream_t s, const Repair* repair) {
   if (batch == 0 || total_q == 0 || max_q_len == 0) return cudaSuccess;
   CUtensorMap tq, tk, tv;
   PfParams p;
@@ -1650,6 +1666,7 @@ cudaError_t launch_prefill(const PoolView& pv, int layer, const void* q, int num
   p.plan.span.window = window;
   p.plan.span.sink = sink;
   p.plan.span.gran = pv.block_size;
+  if (repair) p.repair = *repair;
   if (window == 0) return prefill_launch_pairs<kCausal>(tq, tk, tv, p, sm_count, s);
   return pv.head_dim == 64 ? prefill_launch_pairs<kWindow, 64>(tq, tk, tv, p, sm_count, s)
                            : prefill_launch_pairs<kWindow>(tq, tk, tv, p, sm_count, s);
@@ -1658,7 +1675,7 @@ cudaError_t launch_prefill(const PoolView& pv, int layer, const void* q, int num
 cudaError_t launch_prefill_tree(const PoolView& pv, int layer, const void* q, int num_q_heads,
                                 float scale, const int32_t* bt, const PlanParams& plan,
                                 const int32_t* q_pos, const unsigned long long* mask, int words,
-                                float* part, void* out, int* err, int sm_count, cudaStream_t s) {
+                                const Repair& repair, float* part, void* out, int* err, int sm_count, cudaStream_t s) {
   CUtensorMap tq, tk, tv;
   PfParams p;
   const SpanParams& sp = plan.span;
@@ -1668,6 +1685,7 @@ cudaError_t launch_prefill_tree(const PoolView& pv, int layer, const void* q, in
   if (e != cudaSuccess) return e;
   p.out = out;
   p.plan = plan;
+  p.repair = repair;
   p.q_pos = q_pos;
   p.mask = mask;
   p.words = words;

@@ -31,6 +31,7 @@
 #include "cluster.cuh"
 #include "common.cuh"
 #include "mma.cuh"
+#include "repair.cuh"
 #include "span.cuh"
 
 namespace pkv {
@@ -49,6 +50,7 @@ struct RowsParams {
   float* part;  // states of split units
   long long num_blocks;
   int L, layer, row_bytes, scale_off, hq, bs_bits;
+  Repair repair;
   int units_max;  // prefill: units of one kv head of the longest sequence
   long long keys_most;  // prefill: keys that a unit's rows see at most
   float qscale;   // scale * log2(e)
@@ -646,6 +648,8 @@ __device__ __forceinline__ void rows_piece(const RowsParams& p, const RowsPiece&
       *reinterpret_cast<uint2*>(p.out + at * 2) =
           make_uint2(pack_bf16x2(x[0] * inv, x[1] * inv), pack_bf16x2(x[2] * inv, x[3] * inv));
     }
+    if ((nonfinite(x[0]) || nonfinite(x[1]) || nonfinite(x[2]) || nonfinite(x[3])) && !nonfinite(sum))
+      repair_query<4>(p.repair, w.b, tok, w.g * G + (r - tok * G), d, 4);
   };
 
   // ---- the states to shared memory, and their merge ----
@@ -752,7 +756,7 @@ __device__ __forceinline__ void rows_piece(const RowsParams& p, const RowsPiece&
 // Tree: the batch's tiles split evenly over the grid (span.cuh).
 template <int MODE, int D, int MT, int RG>
 __global__ void __launch_bounds__(kRowsThreads, (RowsLayout<MODE, D, MT, RG>::kCtas))
-    rows_tree_kernel(const RowsParams p) {
+    rows_tree_kernel(const __grid_constant__ RowsParams p) {
   constexpr int KT = RowsTile<MODE, D>::kKeys, M = RowsLayout<MODE, D, MT, RG>::kRows;
   extern __shared__ __align__(128) unsigned char smem[];
   __shared__ long long scratch[32];
@@ -797,7 +801,7 @@ __global__ void __launch_bounds__(kRowsThreads, (RowsLayout<MODE, D, MT, RG>::kC
 // rows' units first.
 template <int MODE, int D, int MT, int RG>
 __global__ void __launch_bounds__(kRowsThreads, (RowsLayout<MODE, D, MT, RG>::kCtas))
-    rows_prefill_kernel(const RowsParams p) {
+    rows_prefill_kernel(const __grid_constant__ RowsParams p) {
   constexpr int KT = RowsTile<MODE, D>::kKeys, M = RowsLayout<MODE, D, MT, RG>::kRows;
   extern __shared__ __align__(128) unsigned char smem[];
   griddep_wait();

@@ -299,6 +299,8 @@ __device__ __forceinline__ PlanShare plan_share(const PlanParams& p, int cta, in
 cudaError_t launch_validate_spans(const SpanParams& p, const int32_t* bt, long long num_blocks,
                                   int* err, cudaStream_t s);
 
+struct Repair;  // repair.cuh
+
 // Host side (prefill.cu): whether the tcgen05 kernels take a windowed prefill (pairs) or a tree.
 bool span_supported(const PoolView& pv, int num_q_heads, bool pairs);
 // The tree decode on them: units of two tiles of 128 / G tokens, or of one where no sequence has
@@ -306,6 +308,6 @@ bool span_supported(const PoolView& pv, int num_q_heads, bool pairs);
 cudaError_t launch_prefill_tree(const PoolView& pv, int layer, const void* q, int num_q_heads,
                                 float scale, const int32_t* bt, const PlanParams& plan,
                                 const int32_t* q_pos, const unsigned long long* mask, int words,
-                                float* part, void* out, int* err, int sm_count, cudaStream_t s);
+                                const Repair& repair, float* part, void* out, int* err, int sm_count, cudaStream_t s);
 
 }  // namespace pkv

@@ -19,11 +19,12 @@ struct CombineParams {
   int hq, D, f32, grid;  // grid: CTAs of the kernel that left the states
   int blocks_seq;        // CTAs of a sequence
   int rows_warp;         // rows a warp takes, one after the other
+  Repair repair;
 };
 
 // One (token, query head) row, by one warp: the states of its unit in the CTAs that shared it,
 // by the log-sum-exp rule.  Rows that one CTA finished are left alone.
-__device__ __forceinline__ void combine_row(const CombineParams& p, const SeqPlan& q,
+__device__ __forceinline__ void combine_row(const CombineParams& p, const SeqPlan& q, int b,
                                             long long chunk, long long before, int row) {
   const int lane = threadIdx.x & 31;
   const int tok = row / p.hq, h = row - tok * p.hq, g = h / p.plan.G;
@@ -79,11 +80,14 @@ __device__ __forceinline__ void combine_row(const CombineParams& p, const SeqPla
   else
     *reinterpret_cast<uint2*>(p.out + dst * 2) =
         make_uint2(pack_bf16x2(x[0] * inv, x[1] * inv), pack_bf16x2(x[2] * inv, x[3] * inv));
+  if ((nonfinite(x[0]) || nonfinite(x[1]) || nonfinite(x[2]) || nonfinite(x[3])) && !nonfinite(sum))
+    repair_query<4>(p.repair, b, tok, h, d, 4);
 }
 
 // A CTA takes kCombineWarps * rows_warp rows of one sequence.
 template <int KT>
-__global__ void __launch_bounds__(kCombineWarps * 32) tree_combine_kernel(const CombineParams p) {
+__global__ void __launch_bounds__(kCombineWarps * 32)
+    tree_combine_kernel(const __grid_constant__ CombineParams p) {
   __shared__ long long scratch[32];
   // What stands before the wait reads inputs alone, which were complete when the grid that
   // leaves the states let this one launch: it runs beside that grid's end.
@@ -102,7 +106,7 @@ __global__ void __launch_bounds__(kCombineWarps * 32) tree_combine_kernel(const 
   for (int i = 0; i < p.rows_warp; ++i) {
     const int row = first_row + i * kCombineWarps + (int)(threadIdx.x >> 5);
     if (row >= q.s.n * p.hq) break;
-    combine_row(p, q, chunk, before, row);
+    combine_row(p, q, b, chunk, before, row);
   }
 }
 
@@ -250,6 +254,24 @@ RowsParams rows_params(const Call& c, const PoolView& v, int* err) {
   p.hq = c.num_q_heads;
   while (1 << p.bs_bits < v.block_size) ++p.bs_bits;
   p.qscale = c.scale * kLog2e;
+  Repair& r = p.repair;
+  r.span = s;
+  r.k = v.k;
+  r.v = v.v;
+  r.q = p.q;
+  r.out = p.out;
+  r.bt = p.bt;
+  r.num_blocks = v.num_blocks;
+  r.hq = c.num_q_heads;
+  r.G = p.plan.G;
+  r.L = v.num_layers;
+  r.layer = c.layer;
+  r.bs_bits = p.bs_bits;
+  r.row_bytes = v.row_bytes;
+  r.scale_off = v.scale_off;
+  r.D = v.head_dim;
+  r.dtype = c.pool->dtype;
+  r.qscale = p.qscale;
   return p;
 }
 
@@ -321,11 +343,14 @@ pkv_status pkv_decode_attention_tree(const pkv_pool* pool, int32_t layer, const 
   p.mask = reinterpret_cast<const unsigned long long*>(tree_mask);
   p.words = mask_words;
   p.q_pos = q_pos;
+  p.repair.mask = p.mask;
+  p.repair.words = mask_words;
+  p.repair.q_pos = q_pos;
   if (validate && (st = pkv::validate_call(p, stream)) != PKV_OK) return (pkv_status)st;
   const cudaError_t e =
       path.tcgen05
           ? pkv::launch_prefill_tree(v, layer, q, num_q_heads, scale, block_tables, p.plan, q_pos,
-                                     p.mask, mask_words, p.part, out, err, sms, stream)
+                                     p.mask, mask_words, p.repair, p.part, out, err, sms, stream)
           : pkv::launch_rows(v, p, true, path.grid, dev, stream);
   if ((st = pkv::launch_status(e)) != PKV_OK) return (pkv_status)st;
   pkv::CombineParams m = {};
@@ -336,6 +361,7 @@ pkv_status pkv_decode_attention_tree(const pkv_pool* pool, int32_t layer, const 
   m.D = v.head_dim;
   m.f32 = v.io_size == 4;
   m.grid = path.grid;
+  m.repair = p.repair;
   // as many CTAs as the device holds about at once: each goes over the batch first
   const int64_t rows = (int64_t)max_q_len * num_q_heads;
   const int64_t all = rows * batch / pkv::kCombineWarps;
@@ -382,7 +408,7 @@ pkv_status pkv_prefill_attention_window(const pkv_pool* pool, int32_t layer, con
       pkv::prefill_on_tcgen05(v, p, sms)
           ? pkv::launch_prefill(v, layer, q, num_q_heads, scale, block_tables, max_blocks_per_seq,
                                 seq_lens, offsets, cu_q, batch, total_q, max_q_len, window,
-                                p.plan.span.sink, out, err, sms, stream)
+                                p.plan.span.sink, out, err, sms, stream, &p.repair)
           : pkv::launch_rows(v, p, false, 0, dev, stream);
   if ((st = pkv::launch_status(e)) != PKV_OK) return (pkv_status)st;
   return validate ? (pkv_status)pkv::read_and_clear_error_word(err, stream) : PKV_OK;

@@ -427,6 +427,44 @@ def test_tree_many_sequences(dev):
     _run_tree(dev, "bf16", 1, 16, 128, 8, lens, new, 0, 0, seed=14)
 
 
+# ---- values that some queries see and others do not -------------------------------------
+
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+@pytest.mark.parametrize("dtype,G,D,ctx,n", [
+    ("bf16", 4, 128, 300, 40), ("bf16", 4, 128, 300, 20), ("bf16", 4, 128, 300, 6), ("bf16", 4, 128, 6000, 40),
+    ("bf16", 4, 128, 6000, 20), ("bf16", 2, 64, 300, 100), ("bf16", 2, 64, 4000, 20), ("bf16", 3, 64, 700, 5),
+    ("f32", 3, 64, 500, 9), ("f32", 1, 128, 2000, 30), ("i8", 4, 128, 300, 12), ("i8", 2, 64, 3000, 5)])
+def test_unseen_values_do_not_spread(dev, dtype, G, D, ctx, n, bad):
+    """A V row of NaN or infinities shows in the queries that see it and in no other: a drafted
+    token's siblings, the tokens before it, those that its window has left behind."""
+    c = Case(dev, dtype, 2, G, D, 16, [ctx + n, 70], [n, 3], seed=51)
+    sees, depth = _random_tree(c.rng, n)
+    mask, pos = _tree_args(c, [sees, np.tril(np.ones((3, 3)))], [depth, np.arange(3)], -(-n // 64))
+    j = n // 2
+    place = int(c.offs[0]) + ctx + j
+    blk, row = int(c.home[0, place // 16]), place % 16
+    calls = {"tree": lambda: _tree(c, mask, pos), "chain": lambda: _tree(c, None, None),
+             "prefill": lambda: _prefill(c, 3, 1), "wide": lambda: _prefill(c, 1 << 20, 0)}
+    seen = {"tree": sees[:, j], "chain": np.arange(n) >= j,
+            "prefill": np.array([j <= i < j + 3 for i in range(n)]), "wide": np.arange(n) >= j}
+    clean = {k: f() for k, f in calls.items()}
+    if dtype == "i8":
+        c.v[blk, c.layer, row, 2 * D:2 * D + 8].view(torch.float32).fill_(bad)
+    else:
+        c.v[blk, c.layer, row] = bad
+    for k, f in calls.items():
+        got = f()
+        assert bool(got[n:].isfinite().all()), k
+        touched = torch.from_numpy(seen[k]).to(dev)
+        keep = got[:n][~touched].float()
+        assert bool(keep.isfinite().all()), k
+        # (computed another way: two roundings of the output apart, and those of the weights)
+        want = clean[k][:n][~touched].float()
+        assert float((keep - want).abs().max() if keep.numel() else 0.0) <= (0.04 if dtype != "f32" else 1e-5), k
+        assert not bool(got[:n][touched].isfinite().any()) or dtype == "i8", k
+    assert pkv.device_error() == "PKV_OK"
+
+
 # ---- accepted tokens ----------------------------------------------------------------
 
 def _accept_case(dev, dtype, H, D, bs, lens, new, paths, layers=3):
