@@ -56,13 +56,22 @@ struct RowsParams {
   float qscale;   // scale * log2(e)
 };
 
-constexpr int kRowsWarps = 4;
+constexpr int kRowsWarps = 8;
 constexpr int kRowsMaxCluster = 8;
 constexpr int kRowsThreads = kRowsWarps * 32;
+
+// Keys of a tile.  int8, 32 rows: 128, so that each K code is converted by one warp only (32
+// sequences of 4 to 8 tokens behind 1024 to 8192, 8 kv heads, D 128, G 4: 133 us with 64 keys, 125;
+// with 64 rows the scores of 128 keys do not fit in the registers: 325 us where 64 take 301, on
+// 4096 tokens of a prompt under a window of 1024).
+constexpr int rows_tile_keys(int mode, int rows) {
+  return mode == PKV_F32 ? 32 : mode == PKV_I8 && rows == 32 ? 128 : 64;
+}
 
 namespace {
 
 constexpr unsigned kAllLanes = 0xffffffffu;
+constexpr float kMostUnits = 128.f;  // of a V scale: times a weight of up to 2^8, 2^15 in all
 
 __device__ __forceinline__ uint32_t tf32_of(float x) {
   uint32_t r;
@@ -82,64 +91,50 @@ __device__ __forceinline__ void mma8_tf32(float (&d)[4], const uint32_t (&a)[4],
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
-// Four codes (bytes c + 128) to bf16 pairs.  The low 7 bits of a byte behind 0x43 are
-// 128 + them; the byte's top bit says whether 128 or 256 is to be taken off.
-__device__ __forceinline__ uint32_t codes_pair_bf16(uint32_t spread) {
-  const uint32_t x = spread & 0xFF7FFF7Fu, y = (~spread & 0x00800080u) | 0x43004300u;
-  const __nv_bfloat162 d = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&x),
-                                   *reinterpret_cast<const __nv_bfloat162*>(&y));
-  return *reinterpret_cast<const uint32_t*>(&d);
-}
-__device__ __forceinline__ void codes_to_bf16(uint32_t w, uint32_t& lo, uint32_t& hi) {
-  uint32_t a, b;
-  asm("prmt.b32 %0, %1, 0x43434343, 0x4140;" : "=r"(a) : "r"(w));
-  asm("prmt.b32 %0, %1, 0x43434343, 0x4342;" : "=r"(b) : "r"(w));
-  lo = codes_pair_bf16(a);
-  hi = codes_pair_bf16(b);
-}
-
-template <int MODE, int D>
+template <int MODE, int D, int M>
 struct RowsTile {
   static constexpr int kEs = MODE == PKV_F32 ? 4 : MODE == PKV_BF16 ? 2 : 1;
-  static constexpr int kKeys = MODE == PKV_F32 ? 32 : 64;
+  static constexpr int kKeys = rows_tile_keys(MODE, M);
   static constexpr int kRow = D * kEs;
   static constexpr int kChunks = kRow / 16;
   static constexpr int kHalf = kKeys * kRow;
   static constexpr int kBytes = 2 * kHalf + (MODE == PKV_I8 ? 2 * kKeys * 16 : 0);
-  static constexpr int kStages = kBytes > 16384 ? 3 : 4;
   // Byte offset of chunk c of row r, permuted so that each 8-lane phase of the reads
   // falls in 8 different 16-byte columns.
   static __device__ __forceinline__ int at(int r, int c) {
     if constexpr (MODE == PKV_I8) {
       if constexpr (D == 64) return r * kRow + ((c ^ ((r >> 1) & 3)) << 4);
       return r * kRow + ((c ^ (((r & 1) << 2) | ((r >> 1) & 3))) << 4);
-    } else if constexpr (MODE == PKV_F32) {
-      return r * kRow + ((c ^ (((r & 6)) ^ ((r & 1) << 2))) << 4);
     }
     return r * kRow + ((c ^ (r & 7)) << 4);
   }
 };
 
-// MT: 16-row tiles of a warp; RG: groups of warps that share out a unit's rows.
-template <int MODE, int D, int MT, int RG>
+// M: rows of a unit.  The scores of a tile are shared out over the warps by KG groups of 8 keys
+// and, where those are fewer than the warps, by row tiles.
+template <int MODE, int D, int M>
 struct RowsLayout {
-  using Tl = RowsTile<MODE, D>;
-  static constexpr int kRows = 16 * MT * RG;
-  static constexpr int kRing = Tl::kStages * Tl::kBytes;
-  // Q: with two row tiles in shared memory (fp32 as two tf32 parts), with one in registers
-  static constexpr bool kQShared = MT > 1;
-  static constexpr int kQRow = D * (MODE == PKV_F32 ? 4 : 2);
-  static constexpr int kQ = kQShared ? kRows * kQRow * (MODE == PKV_F32 ? 2 : 1) : 0;
-  static constexpr int kAccRow = D + 4;  // floats between rows of a merged state
-  static constexpr int kMerge = kRowsWarps * 16 * MT * (kAccRow + 2) * 4;
-  static constexpr int kQAt = kRing > kMerge ? kRing : kMerge;
-  static constexpr int kSeenAt = kQAt + kQ;  // what each of a warp's rows sees
-  static constexpr int kSmem = kSeenAt + kRowsWarps * 16 * MT * (int)sizeof(RowSees);
-  // CTAs that an SM holds at once, of the tree kernel its grid: what shared memory and O's
-  // registers allow
+  using Tl = RowsTile<MODE, D, M>;
+  static constexpr bool kF32 = MODE == PKV_F32;
+  static constexpr int KN = M > 16 && !kF32 ? 2 : 1;  // 8-key groups of a warp's scores
+  static constexpr int MT = M / 16, KG = Tl::kKeys / 8 / KN, MG = kRowsWarps / KG;
+  static constexpr int MS = MT > MG ? MT / MG : 1;  // row tiles of a warp's scores
+  static constexpr bool kTwoParts = M == 16 && MODE == PKV_BF16;  // of a weight in P V
+  static constexpr int kStages = Tl::kBytes > 32768 || (Tl::kBytes == 32768 && (kF32 || M == 64)) ? 2 : 3;
+  static constexpr int kRing = kStages * Tl::kBytes;
+  static constexpr int kQRow = D * (kF32 ? 4 : 2), kQPart = M * kQRow;  // fp32: two tf32 parts
+  static constexpr int kQAt = kRing;
+  static constexpr int kPRow = Tl::kKeys * (kF32 ? 4 : 2), kPPart = M * kPRow;
+  static constexpr int kPAt = kQAt + kQPart * (kF32 ? 2 : 1);
+  static constexpr int kSeenAt = kPAt + kPPart * (kF32 || kTwoParts ? 2 : 1);
+  // of each row: maximum, factor, sum, [KG]; int8 also units, factor of O, [KG]
+  static constexpr int kRowAt = kSeenAt + M * (int)sizeof(RowSees);
+  static constexpr int kSmem = kRowAt + (3 + KG) * M * 4 + (MODE == PKV_I8 ? (2 + KG) * M * 4 : 0);
+  static constexpr int kAccRow = D + 4;  // floats between rows of a state in the merge of a cluster
+  static_assert(M * (kAccRow + 2) * 4 <= kRing, "the merge lies over the ring");
+  // CTAs that an SM holds at once, of the tree kernel its grid
   static constexpr int kFit = 227 * 1024 / (kSmem + 2048);
-  static constexpr int kMost = D == 64 || (MODE == PKV_I8 && MT == 1) ? 3 : 2;
-  static constexpr int kCtas = kFit < kMost ? kFit : kMost;
+  static constexpr int kCtas = kFit < 2 ? kFit : 2;
 };
 
 // One unit's work: rows first_row .. of sequence b, kv head g, tiles t0 .. t1 of its list.
@@ -151,22 +146,32 @@ struct RowsPiece {
   float* part;   // where the state goes, or NULL: finished here
 };
 
-template <int MODE, int D, int MT, int RG, bool TREE>
+template <int MODE, int D, int M, bool TREE>
 __device__ __forceinline__ void rows_piece(const RowsParams& p, const RowsPiece& w, int ctas,
                                            unsigned char* smem) {
-  using Tl = RowsTile<MODE, D>;
-  using Lay = RowsLayout<MODE, D, MT, RG>;
-  constexpr bool kI8 = MODE == PKV_I8, kF32 = MODE == PKV_F32;
-  constexpr int WK = kRowsWarps / RG, KT = Tl::kKeys, KW = KT / WK, NT = KW / 8;
-  constexpr int NST = Tl::kStages, M = Lay::kRows, NO = D / 8;
-  constexpr bool kTwoParts = MT == 1;  // of a weight in P V
+  using Tl = RowsTile<MODE, D, M>;
+  using Lay = RowsLayout<MODE, D, M>;
+  constexpr bool kI8 = MODE == PKV_I8, kF32 = MODE == PKV_F32, kTwoParts = Lay::kTwoParts;
+  constexpr int KT = Tl::kKeys, NST = Lay::kStages, MT = Lay::MT, MS = Lay::MS, KG = Lay::KG;
+  constexpr int KN = Lay::KN, KS = kF32 ? D / 8 : D / 16;         // steps of a score
+  constexpr int NO = D / kRowsWarps / 8;            // 8-dim output tiles of a warp
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int wr = warp % RG, wk = warp / RG;
+  const int kg = warp % KG, mg = warp / KG;  // scores: KN groups of 8 keys from KN kg, row tiles from mg MS
+  const bool scores = mg * MS < MT;
   const int gl = lane >> 2, qi = lane & 3;
   const int G = p.plan.G, n = w.s.n, rows = n * G, off = w.s.off;
-  const uint32_t base = smem_addr(smem), sq = base + Lay::kQAt;
+  const uint32_t base = smem_addr(smem), sq = base + Lay::kQAt, sp = base + Lay::kPAt;
+  RowSees* seen_rows = reinterpret_cast<RowSees*>(smem + Lay::kSeenAt);
+  float* row_max = reinterpret_cast<float*>(smem + Lay::kRowAt);  // [M]: what P is taken against
+  float* row_factor = row_max + M;                                // [M]: of O, when it moved
+  float* row_sum = row_factor + M;                                // [M]: at the end
+  float* row_part = row_sum + M;                                  // [KG][M]
+  // int8: O is in units of 2^row_units (in the scores' base), so that weight x V scale fits fp16
+  [[maybe_unused]] float* row_units = row_part + KG * M;
+  [[maybe_unused]] float* row_factor_o = row_units + M;
+  [[maybe_unused]] float* row_top = row_factor_o + M;  // [KG][M]
 
-  // ---- copies: each warp a quarter of a tile's rows ----
+  // ---- copies: each warp an eighth of a tile's rows ----
   constexpr int RW = KT / kRowsWarps;
   const int sink_end = off + p.plan.span.sink;  // table position
   const int my_r = warp * RW + lane % RW;  // the row of a tile that this lane looks up
@@ -206,80 +211,48 @@ __device__ __forceinline__ void rows_piece(const RowsParams& p, const RowsPiece&
         cp_async16(d + Tl::kHalf, p.v + (on ? src : 0), on);
       }
       if constexpr (kI8) {
-        // the 16 bytes that hold the head's scale: lanes 0-15 of K, the others of V
+        // the 16 bytes that hold the head's scale: lanes 0-7 of K, 8-15 of V
         const bool on = live >> lane & 1;
         const long long src = on ? at + p.scale_off + (4 * w.g & ~15) : 0;
-        cp_async16(dst + 2 * Tl::kHalf + (lane / RW * KT + my_r) * 16,
-                   (lane < RW ? p.k : p.v) + src, on);
+        if (lane < 2 * RW)
+          cp_async16(dst + 2 * Tl::kHalf + (lane / RW * KT + my_r) * 16,
+                     (lane < RW ? p.k : p.v) + src, on);
       }
     }
     cp_commit();
   };
+  static_assert(RW * Tl::kChunks >= 32, "every lane copies");
 #pragma unroll 1
   for (int s = 0; s < NST - 1; ++s) issue(w.t0 + s, s);
 
-  // ---- what the warp's rows see, a row a lane: kept in shared memory ----
-  const int warp_row = w.first_row + wr * 16 * MT;
-  RowSees* seen_rows = reinterpret_cast<RowSees*>(smem + Lay::kSeenAt) + warp * (16 * MT);
-  int full_lo, full_hi;  // places that every row of the warp sees
-  {
-    const int r = warp_row + lane % (16 * MT);
-    const bool live = r < rows;
+  // ---- what the rows see: kept in shared memory, and the places that all of them see ----
+  int full_lo = INT_MIN, full_hi = INT_MAX;
+  for (int r0 = 0; r0 < M; r0 += 32) {
+    const int r = w.first_row + r0 + lane;
+    const bool live = r0 + lane < M && r < rows;
     const int tok = live ? r / G : 0;
     const RowSees row = row_sees(p.plan.span, w.t, off, w.s.ctx, n, tok, w.s.q0 + tok,
                                  TREE ? p.q_pos : nullptr, TREE ? p.mask : nullptr, p.words);
-    if (lane < 16 * MT) seen_rows[lane] = row;
-    full_lo = max(row.first, __reduce_max_sync(kAllLanes, live ? row.lo : INT_MIN));
-    full_hi = __reduce_min_sync(kAllLanes, live ? row.top : INT_MAX);
-    __syncwarp();
+    if (r0 + lane < M && warp == (r0 >> 5)) seen_rows[r0 + lane] = row;
+    full_lo = max(full_lo, max(row.first, __reduce_max_sync(kAllLanes, live ? row.lo : INT_MIN)));
+    full_hi = min(full_hi, __reduce_min_sync(kAllLanes, live ? row.top : INT_MAX));
+  }
+  if (tid < M) {
+    row_max[tid] = -INFINITY;
+    if constexpr (kI8) row_units[tid] = -INFINITY;
   }
 
-  // ---- Q, rows behind the last one as zeros ----
+  // ---- Q to shared memory, rows behind the last one as zeros ----
   auto q_row = [&](int r) {
     const int tok = r / G;
     return p.q + ((w.s.q0 + tok) * p.hq + w.g * G + (r - tok * G)) * (long long)Lay::kQRow;
   };
-  constexpr int KS = kF32 ? D / 8 : D / 16;
-  [[maybe_unused]] uint32_t qa[Lay::kQShared ? 1 : KS][4];
-  if constexpr (!Lay::kQShared) {
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int r = warp_row + gl + 8 * i;
-      const bool live = r < rows;
-      const char* src = q_row(live ? r : 0);
-      if constexpr (MODE == PKV_BF16) {
-#pragma unroll
-        for (int k = 0; k < KS; ++k) {
-          const char* x = src + (k * 16 + 2 * qi) * 2;
-          qa[k][i] = live ? *reinterpret_cast<const uint32_t*>(x) : 0u;
-          qa[k][2 + i] = live ? *reinterpret_cast<const uint32_t*>(x + 16) : 0u;
-        }
-      } else if constexpr (kI8) {
-        // step 4 i + j: dims 64 i + 16 qi + 4 j .. + 3, the order of the K codes
-#pragma unroll
-        for (int k = 0; k < KS; ++k) {
-          const char* x = src + ((k >> 2) * 64 + 16 * qi + 4 * (k & 3)) * 2;
-          const uint2 y = live ? *reinterpret_cast<const uint2*>(x) : make_uint2(0u, 0u);
-          qa[k][i] = y.x;
-          qa[k][2 + i] = y.y;
-        }
-      } else {
-        // steps 2 i, 2 i + 1: dims 16 i + 4 qi .. + 3
-#pragma unroll
-        for (int k = 0; k < KS; k += 2) {
-          const char* x = src + (k * 8 + 4 * qi) * 4;
-          const uint4 y = live ? *reinterpret_cast<const uint4*>(x) : make_uint4(0u, 0u, 0u, 0u);
-          qa[k][i] = y.x;
-          qa[k][2 + i] = y.y;
-          qa[k + 1][i] = y.z;
-          qa[k + 1][2 + i] = y.w;
-        }
-      }
-    }
-  } else {
+  {
     // 16-byte chunks; int8: a chunk's two groups of 4 dims (64 i + 16 c + 4 j ..) go where step
-    // 4 i + j takes them, columns 2 c, 2 c + 1 and 8 + 2 c, 9 + 2 c of it
+    // 4 i + j takes them, columns 2 c, 2 c + 1 and 8 + 2 c, 9 + 2 c of it: the order of the K codes
     constexpr int C = Lay::kQRow / 16;
+    static_assert(C <= 32 && M * C % 32 == 0, "a row's chunks lie in one warp");
+    [[maybe_unused]] float* q_unit = row_sum;  // until the end
 #pragma unroll 4
     for (int e = tid; e < M * C; e += kRowsThreads) {
       const int r = e / C, c = e % C;
@@ -289,6 +262,24 @@ __device__ __forceinline__ void rows_piece(const RowsParams& p, const RowsPiece&
       if constexpr (MODE == PKV_BF16) {
         sts128(at + ((c ^ (r & 7)) << 4), x);
       } else if constexpr (kI8) {
+        // fp16, in units of a power of two that puts the row's largest in 2^14 .. 2^15: exact, but
+        // for what lies under 2^-39 of the largest (infinities stay)
+        int top = 0;
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {
+          const uint32_t word = u < 2 ? x.x : u < 4 ? x.y : u < 6 ? x.z : x.w;
+          const int e = (word >> (16 * (u & 1) + 7)) & 255;
+          if (e != 255) top = max(top, e);
+        }
+#pragma unroll
+        for (int u = 1; u < C; u <<= 1) top = max(top, __shfl_xor_sync(kAllLanes, top, u));
+        top = max(top, 15);
+        const float up = __int_as_float((141 - top + 127) << 23);
+        if (c == 0) q_unit[r] = __int_as_float((top - 141 + 127) << 23);
+        x.x = pack_f16x2(bf16_lo(x.x) * up, bf16_hi(x.x) * up);
+        x.y = pack_f16x2(bf16_lo(x.y) * up, bf16_hi(x.y) * up);
+        x.z = pack_f16x2(bf16_lo(x.z) * up, bf16_hi(x.z) * up);
+        x.w = pack_f16x2(bf16_lo(x.w) * up, bf16_hi(x.w) * up);
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
           const int d = 8 * c + 4 * u, step = (d >> 6) * 4 + ((d >> 2) & 3), col = (d >> 4) & 3;
@@ -301,420 +292,488 @@ __device__ __forceinline__ void rows_piece(const RowsParams& p, const RowsPiece&
         split_tf32(__uint_as_float(x.y), h.y, l.y);
         split_tf32(__uint_as_float(x.z), h.z, l.z);
         split_tf32(__uint_as_float(x.w), h.w, l.w);
-        sts128(sq + Tl::at(r, c), h);
-        sts128(sq + M * Lay::kQRow + Tl::at(r, c), l);
+        sts128(at + ((c ^ (r & 7)) << 4), h);
+        sts128(at + Lay::kQPart + ((c ^ (r & 7)) << 4), l);
       }
     }
   }
-  // the A operand of step k of row tile mt (bf16, int8)
-  auto q_frag = [&](int mt, int k, uint32_t (&a)[4]) {
-    if constexpr (Lay::kQShared) {
-      const int r = wr * 16 * MT + mt * 16 + (lane & 15);
-      ldsm_x4(a, sq + r * Lay::kQRow + (((2 * k + (lane >> 4)) ^ (r & 7)) << 4));
-    } else {
-#pragma unroll
-      for (int c = 0; c < 4; ++c) a[c] = qa[k][c];
-    }
-  };
-  // fp32: both parts of steps k, k + 1
-  auto q_frag_tf32 = [&](int mt, int k, uint32_t (&h)[2][4], uint32_t (&l)[2][4]) {
-    if constexpr (Lay::kQShared) {
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int r = wr * 16 * MT + mt * 16 + gl + 8 * i;
-        const uint4 x = lds128(sq + Tl::at(r, 2 * k + qi));
-        const uint4 y = lds128(sq + M * Lay::kQRow + Tl::at(r, 2 * k + qi));
-        h[0][i] = x.x; h[0][2 + i] = x.y; h[1][i] = x.z; h[1][2 + i] = x.w;
-        l[0][i] = y.x; l[0][2 + i] = y.y; l[1][i] = y.z; l[1][2 + i] = y.w;
-      }
-    } else {
-#pragma unroll
-      for (int u = 0; u < 2; ++u)
-#pragma unroll
-        for (int c = 0; c < 4; ++c) split_tf32(__uint_as_float(qa[k + u][c]), h[u][c], l[u][c]);
-    }
+  // An A operand of 16 rows and two 16-byte chunks: of Q (a step of bf16: 16 dims; of tf32: 8), of P.
+  auto a_frag = [&](uint32_t from, int row_bytes, int mt, int step, uint32_t (&a)[4]) {
+    const int r = mt * 16 + (lane & 15);
+    ldsm_x4(a, from + r * row_bytes + (((2 * step + (lane >> 4)) ^ (r & 7)) << 4));
   };
 
-  float o[MT][NO][4], m[MT][2], l[MT][2];
+  float o[MT][NO][4], m[MS][2], l[MS][2];
+  [[maybe_unused]] float unit[MS][2], q_unit[MS][2];
+  if constexpr (kI8) {
+    __syncthreads();
 #pragma unroll
-  for (int mt = 0; mt < MT; ++mt) {
+    for (int j = 0; j < MS; ++j)
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        unit[j][r] = 1.f;
+        q_unit[j][r] = scores ? row_sum[(mg * MS + j) * 16 + gl + 8 * r] * p.qscale : 0.f;
+      }
+  }
+#pragma unroll
+  for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
     for (int k = 0; k < NO; ++k)
 #pragma unroll
       for (int c = 0; c < 4; ++c) o[mt][k][c] = 0.f;
-    m[mt][0] = m[mt][1] = -INFINITY;
-    l[mt][0] = l[mt][1] = 0.f;
+#pragma unroll
+  for (int i = 0; i < MS; ++i) {
+    m[i][0] = m[i][1] = -INFINITY;
+    l[i][0] = l[i][1] = 0.f;
   }
 
   int stage = 0;
 #pragma unroll 1
   for (int i = w.t0; i < w.t1; ++i) {
     cp_wait<NST - 2>();
-    __syncthreads();
+    __syncthreads();  // the tile is there, and the last one's P and stage are done with
     issue(i + NST - 1, stage == 0 ? NST - 1 : stage - 1);
     const uint32_t st = base + stage * Tl::kBytes, sv = st + Tl::kHalf;
     if (++stage == NST) stage = 0;
-    const int k0 = wk * KW;  // the warp's keys of the tile
 
-    // ---- scores ----
-    float s[MT][NT][4];
+    // ---- the warp's scores ----
+    float s[MS][KN][4];
+    [[maybe_unused]] float scale_v[KN][2];
+    bool raise = false;
+    if (scores) {
 #pragma unroll
-    for (int mt = 0; mt < MT; ++mt)
+      for (int j = 0; j < MS; ++j)
 #pragma unroll
-      for (int j = 0; j < NT; ++j)
+        for (int e = 0; e < KN; ++e)
 #pragma unroll
-        for (int c = 0; c < 4; ++c) s[mt][j][c] = 0.f;
-    if constexpr (MODE == PKV_BF16) {
-      const int r = k0 + (lane & 7) + ((lane >> 4) & 1) * 8, cc = (lane >> 3) & 1;
+          for (int c = 0; c < 4; ++c) s[j][e][c] = 0.f;
+      if constexpr (MODE == PKV_BF16) {
 #pragma unroll
-      for (int k = 0; k < KS; ++k) {
-        uint32_t a[MT][4];
+        for (int k = 0; k < KS; k += 2) {
+          uint32_t b[KN][4];
 #pragma unroll
-        for (int mt = 0; mt < MT; ++mt) q_frag(mt, k, a[mt]);
+          for (int e = 0; e < KN; ++e)
+            ldsm_x4(b[e], st + Tl::at((kg * KN + e) * 8 + (lane & 7), 2 * k + (lane >> 3)));
 #pragma unroll
-        for (int j = 0; j < NT; j += 2) {
-          uint32_t b[4];
-          ldsm_x4(b, st + Tl::at(r + j * 8, 2 * k + cc));
+          for (int j = 0; j < MS; ++j)
 #pragma unroll
-          for (int mt = 0; mt < MT; ++mt) {
-            mma16<false>(s[mt][j], a[mt][0], a[mt][1], a[mt][2], a[mt][3], b[0], b[1]);
-            mma16<false>(s[mt][j + 1], a[mt][0], a[mt][1], a[mt][2], a[mt][3], b[2], b[3]);
+            for (int u = 0; u < 2; ++u) {
+              uint32_t a[4];
+              a_frag(sq, Lay::kQRow, mg * MS + j, k + u, a);
+#pragma unroll
+              for (int e = 0; e < KN; ++e)
+                mma16<false>(s[j][e], a[0], a[1], a[2], a[3], b[e][2 * u], b[e][2 * u + 1]);
+            }
+        }
+      } else if constexpr (kI8) {
+#pragma unroll
+        for (int u = 0; u < KS / 4; ++u) {
+          uint4 x[KN];
+#pragma unroll
+          for (int e = 0; e < KN; ++e)
+            x[e] = lds128(st + Tl::at((kg * KN + e) * 8 + gl, 4 * u + qi));
+#pragma unroll
+          for (int v = 0; v < 4; ++v) {
+            uint32_t b[KN][2];
+#pragma unroll
+            for (int e = 0; e < KN; ++e)
+              codes_to_f16(v == 0 ? x[e].x : v == 1 ? x[e].y : v == 2 ? x[e].z : x[e].w, b[e][0],
+                            b[e][1]);
+#pragma unroll
+            for (int j = 0; j < MS; ++j) {
+              uint32_t a[4];
+              a_frag(sq, Lay::kQRow, mg * MS + j, 4 * u + v, a);
+#pragma unroll
+              for (int e = 0; e < KN; ++e)
+                mma16<true>(s[j][e], a[0], a[1], a[2], a[3], b[e][0], b[e][1]);
+            }
           }
         }
+      } else {
+        float big[MS][4];
+#pragma unroll
+        for (int j = 0; j < MS; ++j)
+#pragma unroll
+          for (int c = 0; c < 4; ++c) big[j][c] = 0.f;
+#pragma unroll
+        for (int k = 0; k < KS; k += 2) {
+          uint32_t b[4], bh[4], bl[4];
+          ldsm_x4(b, st + Tl::at(kg * 8 + (lane & 7), 2 * k + (lane >> 3)));
+#pragma unroll
+          for (int c = 0; c < 4; ++c) split_tf32(__uint_as_float(b[c]), bh[c], bl[c]);
+#pragma unroll
+          for (int j = 0; j < MS; ++j)
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+              uint32_t ah[4], al[4];
+              a_frag(sq, Lay::kQRow, mg * MS + j, k + u, ah);
+              a_frag(sq + Lay::kQPart, Lay::kQRow, mg * MS + j, k + u, al);
+              mma8_tf32(s[j][0], al, bh[2 * u], bh[2 * u + 1]);
+              mma8_tf32(s[j][0], ah, bl[2 * u], bl[2 * u + 1]);
+              mma8_tf32(big[j], ah, bh[2 * u], bh[2 * u + 1]);
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < MS; ++j)
+#pragma unroll
+          for (int c = 0; c < 4; ++c) s[j][0][c] += big[j][c];
       }
-    } else if constexpr (kI8) {
-      const int r = k0 + 4 * (gl >> 1) + (gl & 1);
+      // scaled, masked, and looked at: P is taken against a maximum that moves only when a score
+      // passes it by more than 8 (in log2 units, so P stays below 2^8)
 #pragma unroll
-      for (int u = 0; u < KS / 4; ++u) {
-        uint4 x[NT];
+      for (int e = 0; e < KN; ++e) {
+        [[maybe_unused]] float f[2];
+        if constexpr (kI8) {
+          const uint32_t sc = st + 2 * Tl::kHalf + ((kg * KN + e) * 8 + 2 * qi) * 16 + (4 * w.g & 15);
 #pragma unroll
-        for (int j = 0; j < NT; ++j)
-          x[j] = lds128(st + Tl::at(r + (j >> 1) * 16 + (j & 1) * 2, 4 * u + qi));
+          for (int c = 0; c < 2; ++c) {
+            f[c] = lds_f32(sc + c * 16);
+            scale_v[e][c] = lds_f32(sc + (KT + c) * 16);
+          }
+        }
+        const int x0 = i * KT + (kg * KN + e) * 8;
+        const bool full = x0 >= full_lo && x0 + 7 <= full_hi;
 #pragma unroll
-        for (int v = 0; v < 4; ++v) {
-          uint32_t a[MT][4];
+        for (int j = 0; j < MS; ++j)
 #pragma unroll
-          for (int mt = 0; mt < MT; ++mt) q_frag(mt, 4 * u + v, a[mt]);
+          for (int r = 0; r < 2; ++r) {
+            float &x = s[j][e][2 * r], &y = s[j][e][2 * r + 1];
+            if constexpr (kI8) {
+              x *= q_unit[j][r] * f[0];
+              y *= q_unit[j][r] * f[1];
+            } else {
+              x *= p.qscale;
+              y *= p.qscale;
+            }
+            if (!full) {
+              const uint32_t bits =
+                  seen_rows[(mg * MS + j) * 16 + gl + 8 * r].bits_from(x0) >> (2 * qi);
+              if (!(bits & 1)) x = -INFINITY;
+              if (!(bits & 2)) y = -INFINITY;
+            }
+            raise |= fmaxf(x, y) > m[j][r] + 8.f;
+            if constexpr (kI8)
+              raise |= fmaxf(fabsf(scale_v[e][0]), fabsf(scale_v[e][1])) * unit[j][r] > kMostUnits;
+          }
+      }
+    }
+    if (__syncthreads_or(raise)) {
+      // the rows' new maxima, agreed on through shared memory
+      if (scores) {
 #pragma unroll
-          for (int j = 0; j < NT; ++j) {
-            uint32_t b0, b1;
-            codes_to_bf16(v == 0 ? x[j].x : v == 1 ? x[j].y : v == 2 ? x[j].z : x[j].w, b0, b1);
+        for (int j = 0; j < MS; ++j)
 #pragma unroll
-            for (int mt = 0; mt < MT; ++mt)
-              mma16<false>(s[mt][j], a[mt][0], a[mt][1], a[mt][2], a[mt][3], b0, b1);
+          for (int r = 0; r < 2; ++r) {
+            float x = fmaxf(s[j][0][2 * r], s[j][0][2 * r + 1]);
+            if constexpr (KN == 2) x = fmaxf(x, fmaxf(s[j][1][2 * r], s[j][1][2 * r + 1]));
+            x = fmaxf(x, __shfl_xor_sync(kAllLanes, x, 1));
+            x = fmaxf(x, __shfl_xor_sync(kAllLanes, x, 2));
+            if (qi == 0) row_part[kg * M + (mg * MS + j) * 16 + gl + 8 * r] = x;
+            if constexpr (kI8) {
+              float top = -INFINITY;  // of weight x V scale
+#pragma unroll
+              for (int e = 0; e < KN; ++e)
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                  const float f = log2f(fabsf(scale_v[e][c]));
+                  if (f < 129.f) top = fmaxf(top, s[j][e][2 * r + c] + f);
+                }
+              top = fmaxf(top, __shfl_xor_sync(kAllLanes, top, 1));
+              top = fmaxf(top, __shfl_xor_sync(kAllLanes, top, 2));
+              if (qi == 0) row_top[kg * M + (mg * MS + j) * 16 + gl + 8 * r] = top;
+            }
+          }
+      }
+      __syncthreads();
+      if (tid < M) {
+        const float old = row_max[tid];
+        float x = old;
+#pragma unroll
+        for (int u = 0; u < KG; ++u) x = fmaxf(x, row_part[u * M + tid]);
+        row_max[tid] = x;
+        row_factor[tid] = old == -INFINITY ? 0.f : exp2f(old - x);
+        if constexpr (kI8) {
+          const float before = row_units[tid];
+          float top = fmaxf(before, x - 110.f);
+#pragma unroll
+          for (int u = 0; u < KG; ++u) top = fmaxf(top, row_top[u * M + tid] - 2.f);
+          row_units[tid] = top;
+          row_factor_o[tid] = before == -INFINITY ? 0.f : exp2f(before - top);
+        }
+      }
+      __syncthreads();
+      if (scores) {
+#pragma unroll
+        for (int j = 0; j < MS; ++j)
+#pragma unroll
+          for (int r = 0; r < 2; ++r) {
+            const int row = (mg * MS + j) * 16 + gl + 8 * r;
+            m[j][r] = row_max[row];
+            l[j][r] *= row_factor[row];
+            if constexpr (kI8) unit[j][r] = m[j][r] == -INFINITY ? 1.f : exp2f(m[j][r] - row_units[row]);
+          }
+      }
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+          const float a = (kI8 ? row_factor_o : row_factor)[mt * 16 + gl + 8 * r];
+#pragma unroll
+          for (int k = 0; k < NO; ++k) {
+            o[mt][k][2 * r] *= a;
+            o[mt][k][2 * r + 1] *= a;
+          }
+        }
+    }
+    // ---- P to shared memory, in the order in which the products below take the keys ----
+    if (scores) {
+#pragma unroll
+      for (int j = 0; j < MS; ++j)
+#pragma unroll
+        for (int r = 0; r < 2; ++r)
+#pragma unroll
+        for (int e = 0; e < KN; ++e) {
+          const int grp = kg * KN + e;
+          const int row = (mg * MS + j) * 16 + gl + 8 * r;
+          // scores of -inf carry no weight, even while they are all there is
+          const float mr = m[j][r] == -INFINITY ? 0.f : m[j][r];
+          float x = exp2f(s[j][e][2 * r] - mr), y = exp2f(s[j][e][2 * r + 1] - mr);
+          l[j][r] += x + y;
+          const uint32_t at = sp + row * Lay::kPRow;
+          if constexpr (kF32) {
+            // keys 2 t, 2 t + 1 of the group: columns t, t + 4
+            uint32_t h, lo;
+            split_tf32(x, h, lo);
+            sts32(at + (((2 * grp) ^ (row & 7)) << 4) + qi * 4, h);
+            sts32(at + Lay::kPPart + (((2 * grp) ^ (row & 7)) << 4) + qi * 4, lo);
+            split_tf32(y, h, lo);
+            sts32(at + (((2 * grp + 1) ^ (row & 7)) << 4) + qi * 4, h);
+            sts32(at + Lay::kPPart + (((2 * grp + 1) ^ (row & 7)) << 4) + qi * 4, lo);
+          } else {
+            int chunk = grp, col = qi * 4;
+            if constexpr (kI8) {
+              // keys 4 T + u of 16: columns 2 T + u, and 8 + 2 T + u - 2 from u = 2 on
+              x = x * unit[j][r] * scale_v[e][0];
+              y = y * unit[j][r] * scale_v[e][1];
+              chunk = 2 * (grp >> 1) + (qi & 1);
+              col = (2 * (grp & 1) + (qi >> 1)) * 4;
+            }
+            uint32_t h;
+            if constexpr (kI8) {
+              h = pack_f16x2(x, y);
+            } else if constexpr (!kTwoParts) {
+              h = pack_bf16x2(x, y);
+            } else {
+              h = below_bf16x2(x, y);
+              sts32(at + Lay::kPPart + ((chunk ^ (row & 7)) << 4) + col,
+                    pack_bf16x2(x - bf16_lo(h), y - bf16_hi(h)));
+            }
+            sts32(at + ((chunk ^ (row & 7)) << 4) + col, h);
+          }
+        }
+    }
+    __syncthreads();
+
+    // ---- O += P V: every warp all keys, D / 8 of the dims ----
+    if constexpr (!kF32) {
+#pragma unroll
+      for (int k = 0; k < KT / 16; ++k) {
+        uint32_t b[NO][2];
+        if constexpr (kI8) {
+          uint32_t r0, r1;
+          ldsm_b8_t(r0, r1, sv + Tl::at(k * 16 + (lane & 15), NO == 2 ? warp : warp >> 1));
+          if constexpr (NO == 2) {
+            codes_to_f16(r0, b[0][0], b[0][1]);
+            codes_to_f16(r1, b[1][0], b[1][1]);
+          } else {
+            codes_to_f16(warp & 1 ? r1 : r0, b[0][0], b[0][1]);
+          }
+        } else if constexpr (NO == 2) {
+          uint32_t v[4];
+          ldsm_x4_t(v, sv + Tl::at(k * 16 + (lane & 7) + ((lane >> 3) & 1) * 8, 2 * warp + (lane >> 4)));
+          b[0][0] = v[0]; b[0][1] = v[1]; b[1][0] = v[2]; b[1][1] = v[3];
+        } else {
+          ldsm_x2_t(b[0][0], b[0][1], sv + Tl::at(k * 16 + (lane & 15), warp));
+        }
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt) {
+          uint32_t a[4];
+          a_frag(sp, Lay::kPRow, mt, k, a);
+#pragma unroll
+          for (int u = 0; u < NO; ++u) mma16<kI8>(o[mt][u], a[0], a[1], a[2], a[3], b[u][0], b[u][1]);
+          if constexpr (kTwoParts) {
+            a_frag(sp + Lay::kPPart, Lay::kPRow, mt, k, a);
+#pragma unroll
+            for (int u = 0; u < NO; ++u)
+              mma16<false>(o[mt][u], a[0], a[1], a[2], a[3], b[u][0], b[u][1]);
           }
         }
       }
     } else {
-      float big[MT][NT][4];
+      // dims NO column + u of the warp's output tile u
+      float acc[MT][NO][4], big[MT][NO][4];
 #pragma unroll
       for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-        for (int j = 0; j < NT; ++j)
+        for (int u = 0; u < NO; ++u)
 #pragma unroll
-          for (int c = 0; c < 4; ++c) big[mt][j][c] = 0.f;
+          for (int c = 0; c < 4; ++c) acc[mt][u][c] = big[mt][u][c] = 0.f;
 #pragma unroll
-      for (int k = 0; k < KS; k += 2) {
-        uint32_t bh[NT][4], bl[NT][4];
+      for (int k = 0; k < KT / 8; ++k) {
+        uint32_t h[NO][2], lo[NO][2];
 #pragma unroll
-        for (int j = 0; j < NT; ++j) {
-          const uint4 x = lds128(st + Tl::at(k0 + j * 8 + gl, 2 * k + qi));
-          split_tf32(__uint_as_float(x.x), bh[j][0], bl[j][0]);
-          split_tf32(__uint_as_float(x.y), bh[j][1], bl[j][1]);
-          split_tf32(__uint_as_float(x.z), bh[j][2], bl[j][2]);
-          split_tf32(__uint_as_float(x.w), bh[j][3], bl[j][3]);
+        for (int c = 0; c < 2; ++c) {
+          const int r = k * 8 + 2 * qi + c, byte = (warp * NO * 8 + gl * NO) * 4;
+          const uint32_t at = sv + Tl::at(r, byte >> 4) + (byte & 15);
+          if constexpr (NO == 2) {
+            const float2 x = lds_f32x2(at);
+            split_tf32(x.x, h[0][c], lo[0][c]);
+            split_tf32(x.y, h[1][c], lo[1][c]);
+          } else {
+            split_tf32(lds_f32(at), h[0][c], lo[0][c]);
+          }
         }
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt) {
-          uint32_t ah[2][4], al[2][4];
-          q_frag_tf32(mt, k, ah, al);
+          uint32_t ah[4], al[4];
+          a_frag(sp, Lay::kPRow, mt, k, ah);
+          a_frag(sp + Lay::kPPart, Lay::kPRow, mt, k, al);
 #pragma unroll
-          for (int u = 0; u < 2; ++u)
-#pragma unroll
-            for (int j = 0; j < NT; ++j) {
-              mma8_tf32(s[mt][j], al[u], bh[j][2 * u], bh[j][2 * u + 1]);
-              mma8_tf32(s[mt][j], ah[u], bl[j][2 * u], bl[j][2 * u + 1]);
-              mma8_tf32(big[mt][j], ah[u], bh[j][2 * u], bh[j][2 * u + 1]);
-            }
+          for (int u = 0; u < NO; ++u) {
+            mma8_tf32(acc[mt][u], al, h[u][0], h[u][1]);
+            mma8_tf32(acc[mt][u], ah, lo[u][0], lo[u][1]);
+            mma8_tf32(big[mt][u], ah, h[u][0], h[u][1]);
+          }
         }
       }
 #pragma unroll
       for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-        for (int j = 0; j < NT; ++j)
+        for (int u = 0; u < NO; ++u)
 #pragma unroll
-          for (int c = 0; c < 4; ++c) s[mt][j][c] += big[mt][j][c];
+          for (int c = 0; c < 4; ++c) o[mt][u][c] += acc[mt][u][c] + big[mt][u][c];
     }
+  }
+  cp_wait<0>();
 
-    // ---- softmax ----
-    // key of column c (0, 1) of score tile j, within the warp's keys
-    auto key = [&](int j, int c) {
-      if constexpr (kI8) return (j >> 1) * 16 + 4 * qi + (j & 1) * 2 + c;
-      return j * 8 + 2 * qi + c;
-    };
-    const int p0 = i * KT + k0;
-    const bool full = p0 >= full_lo && p0 + KW - 1 <= full_hi;
-    [[maybe_unused]] float factor[NT][2], scale_v[NT][2];
-    if constexpr (kI8) {
+  // ---- the rows' sums ----
+  if (scores) {
 #pragma unroll
-      for (int j = 0; j < NT; ++j)
+    for (int j = 0; j < MS; ++j)
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          const uint32_t sc = st + 2 * Tl::kHalf + (k0 + key(j, c)) * 16 + (4 * w.g & 15);
-          factor[j][c] = p.qscale * lds_f32(sc);
-          scale_v[j][c] = lds_f32(sc + KT * 16);
-        }
-    }
-    float a[MT][2];
+      for (int r = 0; r < 2; ++r) {
+        float x = l[j][r];
+        x += __shfl_xor_sync(kAllLanes, x, 1);
+        x += __shfl_xor_sync(kAllLanes, x, 2);
+        if (qi == 0) row_part[kg * M + (mg * MS + j) * 16 + gl + 8 * r] = x;
+      }
+  }
+  __syncthreads();
+  if (tid < M) {
+    float x = 0.f;
+#pragma unroll
+    for (int u = 0; u < KG; ++u) x += row_part[u * M + tid];
+    row_sum[tid] = x;
+  }
+  __syncthreads();
+  if constexpr (kI8) {  // O in units of 1
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
       for (int r = 0; r < 2; ++r) {
-        float mx = -INFINITY;
+        const int row = mt * 16 + gl + 8 * r;
+        const float a = row_max[row] == -INFINITY ? 1.f : exp2f(row_units[row] - row_max[row]);
 #pragma unroll
-        for (int j = 0; j < NT; ++j)
-#pragma unroll
-          for (int c = 0; c < 2; ++c) s[mt][j][2 * r + c] *= kI8 ? factor[j][c] : p.qscale;
-        if (!full) {
-          const uint32_t bits = seen_rows[mt * 16 + gl + 8 * r].bits_from(p0) >> key(0, 0);
-#pragma unroll
-          for (int j = 0; j < NT; ++j)
-#pragma unroll
-            for (int c = 0; c < 2; ++c)
-              if (!(bits >> (key(j, c) - key(0, 0)) & 1)) s[mt][j][2 * r + c] = -INFINITY;
-        }
-#pragma unroll
-        for (int j = 0; j < NT; ++j)
-#pragma unroll
-          for (int c = 0; c < 2; ++c) mx = fmaxf(mx, s[mt][j][2 * r + c]);
-        a[mt][r] = 1.f;
-        // the running maximum moves only where some lane passes it
-        if (__any_sync(kAllLanes, mx > m[mt][r])) {
-          mx = fmaxf(mx, __shfl_xor_sync(kAllLanes, mx, 1));
-          mx = fmaxf(mx, __shfl_xor_sync(kAllLanes, mx, 2));
-          const float top_m = fmaxf(m[mt][r], mx);
-          a[mt][r] = m[mt][r] == -INFINITY ? 0.f : exp2f(m[mt][r] - top_m);
-          m[mt][r] = top_m;
-        }
-        // scores of -inf carry no weight, even while they are all there is
-        const float base_m = m[mt][r] == -INFINITY ? 0.f : m[mt][r];
-        float sum = 0.f;
-#pragma unroll
-        for (int j = 0; j < NT; ++j)
-#pragma unroll
-          for (int c = 0; c < 2; ++c) {
-            const float e = exp2f(s[mt][j][2 * r + c] - base_m);
-            sum += e;
-            s[mt][j][2 * r + c] = e;
-            if constexpr (kI8) s[mt][j][2 * r + c] = e * scale_v[j][c];
-          }
-        l[mt][r] = l[mt][r] * a[mt][r] + sum;
-      }
-    if constexpr (!kF32) {
-#pragma unroll
-      for (int mt = 0; mt < MT; ++mt)
-        if (__any_sync(kAllLanes, a[mt][0] != 1.f || a[mt][1] != 1.f)) {
-#pragma unroll
-          for (int k = 0; k < NO; ++k) {
-            o[mt][k][0] *= a[mt][0];
-            o[mt][k][1] *= a[mt][0];
-            o[mt][k][2] *= a[mt][1];
-            o[mt][k][3] *= a[mt][1];
-          }
-        }
-    }
-
-    // ---- O += P V ----
-    if constexpr (!kF32) {
-      uint32_t ph[MT][NT / 2][4];
-      [[maybe_unused]] uint32_t pl[MT][NT / 2][4];
-#pragma unroll
-      for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-        for (int j = 0; j < NT / 2; ++j)
-#pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            const float x = s[mt][2 * j + (c >> 1)][2 * (c & 1)];
-            const float y = s[mt][2 * j + (c >> 1)][2 * (c & 1) + 1];
-            if constexpr (!kTwoParts) {
-              ph[mt][j][c] = pack_bf16x2(x, y);
-            } else {
-              if constexpr (kI8) {  // (infinite products: what the finite part leaves is infinite)
-                constexpr float kMost = 3.38953139e38f;
-                ph[mt][j][c] =
-                    pack_bf16x2(fminf(fmaxf(x, -kMost), kMost), fminf(fmaxf(y, -kMost), kMost));
-              } else {
-                ph[mt][j][c] = below_bf16x2(x, y);
-              }
-              pl[mt][j][c] = pack_bf16x2(x - bf16_lo(ph[mt][j][c]), y - bf16_hi(ph[mt][j][c]));
-            }
-          }
-      // two output tiles' worth of one V operand
-      auto add = [&](int j, int k, uint32_t b0, uint32_t b1) {
-#pragma unroll
-        for (int mt = 0; mt < MT; ++mt) {
-          mma16<false>(o[mt][k], ph[mt][j][0], ph[mt][j][1], ph[mt][j][2], ph[mt][j][3], b0, b1);
-          if constexpr (kTwoParts)
-            mma16<false>(o[mt][k], pl[mt][j][0], pl[mt][j][1], pl[mt][j][2], pl[mt][j][3], b0, b1);
-        }
-      };
-      if constexpr (kI8) {
-#pragma unroll
-        for (int k = 0; k < NO; k += 2)
-#pragma unroll
-          for (int j = 0; j < NT / 2; ++j) {
-            uint32_t r0, r1, b0, b1, b2, b3;
-            ldsm_b8_t(r0, r1, sv + Tl::at(k0 + j * 16 + (lane & 15), k / 2));
-            codes_to_bf16(r0, b0, b1);
-            codes_to_bf16(r1, b2, b3);
-            add(j, k, b0, b1);
-            add(j, k + 1, b2, b3);
-          }
-      } else {
-        const int r = k0 + (lane & 7) + ((lane >> 3) & 1) * 8, cc = lane >> 4;
-#pragma unroll
-        for (int j = 0; j < NT / 2; ++j)
-#pragma unroll
-          for (int k = 0; k < NO; k += 2) {
-            uint32_t b[4];
-            ldsm_x4_t(b, sv + Tl::at(r + j * 16, k + cc));
-            add(j, k, b[0], b[1]);
-            add(j, k + 1, b[2], b[3]);
-          }
-      }
-    } else {
-      uint32_t ph[MT][NT][4], pl[MT][NT][4];  // columns qi, qi + 4 of a step: keys 2 qi, 2 qi + 1
-#pragma unroll
-      for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-        for (int j = 0; j < NT; ++j) {
-          split_tf32(s[mt][j][0], ph[mt][j][0], pl[mt][j][0]);
-          split_tf32(s[mt][j][2], ph[mt][j][1], pl[mt][j][1]);
-          split_tf32(s[mt][j][1], ph[mt][j][2], pl[mt][j][2]);
-          split_tf32(s[mt][j][3], ph[mt][j][3], pl[mt][j][3]);
-        }
-      // dims 32 q + 4 column + u of the four output tiles 4 q + u
-#pragma unroll
-      for (int q = 0; q < D / 32; ++q) {
-        uint4 x[NT], y[NT];
-#pragma unroll
-        for (int j = 0; j < NT; ++j) {
-          x[j] = lds128(sv + Tl::at(k0 + j * 8 + 2 * qi, 8 * q + gl));
-          y[j] = lds128(sv + Tl::at(k0 + j * 8 + 2 * qi + 1, 8 * q + gl));
-        }
-#pragma unroll
-        for (int u = 0; u < 4; ++u) {
-          float acc[MT][4], big[MT][4];
-#pragma unroll
-          for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-            for (int c = 0; c < 4; ++c) acc[mt][c] = big[mt][c] = 0.f;
-#pragma unroll
-          for (int j = 0; j < NT; ++j) {
-            uint32_t h0, l0, h1, l1;
-            split_tf32(__uint_as_float(u == 0 ? x[j].x : u == 1 ? x[j].y : u == 2 ? x[j].z : x[j].w),
-                       h0, l0);
-            split_tf32(__uint_as_float(u == 0 ? y[j].x : u == 1 ? y[j].y : u == 2 ? y[j].z : y[j].w),
-                       h1, l1);
-#pragma unroll
-            for (int mt = 0; mt < MT; ++mt) {
-              mma8_tf32(acc[mt], pl[mt][j], h0, h1);
-              mma8_tf32(acc[mt], ph[mt][j], l0, l1);
-              mma8_tf32(big[mt], ph[mt][j], h0, h1);
-            }
-          }
-#pragma unroll
-          for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-            for (int c = 0; c < 4; ++c)
-              o[mt][4 * q + u][c] =
-                  fmaf(o[mt][4 * q + u][c], a[mt][c >> 1], acc[mt][c] + big[mt][c]);
+        for (int k = 0; k < NO; ++k) {
+          o[mt][k][2 * r] *= a;
+          o[mt][k][2 * r + 1] *= a;
         }
       }
-    }
   }
-  cp_wait<0>();
-  __syncthreads();
-
-  // four dims of a row's result
-  auto finish = [&](int r, int d, float sum, const float (&x)[4]) {
+  // N dims from d on of row r's result
+  auto finish = [&](int r, int d, float sum, const auto& x) {
+    constexpr int N = sizeof(x) / sizeof(x[0]);
     const float inv = sum == 0.f ? 0.f : 1.f / sum;  // no weight at all: zeros
     const int tok = r / G;
     const long long at = ((w.s.q0 + tok) * p.hq + w.g * G + (r - tok * G)) * D + d;
-    if constexpr (kF32) {
-      *reinterpret_cast<float4*>(p.out + at * 4) =
-          make_float4(x[0] * inv, x[1] * inv, x[2] * inv, x[3] * inv);
-    } else {
-      *reinterpret_cast<uint2*>(p.out + at * 2) =
-          make_uint2(pack_bf16x2(x[0] * inv, x[1] * inv), pack_bf16x2(x[2] * inv, x[3] * inv));
+    bool finite = true;
+#pragma unroll
+    for (int e = 0; e < N; e += 2) {
+      if constexpr (kF32)
+        *reinterpret_cast<float2*>(p.out + (at + e) * 4) = make_float2(x[e] * inv, x[e + 1] * inv);
+      else
+        *reinterpret_cast<uint32_t*>(p.out + (at + e) * 2) = pack_bf16x2(x[e] * inv, x[e + 1] * inv);
+      finite &= !nonfinite(x[e]) && !nonfinite(x[e + 1]);
     }
-    if ((nonfinite(x[0]) || nonfinite(x[1]) || nonfinite(x[2]) || nonfinite(x[3])) && !nonfinite(sum))
-      repair_query<4>(p.repair, w.b, tok, w.g * G + (r - tok * G), d, 4);
+    if (!finite && !nonfinite(sum))
+      repair_query<4>(p.repair, w.b, tok, w.g * G + (r - tok * G), d, N);
   };
-
-  // ---- the states to shared memory, and their merge ----
-  float* acc = reinterpret_cast<float*>(smem);
-  float* ml = acc + kRowsWarps * 16 * MT * Lay::kAccRow;
+  // this warp's values of a row: dim(u, c) is column c of output tile u
+  auto dim = [&](int u, int c) {
+    if constexpr (kF32) return warp * NO * 8 + (2 * qi + c) * NO + u;
+    return warp * NO * 8 + u * 8 + 2 * qi + c;
+  };
+  const bool cluster = !TREE && ctas > 1;
+  float* acc = reinterpret_cast<float*>(smem);  // a cluster: [M][kAccRow], over the ring
+  float2* state = reinterpret_cast<float2*>(acc + M * Lay::kAccRow);
 #pragma unroll
   for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-    for (int r = 0; r < 2; ++r) {
-      float sum = l[mt][r];
-      sum += __shfl_xor_sync(kAllLanes, sum, 1);
-      sum += __shfl_xor_sync(kAllLanes, sum, 2);
-      const int row = wk * M + wr * 16 * MT + mt * 16 + gl + 8 * r;
-      if (qi == 0) {
-        ml[2 * row] = m[mt][r];
-        ml[2 * row + 1] = sum;
-      }
+    for (int r8 = 0; r8 < 2; ++r8) {
+      const int row = mt * 16 + gl + 8 * r8, r = w.first_row + row;
+      if (r >= rows) continue;
+      float* dst = cluster ? acc + row * Lay::kAccRow : w.part ? w.part + (long long)row * (D + 4) + 4 : nullptr;
+      if (dst) {
 #pragma unroll
-      for (int k = 0; k < NO; ++k) {
-        if constexpr (kF32) {
-          acc[row * Lay::kAccRow + (k >> 2) * 32 + 8 * qi + (k & 3)] = o[mt][k][2 * r];
-          acc[row * Lay::kAccRow + (k >> 2) * 32 + 8 * qi + 4 + (k & 3)] = o[mt][k][2 * r + 1];
-        } else {
-          *reinterpret_cast<float2*>(acc + row * Lay::kAccRow + k * 8 + 2 * qi) =
-              make_float2(o[mt][k][2 * r], o[mt][k][2 * r + 1]);
+        for (int u = 0; u < NO; ++u)
+#pragma unroll
+          for (int c = 0; c < 2; ++c) dst[dim(u, c)] = o[mt][u][2 * r8 + c];
+      } else if constexpr (kF32 && NO == 2) {
+        const float x[4] = {o[mt][0][2 * r8], o[mt][1][2 * r8], o[mt][0][2 * r8 + 1],
+                            o[mt][1][2 * r8 + 1]};
+        finish(r, dim(0, 0), row_sum[row], x);
+      } else {
+#pragma unroll
+        for (int u = 0; u < NO; ++u) {
+          const float x[2] = {o[mt][u][2 * r8], o[mt][u][2 * r8 + 1]};
+          finish(r, dim(u, 0), row_sum[row], x);
         }
       }
     }
-  __syncthreads();
+  if (w.part && tid < M && w.first_row + tid < rows)
+    *reinterpret_cast<float2*>(w.part + (long long)tid * (D + 4)) =
+        make_float2(row_max[tid], row_sum[tid]);
   if constexpr (!TREE) {
     // prefill: a cluster's CTAs share the unit's tiles, and its rows in their merge
     if (ctas > 1) {
+      if (tid < M) state[tid] = make_float2(row_max[tid], row_sum[tid]);
       cluster_sync();
       const uint32_t rank = cluster_rank();
       for (int e = (int)rank * kRowsThreads + tid; e < M * (D / 4); e += ctas * kRowsThreads) {
         const int row = e / (D / 4), d = e % (D / 4) * 4, r = w.first_row + row;
         if (r >= rows) break;
-        float top_m = -INFINITY, sum = 0.f, x[4] = {0.f, 0.f, 0.f, 0.f};
-        for (int c = 0; c < ctas; ++c) {
-          const uint32_t ml_c = cluster_map(smem_addr(ml), c), acc_c = cluster_map(base, c);
-          float2 s[WK];
-          float4 y[WK];
+        float top = -INFINITY, sum = 0.f, x[4] = {0.f, 0.f, 0.f, 0.f};
+        float2 ml[kRowsMaxCluster];
+        float4 y[kRowsMaxCluster];
 #pragma unroll
-          for (int u = 0; u < WK; ++u) {
-            s[u] = ld_cluster_f32x2(ml_c + (u * M + row) * 8);
-            y[u] = ld_cluster_f32x4(acc_c + ((u * M + row) * Lay::kAccRow + d) * 4);
+        for (int c = 0; c < kRowsMaxCluster; ++c) {
+          ml[c] = make_float2(-INFINITY, 0.f);
+          y[c] = make_float4(0.f, 0.f, 0.f, 0.f);
+          if (c < ctas) {
+            ml[c] = ld_cluster_f32x2(cluster_map(smem_addr(state + row), c));
+            y[c] = ld_cluster_f32x4(cluster_map(smem_addr(acc + row * Lay::kAccRow + d), c));
           }
-          float most = top_m;
+          top = fmaxf(top, ml[c].x);
+        }
 #pragma unroll
-          for (int u = 0; u < WK; ++u) most = fmaxf(most, s[u].x);
-          const float shrink = most == top_m ? 1.f : exp2f(top_m - most);
-          top_m = most;
-          sum *= shrink;
-#pragma unroll
-          for (int k = 0; k < 4; ++k) x[k] *= shrink;
-#pragma unroll
-          for (int u = 0; u < WK; ++u) {
-            // a state at -inf saw nothing, or only NaN: its sum and O are 0, or NaN
-            const float f = s[u].x == -INFINITY ? 1.f : exp2f(s[u].x - top_m);
-            sum += f * s[u].y;
-            x[0] += f * y[u].x;
-            x[1] += f * y[u].y;
-            x[2] += f * y[u].z;
-            x[3] += f * y[u].w;
-          }
+        for (int c = 0; c < kRowsMaxCluster; ++c) {
+          // a state at -inf saw nothing, or only NaN: its sum and O are 0, or NaN
+          const float f = ml[c].x == -INFINITY ? 1.f : exp2f(ml[c].x - top);
+          sum += f * ml[c].y;
+          x[0] += f * y[c].x;
+          x[1] += f * y[c].y;
+          x[2] += f * y[c].z;
+          x[3] += f * y[c].w;
         }
         finish(r, d, sum, x);
       }
@@ -722,63 +781,51 @@ __device__ __forceinline__ void rows_piece(const RowsParams& p, const RowsPiece&
       return;
     }
   }
-  // four dims a thread
-  for (int e = tid; e < M * (D / 4); e += kRowsThreads) {
-    const int row = e / (D / 4), d = e % (D / 4) * 4, r = w.first_row + row;
-    if (r >= rows) break;
-    float top_m = -INFINITY;
-#pragma unroll
-    for (int u = 0; u < WK; ++u) top_m = fmaxf(top_m, ml[2 * (u * M + row)]);
-    float sum = 0.f, x[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-    for (int u = 0; u < WK; ++u) {
-      const float mu = ml[2 * (u * M + row)];
-      // a state at -inf saw nothing, or only NaN: its sum and O are 0, or NaN
-      const float f = mu == -INFINITY ? 1.f : exp2f(mu - top_m);
-      sum += f * ml[2 * (u * M + row) + 1];
-      const float4 y = *reinterpret_cast<const float4*>(acc + (u * M + row) * Lay::kAccRow + d);
-      x[0] += f * y.x;
-      x[1] += f * y.y;
-      x[2] += f * y.z;
-      x[3] += f * y.w;
-    }
-    if (w.part) {
-      float* dst = w.part + (long long)row * (D + 4);
-      *reinterpret_cast<float4*>(dst + 4 + d) = make_float4(x[0], x[1], x[2], x[3]);
-      if (d == 0) *reinterpret_cast<float2*>(dst) = make_float2(top_m, sum);
-      continue;
-    }
-    finish(r, d, sum, x);
-  }
   __syncthreads();  // before the ring is filled again
 }
 
 // Tree: the batch's tiles split evenly over the grid (span.cuh).
-template <int MODE, int D, int MT, int RG>
-__global__ void __launch_bounds__(kRowsThreads, (RowsLayout<MODE, D, MT, RG>::kCtas))
+template <int MODE, int D, int M>
+__global__ void __launch_bounds__(kRowsThreads, (RowsLayout<MODE, D, M>::kCtas))
     rows_tree_kernel(const __grid_constant__ RowsParams p) {
-  constexpr int KT = RowsTile<MODE, D>::kKeys, M = RowsLayout<MODE, D, MT, RG>::kRows;
+  constexpr int KT = RowsTile<MODE, D, M>::kKeys;
   extern __shared__ __align__(128) unsigned char smem[];
   __shared__ long long scratch[32];
   griddep_wait();
   griddep_launch_dependents();
   const PlanShare share = plan_share<KT>(p.plan, blockIdx.x, gridDim.x, scratch);
-  long long at = share.at, first = share.first;
-  const long long end = share.end;
-  int b = share.b;
+  // where the CTA is, kept in shared memory: registers that a piece's work wants for itself
+  volatile long long* line = scratch;  // at, first, end, b
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    line[0] = share.at;
+    line[1] = share.first;
+    line[2] = share.end;
+    line[3] = share.b;
+  }
+  __syncthreads();
   if (blockIdx.x == 0) {
     for (int i = threadIdx.x; i < p.plan.span.batch; i += blockDim.x)
       if (seq_span(p.plan.span, i).bad) set_error(p.err, kErrCapacity);
   }
-  while (at < end) {
-    const SeqPlan q = seq_plan<KT>(p.plan, b);
-    if (at >= first + q.all_steps) {  // the next sequence
+  for (;;) {
+    long long at = line[0], first = line[1];
+    const long long end = line[2];
+    int b = (int)line[3];
+    if (at >= end) break;
+    SeqPlan q = seq_plan<KT>(p.plan, b);
+    while (at >= first + q.all_steps) {  // the next sequence
       first += q.all_steps;
-      ++b;
-      continue;
+      q = seq_plan<KT>(p.plan, ++b);
     }
     const PlanPart part = plan_part(p.plan, q, at - first, end - at);
-    at += part.steps;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+      line[0] = at + part.steps;
+      line[1] = first;
+      line[3] = b;
+    }
+    __syncthreads();
     if (part.t0 == part.t1) continue;
     RowsPiece w;
     w.s = q.s;
@@ -793,16 +840,16 @@ __global__ void __launch_bounds__(kRowsThreads, (RowsLayout<MODE, D, MT, RG>::kC
     w.part = nullptr;
     if (w.t0 > 0 || w.t1 < q.t.nt)
       w.part = p.part + (2ll * blockIdx.x + (w.t0 == 0 ? 1 : 0)) * (M * (D + 4));
-    rows_piece<MODE, D, MT, RG, true>(p, w, 1, smem);
+    rows_piece<MODE, D, M, true>(p, w, 1, smem);
   }
 }
 
 // Prefill: a unit a cluster of CTAs, which take its tiles in turns of equal length; the last
 // rows' units first.
-template <int MODE, int D, int MT, int RG>
-__global__ void __launch_bounds__(kRowsThreads, (RowsLayout<MODE, D, MT, RG>::kCtas))
+template <int MODE, int D, int M>
+__global__ void __launch_bounds__(kRowsThreads, (RowsLayout<MODE, D, M>::kCtas))
     rows_prefill_kernel(const __grid_constant__ RowsParams p) {
-  constexpr int KT = RowsTile<MODE, D>::kKeys, M = RowsLayout<MODE, D, MT, RG>::kRows;
+  constexpr int KT = RowsTile<MODE, D, M>::kKeys;
   extern __shared__ __align__(128) unsigned char smem[];
   griddep_wait();
   griddep_launch_dependents();
@@ -826,14 +873,14 @@ __global__ void __launch_bounds__(kRowsThreads, (RowsLayout<MODE, D, MT, RG>::kC
   w.t0 = (int)((long long)w.t.nt * rank / ctas);
   w.t1 = (int)((long long)w.t.nt * (rank + 1) / ctas);
   w.part = nullptr;
-  rows_piece<MODE, D, MT, RG, false>(p, w, (int)ctas, smem);
+  rows_piece<MODE, D, M, false>(p, w, (int)ctas, smem);
 }
 
-template <int MODE, int D, int MT, int RG>
+template <int MODE, int D, int M>
 cudaError_t launch_tree_as(const RowsParams& p, long long grid, int dev, cudaStream_t s) {
   static std::atomic<int> allowed[kDevices];
-  const auto kern = rows_tree_kernel<MODE, D, MT, RG>;
-  constexpr size_t smem = RowsLayout<MODE, D, MT, RG>::kSmem;
+  const auto kern = rows_tree_kernel<MODE, D, M>;
+  constexpr size_t smem = RowsLayout<MODE, D, M>::kSmem;
   const cudaError_t e = allow_shared(kern, smem, allowed[dev]);
   if (e != cudaSuccess) return e;
   return launch_kernel(kern, dim3((unsigned)grid), dim3(kRowsThreads), smem, s, true, p);
@@ -841,15 +888,15 @@ cudaError_t launch_tree_as(const RowsParams& p, long long grid, int dev, cudaStr
 
 // Clusters of as many CTAs as the device holds at once beside one another, with two tiles each
 // or more.
-template <int MODE, int D, int MT, int RG>
+template <int MODE, int D, int M>
 cudaError_t launch_prefill_as(const RowsParams& p, int dev, cudaStream_t s) {
   static std::atomic<int> allowed[kDevices], known[kDevices][kRowsMaxCluster + 1];
-  using Lay = RowsLayout<MODE, D, MT, RG>;
-  const auto kern = rows_prefill_kernel<MODE, D, MT, RG>;
+  using Lay = RowsLayout<MODE, D, M>;
+  const auto kern = rows_prefill_kernel<MODE, D, M>;
   cudaError_t e = allow_shared(kern, Lay::kSmem, allowed[dev]);
   if (e != cudaSuccess) return e;
   const long long units = (long long)p.units_max * p.plan.span.batch * p.plan.hkv;
-  const long long tiles = (p.keys_most + RowsTile<MODE, D>::kKeys - 1) / RowsTile<MODE, D>::kKeys + 1;
+  const long long tiles = (p.keys_most + RowsTile<MODE, D, M>::kKeys - 1) / RowsTile<MODE, D, M>::kKeys + 1;
   int ctas = 1;
   for (int c = kRowsMaxCluster; c > 1; c >>= 1) {
     int held = 0;
@@ -867,33 +914,30 @@ cudaError_t launch_prefill_as(const RowsParams& p, int dev, cudaStream_t s) {
                          (unsigned)ctas, s, p);
 }
 
-// Units of 16, 32 or 64 rows.  A warp holds two row tiles where its registers allow: what it
-// reads and converts of K and V then serves both.
+// Units of 16, 32 or 64 rows (fp32 with head_dim 128: up to 32, whose Q in two parts fits).
 template <int MODE, int D>
-struct RowsShapes {
-  static constexpr int kMT = MODE == PKV_F32 && D == 128 ? 1 : 2;
-  using R16 = RowsLayout<MODE, D, 1, 1>;
-  using R32 = RowsLayout<MODE, D, kMT, 2 / kMT>;
-  using R64 = RowsLayout<MODE, D, kMT, 4 / kMT>;
-};
+constexpr int rows_most() {
+  return MODE == PKV_F32 && D == 128 ? 32 : 64;
+}
 
 template <int MODE, int D>
 cudaError_t launch_rows_d(const RowsParams& p, bool tree, long long grid, int dev, cudaStream_t s) {
-  constexpr int MT = RowsShapes<MODE, D>::kMT;
+  constexpr int kMost = rows_most<MODE, D>();
   const int rows = p.plan.unit_rows;
   if (tree)
-    return rows == 16   ? launch_tree_as<MODE, D, 1, 1>(p, grid, dev, s)
-           : rows == 32 ? launch_tree_as<MODE, D, MT, 2 / MT>(p, grid, dev, s)
-                        : launch_tree_as<MODE, D, MT, 4 / MT>(p, grid, dev, s);
-  return rows == 16   ? launch_prefill_as<MODE, D, 1, 1>(p, dev, s)
-         : rows == 32 ? launch_prefill_as<MODE, D, MT, 2 / MT>(p, dev, s)
-                      : launch_prefill_as<MODE, D, MT, 4 / MT>(p, dev, s);
+    return rows == 16   ? launch_tree_as<MODE, D, 16>(p, grid, dev, s)
+           : rows == 32 ? launch_tree_as<MODE, D, 32>(p, grid, dev, s)
+                        : launch_tree_as<MODE, D, kMost>(p, grid, dev, s);
+  return rows == 16   ? launch_prefill_as<MODE, D, 16>(p, dev, s)
+         : rows == 32 ? launch_prefill_as<MODE, D, 32>(p, dev, s)
+                      : launch_prefill_as<MODE, D, kMost>(p, dev, s);
 }
 
 template <int MODE, int D>
 constexpr int rows_ctas_d(int unit_rows) {
-  using S = RowsShapes<MODE, D>;
-  return unit_rows == 16 ? S::R16::kCtas : unit_rows == 32 ? S::R32::kCtas : S::R64::kCtas;
+  return unit_rows == 16   ? RowsLayout<MODE, D, 16>::kCtas
+         : unit_rows == 32 ? RowsLayout<MODE, D, 32>::kCtas
+                           : RowsLayout<MODE, D, rows_most<MODE, D>()>::kCtas;
 }
 
 }  // namespace

@@ -46,8 +46,6 @@
 #include <cmath>
 #include <type_traits>
 
-#include <cuda_fp16.h>
-
 #include "cluster.cuh"
 #include "common.cuh"
 #include "mma.cuh"
@@ -104,11 +102,6 @@ __device__ __forceinline__ uint32_t movmatrix_t(uint32_t x) {
   asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
   return r;
 }
-__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
-  uint32_t r;
-  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-  return r;
-}
 // The nearest finite fp16 of each: what an infinite product leaves is infinite.
 __device__ __forceinline__ uint32_t pack_f16x2_finite(float lo, float hi) {
   uint32_t r;
@@ -118,18 +111,6 @@ __device__ __forceinline__ uint32_t pack_f16x2_finite(float lo, float hi) {
 __device__ __forceinline__ float2 unpack_f16x2(uint32_t w) {
   return __half22float2(*reinterpret_cast<const __half2*>(&w));
 }
-// Four codes (bytes c + 128) to fp16 pairs: 1024 + byte, minus 1152.
-__device__ __forceinline__ void codes_to_f16(uint32_t w, uint32_t& lo, uint32_t& hi) {
-  uint32_t a, b;
-  asm("prmt.b32 %0, %1, 0x64646464, 0x4140;" : "=r"(a) : "r"(w));
-  asm("prmt.b32 %0, %1, 0x64646464, 0x4342;" : "=r"(b) : "r"(w));
-  const __half2 bias = __half2half2(__ushort_as_half(0x6480));
-  const __half2 x = __hsub2(*reinterpret_cast<const __half2*>(&a), bias);
-  const __half2 y = __hsub2(*reinterpret_cast<const __half2*>(&b), bias);
-  lo = *reinterpret_cast<const uint32_t*>(&x);
-  hi = *reinterpret_cast<const uint32_t*>(&y);
-}
-
 // ---- staging -------------------------------------------------------------------
 
 // One tile in a warp's ring: K rows, V rows, and for int8 pools their scales.

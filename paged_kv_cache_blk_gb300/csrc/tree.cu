@@ -127,6 +127,12 @@ __global__ void validate_spans_kernel(const SpanParams p, const int32_t* bt, lon
   }
 }
 
+// Rows of a unit of the mma.sync kernels, where a sequence has up to `rows` of a kv head.
+int rows_unit(const PoolView& v, int64_t rows) {
+  const int most = v.io_size == 4 && v.head_dim == 128 ? 32 : 64;
+  return rows <= 16 ? 16 : rows <= 32 ? 32 : most;
+}
+
 // How a tree call runs: units of unit_rows rows, split over `grid` CTAs.
 struct TreePath {
   bool tcgen05;
@@ -145,7 +151,7 @@ TreePath tree_path(const PoolView& v, int G, int max_q_len, int sms) {
     t.bytes = (size_t)2 * t.grid * t.unit_rows * (v.head_dim + 4) * 4;
     return t;
   }
-  t.unit_rows = rows <= 16 ? 16 : rows <= 32 ? 32 : 64;
+  t.unit_rows = rows_unit(v, rows);
   const int ctas = v.quant          ? rows_ctas_i8(v.head_dim, t.unit_rows)
                    : v.io_size == 2 ? rows_ctas_bf16(v.head_dim, t.unit_rows)
                                     : rows_ctas_f32(v.head_dim, t.unit_rows);
@@ -368,9 +374,10 @@ pkv_status pkv_decode_attention_tree(const pkv_pool* pool, int32_t layer, const 
   m.rows_warp = (int)std::max<int64_t>(1, std::min<int64_t>(64, all / (6 * sms)));
   const int64_t cta_rows = (int64_t)pkv::kCombineWarps * m.rows_warp;
   m.blocks_seq = (int)((rows + cta_rows - 1) / cta_rows);
-  const auto kern = path.tcgen05 ? pkv::tree_combine_kernel<128>
-                    : m.f32      ? pkv::tree_combine_kernel<32>
-                                 : pkv::tree_combine_kernel<64>;
+  const int keys = path.tcgen05 ? 128 : pkv::rows_tile_keys(v.quant ? PKV_I8 : m.f32 ? PKV_F32 : PKV_BF16, path.unit_rows);
+  const auto kern = keys == 128  ? pkv::tree_combine_kernel<128>
+                    : keys == 64 ? pkv::tree_combine_kernel<64>
+                                 : pkv::tree_combine_kernel<32>;
   st = pkv::launch_status(pkv::launch_kernel(kern, dim3((unsigned)(m.blocks_seq * batch)),
                                              dim3(pkv::kCombineWarps * 32), 0, stream, true, m));
   if (st != PKV_OK) return (pkv_status)st;
@@ -399,7 +406,7 @@ pkv_status pkv_prefill_attention_window(const pkv_pool* pool, int32_t layer, con
   if ((st = pkv::device_sm_count(&sms, &dev)) != PKV_OK) return (pkv_status)st;
   pkv::RowsParams p = pkv::rows_params(c, v, err);
   const int64_t rows = (int64_t)max_q_len * p.plan.G;
-  p.plan.unit_rows = rows <= 16 ? 16 : rows <= 32 ? 32 : 64;
+  p.plan.unit_rows = pkv::rows_unit(v, rows);
   if (validate && (st = pkv::validate_call(p, stream)) != PKV_OK) return (pkv_status)st;
   p.units_max = (int)((rows + p.plan.unit_rows - 1) / p.plan.unit_rows);
   const int64_t held = (int64_t)max_blocks_per_seq * v.block_size;
