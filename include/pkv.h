@@ -542,9 +542,18 @@ PKV_API pkv_status pkv_decode_attention_window(const pkv_pool* pool, int32_t lay
 
 /* The same for the last n_b = cu_q[b+1] - cu_q[b] tokens of each sequence (prompts,
  * chunks after a cached context): arguments, their rules and errors as
- * pkv_prefill_attention, with every pool dtype and block size.  out rows
+ * pkv_prefill_attention, with every pool dtype and block size (an invalid block
+ * id reads as rows of zeros and sets the device error word).  out rows
  * behind cu_q[batch], and those of skipped sequences, are not written.  No
- * workspace. */
+ * workspace; may be captured in a CUDA graph.
+ * Arithmetic, here and in pkv_decode_attention_tree: sums, softmax statistics and
+ * states in fp32.  bf16 pools: the weights enter their product with V as the
+ * nearest bf16, as in pkv_prefill_attention, or where max_q_len times the query
+ * heads of a kv head is at most 16 as two bf16 parts, within 2^-16 together.
+ * PKV_I8 pools: exact codes and exact q (but for what lies under 2^-39 of a row's
+ * largest), the weights times the V scales as one fp16, within 2^-11 of each or
+ * 2^-27 of the largest of the row; as two, within 2^-22, where bf16 has two.
+ * fp32 pools: every product within 2^-21. */
 PKV_API pkv_status pkv_prefill_attention_window(const pkv_pool* pool, int32_t layer, const void* q,
                                                 int32_t num_q_heads, float scale,
                                                 const int32_t* block_tables,
@@ -578,7 +587,8 @@ PKV_API pkv_status pkv_prefill_attention_window(const pkv_pool* pool, int32_t la
  * states of split parts go to `workspace`
  * (>= pkv_decode_tree_workspace_size bytes, 16-byte aligned, contents need no
  * initialisation; two calls that may run at once need one each) and a second
- * kernel merges them.  0 from the size call: bad shape or no device. */
+ * kernel merges them.  May be captured in a CUDA graph.  0 from the size call:
+ * bad shape or no device. */
 PKV_API size_t pkv_decode_tree_workspace_size(const pkv_pool* pool, int32_t batch,
                                               int32_t num_q_heads, int32_t max_q_len);
 PKV_API pkv_status pkv_decode_attention_tree(const pkv_pool* pool, int32_t layer, const void* q,

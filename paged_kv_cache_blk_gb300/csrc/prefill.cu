@@ -40,6 +40,22 @@
 //    64-column half of every tile by TMA and copies it into the other CTA's
 //    ring (a shared-memory bulk copy within the cluster), so each tile is
 //    read from L2 once for both SMs.  No tensor copy is multicast.
+//
+// Windows and trees (kWindow, kTree, kNarrow; head_dim 64 too, any group of up to 16
+// heads: 128 / G tokens a tile, rows behind them zero) take a list of key tiles from
+// span.cuh, first tokens and window packed together, and a row's mask as words; V
+// rows that no query of the item sees are cleared in shared memory before they are
+// multiplied (a freed block may hold NaN).
+//  * kWindow: the CTA pairs of prefill; 8 prompts of up to 4096 tokens under a window
+//    of 1024, 32 / 8 heads, D 128, 590 us (220 by the products alone).
+//  * kTree: a CTA an SM takes an even share of the batch's tiles, whatever the units
+//    (span.cuh), and leaves a state of each unit that it did not finish.  Its own loads
+//    all: K by warp 8, V by warp 11, table entries looked up a tile ahead (one warp for
+//    both, entries when needed: 16 trees of 256 rows on 8192 tokens 188 us, now 164).
+//  * kNarrow, up to 128 rows: both softmax groups work on those rows, half of each key
+//    tile each, and S of the next tile is issued ahead of P V: 16 trees of 64 rows on
+//    8192 tokens 109 us (kTree, half of it empty, 163), 79 by the bytes; the two states
+//    of a row are merged in TMEM at the end.
 // Every wait is bounded; on a timeout the CTA records the error, drains its
 // MMAs and frees its TMEM before returning.
 #include <cuda.h>

@@ -1,28 +1,52 @@
 // Attention of several query rows a kv head over one stream of its keys, on mma.sync:
 // the general form of pkv_decode_attention_tree and pkv_prefill_attention_window, for
 // every pool type, head_dim 64 and 128, any group of heads and block size (prefill.cu
-// holds the tcgen05 form for bf16 pools of head_dim 128).
+// holds the tcgen05 form for bf16 pools; tree.cu says which call takes which).
 //
 // What is computed.  The rows of a unit are (new token, query head of kv head g) pairs
-// of one sequence, M = 16 WR of them (WR 1, 2 or 4).  Softmax attention over the keys
-// that each row sees (span.cuh: a window, first tokens, a mask among the new tokens), K
-// and V read in place through the block table.
+// of one sequence, M = 16, 32 or 64 of them.  Softmax attention over the keys that each
+// row sees (span.cuh: a window, first tokens, a mask among the new tokens), K and V read
+// in place through the block table.
 //
-// How.  A CTA of 4 warps streams the unit's tiles of KT keys through a ring of cp.async
-// stages; rows that no query of the unit sees arrive as zeros, and are not read.  WR
-// warps share out the rows and WK = 4 / WR the keys of each tile, so few rows cost few
-// products (16 rows: every warp takes a quarter of the keys).  Each warp holds Q in
-// registers and a running softmax (maximum, sum, O) of its 16 rows over its keys; the WK
-// states of a row are merged in shared memory at the end.
-//   bf16: S = Q K^T and O += P V on mma m16n8k16.  A weight enters P V as two bf16 parts,
-//     within 2^-16 of it together (one part alone would be the largest error of the result).
-//   int8: the same: codes are whole numbers up to 127, exact in bf16, K's scales are
-//     factors of the scores and V's of the weights.  The tile's keys are taken in the
-//     order that makes the byte-transposing V load agree with the scores' registers.
+// How.  A CTA of 8 warps streams the unit's tiles of KT keys through a ring of 2 or 3
+// cp.async stages; rows that no query of the unit sees arrive as zeros, and are not read.
+// A tile's scores are shared out by keys (8 or 16 a warp) and, where a tile has fewer
+// keys than that, by rows; P then passes through shared memory, and O += P V is shared
+// out by dims, an eighth a warp: so no two warps convert or load the same V, and O takes
+// M / 16 x D / 64 x 4 registers.  (With keys shared out in both products, four warps a CTA
+// and O whole in each, registers held 2 warps a scheduler: 30 tokens on 4096 under a
+// window of 4096 35 us instead of 26, an int8 batch of 32 trees 143 instead of 124, fp32
+// trees of 32 tokens, D 128, 498 instead of 398; only int8 prompts of D 64 gained by it,
+// 186 instead of 235, where a tile has few products for its three barriers.  Two barriers
+// a tile, with three stages: 2% less on 64 rows, 3% more on 16.)
+//   P is taken against a maximum of the row that moves only when a score passes it by
+// more than 8 in log2 units: then, and in the first tile, the warps agree on a new one in
+// shared memory; else one __syncthreads_or is all that they exchange.  The sums of a row
+// stay in its lanes until the end.
+//   bf16: S = Q K^T and O += P V on mma m16n8k16.  Up to 16 rows a weight enters P V as
+//     two bf16 parts, within 2^-16 of it together; with more rows, where products are
+//     what the kernel spends its time on, as the nearest bf16, as in prefill.cu: off by
+//     2^-8 at most, at random, which sums of many keys average out (0.0024 of the
+//     result's norm at most was seen against 64 bits, where the output's own rounding is
+//     0.0017).
+//   int8: fp16 products over the exact codes (to bf16 a code takes three times the
+//     instructions of the busiest pipe).  Q is scaled into fp16 by a power of two a row,
+//     K's scales are factors of the scores and V's of the weights.  O is kept in units a
+//     row in which the largest weight x V scale, at the time that they are chosen, is
+//     2^2; they are chosen again with the maximum, and when a V scale passes 2^7 of them
+//     (so no product passes 2^15).  A product enters as one fp16, within 2^-11 of it or
+//     2^-27 of the largest; up to 16 rows as two, within 2^-22.  (With 2^6 for 2^2 other scales passed 2^7 in most tiles: an
+//     int8 prompt took 355 us instead of 301.)  The tile's keys are taken in the order that
+//     makes the byte-transposing V load agree with P.
 //   fp32: mma m16n8k8 on tf32 in three products: x = hi + lo, each the nearest tf32, and
 //     x y ~ hi hi + hi lo + lo hi, within 2^-21 of it.  The tensor cores add with
-//     truncation, so the small products come first, and O is not their accumulator: each
-//     tile's P V is summed from zero and added to O with rounding.
+//     truncation, so the small products have a sum of their own, and O is not their
+//     accumulator: each tile's P V is summed from zero and added to O with rounding.
+//
+// What bounds it.  Few rows: the keys' bytes (bf16, 16 trees of 8 tokens on 8192, groups of
+// 4, D 128: 102 us, 79 by the bytes; int8 107, 41).  Many rows, int8 and fp32: what lies
+// around the products - conversions, operands through shared memory, barriers - at 55%
+// of the issue slots and 27% of the tensor pipe.
 #pragma once
 
 #include <climits>
@@ -119,7 +143,7 @@ struct RowsLayout {
   static constexpr int KN = M > 16 && !kF32 ? 2 : 1;  // 8-key groups of a warp's scores
   static constexpr int MT = M / 16, KG = Tl::kKeys / 8 / KN, MG = kRowsWarps / KG;
   static constexpr int MS = MT > MG ? MT / MG : 1;  // row tiles of a warp's scores
-  static constexpr bool kTwoParts = M == 16 && MODE == PKV_BF16;  // of a weight in P V
+  static constexpr bool kTwoParts = M == 16 && !kF32;  // of a weight in P V
   static constexpr int kStages = Tl::kBytes > 32768 || (Tl::kBytes == 32768 && (kF32 || M == 64)) ? 2 : 3;
   static constexpr int kRing = kStages * Tl::kBytes;
   static constexpr int kQRow = D * (kF32 ? 4 : 2), kQPart = M * kQRow;  // fp32: two tf32 parts
@@ -273,7 +297,7 @@ __device__ __forceinline__ void rows_piece(const RowsParams& p, const RowsPiece&
         }
 #pragma unroll
         for (int u = 1; u < C; u <<= 1) top = max(top, __shfl_xor_sync(kAllLanes, top, u));
-        top = max(top, 15);
+        top = max(top, 40);  // (no unit under 2^-101)
         const float up = __int_as_float((141 - top + 127) << 23);
         if (c == 0) q_unit[r] = __int_as_float((top - 141 + 127) << 23);
         x.x = pack_f16x2(bf16_lo(x.x) * up, bf16_hi(x.x) * up);
@@ -559,14 +583,19 @@ __device__ __forceinline__ void rows_piece(const RowsParams& p, const RowsPiece&
               col = (2 * (grp & 1) + (qi >> 1)) * 4;
             }
             uint32_t h;
-            if constexpr (kI8) {
-              h = pack_f16x2(x, y);
-            } else if constexpr (!kTwoParts) {
-              h = pack_bf16x2(x, y);
+            if constexpr (!kTwoParts) {
+              h = kI8 ? pack_f16x2(x, y) : pack_bf16x2(x, y);
             } else {
-              h = below_bf16x2(x, y);
-              sts32(at + Lay::kPPart + ((chunk ^ (row & 7)) << 4) + col,
-                    pack_bf16x2(x - bf16_lo(h), y - bf16_hi(h)));
+              uint32_t rest;
+              if constexpr (kI8) {
+                h = pack_f16x2_finite(x, y);
+                const float2 f = unpack_f16x2(h);
+                rest = pack_f16x2(x - f.x, y - f.y);
+              } else {
+                h = below_bf16x2(x, y);
+                rest = pack_bf16x2(x - bf16_lo(h), y - bf16_hi(h));
+              }
+              sts32(at + Lay::kPPart + ((chunk ^ (row & 7)) << 4) + col, rest);
             }
             sts32(at + ((chunk ^ (row & 7)) << 4) + col, h);
           }
@@ -605,7 +634,7 @@ __device__ __forceinline__ void rows_piece(const RowsParams& p, const RowsPiece&
             a_frag(sp + Lay::kPPart, Lay::kPRow, mt, k, a);
 #pragma unroll
             for (int u = 0; u < NO; ++u)
-              mma16<false>(o[mt][u], a[0], a[1], a[2], a[3], b[u][0], b[u][1]);
+              mma16<kI8>(o[mt][u], a[0], a[1], a[2], a[3], b[u][0], b[u][1]);
           }
         }
       }

@@ -102,15 +102,6 @@ __device__ __forceinline__ uint32_t movmatrix_t(uint32_t x) {
   asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
   return r;
 }
-// The nearest finite fp16 of each: what an infinite product leaves is infinite.
-__device__ __forceinline__ uint32_t pack_f16x2_finite(float lo, float hi) {
-  uint32_t r;
-  asm("cvt.rn.satfinite.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-  return r;
-}
-__device__ __forceinline__ float2 unpack_f16x2(uint32_t w) {
-  return __half22float2(*reinterpret_cast<const __half2*>(&w));
-}
 // ---- staging -------------------------------------------------------------------
 
 // One tile in a warp's ring: K rows, V rows, and for int8 pools their scales.

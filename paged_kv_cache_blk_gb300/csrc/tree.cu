@@ -133,7 +133,10 @@ int rows_unit(const PoolView& v, int64_t rows) {
   return rows <= 16 ? 16 : rows <= 32 ? 32 : most;
 }
 
-// How a tree call runs: units of unit_rows rows, split over `grid` CTAs.
+// How a tree call runs: units of unit_rows rows, split over `grid` CTAs.  tcgen05 from more than
+// 32 rows of a kv head on, where it can.  16 sequences on 8192, 8 kv heads, mma.sync and tcgen05:
+// 48 rows (a group of 4) 148 and 104 us, 64 rows 152 and 108, with D 64 109 and 91; one sequence
+// of 64 rows on 16384 37 and 26; 24 rows on 500, two sequences 13 and 12.
 struct TreePath {
   bool tcgen05;
   int unit_rows, grid;
@@ -170,21 +173,22 @@ cudaError_t launch_rows(const PoolView& v, const RowsParams& p, bool tree, long 
 // Whether a windowed prefill takes the tcgen05 kernel, where both could.  It works on whole
 // windows of 4 tiles of 128 rows a CTA pair; the mma.sync kernel shares a unit's keys out over a
 // cluster where units are few.  Estimated from a tile's time in us (128 keys x 2 tiles a CTA; 64
-// keys x 64 rows a CTA, beside the others of its SM) and what an item costs besides: 30 tokens on
-// 4096 under a window of 4096, 32 / 8 heads, D 128: tcgen05 66 us, mma.sync 35; 100 tokens 78
-// and 58; 512 tokens 79 and 200; under a window of 500, 100 tokens 20 and 18.
+// keys x 64 rows a CTA, beside the others of its SM) and what an item costs besides.  On 4096
+// under a window of 4096, 32 / 8 heads, D 128, tcgen05 and mma.sync took for 30 tokens 68 and 26
+// us, 100 tokens 78 and 45, 300 tokens 79 and 80, 512 tokens 79 and 146; under a window of 500,
+// 100 tokens 21 and 17, 512 tokens 21 and 30; with D 64, 100 tokens 69 and 34.
 bool prefill_on_tcgen05(const PoolView& v, const RowsParams& p, int sms) {
   if (!span_supported(v, p.hq, true) || p.plan.unit_rows <= 32) return false;
   const bool d64 = v.head_dim == 64;
   const double heads = (double)p.plan.span.batch * v.num_kv_heads;
   const int tokens = 128 / p.plan.G, tiles_q = (p.plan.span.max_q_len + tokens - 1) / tokens;
   const double items = (tiles_q + 3) / 4 * heads;
-  const double pairs_us = std::ceil(items / (sms / 2)) * (p.keys_most / 128. * (d64 ? 2.1 : 2.5) + 8);
+  const double pairs_us = std::ceil(items / (sms / 2)) * (p.keys_most / 128. * (d64 ? 1.9 : 2.3) + 8);
   const double units = p.units_max * heads, held = sms * rows_ctas_bf16(v.head_dim, 64);
   int ctas = kRowsMaxCluster;
   while (ctas > 1 && units * ctas > held) ctas >>= 1;
   const double rows_us =
-      std::ceil(units * ctas / held) * (p.keys_most / 64. / ctas * (d64 ? 2.0 : 3.3) + 7);
+      std::ceil(units * ctas / held) * (p.keys_most / 64. / ctas * (d64 ? 1.6 : 2.3) + 7);
   return pairs_us <= rows_us;
 }
 

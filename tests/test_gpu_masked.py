@@ -465,6 +465,57 @@ def test_unseen_values_do_not_spread(dev, dtype, G, D, ctx, n, bad):
     assert pkv.device_error() == "PKV_OK"
 
 
+@pytest.mark.parametrize("D,G,n", [(64, 4, 3), (128, 4, 7), (128, 8, 8), (64, 16, 9)])
+@pytest.mark.parametrize("heavy", [False, True])
+def test_i8_scales_far_apart(dev, D, G, n, heavy):
+    """V scales from 2^-24 to 2^24: each product counts for what it is, whether the keys of great
+    scale carry weight or (``heavy`` False) next to none.  Every weight is off by 2^-11 of itself
+    (one fp16) and by 2^-27 of the largest product so far, times a code of up to 127."""
+    c = Case(dev, "i8", 2, G, D, 16, [150 + n, 40], [n, 2], seed=77)
+    at = c.v[..., 2 * D:2 * D + 8].view(torch.float32)
+    e = c.rng.integers(-24, 25, at.shape)
+    e[..., 0] = np.where(c.rng.random(e.shape[:-1]) < 0.03, 24, -20)
+    at.copy_(torch.from_numpy(2.0 ** e).to(dev, torch.float32))
+    if not heavy:  # great V scales beside keys that point away from every query
+        c.q.copy_(c.q.abs())
+        big = (at[..., 0] > 1) | (at[..., 1] > 2.0 ** 10)
+        c.k[..., :2 * D] = torch.where(big[..., None], torch.full_like(c.k[..., :2 * D], 28), c.k[..., :2 * D])
+    k, v = c.values(c.k), c.values(c.v)
+    sees, depth = _random_tree(c.rng, n)
+    mask, pos = _tree_args(c, [sees, np.tril(np.ones((2, 2)))], [depth, np.arange(2)], 1)
+    outs = {"tree": _tree(c, mask, pos), "prefill": _prefill(c, 90, 2)}
+    q = widen_out(c.q)
+    for name, out in outs.items():
+        got = widen_out(out)
+        for b in range(2):
+            blk, row = c.rows(b)
+            ctx = int(c.lens[b] - c.new[b])
+            for i in range(int(c.new[b])):
+                full = np.zeros(len(blk), bool)
+                if name == "tree":
+                    s = MK.tree_seen(ctx, sees if b == 0 else np.tril(np.ones((2, 2), bool)), i,
+                                     ctx + i, 0, 0)
+                else:
+                    s = MK.window_seen(ctx + i, 90, 2)
+                full[:len(s)] = s
+                for g in range(2):
+                    rows = slice(g * G, g * G + G)
+                    t = int(c.cu[b]) + i
+                    kk, vv = k[blk, row, g], v[blk, row, g]
+                    ref, mean, top = MK.attention(q[t, rows], kk, vv, full, c.scale)
+                    x = c.scale * (q[t, rows] @ kk[full].T)
+                    w = np.exp(x - x.max(1, keepdims=True))
+                    w /= w.sum(1, keepdims=True)
+                    scales = np.abs(vv[full]).max(1) / 127
+                    most = (w * scales).max(1, keepdims=True)
+                    d = (D + 8) * 2.0 ** -23 * c.scale * top[:, None] + 2.0 ** -21
+                    n_keys = int(full.sum())
+                    tol = (2 * d + n_keys * 2.0 ** -23 + 2.0 ** -11) * mean
+                    tol += n_keys * 127 * 2.0 ** -27 * most + 1.01 * 2.0 ** -8 * np.abs(ref)
+                    err = np.abs(got[t, rows] - ref)
+                    assert np.all(err <= tol), (name, b, i, g, float((err / tol).max()))
+
+
 # ---- accepted tokens ----------------------------------------------------------------
 
 def _accept_case(dev, dtype, H, D, bs, lens, new, paths, layers=3):
