@@ -75,6 +75,7 @@ struct RowsParams {
   long long num_blocks;
   int L, layer, row_bytes, scale_off, hq, bs_bits;
   Repair repair;
+  int lines;      // tree: 1, or a line of steps a kv head (tree.cu)
   int units_max;  // prefill: units of one kv head of the longest sequence
   long long keys_most;  // prefill: keys that a unit's rows see at most
   float qscale;   // scale * log2(e)
@@ -822,7 +823,9 @@ __global__ void __launch_bounds__(kRowsThreads, (RowsLayout<MODE, D, M>::kCtas))
   __shared__ long long scratch[32];
   griddep_wait();
   griddep_launch_dependents();
-  const PlanShare share = plan_share<KT>(p.plan, blockIdx.x, gridDim.x, scratch);
+  const int line_of = (int)blockIdx.x % p.lines;
+  const PlanShare share =
+      plan_share<KT>(p.plan, (int)blockIdx.x / p.lines, (int)gridDim.x / p.lines, scratch);
   // where the CTA is, kept in shared memory: registers that a piece's work wants for itself
   volatile long long* line = scratch;  // at, first, end, b
   __syncthreads();
@@ -860,8 +863,9 @@ __global__ void __launch_bounds__(kRowsThreads, (RowsLayout<MODE, D, M>::kCtas))
     w.s = q.s;
     w.t = q.t;
     w.b = b;
-    w.g = part.unit / q.nru;
-    w.first_row = (part.unit - w.g * q.nru) * M;
+    const int g = part.unit / q.nru;  // (0 where each kv head has its line)
+    w.g = line_of + g;
+    w.first_row = (part.unit - g * q.nru) * M;
     w.t0 = part.t0;
     w.t1 = part.t1;
     w.lo = window_start(q.s.ctx, p.plan.span.window);

@@ -16,7 +16,8 @@ struct CombineParams {
   PlanParams plan;
   const float* part;
   char* out;
-  int hq, D, f32, grid;  // grid: CTAs of the kernel that left the states
+  int hq, D, f32, grid;  // grid: CTAs of a line of the kernel that left the states
+  int lines;
   int blocks_seq;        // CTAs of a sequence
   int rows_warp;         // rows a warp takes, one after the other
   Repair repair;
@@ -29,13 +30,17 @@ __device__ __forceinline__ void combine_row(const CombineParams& p, const SeqPla
   const int lane = threadIdx.x & 31;
   const int tok = row / p.hq, h = row - tok * p.hq, g = h / p.plan.G;
   const int r = tok * p.plan.G + h - g * p.plan.G, ur = p.plan.unit_rows, unit = r / ur;
-  const long long start = before + ((long long)g * q.nru + unit) * q.steps + p.plan.lead;
+  const bool own_line = p.lines > 1;  // of the kv head
+  const long long start =
+      before + ((long long)(own_line ? 0 : g) * q.nru + unit) * q.steps + p.plan.lead;
   const long long c0 = div_pos(start, chunk), c1 = div_pos(start + q.t.nt - 1, chunk);
   if (c0 == c1) return;
   const long long row_floats = p.D + 4, slot = ur * row_floats;
   const float* at = p.part + (r - unit * ur) * row_floats;
   // (the CTA with the unit's first tile left its part in slot 2 c + 1)
-  auto state = [&](long long c) { return at + (2 * c + (c == c0 ? 1 : 0)) * slot; };
+  auto state = [&](long long c) {
+    return at + (2 * (c * p.lines + (own_line ? g : 0)) + (c == c0 ? 1 : 0)) * slot;
+  };
   const int pieces = (int)(c1 - c0) + 1, d = lane * 4;
   float top = -INFINITY, sum = 0.f, x[4] = {0.f, 0.f, 0.f, 0.f};
   // a state's numbers and values are loaded together: one round trip for kInFlight of them
@@ -140,11 +145,13 @@ int rows_unit(const PoolView& v, int64_t rows) {
 struct TreePath {
   bool tcgen05;
   int unit_rows, grid;
+  int lines;     // 1, or num_kv_heads: each kv head's units are a line of their own
   size_t bytes;  // of workspace
 };
 
 TreePath tree_path(const PoolView& v, int G, int max_q_len, int sms) {
   TreePath t;
+  t.lines = 1;
   const long long rows = (long long)max_q_len * G;
   t.tcgen05 = rows > 32 && span_supported(v, G * v.num_kv_heads, false);
   if (t.tcgen05) {
@@ -159,6 +166,17 @@ TreePath tree_path(const PoolView& v, int G, int max_q_len, int sms) {
                    : v.io_size == 2 ? rows_ctas_bf16(v.head_dim, t.unit_rows)
                                     : rows_ctas_f32(v.head_dim, t.unit_rows);
   t.grid = sms * ctas;
+  // int8: a row's codes of one head share their last lines with the next head's, and the scales of
+  // all heads are one sector: where the heads are read at the same time, each comes from memory
+  // once.  So each head's line is split in the same way, and CTAs of one place follow one another,
+  // unless that leaves more than a tenth of the grid without work.
+  if (v.quant) {
+    const int pieces = t.grid / v.num_kv_heads;
+    if (pieces > 0 && (t.grid - pieces * v.num_kv_heads) * 10 <= t.grid) {
+      t.lines = v.num_kv_heads;
+      t.grid = pieces * t.lines;
+    }
+  }
   t.bytes = (size_t)2 * t.grid * t.unit_rows * (v.head_dim + 4) * 4;
   return t;
 }
@@ -348,6 +366,8 @@ pkv_status pkv_decode_attention_tree(const pkv_pool* pool, int32_t layer, const 
   if (workspace_bytes < path.bytes) return PKV_ERR_WORKSPACE;
   p.plan.unit_rows = path.unit_rows;
   p.plan.lead = path.tcgen05 ? 2 : 4;
+  p.lines = path.lines;
+  if (path.lines > 1) p.plan.hkv = 1;
   if (path.tcgen05) p.plan.span.gran = v.block_size;  // (tensor copies of whole blocks)
   p.part = static_cast<float*>(workspace);
   p.mask = reinterpret_cast<const unsigned long long*>(tree_mask);
@@ -370,7 +390,8 @@ pkv_status pkv_decode_attention_tree(const pkv_pool* pool, int32_t layer, const 
   m.hq = num_q_heads;
   m.D = v.head_dim;
   m.f32 = v.io_size == 4;
-  m.grid = path.grid;
+  m.grid = path.grid / path.lines;
+  m.lines = path.lines;
   m.repair = p.repair;
   // as many CTAs as the device holds about at once: each goes over the batch first
   const int64_t rows = (int64_t)max_q_len * num_q_heads;
