@@ -209,11 +209,9 @@ __device__ __forceinline__ void rows_piece(const RowsParams& p, const RowsPiece&
     const int pos = w.t.position(i * KT + my_r);
     return seen_by_some(pos) ? table[pos >> p.bs_bits] : INT_MIN;
   };
-  int ahead = lookup(w.t0);
-  auto issue = [&](int i, int stage) {
+  auto issue = [&](int i, int stage, int blk, auto look) {
     if (i < w.t1) {
       const int pos = w.t.position(i * KT + my_r);
-      int blk = ahead;
       if (blk != INT_MIN && (blk < 0 || blk >= p.num_blocks)) {
         set_error(p.err, kErrIndex);
         blk = INT_MIN;
@@ -223,8 +221,8 @@ __device__ __forceinline__ void rows_piece(const RowsParams& p, const RowsPiece&
           blk == INT_MIN ? 0
                          : ((((long long)blk * p.L + p.layer) << p.bs_bits) +
                             (pos & ((1 << p.bs_bits) - 1))) * p.row_bytes;
-      ahead = lookup(i + 1);
       const uint32_t dst = base + stage * Tl::kBytes;
+      look();
       constexpr int C = Tl::kChunks;
 #pragma unroll
       for (int u = 0; u < RW * C / 32; ++u) {
@@ -247,8 +245,12 @@ __device__ __forceinline__ void rows_piece(const RowsParams& p, const RowsPiece&
     cp_commit();
   };
   static_assert(RW * Tl::kChunks >= 32, "every lane copies");
-#pragma unroll 1
-  for (int s = 0; s < NST - 1; ++s) issue(w.t0 + s, s);
+  int ahead[NST];  // looked up together
+#pragma unroll
+  for (int s = 0; s < NST; ++s) ahead[s] = lookup(w.t0 + s);
+#pragma unroll
+  for (int s = 0; s < NST - 1; ++s) issue(w.t0 + s, s, ahead[s], [] {});
+  int next = ahead[NST - 1];  // of the tile that is copied next
 
   // ---- what the rows see: kept in shared memory, and the places that all of them see ----
   int full_lo = INT_MIN, full_hi = INT_MAX;
@@ -357,7 +359,7 @@ __device__ __forceinline__ void rows_piece(const RowsParams& p, const RowsPiece&
   for (int i = w.t0; i < w.t1; ++i) {
     cp_wait<NST - 2>();
     __syncthreads();  // the tile is there, and the last one's P and stage are done with
-    issue(i + NST - 1, stage == 0 ? NST - 1 : stage - 1);
+    issue(i + NST - 1, stage == 0 ? NST - 1 : stage - 1, next, [&] { next = lookup(i + NST); });
     const uint32_t st = base + stage * Tl::kBytes, sv = st + Tl::kHalf;
     if (++stage == NST) stage = 0;
 
