@@ -46,7 +46,7 @@
 // span.cuh, first tokens and window packed together, and a row's mask as words; V
 // rows that no query of the item sees are cleared in shared memory before they are
 // multiplied (a freed block may hold NaN).
-//  * kWindow: the CTA pairs of prefill; 8 prompts of up to 4096 tokens under a window
+//  * kWindow: the CTA pairs of prefill; 8 prompts of 1024 to 8192 tokens under a window
 //    of 1024, 32 / 8 heads, D 128, 590 us (220 by the products alone).
 //  * kTree: a CTA an SM takes an even share of the batch's tiles, whatever the units
 //    (span.cuh), and leaves a state of each unit that it did not finish.  Its own loads

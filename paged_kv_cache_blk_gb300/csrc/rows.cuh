@@ -15,7 +15,7 @@
 // out by dims, an eighth a warp: so no two warps convert or load the same V, and O takes
 // M / 16 x D / 64 x 4 registers.  (With keys shared out in both products, four warps a CTA
 // and O whole in each, registers held 2 warps a scheduler: 30 tokens on 4096 under a
-// window of 4096 35 us instead of 26, an int8 batch of 32 trees 143 instead of 124, fp32
+// window of 4096 35 us instead of 26, an int8 batch of 32 trees 143 instead of 122, fp32
 // trees of 32 tokens, D 128, 498 instead of 398; only int8 prompts of D 64 gained by it,
 // 186 instead of 235, where a tile has few products for its three barriers.  Two barriers
 // a tile, with three stages: 2% less on 64 rows, 3% more on 16.)
@@ -44,7 +44,7 @@
 //     accumulator: each tile's P V is summed from zero and added to O with rounding.
 //
 // What bounds it.  Few rows: the keys' bytes (bf16, 16 trees of 8 tokens on 8192, groups of
-// 4, D 128: 102 us, 79 by the bytes; int8 107, 41).  Many rows, int8 and fp32: what lies
+// 4, D 128: 104 us, 79 by the bytes; int8 104, 41).  Many rows, int8 and fp32: what lies
 // around the products - conversions, operands through shared memory, barriers - at 55%
 // of the issue slots and 27% of the tensor pipe.
 #pragma once
