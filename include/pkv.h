@@ -553,7 +553,8 @@ PKV_API pkv_status pkv_decode_attention_window(const pkv_pool* pool, int32_t lay
  * PKV_I8 pools: exact codes and exact q (but for what lies under 2^-39 of a row's
  * largest), the weights times the V scales as one fp16, within 2^-11 of each or
  * 2^-27 of the largest of the row; as two, within 2^-22, where bf16 has two.
- * fp32 pools: every product within 2^-21. */
+ * fp32 pools: every product within 2^-21 (an infinite element of q or of a seen key
+ * may count as NaN in its scores). */
 PKV_API pkv_status pkv_prefill_attention_window(const pkv_pool* pool, int32_t layer, const void* q,
                                                 int32_t num_q_heads, float scale,
                                                 const int32_t* block_tables,

@@ -165,6 +165,10 @@ def _ptr(t: Optional[torch.Tensor]) -> Optional[int]:
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
+# (a pool lies on the device: torch is initialised)
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+
+
 def _stream(dev: torch.device) -> int:
     if dev.index is None:
         raise ValueError(f"the pool is on {dev}, not on a CUDA device")
@@ -231,7 +235,7 @@ _NO_SWITCH = _NoSwitch()
 def _dev(pool: Pool):
     """Make the pool's device current for the call (no-op when it already is)."""
     idx = pool.device.index
-    if idx is None or idx == torch.cuda.current_device():
+    if idx is None or idx == _current_device():
         return _NO_SWITCH
     return torch.cuda.device(pool.device)
 

@@ -533,7 +533,8 @@ __device__ __forceinline__ Item make_item(const PfParams& p, long long i, int ti
   if (px >= (ntq + 1) / 2) return it;
   const long long len = p.lens[it.b];
   it.off = p.offs ? p.offs[it.b] : 0;
-  if ((MODE == kWindow && it.q0 < 0) || it.nq > p.max_q_len || len < it.nq || it.off < 0 || it.off >= p.bs || q1 > p.total_q ||
+  if ((MODE == kWindow && it.q0 < 0) || it.nq > p.max_q_len || len < it.nq || it.off < 0 ||
+      it.off >= p.bs || q1 > p.total_q ||
       (long long)it.off + len > (long long)p.mb * p.bs) {
     // reported once, by the item of the sequence's first pair and head
     if (px == 0 && it.g == 0 && tid == 0) set_error(p.err, kErrCapacity);
@@ -1691,7 +1692,8 @@ cudaError_t launch_prefill(const PoolView& pv, int layer, const void* q, int num
 cudaError_t launch_prefill_tree(const PoolView& pv, int layer, const void* q, int num_q_heads,
                                 float scale, const int32_t* bt, const PlanParams& plan,
                                 const int32_t* q_pos, const unsigned long long* mask, int words,
-                                const Repair& repair, float* part, void* out, int* err, int sm_count, cudaStream_t s) {
+                                const Repair& repair, float* part, void* out, int* err, int sm_count,
+                                cudaStream_t s) {
   CUtensorMap tq, tk, tv;
   PfParams p;
   const SpanParams& sp = plan.span;

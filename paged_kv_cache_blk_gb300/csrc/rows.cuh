@@ -35,9 +35,10 @@
 //     row in which the largest weight x V scale, at the time that they are chosen, is
 //     2^2; they are chosen again with the maximum, and when a V scale passes 2^7 of them
 //     (so no product passes 2^15).  A product enters as one fp16, within 2^-11 of it or
-//     2^-27 of the largest; up to 16 rows as two, within 2^-22.  (With 2^6 for 2^2 other scales passed 2^7 in most tiles: an
-//     int8 prompt took 355 us instead of 301.)  The tile's keys are taken in the order that
-//     makes the byte-transposing V load agree with P.
+//     2^-27 of the largest; up to 16 rows as two, within 2^-22.  (With 2^6 for 2^2 other
+//     scales passed 2^7 in most tiles: an int8 prompt took 355 us instead of 301.)  The
+//     tile's keys are taken in the order that makes the byte-transposing V load agree
+//     with P.
 //   fp32: mma m16n8k8 on tf32 in three products: x = hi + lo, each the nearest tf32, and
 //     x y ~ hi hi + hi lo + lo hi, within 2^-21 of it.  The tensor cores add with
 //     truncation, so the small products have a sum of their own, and O is not their
@@ -68,7 +69,7 @@ struct RowsParams {
   char* out;
   const int32_t* bt;
   const int32_t* q_pos;          // tree: positions of the queries, or NULL
-  const unsigned long long* mask;  // tree: [total_q, words], or NULL (each token sees those before it)
+  const unsigned long long* mask;  // tree: [total_q, words], or NULL (tokens see those before)
   int words;
   int* err;
   float* part;  // states of split units
@@ -145,7 +146,9 @@ struct RowsLayout {
   static constexpr int MT = M / 16, KG = Tl::kKeys / 8 / KN, MG = kRowsWarps / KG;
   static constexpr int MS = MT > MG ? MT / MG : 1;  // row tiles of a warp's scores
   static constexpr bool kTwoParts = M == 16 && !kF32;  // of a weight in P V
-  static constexpr int kStages = Tl::kBytes > 32768 || (Tl::kBytes == 32768 && (kF32 || M == 64)) ? 2 : 3;
+  // what leaves room for two CTAs an SM
+  static constexpr int kStages =
+      Tl::kBytes > 32768 || (Tl::kBytes == 32768 && (kF32 || M == 64)) ? 2 : 3;
   static constexpr int kRing = kStages * Tl::kBytes;
   static constexpr int kQRow = D * (kF32 ? 4 : 2), kQPart = M * kQRow;  // fp32: two tf32 parts
   static constexpr int kQAt = kRing;
@@ -181,7 +184,8 @@ __device__ __forceinline__ void rows_piece(const RowsParams& p, const RowsPiece&
   constexpr int KN = Lay::KN, KS = kF32 ? D / 8 : D / 16;         // steps of a score
   constexpr int NO = D / kRowsWarps / 8;            // 8-dim output tiles of a warp
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int kg = warp % KG, mg = warp / KG;  // scores: KN groups of 8 keys from KN kg, row tiles from mg MS
+  // scores: KN groups of 8 keys from KN kg, row tiles from mg MS
+  const int kg = warp % KG, mg = warp / KG;
   const bool scores = mg * MS < MT;
   const int gl = lane >> 2, qi = lane & 3;
   const int G = p.plan.G, n = w.s.n, rows = n * G, off = w.s.off;
@@ -324,7 +328,7 @@ __device__ __forceinline__ void rows_piece(const RowsParams& p, const RowsPiece&
       }
     }
   }
-  // An A operand of 16 rows and two 16-byte chunks: of Q (a step of bf16: 16 dims; of tf32: 8), of P.
+  // An A operand of 16 rows and two 16-byte chunks (16 columns of 16 bits, 8 of tf32) of Q or P.
   auto a_frag = [&](uint32_t from, int row_bytes, int mt, int step, uint32_t (&a)[4]) {
     const int r = mt * 16 + (lane & 15);
     ldsm_x4(a, from + r * row_bytes + (((2 * step + (lane >> 4)) ^ (r & 7)) << 4));
@@ -451,7 +455,8 @@ __device__ __forceinline__ void rows_piece(const RowsParams& p, const RowsPiece&
       for (int e = 0; e < KN; ++e) {
         [[maybe_unused]] float f[2];
         if constexpr (kI8) {
-          const uint32_t sc = st + 2 * Tl::kHalf + ((kg * KN + e) * 8 + 2 * qi) * 16 + (4 * w.g & 15);
+          const uint32_t sc =
+              st + 2 * Tl::kHalf + ((kg * KN + e) * 8 + 2 * qi) * 16 + (4 * w.g & 15);
 #pragma unroll
           for (int c = 0; c < 2; ++c) {
             f[c] = lds_f32(sc + c * 16);
@@ -537,7 +542,8 @@ __device__ __forceinline__ void rows_piece(const RowsParams& p, const RowsPiece&
             const int row = (mg * MS + j) * 16 + gl + 8 * r;
             m[j][r] = row_max[row];
             l[j][r] *= row_factor[row];
-            if constexpr (kI8) unit[j][r] = m[j][r] == -INFINITY ? 1.f : exp2f(m[j][r] - row_units[row]);
+            if constexpr (kI8)
+              unit[j][r] = m[j][r] == -INFINITY ? 1.f : exp2f(m[j][r] - row_units[row]);
           }
       }
 #pragma unroll
@@ -622,7 +628,7 @@ __device__ __forceinline__ void rows_piece(const RowsParams& p, const RowsPiece&
           }
         } else if constexpr (NO == 2) {
           uint32_t v[4];
-          ldsm_x4_t(v, sv + Tl::at(k * 16 + (lane & 7) + ((lane >> 3) & 1) * 8, 2 * warp + (lane >> 4)));
+          ldsm_x4_t(v, sv + Tl::at(k * 16 + (lane & 15), 2 * warp + (lane >> 4)));
           b[0][0] = v[0]; b[0][1] = v[1]; b[1][0] = v[2]; b[1][1] = v[3];
         } else {
           ldsm_x2_t(b[0][0], b[0][1], sv + Tl::at(k * 16 + (lane & 15), warp));
@@ -632,7 +638,8 @@ __device__ __forceinline__ void rows_piece(const RowsParams& p, const RowsPiece&
           uint32_t a[4];
           a_frag(sp, Lay::kPRow, mt, k, a);
 #pragma unroll
-          for (int u = 0; u < NO; ++u) mma16<kI8>(o[mt][u], a[0], a[1], a[2], a[3], b[u][0], b[u][1]);
+          for (int u = 0; u < NO; ++u)
+            mma16<kI8>(o[mt][u], a[0], a[1], a[2], a[3], b[u][0], b[u][1]);
           if constexpr (kTwoParts) {
             a_frag(sp + Lay::kPPart, Lay::kPRow, mt, k, a);
 #pragma unroll
@@ -734,7 +741,8 @@ __device__ __forceinline__ void rows_piece(const RowsParams& p, const RowsPiece&
       if constexpr (kF32)
         *reinterpret_cast<float2*>(p.out + (at + e) * 4) = make_float2(x[e] * inv, x[e + 1] * inv);
       else
-        *reinterpret_cast<uint32_t*>(p.out + (at + e) * 2) = pack_bf16x2(x[e] * inv, x[e + 1] * inv);
+        *reinterpret_cast<uint32_t*>(p.out + (at + e) * 2) =
+            pack_bf16x2(x[e] * inv, x[e + 1] * inv);
       finite &= !nonfinite(x[e]) && !nonfinite(x[e + 1]);
     }
     if (!finite && !nonfinite(sum))
@@ -754,7 +762,9 @@ __device__ __forceinline__ void rows_piece(const RowsParams& p, const RowsPiece&
     for (int r8 = 0; r8 < 2; ++r8) {
       const int row = mt * 16 + gl + 8 * r8, r = w.first_row + row;
       if (r >= rows) continue;
-      float* dst = cluster ? acc + row * Lay::kAccRow : w.part ? w.part + (long long)row * (D + 4) + 4 : nullptr;
+      float* dst = cluster  ? acc + row * Lay::kAccRow
+                   : w.part ? w.part + (long long)row * (D + 4) + 4
+                            : nullptr;
       if (dst) {
 #pragma unroll
         for (int u = 0; u < NO; ++u)
@@ -931,7 +941,8 @@ cudaError_t launch_prefill_as(const RowsParams& p, int dev, cudaStream_t s) {
   cudaError_t e = allow_shared(kern, Lay::kSmem, allowed[dev]);
   if (e != cudaSuccess) return e;
   const long long units = (long long)p.units_max * p.plan.span.batch * p.plan.hkv;
-  const long long tiles = (p.keys_most + RowsTile<MODE, D, M>::kKeys - 1) / RowsTile<MODE, D, M>::kKeys + 1;
+  constexpr int KT = RowsTile<MODE, D, M>::kKeys;
+  const long long tiles = (p.keys_most + KT - 1) / KT + 1;
   int ctas = 1;
   for (int c = kRowsMaxCluster; c > 1; c >>= 1) {
     int held = 0;

@@ -308,6 +308,7 @@ bool span_supported(const PoolView& pv, int num_q_heads, bool pairs);
 cudaError_t launch_prefill_tree(const PoolView& pv, int layer, const void* q, int num_q_heads,
                                 float scale, const int32_t* bt, const PlanParams& plan,
                                 const int32_t* q_pos, const unsigned long long* mask, int words,
-                                const Repair& repair, float* part, void* out, int* err, int sm_count, cudaStream_t s);
+                                const Repair& repair, float* part, void* out, int* err, int sm_count,
+                                cudaStream_t s);
 
 }  // namespace pkv

@@ -399,7 +399,7 @@ pkv_status pkv_decode_attention_tree(const pkv_pool* pool, int32_t layer, const 
   m.rows_warp = (int)std::max<int64_t>(1, std::min<int64_t>(64, all / (6 * sms)));
   const int64_t cta_rows = (int64_t)pkv::kCombineWarps * m.rows_warp;
   m.blocks_seq = (int)((rows + cta_rows - 1) / cta_rows);
-  const int keys = path.tcgen05 ? 128 : pkv::rows_tile_keys(v.quant ? PKV_I8 : m.f32 ? PKV_F32 : PKV_BF16, path.unit_rows);
+  const int keys = path.tcgen05 ? 128 : pkv::rows_tile_keys(pool->dtype, path.unit_rows);
   const auto kern = keys == 128  ? pkv::tree_combine_kernel<128>
                     : keys == 64 ? pkv::tree_combine_kernel<64>
                                  : pkv::tree_combine_kernel<32>;
