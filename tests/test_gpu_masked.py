@@ -427,6 +427,14 @@ def test_tree_many_sequences(dev):
     _run_tree(dev, "bf16", 1, 16, 128, 8, lens, new, 0, 0, seed=14)
 
 
+@pytest.mark.parametrize("H,G,D,lens,new", [
+    (8, 4, 128, [5000, 300], [4, 3]), (8, 4, 64, [2500, 900, 3], [8, 5, 3]), (3, 5, 128, [6000, 41], [12, 0]),
+    (105, 1, 64, [700, 90], [3, 16]), (5, 2, 64, list(range(20, 340)), [3, 0, 2, 1] * 80)])
+def test_tree_i8_heads(dev, H, G, D, lens, new):
+    """Heads whose units are split in the same way, and 105 of them, which would leave CTAs idle."""
+    _run_tree(dev, "i8", H, G, D, 16, lens, new, 0, 0, seed=21)
+
+
 # ---- values that some queries see and others do not -------------------------------------
 
 @pytest.mark.parametrize("bad", [float("nan"), float("inf")])
