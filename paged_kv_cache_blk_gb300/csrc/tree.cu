@@ -10,7 +10,6 @@ namespace {
 
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr int kCombineWarps = 8;
-constexpr int kInFlight = 8;  // states that a warp of the merge loads at once
 
 struct CombineParams {
   PlanParams plan;
@@ -25,6 +24,8 @@ struct CombineParams {
 
 // One (token, query head) row, by one warp: the states of its unit in the CTAs that shared it,
 // by the log-sum-exp rule.  Rows that one CTA finished are left alone.
+// kInFlight: states that a warp loads at once.
+template <int kInFlight>
 __device__ __forceinline__ void combine_row(const CombineParams& p, const SeqPlan& q, int b,
                                             long long chunk, long long before, int row) {
   const int lane = threadIdx.x & 31;
@@ -90,7 +91,7 @@ __device__ __forceinline__ void combine_row(const CombineParams& p, const SeqPla
 }
 
 // A CTA takes kCombineWarps * rows_warp rows of one sequence.
-template <int KT>
+template <int KT, int kInFlight>
 __global__ void __launch_bounds__(kCombineWarps * 32)
     tree_combine_kernel(const __grid_constant__ CombineParams p) {
   __shared__ long long scratch[32];
@@ -111,7 +112,7 @@ __global__ void __launch_bounds__(kCombineWarps * 32)
   for (int i = 0; i < p.rows_warp; ++i) {
     const int row = first_row + i * kCombineWarps + (int)(threadIdx.x >> 5);
     if (row >= q.s.n * p.hq) break;
-    combine_row(p, q, b, chunk, before, row);
+    combine_row<kInFlight>(p, q, b, chunk, before, row);
   }
 }
 
@@ -400,9 +401,14 @@ pkv_status pkv_decode_attention_tree(const pkv_pool* pool, int32_t layer, const 
   const int64_t cta_rows = (int64_t)pkv::kCombineWarps * m.rows_warp;
   m.blocks_seq = (int)((rows + cta_rows - 1) / cta_rows);
   const int keys = path.tcgen05 ? 128 : pkv::rows_tile_keys(pool->dtype, path.unit_rows);
-  const auto kern = keys == 128  ? pkv::tree_combine_kernel<128>
-                    : keys == 64 ? pkv::tree_combine_kernel<64>
-                                 : pkv::tree_combine_kernel<32>;
+  // Few CTAs: a long context's states are a chain of loads, 16 at a time (one tree of 24 tokens on
+  // 16384 28.0 us with 8, 26.4; of 8 on 30000 44.1, 41.0).  Many: registers for more of them (16
+  // trees of 64 tokens 206 us with 8, 220 with 16).
+  const bool few = (int64_t)m.blocks_seq * batch <= 2 * sms;
+  const auto kern = keys == 128  ? few ? pkv::tree_combine_kernel<128, 16> : pkv::tree_combine_kernel<128, 8>
+                    : keys == 64 ? few ? pkv::tree_combine_kernel<64, 16> : pkv::tree_combine_kernel<64, 8>
+                    : few        ? pkv::tree_combine_kernel<32, 16>
+                                 : pkv::tree_combine_kernel<32, 8>;
   st = pkv::launch_status(pkv::launch_kernel(kern, dim3((unsigned)(m.blocks_seq * batch)),
                                              dim3(pkv::kCombineWarps * 32), 0, stream, true, m));
   if (st != PKV_OK) return (pkv_status)st;
