@@ -44,10 +44,12 @@
 //     truncation, so the small products have a sum of their own, and O is not their
 //     accumulator: each tile's P V is summed from zero and added to O with rounding.
 //
-// What bounds it.  Few rows: the keys' bytes (bf16, 16 trees of 8 tokens on 8192, groups of
-// 4, D 128: 104 us, 79 by the bytes; int8 104, 41).  Many rows, int8 and fp32: what lies
-// around the products - conversions, operands through shared memory, barriers - at 55%
-// of the issue slots and 27% of the tensor pipe.
+// What bounds it.  Few rows: the keys' bytes (bf16, 16 trees of 4 tokens on 8192, groups of
+// 4, D 128: 91 us, 79 by the bytes; of 8 tokens, D 64, 70 and 40).  int8: the lines that a
+// row's heads share and their scales come from memory more than once (the same trees of 4
+// tokens 520 MB for 278, 91 us), and with more rows, as in fp32, what lies around the
+// products: conversions, operands through shared memory, barriers - 55% of the issue
+// slots and 27% of the tensor pipe.
 #pragma once
 
 #include <climits>

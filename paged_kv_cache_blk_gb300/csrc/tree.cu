@@ -139,10 +139,12 @@ int rows_unit(const PoolView& v, int64_t rows) {
   return rows <= 16 ? 16 : rows <= 32 ? 32 : most;
 }
 
-// How a tree call runs: units of unit_rows rows, split over `grid` CTAs.  tcgen05 from more than
-// 32 rows of a kv head on, where it can.  16 sequences on 8192, 8 kv heads, mma.sync and tcgen05:
-// 48 rows (a group of 4) 148 and 104 us, 64 rows 152 and 108, with D 64 109 and 91; one sequence
-// of 64 rows on 16384 37 and 26; 24 rows on 500, two sequences 13 and 12.
+// How a tree call runs: units of unit_rows rows, split over `grid` CTAs.  tcgen05, where it can,
+// from more than 16 rows of a kv head on with head_dim 128, 32 with 64 (its work does not depend
+// on the rows, that of mma.sync does).  mma.sync and tcgen05, 8 kv heads, groups of 4, D 128: 16
+// rows, 16 sequences on 8192 91 and 101 us, one on 8192 18 and 20; 32 rows 103 and 103, one on
+// 16384 27 and 25, on 30000 41 and 38; 64 rows 152 and 108.  D 64: 32 rows, 16 sequences on 8192
+// 70 and 87, one on 30000 28 and 30; 64 rows 109 and 91.
 struct TreePath {
   bool tcgen05;
   int unit_rows, grid;
@@ -154,7 +156,7 @@ TreePath tree_path(const PoolView& v, int G, int max_q_len, int sms) {
   TreePath t;
   t.lines = 1;
   const long long rows = (long long)max_q_len * G;
-  t.tcgen05 = rows > 32 && span_supported(v, G * v.num_kv_heads, false);
+  t.tcgen05 = rows > (v.head_dim == 128 ? 16 : 32) && span_supported(v, G * v.num_kv_heads, false);
   if (t.tcgen05) {
     const int tile = 128 / G * G;  // rows of whole tokens
     t.unit_rows = rows <= tile ? tile : 2 * tile;
@@ -202,7 +204,8 @@ bool prefill_on_tcgen05(const PoolView& v, const RowsParams& p, int sms) {
   const double heads = (double)p.plan.span.batch * v.num_kv_heads;
   const int tokens = 128 / p.plan.G, tiles_q = (p.plan.span.max_q_len + tokens - 1) / tokens;
   const double items = (tiles_q + 3) / 4 * heads;
-  const double pairs_us = std::ceil(items / (sms / 2)) * (p.keys_most / 128. * (d64 ? 1.9 : 2.3) + 8);
+  const double pairs_us =
+      std::ceil(items / (sms / 2)) * (p.keys_most / 128. * (d64 ? 1.9 : 2.3) + 8);
   const double units = p.units_max * heads, held = sms * rows_ctas_bf16(v.head_dim, 64);
   int ctas = kRowsMaxCluster;
   while (ctas > 1 && units * ctas > held) ctas >>= 1;
@@ -405,10 +408,13 @@ pkv_status pkv_decode_attention_tree(const pkv_pool* pool, int32_t layer, const 
   // 16384 28.0 us with 8, 26.4; of 8 on 30000 44.1, 41.0).  Many: registers for more of them (16
   // trees of 64 tokens 206 us with 8, 220 with 16).
   const bool few = (int64_t)m.blocks_seq * batch <= 2 * sms;
-  const auto kern = keys == 128  ? few ? pkv::tree_combine_kernel<128, 16> : pkv::tree_combine_kernel<128, 8>
-                    : keys == 64 ? few ? pkv::tree_combine_kernel<64, 16> : pkv::tree_combine_kernel<64, 8>
-                    : few        ? pkv::tree_combine_kernel<32, 16>
-                                 : pkv::tree_combine_kernel<32, 8>;
+  const auto kern =
+      few ? keys == 128  ? pkv::tree_combine_kernel<128, 16>
+            : keys == 64 ? pkv::tree_combine_kernel<64, 16>
+                         : pkv::tree_combine_kernel<32, 16>
+          : keys == 128  ? pkv::tree_combine_kernel<128, 8>
+            : keys == 64 ? pkv::tree_combine_kernel<64, 8>
+                         : pkv::tree_combine_kernel<32, 8>;
   st = pkv::launch_status(pkv::launch_kernel(kern, dim3((unsigned)(m.blocks_seq * batch)),
                                              dim3(pkv::kCombineWarps * 32), 0, stream, true, m));
   if (st != PKV_OK) return (pkv_status)st;
