@@ -2,6 +2,7 @@
 // pkv_prefill_attention_window): checks, choice of the kernel, and the merge of the states
 // that the tree kernels leave where a unit of work was split.
 #include <algorithm>
+#include <type_traits>
 
 #include "rows.cuh"
 
@@ -24,7 +25,7 @@ struct CombineParams {
 
 // One (token, query head) row, by one warp: the states of its unit in the CTAs that shared it,
 // by the log-sum-exp rule.  Rows that one CTA finished are left alone.
-// kInFlight: states that a warp loads at once.
+// kInFlight: states that a warp loads at once, where there are more than 4.
 template <int kInFlight>
 __device__ __forceinline__ void combine_row(const CombineParams& p, const SeqPlan& q, int b,
                                             long long chunk, long long before, int row) {
@@ -36,38 +37,37 @@ __device__ __forceinline__ void combine_row(const CombineParams& p, const SeqPla
       before + ((long long)(own_line ? 0 : g) * q.nru + unit) * q.steps + p.plan.lead;
   const long long c0 = div_pos(start, chunk), c1 = div_pos(start + q.t.nt - 1, chunk);
   if (c0 == c1) return;
-  const long long row_floats = p.D + 4, slot = ur * row_floats;
-  const float* at = p.part + (r - unit * ur) * row_floats;
-  // (the CTA with the unit's first tile left its part in slot 2 c + 1)
-  auto state = [&](long long c) {
-    return at + (2 * (c * p.lines + (own_line ? g : 0)) + (c == c0 ? 1 : 0)) * slot;
-  };
+  const long long row_floats = p.D + 4, slot = ur * row_floats, stride = 2 * p.lines * slot;
+  const float* first = p.part + (r - unit * ur) * row_floats + c0 * stride +
+                       (own_line ? 2 * g * slot : 0);
   const int pieces = (int)(c1 - c0) + 1, d = lane * 4;
   float top = -INFINITY, sum = 0.f, x[4] = {0.f, 0.f, 0.f, 0.f};
-  // a state's numbers and values are loaded together: one round trip for kInFlight of them
-  for (int i0 = 0; i0 < pieces; i0 += kInFlight) {
-    float2 ml[kInFlight];
-    float4 y[kInFlight];
+  // a state's numbers and values are loaded together: one round trip for N of them
+  auto merge = [&](auto n, int i0) {
+    constexpr int N = decltype(n)::value;
+    float2 ml[N];
+    float4 y[N];
 #pragma unroll
-    for (int u = 0; u < kInFlight; ++u) {
+    for (int u = 0; u < N; ++u) {
       ml[u] = make_float2(-INFINITY, 0.f);
       y[u] = make_float4(0.f, 0.f, 0.f, 0.f);
       if (i0 + u < pieces) {
-        const float* s = state(c0 + i0 + u);
+        // (the CTA with the unit's first tile left its part in its second slot)
+        const float* s = first + (i0 + u) * stride + (i0 + u == 0 ? slot : 0);
         ml[u] = *reinterpret_cast<const float2*>(s);
         if (d < p.D) y[u] = *reinterpret_cast<const float4*>(s + 4 + d);
       }
     }
     float most = top;
 #pragma unroll
-    for (int u = 0; u < kInFlight; ++u) most = fmaxf(most, ml[u].x);
+    for (int u = 0; u < N; ++u) most = fmaxf(most, ml[u].x);
     const float shrink = most == top ? 1.f : exp2f(top - most);
     top = most;
     sum *= shrink;
 #pragma unroll
     for (int e = 0; e < 4; ++e) x[e] *= shrink;
 #pragma unroll
-    for (int u = 0; u < kInFlight; ++u) {
+    for (int u = 0; u < N; ++u) {
       // a state at -inf saw nothing, or only NaN: its sum and O are 0, or NaN
       const float f = ml[u].x == -INFINITY ? 1.f : exp2f(ml[u].x - top);
       sum += f * ml[u].y;
@@ -76,6 +76,16 @@ __device__ __forceinline__ void combine_row(const CombineParams& p, const SeqPla
       x[2] += f * y[u].z;
       x[3] += f * y[u].w;
     }
+  };
+  // (states that are not there cost as much as the others: 16 trees of 64 tokens, of 2 to 4 states a
+  // row, MERGE_BEFORE with kInFlight alone, MERGE_AFTER)
+  if (pieces <= 2) {
+    merge(std::integral_constant<int, 2>(), 0);
+  } else if (pieces <= 4) {
+    merge(std::integral_constant<int, 4>(), 0);
+  } else {
+    for (int i0 = 0; i0 < pieces; i0 += kInFlight)
+      merge(std::integral_constant<int, kInFlight>(), i0);
   }
   if (d >= p.D) return;
   const float inv = sum == 0.f ? 0.f : 1.f / sum;  // no weight at all: zeros
