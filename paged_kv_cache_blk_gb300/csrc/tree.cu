@@ -78,7 +78,8 @@ __device__ __forceinline__ void combine_row(const CombineParams& p, const SeqPla
     }
   };
   // (states that are not there cost as much as the others: 16 trees of 64 tokens, of 2 to 4 states a
-  // row, MERGE_BEFORE with kInFlight alone, MERGE_AFTER)
+  // row, 208 us with kInFlight alone, 203; two rows at once, for more loads in flight, took registers
+  // that warps need more: 206)
   if (pieces <= 2) {
     merge(std::integral_constant<int, 2>(), 0);
   } else if (pieces <= 4) {
