@@ -44,12 +44,11 @@
 //     truncation, so the small products have a sum of their own, and O is not their
 //     accumulator: each tile's P V is summed from zero and added to O with rounding.
 //
-// What bounds it.  Few rows: the keys' bytes (bf16, 16 trees of 4 tokens on 8192, groups of
-// 4, D 128: 91 us, 79 by the bytes; of 8 tokens, D 64, 70 and 40).  int8: the lines that a
-// row's heads share and their scales come from memory more than once (the same trees of 4
-// tokens 520 MB for 278, 91 us), and with more rows, as in fp32, what lies around the
-// products: conversions, operands through shared memory, barriers - 55% of the issue
-// slots and 27% of the tensor pipe.
+// What bounds it.  Few rows of bf16: the keys' bytes (16 trees of 4 tokens on 8192, groups of 4,
+// D 128: 91 us, 79 by the bytes; of 8 tokens, D 64, 70 and 40).  int8 (the same trees of 4 tokens
+// 91 us, 41 by the bytes), and with more rows, as in fp32, what lies around the products:
+// conversions, operands through shared memory, barriers - 50 to 55% of the issue slots and a
+// quarter to a third of the tensor pipe.
 #pragma once
 
 #include <climits>

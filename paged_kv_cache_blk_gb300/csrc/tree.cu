@@ -183,7 +183,8 @@ TreePath tree_path(const PoolView& v, int G, int max_q_len, int sms) {
   // int8: a row's codes of one head share their last lines with the next head's, and the scales of
   // all heads are one sector: where the heads are read at the same time, each comes from memory
   // once.  So each head's line is split in the same way, and CTAs of one place follow one another,
-  // unless that leaves more than a tenth of the grid without work.
+  // unless that leaves more than a tenth of the grid without work (32 trees of 4 to 8 tokens behind
+  // 1024 to 8192: 579 MB and 125 us in one line, 327 MB and 122 us).
   if (v.quant) {
     const int pieces = t.grid / v.num_kv_heads;
     if (pieces > 0 && (t.grid - pieces * v.num_kv_heads) * 10 <= t.grid) {
