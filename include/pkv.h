@@ -731,6 +731,14 @@ PKV_API uint64_t pkv_get_wait_limit_ns(void);
  * PKV_ERR_INVALID_ARG.  Never needed outside tests. */
 PKV_API pkv_status pkv_set_debug_skip_fill(int32_t mode);
 
+/* Test hook, process-wide, default 0: pkv_prefill_attention_window chooses
+ * between its two kernels by what each is estimated to cost.  With 1 every call
+ * takes the mma.sync kernel, with 2 the tcgen05 one, and a call that this
+ * kernel cannot do returns PKV_ERR_UNSUPPORTED.  Results agree to the rounding
+ * that the call documents.  Other values: PKV_ERR_INVALID_ARG.  Never needed
+ * outside tests. */
+PKV_API pkv_status pkv_set_debug_window_path(int32_t path);
+
 /* Validate mode (process-wide, default off): see "Errors" above. */
 PKV_API pkv_status pkv_set_validate(int32_t on);
 PKV_API int32_t pkv_get_validate(void);

@@ -104,6 +104,7 @@ _SIGS = {
     "pkv_set_wait_limit_ns": (_I32, [ctypes.c_uint64]),
     "pkv_get_wait_limit_ns": (ctypes.c_uint64, []),
     "pkv_set_debug_skip_fill": (_I32, [_I32]),
+    "pkv_set_debug_window_path": (_I32, [_I32]),
     "pkv_get_validate": (_I32, []),
     "pkv_device_error": (_I32, [ctypes.POINTER(ctypes.c_int32), _I32]),
     "pkv_alloc_create": (_I32, [_I64, _I32, _P, ctypes.POINTER(ctypes.c_void_p)]),
@@ -811,6 +812,13 @@ def set_debug_skip_fill(mode: int) -> None:
     prefill launch leaves its first stage unfilled, so a wait there can only
     give up; 0 turns it off."""
     _check(load().pkv_set_debug_skip_fill(int(mode)), "pkv_set_debug_skip_fill")
+
+
+def set_debug_window_path(path: int) -> None:
+    """Test hook: ``prefill_attention_window`` takes the mma.sync kernel (1) or
+    the tcgen05 kernel (2, refused where that cannot) instead of the one that
+    its rule chooses (0)."""
+    _check(load().pkv_set_debug_window_path(int(path)), "pkv_set_debug_window_path")
 
 
 def get_validate() -> bool:

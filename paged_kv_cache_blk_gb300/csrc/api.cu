@@ -23,6 +23,7 @@ std::atomic<cudaEvent_t> g_ev_start{nullptr};
 std::atomic<cudaEvent_t> g_ev_stop{nullptr};
 std::atomic<unsigned long long> g_wait_ns{0};
 std::atomic<int> g_skip_fill{0};
+std::atomic<int> g_window_path{0};
 std::atomic<unsigned> g_epoch{0};
 
 struct DevInfo {
@@ -188,6 +189,8 @@ int launch_status(cudaError_t e) { return launched(e); }
 unsigned long long wait_limit_ns() { return g_wait_ns.load(); }
 
 int debug_skip_fill() { return g_skip_fill.load(); }
+
+int debug_window_path() { return g_window_path.load(); }
 
 int next_launch_epoch() {
   unsigned e = g_epoch.fetch_add(1) + 1;
@@ -620,6 +623,12 @@ uint64_t pkv_get_wait_limit_ns(void) {
 pkv_status pkv_set_debug_skip_fill(int32_t mode) {
   if (mode < 0 || mode > 2) return PKV_ERR_INVALID_ARG;
   g_skip_fill.store(mode);
+  return PKV_OK;
+}
+
+pkv_status pkv_set_debug_window_path(int32_t path) {
+  if (path < 0 || path > 2) return PKV_ERR_INVALID_ARG;
+  g_window_path.store(path);
   return PKV_OK;
 }
 

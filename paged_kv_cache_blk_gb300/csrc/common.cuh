@@ -417,6 +417,7 @@ cudaError_t launch_prefill(const PoolView& pv, int layer, const void* q, int num
 // launch with bounded waits (distinct, nonzero; see WaitCtl).
 unsigned long long wait_limit_ns();
 int debug_skip_fill();
+int debug_window_path();  // (pkv_set_debug_window_path)
 int next_launch_epoch();
 
 // Shared-prefix decode, prefix pass (on the prefill kernel): the key tiles of

@@ -45,7 +45,8 @@
 // heads: 128 / G tokens a tile, rows behind them zero) take a list of key tiles from
 // span.cuh, first tokens and window packed together, and a row's mask as words; V
 // rows that no query of the item sees are cleared in shared memory before they are
-// multiplied (a freed block may hold NaN).
+// multiplied (a freed block may hold NaN).  Rows that a V row of others spoiled are computed
+// again after the CTA's last item (repair.cuh).
 //  * kWindow: the CTA pairs of prefill; 8 prompts of 1024 to 8192 tokens under a window
 //    of 1024, 32 / 8 heads, D 128, 590 us (220 by the products alone).
 //  * kTree: a CTA an SM takes an even share of the batch's tiles, whatever the units
@@ -108,6 +109,7 @@ constexpr int kOffQ = 0;                              // Q_A, Q_B
 constexpr int kOffKV = 2 * kTileBytes;                // ring of kSlots tiles
 constexpr int kOffBar = kOffKV + kSlots * kTileBytes;
 constexpr int kOffTslot = kOffBar + 384;              // TMEM address, after the barriers
+constexpr int kOffSpoiled = kOffTslot + 16;           // first and last item with a marked row
 constexpr int kItemRing = 4;                          // items the loads warp publishes ahead
 constexpr int kOffItems = kOffBar + 512;              // [kItemRing][own item, lead item]
 constexpr int kSmemBytes = kOffItems + 1024 + 1024;   // + alignment slack
@@ -698,6 +700,45 @@ __device__ __forceinline__ long long item_of(const PfParams& p, long long c, uin
 // Each CTA waits for every release of its slots before it leaves (so no
 // copy or arrive of the other CTA still targets it), and the two leave
 // together (a cluster barrier).
+//
+// Windows and trees: rows that a value outside them spoiled (repair.cuh) are marked in the output,
+// and the CTA's first and last item with one kept in shared memory; they are computed again once
+// the CTA has left its pipeline (repair_marked).
+
+// A result's row (or a half of it) that is to be computed again, of the item at place `at` of the
+// CTA's walk.
+__device__ __forceinline__ void mark_spoiled(__nv_bfloat16* row, unsigned long long* spoiled,
+                                             long long at) {
+  *reinterpret_cast<volatile unsigned short*>(row) = kSpoiled;
+  atomicMin(spoiled, (unsigned long long)at);
+  atomicMax(spoiled + 1, (unsigned long long)at);
+}
+
+// The rows that an item's tiles have marked, by the warps of the CTA.
+template <int MODE, int HD>
+__device__ __forceinline__ void repair_item(const PfParams& p, const Item& it) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+  for (int x = MODE == kNarrow ? 1 : 0; x < 2; ++x) {  // (narrow trees: both tiles are the same rows)
+    if ((x == 0 ? it.nA : it.nB) == 0) continue;
+    const long long tok0 = (x == 0 ? it.qtA : it.qtB) * p.TQ;
+    const int rows = (int)min((long long)p.TQ, it.nq - tok0) * p.G;
+    for (int r0 = warp * 32; r0 < rows; r0 += warps * 32) {
+      const int r = r0 + lane;
+      bool marked = false;
+      if (r < rows) {
+        const unsigned short* row =
+            static_cast<const unsigned short*>(p.out) +
+            ((it.q0 + tok0 + r / p.G) * p.hq + (long long)it.g * p.G + r % p.G) * HD;
+        marked = __ldcg(row) == kSpoiled || (MODE == kNarrow && __ldcg(row + HD / 2) == kSpoiled);
+      }
+      for (unsigned todo = __ballot_sync(0xffffffffu, marked); todo; todo &= todo - 1) {
+        const int m = r0 + __ffs(todo) - 1;
+        repair_row(p.repair, it.b, (int)tok0 + m / p.G, it.g * p.G + m % p.G);
+      }
+    }
+  }
+}
+
 template <int MODE, bool SHARE, int HD>
 __global__ void __launch_bounds__((pf_threads<MODE, SHARE>()), 1)
     prefill_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk,
@@ -763,6 +804,8 @@ __global__ void __launch_bounds__((pf_threads<MODE, SHARE>()), 1)
     return (tile & 1 ? b_odd0 + 16u : b_pvdone0) + 8u * x;
   };
   Item* s_items = reinterpret_cast<Item*>(smem + kOffItems);
+  [[maybe_unused]] unsigned long long* spoiled =
+      reinterpret_cast<unsigned long long*>(smem + kOffSpoiled);
   auto slot_full = [&](int i) { return b_full0 + 8u * i; };
   auto slot_empty = [&](int i) { return b_empty0 + 8u * i; };
   auto slot_half = [&](int i) { return b_half0 + 8u * i; };
@@ -770,6 +813,8 @@ __global__ void __launch_bounds__((pf_threads<MODE, SHARE>()), 1)
   auto slot_ptr = [&](int i) { return smem + kOffKV + i * kTileBytes; };
 
   if (tid == 0) {
+    spoiled[0] = ~0ull;
+    spoiled[1] = 0;
     mbar_init(b_qfull, 1);
     mbar_init(b_qempty, 1);
     for (int i = 0; i < kSlots; ++i) {
@@ -1399,7 +1444,7 @@ __global__ void __launch_bounds__((pf_threads<MODE, SHARE>()), 1)
           mbar_arrive(b_ofree0 + 8u);
         }
         if (row_ok && !part && nonfinite(finite) && !nonfinite(sum))
-          repair_query<16>(p.repair, it.b, (int)qi, it.g * G + hh, x * (kD / 2), kD / 2);
+          mark_spoiled(orow + x * (kD / 2), spoiled, cur.at);
         continue;
       }
       if constexpr (PREFIX) {
@@ -1498,7 +1543,7 @@ __global__ void __launch_bounds__((pf_threads<MODE, SHARE>()), 1)
       if (lane == 0) mbar_arrive(b_ofree);
       if constexpr (SPAN) {
         if (row_ok && nonfinite(finite) && !nonfinite(st.l))
-          repair_query<16>(p.repair, it.b, (int)qi, it.g * G + hh, 0, kD);
+          mark_spoiled(orow, spoiled, TREE ? cur.at : i);
       }
     }
   }
@@ -1515,6 +1560,28 @@ __global__ void __launch_bounds__((pf_threads<MODE, SHARE>()), 1)
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem),
                  "r"(kTmemCols)
                  : "memory");
+  }
+  if constexpr (SPAN) {
+    // (the marks and the marked rows are this CTA's own, made before the barrier above)
+    const unsigned long long from = spoiled[0], to = spoiled[1];
+    if (from <= to) {
+      if constexpr (TREE) {
+        const PlanShare share =
+            plan_share<kKeys>(p.plan, blockIdx.x, gridDim.x, reinterpret_cast<long long*>(s_items));
+        TreeCursor<NARROW> walk{share.at, share.end, share.first, share.b};
+        Item it;
+        while (walk.next(p, it)) {
+          if ((unsigned long long)walk.at > to) break;
+          if ((unsigned long long)walk.at >= from && it.slot < 0) repair_item<MODE, kD>(p, it);
+        }
+      } else {
+        // (an item's place is where the walk stands behind it)
+        for (unsigned long long at = from; at <= to; at += i_step) {
+          const Item it = own_item((long long)at - i_step);
+          if (it.valid) repair_item<MODE, kD>(p, it);
+        }
+      }
+    }
   }
   if constexpr (PREFIX) griddep_wait();
 }

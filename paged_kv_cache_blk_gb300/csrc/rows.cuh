@@ -714,6 +714,7 @@ __device__ __forceinline__ void rows_piece(const RowsParams& p, const RowsPiece&
 #pragma unroll
     for (int u = 0; u < KG; ++u) x += row_part[u * M + tid];
     row_sum[tid] = x;
+    row_factor[tid] = 0.f;  // from here on: 1 where the row is to be computed again
   }
   __syncthreads();
   if constexpr (kI8) {  // O in units of 1
@@ -731,6 +732,7 @@ __device__ __forceinline__ void rows_piece(const RowsParams& p, const RowsPiece&
       }
   }
   // N dims from d on of row r's result
+  bool spoiled = false;
   auto finish = [&](int r, int d, float sum, const auto& x) {
     constexpr int N = sizeof(x) / sizeof(x[0]);
     const float inv = sum == 0.f ? 0.f : 1.f / sum;  // no weight at all: zeros
@@ -746,8 +748,20 @@ __device__ __forceinline__ void rows_piece(const RowsParams& p, const RowsPiece&
             pack_bf16x2(x[e] * inv, x[e + 1] * inv);
       finite &= !nonfinite(x[e]) && !nonfinite(x[e + 1]);
     }
-    if (!finite && !nonfinite(sum))
-      repair_query<4>(p.repair, w.b, tok, w.g * G + (r - tok * G), d, N);
+    if (!finite && !nonfinite(sum)) {
+      spoiled = true;
+      row_factor[r - w.first_row] = 1.f;
+    }
+  };
+  // over the whole CTA, and a barrier of it: the rows that a value outside them spoiled (repair.cuh)
+  auto repair_spoiled = [&] {
+    if (!__syncthreads_or(spoiled)) return;
+    for (int row = warp; row < M; row += kRowsWarps) {
+      if (row_factor[row] == 0.f) continue;
+      const int r = w.first_row + row, tok = r / G;
+      repair_row(p.repair, w.b, tok, w.g * G + (r - tok * G));
+    }
+    __syncthreads();
   };
   // this warp's values of a row: dim(u, c) is column c of output tile u
   auto dim = [&](int u, int c) {
@@ -820,11 +834,12 @@ __device__ __forceinline__ void rows_piece(const RowsParams& p, const RowsPiece&
         }
         finish(r, d, sum, x);
       }
+      repair_spoiled();
       cluster_sync();  // no CTA leaves while another may still read its states
       return;
     }
   }
-  __syncthreads();  // before the ring is filled again
+  repair_spoiled();  // (a barrier, too, before the ring is filled again)
 }
 
 // Tree: the batch's tiles split evenly over the grid (span.cuh).

@@ -88,17 +88,19 @@ __device__ __forceinline__ void combine_row(const CombineParams& p, const SeqPla
     for (int i0 = 0; i0 < pieces; i0 += kInFlight)
       merge(std::integral_constant<int, kInFlight>(), i0);
   }
-  if (d >= p.D) return;
   const float inv = sum == 0.f ? 0.f : 1.f / sum;  // no weight at all: zeros
   const long long dst = ((q.s.q0 + tok) * p.hq + h) * p.D + d;
-  if (p.f32)
-    *reinterpret_cast<float4*>(p.out + dst * 4) =
-        make_float4(x[0] * inv, x[1] * inv, x[2] * inv, x[3] * inv);
-  else
-    *reinterpret_cast<uint2*>(p.out + dst * 2) =
-        make_uint2(pack_bf16x2(x[0] * inv, x[1] * inv), pack_bf16x2(x[2] * inv, x[3] * inv));
-  if ((nonfinite(x[0]) || nonfinite(x[1]) || nonfinite(x[2]) || nonfinite(x[3])) && !nonfinite(sum))
-    repair_query<4>(p.repair, b, tok, h, d, 4);
+  if (d < p.D) {
+    if (p.f32)
+      *reinterpret_cast<float4*>(p.out + dst * 4) =
+          make_float4(x[0] * inv, x[1] * inv, x[2] * inv, x[3] * inv);
+    else
+      *reinterpret_cast<uint2*>(p.out + dst * 2) =
+          make_uint2(pack_bf16x2(x[0] * inv, x[1] * inv), pack_bf16x2(x[2] * inv, x[3] * inv));
+  }
+  // (lanes behind the dims hold zeros)
+  const bool bad = nonfinite(x[0]) || nonfinite(x[1]) || nonfinite(x[2]) || nonfinite(x[3]);
+  if (__any_sync(0xffffffffu, bad) && !nonfinite(sum)) repair_row(p.repair, b, tok, h);
 }
 
 // A CTA takes kCombineWarps * rows_warp rows of one sequence.
@@ -460,8 +462,10 @@ pkv_status pkv_prefill_attention_window(const pkv_pool* pool, int32_t layer, con
   p.units_max = (int)((rows + p.plan.unit_rows - 1) / p.plan.unit_rows);
   const int64_t held = (int64_t)max_blocks_per_seq * v.block_size;
   p.keys_most = std::min(held, (int64_t)window + p.plan.span.sink + p.plan.unit_rows / p.plan.G);
+  const int asked = pkv::debug_window_path();
+  if (asked == 2 && !pkv::span_supported(v, num_q_heads, true)) return PKV_ERR_UNSUPPORTED;
   const cudaError_t e =
-      pkv::prefill_on_tcgen05(v, p, sms)
+      (asked == 0 ? pkv::prefill_on_tcgen05(v, p, sms) : asked == 2)
           ? pkv::launch_prefill(v, layer, q, num_q_heads, scale, block_tables, max_blocks_per_seq,
                                 seq_lens, offsets, cu_q, batch, total_q, max_q_len, window,
                                 p.plan.span.sink, out, err, sms, stream, &p.repair)
