@@ -209,10 +209,11 @@ __device__ __forceinline__ void rows_piece(const RowsParams& p, const RowsPiece&
   auto seen_by_some = [&](int pos) {
     return pos >= off && pos <= off + w.hi && (pos >= off + w.lo || pos < sink_end);
   };
-  auto lookup = [&](int i) -> int {  // block of the lane's row in tile i, INT_MIN: a row of zeros
+  // block of the lane's row in tile i; INT_MIN: a row of zeros (ids below the pool's become -1)
+  auto lookup = [&](int i) -> int {
     if (i >= w.t1) return INT_MIN;
     const int pos = w.t.position(i * KT + my_r);
-    return seen_by_some(pos) ? table[pos >> p.bs_bits] : INT_MIN;
+    return seen_by_some(pos) ? max(table[pos >> p.bs_bits], -1) : INT_MIN;
   };
   auto issue = [&](int i, int stage, int blk, auto look) {
     if (i < w.t1) {
