@@ -520,7 +520,7 @@ PKV_API pkv_status pkv_prefill_attention(const pkv_pool* pool, int32_t layer, co
  * the window's `window` tokens, its own among them, and the first `sink`
  * tokens of the sequence, which stay visible.  window >= 1, sink >= 0
  * (PKV_ERR_INVALID_ARG).  Table entries whose block holds no key that a query of
- * the call sees are not read: their blocks may have been freed and the
+ * the call sees do not matter: their blocks may have been freed and the
  * entries may hold anything.  What a key or value row holds that a query does
  * not see, NaN and infinities included, does not reach that query's result.
  * Supported by both calls: any pool dtype; head_dim 64 or 128; any num_kv_heads;

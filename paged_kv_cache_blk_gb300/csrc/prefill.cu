@@ -110,6 +110,7 @@ constexpr int kOffKV = 2 * kTileBytes;                // ring of kSlots tiles
 constexpr int kOffBar = kOffKV + kSlots * kTileBytes;
 constexpr int kOffTslot = kOffBar + 384;              // TMEM address, after the barriers
 constexpr int kOffSpoiled = kOffTslot + 16;           // first and last item with a marked row
+constexpr int kOffBadEntry = kOffSpoiled + 16;        // trees: an entry outside the pool was met
 constexpr int kItemRing = 4;                          // items the loads warp publishes ahead
 constexpr int kOffItems = kOffBar + 512;              // [kItemRing][own item, lead item]
 constexpr int kSmemBytes = kOffItems + 1024 + 1024;   // + alignment slack
@@ -739,6 +740,18 @@ __device__ __forceinline__ void repair_item(const PfParams& p, const Item& it) {
   }
 }
 
+// Trees: the entries outside the pool among those of an item's tiles.
+__device__ __forceinline__ void report_entries(const PfParams& p, const Item& it) {
+  const int places = it.nB * kKeys;
+  for (int x = threadIdx.x * p.bs; x < places; x += blockDim.x * p.bs) {
+    const int e = it.list.position(it.t0 * kKeys + x) / p.bs;
+    if (e >= it.spanned) continue;
+    const int blk = p.bt[(long long)it.b * p.mb + e];
+    if (blk < 0 || blk >= p.num_blocks)
+      report_entry(p.plan.span, p.q_pos, p.mask, p.words, it.b, e, p.err);
+  }
+}
+
 template <int MODE, bool SHARE, int HD>
 __global__ void __launch_bounds__((pf_threads<MODE, SHARE>()), 1)
     prefill_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk,
@@ -806,6 +819,7 @@ __global__ void __launch_bounds__((pf_threads<MODE, SHARE>()), 1)
   Item* s_items = reinterpret_cast<Item*>(smem + kOffItems);
   [[maybe_unused]] unsigned long long* spoiled =
       reinterpret_cast<unsigned long long*>(smem + kOffSpoiled);
+  [[maybe_unused]] volatile int* bad_entry = reinterpret_cast<int*>(smem + kOffBadEntry);
   auto slot_full = [&](int i) { return b_full0 + 8u * i; };
   auto slot_empty = [&](int i) { return b_empty0 + 8u * i; };
   auto slot_half = [&](int i) { return b_half0 + 8u * i; };
@@ -815,6 +829,7 @@ __global__ void __launch_bounds__((pf_threads<MODE, SHARE>()), 1)
   if (tid == 0) {
     spoiled[0] = ~0ull;
     spoiled[1] = 0;
+    *bad_entry = 0;
     mbar_init(b_qfull, 1);
     mbar_init(b_qempty, 1);
     for (int i = 0; i < kSlots; ++i) {
@@ -958,7 +973,10 @@ __global__ void __launch_bounds__((pf_threads<MODE, SHARE>()), 1)
         if (lb >= lead.spanned) return -1;
         const int blk = p.bt[(long long)lead.b * p.mb + lb];
         if (blk >= 0 && blk < p.num_blocks) return blk;
-        set_error(p.err, kErrIndex);
+        if constexpr (TREE)
+          *bad_entry = 1;  // looked into at the end
+        else
+          set_error(p.err, kErrIndex);
         return -1;
       };
       [[maybe_unused]] int ahead = -1, now = -1;
@@ -1564,15 +1582,17 @@ __global__ void __launch_bounds__((pf_threads<MODE, SHARE>()), 1)
   if constexpr (SPAN) {
     // (the marks and the marked rows are this CTA's own, made before the barrier above)
     const unsigned long long from = spoiled[0], to = spoiled[1];
-    if (from <= to) {
+    const bool look = TREE && *bad_entry != 0;
+    if (from <= to || look) {
       if constexpr (TREE) {
         const PlanShare share =
             plan_share<kKeys>(p.plan, blockIdx.x, gridDim.x, reinterpret_cast<long long*>(s_items));
         TreeCursor<NARROW> walk{share.at, share.end, share.first, share.b};
         Item it;
         while (walk.next(p, it)) {
-          if ((unsigned long long)walk.at > to) break;
-          if ((unsigned long long)walk.at >= from && it.slot < 0) repair_item<MODE, kD>(p, it);
+          const unsigned long long at = (unsigned long long)walk.at;
+          if (at >= from && at <= to && it.slot < 0) repair_item<MODE, kD>(p, it);
+          if (look) report_entries(p, it);
         }
       } else {
         // (an item's place is where the walk stands behind it)

@@ -177,7 +177,7 @@ struct RowsPiece {
 
 template <int MODE, int D, int M, bool TREE>
 __device__ __forceinline__ void rows_piece(const RowsParams& p, const RowsPiece& w, int ctas,
-                                           unsigned char* smem) {
+                                           unsigned char* smem, volatile int* bad_entry = nullptr) {
   using Tl = RowsTile<MODE, D, M>;
   using Lay = RowsLayout<MODE, D, M>;
   constexpr bool kI8 = MODE == PKV_I8, kF32 = MODE == PKV_F32, kTwoParts = Lay::kTwoParts;
@@ -219,7 +219,10 @@ __device__ __forceinline__ void rows_piece(const RowsParams& p, const RowsPiece&
     if (i < w.t1) {
       const int pos = w.t.position(i * KT + my_r);
       if (blk != INT_MIN && (blk < 0 || blk >= p.num_blocks)) {
-        set_error(p.err, kErrIndex);
+        if constexpr (TREE)
+          *bad_entry = 1;  // looked into at the end
+        else
+          set_error(p.err, kErrIndex);
         blk = INT_MIN;
       }
       const unsigned live = __ballot_sync(kAllLanes, blk != INT_MIN);
@@ -841,6 +844,20 @@ __device__ __forceinline__ void rows_piece(const RowsParams& p, const RowsPiece&
     }
   }
   repair_spoiled();  // (a barrier, too, before the ring is filled again)
+  if constexpr (TREE) {
+    if (*bad_entry) {  // a table entry outside the pool
+      for (int x = w.t0 * KT + tid; x < w.t1 * KT; x += kRowsThreads) {
+        const int pos = w.t.position(x), e = pos >> p.bs_bits;
+        if (!seen_by_some(pos) || (x > w.t0 * KT && w.t.position(x - 1) >> p.bs_bits == e)) continue;
+        const int blk = table[e];
+        if (blk < 0 || blk >= p.num_blocks)
+          report_entry(p.plan.span, p.q_pos, p.mask, p.words, w.b, e, p.err);
+      }
+      __syncthreads();
+      if (tid == 0) *bad_entry = 0;
+      __syncthreads();
+    }
+  }
 }
 
 // Tree: the batch's tiles split evenly over the grid (span.cuh).
@@ -850,6 +867,8 @@ __global__ void __launch_bounds__(kRowsThreads, (RowsLayout<MODE, D, M>::kCtas))
   constexpr int KT = RowsTile<MODE, D, M>::kKeys;
   extern __shared__ __align__(128) unsigned char smem[];
   __shared__ long long scratch[32];
+  __shared__ int bad_entry;
+  if (threadIdx.x == 0) bad_entry = 0;
   griddep_wait();
   griddep_launch_dependents();
   const int line_of = (int)blockIdx.x % p.lines;
@@ -902,7 +921,7 @@ __global__ void __launch_bounds__(kRowsThreads, (RowsLayout<MODE, D, M>::kCtas))
     w.part = nullptr;
     if (w.t0 > 0 || w.t1 < q.t.nt)
       w.part = p.part + (2ll * blockIdx.x + (w.t0 == 0 ? 1 : 0)) * (M * (D + 4));
-    rows_piece<MODE, D, M, true>(p, w, 1, smem);
+    rows_piece<MODE, D, M, true>(p, w, 1, smem, &bad_entry);
   }
 }
 

@@ -143,6 +143,31 @@ __device__ __forceinline__ RowSees row_sees(const SpanParams& p, const KeyList& 
   return r;
 }
 
+// An entry of sequence b's table that is outside the pool: an error where some query sees a key of
+// its block.  A windowed call lists no others; a tree's list begins with the window of a token right
+// behind the context and holds every drafted token, so here the queries are asked (positions may all
+// be later, and a bit may be set in no row).  Off the usual path.
+static __device__ __noinline__ void report_entry(const SpanParams& p, const int32_t* q_pos,
+                                                 const unsigned long long* mask, int words, int b,
+                                                 int entry, int* err) {
+  const SeqSpan s = seq_span(p, b);
+  const int first = max(0, entry * p.bs - s.off);  // the block's keys: first .. end - 1
+  const int end = min(s.ctx + s.n, (entry + 1) * p.bs - s.off);
+  bool seen = mask == nullptr || (first < s.ctx && (p.window == 0 || first < p.sink));
+  const int last_ctx = min(end, s.ctx) - 1, d0 = max(first, s.ctx) - s.ctx, d1 = end - 1 - s.ctx;
+  for (int i = 0; i < s.n && !seen; ++i) {
+    const long long query = s.q0 + i;
+    const int pos = q_pos ? max(s.ctx, q_pos[query]) : s.ctx + i;
+    seen = last_ctx >= first && last_ctx > (long long)pos - p.window;
+    for (int w = d0 >> 6; d1 >= d0 && w <= d1 >> 6; ++w) {
+      const int lo = max(d0 - 64 * w, 0), hi = min(d1 - 64 * w, 63);
+      const unsigned long long of_block = (~0ull << lo) & (~0ull >> (63 - hi));
+      seen |= (mask[query * words + w] & of_block) != 0;
+    }
+  }
+  if (seen) set_error(err, kErrIndex);
+}
+
 // ---- one list of tiles for a batch, split evenly over a grid --------------------------
 //
 // A unit is UR query rows (tokens x heads of a group) of one sequence and kv head over
@@ -295,9 +320,10 @@ __device__ __forceinline__ PlanShare plan_share(const PlanParams& p, int cta, in
 }
 
 // Host side (tree.cu): checks the sequences and the table entries that hold a key which is
-// seen, for validate mode.
-cudaError_t launch_validate_spans(const SpanParams& p, const int32_t* bt, long long num_blocks,
-                                  int* err, cudaStream_t s);
+// seen, for validate mode (trees: with their positions and mask).
+cudaError_t launch_validate_spans(const SpanParams& p, const int32_t* q_pos,
+                                  const unsigned long long* mask, int words, const int32_t* bt,
+                                  long long num_blocks, int* err, cudaStream_t s);
 
 struct Repair;  // repair.cuh
 

@@ -1064,8 +1064,8 @@ extern "C" pkv_status pkv_decode_attention_window(
     sp.window = window;
     sp.sink = p.sink;
     if ((st = pkv::clear_error_word(err, stream)) != PKV_OK) return (pkv_status)st;
-    if ((st = pkv::launch_status(pkv::launch_validate_spans(sp, block_tables, v.num_blocks, err,
-                                                            stream))) != PKV_OK)
+    if ((st = pkv::launch_status(pkv::launch_validate_spans(sp, nullptr, nullptr, 0, block_tables,
+                                                            v.num_blocks, err, stream))) != PKV_OK)
       return (pkv_status)st;
     if ((st = pkv::read_and_clear_error_word(err, stream)) != PKV_OK) return (pkv_status)st;
   }

@@ -130,8 +130,9 @@ __global__ void __launch_bounds__(kCombineWarps * 32)
 }
 
 // One CTA a sequence: its numbers, and the entries of the blocks that hold a seen key.
-__global__ void validate_spans_kernel(const SpanParams p, const int32_t* bt, long long num_blocks,
-                                      int* err) {
+__global__ void validate_spans_kernel(const SpanParams p, const int32_t* q_pos,
+                                      const unsigned long long* mask, int words, const int32_t* bt,
+                                      long long num_blocks, int* err) {
   const int b = blockIdx.x;
   const SeqSpan s = seq_span(p, b);
   if (s.bad && threadIdx.x == 0) set_error(err, kErrCapacity);
@@ -142,7 +143,7 @@ __global__ void validate_spans_kernel(const SpanParams p, const int32_t* bt, lon
     const int first = max(s.off, e * p.bs), end = min(last + 1, (e + 1) * p.bs);
     if (end <= lo && first >= sink_end) continue;
     const int blk = bt[(long long)b * p.mb + e];
-    if (blk < 0 || blk >= num_blocks) set_error(err, kErrIndex);
+    if (blk < 0 || blk >= num_blocks) report_entry(p, q_pos, mask, words, b, e, err);
   }
 }
 
@@ -324,17 +325,18 @@ RowsParams rows_params(const Call& c, const PoolView& v, int* err) {
 int validate_call(const RowsParams& p, cudaStream_t stream) {
   int st;
   if ((st = clear_error_word(p.err, stream)) != PKV_OK) return st;
-  if ((st = launch_status(launch_validate_spans(p.plan.span, p.bt, p.num_blocks, p.err,
-                                                stream))) != PKV_OK)
+  if ((st = launch_status(launch_validate_spans(p.plan.span, p.q_pos, p.mask, p.words, p.bt,
+                                                p.num_blocks, p.err, stream))) != PKV_OK)
     return st;
   return read_and_clear_error_word(p.err, stream);
 }
 
 }  // namespace
 
-cudaError_t launch_validate_spans(const SpanParams& p, const int32_t* bt, long long num_blocks,
-                                  int* err, cudaStream_t s) {
-  validate_spans_kernel<<<(unsigned)p.batch, 128, 0, s>>>(p, bt, num_blocks, err);
+cudaError_t launch_validate_spans(const SpanParams& p, const int32_t* q_pos,
+                                  const unsigned long long* mask, int words, const int32_t* bt,
+                                  long long num_blocks, int* err, cudaStream_t s) {
+  validate_spans_kernel<<<(unsigned)p.batch, 128, 0, s>>>(p, q_pos, mask, words, bt, num_blocks, err);
   return cudaGetLastError();
 }
 

@@ -1,5 +1,5 @@
 """Table entries of windowed calls and trees: any id outside the pool is an error where a query sees a
-key of its block."""
+key of its block, and no entry matters whose block holds no seen key."""
 
 import numpy as np
 import pytest
@@ -77,4 +77,44 @@ def test_ids_outside_the_pool(dev, window_path, what, dtype, D, bad):
         return s
 
     c.check(got, *kv, seen_of, _weight_err(dtype, n * 4 > 16), fma=what == "window")
+    _both(call, "PKV_ERR_INDEX")
+
+
+@pytest.mark.parametrize("dtype,G,D,bs,n", [
+    ("bf16", 4, 128, 16, 40), ("bf16", 4, 128, 16, 6), ("bf16", 2, 128, 16, 100), ("bf16", 4, 64, 16, 20),
+    ("bf16", 4, 64, 4, 20), ("f32", 3, 64, 8, 30), ("i8", 4, 128, 16, 24), ("i8", 2, 64, 16, 4)])
+def test_entries_that_no_query_of_a_tree_sees(dev, dtype, G, D, bs, n):
+    """Positions that all lie above the context's end leave its oldest window tokens behind, and bits
+    that no row sets hide drafted tokens: entries of blocks with nothing else may hold anything."""
+    window, sink, ctx = 50, 3, 150
+    c = Case(dev, dtype, 2, G, D, bs, [ctx + n, 70 + n], [n, n], seed=72)
+    kv = c.values(c.k), c.values(c.v)
+    sees = np.tril(np.ones((n, n), bool))
+    hidden = slice(n // 3, n // 3 + max(1, n // 2))
+    sees[:, hidden] = False
+    depth = np.arange(n) + 45  # (the windows begin in the context for the first five tokens)
+    mask, pos = _tree_args(c, [sees, sees], [depth, depth], -(-n // 64))
+
+    def seen_of(b, i):
+        at = int(c.lens[b] - n)
+        return MK.tree_seen(at, sees, i, at + int(depth[i]), window, sink)
+
+    some = []
+    for b in range(2):
+        s = np.zeros(int(c.lens[b]), bool)
+        for i in range(n):
+            s |= seen_of(b, i)
+        some.append(s)
+    c.poison(some)
+    call = lambda: _tree(c, mask, pos, window, sink)
+    got = call()
+    assert pkv.device_error() == "PKV_OK"
+    c.check(got, *kv, seen_of, _weight_err(dtype, n * G > 16))
+    _both(call, "PKV_OK")
+    # the block of the first token that only some rows see
+    b_seen = int(c.offs[0] + ctx + n - 1) // bs
+    c.table[0, b_seen] = -1
+    _both(call, "PKV_ERR_INDEX")
+    c.table[0, b_seen] = c.home[0, b_seen]
+    c.table[1, 0] = 1 << 30
     _both(call, "PKV_ERR_INDEX")
