@@ -607,24 +607,38 @@ def decode_attention_sparse(pool: Pool, layer: int, q: torch.Tensor, scale: floa
     _check(st, "pkv_decode_attention_sparse")
 
 
+def _given(**tensors: Optional[torch.Tensor]) -> None:
+    for name, t in tensors.items():
+        if t is None:
+            raise ValueError(f"{name} must be given")
+
+
 def _sequences(pool: Pool, block_tables: torch.Tensor, seq_lens: torch.Tensor,
-               offsets: Optional[torch.Tensor], cu_q: Optional[torch.Tensor]):
-    """Checks of the tables, lengths and offsets of a batch (and of where its
-    queries lie), and their pointers and numbers."""
+               offsets: Optional[torch.Tensor]):
+    """Checks of the tables, lengths and offsets of a batch, and their pointers
+    and numbers."""
+    _given(block_tables=block_tables, seq_lens=seq_lens)
     bt, lens = _index(block_tables, pool, "block_tables", 2), _index(seq_lens, pool, "seq_lens", 1)
     offs = _index(offsets, pool, "offsets", 1)
     B, mb = block_tables.shape
     if seq_lens.shape[0] != B or (offsets is not None and offsets.shape[0] != B):
         raise ValueError("seq_lens and offsets must have one entry per row of block_tables")
-    if cu_q is not None and (cu_q.dtype is not torch.int64 or cu_q.get_device() != pool.index
-                             or cu_q.shape != (B + 1,) or not cu_q.is_contiguous()):
-        raise ValueError(f"cu_q must be a contiguous int64 tensor of {B + 1} entries on "
-                         f"{pool.device}")
     return bt, mb, lens, offs, B
+
+
+def _new_tokens(pool: Pool, cu_q: torch.Tensor, batch: int) -> int:
+    """Check of where the new tokens of a batch lie, and its pointer."""
+    _given(cu_q=cu_q)
+    if cu_q.dtype is not torch.int64 or cu_q.get_device() != pool.index \
+            or cu_q.shape != (batch + 1,) or not cu_q.is_contiguous():
+        raise ValueError(f"cu_q must be a contiguous int64 tensor of {batch + 1} entries on "
+                         f"{pool.device}")
+    return cu_q.data_ptr()
 
 
 def _attended(pool: Pool, q: torch.Tensor, out: torch.Tensor, rows: Optional[int] = None) -> int:
     """Checks of q and out ([rows, Hq, D], contiguous); the number of heads."""
+    _given(q=q, out=out)
     hq = _heads_of(q)
     shape = (q.shape[0] if rows is None else rows, hq, pool.head_dim)
     for t, name in ((q, "q"), (out, "out")):
@@ -640,7 +654,7 @@ def decode_attention_window(pool: Pool, layer: int, q: torch.Tensor, scale: floa
     """Decode attention of ``q`` ([B, Hq, D]) into ``out`` over the last
     ``window`` tokens of each sequence and its first ``sink``."""
     lib = load()
-    bt, mb, lens, offs, B = _sequences(pool, block_tables, seq_lens, offsets, None)
+    bt, mb, lens, offs, B = _sequences(pool, block_tables, seq_lens, offsets)
     hq = _attended(pool, q, out, B)
     with _dev(pool):
         st = lib.pkv_decode_attention_window(pool.ref, layer, q.data_ptr(), hq, float(scale), bt,
@@ -657,11 +671,12 @@ def prefill_attention_window(pool: Pool, layer: int, q: torch.Tensor, scale: flo
     of each sequence) into ``out``, each token over the last ``window`` tokens
     up to its own and the first ``sink``."""
     lib = load()
-    bt, mb, lens, offs, B = _sequences(pool, block_tables, seq_lens, offsets, cu_q)
+    bt, mb, lens, offs, B = _sequences(pool, block_tables, seq_lens, offsets)
+    cu = _new_tokens(pool, cu_q, B)
     hq = _attended(pool, q, out)
     with _dev(pool):
         st = lib.pkv_prefill_attention_window(pool.ref, layer, q.data_ptr(), hq, float(scale), bt,
-                                              mb, lens, offs, cu_q.data_ptr(), B, q.shape[0],
+                                              mb, lens, offs, cu, B, q.shape[0],
                                               max_q_len, window, sink, out.data_ptr(),
                                               _stream(pool.device))
     _check(st, "pkv_prefill_attention_window")
@@ -688,7 +703,8 @@ def decode_attention_tree(pool: Pool, layer: int, q: torch.Tensor, scale: float,
     another.  ``window`` (0: none) and ``sink`` limit the context around
     ``q_pos`` (int32 [T], positions along the tree)."""
     lib = load()
-    bt, mb, lens, offs, B = _sequences(pool, block_tables, seq_lens, offsets, cu_q)
+    bt, mb, lens, offs, B = _sequences(pool, block_tables, seq_lens, offsets)
+    cu = _new_tokens(pool, cu_q, B)
     hq = _attended(pool, q, out)
     T, words, mask = q.shape[0], 0, None
     if tree_mask is not None:
@@ -705,11 +721,12 @@ def decode_attention_tree(pool: Pool, layer: int, q: torch.Tensor, scale: float,
         raise ValueError("q_pos goes with tree_mask and has one entry per token")
     if T == 0:  # (tensors of no elements have no address)
         words, mask, qp = 0, None, None
+    _given(workspace=workspace)
     if workspace.get_device() != pool.index or not workspace.is_contiguous():
         raise ValueError(f"workspace must be a contiguous tensor on {pool.device}")
     with _dev(pool):
         st = lib.pkv_decode_attention_tree(pool.ref, layer, q.data_ptr(), hq, float(scale), bt, mb,
-                                           lens, offs, cu_q.data_ptr(), B, T, max_q_len, mask,
+                                           lens, offs, cu, B, T, max_q_len, mask,
                                            words, qp, window, sink, out.data_ptr(),
                                            workspace.data_ptr(),
                                            workspace.numel() * workspace.element_size(),
@@ -724,12 +741,14 @@ def accept_tokens(pool: Pool, layer: int, block_tables: torch.Tensor, seq_lens: 
     context: ``accepted`` (int32 [B, most]) holds the ``count`` (int32 [B])
     ascending indices of each sequence; one layer or every one (-1)."""
     lib = load()
-    bt, mb, lens, offs, B = _sequences(pool, block_tables, seq_lens, offsets, cu_q)
+    _given(accepted=accepted, count=count)
+    bt, mb, lens, offs, B = _sequences(pool, block_tables, seq_lens, offsets)
+    cu = _new_tokens(pool, cu_q, B)
     path, cnt = _index(accepted, pool, "accepted", 2), _index(count, pool, "count", 1)
     if accepted.shape[0] != B or count.shape[0] != B:
         raise ValueError("accepted and count must have one entry per row of block_tables")
     with _dev(pool):
-        st = lib.pkv_accept_tokens(pool.ref, layer, bt, mb, lens, offs, cu_q.data_ptr(), B, path,
+        st = lib.pkv_accept_tokens(pool.ref, layer, bt, mb, lens, offs, cu, B, path,
                                    accepted.shape[1], cnt, _stream(pool.device))
     _check(st, "pkv_accept_tokens")
 

@@ -93,3 +93,32 @@ def test_import_without_torchs_short_cut():
             "from paged_kv_cache_blk_gb300 import _binding as B\n"
             "assert B._raw_stream is None\n")
     assert subprocess.run([sys.executable, "-c", code]).returncode == 0
+
+
+def test_a_tensor_that_is_not_given_is_refused_by_name():
+    """None for a tensor that a windowed call, a tree or a move of accepted rows needs: a ValueError, as
+    for any other wrong argument."""
+    i = lambda *s: torch.zeros(s, dtype=torch.int32)
+    pool = pkv.Pool(torch.zeros(4, 1, 16, 2, 64), torch.zeros(4, 1, 16, 2, 64))
+    pool.index = -1  # (host tensors pass as the pool's)
+    q, out, cu = torch.zeros(2, 4, 64), torch.zeros(2, 4, 64), torch.zeros(3, dtype=torch.int64)
+    good = dict(q=q, out=out, block_tables=i(2, 4), seq_lens=i(2), cu_q=cu, workspace=torch.zeros(64),
+                accepted=i(2, 5), count=i(2))
+    calls = {
+        "window": (lambda a: pkv.decode_attention_window(
+            pool, 0, a["q"], 0.1, a["block_tables"], a["seq_lens"], None, 4, a["out"]),
+            ("q", "out", "block_tables", "seq_lens")),
+        "prefill": (lambda a: pkv.prefill_attention_window(
+            pool, 0, a["q"], 0.1, a["block_tables"], a["seq_lens"], None, a["cu_q"], 1, 4, a["out"]),
+            ("q", "out", "block_tables", "seq_lens", "cu_q")),
+        "tree": (lambda a: pkv.decode_attention_tree(
+            pool, 0, a["q"], 0.1, a["block_tables"], a["seq_lens"], None, a["cu_q"], 1, None, a["out"],
+            a["workspace"]), ("q", "out", "block_tables", "seq_lens", "cu_q", "workspace")),
+        "accept": (lambda a: pkv.accept_tokens(
+            pool, -1, a["block_tables"], a["seq_lens"], None, a["cu_q"], a["accepted"], a["count"]),
+            ("block_tables", "seq_lens", "cu_q", "accepted", "count")),
+    }
+    for what, (call, needed) in calls.items():
+        for name in needed:
+            with pytest.raises(ValueError, match=name):
+                call({**good, name: None})
