@@ -607,17 +607,17 @@ def decode_attention_sparse(pool: Pool, layer: int, q: torch.Tensor, scale: floa
     _check(st, "pkv_decode_attention_sparse")
 
 
-def _given(**tensors: Optional[torch.Tensor]) -> None:
-    for name, t in tensors.items():
-        if t is None:
-            raise ValueError(f"{name} must be given")
+def _refuse_none(**tensors: Optional[torch.Tensor]) -> None:
+    missing = [name for name, t in tensors.items() if t is None]
+    raise ValueError(f"{', '.join(missing)} must be given")
 
 
 def _sequences(pool: Pool, block_tables: torch.Tensor, seq_lens: torch.Tensor,
                offsets: Optional[torch.Tensor]):
     """Checks of the tables, lengths and offsets of a batch, and their pointers
     and numbers."""
-    _given(block_tables=block_tables, seq_lens=seq_lens)
+    if block_tables is None or seq_lens is None:
+        _refuse_none(block_tables=block_tables, seq_lens=seq_lens)
     bt, lens = _index(block_tables, pool, "block_tables", 2), _index(seq_lens, pool, "seq_lens", 1)
     offs = _index(offsets, pool, "offsets", 1)
     B, mb = block_tables.shape
@@ -628,7 +628,8 @@ def _sequences(pool: Pool, block_tables: torch.Tensor, seq_lens: torch.Tensor,
 
 def _new_tokens(pool: Pool, cu_q: torch.Tensor, batch: int) -> int:
     """Check of where the new tokens of a batch lie, and its pointer."""
-    _given(cu_q=cu_q)
+    if cu_q is None:
+        _refuse_none(cu_q=cu_q)
     if cu_q.dtype is not torch.int64 or cu_q.get_device() != pool.index \
             or cu_q.shape != (batch + 1,) or not cu_q.is_contiguous():
         raise ValueError(f"cu_q must be a contiguous int64 tensor of {batch + 1} entries on "
@@ -638,7 +639,8 @@ def _new_tokens(pool: Pool, cu_q: torch.Tensor, batch: int) -> int:
 
 def _attended(pool: Pool, q: torch.Tensor, out: torch.Tensor, rows: Optional[int] = None) -> int:
     """Checks of q and out ([rows, Hq, D], contiguous); the number of heads."""
-    _given(q=q, out=out)
+    if q is None or out is None:
+        _refuse_none(q=q, out=out)
     hq = _heads_of(q)
     shape = (q.shape[0] if rows is None else rows, hq, pool.head_dim)
     for t, name in ((q, "q"), (out, "out")):
@@ -721,7 +723,8 @@ def decode_attention_tree(pool: Pool, layer: int, q: torch.Tensor, scale: float,
         raise ValueError("q_pos goes with tree_mask and has one entry per token")
     if T == 0:  # (tensors of no elements have no address)
         words, mask, qp = 0, None, None
-    _given(workspace=workspace)
+    if workspace is None:
+        _refuse_none(workspace=workspace)
     if workspace.get_device() != pool.index or not workspace.is_contiguous():
         raise ValueError(f"workspace must be a contiguous tensor on {pool.device}")
     with _dev(pool):
@@ -741,7 +744,8 @@ def accept_tokens(pool: Pool, layer: int, block_tables: torch.Tensor, seq_lens: 
     context: ``accepted`` (int32 [B, most]) holds the ``count`` (int32 [B])
     ascending indices of each sequence; one layer or every one (-1)."""
     lib = load()
-    _given(accepted=accepted, count=count)
+    if accepted is None or count is None:
+        _refuse_none(accepted=accepted, count=count)
     bt, mb, lens, offs, B = _sequences(pool, block_tables, seq_lens, offsets)
     cu = _new_tokens(pool, cu_q, B)
     path, cnt = _index(accepted, pool, "accepted", 2), _index(count, pool, "count", 1)
