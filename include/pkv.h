@@ -575,7 +575,11 @@ PKV_API pkv_status pkv_prefill_attention_window(const pkv_pool* pool, int32_t la
  *   - drafted token j where bit j % 64 of
  *     tree_mask[(cu_q[b] + i) * mask_words + j / 64] is set, j < n_b: for a
  *     tree, the token itself and what it hangs on.  The bits alone decide
- *     among drafted tokens; bits from n_b on are ignored.
+ *     among drafted tokens, under a window too: a window layer's mask has to
+ *     leave out the tokens that the window of a branch has passed (those j
+ *     with q_pos of j <= P - window, but for the first `sink` positions);
+ *     they are then hidden as the chain below hides them.  Bits from n_b on
+ *     are ignored.
  * tree_mask NULL (mask_words 0, q_pos NULL): a chain; query i sees the keys up
  * to ctx + i, under the window if there is one, as in
  * pkv_prefill_attention_window.  window 0: no window (sink is then ignored).
