@@ -734,7 +734,7 @@ __device__ __forceinline__ void repair_item(const PfParams& p, const Item& it) {
       }
       for (unsigned todo = __ballot_sync(0xffffffffu, marked); todo; todo &= todo - 1) {
         const int m = r0 + __ffs(todo) - 1;
-        repair_row(p.repair, it.b, (int)tok0 + m / p.G, it.g * p.G + m % p.G);
+        repair_row<4>(p.repair, it.b, (int)tok0 + m / p.G, it.g * p.G + m % p.G);
       }
     }
   }

@@ -38,29 +38,30 @@ struct Repair {
   float qscale;  // scale * log2(e)
 };
 
-// E elements of a row from number i on (a multiple of E), E = 2 or 4.
-template <int E>
-__device__ __forceinline__ void repair_elements(const char* row, int dtype, int i, float (&x)[E]) {
+// Four elements of a row from number i on (a multiple of four).
+__device__ __forceinline__ void repair_elements(const char* row, int dtype, int i, float (&x)[4]) {
   if (dtype == PKV_F32) {
-    const float2* a = reinterpret_cast<const float2*>(row) + i / 2;
-#pragma unroll
-    for (int e = 0; e < E / 2; ++e) x[2 * e] = a[e].x, x[2 * e + 1] = a[e].y;
+    const float4 a = *reinterpret_cast<const float4*>(row + 4 * i);
+    x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w;
   } else if (dtype == PKV_BF16) {
-    const uint32_t* a = reinterpret_cast<const uint32_t*>(row) + i / 2;
-#pragma unroll
-    for (int e = 0; e < E / 2; ++e) x[2 * e] = bf16_lo(a[e]), x[2 * e + 1] = bf16_hi(a[e]);
+    const uint2 a = *reinterpret_cast<const uint2*>(row + 2 * i);
+    x[0] = bf16_lo(a.x), x[1] = bf16_hi(a.x), x[2] = bf16_lo(a.y), x[3] = bf16_hi(a.y);
   } else {
-    const uchar2* a = reinterpret_cast<const uchar2*>(row) + i / 2;
-#pragma unroll
-    for (int e = 0; e < E / 2; ++e) x[2 * e] = a[e].x - 128.f, x[2 * e + 1] = a[e].y - 128.f;
+    const uchar4 a = *reinterpret_cast<const uchar4*>(row + i);
+    x[0] = a.x - 128.f, x[1] = a.y - 128.f, x[2] = a.z - 128.f, x[3] = a.w - 128.f;
   }
 }
 
-// The result of token tok and query head h of sequence b.
-template <int E>
-static __device__ __noinline__ void repair_row_of(const Repair& p, int b, int tok, int h) {
+// The result of token tok and query head h of sequence b, by a whole warp, four dims a lane
+// (head_dim 64: by half of it); what the lanes stored of the row before is replaced.
+// kKeysAtOnce: 4, so that their loads are under way together, or 1 where the kernel pays for the
+// registers of a call that it hardly ever makes (with 4 and 1, the merge of one tree of 24 tokens on
+// 16384 31.8 and 28.6 us a call, without repair 28.4; rows_tree_kernel, 32 int8 trees, 121.8 and 118.4).
+template <int kKeysAtOnce>
+static __device__ __noinline__ void repair_row(const Repair& p, int b, int tok, int h) {
   constexpr unsigned kWarp = 0xffffffffu;
-  constexpr int kKeysAtOnce = 4;
+  constexpr int E = 4;
+  __syncwarp();
   const int lane = threadIdx.x & 31, d = lane * E;
   const SeqSpan s = seq_span(p.span, b);
   const int last = p.mask ? s.ctx + s.n - 1 : s.ctx + tok, g = h / p.G, first = g * p.D + d;
@@ -68,8 +69,9 @@ static __device__ __noinline__ void repair_row_of(const Repair& p, int b, int to
   const long long query = s.q0 + tok, at_q = (query * p.hq + h) * p.D;
   const RowSees sees = row_sees(p.span, t, s.off, s.ctx, s.n, tok, query, p.q_pos, p.mask, p.words);
   const int io = p.dtype == PKV_F32 ? PKV_F32 : PKV_BF16;
-  float q[E], o[E], m = -INFINITY, l = 0.f;
-  repair_elements<E>(p.q + at_q * (io == PKV_F32 ? 4 : 2), io, d, q);
+  const bool mine = d < p.D;
+  float q[E] = {}, o[E], m = -INFINITY, l = 0.f;
+  if (mine) repair_elements(p.q + at_q * (io == PKV_F32 ? 4 : 2), io, d, q);
 #pragma unroll
   for (int e = 0; e < E; ++e) o[e] = 0.f;
   for (int x0 = 0; x0 < t.nt * 32; x0 += 32) {
@@ -96,10 +98,10 @@ static __device__ __noinline__ void repair_row_of(const Repair& p, int b, int to
         x[u] = 0.f;
 #pragma unroll
         for (int e = 0; e < E; ++e) v[u][e] = 0.f;
-        if (on[u] && row >= 0) {
+        if (on[u] && row >= 0 && mine) {
           float k[E];
-          repair_elements<E>(p.k + row, p.dtype, first, k);
-          repair_elements<E>(p.v + row, p.dtype, first, v[u]);
+          repair_elements(p.k + row, p.dtype, first, k);
+          repair_elements(p.v + row, p.dtype, first, v[u]);
 #pragma unroll
           for (int e = 0; e < E; ++e) x[u] = fmaf(q[e], k[e], x[u]);
           if (p.dtype == PKV_I8) {
@@ -133,27 +135,17 @@ static __device__ __noinline__ void repair_row_of(const Repair& p, int b, int to
     // a NaN in every dim stays
     bool lost = true;
 #pragma unroll
-    for (int e = 0; e < E; ++e) lost &= o[e] != o[e];
+    for (int e = 0; e < E; ++e) lost &= o[e] != o[e] || !mine;
     if (__all_sync(kWarp, lost)) break;
   }
   const float inv = l == 0.f ? 0.f : 1.f / l;
-#pragma unroll
-  for (int e = 0; e < E; e += 2) {
-    const long long i = at_q + d + e;
-    if (io == PKV_F32)
-      *reinterpret_cast<float2*>(p.out + i * 4) = make_float2(o[e] * inv, o[e + 1] * inv);
-    else
-      *reinterpret_cast<uint32_t*>(p.out + i * 2) = pack_bf16x2(o[e] * inv, o[e + 1] * inv);
-  }
-}
-
-// By a whole warp; what its lanes stored of the row before is replaced.
-__device__ __forceinline__ void repair_row(const Repair& p, int b, int tok, int h) {
-  __syncwarp();
-  if (p.D == 64)
-    repair_row_of<2>(p, b, tok, h);
+  if (!mine) return;
+  if (io == PKV_F32)
+    *reinterpret_cast<float4*>(p.out + (at_q + d) * 4) =
+        make_float4(o[0] * inv, o[1] * inv, o[2] * inv, o[3] * inv);
   else
-    repair_row_of<4>(p, b, tok, h);
+    *reinterpret_cast<uint2*>(p.out + (at_q + d) * 2) =
+        make_uint2(pack_bf16x2(o[0] * inv, o[1] * inv), pack_bf16x2(o[2] * inv, o[3] * inv));
 }
 
 }  // namespace pkv

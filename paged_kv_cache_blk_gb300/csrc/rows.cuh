@@ -209,20 +209,22 @@ __device__ __forceinline__ void rows_piece(const RowsParams& p, const RowsPiece&
   auto seen_by_some = [&](int pos) {
     return pos >= off && pos <= off + w.hi && (pos >= off + w.lo || pos < sink_end);
   };
-  // block of the lane's row in tile i; INT_MIN: a row of zeros (ids below the pool's become -1)
+  // block of the lane's row in tile i; INT_MIN: a row of zeros
   auto lookup = [&](int i) -> int {
     if (i >= w.t1) return INT_MIN;
     const int pos = w.t.position(i * KT + my_r);
-    return seen_by_some(pos) ? max(table[pos >> p.bs_bits], -1) : INT_MIN;
+    return seen_by_some(pos) ? table[pos >> p.bs_bits] : INT_MIN;
   };
   auto issue = [&](int i, int stage, int blk, auto look) {
     if (i < w.t1) {
       const int pos = w.t.position(i * KT + my_r);
-      if (blk != INT_MIN && (blk < 0 || blk >= p.num_blocks)) {
-        if constexpr (TREE)
-          *bad_entry = 1;  // looked into at the end
-        else
-          set_error(p.err, kErrIndex);
+      if (blk < 0 || blk >= p.num_blocks) {
+        if (seen_by_some(pos)) {  // (an entry may hold any number, INT_MIN too)
+          if constexpr (TREE)
+            *bad_entry = 1;  // looked into at the end
+          else
+            set_error(p.err, kErrIndex);
+        }
         blk = INT_MIN;
       }
       const unsigned live = __ballot_sync(kAllLanes, blk != INT_MIN);
@@ -763,7 +765,7 @@ __device__ __forceinline__ void rows_piece(const RowsParams& p, const RowsPiece&
     for (int row = warp; row < M; row += kRowsWarps) {
       if (row_factor[row] == 0.f) continue;
       const int r = w.first_row + row, tok = r / G;
-      repair_row(p.repair, w.b, tok, w.g * G + (r - tok * G));
+      repair_row<1>(p.repair, w.b, tok, w.g * G + (r - tok * G));
     }
     __syncthreads();
   };
