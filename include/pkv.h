@@ -548,11 +548,14 @@ PKV_API pkv_status pkv_decode_attention_window(const pkv_pool* pool, int32_t lay
  * workspace; may be captured in a CUDA graph.
  * Arithmetic, here and in pkv_decode_attention_tree: sums, softmax statistics and
  * states in fp32.  bf16 pools: the weights enter their product with V as the
- * nearest bf16, as in pkv_prefill_attention, or where max_q_len times the query
- * heads of a kv head is at most 16 as two bf16 parts, within 2^-16 together.
+ * nearest bf16, within 2^-8, as in pkv_prefill_attention (rounded twice, within
+ * 2^-7, where a later key of their tile of 128 lies 2^8 above the row's maximum so
+ * far), or where max_q_len times the query heads of a kv head is at most 16 as two
+ * bf16 parts, within 2^-16 together.
  * PKV_I8 pools: exact codes and exact q (but for what lies under 2^-39 of a row's
  * largest), the weights times the V scales as one fp16, within 2^-11 of each or
- * 2^-27 of the largest of the row; as two, within 2^-22, where bf16 has two.
+ * 2^-27 of the largest of the row; as two, within 2^-22 of each or the same of the
+ * largest, where bf16 has two.
  * fp32 pools: every product within 2^-21 (an infinite element of q or of a seen key
  * may count as NaN in its scores). */
 PKV_API pkv_status pkv_prefill_attention_window(const pkv_pool* pool, int32_t layer, const void* q,
