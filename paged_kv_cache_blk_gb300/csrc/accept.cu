@@ -12,7 +12,8 @@
 // kBatch loads before their stores.  a_k >= k and ascending, so a store never overwrites a
 // row that a later token still has to read, and as only this thread touches its columns
 // no barrier stands between tokens.  5 rows of 32 layers: 3.2 us on the device, of a call's
-// 7.5; 8 rows each of 64 sequences in 16 layers, whose bytes take 2.3 us, the same.
+// 7.5; up to 8 rows of each of 64 sequences in 16 layers, whose bytes take 2.3 us, 6.2 (one call
+// after another, replayed).
 #include <climits>
 
 #include "common.cuh"

@@ -48,14 +48,14 @@
 // multiplied (a freed block may hold NaN).  Rows that a V row of others spoiled are computed
 // again after the CTA's last item (repair.cuh).
 //  * kWindow: the CTA pairs of prefill; 8 prompts of 1024 to 8192 tokens under a window
-//    of 1024, 32 / 8 heads, D 128, 590 us (220 by the products alone).
+//    of 1024, 32 / 8 heads, D 128, 582 us (220 by the products alone).
 //  * kTree: a CTA an SM takes an even share of the batch's tiles, whatever the units
 //    (span.cuh), and leaves a state of each unit that it did not finish.  Its own loads
 //    all: K by warp 8, V by warp 11, table entries looked up a tile ahead (one warp for
-//    both, entries when needed: 16 trees of 256 rows on 8192 tokens 188 us, now 164).
+//    both, entries when needed: 16 trees of 256 rows on 8192 tokens 188 us, now 162).
 //  * kNarrow, up to 128 rows: both softmax groups work on those rows, half of each key
 //    tile each, and S of the next tile is issued ahead of P V: 16 trees of 64 rows on
-//    8192 tokens 109 us (kTree, half of it empty, 163), 79 by the bytes; the two states
+//    8192 tokens 107 us (kTree, half of it empty, 163), 80 by the bytes; the two states
 //    of a row are merged in TMEM at the end.
 // Every wait is bounded; on a timeout the CTA records the error, drains its
 // MMAs and frees its TMEM before returning.

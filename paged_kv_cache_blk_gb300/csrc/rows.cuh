@@ -45,8 +45,8 @@
 //     accumulator: each tile's P V is summed from zero and added to O with rounding.
 //
 // What bounds it.  Few rows of bf16: the keys' bytes (16 trees of 4 tokens on 8192, groups of 4,
-// D 128: 91 us, 79 by the bytes; of 8 tokens, D 64, 70 and 40).  int8 (the same trees of 4 tokens
-// 91 us, 41 by the bytes), and with more rows, as in fp32, what lies around the products:
+// D 128: 89 us, 79 by the bytes; of 8 tokens, D 64, 68 and 40).  int8 (the same trees of 4 tokens
+// 88 us, 41 by the bytes), and with more rows, as in fp32, what lies around the products:
 // conversions, operands through shared memory, barriers - 50 to 55% of the issue slots and a
 // quarter to a third of the tensor pipe.
 #pragma once

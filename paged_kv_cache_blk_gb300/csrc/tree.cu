@@ -212,7 +212,9 @@ cudaError_t launch_rows(const PoolView& v, const RowsParams& p, bool tree, long 
 // keys x 64 rows a CTA, beside the others of its SM) and what an item costs besides.  On 4096
 // under a window of 4096, 32 / 8 heads, D 128, tcgen05 and mma.sync took for 30 tokens 68 and 26
 // us, 100 tokens 78 and 45, 300 tokens 79 and 80, 512 tokens 79 and 146; under a window of 500,
-// 100 tokens 21 and 17, 512 tokens 21 and 30; with D 64, 100 tokens 69 and 34.
+// 100 tokens 21 and 17, 512 tokens 21 and 30; with D 64, 100 tokens 69 and 34.  Over 448 shapes (1 to 16
+// sequences of 16 to 4096 tokens behind windows of 128 to 8192, 4 and 8 kv heads, groups of 1 to 16, both D),
+// each measured on both kernels, the one chosen was never more than 1.12 of the other, nor 7 us above it.
 bool prefill_on_tcgen05(const PoolView& v, const RowsParams& p, int sms) {
   if (!span_supported(v, p.hq, true) || p.plan.unit_rows <= 32) return false;
   const bool d64 = v.head_dim == 64;
