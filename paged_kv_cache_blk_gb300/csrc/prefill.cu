@@ -723,19 +723,18 @@ __device__ __forceinline__ void repair_item(const PfParams& p, const Item& it) {
     if ((x == 0 ? it.nA : it.nB) == 0) continue;
     const long long tok0 = (x == 0 ? it.qtA : it.qtB) * p.TQ;
     const int rows = (int)min((long long)p.TQ, it.nq - tok0) * p.G;
-    for (int r0 = warp * 32; r0 < rows; r0 += warps * 32) {
-      const int r = r0 + lane;
-      bool marked = false;
-      if (r < rows) {
-        const unsigned short* row =
-            static_cast<const unsigned short*>(p.out) +
-            ((it.q0 + tok0 + r / p.G) * p.hq + (long long)it.g * p.G + r % p.G) * HD;
-        marked = __ldcg(row) == kSpoiled || (MODE == kNarrow && __ldcg(row + HD / 2) == kSpoiled);
-      }
-      for (unsigned todo = __ballot_sync(0xffffffffu, marked); todo; todo &= todo - 1) {
-        const int m = r0 + __ffs(todo) - 1;
-        repair_row<4>(p.repair, it.b, (int)tok0 + m / p.G, it.g * p.G + m % p.G);
-      }
+    // a warp's rows: warp, warp + warps, ..., looked at a lane each (128 rows, at least 10 warps)
+    const int r = warp + lane * warps;
+    bool marked = false;
+    if (r < rows) {
+      const unsigned short* row =
+          static_cast<const unsigned short*>(p.out) +
+          ((it.q0 + tok0 + r / p.G) * p.hq + (long long)it.g * p.G + r % p.G) * HD;
+      marked = __ldcg(row) == kSpoiled || (MODE == kNarrow && __ldcg(row + HD / 2) == kSpoiled);
+    }
+    for (unsigned todo = __ballot_sync(0xffffffffu, marked); todo; todo &= todo - 1) {
+      const int m = warp + (__ffs(todo) - 1) * warps;
+      repair_row<PKV_BF16, 4>(p.repair, it.b, (int)tok0 + m / p.G, it.g * p.G + m % p.G);
     }
   }
 }

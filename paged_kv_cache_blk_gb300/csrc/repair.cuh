@@ -3,7 +3,8 @@
 // The kernels multiply a tile's V rows by the weights of several queries at once, 0 where a
 // query does not see a row; 0 times an infinity or a NaN is NaN.  A result that came out NaN or
 // infinite although its weights' sum is finite (scores of seen keys decide that sum alone) is
-// computed again over the seen keys only, a warp a row: lanes over the dims, each score once.
+// computed again over the seen keys only, a warp a row: lanes over the dims, each score once.  (Where
+// the row does see it the result stays what it was.)
 //
 // Where: nothing waits for it.  prefill.cu marks such rows and goes on; a CTA computes its marked
 // rows after its last item, when its pipeline is over and its tensor memory free, so that however
@@ -54,24 +55,29 @@ __device__ __forceinline__ void repair_elements(const char* row, int dtype, int 
 
 // The result of token tok and query head h of sequence b, by a whole warp, four dims a lane
 // (head_dim 64: by half of it); what the lanes stored of the row before is replaced.
-// kKeysAtOnce: 4, so that their loads are under way together, or 1 where the kernel pays for the
-// registers of a call that it hardly ever makes (with 4 and 1, the merge of one tree of 24 tokens on
-// 16384 31.8 and 28.6 us a call, without repair 28.4; rows_tree_kernel, 32 int8 trees, 121.8 and 118.4).
-template <int kKeysAtOnce>
+// kType: of the pool, or -1: p.dtype.  kKeysAtOnce: 4, whose loads are under way together, or 1 where
+// the kernel pays for the registers of a call that it hardly ever makes (with 4 and 1, the call of one
+// tree of 24 tokens on 16384 31.8 and 28.6 us, without repair in the merge 28.4; rows_tree_kernel, 32
+// int8 trees, 121.8 and 118.4).  At worst, an infinity that all queries see, every row is computed
+// again: 4096 tokens under a window of 1024, 32 / 8 heads, D 128, 14 ms on the tcgen05 kernel (39 with a
+// third of the warps, 89 with branches between the loads too), 17 on the mma.sync one; NaN 0.7 and 0.5.
+template <int kType, int kKeysAtOnce>
 static __device__ __noinline__ void repair_row(const Repair& p, int b, int tok, int h) {
   constexpr unsigned kWarp = 0xffffffffu;
   constexpr int E = 4;
   __syncwarp();
+  const int dtype = kType >= 0 ? kType : p.dtype;
   const int lane = threadIdx.x & 31, d = lane * E;
+  const bool mine = d < p.D;
   const SeqSpan s = seq_span(p.span, b);
-  const int last = p.mask ? s.ctx + s.n - 1 : s.ctx + tok, g = h / p.G, first = g * p.D + d;
+  const int last = p.mask ? s.ctx + s.n - 1 : s.ctx + tok, g = h / p.G;
+  const int first = g * p.D + (mine ? d : 0);
   const KeyList t = key_list<32>(p.span, s.off, window_start(s.ctx, p.span.window), last);
   const long long query = s.q0 + tok, at_q = (query * p.hq + h) * p.D;
   const RowSees sees = row_sees(p.span, t, s.off, s.ctx, s.n, tok, query, p.q_pos, p.mask, p.words);
-  const int io = p.dtype == PKV_F32 ? PKV_F32 : PKV_BF16;
-  const bool mine = d < p.D;
-  float q[E] = {}, o[E], m = -INFINITY, l = 0.f;
-  if (mine) repair_elements(p.q + at_q * (io == PKV_F32 ? 4 : 2), io, d, q);
+  const int io = dtype == PKV_F32 ? PKV_F32 : PKV_BF16;
+  float q[E], o[E], m = -INFINITY, l = 0.f;
+  repair_elements(p.q + at_q * (io == PKV_F32 ? 4 : 2), io, mine ? d : 0, q);
 #pragma unroll
   for (int e = 0; e < E; ++e) o[e] = 0.f;
   for (int x0 = 0; x0 < t.nt * 32; x0 += 32) {
@@ -95,22 +101,24 @@ static __device__ __noinline__ void repair_row(const Repair& p, int b, int tok, 
         const int key = on[u] ? __ffs(todo) - 1 : 0;
         todo &= todo - 1;
         const long long row = __shfl_sync(kWarp, at, key);
+        // (without a branch: what is not a key of this lane's dims is loaded from elsewhere and dropped)
+        const bool held = on[u] && row >= 0 && mine;
+        const char *k_row = p.k + (held ? row : 0), *v_row = p.v + (held ? row : 0);
+        float k[E];
+        repair_elements(k_row, dtype, first, k);
+        repair_elements(v_row, dtype, first, v[u]);
+        float sk = 1.f, sv = 1.f;
+        if (dtype == PKV_I8) {
+          sk = *reinterpret_cast<const float*>(k_row + p.scale_off + 4 * g);
+          sv = *reinterpret_cast<const float*>(v_row + p.scale_off + 4 * g);
+        }
         x[u] = 0.f;
 #pragma unroll
-        for (int e = 0; e < E; ++e) v[u][e] = 0.f;
-        if (on[u] && row >= 0 && mine) {
-          float k[E];
-          repair_elements(p.k + row, p.dtype, first, k);
-          repair_elements(p.v + row, p.dtype, first, v[u]);
-#pragma unroll
-          for (int e = 0; e < E; ++e) x[u] = fmaf(q[e], k[e], x[u]);
-          if (p.dtype == PKV_I8) {
-            x[u] *= *reinterpret_cast<const float*>(p.k + row + p.scale_off + 4 * g);
-            const float sv = *reinterpret_cast<const float*>(p.v + row + p.scale_off + 4 * g);
-#pragma unroll
-            for (int e = 0; e < E; ++e) v[u][e] *= sv;
-          }
+        for (int e = 0; e < E; ++e) {
+          x[u] = fmaf(q[e], k[e], x[u]);
+          v[u][e] = held ? v[u][e] * sv : 0.f;
         }
+        x[u] = held ? x[u] * sk : 0.f;
       }
 #pragma unroll
       for (int u = 0; u < kKeysAtOnce; ++u) {

@@ -765,7 +765,7 @@ __device__ __forceinline__ void rows_piece(const RowsParams& p, const RowsPiece&
     for (int row = warp; row < M; row += kRowsWarps) {
       if (row_factor[row] == 0.f) continue;
       const int r = w.first_row + row, tok = r / G;
-      repair_row<1>(p.repair, w.b, tok, w.g * G + (r - tok * G));
+      repair_row<MODE, 1>(p.repair, w.b, tok, w.g * G + (r - tok * G));
     }
     __syncthreads();
   };

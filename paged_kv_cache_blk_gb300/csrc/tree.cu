@@ -100,7 +100,7 @@ __device__ __forceinline__ void combine_row(const CombineParams& p, const SeqPla
   }
   // (lanes behind the dims hold zeros)
   const bool bad = nonfinite(x[0]) || nonfinite(x[1]) || nonfinite(x[2]) || nonfinite(x[3]);
-  if (__any_sync(0xffffffffu, bad) && !nonfinite(sum)) repair_row<1>(p.repair, b, tok, h);
+  if (__any_sync(0xffffffffu, bad) && !nonfinite(sum)) repair_row<-1, 1>(p.repair, b, tok, h);
 }
 
 // A CTA takes kCombineWarps * rows_warp rows of one sequence.
