@@ -378,3 +378,56 @@ def test_pools_past_two_to_the_32_bytes(dev, window_path, dtype, D, n, path):
     assert all(torch.equal(a, b) for a, b in zip(*got))
     for b, x in zip(big, (c.k, c.v)):
         assert torch.equal(b[N - m:], x)
+
+
+# ---- shapes that the lists above leave out ---------------------------------------------------
+
+@pytest.mark.parametrize("dtype,H,G,D,bs,lens,new", [
+    ("bf16", 1, 2, 128, 16, [900, 333], [300, 333]), ("bf16", 1, 3, 64, 32, [1400], [700]),
+    ("f32", 1, 1, 64, 16, [500, 300], [257, 300]), ("i8", 1, 2, 128, 16, [700], [400]),
+    ("bf16", 105, 1, 64, 16, [300, 40], [40, 3]), ("bf16", 33, 2, 128, 8, [200], [20])])
+def test_wide_trees_and_many_heads(dev, dtype, H, G, D, bs, lens, new):
+    """Masks of several words over several units, and kv heads of any number."""
+    c = Case(dev, dtype, H, G, D, bs, lens, new, 151)
+    kv = c.values(c.k), c.values(c.v)
+    made = [_random_tree(c.rng, int(n)) for n in new]
+    words = -(-max(new) // 64) + 1
+    mask, pos = _tree_args(c, [t for t, _ in made], [d for _, d in made], words)
+
+    def seen_of(b, i):
+        ctx = int(c.lens[b] - c.new[b])
+        return MK.tree_seen(ctx, made[b][0], i, ctx + int(made[b][1][i]), 90, 5)
+
+    _check_weights(c, _tree(c, mask, pos, 90, 5), *kv, seen_of, _weight(dtype, max(new) * G > 16))
+
+
+@pytest.mark.parametrize("dtype,D,n", [("bf16", 128, 3), ("bf16", 128, 20), ("bf16", 128, 100), ("bf16", 64, 20),
+                                       ("f32", 64, 9), ("i8", 128, 12)])
+def test_rows_behind_the_last_sequence_stay(dev, window_path, dtype, D, n):
+    """A padded batch: more rows of q (NaN), out, mask and positions than cu_q names, and a bound above
+    every length.  (The bound chooses the kernel and the split: to rounding, tests above hold the rest.)"""
+    c = Case(dev, dtype, 2, 4, D, 16, [90 + n, 40, n], [n, 0, n], seed=161)
+    made = [_random_tree(c.rng, int(m)) for m in c.new]
+    mask, pos = _tree_args(c, [t for t, _ in made], [d for _, d in made], 4)
+    real = c.q
+    want = {"tree": _tree(c, mask, pos, most=150), "chain": _tree(c, None, None, most=150), "prefill": _prefill(c, 40, 2, 150)}
+    pad = lambda x, v: torch.cat([x, torch.full((33,) + tuple(x.shape[1:]), v, dtype=x.dtype, device=dev)])
+    c.q = pad(real, float("nan"))
+    got = {"tree": _tree(c, pad(mask, -1), pad(pos, -1), most=150), "chain": _tree(c, None, None, most=150),
+           "prefill": _prefill(c, 40, 2, 150)}
+    for k, x in got.items():
+        assert torch.equal(x[:len(real)], want[k]) and bool((x[len(real):] == 7.0).all()), k
+    assert pkv.device_error() == "PKV_OK"
+
+
+def test_one_workspace_for_calls_in_a_row(dev):
+    """Calls on one stream may share a workspace, of any size that the largest asks for."""
+    cases = [Case(dev, "bf16", 2, 4, 128, 16, [700, 90], [m, 2], seed=171 + m) for m in (3, 40, 12, 100, 4)]
+    big = torch.full((max(_workspace(c, int(c.new.max())).numel() for c in cases),), 255, dtype=torch.uint8, device=dev)
+    want = [_tree(c, None, None) for c in cases]
+    args = [c.device() for c in cases]
+    outs = [torch.full_like(c.q, 7.0) for c in cases]
+    torch.cuda.synchronize()
+    for c, (bt, lens, offs, cu), out in zip(cases, args, outs):
+        pkv.decode_attention_tree(c.pool, c.layer, c.q, c.scale, bt, lens, offs, cu, int(c.new.max()), None, out, big)
+    assert all(torch.equal(a, b) for a, b in zip(outs, want))
